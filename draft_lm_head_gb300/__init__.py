@@ -8,6 +8,9 @@ views of bf16 bits. Names follow the C ABI (include/lmhead.h) without the
 
     ids, logits, q = two_stage(LOCAL, W, A, B, h, token_ids, T, k_tile)
 
+The serving operators around the head are in draft_lm_head_gb300.serving and
+re-exported here.
+
 Offline preparation of A and B (the Freq-aware SVD) is in
 draft_lm_head_gb300.prep.
 """
@@ -28,7 +31,8 @@ __all__ = [
     "lowrank_score_topk", "gather_logits", "candidate_softmax", "two_stage", "dense_head",
     "pruned_head", "cluster_candidate_count", "cluster_workspace_size", "cluster_two_stage",
     "draft_select", "verify_chain", "last_device_error", "debug_set_wait_cycles", "version",
-    "Workspace", "shard_workspace_size", "shard_two_stage", "shard_softmax",
+    "Workspace", "shard_workspace_size", "shard_two_stage", "shard_softmax", "PagePlan",
+    "page_plan",
 ]
 
 _BF16_OK = (torch.bfloat16, torch.int16, torch.uint16) if hasattr(torch, "uint16") else (
@@ -371,3 +375,6 @@ def verify_chain(p: torch.Tensor, x: torch.Tensor, cand_ids: torch.Tensor, cand_
         _typed(r, torch.float32, "r"), _typed(u, torch.float32, "u"), tokens.data_ptr(),
         count.data_ptr(), _stream_ptr(stream)), "verify_chain")
     return tokens, count
+
+
+from .serving import PagePlan, page_plan  # noqa: E402,F401

@@ -43,6 +43,7 @@ SIGNATURES = {
     "lmhead_cluster_workspace_size": (_SZ, [_I64, _I, _I, _I, _I, _I]),
     "lmhead_cluster_two_stage": (_I, [_P, _P, _P, _P, _I64, _I, _I, _I, _I, _I, _F,
                                       _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "lmhead_page_plan": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P]),
     "lmhead_two_stage_local_noalloc": (_I, [_P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _I, _F,
                                             _P, _P, _P, _P]),
 }

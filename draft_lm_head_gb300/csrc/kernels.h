@@ -149,6 +149,14 @@ cudaError_t launch_verify_chain(const float* p, int64_t n, int B, int Kd, const 
                                 const float* u, int32_t* out_tokens, int32_t* out_count, int* err,
                                 cudaStream_t s);
 
+// ---- serving operators around the head
+// Block tables and slot maps of a step's new tokens (paged.cu).
+cudaError_t launch_page_plan(const int32_t* lens, const int32_t* fresh, int S, int32_t* table,
+                             int width, const int32_t* free_pages, int free_cap,
+                             const int32_t* free_count, int page, int T, int32_t* slots,
+                             int32_t* positions, int32_t* cu, int32_t* granted,
+                             int32_t* free_left, int* err, cudaStream_t s);
+
 int* device_error_word();  // this device's error word (nullptr on failure)
 // Budget (SM cycles) of the tensor-core kernels' role waits; tc::kWaitCycles
 // unless lmhead_debug_set_wait_cycles changed it.

@@ -62,6 +62,13 @@ typedef enum {
   LMHEAD_LOCAL = 1   /* ids = concat over vocabulary tiles of each tile's top-k_tile */
 } lmhead_mode;
 
+/* Element types of the serving operators (hidden vectors, caches, logits). */
+typedef enum {
+  LMHEAD_BF16 = 0,
+  LMHEAD_FP16 = 1,
+  LMHEAD_FP32 = 2
+} lmhead_dtype;
+
 /* Library version (major*10000 + minor*100 + patch). */
 int lmhead_version(void);
 
@@ -363,6 +370,47 @@ int lmhead_shard_two_stage(const lmhead_bf16* W_shard, const lmhead_bf16* A_shar
  */
 int lmhead_shard_softmax(const float* all_stats, int G, const float* logits, int M, int K,
                          float temperature, float* out_q, lmhead_stream stream);
+
+/*
+ * ---- Serving operators around the head: one drafting step needs pages for
+ * its new tokens, attention over the cache that holds the earlier ones, a
+ * head that is cheap to read, and the choice over all live beams. The pages
+ * have no counterpart to them beyond the steps they name ("EAGLE -> EAGLE-2
+ * -> EAGLE-3 -> DFlash": the drafter's layer attends over the accepted prefix
+ * and the draft tree; Expansion Phase: the best nodes of a layer are
+ * expanded). Conventions as above; sizes and errors as said at each.
+ *
+ * Page plan: block tables and slot maps of a step's new tokens, from the
+ * requests' lengths.
+ *   lens, new_lens  S int32: tokens already cached, tokens about to be written.
+ *   table       S x width int32, in place: the pages of each request in order.
+ *               Those of its ceil(len / page_size) held pages are read; the
+ *               entries of new pages are written.
+ *   free_pages  int32 page ids, a stack whose first *free_count entries
+ *               (at most free_cap) are free. Pages are taken from its top in
+ *               request order: page j of a request whose predecessors need e
+ *               pages is free_pages[*free_count - 1 - e - j].
+ *   max_tokens  capacity of out_slots and out_positions.
+ *   out_slots   max_tokens int32: page * page_size + offset of each new
+ *               token, request after request; -1 for tokens of a request that
+ *               was not granted, and past the last token.
+ *   out_positions  max_tokens int32: position in its request, -1 likewise.
+ *   out_cu      S + 1 int32: where each request's tokens start.
+ *   out_granted S int32: 1 if the request's tokens have places. A request
+ *               is refused if it needs pages and the running sum of the needs
+ *               up to it passes the free count, if a length is negative, or if
+ *               len + new passes width * page_size (its need then counts 0).
+ *   out_free_left  1 int32: free pages after the plan (the caller's next
+ *               free_count; must not alias free_count).
+ * More new tokens than max_tokens: the excess gets no slots and
+ * LMHEAD_ERR_DEVICE_CHECK is recorded. page_size 1..65536, S up to 2^20;
+ * page ids * page_size must stay below 2^31.
+ */
+int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_t* table,
+                     int width, const int32_t* free_pages, int free_cap,
+                     const int32_t* free_count, int page_size, int max_tokens,
+                     int32_t* out_slots, int32_t* out_positions, int32_t* out_cu,
+                     int32_t* out_granted, int32_t* out_free_left, lmhead_stream stream);
 
 /*
  * Test hook for the timeout path (the pages have no counterpart). Every wait

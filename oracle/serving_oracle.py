@@ -1,0 +1,34 @@
+"""fp64 CPU oracle of the serving operators around the head. Written from the
+definitions in include/lmhead.h, element by element."""
+from __future__ import annotations
+
+import numpy as np
+
+
+def page_plan(lens, new, table, free_pages, free_count, page, max_tokens):
+    """Returns (slots, positions, cu, granted, free_left, table)."""
+    table = np.array(table)
+    width = table.shape[1]
+    F = max(0, min(int(free_count), len(free_pages)))
+    slots = np.full(max_tokens, -1, dtype=np.int64)
+    positions = np.full(max_tokens, -1, dtype=np.int64)
+    cu, granted, before, left = [0], [], 0, F
+    for s, (l, m) in enumerate(zip(lens, new)):
+        l, m = int(l), int(m)
+        fits = l >= 0 and m >= 0 and l + m <= width * page
+        need = -(-(l + m) // page) - -(-l // page) if fits else 0
+        ok = fits and (need == 0 or before + need <= F)
+        if ok:
+            held = -(-l // page)
+            for j in range(need):
+                table[s, held + j] = free_pages[F - 1 - before - j]
+            left -= need
+            for i in range(m):
+                t = cu[-1] + i
+                if t < max_tokens:
+                    positions[t] = l + i
+                    slots[t] = int(table[s, (l + i) // page]) * page + (l + i) % page
+        before += need
+        granted.append(int(ok))
+        cu.append(cu[-1] + max(m, 0))
+    return slots, positions, np.array(cu), np.array(granted), left, table
