@@ -44,6 +44,10 @@ SIGNATURES = {
     "lmhead_cluster_two_stage": (_I, [_P, _P, _P, _P, _I64, _I, _I, _I, _I, _I, _F,
                                       _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "lmhead_page_plan": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "lmhead_beam_workspace_size": (_SZ, [_I, _I, _I64, _I]),
+    "lmhead_beam_select": (_I, [_I, _P, _I64, _P, _P, _P, _I, _I, _I64, _I, _I, _P, _P, _P, _P,
+                                _SZ, _P]),
+    "lmhead_beam_reorder": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P]),
     "lmhead_two_stage_local_noalloc": (_I, [_P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _I, _F,
                                             _P, _P, _P, _P]),
 }

@@ -157,6 +157,32 @@ cudaError_t launch_page_plan(const int32_t* lens, const int32_t* fresh, int S, i
                              int32_t* positions, int32_t* cu, int32_t* granted,
                              int32_t* free_left, int* err, cudaStream_t s);
 
+// Beam selection and the reordering of the beams' states (beams.cu).
+constexpr int kBeamMaxK = 32;
+constexpr int kBeamMaxBeams = 256;
+struct BeamArgs {
+  int dtype;  // lmhead_dtype
+  const void* logits;
+  int64_t row_stride, n;  // elements
+  const float* scores;
+  const int32_t* ids;
+  const uint8_t* finished;
+  int S, beams, k, eos;
+  int32_t *parent, *token;
+  float* out_score;
+};
+size_t beam_scratch_bytes(int S, int beams, int64_t n, int k);
+cudaError_t launch_beam_select(const BeamArgs& a, void* scratch, cudaStream_t s);
+constexpr int kReorderMax = 8;
+struct ReorderArgs {
+  const void* src[kReorderMax];
+  void* dst[kReorderMax];
+  int64_t bytes[kReorderMax];  // of one row
+  int count, S, beams, k;
+  const int32_t* parent;
+};
+cudaError_t launch_beam_reorder(const ReorderArgs& a, int* err, cudaStream_t s);
+
 int* device_error_word();  // this device's error word (nullptr on failure)
 // Budget (SM cycles) of the tensor-core kernels' role waits; tc::kWaitCycles
 // unless lmhead_debug_set_wait_cycles changed it.

@@ -29,9 +29,9 @@ __device__ __forceinline__ Plan plan_of(int32_t len, int32_t fresh, int page, in
   Plan p;
   const bool sane = len >= 0 && fresh >= 0;
   const int64_t l = sane ? len : 0, m = sane ? fresh : 0;
-  p.fits = sane && l + m <= (int64_t)width * page;
+  p.fits = sane && l + m <= min((int64_t)width * page, (int64_t)INT32_MAX - page);
   p.fresh = fresh > 0 ? fresh : 0;
-  // both lengths and their sum, a page less one added, fit in 32 unsigned bits
+  // a page less one added, lengths that fit stay within 32 bits
   const uint32_t up = (uint32_t)page - 1u;
   p.need = p.fits ? ((uint32_t)(l + m) + up) / (uint32_t)page - ((uint32_t)l + up) / (uint32_t)page : 0;
   return p;

@@ -13,7 +13,18 @@ namespace {
 
 constexpr int kMaxRows = 1 << 20;
 
+inline bool aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
 inline int status(cudaError_t e) { return e == cudaSuccess ? LMHEAD_OK : LMHEAD_ERR_CUDA; }
+
+int check_beams(int S, int beams, int64_t n, int k) {
+  if (S < 1 || beams < 1 || n < 1 || k < 1) return LMHEAD_ERR_SHAPE;
+  if (k > kBeamMaxK || beams > kBeamMaxBeams) return LMHEAD_ERR_UNSUPPORTED;
+  if ((int64_t)S * beams > 65535 || n > (1ll << 30) || beams * n > INT32_MAX)
+    return LMHEAD_ERR_SHAPE;
+  return LMHEAD_OK;
+}
 
 }  // namespace
 
@@ -35,6 +46,66 @@ int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_
                                  page_size, max_tokens, out_slots, out_positions, out_cu,
                                  out_granted, out_free_left, device_error_word(),
                                  (cudaStream_t)stream));
+}
+
+size_t lmhead_beam_workspace_size(int S, int beams, int64_t n, int k) {
+  if (check_beams(S, beams, n, k) != LMHEAD_OK) return 0;
+  return beam_scratch_bytes(S, beams, n, k);
+}
+
+int lmhead_beam_select(int dtype, const void* logits, int64_t row_stride, const float* scores,
+                       const int32_t* ids, const void* finished, int S, int beams, int64_t n,
+                       int k, int eos, int32_t* out_parent, int32_t* out_token, float* out_score,
+                       void* workspace, size_t workspace_bytes, lmhead_stream stream) {
+  if (!logits || !scores || !out_parent || !out_token || !out_score) return LMHEAD_ERR_NULL;
+  if (dtype != LMHEAD_BF16 && dtype != LMHEAD_FP16 && dtype != LMHEAD_FP32)
+    return LMHEAD_ERR_UNSUPPORTED;
+  const int st = check_beams(S, beams, n, k);
+  if (st != LMHEAD_OK) return st;
+  if (row_stride < n || row_stride > (1ll << 40)) return LMHEAD_ERR_SHAPE;
+  if (!aligned(logits, dtype == LMHEAD_FP32 ? 4 : 2)) return LMHEAD_ERR_ALIGN;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < beam_scratch_bytes(S, beams, n, k))
+    return LMHEAD_ERR_WORKSPACE;
+  BeamArgs a = {};
+  a.dtype = dtype;
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.n = n;
+  a.scores = scores;
+  a.ids = ids;
+  a.finished = static_cast<const uint8_t*>(finished);
+  a.S = S;
+  a.beams = beams;
+  a.k = k;
+  a.eos = eos;
+  a.parent = out_parent;
+  a.token = out_token;
+  a.out_score = out_score;
+  return status(launch_beam_select(a, workspace, (cudaStream_t)stream));
+}
+
+int lmhead_beam_reorder(const int32_t* parent, int S, int beams, int k, int count,
+                        const void* const* src, void* const* dst, const int64_t* row_bytes,
+                        lmhead_stream stream) {
+  if (!parent || !src || !dst || !row_bytes) return LMHEAD_ERR_NULL;
+  if (S < 1 || beams < 1 || k < 1 || (int64_t)S * k > INT32_MAX || (int64_t)S * beams > INT32_MAX)
+    return LMHEAD_ERR_SHAPE;
+  if (count < 1 || count > kReorderMax) return LMHEAD_ERR_UNSUPPORTED;
+  ReorderArgs a = {};
+  for (int i = 0; i < count; ++i) {
+    if (!src[i] || !dst[i]) return LMHEAD_ERR_NULL;
+    if (row_bytes[i] < 1 || row_bytes[i] > (1ll << 29)) return LMHEAD_ERR_SHAPE;
+    a.src[i] = src[i];
+    a.dst[i] = dst[i];
+    a.bytes[i] = row_bytes[i];
+  }
+  a.count = count;
+  a.S = S;
+  a.beams = beams;
+  a.k = k;
+  a.parent = parent;
+  return status(launch_beam_reorder(a, device_error_word(), (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -2,14 +2,20 @@
 operators around the head").
 
     plan = page_plan(lens, new_lens, table, free_pages, free_count, P, max_tokens)
+    parent, token, score = beam_select(logits, scores, beams, k, ids=ids)
+    h, table = beam_reorder(parent, [h, table], beams)
 """
 from __future__ import annotations
 
-from typing import NamedTuple, Optional
+import ctypes
+import functools
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
 from ._lib import check, load
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class PagePlan(NamedTuple):
@@ -57,6 +63,12 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
     return t
 
 
+def _workspace(workspace, nbytes: int, device, stream) -> torch.Tensor:
+    if workspace is None:
+        return _empty(max(nbytes, 256), torch.uint8, device, stream)
+    return workspace.get(nbytes, device) if hasattr(workspace, "get") else workspace
+
+
 def page_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor,
               free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int, max_tokens: int,
               out: Optional[PagePlan] = None, stream=None) -> PagePlan:
@@ -82,4 +94,75 @@ def page_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor,
         _dense(out.positions, i32, (max_tokens,), dev, "positions"),
         _dense(out.cu, i32, (S + 1,), dev, "cu"), _dense(out.granted, i32, (S,), dev, "granted"),
         _dense(out.free_left, i32, (1,), dev, "free_left"), _stream(stream, dev)), "page_plan")
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _beam_bytes(device, S: int, beams: int, n: int, k: int) -> int:
+    with torch.cuda.device(device):
+        return int(load().lmhead_beam_workspace_size(S, beams, n, k))
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, k: int,
+                ids: Optional[torch.Tensor] = None, finished: Optional[torch.Tensor] = None,
+                eos: int = -1, workspace=None, out=None, stream=None):
+    """The k best continuations of each sequence over its beams' rows of logits
+    (S*beams x n, rows may be strided): (parent, token, score), each S x k.
+    scores: S*beams fp32 log-probabilities so far; ids: the entries' tokens;
+    finished: bool, beams that have ended (see lmhead_beam_select)."""
+    dev = _cuda(logits, "logits")
+    _need(logits.dim() == 2, "logits", "expected beams x entries")
+    if logits.dtype not in _DTYPES:
+        raise TypeError(f"logits: expected bf16, fp16 or fp32, got {logits.dtype}")
+    rows, n = logits.shape
+    _need(beams >= 1 and rows >= 1 and rows % beams == 0, "beams", f"does not divide {rows} rows")
+    _need(n >= 1, "logits", "no entries")
+    _need(1 <= k <= 32, "k", "must be 1 to 32")
+    if logits.stride(1) != 1 and n > 1:
+        raise TypeError("logits: expected contiguous rows")
+    S = rows // beams
+    stride = logits.stride(0) if rows > 1 else n
+    _need(stride >= n, "logits", "rows overlap")
+    if out is None:
+        parent, token = _empty((2, S, k), torch.int32, dev, stream).unbind(0)
+        score = _empty((S, k), torch.float32, dev, stream)
+    else:
+        parent, token, score = out
+    nbytes = _beam_bytes(dev, S, beams, n, k)
+    ws = _workspace(workspace, nbytes, dev, stream)
+    if finished is not None and finished.dtype == torch.bool:
+        finished = finished.view(torch.uint8)
+    i32 = torch.int32
+    check(load().lmhead_beam_select(
+        _DTYPES[logits.dtype], logits.data_ptr(), stride,
+        _dense(scores, torch.float32, (rows,), dev, "scores"),
+        _dense(ids, i32, (rows, n), dev, "ids"),
+        _dense(finished, torch.uint8, (rows,), dev, "finished"), S, beams, n, k, eos,
+        _dense(parent, i32, (S, k), dev, "parent"), _dense(token, i32, (S, k), dev, "token"),
+        _dense(score, torch.float32, (S, k), dev, "score"), ws.data_ptr(), ws.numel(),
+        _stream(stream, dev)), "beam_select")
+    return parent, token, score
+
+
+def beam_reorder(parent: torch.Tensor, states: Sequence[torch.Tensor], beams: int, out=None,
+                 stream=None):
+    """Each state tensor (S*beams rows of any type, contiguous) by the parents
+    chosen (S x k): a list of tensors of S*k rows, zeros where parent is -1."""
+    dev = _cuda(parent, "parent")
+    _need(parent.dim() == 2 and parent.numel() > 0, "parent", "expected sequences x k")
+    S, k = parent.shape
+    n = len(states)
+    _need(1 <= n <= 8, "states", "1 to 8 tensors")
+    _need(beams >= 1, "beams", "must be positive")
+    if out is None:
+        out = [_empty((S * k,) + tuple(t.shape[1:]), t.dtype, dev, stream) for t in states]
+    _need(len(out) == n, "out", "one tensor per state")
+    src, dst, size = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
+    for i, (t, o) in enumerate(zip(states, out)):
+        src[i] = _dense(t, t.dtype, (S * beams,) + tuple(t.shape[1:]), dev, f"states[{i}]")
+        dst[i] = _dense(o, t.dtype, (S * k,) + tuple(t.shape[1:]), dev, f"out[{i}]")
+        size[i] = t.numel() // (S * beams) * t.element_size()
+    check(load().lmhead_beam_reorder(
+        _dense(parent, torch.int32, (S, k), dev, "parent"), S, beams, k, n, src, dst, size,
+        _stream(stream, dev)), "beam_reorder")
     return out

@@ -399,7 +399,8 @@ int lmhead_shard_softmax(const float* all_stats, int G, const float* logits, int
  *   out_granted S int32: 1 if the request's tokens have places. A request
  *               is refused if it needs pages and the running sum of the needs
  *               up to it passes the free count, if a length is negative, or if
- *               len + new passes width * page_size (its need then counts 0).
+ *               len + new passes width * page_size or 2^31 - 1 - page_size (its
+ *               need then counts 0).
  *   out_free_left  1 int32: free pages after the plan (the caller's next
  *               free_count; must not alias free_count).
  * More new tokens than max_tokens: the excess gets no slots and
@@ -411,6 +412,41 @@ int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_
                      const int32_t* free_count, int page_size, int max_tokens,
                      int32_t* out_slots, int32_t* out_positions, int32_t* out_cu,
                      int32_t* out_granted, int32_t* out_free_left, lmhead_stream stream);
+
+/*
+ * One step of a beam search over S sequences of `beams` rows each:
+ *   score(b, j) = scores[b] + logits[b, j] - log sum_j exp(logits[b, j]),
+ * and per sequence the k largest over all its beams and entries (ties: the
+ * smaller b * n + j), best first.
+ *   logits    S*beams x n (bf16, fp16 or fp32), row_stride elements a row.
+ *   scores    S*beams fp32, the beams' log-probabilities so far.
+ *   ids       S*beams x n int32: the token of each entry (a candidate head's
+ *             out_ids), or NULL (entry j is token j).
+ *   finished  S*beams bytes or NULL: a beam with a non-zero byte has ended and
+ *             offers one entry, token eos with its score unchanged (as j = 0).
+ *   out_parent, out_token, out_score  S x k: the beam (0..beams-1), the token
+ *             and the score. Entries that score -inf or NaN (a masked logit, a
+ *             dead beam, a row with a NaN or +inf) are never taken; places left
+ *             over hold -1, -1 and -inf.
+ * 1 <= k <= 32, beams <= 256, S * beams <= 65535, n <= 2^30 and beams * n below 2^31.
+ * Workspace: lmhead_beam_workspace_size bytes, 256-byte aligned.
+ */
+size_t lmhead_beam_workspace_size(int S, int beams, int64_t n, int k);
+int lmhead_beam_select(int dtype, const void* logits, int64_t row_stride, const float* scores,
+                       const int32_t* ids, const void* finished, int S, int beams, int64_t n,
+                       int k, int eos, int32_t* out_parent, int32_t* out_token, float* out_score,
+                       void* workspace, size_t workspace_bytes, lmhead_stream stream);
+
+/*
+ * The states of the chosen beams: for each of `count` (1..8) state tensors,
+ * dst[s, j] = src[s, parent[s, j]], rows of row_bytes[i] bytes, src S*beams
+ * rows, dst S*k rows (not overlapping src). parent -1 gives zeros; any other
+ * value outside 0..beams-1 does too and records LMHEAD_ERR_DEVICE_CHECK.
+ *   src, dst, row_bytes  HOST arrays of `count` device pointers and sizes.
+ */
+int lmhead_beam_reorder(const int32_t* parent, int S, int beams, int k, int count,
+                        const void* const* src, void* const* dst, const int64_t* row_bytes,
+                        lmhead_stream stream);
 
 /*
  * Test hook for the timeout path (the pages have no counterpart). Every wait

@@ -32,3 +32,29 @@ def page_plan(lens, new, table, free_pages, free_count, page, max_tokens):
         granted.append(int(ok))
         cu.append(cu[-1] + max(m, 0))
     return slots, positions, np.array(cu), np.array(granted), left, table
+
+
+def beam_step(logits, scores, beams, k, finished=None):
+    """Per sequence: [(score, flat index)] of its k best, best first, ties to the
+    lower index, entries that score -inf or NaN left out."""
+    rows, n = logits.shape
+    res = []
+    for s in range(rows // beams):
+        val, idx = [], []
+        for b in range(beams):
+            r = s * beams + b
+            if finished is not None and finished[r]:
+                val.append(np.array([scores[r]], dtype=np.float64))
+                idx.append(np.array([b * n]))
+                continue
+            with np.errstate(all="ignore"):
+                x = logits[r].astype(np.float64)
+                top = x.max()
+                val.append(float(scores[r]) + (x - (top + np.log(np.exp(x - top).sum()))))
+            idx.append(b * n + np.arange(n))
+        val, idx = np.concatenate(val), np.concatenate(idx)
+        keep = val > -np.inf  # false for NaN too
+        val, idx = val[keep], idx[keep]
+        order = np.lexsort((idx, -val))[:k]
+        res.append([(val[o], int(idx[o])) for o in order])
+    return res
