@@ -254,7 +254,9 @@ __device__ __forceinline__ bool ahead(double sa, int32_t ia, double sb, int32_t 
 __global__ void __launch_bounds__(kRowThreads)
 beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
                   const int32_t* best_i) {
-  __shared__ double lse[kBeamMaxBeams];
+  // lse in its two parts: x - top is small where top is not
+  __shared__ float row_top[kBeamMaxBeams];
+  __shared__ double row_log[kBeamMaxBeams];
   __shared__ double b_score[kBuf];
   __shared__ int32_t b_flat[kBuf];
   __shared__ float sh_f[kRowThreads];
@@ -276,7 +278,8 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
       const Slice sl = slices[(size_t)row * nsl + i];
       if (sl.top != kNegInf || sl.sum != 0.0) sum += sl.sum * exp((double)sl.top - (double)top);
     }
-    lse[b] = (double)top + log(sum);
+    row_top[b] = top;
+    row_log[b] = log(sum);
   }
   if (tid == 0) sh_count = 0;
   cta_sync();
@@ -292,7 +295,8 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
       const int32_t i = best_i[(size_t)row * per + r];
       flat = b * n + i;
       if (i < 0) return (double)kNegInf;
-      sc = (double)a.scores[row] + ((double)best_v[(size_t)row * per + r] - lse[b]);
+      sc = (double)a.scores[row] +
+           (((double)best_v[(size_t)row * per + r] - (double)row_top[b]) - row_log[b]);
     }
     return sc == sc ? sc : (double)kNegInf;
   };

@@ -50,7 +50,7 @@ def beam_step(logits, scores, beams, k, finished=None):
             with np.errstate(all="ignore"):
                 x = logits[r].astype(np.float64)
                 top = x.max()
-                val.append(float(scores[r]) + (x - (top + np.log(np.exp(x - top).sum()))))
+                val.append(float(scores[r]) + ((x - top) - np.log(np.exp(x - top).sum())))
             idx.append(b * n + np.arange(n))
         val, idx = np.concatenate(val), np.concatenate(idx)
         keep = val > -np.inf  # false for NaN too
