@@ -157,6 +157,19 @@ cudaError_t launch_page_plan(const int32_t* lens, const int32_t* fresh, int S, i
                              int32_t* positions, int32_t* cu, int32_t* granted,
                              int32_t* free_left, int* err, cudaStream_t s);
 
+// 4-bit rows with group scales (q4.cu): out[m * ldo + j] = row_j . h[m] over
+// rows 0..n-1, or over rows ids[m * K + j] when ids != nullptr.
+struct Q4Args {
+  int dtype;
+  const uint8_t* codes;
+  const void *scales, *mins, *h;
+  const int32_t* ids;
+  int64_t n;
+  int d, group, M, K;
+  float* out;
+};
+cudaError_t launch_q4(const Q4Args& a, int* err, cudaStream_t s);
+
 // Beam selection and the reordering of the beams' states (beams.cu).
 constexpr int kBeamMaxK = 32;
 constexpr int kBeamMaxBeams = 256;

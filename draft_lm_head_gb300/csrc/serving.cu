@@ -12,11 +12,41 @@ using namespace lmhead;
 namespace {
 
 constexpr int kMaxRows = 1 << 20;
+constexpr int kMaxDim = 65536;
 
 inline bool aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 inline int status(cudaError_t e) { return e == cudaSuccess ? LMHEAD_OK : LMHEAD_ERR_CUDA; }
+
+int check_q4(int dtype, int64_t n, int d, int group, int M) {
+  if (dtype != LMHEAD_BF16 && dtype != LMHEAD_FP16) return LMHEAD_ERR_UNSUPPORTED;
+  if (group != 32 && group != 64 && group != 128) return LMHEAD_ERR_UNSUPPORTED;
+  if (n < 1 || n > INT32_MAX || d < group || d % group || d > kMaxDim || M < 1 || M > 65535)
+    return LMHEAD_ERR_SHAPE;
+  return LMHEAD_OK;
+}
+
+int q4(int dtype, const void* codes, const void* scales, const void* mins, const void* h,
+       const int32_t* ids, int64_t n, int d, int group, int M, int K, float* out,
+       lmhead_stream stream) {
+  if (!aligned(codes, 16) || !aligned(scales, 2) || !aligned(mins, 2) || !aligned(h, 16))
+    return LMHEAD_ERR_ALIGN;
+  Q4Args a = {};
+  a.dtype = dtype;
+  a.codes = static_cast<const uint8_t*>(codes);
+  a.scales = scales;
+  a.mins = mins;
+  a.h = h;
+  a.ids = ids;
+  a.n = n;
+  a.d = d;
+  a.group = group;
+  a.M = M;
+  a.K = K;
+  a.out = out;
+  return status(launch_q4(a, device_error_word(), (cudaStream_t)stream));
+}
 
 int check_beams(int S, int beams, int64_t n, int k) {
   if (S < 1 || beams < 1 || n < 1 || k < 1) return LMHEAD_ERR_SHAPE;
@@ -46,6 +76,25 @@ int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_
                                  page_size, max_tokens, out_slots, out_positions, out_cu,
                                  out_granted, out_free_left, device_error_word(),
                                  (cudaStream_t)stream));
+}
+
+int lmhead_q4_head(int dtype, const void* codes, const void* scales, const void* mins,
+                   const void* h, int64_t n, int d, int group, int M, float* out_logits,
+                   lmhead_stream stream) {
+  if (!codes || !scales || !h || !out_logits) return LMHEAD_ERR_NULL;
+  const int st = check_q4(dtype, n, d, group, M);
+  if (st != LMHEAD_OK) return st;
+  return q4(dtype, codes, scales, mins, h, nullptr, n, d, group, M, 0, out_logits, stream);
+}
+
+int lmhead_q4_gather_logits(int dtype, const void* codes, const void* scales, const void* mins,
+                            const void* h, const int32_t* ids, int64_t n, int d, int group, int M,
+                            int K, float* out_logits, lmhead_stream stream) {
+  if (!codes || !scales || !h || !ids || !out_logits) return LMHEAD_ERR_NULL;
+  const int st = check_q4(dtype, n, d, group, M);
+  if (st != LMHEAD_OK) return st;
+  if (K < 1 || (int64_t)M * K > INT32_MAX) return LMHEAD_ERR_SHAPE;
+  return q4(dtype, codes, scales, mins, h, ids, n, d, group, M, K, out_logits, stream);
 }
 
 size_t lmhead_beam_workspace_size(int S, int beams, int64_t n, int k) {

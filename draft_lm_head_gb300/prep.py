@@ -26,7 +26,8 @@ from typing import Optional
 
 import numpy as np
 
-__all__ = ["smoothed_frequency", "freq_aware_factors", "bf16_bits", "pruned_rows"]
+__all__ = ["smoothed_frequency", "freq_aware_factors", "bf16_bits", "pruned_rows",
+           "quantise_rows"]
 
 
 def smoothed_frequency(counts: np.ndarray) -> np.ndarray:
@@ -84,3 +85,44 @@ def pruned_rows(W_bits: np.ndarray, counts: np.ndarray, n_keep: int = 32000):
     f = smoothed_frequency(counts)
     kept = np.sort(np.argsort(-f, kind="stable")[:n_keep]).astype(np.int64)
     return np.ascontiguousarray(W_bits[kept]), kept
+
+
+def quantise_rows(W: np.ndarray, group: int, offsets: bool = False, fp16: bool = False,
+                  block: int = 8192) -> dict:
+    """4-bit codes of a head's rows with one scale per `group` elements, for
+    q4_head and q4_gather_logits (offline, nearest code to each weight).
+
+    W: n x d bf16 bits (uint16) or floats. Without offsets a weight is
+    s * (code - 8), s = max |w| / 7; with them s * code + min, s = (max - min)
+    / 15. Scales and mins are rounded to bf16 (fp16 with `fp16`) before the
+    codes are chosen. Returns dict(codes=uint8 n x d/2 (even element in the low
+    four bits), scales, mins (None without offsets): uint16 bits or float16)."""
+    n, d = W.shape
+    if group not in (32, 64, 128) or d % group:
+        raise ValueError(f"group={group} must be 32, 64 or 128 and divide d={d}")
+    codes = np.empty((n, d // 2), dtype=np.uint8)
+    kind = np.float16 if fp16 else np.uint16
+    scales = np.empty((n, d // group), dtype=kind)
+    mins = np.empty((n, d // group), dtype=kind) if offsets else None
+
+    def rounded(x):
+        if fp16:
+            r = x.astype(np.float16)
+            return r, r.astype(np.float64)
+        b = bf16_bits(x)
+        return b, _bits_to_f64(b)
+
+    for r0 in range(0, n, block):
+        w = W[r0:r0 + block]
+        w = (_bits_to_f64(w) if w.dtype == np.uint16 else w.astype(np.float64)).reshape(-1, d // group, group)
+        if offsets:
+            lo = w.min(axis=2)
+            mins[r0:r0 + block], low = rounded(lo)
+            scales[r0:r0 + block], s = rounded((w.max(axis=2) - lo) / 15)
+            c = (w - low[..., None]) / np.where(s > 0, s, 1.0)[..., None]
+        else:
+            scales[r0:r0 + block], s = rounded(np.abs(w).max(axis=2) / 7)
+            c = w / np.where(s > 0, s, 1.0)[..., None] + 8
+        c = np.clip(np.rint(c), 0, 15).astype(np.uint8).reshape(-1, d)
+        codes[r0:r0 + block] = c[:, 0::2] | (c[:, 1::2] << 4)
+    return {"codes": codes, "scales": scales, "mins": mins}

@@ -2,8 +2,11 @@
 operators around the head").
 
     plan = page_plan(lens, new_lens, table, free_pages, free_count, P, max_tokens)
+    logits = q4_gather_logits(codes, scales, h, ids, group)
     parent, token, score = beam_select(logits, scores, beams, k, ids=ids)
     h, table = beam_reorder(parent, [h, table], beams)
+
+Codes and scales of a 4-bit head come from prep.quantise_rows.
 """
 from __future__ import annotations
 
@@ -95,6 +98,54 @@ def page_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor,
         _dense(out.cu, i32, (S + 1,), dev, "cu"), _dense(out.granted, i32, (S,), dev, "granted"),
         _dense(out.free_left, i32, (1,), dev, "free_left"), _stream(stream, dev)), "page_plan")
     return out
+
+
+def _q4(name, codes, scales, h, ids, group, mins, out, stream):
+    dev = _cuda(h, "h")
+    dt = h.dtype
+    if dt not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"h: expected bf16 or fp16, got {dt}")
+    _need(h.dim() == 2, "h", "expected vectors x d")
+    _need(codes.dim() == 2, "codes", "expected rows x d/2")
+    _need(group in (32, 64, 128), "group", "must be 32, 64 or 128")
+    M, d = h.shape
+    n = codes.shape[0]
+    _need(d % group == 0 and d >= group, "group", f"does not divide d = {d}")
+    K = n
+    if ids is not None:
+        _need(ids.dim() == 2, "ids", "expected vectors x candidates")
+        K = ids.shape[1]
+    if out is None:
+        out = _empty((M, K), torch.float32, dev, stream)
+    args = [_DTYPES[dt], _dense(codes, torch.uint8, (n, d // 2), dev, "codes"),
+            _dense(scales, dt, (n, d // group), dev, "scales"),
+            _dense(mins, dt, (n, d // group), dev, "mins"), _dense(h, dt, (M, d), dev, "h")]
+    o = _dense(out, torch.float32, (M, K), dev, "out")
+    if ids is None:
+        check(load().lmhead_q4_head(*args, n, d, group, M, o, _stream(stream, dev)), name)
+    else:
+        check(load().lmhead_q4_gather_logits(
+            *args, _dense(ids, torch.int32, (M, K), dev, "ids"), n, d, group, M, K, o,
+            _stream(stream, dev)), name)
+    return out
+
+
+def q4_head(codes: torch.Tensor, scales: torch.Tensor, h: torch.Tensor, group: int,
+            mins: Optional[torch.Tensor] = None, workspace=None,
+            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Logits (M x n, fp32) of every row of a 4-bit head: codes n x d/2 uint8,
+    scales (and mins) n x d/group of h's type (see lmhead_q4_head). Needs no
+    scratch: `workspace` is taken like the other heads' and left alone."""
+    return _q4("q4_head", codes, scales, h, None, group, mins, out, stream)
+
+
+def q4_gather_logits(codes: torch.Tensor, scales: torch.Tensor, h: torch.Tensor,
+                     ids: torch.Tensor, group: int, mins: Optional[torch.Tensor] = None,
+                     workspace=None, out: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Exact logits (M x K, fp32) of the candidate rows ids (M x K) of a 4-bit
+    head (see lmhead_q4_gather_logits); `workspace` as for q4_head."""
+    return _q4("q4_gather_logits", codes, scales, h, ids, group, mins, out, stream)
 
 
 @functools.lru_cache(maxsize=4096)

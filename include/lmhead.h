@@ -414,6 +414,24 @@ int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_
                      int32_t* out_granted, int32_t* out_free_left, lmhead_stream stream);
 
 /*
+ * The head with 4-bit weights: row i is s * (c - 8) (mins NULL) or s * c + min
+ * with codes c in 0..15, one scale (and min) per `group` codes along d.
+ *   codes   n x d/2 bytes, the even element in the low four bits.
+ *   scales, mins  n x d/group, of type dtype (LMHEAD_BF16 or LMHEAD_FP16), as h.
+ *   h       M x d; group 32, 64 or 128; d a multiple of group.
+ *   lmhead_q4_head: out_logits M x n fp32, every row.
+ *   lmhead_q4_gather_logits: out_logits M x K fp32, row ids[m, j] (an id
+ *           outside [0, n) gives NaN and LMHEAD_ERR_DEVICE_CHECK).
+ * Codes are exact, products are summed in fp32, scales applied in fp32.
+ */
+int lmhead_q4_head(int dtype, const void* codes, const void* scales, const void* mins,
+                   const void* h, int64_t n, int d, int group, int M, float* out_logits,
+                   lmhead_stream stream);
+int lmhead_q4_gather_logits(int dtype, const void* codes, const void* scales, const void* mins,
+                            const void* h, const int32_t* ids, int64_t n, int d, int group, int M,
+                            int K, float* out_logits, lmhead_stream stream);
+
+/*
  * One step of a beam search over S sequences of `beams` rows each:
  *   score(b, j) = scores[b] + logits[b, j] - log sum_j exp(logits[b, j]),
  * and per sequence the k largest over all its beams and entries (ties: the

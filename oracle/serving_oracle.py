@@ -58,3 +58,13 @@ def beam_step(logits, scores, beams, k, finished=None):
         order = np.lexsort((idx, -val))[:k]
         res.append([(val[o], int(idx[o])) for o in order])
     return res
+
+
+def q4_rows(codes, scales, mins, group):
+    """The weights of 4-bit rows in fp64."""
+    c = np.empty((codes.shape[0], codes.shape[1] * 2))
+    c[:, 0::2] = codes & 15
+    c[:, 1::2] = codes >> 4
+    c = c.reshape(codes.shape[0], -1, group)
+    w = (c - 8) * scales[..., None] if mins is None else c * scales[..., None] + mins[..., None]
+    return w.reshape(codes.shape[0], -1)
