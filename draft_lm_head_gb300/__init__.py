@@ -32,7 +32,7 @@ __all__ = [
     "pruned_head", "cluster_candidate_count", "cluster_workspace_size", "cluster_two_stage",
     "draft_select", "verify_chain", "last_device_error", "debug_set_wait_cycles", "version",
     "Workspace", "shard_workspace_size", "shard_two_stage", "shard_softmax", "PagePlan",
-    "page_plan", "q4_head", "q4_gather_logits", "beam_select", "beam_reorder",
+    "page_plan", "chunk_attention", "q4_head", "q4_gather_logits", "beam_select", "beam_reorder",
 ]
 
 _BF16_OK = (torch.bfloat16, torch.int16, torch.uint16) if hasattr(torch, "uint16") else (
@@ -377,5 +377,5 @@ def verify_chain(p: torch.Tensor, x: torch.Tensor, cand_ids: torch.Tensor, cand_
     return tokens, count
 
 
-from .serving import (PagePlan, beam_reorder, beam_select, page_plan,  # noqa: E402,F401
-                      q4_gather_logits, q4_head)
+from .serving import (PagePlan, beam_reorder, beam_select, chunk_attention,  # noqa: E402,F401
+                      page_plan, q4_gather_logits, q4_head)

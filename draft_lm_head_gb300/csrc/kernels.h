@@ -157,6 +157,32 @@ cudaError_t launch_page_plan(const int32_t* lens, const int32_t* fresh, int S, i
                              int32_t* positions, int32_t* cu, int32_t* granted,
                              int32_t* free_left, int* err, cudaStream_t s);
 
+struct CacheStrides {
+  int64_t page, token, head;  // bytes
+};
+// Validated arguments of lmhead_chunk_attention; strides in bytes.
+struct AttnArgs {
+  int dtype;  // lmhead_dtype
+  const void *q, *k, *v;
+  int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head;
+  void *k_cache, *v_cache;
+  CacheStrides ks, vs;
+  int64_t pages;
+  int page_shift;  // log2 of the page size
+  const int32_t *table, *lens, *cu, *slots;
+  int width, S, T, heads, kv_heads, dim, window;
+  const uint64_t* tree;
+  float scale;
+  void* out;
+  float* lse;
+};
+// The new tokens' K and V to their slots (paged.cu).
+cudaError_t launch_append(const AttnArgs& a, int* err, cudaStream_t s);
+// The chunk's attention over the pages (attention.cu); scratch holds
+// attention_scratch_bytes(...) bytes.
+size_t attention_scratch_bytes(int S, int T, int heads, int kv_heads, int dim);
+cudaError_t launch_attention(const AttnArgs& a, void* scratch, int* err, cudaStream_t s);
+
 // 4-bit rows with group scales (q4.cu): out[m * ldo + j] = row_j . h[m] over
 // rows 0..n-1, or over rows ids[m * K + j] when ids != nullptr.
 struct Q4Args {

@@ -19,6 +19,19 @@ inline bool aligned(const void* p, uintptr_t a) {
 }
 inline int status(cudaError_t e) { return e == cudaSuccess ? LMHEAD_OK : LMHEAD_ERR_CUDA; }
 
+// Strides of a tensor read 16 bytes at a time: non-negative multiples of 8
+// elements, small enough that byte offsets stay far from 2^63.
+inline bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < (1ll << 38); }
+
+int check_attention(int heads, int kv_heads, int dim, int S, int T) {
+  if (S < 1 || S > kMaxRows || T < 1 || kv_heads < 1 || heads < kv_heads || heads % kv_heads ||
+      heads > 65535 || heads / kv_heads > 128)
+    return LMHEAD_ERR_SHAPE;
+  if ((int64_t)T * heads > INT32_MAX) return LMHEAD_ERR_SHAPE;
+  if (dim != 64 && dim != 128) return LMHEAD_ERR_UNSUPPORTED;
+  return LMHEAD_OK;
+}
+
 int check_q4(int dtype, int64_t n, int d, int group, int M) {
   if (dtype != LMHEAD_BF16 && dtype != LMHEAD_FP16) return LMHEAD_ERR_UNSUPPORTED;
   if (group != 32 && group != 64 && group != 128) return LMHEAD_ERR_UNSUPPORTED;
@@ -76,6 +89,88 @@ int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_
                                  page_size, max_tokens, out_slots, out_positions, out_cu,
                                  out_granted, out_free_left, device_error_word(),
                                  (cudaStream_t)stream));
+}
+
+size_t lmhead_chunk_attention_workspace_size(int S, int T, int heads, int kv_heads, int dim) {
+  if (check_attention(heads, kv_heads, dim, S, T) != LMHEAD_OK) return 0;
+  return attention_scratch_bytes(S, T, heads, kv_heads, dim);
+}
+
+int lmhead_chunk_attention(int dtype, const void* q, int64_t q_tok, int64_t q_head, const void* k,
+                           int64_t k_tok, int64_t k_head, const void* v, int64_t v_tok,
+                           int64_t v_head, void* k_cache, int64_t kc_page, int64_t kc_token,
+                           int64_t kc_head, void* v_cache, int64_t vc_page, int64_t vc_token,
+                           int64_t vc_head, int64_t pages, int page_size, const int32_t* table,
+                           int width, const int32_t* lens, const int32_t* cu,
+                           const int32_t* slots, const uint64_t* tree, int S, int T, int heads,
+                           int kv_heads, int dim, int window, float scale, void* out,
+                           float* out_lse, void* workspace, size_t workspace_bytes,
+                           lmhead_stream stream) {
+  if (!q || !k_cache || !v_cache || !table || !lens || !cu || !out) return LMHEAD_ERR_NULL;
+  if ((k == nullptr) != (v == nullptr) || (k && !slots)) return LMHEAD_ERR_NULL;
+  if (dtype != LMHEAD_BF16 && dtype != LMHEAD_FP16) return LMHEAD_ERR_UNSUPPORTED;
+  const int st = check_attention(heads, kv_heads, dim, S, T);
+  if (st != LMHEAD_OK) return st;
+  if (width < 1 || (int64_t)S * width > INT32_MAX || pages < 1 || window < 0 || !(scale > 0.f) ||
+      !isfinite(scale))
+    return LMHEAD_ERR_SHAPE;
+  int shift = 4;
+  while (shift < 8 && (1 << shift) != page_size) ++shift;
+  if ((1 << shift) != page_size) return LMHEAD_ERR_UNSUPPORTED;
+  if (pages > (INT32_MAX >> shift) || width > (INT32_MAX >> shift)) return LMHEAD_ERR_SHAPE;
+  if (tree && window) return LMHEAD_ERR_UNSUPPORTED;
+  const int64_t strides[] = {q_tok, q_head, kc_page, kc_token, kc_head, vc_page, vc_token, vc_head};
+  for (int64_t x : strides)
+    if (!stride_ok(x)) return LMHEAD_ERR_SHAPE;
+  if (kc_token < dim || vc_token < dim || kc_page < dim || vc_page < dim ||
+      (kv_heads > 1 && (kc_head < dim || vc_head < dim)))
+    return LMHEAD_ERR_SHAPE;
+  if (k && (!stride_ok(k_tok) || !stride_ok(k_head) || !stride_ok(v_tok) || !stride_ok(v_head)))
+    return LMHEAD_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(tree, 8))
+    return LMHEAD_ERR_ALIGN;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < attention_scratch_bytes(S, T, heads, kv_heads, dim))
+    return LMHEAD_ERR_WORKSPACE;
+  AttnArgs a = {};
+  a.dtype = dtype;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_tok = q_tok * 2;
+  a.q_head = q_head * 2;
+  a.k_tok = k_tok * 2;
+  a.k_head = k_head * 2;
+  a.v_tok = v_tok * 2;
+  a.v_head = v_head * 2;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.ks = {kc_page * 2, kc_token * 2, kc_head * 2};
+  a.vs = {vc_page * 2, vc_token * 2, vc_head * 2};
+  a.pages = pages;
+  a.page_shift = shift;
+  a.table = table;
+  a.lens = lens;
+  a.cu = cu;
+  a.slots = slots;
+  a.width = width;
+  a.S = S;
+  a.T = T;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.dim = dim;
+  a.window = window;
+  a.tree = tree;
+  a.scale = scale;
+  a.out = out;
+  a.lse = out_lse;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (k) {
+    const cudaError_t e = launch_append(a, device_error_word(), s);
+    if (e != cudaSuccess) return LMHEAD_ERR_CUDA;
+  }
+  return status(launch_attention(a, workspace, device_error_word(), s));
 }
 
 int lmhead_q4_head(int dtype, const void* codes, const void* scales, const void* mins,

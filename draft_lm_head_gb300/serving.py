@@ -2,6 +2,7 @@
 operators around the head").
 
     plan = page_plan(lens, new_lens, table, free_pages, free_count, P, max_tokens)
+    o = chunk_attention(q, k_cache, v_cache, table, lens, plan.cu, k=k, v=v, slots=plan.slots)
     logits = q4_gather_logits(codes, scales, h, ids, group)
     parent, token, score = beam_select(logits, scores, beams, k, ids=ids)
     h, table = beam_reorder(parent, [h, table], beams)
@@ -98,6 +99,90 @@ def page_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor,
         _dense(out.cu, i32, (S + 1,), dev, "cu"), _dense(out.granted, i32, (S,), dev, "granted"),
         _dense(out.free_left, i32, (1,), dev, "free_left"), _stream(stream, dev)), "page_plan")
     return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_bytes(device, S: int, T: int, heads: int, kv_heads: int, dim: int) -> int:
+    with torch.cuda.device(device):
+        return int(load().lmhead_chunk_attention_workspace_size(S, T, heads, kv_heads, dim))
+
+
+def _heads_tensor(t: torch.Tensor, dtype, shape, device, name: str):
+    """Address and strides (elements) of a tensor whose last dimension alone
+    has to be contiguous."""
+    if t.dtype != dtype or t.stride(-1) != 1:
+        raise TypeError(f"{name}: expected {dtype} with a contiguous last dimension, got {t.dtype} "
+                        f"with strides {t.stride()}")
+    if t.shape != shape or t.device != device:
+        raise ValueError(f"{name}: expected shape {tuple(shape)} on {device}, got {tuple(t.shape)} "
+                         f"on {t.device}")
+    return (t.data_ptr(),) + t.stride()[:-1]
+
+
+def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
+                    k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                    slots: Optional[torch.Tensor] = None, tree: Optional[torch.Tensor] = None,
+                    window: int = 0, scale: Optional[float] = None, with_lse: bool = False,
+                    workspace=None, out=None, stream=None):
+    """Attention of T new tokens (q: T x heads x dim) over the paged caches
+    (pages x page_size x kv_heads x dim, any strides with dim contiguous), after
+    writing k and v (T x kv_heads x dim) to `slots`, if given. lens: tokens
+    cached before; cu: starts of the requests' tokens. Causal within a request,
+    over the last `window` keys if window > 0, or by `tree` (int64 bits of the
+    new tokens each new token sees, besides all cached ones). Returns out, or
+    (out, lse) with with_lse or when `out` is such a pair (see
+    lmhead_chunk_attention)."""
+    dev = _cuda(q, "q")
+    _need(q.dim() == 3, "q", "expected tokens x heads x dim")
+    _need(k_cache.dim() == 4, "k_cache", "expected pages x page_size x kv_heads x dim")
+    T, heads, dim = q.shape
+    pages, P, kv_heads, _ = k_cache.shape
+    dt = q.dtype
+    if dt not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"q: expected bf16 or fp16, got {dt}")
+    _need(table.dim() == 2, "table", "expected requests x pages")
+    S, width = table.shape
+    cache = (pages, P, kv_heads, dim)
+    qa, q_tok, q_head = _heads_tensor(q, dt, (T, heads, dim), dev, "q")
+    kca, kc_page, kc_tok, kc_head = _heads_tensor(k_cache, dt, cache, dev, "k_cache")
+    vca, vc_page, vc_tok, vc_head = _heads_tensor(v_cache, dt, cache, dev, "v_cache")
+    ka = va = k_tok = k_head = v_tok = v_head = 0
+    if k is not None or v is not None:
+        _need(k is not None and v is not None and slots is not None, "k, v, slots",
+              "are given together")
+        ka, k_tok, k_head = _heads_tensor(k, dt, (T, kv_heads, dim), dev, "k")
+        va, v_tok, v_head = _heads_tensor(v, dt, (T, kv_heads, dim), dev, "v")
+    # the stride of a dimension of one means nothing
+    if kv_heads == 1:
+        kc_head = vc_head = k_head = v_head = 0
+    if pages == 1:
+        kc_page, vc_page = max(kc_page, dim), max(vc_page, dim)
+    if T == 1:
+        q_tok = k_tok = v_tok = 0
+    if heads == 1:
+        q_head = 0
+    o, lse = out if isinstance(out, (tuple, list)) else (out, None)
+    if o is None:
+        o = _empty((T, heads, dim), dt, dev, stream)
+    if lse is None and with_lse:
+        lse = _empty((T, heads), torch.float32, dev, stream)
+    if slots is not None and slots.shape[0] != T:
+        # a plan's buffers may be longer than the step's tokens
+        _need(slots.dim() == 1 and slots.shape[0] > T, "slots", "expected a slot per token")
+        slots = slots[:T]
+    i32 = torch.int32
+    ws = _workspace(workspace, _attention_bytes(dev, S, T, heads, kv_heads, dim), dev, stream)
+    check(load().lmhead_chunk_attention(
+        _DTYPES[dt], qa, q_tok, q_head, ka, k_tok, k_head, va, v_tok, v_head, kca, kc_page, kc_tok,
+        kc_head, vca, vc_page, vc_tok, vc_head, pages, P,
+        _dense(table, i32, (S, width), dev, "table"), width, _dense(lens, i32, (S,), dev, "lens"),
+        _dense(cu, i32, (S + 1,), dev, "cu"), _dense(slots, i32, (T,), dev, "slots"),
+        _dense(tree, torch.int64, (T,), dev, "tree"), S, T, heads, kv_heads, dim, window,
+        dim ** -0.5 if scale is None else scale, _dense(o, dt, (T, heads, dim), dev, "out"),
+        _dense(lse, torch.float32, (T, heads), dev, "lse"), ws.data_ptr(), ws.numel(),
+        _stream(stream, dev)), "chunk_attention")
+    return o if lse is None else (o, lse)
 
 
 def _q4(name, codes, scales, h, ids, group, mins, out, stream):

@@ -414,6 +414,49 @@ int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_
                      int32_t* out_granted, int32_t* out_free_left, lmhead_stream stream);
 
 /*
+ * Attention of a chunk of new tokens over a paged cache, after writing the
+ * chunk's own K and V to it.
+ *   dtype     LMHEAD_BF16 or LMHEAD_FP16, of q, k, v, the caches and out.
+ *   q         T tokens x heads x dim; k, v  T x kv_heads x dim, or both NULL
+ *             when the cache holds the chunk already. *_tok, *_head: strides
+ *             in elements (dim is contiguous), so q, k and v may be parts of
+ *             one projection's output. heads is a multiple of kv_heads, head a
+ *             reads K/V head a / (heads / kv_heads); heads / kv_heads <= 128;
+ *             dim 64 or 128.
+ *   k_cache, v_cache  pages x page_size x kv_heads x dim; *c_page, *c_token,
+ *             *c_head: strides in elements, any order. page_size 16, 32, 64,
+ *             128 or 256. Bases 16-byte aligned, strides multiples of 8.
+ *   table, lens, cu  as of lmhead_page_plan: pages (S x width), tokens cached
+ *             before the chunk, starts of the requests' tokens (S + 1).
+ *   slots     T int32 (only with k and v): where each token goes, negative:
+ *             nowhere.
+ *   tree      NULL: token i of a request sees the keys at positions <= len + i,
+ *             with window > 0 only the last `window` of those. Otherwise T
+ *             uint64 (window must be 0): it sees the len cached keys and the
+ *             new tokens j < 64 of its request whose bit j is set (its own
+ *             counts too).
+ *   out       T x heads x dim; out_lse T x heads fp32 (natural log) or NULL.
+ *             A row that sees no key gives 0 and -inf.
+ * Tokens outside every [cu[s], cu[s+1]) are left unwritten. Slots of the cache
+ * past a request's tokens are never used, whatever they hold; a non-finite V
+ * of a token of the request itself may reach every row of its chunk.
+ * A page id outside [0, pages) makes its request's rows NaN and records
+ * LMHEAD_ERR_DEVICE_CHECK. scale > 0. No two calls in flight may share the
+ * workspace (lmhead_chunk_attention_workspace_size bytes, 256-byte aligned).
+ */
+size_t lmhead_chunk_attention_workspace_size(int S, int T, int heads, int kv_heads, int dim);
+int lmhead_chunk_attention(int dtype, const void* q, int64_t q_tok, int64_t q_head, const void* k,
+                           int64_t k_tok, int64_t k_head, const void* v, int64_t v_tok,
+                           int64_t v_head, void* k_cache, int64_t kc_page, int64_t kc_token,
+                           int64_t kc_head, void* v_cache, int64_t vc_page, int64_t vc_token,
+                           int64_t vc_head, int64_t pages, int page_size, const int32_t* table,
+                           int width, const int32_t* lens, const int32_t* cu,
+                           const int32_t* slots, const uint64_t* tree, int S, int T, int heads,
+                           int kv_heads, int dim, int window, float scale, void* out,
+                           float* out_lse, void* workspace, size_t workspace_bytes,
+                           lmhead_stream stream);
+
+/*
  * The head with 4-bit weights: row i is s * (c - 8) (mins NULL) or s * c + min
  * with codes c in 0..15, one scale (and min) per `group` codes along d.
  *   codes   n x d/2 bytes, the even element in the low four bits.

@@ -68,3 +68,41 @@ def q4_rows(codes, scales, mins, group):
     c = c.reshape(codes.shape[0], -1, group)
     w = (c - 8) * scales[..., None] if mins is None else c * scales[..., None] + mins[..., None]
     return w.reshape(codes.shape[0], -1)
+
+
+def chunk_attention(q, k_cache, v_cache, table, lens, cu, scale, window=0, tree=None):
+    """q T x H x D, caches pages x P x Hk x D (the chunk's own K and V already in
+    them), all fp64. Returns (out, lse, magnitude, reach): magnitude is sum_j
+    p_j |v_j| and reach max_j scale sum_d |q_d k_jd| over the visible keys."""
+    T, H, D = q.shape
+    P, Hk = k_cache.shape[1], k_cache.shape[2]
+    G = H // Hk
+    out, mag = np.zeros((T, H, D)), np.zeros((T, H, D))
+    lse, reach = np.full((T, H), -np.inf), np.zeros((T, H))
+    for s in range(len(lens)):
+        l, m = int(lens[s]), int(cu[s + 1] - cu[s])
+        j = np.arange(l + m)
+        slot = np.asarray(table[s])[j // P].astype(np.int64) * P + j % P
+        K = k_cache.reshape(-1, Hk, D)[slot]
+        V = v_cache.reshape(-1, Hk, D)[slot]
+        for i in range(m):
+            t = int(cu[s]) + i
+            if tree is None:
+                lo = max(0, l + i + 1 - window) if window else 0
+                keys = np.arange(lo, l + i + 1)
+            else:
+                bits = int(tree[t]) & ((1 << 64) - 1)
+                keys = np.array(list(range(l)) + [l + x for x in range(min(m, 64)) if bits >> x & 1], dtype=int)
+            if not len(keys):
+                continue
+            for b in range(Hk):
+                Ka, Va, qa = K[keys, b], V[keys, b], q[t, b * G:(b + 1) * G]
+                x = scale * (qa @ Ka.T)
+                top = x.max(axis=1, keepdims=True)
+                e = np.exp(x - top)
+                z = e.sum(axis=1, keepdims=True)
+                heads = slice(b * G, (b + 1) * G)
+                out[t, heads], mag[t, heads] = (e / z) @ Va, (e / z) @ np.abs(Va)
+                lse[t, heads] = (top + np.log(z))[:, 0]
+                reach[t, heads] = scale * (np.abs(qa) @ np.abs(Ka).T).max(axis=1)
+    return out, lse, mag, reach
