@@ -6,144 +6,913 @@
 // the cached ones and those whose bit is set in the token's tree word. A row
 // left with no key gives o = 0 and lse = -inf.
 //
-// A warp per (token, head): 32 keys at a time, a key per lane for the scores,
-// running maximum and sum of the softmax in 32 bits, then D/32 dimensions per
-// lane for the sum over values.
+// Both products run on the tensor cores: the rows of one K/V head (tokens x
+// the G = heads / kv_heads query heads that share it) are packed into tiles of
+// 128, so that a decoding step of G heads reads its K and V once, and a block
+// of 128 keys is one 128 x 128 product of scores and one 128 x dim product of
+// values. Three launches:
+//   prepare   writes the chunk's K and V to the cache, and (one CTA) cuts the
+//             work into items (a request's one or two row tiles x a K/V head)
+//             and shares their key blocks out evenly over the CTAs, wherever
+//             an item's end falls;
+//   attend    one CTA per SM, warp-specialised; walks over its range of
+//             blocks: a TMA warp streams pages into a ring of shared memory, a
+//             warp issues the MMAs, two warpgroups (a row per thread) turn
+//             scores into weights. With two row tiles each warpgroup has its
+//             own and both use every block; with one tile they take blocks in
+//             turn and join at the end, so the tensor cores work on one while
+//             the other is exponentiated;
+//   combine   joins the pieces of items that were cut between CTAs.
+// Bound: few rows, by reading K and V once; many rows, by the tensor cores.
+//
+// The softmax runs in the base-2 domain with a running reference instead of
+// the running maximum: while no row's maximum has passed its reference by more
+// than 2^8, accumulators keep it and need no rescaling (weights up to 256 are
+// as exact in fp16 and bf16 as weights up to 1). Scores, sums, references and
+// accumulators are fp32; the weights are rounded once, to 16 bits, as the
+// tensor cores take them.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tc_util.cuh"
 
 namespace lmhead {
 namespace {
 
-template <bool BF16> __device__ __forceinline__ float2 pair_to_float(uint32_t w) {
-  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+constexpr int kRows = 128;  // rows of a tile
+constexpr int kKeys = 128;  // keys of a block
+constexpr int kItemCost = 1;
+// Two softmax warpgroups and one of which two warps work (TMA, MMAs). The
+// block is launched with 168 registers a thread and splits them 216 + 216 + 72.
+constexpr int kThreads = 384;
+constexpr int kRegsMore = 216, kRegsLess = 72;
+constexpr int kPrepThreads = 256;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// An item: up to two row tiles of one request, for every K/V head alike.
+struct Item {
+  int s, tok0, ntok, len;        // request, its first token (of all), tokens, cached before
+  int i0, kb0, nblk, ntile;      // first token in the request, key blocks, row tiles
+  int kend, kbeg, prefix, pad;   // keys [kbeg, kend) are loaded; units before it
+};
+static_assert(sizeof(Item) == 48, "three 16-byte loads");
+
+struct Header {
+  long long units;  // of all heads
+  int items, per_head, parts;
+};
+
+// Work units of an item: one per row tile and block, and kItemCost for what an
+// item costs besides. Unit x of an item is at block ceil((x - kItemCost) / ntile).
+__host__ __device__ inline int item_units(int nblk, int ntile) { return nblk * ntile + kItemCost; }
+__device__ __forceinline__ int block_at(int x, int nblk, int ntile) {
+  const int y = x - kItemCost;
+  return y <= 0 ? 0 : min(nblk, (y + ntile - 1) / ntile);
+}
+
+struct Scratch {
+  Header* head;
+  int4* start;    // per CTA: item, K/V head, units of the item before its range
+  int4* flag;     // per CTA, [0] piece of an item begun earlier, [1] of one that
+                  // goes on later: state (0 none, 1, 2 the item's last), item, head
+  float2* ml;     // per CTA and piece, 256 rows: reference (base 2) and sum
+  float* o;       // per CTA and piece, 256 rows x dim, not normalised
+  Item* items;
+};
+
+struct ScratchSize {
+  size_t start, flag, ml, o, items, total;
+};
+
+__host__ inline ScratchSize scratch_size(int parts, int64_t items, int dim) {
+  ScratchSize z;
+  size_t at = 256;
+  auto take = [&](size_t bytes) {
+    const size_t was = at;
+    at = (at + bytes + 255) / 256 * 256;
+    return was;
+  };
+  z.start = take((size_t)parts * sizeof(int4));
+  z.flag = take((size_t)parts * 2 * sizeof(int4));
+  z.ml = take((size_t)parts * 2 * 256 * sizeof(float2));
+  z.o = take((size_t)parts * 2 * 256 * dim * sizeof(float));
+  z.items = take((size_t)items * sizeof(Item));
+  z.total = at;
+  return z;
+}
+
+inline int64_t most_items(int S, int T, int group) { return (int64_t)S + T / (2 * (kRows / group)) + 1; }
+inline int part_count() { return sm_count() > 0 ? sm_count() : 1; }
+
+// ------------------------------------------------------------------ prepare
+
+__device__ __forceinline__ Item make_item(const AttnArgs& a, int s, int tok0, int m, int len,
+                                          int x, int tile_tok) {
+  Item it;
+  it.s = s;
+  it.i0 = x * 2 * tile_tok;
+  it.tok0 = tok0 + it.i0;
+  it.ntok = min(m - it.i0, 2 * tile_tok);
+  it.len = len;
+  it.ntile = it.ntok > tile_tok ? 2 : 1;
+  it.kend = len + m;
+  const int end = a.tree ? len + min(m, 64) : len + it.i0 + it.ntok;
+  const int beg = a.window > 0 ? max(0, len + it.i0 + 1 - a.window) : 0;
+  it.kb0 = beg / kKeys;
+  it.nblk = (end + kKeys - 1) / kKeys - it.kb0;
+  it.kbeg = beg >> a.page_shift << a.page_shift;
+  it.prefix = 0;
+  it.pad = 0;
+  return it;
+}
+
+// The items of all requests with the units before each, and where each CTA
+// starts: CTA c of `parts` has the units [c U / parts, (c + 1) U / parts) of the
+// sequence (K/V head, item).
+__device__ void make_plan(const AttnArgs& a, const Scratch& sc, int most_parts) {
+  constexpr int kKept = 1024;
+  __shared__ int sh_n[kPrepThreads / 32], sh_w[kPrepThreads / 32];
+  __shared__ int sh_prefix[kKept];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tile_tok = kRows / (a.heads / a.kv_heads);
+  int base_n = 0, base_w = 0;
+  for (int s0 = 0; s0 < a.S; s0 += kPrepThreads) {
+    const int s = s0 + tid;
+    int tok0 = 0, m = 0, len = 0, n = 0, w = 0;
+    if (s < a.S) {
+      tok0 = a.cu[s];
+      m = a.cu[s + 1] - tok0;
+      len = max(a.lens[s], 0);
+      if (tok0 < 0 || tok0 > a.T) m = 0;
+      m = max(0, min(m, a.T - tok0));
+      n = (m + 2 * tile_tok - 1) / (2 * tile_tok);
+      for (int x = 0; x < n; ++x) {
+        const Item it = make_item(a, s, tok0, m, len, x, tile_tok);
+        w += item_units(it.nblk, it.ntile);
+      }
+    }
+    int sn = n, sw = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int pn = __shfl_up_sync(0xFFFFFFFFu, sn, o), pw = __shfl_up_sync(0xFFFFFFFFu, sw, o);
+      if (lane >= o) {
+        sn += pn;
+        sw += pw;
+      }
+    }
+    if (lane == 31) {
+      sh_n[warp] = sn;
+      sh_w[warp] = sw;
+    }
+    cta_sync();
+    int bn = base_n, bw = base_w;
+    for (int i = 0; i < kPrepThreads / 32; ++i) {
+      if (i < warp) {
+        bn += sh_n[i];
+        bw += sh_w[i];
+      }
+      base_n += sh_n[i];
+      base_w += sh_w[i];
+    }
+    int at = bn + sn - n, pre = bw + sw - w;
+    for (int x = 0; x < n; ++x, ++at) {
+      Item it = make_item(a, s, tok0, m, len, x, tile_tok);
+      it.prefix = pre;
+      pre += item_units(it.nblk, it.ntile);
+      sc.items[at] = it;
+      if (at < kKept) sh_prefix[at] = it.prefix;
+    }
+    cta_sync();
+  }
+  const long long units = (long long)base_w * a.kv_heads;
+  const int parts = (int)min((long long)most_parts, units);
+  if (tid == 0) {
+    sc.head->units = units;
+    sc.head->items = base_n;
+    sc.head->per_head = base_w;
+    sc.head->parts = parts;
+  }
+  for (int c = tid; c < parts; c += kPrepThreads) {
+    const long long u = units * c / parts;
+    const int hk = (int)(u / base_w), rem = (int)(u - (long long)hk * base_w);
+    int lo = 0, hi = base_n;  // the last item that starts at or before rem
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      const int p = mid < kKept ? sh_prefix[mid] : sc.items[mid].prefix;
+      if (p <= rem) lo = mid; else hi = mid;
+    }
+    const int p = lo < kKept ? sh_prefix[lo] : sc.items[lo].prefix;
+    sc.start[c] = make_int4(lo, hk, rem - p, 0);
+  }
+}
+
+// CTA 0 plans; the others copy K and V of the new tokens to their slots, 16
+// bytes a thread.
+__global__ void __launch_bounds__(kPrepThreads)
+prepare_kernel(AttnArgs a, Scratch sc, int most_parts, int pieces, int* err) {
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0) {
+    make_plan(a, sc, most_parts);
+    return;
+  }
+  const int per = a.kv_heads * pieces;
+  const int64_t all = (int64_t)a.T * per;
+  const int64_t num_slots = a.pages << a.page_shift;
+  for (int64_t e = (int64_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x; e < all;
+       e += (int64_t)(gridDim.x - 1) * blockDim.x) {
+    const int t = (int)(e / per), x = (int)(e - (int64_t)t * per);
+    const int hd = x / pieces, c = (x - hd * pieces) * 16;
+    const int32_t slot = a.slots[t];
+    if (slot < 0) continue;  // a token without a place
+    if (slot >= num_slots) {
+      record_error(err, kDevErrBadId);
+      continue;
+    }
+    const int64_t pg = slot >> a.page_shift, off = slot & ((1 << a.page_shift) - 1);
+    const char *k = static_cast<const char*>(a.k), *v = static_cast<const char*>(a.v);
+    char *kc = static_cast<char*>(a.k_cache), *vc = static_cast<char*>(a.v_cache);
+    const uint4 kv = *reinterpret_cast<const uint4*>(k + t * a.k_tok + hd * a.k_head + c);
+    const uint4 vv = *reinterpret_cast<const uint4*>(v + t * a.v_tok + hd * a.v_head + c);
+    *reinterpret_cast<uint4*>(kc + pg * a.ks.page + off * a.ks.token + hd * a.ks.head + c) = kv;
+    *reinterpret_cast<uint4*>(vc + pg * a.vs.page + off * a.vs.token + hd * a.vs.head + c) = vv;
+  }
+}
+
+// ------------------------------------------------------------------- attend
+
+template <int D> struct Shape {
+  static constexpr int kHalves = D / 64;             // 64-element (128-byte) columns of a row
+  static constexpr int kBuf = kKeys * D * 2;         // one K or V block
+  static constexpr int kStages = D == 128 ? 5 : 10;  // 160 KB
+  static constexpr int kQ = 2 * kRows * D * 2;
+  static constexpr int kSmem = kQ + kStages * kBuf + 1024;
+};
+
+constexpr int kBadSlots = 16;  // more pieces than the TMA warp can be ahead
+
+template <int NS> struct Ctl {
+  uint64_t full[NS], empty[NS];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t ex1, ex2, drain;
+  uint32_t tmem;
+  int abort;
+  int bad[kBadSlots];
+};
+
+// The CTA's pieces, in order; every role walks over them by itself.
+struct Cursor {
+  const Header* head;
+  const Item* items;
+  long long left;
+  int idx, hk, off, n_items;
+  // the piece
+  Item it;
+  int b0, b1, p_hk, p_idx;
+
+  __device__ void init(const Scratch& sc, int cta) {
+    head = sc.head;
+    items = sc.items;
+    const int parts = head->parts;
+    left = 0;
+    if (cta >= parts) return;
+    const long long u = head->units;
+    left = u * (cta + 1) / parts - u * cta / parts;
+    n_items = head->items;
+    const int4 st = sc.start[cta];
+    idx = st.x;
+    hk = st.y;
+    off = st.z;
+  }
+  __device__ bool next() {
+    while (left > 0) {
+      const int4* src = reinterpret_cast<const int4*>(items + idx);
+      const int4 x = src[0], y = src[1], z = src[2];
+      it.s = x.x; it.tok0 = x.y; it.ntok = x.z; it.len = x.w;
+      it.i0 = y.x; it.kb0 = y.y; it.nblk = y.z; it.ntile = y.w;
+      it.kend = z.x; it.kbeg = z.y;
+      const int w = item_units(it.nblk, it.ntile);
+      const int end = (int)min((long long)w, off + left);
+      b0 = block_at(off, it.nblk, it.ntile);
+      b1 = block_at(end, it.nblk, it.ntile);
+      left -= end - off;
+      off = 0;
+      p_hk = hk;
+      p_idx = idx;
+      if (++idx == n_items) {
+        idx = 0;
+        ++hk;
+      }
+      if (b1 > b0) return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         long long budget) {
+  return __all_sync(0xFFFFFFFFu, tc::mbar_wait(bar, parity, abort, budget));
+}
+
+// Bits [lo, hi) of 32, either end anywhere.
+__device__ __forceinline__ uint32_t span_bits(int lo, int hi) {
+  const uint32_t below_hi = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u;
+  const uint32_t below_lo = lo >= 32 ? ~0u : lo <= 0 ? 0u : (1u << lo) - 1u;
+  return below_hi & ~below_lo;
+}
+
+template <bool BF16> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 32 columns of an output row from column c on: 16-bit results, or fp32 parts.
+template <bool BF16>
+__device__ __forceinline__ void store_cols(const float (&v)[32], char* out16, float* out32, int c) {
+  if (out16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(out16 + (c + 8 * i) * 2) =
+          make_uint4(pack2<BF16>(v[8 * i], v[8 * i + 1]), pack2<BF16>(v[8 * i + 2], v[8 * i + 3]),
+                     pack2<BF16>(v[8 * i + 4], v[8 * i + 5]), pack2<BF16>(v[8 * i + 6], v[8 * i + 7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<float4*>(out32 + c + 4 * i) =
+          make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
 }
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(128) attention_rows_kernel(AttnArgs a, int* err) {
-  __shared__ float qs[4][D];
+__global__ void __launch_bounds__(kThreads, 1)
+attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+              const AttnArgs a, const Scratch sc, int k_head_first, int v_head_first,
+              long long budget, int* err) {
+  using Sh = Shape<D>;
+  constexpr int NS = Sh::kStages;
+  extern __shared__ uint8_t dsmem_raw[];
+  __shared__ Ctl<NS> ctl;
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* q_s = base;
+  uint8_t* ring = base + Sh::kQ;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &ctl.abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(&ctl.full[i], 1);
+      tc::mbar_init(&ctl.empty[i], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      tc::mbar_init(&ctl.q_full[w], kRows);
+      tc::mbar_init(&ctl.s_full[w], 1);
+      tc::mbar_init(&ctl.p_full[w], kRows);
+      tc::mbar_init(&ctl.o_full[w], 1);
+    }
+    tc::mbar_init(&ctl.ex1, 2 * kRows);
+    tc::mbar_init(&ctl.ex2, 2 * kRows);
+    tc::mbar_init(&ctl.drain, 1);
+    ctl.abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(&ctl.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tc::prefetch_tmap(&kmap);
+    tc::prefetch_tmap(&vmap);
+  }
+  tc::fence_before_sync();
+  cta_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = ctl.tmem;  // scores and weights at 0 and 128, outputs at 256 and 384
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * 4 + warp;
-  if (unit >= (int64_t)a.T * a.heads) return;
-  const int t = (int)(unit / a.heads), head = (int)(unit - (int64_t)t * a.heads);
-  const int kvh = head / (a.heads / a.kv_heads);
-  uint16_t* o = static_cast<uint16_t*>(a.out) + unit * D;
-  // the request: the last one that starts at or before t
-  int lo = 0, hi = a.S;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.cu[mid] <= t) lo = mid; else hi = mid;
-  }
-  const int s = lo, i = t - a.cu[s], fresh = a.cu[s + 1] - a.cu[s];
-  if (i < 0 || i >= fresh) return;
-  constexpr int E = D / 32;
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float m = -__builtin_huge_valf(), l = 0.f;
-  bool bad = false;
-  const int len = max(a.lens[s], 0);
-  const char* q = static_cast<const char*>(a.q) + t * a.q_tok + head * a.q_head;
-  for (int e = lane; e < D / 2; e += 32) {
-    const float2 f = pair_to_float<BF16>(*reinterpret_cast<const uint32_t*>(q + e * 4));
-    qs[warp][2 * e] = f.x;
-    qs[warp][2 * e + 1] = f.y;
-  }
-  __syncwarp();
-  const uint64_t bits = a.tree ? a.tree[t] : 0;
-  const int end = a.tree ? len + min(fresh, 64) : len + i + 1;
-  const int begin = a.window > 0 ? max(0, len + i + 1 - a.window) : 0;
-  for (int j0 = begin; j0 < end; j0 += 32) {
-    const int j = j0 + lane;
-    bool see = j < end;
-    if (a.tree && j >= len) see = see && ((bits >> (j - len)) & 1);
-    const int pg = j >> a.page_shift;
-    int32_t id = -1;
-    if (j < end) {
-      if (pg < a.width) id = a.table[(size_t)s * a.width + pg];
-      if (id < 0 || id >= a.pages) {
-        bad = true;
-        id = -1;
+  const int group = a.heads / a.kv_heads, tile_tok = kRows / group;
+  Cursor cur;
+  cur.init(sc, blockIdx.x);
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLess));
+    if (warp == 8) {
+      // ------------------------------------------------------------ pages by TMA
+      // the cache was written by the launch before through the other proxy
+      asm volatile("fence.proxy.async;" ::: "memory");
+      const int unit_tok = min(kKeys, 1 << a.page_shift), units = kKeys / unit_tok;
+      const int u = lane / Sh::kHalves, half = lane % Sh::kHalves;
+      const bool mine = u < units;
+      uint32_t n = 0;
+      int piece = 0;
+      bool ok = true;
+      while (ok && cur.next()) {
+        if (lane == 0) *(volatile int*)&ctl.bad[piece % kBadSlots] = 0;
+        const int32_t* row = a.table + (size_t)cur.it.s * a.width;
+        for (int b = cur.b0; b < cur.b1 && ok; ++b) {
+          const int key = (cur.it.kb0 + b) * kKeys + u * unit_tok;
+          const bool want = mine && key < cur.it.kend && key + unit_tok > cur.it.kbeg;
+          int32_t id = 0;
+          bool bad = false;
+          if (want) {
+            const int pg = key >> a.page_shift;
+            id = pg < a.width ? row[pg] : -1;
+            bad = id < 0 || id >= a.pages;
+          }
+          const uint32_t load = __ballot_sync(0xFFFFFFFFu, want && !bad);
+          if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) {
+            *(volatile int*)&ctl.bad[piece % kBadSlots] = 1;
+            record_error(err, kDevErrBadId);
+          }
+          const int off = key & ((1 << a.page_shift) - 1);
+  #pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const int slot = (int)(n % NS);
+            if (n >= (uint32_t)NS) {
+              ok = wait_all(&ctl.empty[slot], ((n / NS) & 1) ^ 1, abort_flag, budget);
+              if (!ok) break;
+            }
+            if (lane == 0)
+              tc::mbar_arrive_expect_tx(&ctl.full[slot], (uint32_t)(__popc(load) * unit_tok * 128));
+            __syncwarp();
+            if (want && !bad) {
+              uint8_t* dst = ring + slot * Sh::kBuf + half * (kKeys * 128) + u * unit_tok * 128;
+              const bool hf = kv ? v_head_first : k_head_first;
+              tc::tma_load_4d(dst, kv ? &vmap : &kmap, &ctl.full[slot], half * 64,
+                              hf ? cur.p_hk : off, hf ? off : cur.p_hk, id);
+            }
+          }
+        }
+        ++piece;
       }
-    }
-    const int64_t off = j & ((1 << a.page_shift) - 1);
-    float x = -__builtin_huge_valf();
-    if (see && id >= 0) {
-      const char* k = static_cast<const char*>(a.k_cache) + id * a.ks.page + off * a.ks.token +
-                      kvh * a.ks.head;
-      x = 0.f;
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4*>(k + c * 16);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = pair_to_float<BF16>(w[e]);
-          x = fmaf(f.x, qs[warp][c * 8 + 2 * e], x);
-          x = fmaf(f.y, qs[warp][c * 8 + 2 * e + 1], x);
+      if (!ok && lane == 0) {
+        *abort_flag = 1;
+        record_error(err, kDevErrTimeout);
+      }
+      __syncwarp();
+      if (*abort_flag && lane == 0) {
+        // drain (bounded) the copies issued last on every stage
+        const uint32_t first = n > (uint32_t)NS ? n - NS : 0;
+        for (uint32_t j = first; j < n; ++j) {
+          const long long t0 = clock64();
+          while (!tc::mbar_try_wait(&ctl.full[j % NS], (j / NS) & 1) &&
+                 clock64() - t0 < tc::kWaitCycles) {
+          }
         }
       }
-      x *= a.scale;
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMAs
+      // A step is one tile x one block; steps alternate between the warpgroups.
+      // Scores of step k + 2 are issued behind the values of step k, which read
+      // the weights that they overwrite (MMAs of one thread run in order).
+      const uint32_t idesc_s = tc::idesc_f16_f32(BF16, kRows, kKeys, false);
+      const uint32_t idesc_o = tc::idesc_f16_f32(BF16, kRows, D, true);
+      const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_addr(q_s));
+      const uint64_t k_desc = tc::sw128_kmajor_desc(tc::smem_addr(ring));
+      const uint64_t v_desc = tc::sw128_mnmajor_desc(tc::smem_addr(ring), kKeys * 128);
+      uint32_t blocks = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;
+      bool ok = true;
+      while (ok && cur.next()) {
+        const bool pair = cur.it.ntile == 2;
+        const int nb = cur.b1 - cur.b0, steps = pair ? 2 * nb : nb;
+        auto scores = [&](int k) -> bool {
+          const int w = k & 1, j = pair ? k >> 1 : k;
+          const uint32_t n = 2 * (blocks + j);
+          const int slot = (int)(n % NS);
+          if (k == 0 || (pair && k == 1)) {
+            const uint32_t use = k ? nq1++ : nq0++;
+            if (!wait_all(&ctl.q_full[k], use & 1, abort_flag, budget)) return false;
+          }
+          if (!wait_all(&ctl.full[slot], (n / NS) & 1, abort_flag, budget)) return false;
+          tc::fence_after_sync();
+          if (lane == 0) {
+            // addresses count 16 bytes and stay below 2^14 of them
+            const uint64_t qd = q_desc + (pair ? w : 0) * (kRows * D * 2 / 16);
+            const uint64_t kd = k_desc + slot * (Sh::kBuf / 16);
+  #pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              constexpr int kHalf = kRows * 128 / 16;
+              tc::mma_bf16(tmem + w * 128, qd + (c / 4) * kHalf + (c % 4) * 2,
+                           kd + (c / 4) * kHalf + (c % 4) * 2, idesc_s, c > 0);
+            }
+            tc::mma_commit(&ctl.s_full[w]);
+            if (!pair || w == 1) tc::mma_commit(&ctl.empty[slot]);
+          }
+          __syncwarp();
+          return true;
+        };
+        auto values = [&](int k) -> bool {
+          const int w = k & 1, j = pair ? k >> 1 : k;
+          const uint32_t n = 2 * (blocks + j) + 1;
+          const int slot = (int)(n % NS);
+          if (!wait_all(&ctl.full[slot], (n / NS) & 1, abort_flag, budget)) return false;
+          // keys that are no token's, or whose page was not loaded, hold anything
+          // at all, and weight 0 times NaN is NaN: they are zeroed
+          const int first = (cur.it.kb0 + cur.b0 + j) * kKeys;
+          const int lo = max(0, min(kKeys, cur.it.kbeg - first));
+          const int hi = min(kKeys, cur.it.kend - first);
+          if ((lo > 0 || hi < kKeys) && (!pair || w == 0)) {
+            uint8_t* v = ring + slot * Sh::kBuf;
+            for (int e = lane; e < kKeys * 8; e += 32) {
+              const int r = e >> 3;
+              if (r < lo || r >= hi)
+  #pragma unroll
+                for (int h = 0; h < Sh::kHalves; ++h)
+                  *reinterpret_cast<uint4*>(v + h * (kKeys * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+          }
+          const uint32_t use = w ? np1++ : np0++;
+          if (!wait_all(&ctl.p_full[w], use & 1, abort_flag, budget)) return false;
+          tc::fence_after_sync();
+          if (lane == 0) {
+            const uint64_t vd = v_desc + slot * (Sh::kBuf / 16);
+  #pragma unroll
+            for (int c = 0; c < kKeys / 16; ++c)
+              tc::mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + c * 8, vd + c * (16 * 128 / 16),
+                             idesc_o, k >= 2 || c > 0);
+            if (!pair || w == 1) tc::mma_commit(&ctl.empty[slot]);
+            if (k + 2 >= steps) tc::mma_commit(&ctl.o_full[w]);
+          }
+          __syncwarp();
+          return true;
+        };
+  #pragma unroll 1
+        for (int k = -2; k < steps && ok; ++k)
+          ok = (k < 0 || values(k)) && (k + 2 >= steps || scores(k + 2));
+        blocks += nb;
+      }
+      if (!ok && lane == 0) {
+        *abort_flag = 1;
+        record_error(err, kDevErrTimeout);
+        tc::mma_drain(&ctl.drain);  // TMEM is freed below
+      }
+      __syncwarp();
     }
-    const float nm = fmaxf(m, warp_max(x)), ref = nm == -__builtin_huge_valf() ? 0.f : nm;
-    const float p = expf(x - ref), f = expf(m - ref);
-    l = l * f + warp_sum(p);
-    m = nm;
+  } else {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMore));
+    const int w = warp >> 2;                // warpgroup
+    const int r = threadIdx.x & 127;        // row of the tile = TMEM lane
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + w * 128, t_o = tmem + lanes + 256 + w * 128;
+    const float sl = a.scale * kLog2e;
+    const int row_tok = min(r / group, tile_tok - 1);  // rows past the tile go along
+    const int row_head = r - r / group * group;
+    uint32_t ns = 0, no0 = 0, no1 = 0, nx = 0;
+    int piece = 0;
+    int4 flag0 = make_int4(0, 0, 0, 0), flag1 = make_int4(0, 0, 0, 0);
+    bool ok = true;
+    for (; ok && cur.next(); ++piece) {
+      const Item& it = cur.it;
+      const bool pair = it.ntile == 2;
+      const int nb = cur.b1 - cur.b0;
+      const int tile = pair ? w : 0;
+      const bool first = cur.b0 == 0, last = cur.b1 == it.nblk;
+      const int tok = tile * tile_tok + row_tok;
+      const bool valid = r < tile_tok * group && tok < it.ntok;
+      const int tokc = min(tok, it.ntok - 1);
+      const int head = cur.p_hk * group + row_head;
+      const int64_t out_row = (int64_t)(it.tok0 + tok) * a.heads + head;
+      if (pair || w == 0) {
+        const char* q = static_cast<const char*>(a.q) + (int64_t)(it.tok0 + tok) * a.q_tok +
+                        head * a.q_head;
+        uint8_t* dst = q_s + tile * (kRows * D * 2) + r * 128;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= f;
-    const int64_t vo = id >= 0 ? id * a.vs.page + off * a.vs.token + kvh * a.vs.head : -1;
-    for (int y = 0; y < 32; ++y) {
-      const float py = __shfl_sync(0xFFFFFFFFu, p, y);
-      const int64_t at = __shfl_sync(0xFFFFFFFFu, vo, y);
-      const bool sy = __shfl_sync(0xFFFFFFFFu, (int)see, y);
-      if (!sy || at < 0) continue;
-      const char* v = static_cast<const char*>(a.v_cache) + at + lane * E * 2;
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (valid) v = *reinterpret_cast<const uint4*>(q + c * 16);
+          *reinterpret_cast<uint4*>(dst + (c / 8) * (kRows * 128) + (((c % 8) ^ (r & 7)) << 4)) = v;
+        }
+        tc::fence_async_smem();
+        tc::mbar_arrive(&ctl.q_full[tile]);
+      }
+      // the row's keys: [lo, hi), and the new tokens of its tree word
+      const int hi = a.tree ? it.len : it.len + it.i0 + tokc + 1;
+      const int lo = a.window > 0 ? max(0, hi - a.window) : 0;
+      uint64_t bits = 0;
+      if (a.tree) {
+        bits = a.tree[it.tok0 + tokc];
+        const int m = it.kend - it.len;
+        if (m < 64) bits &= (1ull << m) - 1;
+      }
+      const bool idle = !__any_sync(0xFFFFFFFFu, valid);  // no row of this warp is one
+      float ref = kNegInf, sum = 0.f;
+      const int steps = pair ? nb : (nb + 1 - w) / 2;
+      for (int j = 0; j < steps; ++j) {
+        const int b = cur.b0 + (pair ? j : 2 * j + w);
+        const int key0 = (it.kb0 + b) * kKeys;
+        ok = wait_all(&ctl.s_full[w], ns++ & 1, abort_flag, budget);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (!idle) {
+          float s[kKeys];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 z = pair_to_float<BF16>(*reinterpret_cast<const uint32_t*>(v + e * 2));
-        acc[e] = fmaf(py, z.x, acc[e]);
-        acc[e + 1] = fmaf(py, z.y, acc[e + 1]);
+          for (int c = 0; c < 4; ++c)
+            tc::tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
+          tc::tmem_ld_wait();
+          uint32_t see[4];
+          bool whole = true;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int k0 = key0 + 32 * c;
+            see[c] = span_bits(lo - k0, hi - k0);
+            if (a.tree) {
+              const int x = k0 - it.len;
+              if (x > -32 && x < 64) see[c] |= (uint32_t)(x < 0 ? bits << -x : bits >> x);
+            }
+            whole &= see[c] == ~0u;
+          }
+          if (!__all_sync(0xFFFFFFFFu, whole)) {
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c)
+              s[c] = (see[c / 32] >> (c % 32)) & 1 ? s[c] : kNegInf;
+          }
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+          const bool grow = top > ref + 8.f || (ref == kNegInf && top > kNegInf);
+          if (__any_sync(0xFFFFFFFFu, grow)) {
+            const float f = grow ? tc::exp2_approx(ref - top) : 1.f;
+            if (grow) {
+              ref = top;
+              sum *= f;
+            }
+            if (j > 0) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                tc::tmem_ld32(t_o + c * 32, v);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                tc::tmem_st32(t_o + c * 32, v);
+              }
+            }
+          }
+          const float neg = ref == kNegInf ? 0.f : -ref;
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x = tc::exp2_approx(fmaf(s[c * 32 + 2 * i], sl, neg));
+              const float y = tc::exp2_approx(fmaf(s[c * 32 + 2 * i + 1], sl, neg));
+              part[i & 1] += x;
+              part[2 + (i & 1)] += y;
+              pk[i] = pack2<BF16>(x, y);
+            }
+            tc::tmem_st16(t_s + c * 16, pk);
+          }
+          sum += (part[0] + part[1]) + (part[2] + part[3]);
+          tc::tmem_st_wait();
+        }
+        tc::fence_before_sync();
+        tc::mbar_arrive(&ctl.p_full[w]);
+      }
+      if (!ok) break;
+      // with one tile and two blocks or more both warpgroups have values
+      const bool join = !pair && nb > 1;
+      const bool both = pair || nb > 1;  // warpgroup 1 has values
+      if (w == 0 || join) ok = wait_all(&ctl.o_full[0], no0 & 1, abort_flag, budget);
+      if (ok && both && (w == 1 || join)) ok = wait_all(&ctl.o_full[1], no1 & 1, abort_flag, budget);
+      ++no0;
+      no1 += both;
+      if (!ok) break;
+      tc::fence_after_sync();
+      const bool bad = *(volatile int*)&ctl.bad[piece % kBadSlots] != 0;
+      const float nan = __int_as_float(0x7fc00000);
+      // where the row goes: the output, or the piece's place in the scratch
+      const int64_t prow = ((int64_t)blockIdx.x * 2 + (first ? 1 : 0)) * 256 + tile * kRows + r;
+      char* out16 = first && last ? static_cast<char*>(a.out) + out_row * (D * 2) : nullptr;
+      float* out32 = sc.o + prow * D;
+      auto finish = [&](float m, float l) -> float {  // what the sums are scaled by
+        if (first && last) {
+          if (valid && a.lse && (pair || w == 0))
+            a.lse[out_row] = bad ? nan : l == 0.f ? kNegInf : m * kLn2 + logf(l);
+          return bad ? nan : l == 0.f ? 0.f : 1.f / l;
+        }
+        if (valid && (pair || w == 0)) sc.ml[prow] = bad ? make_float2(0.f, nan) : make_float2(m, l);
+        return 1.f;
+      };
+      if (!join) {
+        if (pair || w == 0) {
+          const float f = finish(ref, sum);
+          if (!idle) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tc::tmem_ld32(t_o + c * 32, v);
+              tc::tmem_ld_wait();
+              float x[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = sum == 0.f && !bad ? 0.f : __uint_as_float(v[i]) * f;
+              if (valid) store_cols<BF16>(x, out16, out32, c * 32);
+            }
+          }
+        }
+      } else {
+        // the warpgroups join: they exchange references and sums in the columns
+        // of the scores, and each finishes one half of both outputs' columns
+        if (!idle) {
+          tc::tmem_st2(t_s, ref, sum);
+          tc::tmem_st_wait();
+        }
+        tc::fence_before_sync();
+        tc::mbar_arrive(&ctl.ex1);
+        ok = wait_all(&ctl.ex1, nx & 1, abort_flag, budget);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (!idle) {
+          const float2 other = tc::tmem_ld2(tmem + lanes + (1 - w) * 128);
+          const float m = fmaxf(ref, other.x), ms = m == kNegInf ? 0.f : m;
+          const float f0 = tc::exp2_approx(ref - ms), f1 = tc::exp2_approx(other.x - ms);
+          const float l = sum * f0 + other.y * f1;
+          const float f = finish(m, l);
+          const bool none = l == 0.f && !bad;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t v[32], u[32];
+            const uint32_t at = w * (D / 2) + c * 32;
+            tc::tmem_ld32(t_o + at, v);
+            tc::tmem_ld32(tmem + lanes + 256 + (1 - w) * 128 + at, u);
+            tc::tmem_ld_wait();
+            float x[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              x[i] = none ? 0.f : (__uint_as_float(v[i]) * f0 + __uint_as_float(u[i]) * f1) * f;
+            if (valid) store_cols<BF16>(x, out16, out32, at);
+          }
+        }
+        tc::fence_before_sync();
+        tc::mbar_arrive(&ctl.ex2);
+        ok = wait_all(&ctl.ex2, nx++ & 1, abort_flag, budget);
+        if (!ok) break;
+      }
+      // the next piece's first values overwrite what was read here
+      tc::fence_before_sync();
+      if (!first) flag0 = make_int4(last ? 2 : 1, cur.p_idx, cur.p_hk, 0);
+      else if (!last) flag1 = make_int4(1, cur.p_idx, cur.p_hk, 0);
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      record_error(err, kDevErrTimeout);
+    }
+    if (threadIdx.x == 0) {
+      sc.flag[blockIdx.x * 2] = flag0;
+      sc.flag[blockIdx.x * 2 + 1] = flag1;
+    }
+  }
+  tc::fence_before_sync();
+  cta_sync();
+  if (warp == 9) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ combine
+// CTA (c, y) joins 32 rows of the item that begins in CTA c's range and goes
+// on in those after it: o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
+template <bool BF16, int D>
+__global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Scratch sc) {
+  extern __shared__ int places[];  // the pieces' places, in order
+  __shared__ int sh_n;
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x, parts = sc.head->parts;
+  if (c >= parts) return;
+  const int4 f = sc.flag[c * 2 + 1];
+  if (f.x == 0) return;
+  const int group = a.heads / a.kv_heads, tile_tok = kRows / group;
+  const Item it = sc.items[f.y];
+  const int row0 = blockIdx.y * 32;
+  if (row0 >= it.ntile * kRows || (row0 >> 7) * tile_tok + (row0 & 127) / group >= it.ntok ||
+      (row0 & 127) >= tile_tok * group)
+    return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    int n = 1;
+    if (lane == 0) places[0] = c * 2 + 1;
+    for (int x = c + 1; x < parts; x += 32) {
+      const int state = x + lane < parts ? sc.flag[(x + lane) * 2].x : 0;
+      const uint32_t ends = __ballot_sync(0xFFFFFFFFu, state == 2);
+      const uint32_t some = __ballot_sync(0xFFFFFFFFu, state != 0) &
+                            (ends ? (2u << (__ffs(ends) - 1)) - 1u : ~0u);
+      if (some >> lane & 1) places[n + __popc(some & ((1u << lane) - 1u))] = (x + lane) * 2;
+      n += __popc(some);
+      if (ends) break;
+    }
+    if (lane == 0) sh_n = n;
+  }
+  cta_sync();
+  const int n = sh_n;
+  constexpr int E = D / 32;
+  for (int i = warp; i < 32; i += 8) {
+    const int r = row0 + i, tile = r >> 7, rr = r & 127;
+    const int tok = tile * tile_tok + rr / group;
+    if (rr >= tile_tok * group || tok >= it.ntok) continue;
+    float top = kNegInf;
+    for (int p = lane; p < n; p += 32) top = fmaxf(top, sc.ml[(int64_t)places[p] * 256 + r].x);
+    top = warp_max(top);
+    const float ref = top == kNegInf ? 0.f : top;
+    float l = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int p0 = 0; p0 < n; p0 += 32) {
+      float g = 0.f;
+      int place = 0;
+      if (p0 + lane < n) {
+        place = places[p0 + lane];
+        const float2 ml = sc.ml[(int64_t)place * 256 + r];
+        g = tc::exp2_approx(ml.x - ref);
+        l += g * ml.y;
+      }
+      const int cnt = min(32, n - p0);
+#pragma unroll 4
+      for (int p = 0; p < cnt; ++p) {
+        const float gp = __shfl_sync(0xFFFFFFFFu, g, p);
+        const int pl = __shfl_sync(0xFFFFFFFFu, place, p);
+        const float* o = sc.o + ((int64_t)pl * 256 + r) * D + lane * E;
+        if (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(o);
+          acc[0] = fmaf(gp, v.x, acc[0]);
+          acc[1] = fmaf(gp, v.y, acc[1]);
+          acc[2 % E] = fmaf(gp, v.z, acc[2 % E]);
+          acc[3 % E] = fmaf(gp, v.w, acc[3 % E]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(o);
+          acc[0] = fmaf(gp, v.x, acc[0]);
+          acc[1] = fmaf(gp, v.y, acc[1]);
+        }
       }
     }
-  }
-  bad = __any_sync(0xFFFFFFFFu, bad);
-  if (bad && lane == 0) record_error(err, kDevErrBadId);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+    l = warp_sum(l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t out_row =
+        (int64_t)(it.tok0 + tok) * a.heads + f.z * group + (rr - rr / group * group);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + out_row * (D * 2)) +
+                    lane * (E / 2);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float v = bad ? __int_as_float(0x7fc00000) : acc[e] * inv;
-    if (BF16)
-      reinterpret_cast<__nv_bfloat16*>(o)[lane * E + e] = __float2bfloat16(v);
-    else
-      reinterpret_cast<__half*>(o)[lane * E + e] = __float2half(v);
+    for (int e = 0; e < E; e += 2)
+      dst[e / 2] = l == 0.f ? 0u : (l != l ? 0x7fff7fffu : pack2<BF16>(acc[e] * inv, acc[e + 1] * inv));
+    if (a.lse && lane == 0) a.lse[out_row] = l == 0.f ? kNegInf : ref * kLn2 + logf(l);
   }
-  if (a.lse && lane == 0)
-    a.lse[unit] = bad ? __int_as_float(0x7fc00000)
-                      : (l == 0.f ? -__builtin_huge_valf() : m + logf(l));
+}
+
+template <bool BF16, int D>
+cudaError_t launch_all(const AttnArgs& a, const Scratch& sc, int parts, int* err, cudaStream_t s) {
+  const bool kf = a.ks.head <= a.ks.token, vf = a.vs.head <= a.vs.token;
+  const int page = 1 << a.page_shift, box = page < kKeys ? page : kKeys;
+  CUtensorMap kmap, vmap;
+  if (!make_cache_map(&kmap, a.k_cache, BF16, D, page, a.kv_heads, a.pages, a.ks, box, kf) ||
+      !make_cache_map(&vmap, a.v_cache, BF16, D, page, a.kv_heads, a.pages, a.vs, box, vf))
+    return cudaErrorInvalidValue;
+  int64_t ctas = 0;
+  if (a.k) {
+    const int64_t all = (int64_t)a.T * a.kv_heads * (D / 8);
+    ctas = (all + kPrepThreads - 1) / kPrepThreads;
+    if (ctas > (int64_t)parts * 8) ctas = (int64_t)parts * 8;
+  }
+  cudaError_t e = launch_kernel(true, prepare_kernel, dim3((unsigned)ctas + 1), dim3(kPrepThreads),
+                                0, s, a, sc, parts, D / 8, err);
+  if (e != cudaSuccess) return e;
+  static int smem_set[64] = {0};
+  e = ensure_dynamic_smem(attend_kernel<BF16, D>, Shape<D>::kSmem, smem_set);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(true, attend_kernel<BF16, D>, dim3(parts), dim3(kThreads), Shape<D>::kSmem, s,
+                    kmap, vmap, a, sc, (int)kf, (int)vf, role_wait_cycles(), err);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(true, combine_kernel<BF16, D>, dim3(parts, 2 * kRows / 32), dim3(256),
+                       (size_t)(parts + 1) * sizeof(int), s, a, sc);
 }
 
 }  // namespace
 
 size_t attention_scratch_bytes(int S, int T, int heads, int kv_heads, int dim) {
-  (void)S, (void)T, (void)heads, (void)kv_heads, (void)dim;
-  return 256;
+  return scratch_size(part_count(), most_items(S, T, heads / kv_heads), dim).total;
 }
 
 cudaError_t launch_attention(const AttnArgs& a, void* scratch, int* err, cudaStream_t s) {
-  (void)scratch;
-  const unsigned grid = (unsigned)(((int64_t)a.T * a.heads + 3) / 4);
-#define RUN(B, D) return launch_kernel(true, attention_rows_kernel<B, D>, dim3(grid), dim3(128), 0, s, a, err)
-  if (a.dtype == LMHEAD_BF16) {
-    if (a.dim == 64) RUN(true, 64);
-    RUN(true, 128);
-  }
-  if (a.dim == 64) RUN(false, 64);
-  RUN(false, 128);
-#undef RUN
+  const int parts = part_count();
+  const ScratchSize z = scratch_size(parts, most_items(a.S, a.T, a.heads / a.kv_heads), a.dim);
+  char* p = static_cast<char*>(scratch);
+  const Scratch sc = {reinterpret_cast<Header*>(p),          reinterpret_cast<int4*>(p + z.start),
+                      reinterpret_cast<int4*>(p + z.flag),   reinterpret_cast<float2*>(p + z.ml),
+                      reinterpret_cast<float*>(p + z.o),     reinterpret_cast<Item*>(p + z.items)};
+  if (a.dtype == LMHEAD_BF16)
+    return a.dim == 64 ? launch_all<true, 64>(a, sc, parts, err, s)
+                       : launch_all<true, 128>(a, sc, parts, err, s);
+  return a.dim == 64 ? launch_all<false, 64>(a, sc, parts, err, s)
+                     : launch_all<false, 128>(a, sc, parts, err, s);
 }
 
 }  // namespace lmhead

@@ -176,10 +176,9 @@ struct AttnArgs {
   void* out;
   float* lse;
 };
-// The new tokens' K and V to their slots (paged.cu).
-cudaError_t launch_append(const AttnArgs& a, int* err, cudaStream_t s);
-// The chunk's attention over the pages (attention.cu); scratch holds
-// attention_scratch_bytes(...) bytes.
+// The new tokens' K and V to their slots, if given, and the attention of the
+// chunk over the pages (attention.cu); scratch holds attention_scratch_bytes(...)
+// bytes.
 size_t attention_scratch_bytes(int S, int T, int heads, int kv_heads, int dim);
 cudaError_t launch_attention(const AttnArgs& a, void* scratch, int* err, cudaStream_t s);
 
@@ -231,6 +230,12 @@ long long role_wait_cycles();
 // (box_cols * 2 == 128 bytes), 128-byte swizzle, zero fill out of bounds.
 bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                    uint32_t box_rows, uint32_t box_cols);
+// TMA map of a paged cache (16-bit elements, one head's box of box_tokens rows of
+// 64): dimensions (dim, heads, tokens, pages) when head_first, else (dim, tokens,
+// heads, pages).
+bool make_cache_map(CUtensorMap* map, const void* base, bool bf16, int dim, int page_tokens,
+                    int heads, int64_t pages, const CacheStrides& st, int box_tokens,
+                    bool head_first);
 int sm_count();  // SMs of the current device (cached)
 
 }  // namespace lmhead

@@ -1,6 +1,5 @@
 // The pages of a paged K/V cache: which pages and slots a step's new tokens
-// get (block tables and slot maps, from request lengths alone), and the write
-// of their K and V to those slots.
+// get (block tables and slot maps, from request lengths alone).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -135,42 +134,7 @@ page_plan_kernel(const int32_t* lens, const int32_t* fresh, int S, int32_t* tabl
   }
 }
 
-// ---- K and V of new tokens to their slots: a copy, 16 bytes a thread.
-__global__ void __launch_bounds__(256) append_kernel(AttnArgs a, int pieces, int* err) {
-  pdl_wait();
-  pdl_trigger();
-  const int per = a.kv_heads * pieces;
-  const int64_t all = (int64_t)a.T * per;
-  const int64_t num_slots = a.pages << a.page_shift;
-  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < all;
-       e += (int64_t)gridDim.x * blockDim.x) {
-    const int t = (int)(e / per), x = (int)(e - (int64_t)t * per);
-    const int hd = x / pieces, c = (x - hd * pieces) * 16;
-    const int32_t slot = a.slots[t];
-    if (slot < 0) continue;  // a token without a place
-    if (slot >= num_slots) {
-      record_error(err, kDevErrBadId);
-      continue;
-    }
-    const int64_t pg = slot >> a.page_shift, off = slot & ((1 << a.page_shift) - 1);
-    const char *k = static_cast<const char*>(a.k), *v = static_cast<const char*>(a.v);
-    char *kc = static_cast<char*>(a.k_cache), *vc = static_cast<char*>(a.v_cache);
-    const uint4 kv = *reinterpret_cast<const uint4*>(k + t * a.k_tok + hd * a.k_head + c);
-    const uint4 vv = *reinterpret_cast<const uint4*>(v + t * a.v_tok + hd * a.v_head + c);
-    *reinterpret_cast<uint4*>(kc + pg * a.ks.page + off * a.ks.token + hd * a.ks.head + c) = kv;
-    *reinterpret_cast<uint4*>(vc + pg * a.vs.page + off * a.vs.token + hd * a.vs.head + c) = vv;
-  }
-}
-
 }  // namespace
-
-cudaError_t launch_append(const AttnArgs& a, int* err, cudaStream_t s) {
-  const int pieces = a.dim / 8;
-  const int64_t all = (int64_t)a.T * a.kv_heads * pieces;
-  const int64_t want = (all + 255) / 256, most = (int64_t)sm_count() * 16;
-  return launch_kernel(true, append_kernel, dim3((unsigned)(want < most ? want : most)), dim3(256),
-                       0, s, a, pieces, err);
-}
 
 cudaError_t launch_page_plan(const int32_t* lens, const int32_t* fresh, int S, int32_t* table,
                              int width, const int32_t* free_pages, int free_cap,

@@ -165,12 +165,9 @@ int lmhead_chunk_attention(int dtype, const void* q, int64_t q_tok, int64_t q_he
   a.scale = scale;
   a.out = out;
   a.lse = out_lse;
-  cudaStream_t s = (cudaStream_t)stream;
-  if (k) {
-    const cudaError_t e = launch_append(a, device_error_word(), s);
-    if (e != cudaSuccess) return LMHEAD_ERR_CUDA;
-  }
-  return status(launch_attention(a, workspace, device_error_word(), s));
+  // the stride of a single head means nothing
+  if (kv_heads == 1) a.ks.head = a.ks.token, a.vs.head = a.vs.token;
+  return status(launch_attention(a, workspace, device_error_word(), (cudaStream_t)stream));
 }
 
 int lmhead_q4_head(int dtype, const void* codes, const void* scales, const void* mins,

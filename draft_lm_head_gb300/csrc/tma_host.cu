@@ -43,6 +43,26 @@ bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t c
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_cache_map(CUtensorMap* map, const void* base, bool bf16, int dim, int page_tokens,
+                    int heads, int64_t pages, const CacheStrides& st, int box_tokens,
+                    bool head_first) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t tok = (cuuint64_t)page_tokens, hd = (cuuint64_t)heads;
+  const cuuint64_t dims[4] = {(cuuint64_t)dim, head_first ? hd : tok, head_first ? tok : hd,
+                              (cuuint64_t)pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)(head_first ? st.head : st.token),
+                                 (cuuint64_t)(head_first ? st.token : st.head),
+                                 (cuuint64_t)st.page};
+  const cuuint32_t bt = (cuuint32_t)box_tokens;
+  const cuuint32_t box[4] = {64, head_first ? 1 : bt, head_first ? bt : 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {
   static int cache[64] = {0};
   int dev = 0;
