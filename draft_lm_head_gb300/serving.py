@@ -30,21 +30,24 @@ class PagePlan(NamedTuple):
     free_left: torch.Tensor
 
 
-def _need(ok: bool, name: str, what: str) -> None:
-    if not ok:
-        raise ValueError(f"{name}: {what}")
+# Every call of these operators is a few microseconds of GPU work at its
+# smallest, so the checks before it are written to cost little: one comparison
+# chain a tensor, messages built only when they are raised.
+
+def _wrong(t: torch.Tensor, dtype, shape, device, name: str) -> Exception:
+    if t.dtype != dtype or not t.is_contiguous():
+        return TypeError(f"{name}: expected a contiguous {dtype} tensor, got {t.dtype} "
+                         f"(contiguous={t.is_contiguous()})")
+    return ValueError(f"{name}: expected shape {tuple(shape)} on {device}, got {tuple(t.shape)} "
+                      f"on {t.device}")
 
 
 def _dense(t: Optional[torch.Tensor], dtype, shape, device, name: str) -> int:
     """The address of a contiguous tensor of this type, shape and device."""
     if t is None:
         return 0
-    if t.dtype != dtype or not t.is_contiguous():
-        raise TypeError(f"{name}: expected a contiguous {dtype} tensor, got {t.dtype} "
-                        f"(contiguous={t.is_contiguous()})")
-    if t.shape != shape or t.device != device:
-        raise ValueError(f"{name}: expected shape {tuple(shape)} on {device}, got {tuple(t.shape)} "
-                         f"on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise _wrong(t, dtype, shape, device, name)
     return t.data_ptr()
 
 
@@ -54,8 +57,16 @@ def _cuda(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
+# the current stream's handle without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -70,7 +81,7 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
 def _workspace(workspace, nbytes: int, device, stream) -> torch.Tensor:
     if workspace is None:
         return _empty(max(nbytes, 256), torch.uint8, device, stream)
-    return workspace.get(nbytes, device) if hasattr(workspace, "get") else workspace
+    return workspace if isinstance(workspace, torch.Tensor) else workspace.get(nbytes, device)
 
 
 def page_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor,
@@ -81,23 +92,25 @@ def page_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor,
     int32 (see lmhead_page_plan)."""
     dev = _cuda(lens, "lens")
     i32 = torch.int32
-    _need(lens.dim() == 1, "lens", "expected one length per request")
-    _need(table.dim() == 2, "table", "expected requests x pages")
-    _need(free_pages.dim() == 1, "free_pages", "expected a list of page ids")
+    if lens.dim() != 1 or table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("lens, table, free_pages: expected requests, requests x pages and pages")
     S, width, cap = lens.shape[0], table.shape[1], free_pages.shape[0]
     if out is None:
-        _need(max_tokens >= 1 and S >= 1, "max_tokens", "must be positive, as must the requests")
-        buf = _empty(2 * max_tokens + 2 * S + 2, i32, dev, stream)
-        out = PagePlan(*buf.split([max_tokens, max_tokens, S + 1, S, 1]))
+        if max_tokens < 1 or S < 1:
+            raise ValueError("max_tokens: must be positive, as must the number of requests")
+        out = PagePlan(_empty(max_tokens, i32, dev, stream), _empty(max_tokens, i32, dev, stream),
+                       _empty(S + 1, i32, dev, stream), _empty(S, i32, dev, stream),
+                       _empty(1, i32, dev, stream))
+    slots, positions, cu, granted, free_left = out
     check(load().lmhead_page_plan(
         _dense(lens, i32, (S,), dev, "lens"), _dense(new_lens, i32, (S,), dev, "new_lens"), S,
         _dense(table, i32, (S, width), dev, "table"), width,
         _dense(free_pages, i32, (cap,), dev, "free_pages"), cap,
         _dense(free_count, i32, (1,), dev, "free_count"), page_size, max_tokens,
-        _dense(out.slots, i32, (max_tokens,), dev, "slots"),
-        _dense(out.positions, i32, (max_tokens,), dev, "positions"),
-        _dense(out.cu, i32, (S + 1,), dev, "cu"), _dense(out.granted, i32, (S,), dev, "granted"),
-        _dense(out.free_left, i32, (1,), dev, "free_left"), _stream(stream, dev)), "page_plan")
+        _dense(slots, i32, (max_tokens,), dev, "slots"),
+        _dense(positions, i32, (max_tokens,), dev, "positions"),
+        _dense(cu, i32, (S + 1,), dev, "cu"), _dense(granted, i32, (S,), dev, "granted"),
+        _dense(free_left, i32, (1,), dev, "free_left"), _stream(stream, dev)), "page_plan")
     return out
 
 
@@ -110,13 +123,14 @@ def _attention_bytes(device, S: int, T: int, heads: int, kv_heads: int, dim: int
 def _heads_tensor(t: torch.Tensor, dtype, shape, device, name: str):
     """Address and strides (elements) of a tensor whose last dimension alone
     has to be contiguous."""
-    if t.dtype != dtype or t.stride(-1) != 1:
+    st = t.stride()
+    if t.dtype is not dtype or st[-1] != 1:
         raise TypeError(f"{name}: expected {dtype} with a contiguous last dimension, got {t.dtype} "
-                        f"with strides {t.stride()}")
+                        f"with strides {st}")
     if t.shape != shape or t.device != device:
-        raise ValueError(f"{name}: expected shape {tuple(shape)} on {device}, got {tuple(t.shape)} "
-                         f"on {t.device}")
-    return (t.data_ptr(),) + t.stride()[:-1]
+        raise _wrong(t, dtype, shape, device, name) if t.is_contiguous() else ValueError(
+            f"{name}: expected shape {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
+    return (t.data_ptr(),) + st[:-1]
 
 
 def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -134,14 +148,14 @@ def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     (out, lse) with with_lse or when `out` is such a pair (see
     lmhead_chunk_attention)."""
     dev = _cuda(q, "q")
-    _need(q.dim() == 3, "q", "expected tokens x heads x dim")
-    _need(k_cache.dim() == 4, "k_cache", "expected pages x page_size x kv_heads x dim")
+    if q.dim() != 3 or k_cache.dim() != 4 or table.dim() != 2:
+        raise ValueError("q, k_cache, table: expected tokens x heads x dim, pages x page_size x "
+                         "kv_heads x dim and requests x pages")
     T, heads, dim = q.shape
     pages, P, kv_heads, _ = k_cache.shape
     dt = q.dtype
     if dt not in (torch.bfloat16, torch.float16):
         raise TypeError(f"q: expected bf16 or fp16, got {dt}")
-    _need(table.dim() == 2, "table", "expected requests x pages")
     S, width = table.shape
     cache = (pages, P, kv_heads, dim)
     qa, q_tok, q_head = _heads_tensor(q, dt, (T, heads, dim), dev, "q")
@@ -149,8 +163,8 @@ def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     vca, vc_page, vc_tok, vc_head = _heads_tensor(v_cache, dt, cache, dev, "v_cache")
     ka = va = k_tok = k_head = v_tok = v_head = 0
     if k is not None or v is not None:
-        _need(k is not None and v is not None and slots is not None, "k, v, slots",
-              "are given together")
+        if k is None or v is None or slots is None:
+            raise ValueError("k, v, slots: are given together")
         ka, k_tok, k_head = _heads_tensor(k, dt, (T, kv_heads, dim), dev, "k")
         va, v_tok, v_head = _heads_tensor(v, dt, (T, kv_heads, dim), dev, "v")
     # the stride of a dimension of one means nothing
@@ -169,7 +183,8 @@ def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         lse = _empty((T, heads), torch.float32, dev, stream)
     if slots is not None and slots.shape[0] != T:
         # a plan's buffers may be longer than the step's tokens
-        _need(slots.dim() == 1 and slots.shape[0] > T, "slots", "expected a slot per token")
+        if slots.dim() != 1 or slots.shape[0] < T:
+            raise ValueError("slots: expected a slot per token")
         slots = slots[:T]
     i32 = torch.int32
     ws = _workspace(workspace, _attention_bytes(dev, S, T, heads, kv_heads, dim), dev, stream)
@@ -190,16 +205,13 @@ def _q4(name, codes, scales, h, ids, group, mins, out, stream):
     dt = h.dtype
     if dt not in (torch.bfloat16, torch.float16):
         raise TypeError(f"h: expected bf16 or fp16, got {dt}")
-    _need(h.dim() == 2, "h", "expected vectors x d")
-    _need(codes.dim() == 2, "codes", "expected rows x d/2")
-    _need(group in (32, 64, 128), "group", "must be 32, 64 or 128")
+    if h.dim() != 2 or codes.dim() != 2 or (ids is not None and ids.dim() != 2):
+        raise ValueError("h, codes, ids: expected vectors x d, rows x d/2 and vectors x candidates")
     M, d = h.shape
     n = codes.shape[0]
-    _need(d % group == 0 and d >= group, "group", f"does not divide d = {d}")
-    K = n
-    if ids is not None:
-        _need(ids.dim() == 2, "ids", "expected vectors x candidates")
-        K = ids.shape[1]
+    if group not in (32, 64, 128) or d % group or d < group:
+        raise ValueError(f"group: must be 32, 64 or 128 and divide d = {d}, got {group}")
+    K = n if ids is None else ids.shape[1]
     if out is None:
         out = _empty((M, K), torch.float32, dev, stream)
     args = [_DTYPES[dt], _dense(codes, torch.uint8, (n, d // 2), dev, "codes"),
@@ -247,33 +259,37 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, k: int,
     scores: S*beams fp32 log-probabilities so far; ids: the entries' tokens;
     finished: bool, beams that have ended (see lmhead_beam_select)."""
     dev = _cuda(logits, "logits")
-    _need(logits.dim() == 2, "logits", "expected beams x entries")
+    if logits.dim() != 2:
+        raise ValueError("logits: expected beams x entries")
     if logits.dtype not in _DTYPES:
         raise TypeError(f"logits: expected bf16, fp16 or fp32, got {logits.dtype}")
     rows, n = logits.shape
-    _need(beams >= 1 and rows >= 1 and rows % beams == 0, "beams", f"does not divide {rows} rows")
-    _need(n >= 1, "logits", "no entries")
-    _need(1 <= k <= 32, "k", "must be 1 to 32")
-    if logits.stride(1) != 1 and n > 1:
+    if beams < 1 or rows < 1 or rows % beams or n < 1:
+        raise ValueError(f"beams: {beams} does not divide {rows} rows of {n} entries")
+    if not 1 <= k <= 32:
+        raise ValueError("k: must be 1 to 32")
+    stride, one = logits.stride()
+    if one != 1 and n > 1:
         raise TypeError("logits: expected contiguous rows")
+    if rows == 1:
+        stride = n
+    elif stride < n:
+        raise ValueError("logits: rows overlap")
     S = rows // beams
-    stride = logits.stride(0) if rows > 1 else n
-    _need(stride >= n, "logits", "rows overlap")
+    i32 = torch.int32
     if out is None:
-        parent, token = _empty((2, S, k), torch.int32, dev, stream).unbind(0)
+        parent, token = _empty((S, k), i32, dev, stream), _empty((S, k), i32, dev, stream)
         score = _empty((S, k), torch.float32, dev, stream)
     else:
         parent, token, score = out
-    nbytes = _beam_bytes(dev, S, beams, n, k)
-    ws = _workspace(workspace, nbytes, dev, stream)
-    if finished is not None and finished.dtype == torch.bool:
-        finished = finished.view(torch.uint8)
-    i32 = torch.int32
+    ws = _workspace(workspace, _beam_bytes(dev, S, beams, n, k), dev, stream)
+    # a bool is a byte
+    kind = torch.uint8 if finished is None or finished.dtype is torch.uint8 else torch.bool
     check(load().lmhead_beam_select(
         _DTYPES[logits.dtype], logits.data_ptr(), stride,
         _dense(scores, torch.float32, (rows,), dev, "scores"),
         _dense(ids, i32, (rows, n), dev, "ids"),
-        _dense(finished, torch.uint8, (rows,), dev, "finished"), S, beams, n, k, eos,
+        _dense(finished, kind, (rows,), dev, "finished"), S, beams, n, k, eos,
         _dense(parent, i32, (S, k), dev, "parent"), _dense(token, i32, (S, k), dev, "token"),
         _dense(score, torch.float32, (S, k), dev, "score"), ws.data_ptr(), ws.numel(),
         _stream(stream, dev)), "beam_select")
@@ -285,20 +301,27 @@ def beam_reorder(parent: torch.Tensor, states: Sequence[torch.Tensor], beams: in
     """Each state tensor (S*beams rows of any type, contiguous) by the parents
     chosen (S x k): a list of tensors of S*k rows, zeros where parent is -1."""
     dev = _cuda(parent, "parent")
-    _need(parent.dim() == 2 and parent.numel() > 0, "parent", "expected sequences x k")
+    if parent.dim() != 2 or parent.numel() == 0:
+        raise ValueError("parent: expected sequences x k")
     S, k = parent.shape
-    n = len(states)
-    _need(1 <= n <= 8, "states", "1 to 8 tensors")
-    _need(beams >= 1, "beams", "must be positive")
-    if out is None:
-        out = [_empty((S * k,) + tuple(t.shape[1:]), t.dtype, dev, stream) for t in states]
-    _need(len(out) == n, "out", "one tensor per state")
-    src, dst, size = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
-    for i, (t, o) in enumerate(zip(states, out)):
-        src[i] = _dense(t, t.dtype, (S * beams,) + tuple(t.shape[1:]), dev, f"states[{i}]")
-        dst[i] = _dense(o, t.dtype, (S * k,) + tuple(t.shape[1:]), dev, f"out[{i}]")
-        size[i] = t.numel() // (S * beams) * t.element_size()
+    n, rows = len(states), S * beams
+    if not 1 <= n <= 8 or beams < 1:
+        raise ValueError("states, beams: expected 1 to 8 tensors and a positive number of beams")
+    if out is not None and len(out) != n:
+        raise ValueError("out: expected one tensor per state")
+    res, table = [], (ctypes.c_int64 * (3 * n))()
+    for i, t in enumerate(states):
+        shape, dt = t.shape, t.dtype
+        if t.dim() < 1 or shape[0] != rows or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"states[{i}]: expected {rows} contiguous rows on {dev}")
+        want = (S * k, *shape[1:])
+        o = out[i] if out is not None else _empty(want, dt, dev, stream)
+        res.append(o)
+        table[i] = t.data_ptr()
+        table[n + i] = _dense(o, dt, want, dev, "out") if out is not None else o.data_ptr()
+        table[2 * n + i] = t.numel() // rows * t.element_size()
+    at = ctypes.addressof(table)
     check(load().lmhead_beam_reorder(
-        _dense(parent, torch.int32, (S, k), dev, "parent"), S, beams, k, n, src, dst, size,
-        _stream(stream, dev)), "beam_reorder")
-    return out
+        _dense(parent, torch.int32, (S, k), dev, "parent"), S, beams, k, n, at, at + 8 * n,
+        at + 16 * n, _stream(stream, dev)), "beam_reorder")
+    return res
