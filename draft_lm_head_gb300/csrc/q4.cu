@@ -3,21 +3,25 @@
 // H[m,G] = sum_{k in G} h[m,k]; o = 0 for symmetric codes, and min + 8 s for
 // codes with an offset (w = c s + min).
 //
-// Bound by reading the codes: d/2 + 2 d/group bytes a row. Every code costs an
-// unpack, so the products have to be cheap: a code minus 8 is exact in 16
-// bits, and a warp multiplies 16 rows x 16 codes with up to 8 hidden vectors
-// in one matrix instruction from registers (products exact, sums in 32 bits).
-// The codes go from global memory to the operand registers with no shuffle
-// and no shared memory: the sum over k may take k in any order, so the order
-// in which a lane's own codes unpack is the order of k, and h is laid out to
-// match once per CTA. Group sums are scaled in 32 bits after the matrix
-// products; no weight is ever rounded. (Operands of the tcgen05 instructions
-// would have to be written to shared or tensor memory first, at a store per
-// two codes; here they never leave registers.)
-//   Unpacking a 32-bit word of 8 codes: (w >> 4j) & 0x000f000f joined with the
-// bit pattern of 128 (bf16) or 1024 (fp16), where one unit is the lowest
-// mantissa bit, gives 128 + c (1024 + c) for codes j and j + 4; one packed
-// subtraction leaves c - 8.
+// Bound by reading the codes (d/2 + 2 d/group bytes a row) and by the
+// instructions that unpack them. A code minus 8 is exact in 16 bits, and a warp
+// multiplies 16 rows x 16 codes with up to 8 hidden vectors in one matrix
+// instruction from registers (products exact, sums in 32 bits). The sum over k
+// may take k in any order, so the order in which a lane's own codes unpack is
+// the order of k, and h is laid out to match once per CTA: no shuffle is
+// needed. Each warp streams its own 32 rows through a ring of shared memory
+// with asynchronous copies (128 bytes of a row at a time; loads straight to the
+// operand registers touch 64 bytes of 8 rows at once and were bound by the
+// L1's tags). Group sums are scaled in 32 bits after the matrix products; no
+// weight is ever rounded. (Operands of the tcgen05 instructions would have to
+// be written to shared or tensor memory first, at a store per two codes; here
+// they never leave registers.)
+//   Unpacking a 32-bit word of 8 codes into fp16: joined with the bit pattern
+// of 1024, whose lowest mantissa bit is one unit, the low code of a byte gives
+// 1024 + c and the high one 1024 + 16 c, and one packed addition or
+// multiply-add leaves c - 8: one shift, four logical and four packed
+// instructions. (bf16 has 7 mantissa bits, so every code but the lowest would
+// need its own shift; h is taken to fp16 instead, see below.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,67 +34,88 @@ namespace {
 constexpr int kBlockK = 128;  // codes of a row that four lanes take together
 constexpr int kRowsWarp = 32;
 
-template <bool BF16> struct Half2 {
-  // codes j and j + 4 of word w, minus 8
-  static __device__ __forceinline__ uint32_t codes(uint32_t w, int j) {
-    uint32_t v = ((w >> (4 * j)) & 0x000f000fu) | (BF16 ? 0x43004300u : 0x64006400u);
-    if (BF16) {
-      const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v),
-                                       __floats2bfloat162_rn(136.f, 136.f));
-      return *reinterpret_cast<const uint32_t*>(&r);
-    }
-    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&v), __floats2half2_rn(1032.f, 1032.f));
-    return *reinterpret_cast<const uint32_t*>(&r);
+// The 8 codes of word w, minus 8, as fp16 pairs (0,4), (1,5), (2,6), (3,7).
+__device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t (&u)[4]) {
+  const __half2 low = __floats2half2_rn(-1032.f, -1032.f);
+  const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
+  const __half2 high = __floats2half2_rn(-72.f, -72.f);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t x = w >> (8 * j);
+    uint32_t a = (x & 0x000f000fu) | 0x64006400u, b = (x & 0x00f000f0u) | 0x64006400u;
+    const __half2 p = __hadd2(*reinterpret_cast<__half2*>(&a), low);
+    const __half2 q = __hfma2(*reinterpret_cast<__half2*>(&b), sixteenth, high);
+    u[2 * j] = *reinterpret_cast<const uint32_t*>(&p);
+    u[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&q);
   }
-  static __device__ __forceinline__ float to_float(uint16_t b) {
-    if (BF16) return __uint_as_float((uint32_t)b << 16);
-    return __half2float(__ushort_as_half(b));
-  }
-  static __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-    if (BF16)
-      asm volatile(
-          "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-          "{%8,%9}, {%0,%1,%2,%3};"
-          : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-          : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-      asm volatile(
-          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-          "{%8,%9}, {%0,%1,%2,%3};"
-          : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-          : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  }
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <bool BF16> __device__ __forceinline__ float to_float(uint16_t b) {
+  if (BF16) return __uint_as_float((uint32_t)b << 16);
+  return __half2float(__ushort_as_half(b));
+}
+template <bool BF16> __device__ __forceinline__ float2 pair_to_float(uint32_t w) {
+  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Two fp32 multiply-adds in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// N consecutive 16-bit values of a row: one load where the row allows it, or
+// those below `left` one by one, zeros behind them.
+template <int N> struct Packed {
+  uint32_t w[(N + 1) / 2];
 };
+template <int N>
+__device__ __forceinline__ Packed<N> load_packed(const uint16_t* p, bool whole, int left) {
+  Packed<N> v;
+  if (whole) {
+    if (N == 4) {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+      v.w[0] = x.x;
+      v.w[(N + 1) / 2 - 1] = x.y;
+    } else if (N == 2) {
+      v.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    } else {
+      v.w[0] = __ldg(p);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < (N + 1) / 2; ++i) {
+      v.w[i] = 2 * i < left ? __ldg(p + 2 * i) : 0u;
+      if (2 * i + 1 < N && 2 * i + 1 < left) v.w[i] |= (uint32_t)__ldg(p + 2 * i + 1) << 16;
+    }
+  }
+  return v;
+}
+template <bool BF16, int N> __device__ __forceinline__ float packed_at(const Packed<N>& v, int i) {
+  const float2 f = pair_to_float<BF16>(v.w[i >> 1]);
+  return i & 1 ? f.y : f.x;
+}
 
 // Word i (of 4) of lane chunk t in a 128-code block, so that each matrix
 // instruction stays within one group: bytes t*16 + i*4 for groups of 128,
 // 8 bytes from each of two groups of 64, 4 from each of four groups of 32.
 template <int G> __host__ __device__ __forceinline__ constexpr int word_of(int t, int i) {
   return G == 128 ? 4 * t + i : G == 64 ? (i >> 1) * 8 + 2 * t + (i & 1) : 4 * i + t;
-}
-
-template <int G> __device__ __forceinline__ uint4 load_codes(const uint8_t* row, int t, int left) {
-  // row: at the block; left: codes of the row from here on (>= G)
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (G == 128) {
-    v = ldg_nc_v4(row + t * 16);
-  } else if (G == 64) {
-    const uint2 a = __ldg(reinterpret_cast<const uint2*>(row + t * 8));
-    v.x = a.x;
-    v.y = a.y;
-    if (left > 64) {
-      const uint2 b = __ldg(reinterpret_cast<const uint2*>(row + 32 + t * 8));
-      v.z = b.x;
-      v.w = b.y;
-    }
-  } else {
-    v.x = __ldg(reinterpret_cast<const uint32_t*>(row + t * 4));
-    if (left > 32) v.y = __ldg(reinterpret_cast<const uint32_t*>(row + 16 + t * 4));
-    if (left > 64) v.z = __ldg(reinterpret_cast<const uint32_t*>(row + 32 + t * 4));
-    if (left > 96) v.w = __ldg(reinterpret_cast<const uint32_t*>(row + 48 + t * 4));
-  }
-  return v;
 }
 
 struct Q4Launch {
@@ -105,192 +130,343 @@ struct Q4Launch {
   float* out;
   int tiles;       // row tiles (of each vector in the gather)
   int split;       // warps that share a tile's codes
+  int scales_aligned;  // scales and mins at 16 bytes
 };
 
 // Shared memory: h of the call's vectors, [vector][block][i][t] 16-byte words
 // (8 codes' worth, codes 0,4,1,5,2,6,3,7), rows 64 bytes off a multiple of
 // 128 so that the 8 lanes of a 16-byte read phase (2 vectors x 4 chunks) hit
-// all banks once; then H per group and vector; then the warps' partial sums.
+// all banks once; then H per group and vector; each warp's ring of codes; and
+// the warps' partial sums where several share a tile.
 __host__ __device__ inline int h_stride(int blocks) { return blocks * 256 + 64; }
+// Bytes of h and H together: the rings behind them start at a multiple of 128.
+__host__ __device__ inline int h_bytes(int blocks, int vecs, int sums) {
+  return (vecs * h_stride(blocks) + sums * (int)sizeof(float) + 127) / 128 * 128;
+}
 
-template <bool BF16, int G, int NT, int WARPS, bool MINS, bool GATHER>
-__global__ void __launch_bounds__(WARPS * 32, GATHER || NT == 1 ? 2 : 1)
+// A stage of a warp's ring: SB blocks of 32 rows x 64 bytes. The 16-byte
+// chunks of a row are permuted by it so that the reads of all three group
+// sizes (16 bytes of 2 rows, 8 of 4 rows or 4 of 8 rows at a time) and the
+// copies that write them meet every bank once.
+__device__ __forceinline__ uint32_t ring_at(int blk, int row, int chunk) {
+  const int x = (row & 2) | ((row >> 2) & 1);
+  return (uint32_t)(blk * 2048 + (row ^ blk) * 64 + ((chunk ^ x) * 16));
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  const int n = in ? 16 : 0;  // the rest is zero-filled
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+
+template <bool BF16, int G, int NT, int WARPS, int SB, int NS, bool MINS, bool GATHER>
+__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 2 : 1)
 q4_kernel(Q4Launch a, int* err) {
   extern __shared__ __align__(128) unsigned char smem[];
-  using P = Half2<BF16>;
-  constexpr int GB = kBlockK / G;             // groups a block
-  constexpr int HC = GATHER ? 1 : NT * 8;     // vectors of H
+  __shared__ uint32_t sh_top[WARPS];
+  __shared__ float sh_back[NT * 8];  // what each vector's sums are scaled back by
+  constexpr int GB = kBlockK / G;          // groups a block
+  constexpr int HC = GATHER ? 1 : NT * 8;  // vectors of H
+  constexpr int CPY = SB * 4;              // copies a lane and stage
+  constexpr int CR = 32 / CPY;             // rows a copy of the warp covers
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int kd = a.k_hi - a.k_lo;
-  const int blocks = (kd + kBlockK - 1) / kBlockK, groups = kd / G;
+  const int blocks = (kd + kBlockK - 1) / kBlockK;
   const int stride = h_stride(blocks);
   const int nv = GATHER ? 1 : min(a.M, NT * 8);
   unsigned char* hs = smem;
   float* Hs = reinterpret_cast<float*>(smem + (size_t)nv * stride);  // [group][HC]
-  float* part = Hs + (MINS ? (size_t)(blocks * GB) * HC : 0);
+  unsigned char* rings = smem + h_bytes(blocks, nv, MINS ? blocks * GB * HC : 0);
+  unsigned char* ring = rings + (size_t)warp * (NS * SB * 2048);
+  float* part = reinterpret_cast<float*>(rings + (size_t)WARPS * (NS * SB * 2048));
   pdl_wait();
   pdl_trigger();
   const int vec0 = GATHER ? blockIdx.y : 0;
-  // ---- h, laid out as the codes unpack
-  const int words = blocks * 16;
-  for (int e = tid; e < nv * words; e += WARPS * 32) {
-    const int v = e / words, w = e - v * words, b = w >> 4, p = w & 15;
-    const int src = b * 16 + word_of<G>(p & 3, p >> 2);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (src * 8 < kd)
-      x = *reinterpret_cast<const uint4*>(a.h + (size_t)(vec0 + v) * a.d + a.k_lo + src * 8);
-    uint4 y;
-    y.x = __byte_perm(x.x, x.z, 0x5410);  // 0, 4
-    y.y = __byte_perm(x.x, x.z, 0x7632);  // 1, 5
-    y.z = __byte_perm(x.y, x.w, 0x5410);  // 2, 6
-    y.w = __byte_perm(x.y, x.w, 0x7632);  // 3, 7
-    *reinterpret_cast<uint4*>(hs + (size_t)v * stride + w * 16) = y;
-  }
-  if (MINS) {
-    for (int e = tid; e < blocks * GB * HC; e += WARPS * 32) {
-      const int v = e % HC, gi = e / HC;
-      float s = 0.f;
-      if (v < nv && gi < groups) {
-        const uint16_t* src = a.h + (size_t)(vec0 + v) * a.d + a.k_lo + gi * G;
-        for (int i = 0; i < G; ++i) s += P::to_float(src[i]);
-      }
-      Hs[e] = s;
-    }
-  }
-  cta_sync();
+  const int64_t count = GATHER ? a.K : a.n;
+  const int row_bytes = a.d / 2, row_groups = a.d / G;
 
   const int tiles_cta = WARPS / a.split;
   const int k_warp = warp % a.split, slot = warp / a.split;
-  const int b_lo = blocks * k_warp / a.split, b_hi = blocks * (k_warp + 1) / a.split;
-  const int64_t row_bytes = a.d / 2;
-  const int row_groups = a.d / G;
-  const int64_t count = GATHER ? a.K : a.n;
-  for (int tile0 = blockIdx.x * tiles_cta; tile0 < a.tiles; tile0 += gridDim.x * tiles_cta) {
+  const int all_stages = (blocks + SB - 1) / SB;
+  const int s_lo = all_stages * k_warp / a.split, s_hi = all_stages * (k_warp + 1) / a.split;
+  const int step = gridDim.x * tiles_cta;
+
+  // ---- the copies of this warp's codes run NS - 1 stages ahead, over the ends
+  // of its tiles
+  const int c_row = lane / CPY, c_chunk = lane % CPY;  // of the warp's first copy
+  int c_tile = blockIdx.x * tiles_cta + slot, c_stage = s_lo, c_slot = 0;
+  int32_t c_id[GATHER ? CPY : 1];
+  auto row_id = [&](int64_t i) -> int32_t {  // the row behind entry i, 0 for none
+    if (!GATHER) return i < count ? (int32_t)i : 0;
+    if (i >= count) return 0;
+    const int32_t id = a.ids[(size_t)vec0 * a.K + i];
+    return id >= 0 && id < a.n ? id : 0;
+  };
+  auto copy_ids = [&]() {
+    if (GATHER)
+#pragma unroll
+      for (int j = 0; j < CPY; ++j)
+        c_id[j] = row_id((int64_t)c_tile * kRowsWarp + j * CR + c_row);
+  };
+  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
+  auto copy_stage = [&]() {
+    if (c_tile < a.tiles && s_lo < s_hi) {
+      const int at = a.k_lo / 2 + (c_stage * SB * 4 + c_chunk) * 16;
+      const bool in_k = at < a.k_hi / 2;
+#pragma unroll
+      for (int j = 0; j < CPY; ++j) {
+        const int r = j * CR + c_row;
+        const int64_t i = (int64_t)c_tile * kRowsWarp + r;
+        const int64_t row = GATHER ? (int64_t)c_id[j] : i;
+        const bool in = in_k && i < count;
+        copy16(ring_s + c_slot * (SB * 2048) + ring_at(c_chunk >> 2, r, c_chunk & 3),
+               a.codes + (in ? row * row_bytes + at : 0), in);
+      }
+      if (++c_stage == s_hi) {
+        c_stage = s_lo;
+        c_tile += step;
+        if (c_tile < a.tiles) copy_ids();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    c_slot = c_slot + 1 == NS ? 0 : c_slot + 1;
+  };
+  if (c_tile < a.tiles) copy_ids();
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i) copy_stage();
+
+  // ---- h, laid out as the codes unpack, in fp16: bf16 values are first scaled
+  // by the power of two that takes the vector's largest below 2^15, which keeps
+  // all of their bits down to 2^-29 of the largest (and 2^-40 of it throughout);
+  // the sums are scaled back. A warp takes a vector, or all of them the one.
+  {
+    const int words = blocks * 16;
+    const int lanes = GATHER ? WARPS * 32 : 32, me = GATHER ? tid : lane;
+    for (int v = GATHER ? 0 : warp; v < nv; v += GATHER ? 1 : WARPS) {
+      const uint16_t* src = a.h + (size_t)(vec0 + v) * a.d + a.k_lo;
+      unsigned char* dst = hs + (size_t)v * stride;
+      float scale = 1.f;
+      if (BF16) {
+        uint32_t top = 0;  // the order of magnitudes is that of their bits
+        for (int w = me; w * 8 < kd; w += lanes) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src + w * 8);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = max(top, max((u[i] << 16) & 0x7FFF0000u, u[i] & 0x7FFF0000u));
+        }
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if (GATHER) {
+          if (lane == 0) sh_top[warp] = top;
+          cta_sync();
+#pragma unroll
+          for (int i = 0; i < WARPS; ++i) top = max(top, sh_top[i]);
+        }
+        const int e = (int)(top >> 23) - 127;                  // floor of its logarithm
+        const int k = top == 0 ? 0 : max(-126, min(127, 14 - e));
+        scale = __uint_as_float((uint32_t)(k + 127) << 23);
+        if (me == 0) sh_back[v] = __uint_as_float((uint32_t)(127 - max(k, -126)) << 23);
+        if (me == 0 && k == 127) sh_back[v] = 5.877471754111438e-39f;  // 2^-127
+      } else if (me == 0) {
+        sh_back[v] = 1.f;
+      }
+      for (int w = me; w < words; w += lanes) {
+        const int b = w >> 4, p = w & 15, at = b * 16 + word_of<G>(p & 3, p >> 2);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (at * 8 < kd) x = *reinterpret_cast<const uint4*>(src + at * 8);
+        if (BF16) {
+          uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = pair_to_float<true>(u[i]);
+            const __half2 r = __floats2half2_rn(f.x * scale, f.y * scale);
+            u[i] = *reinterpret_cast<const uint32_t*>(&r);
+          }
+          x = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        uint4 y;
+        y.x = __byte_perm(x.x, x.z, 0x5410);  // 0, 4
+        y.y = __byte_perm(x.x, x.z, 0x7632);  // 1, 5
+        y.z = __byte_perm(x.y, x.w, 0x5410);  // 2, 6
+        y.w = __byte_perm(x.y, x.w, 0x7632);  // 3, 7
+        *reinterpret_cast<uint4*>(dst + w * 16) = y;
+      }
+    }
+  }
+  cta_sync();
+  if (MINS) {
+    // a group's words lie at i in [q * 4 / GB, (q + 1) * 4 / GB), every t
+    for (int e = tid; e < blocks * GB * HC; e += WARPS * 32) {
+      const int v = e % HC, gi = e / HC, b = gi / GB, q = gi - b * GB;
+      float s = 0.f;
+      if (v < nv) {
+        const unsigned char* src = hs + (size_t)v * stride + b * 256 + q * (256 / GB);
+#pragma unroll
+        for (int w = 0; w < 16 / GB; ++w) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src + w * 16);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = pair_to_float<false>(u[i]);
+            s += f.x + f.y;
+          }
+        }
+      }
+      Hs[e] = s;
+    }
+    cta_sync();
+  }
+
+  // This lane's vector columns (columns past the last repeat it and are not
+  // stored) and its places in a stage: row g, with rows g + 8 r 512 bytes apart.
+  const unsigned char* hp[NT];
+#pragma unroll
+  for (int y = 0; y < NT; ++y) hp[y] = hs + (size_t)min(y * 8 + g, nv - 1) * stride + t * 16;
+  constexpr int SC = SB * GB;  // scales of a row and stage
+  const bool whole = row_groups % SC == 0 && a.scales_aligned && (a.k_lo / G) % SC == 0;
+  const int groups = kd / G;
+  int use = 0;  // ring slot
+  for (int tile0 = blockIdx.x * tiles_cta; tile0 < a.tiles; tile0 += step) {
     const int tile = tile0 + slot;
     const bool on = tile < a.tiles;
     const int64_t first = (int64_t)tile * kRowsWarp;
-    // the four rows of this lane: g, g + 8, g + 16, g + 24
-    int64_t row[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t i = first + g + 8 * r;
-      row[r] = 0;
-      if (on && i < count) {
-        if (GATHER) {
-          const int32_t id = a.ids[(size_t)vec0 * a.K + i];
-          row[r] = id >= 0 && id < a.n ? id : 0;
-        } else {
-          row[r] = i;
-        }
-      }
-    }
-    float acc[2][NT][4];
+    float2 acc[2][NT][2];  // columns 2 t and 2 t + 1 of rows g + 16 x + 8 z
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int y = 0; y < NT; ++y)
 #pragma unroll
-        for (int z = 0; z < 4; ++z) acc[x][y][z] = 0.f;
+        for (int z = 0; z < 2; ++z) acc[x][y][z] = make_float2(0.f, 0.f);
     if (on) {
-      const uint8_t* cp[4];
-      const uint16_t* sp[4];
-      const uint16_t* op[4];
+      // scales of this lane's rows g, g + 8, g + 16, g + 24, one stage ahead
+      const uint16_t *sp[4], *op[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        cp[r] = a.codes + row[r] * row_bytes + a.k_lo / 2;
-        sp[r] = a.scales + row[r] * row_groups + a.k_lo / G;
-        op[r] = MINS ? a.mins + row[r] * row_groups + a.k_lo / G : nullptr;
+        const int64_t row = row_id(first + g + 8 * r);
+        sp[r] = a.scales + row * row_groups + a.k_lo / G;
+        op[r] = MINS ? a.mins + row * row_groups + a.k_lo / G : nullptr;
       }
-#pragma unroll 2
-      for (int b = b_lo; b < b_hi; ++b) {
-        const int left = kd - b * kBlockK;
-        uint4 c[4];
-        float sc[4][GB], of[4][GB];
+      Packed<SC> sc_n[4], of_n[4];
+      auto load_scales = [&](int st) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) c[r] = load_codes<G>(cp[r] + b * (kBlockK / 2), t, left);
+        for (int r = 0; r < 4; ++r) {
+          sc_n[r] = load_packed<SC>(sp[r] + st * SC, whole, groups - st * SC);
+          if (MINS) of_n[r] = load_packed<SC>(op[r] + st * SC, whole, groups - st * SC);
+        }
+      };
+      if (s_lo < s_hi) load_scales(s_lo);
+#pragma unroll 1
+      for (int st = s_lo; st < s_hi; ++st) {
+        copy_stage();
+        asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
+        __syncwarp();
+        Packed<SC> sc[4], of[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r) {
+          sc[r] = sc_n[r];
+          if (MINS) of[r] = of_n[r];
+        }
+        if (st + 1 < s_hi) load_scales(st + 1);
+        const unsigned char* codes = ring + use * (SB * 2048);
+        use = use + 1 == NS ? 0 : use + 1;
+#pragma unroll
+        for (int u = 0; u < SB; ++u) {
+          const int b = st * SB + u;
+          if (SB > 1 && u > 0 && b >= blocks) break;
+          uint32_t c[4][4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (G == 128) {
+              const uint4 v = *reinterpret_cast<const uint4*>(codes + ring_at(u, g, t) + r * 512);
+              c[r][0] = v.x, c[r][1] = v.y, c[r][2] = v.z, c[r][3] = v.w;
+            } else if (G == 64) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint2 v = *reinterpret_cast<const uint2*>(
+                    codes + ring_at(u, g, q * 2 + (t >> 1)) + (t & 1) * 8 + r * 512);
+                c[r][2 * q] = v.x, c[r][2 * q + 1] = v.y;
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                c[r][q] =
+                    *reinterpret_cast<const uint32_t*>(codes + ring_at(u, g, q) + t * 4 + r * 512);
+            }
+          }
 #pragma unroll
           for (int q = 0; q < GB; ++q) {
-            const bool in = q * G < left;
-            sc[r][q] = in ? P::to_float(__ldg(sp[r] + b * GB + q)) : 0.f;
-            if (MINS) of[r][q] = in ? P::to_float(__ldg(op[r] + b * GB + q)) + 8.f * sc[r][q] : 0.f;
-          }
+            float p[2][NT][4];
 #pragma unroll
-        for (int q = 0; q < GB; ++q) {
-          float p[2][NT][4];
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+              for (int y = 0; y < NT; ++y)
 #pragma unroll
-            for (int y = 0; y < NT; ++y)
+                for (int z = 0; z < 4; ++z) p[x][y][z] = 0.f;
 #pragma unroll
-              for (int z = 0; z < 4; ++z) p[x][y][z] = 0.f;
+            for (int i = q * (4 / GB); i < (q + 1) * (4 / GB); ++i) {
+              uint4 hb[NT];
 #pragma unroll
-          for (int i = q * (4 / GB); i < (q + 1) * (4 / GB); ++i) {
-            uint4 hb[NT];
+              for (int y = 0; y < NT; ++y)
+                hb[y] = *reinterpret_cast<const uint4*>(hp[y] + b * 256 + i * 64);
 #pragma unroll
-            for (int y = 0; y < NT; ++y) {
-              hb[y] = make_uint4(0, 0, 0, 0);
-              if (y * 8 + g < nv)
-                hb[y] = *reinterpret_cast<const uint4*>(hs + (size_t)(y * 8 + g) * stride +
-                                                        b * 256 + i * 64 + t * 16);
-            }
+              for (int x = 0; x < 2; ++x) {
+                uint32_t u0[4], u1[4];
+                unpack_codes(c[2 * x][i], u0);
+                unpack_codes(c[2 * x + 1][i], u1);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t w0 = reinterpret_cast<const uint32_t*>(&c[2 * x])[i];
-              const uint32_t w1 = reinterpret_cast<const uint32_t*>(&c[2 * x + 1])[i];
-              uint32_t u0[4], u1[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                u0[j] = P::codes(w0, j);
-                u1[j] = P::codes(w1, j);
-              }
-#pragma unroll
-              for (int y = 0; y < NT; ++y) {
-                P::mma(p[x][y], u0[0], u1[0], u0[1], u1[1], hb[y].x, hb[y].y);
-                P::mma(p[x][y], u0[2], u1[2], u0[3], u1[3], hb[y].z, hb[y].w);
-              }
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int y = 0; y < NT; ++y)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                acc[x][y][z] = fmaf(sc[2 * x + (z >> 1)][q], p[x][y][z], acc[x][y][z]);
-                if (MINS) {
-                  const int col = GATHER ? 0 : y * 8 + 2 * t + (z & 1);
-                  acc[x][y][z] = fmaf(of[2 * x + (z >> 1)][q], Hs[(b * GB + q) * HC + col],
-                                      acc[x][y][z]);
+                for (int y = 0; y < NT; ++y) {
+                  mma_f16(p[x][y], u0[0], u1[0], u0[1], u1[1], hb[y].x, hb[y].y);
+                  mma_f16(p[x][y], u0[2], u1[2], u0[3], u1[3], hb[y].z, hb[y].w);
                 }
               }
+            }
+            float s4[4], o4[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              s4[r] = packed_at<BF16, SC>(sc[r], u * GB + q);
+              if (MINS) o4[r] = fmaf(8.f, s4[r], packed_at<BF16, SC>(of[r], u * GB + q));
+            }
+#pragma unroll
+            for (int y = 0; y < NT; ++y) {
+              float2 H = make_float2(0.f, 0.f);
+              if (MINS) {
+                const float* hq = Hs + (b * GB + q) * HC + (GATHER ? 0 : y * 8 + 2 * t);
+                H = GATHER ? make_float2(hq[0], 0.f) : *reinterpret_cast<const float2*>(hq);
+              }
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const int r = 2 * x + z;
+                  float2& d = acc[x][y][z];
+                  d = fma2(make_float2(s4[r], s4[r]),
+                           make_float2(p[x][y][2 * z], p[x][y][2 * z + 1]), d);
+                  if (MINS) d = fma2(make_float2(o4[r], o4[r]), H, d);
+                }
+            }
+          }
         }
+        __syncwarp();  // the next copy may overwrite what was read here
       }
     }
     if (a.split > 1) {
       // the tile's other warps hand their sums over in shared memory, and its
       // first one adds them in their order
-      constexpr int PER = 2 * NT * 4;
-      float* mine = part + (size_t)warp * PER * 32;
+      constexpr int PER = 2 * NT * 2;
+      float2* mine = reinterpret_cast<float2*>(part) + (size_t)warp * PER * 32 + lane;
       if (k_warp > 0) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int y = 0; y < NT; ++y)
-#pragma unroll
-            for (int z = 0; z < 4; ++z) mine[((x * NT + y) * 4 + z) * 32 + lane] = acc[x][y][z];
+        for (int e = 0; e < PER; ++e) mine[e * 32] = acc[e / (NT * 2)][e / 2 % NT][e % 2];
       }
       cta_sync();
       if (k_warp == 0) {
         for (int o = 1; o < a.split; ++o) {
-          const float* from = part + (size_t)(warp + o) * PER * 32;
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int y = 0; y < NT; ++y)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) acc[x][y][z] += from[((x * NT + y) * 4 + z) * 32 + lane];
+          for (int e = 0; e < PER; ++e) {
+            const float2 v = mine[(o * PER + e) * 32];
+            float2& d = acc[e / (NT * 2)][e / 2 % NT][e % 2];
+            d.x += v.x;
+            d.y += v.y;
+          }
         }
       }
       cta_sync();
@@ -306,7 +482,7 @@ q4_kernel(Q4Launch a, int* err) {
           const int col = y * 8 + 2 * t + (z & 1);
           if (i >= count || col >= nv) continue;
           float* o = a.out + (size_t)(vec0 + col) * a.ldo + i;
-          float v = acc[x][y][z];
+          float v = (z & 1 ? acc[x][y][z >> 1].y : acc[x][y][z >> 1].x) * sh_back[col];
           if (a.add) v += *o;
           if (GATHER) {
             const int32_t id = a.ids[(size_t)vec0 * a.K + i];
@@ -318,45 +494,74 @@ q4_kernel(Q4Launch a, int* err) {
           *o = v;
         }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-constexpr size_t kSmemMost = 220 * 1024;
+constexpr size_t kSmemMost = 226 * 1024;
 
-size_t smem_bytes(int kd, int group, int vecs, int cols, bool mins, int warps, int nt) {
+// The kernel's shapes. Up to 8 vectors: stages of 256 codes, 8 warps, two CTAs
+// an SM; up to 16: 128 codes (h alone takes 160 KB at d = 5120), one CTA.
+struct Form {
+  int nt, warps, sb, ns;
+};
+constexpr Form kFormOne = {1, 8, 2, 3}, kFormTwo = {2, 8, 1, 3};
+// Groups of 32 carry four scales a row and block ahead: stages of one block.
+constexpr Form kFormOne32 = {1, 8, 1, 5};
+constexpr Form form_of(int nt, int group) {
+  return nt == 2 ? kFormTwo : group == 32 ? kFormOne32 : kFormOne;
+}
+
+size_t smem_bytes(const Form& f, int kd, int group, int vecs, int cols, bool mins, bool split) {
   const int blocks = (kd + kBlockK - 1) / kBlockK;
-  return (size_t)vecs * h_stride(blocks) +
-         (mins ? (size_t)blocks * (kBlockK / group) * cols * sizeof(float) : 0) +
-         (size_t)warps * nt * 8 * 32 * sizeof(float);
+  return (size_t)h_bytes(blocks, vecs, mins ? blocks * (kBlockK / group) * cols : 0) +
+         (size_t)f.warps * f.ns * f.sb * 2048 +
+         (split ? (size_t)f.warps * f.nt * 8 * 32 * sizeof(float) : 0);
 }
 
-template <bool BF16, int G, int NT, int WARPS, bool MINS, bool GATHER>
+template <bool BF16, int G, int NT, bool MINS, bool GATHER>
 cudaError_t launch_one(const Q4Launch& in, int* err, cudaStream_t s) {
+  constexpr Form f = form_of(NT, G);
+  auto kernel = q4_kernel<BF16, G, NT, f.warps, f.sb, f.ns, MINS, GATHER>;
   Q4Launch a = in;
-  const int vecs = GATHER ? 1 : (a.M < NT * 8 ? a.M : NT * 8), cols = GATHER ? 1 : NT * 8;
+  const int kd = a.k_hi - a.k_lo, vecs = GATHER ? 1 : (a.M < NT * 8 ? a.M : NT * 8);
+  const int cols = GATHER ? 1 : NT * 8;
   const int64_t rows = GATHER ? a.K : a.n;
   a.tiles = (int)((rows + kRowsWarp - 1) / kRowsWarp);
-  // few tiles: more warps share one, until the GPU has about 16 warps an SM
+  const int stages = ((kd + kBlockK - 1) / kBlockK + f.sb - 1) / f.sb;
+  const size_t alone = smem_bytes(f, kd, G, vecs, cols, MINS, false);
+  const int per_sm = alone <= 105 * 1024 && NT == 1 ? 2 : 1;
+  const int64_t warps = (int64_t)sm_count() * per_sm * f.warps;
+  // How many warps share a tile: the last round of tiles leaves warps idle, and
+  // shares of a tile fill it better; a round of s-shares takes 1/s of the time
+  // of a round of tiles (plus the join, so s must gain a twentieth at least).
   const int64_t all = (int64_t)a.tiles * (GATHER ? a.M : 1);
-  const int blocks = (a.k_hi - a.k_lo + kBlockK - 1) / kBlockK;
   a.split = 1;
-  while (a.split < WARPS && a.split * 2 <= blocks && all * a.split < (int64_t)sm_count() * 16)
-    a.split *= 2;
-  const size_t smem = smem_bytes(a.k_hi - a.k_lo, G, vecs, cols, MINS, WARPS, NT);
+  double best = (double)((all + warps - 1) / warps);
+  for (int x = 2; x <= f.warps && x <= stages; x *= 2) {
+    if (smem_bytes(f, kd, G, vecs, cols, MINS, true) > kSmemMost) break;
+    const int64_t teams = warps / x;
+    const double time = (double)((all + teams - 1) / teams) / x;
+    if (time < 0.95 * best) {
+      best = time;
+      a.split = x;
+    }
+  }
+  const size_t smem = smem_bytes(f, kd, G, vecs, cols, MINS, a.split > 1);
   static int smem_set[64] = {0};
-  cudaError_t e = ensure_dynamic_smem(q4_kernel<BF16, G, NT, WARPS, MINS, GATHER>, smem, smem_set);
+  cudaError_t e = ensure_dynamic_smem(kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
-  const int per = WARPS / a.split, ctas = (a.tiles + per - 1) / per;
-  const int resident = sm_count() * ((smem <= 110 * 1024 && (GATHER || NT == 1)) ? 2 : 1);
+  const int per = f.warps / a.split, ctas = (a.tiles + per - 1) / per;
+  const int resident = sm_count() * per_sm;
   const unsigned gx = GATHER ? ctas : (ctas < resident ? ctas : resident);
-  return launch_kernel(true, q4_kernel<BF16, G, NT, WARPS, MINS, GATHER>,
-                       dim3(gx, GATHER ? a.M : 1), dim3(WARPS * 32), smem, s, a, err);
+  return launch_kernel(true, kernel, dim3(gx, GATHER ? a.M : 1), dim3(f.warps * 32), smem, s, a,
+                       err);
 }
 
 template <bool BF16, int G, bool MINS>
 cudaError_t launch_cols(const Q4Launch& a, int* err, cudaStream_t s) {
-  if (a.ids) return launch_one<BF16, G, 1, 8, MINS, true>(a, err, s);
-  if (a.M <= 8) return launch_one<BF16, G, 1, 8, MINS, false>(a, err, s);
-  return launch_one<BF16, G, 2, 16, MINS, false>(a, err, s);
+  if (a.ids) return launch_one<BF16, G, 1, MINS, true>(a, err, s);
+  if (a.M <= 8) return launch_one<BF16, G, 1, MINS, false>(a, err, s);
+  return launch_one<BF16, G, 2, MINS, false>(a, err, s);
 }
 
 template <bool BF16, int G>
@@ -383,6 +588,8 @@ cudaError_t launch_q4(const Q4Args& q, int* err, cudaStream_t s) {
   a.d = q.d;
   a.K = q.K;
   a.ldo = q.ids ? q.K : q.n;
+  a.scales_aligned =
+      ((reinterpret_cast<uintptr_t>(q.scales) | reinterpret_cast<uintptr_t>(q.mins)) & 15u) == 0;
   // hidden vectors of one pass over the rows, then pieces of d, as far as h
   // fits in shared memory; a later piece adds to the former's sums
   const int most = q.ids ? q.M : 16;
@@ -390,10 +597,10 @@ cudaError_t launch_q4(const Q4Args& q, int* err, cudaStream_t s) {
     a.M = q.M - m < most ? q.M - m : most;
     a.h = static_cast<const uint16_t*>(q.h) + (size_t)m * q.d;
     a.out = q.out + (size_t)m * a.ldo;
-    const int nt = !q.ids && a.M > 8 ? 2 : 1, warps = nt == 2 ? 16 : 8;
-    const int vecs = q.ids ? 1 : a.M, cols = q.ids ? 1 : nt * 8;
+    const Form f = form_of(!q.ids && a.M > 8 ? 2 : 1, q.group);
+    const int vecs = q.ids ? 1 : a.M, cols = q.ids ? 1 : f.nt * 8;
     int piece = q.d;
-    while (smem_bytes(piece, q.group, vecs, cols, q.mins != nullptr, warps, nt) > kSmemMost)
+    while (smem_bytes(f, piece, q.group, vecs, cols, q.mins != nullptr, false) > kSmemMost)
       piece = ((piece + 1) / 2 + kBlockK - 1) / kBlockK * kBlockK;
     for (int k = 0; k < q.d; k += piece) {
       a.k_lo = k;
