@@ -1,27 +1,32 @@
 // Products of hidden vectors with rows of 4-bit codes and group scales:
-//   y[m, i] = sum_G ( s[i,G] sum_{k in G} (c[i,k] - 8) h[m,k] + o[i,G] H[m,G] ),
-// H[m,G] = sum_{k in G} h[m,k]; o = 0 for symmetric codes, and min + 8 s for
-// codes with an offset (w = c s + min).
+//   y[m, i] = sum_G ( s[i,G] sum_{k in G} c[i,k] h[m,k] + o[i,G] H[m,G] ),
+// H[m,G] = sum_{k in G} h[m,k]; o = -8 s for symmetric codes, the group's min
+// for codes with an offset.
 //
 // Bound by reading the codes (d/2 + 2 d/group bytes a row) and by the
-// instructions that unpack them. A code minus 8 is exact in 16 bits, and a warp
-// multiplies 16 rows x 16 codes with up to 8 hidden vectors in one matrix
-// instruction from registers (products exact, sums in 32 bits). The sum over k
-// may take k in any order, so the order in which a lane's own codes unpack is
-// the order of k, and h is laid out to match once per CTA: no shuffle is
-// needed. Each warp streams its own 32 rows through a ring of shared memory
-// with asynchronous copies (128 bytes of a row at a time; loads straight to the
-// operand registers touch 64 bytes of 8 rows at once and were bound by the
-// L1's tags). Group sums are scaled in 32 bits after the matrix products; no
-// weight is ever rounded. (Operands of the tcgen05 instructions would have to
-// be written to shared or tensor memory first, at a store per two codes; here
-// they never leave registers.)
-//   Unpacking a 32-bit word of 8 codes into fp16: joined with the bit pattern
-// of 1024, whose lowest mantissa bit is one unit, the low code of a byte gives
-// 1024 + c and the high one 1024 + 16 c, and one packed addition or
-// multiply-add leaves c - 8: one shift, four logical and four packed
-// instructions. (bf16 has 7 mantissa bits, so every code but the lowest would
-// need its own shift; h is taken to fp16 instead, see below.)
+// instructions that unpack them. A warp multiplies 16 rows x 16 codes with up
+// to 8 hidden vectors in one matrix instruction from registers (products
+// exact, sums in 32 bits), and the codes need next to no work to become its
+// operands: four bits among the ten of an fp16 mantissa are a subnormal number,
+// exactly c times its place, so a 32-bit word of 8 codes takes two shifts and
+// four masks. (Adding the bits of
+// 1024 and subtracting 1032 instead, to have c - 8, took nine instructions; the
+// term with H costs one multiply-add a group.) h is kept in fp16, scaled, with
+// the sixteenth for the pairs that need it. The sum over k may take k in any
+// order, so the order in which a lane's own codes unpack is the order of k, and
+// h is laid out to match once per CTA: no shuffle is needed. Each warp streams
+// its own 32 rows through a ring of shared memory with asynchronous copies (128
+// bytes of a row at a time; loads straight to the operand registers touch 64
+// bytes of 8 rows at once and were bound by the L1's tags). Group sums are
+// scaled in 32 bits after the matrix products; no weight is ever rounded.
+// (Operands of the tcgen05 instructions would have to be written to shared or
+// tensor memory first, at a store per two codes; here they never leave
+// registers.)
+//   The matrix instructions cut the products of a sum at a place set by the
+// largest. With codes up to 15 in place of -8..7 a symmetric row's sums lose
+// about two bits more; over long rows that stays near 2^-21 of the result, in
+// short ones (kCentreD) 8 is subtracted from the codes, which costs four packed
+// additions a word and makes H unnecessary.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -33,36 +38,48 @@ namespace {
 
 constexpr int kBlockK = 128;  // codes of a row that four lanes take together
 constexpr int kRowsWarp = 32;
+constexpr int kCentreD = 256;
 
-// The 8 codes of word w, minus 8, as fp16 pairs (0,4), (1,5), (2,6), (3,7).
-__device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t (&u)[4]) {
-  const __half2 low = __floats2half2_rn(-1032.f, -1032.f);
-  const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
-  const __half2 high = __floats2half2_rn(-72.f, -72.f);
+// What becomes of a code: c with a min per group, c with -8 s, or c - 8.
+enum Mode { kMins, kPlain, kCentred };
+
+// The 8 codes of word w as fp16 pairs (0,4), (1,5), (2,6), (3,7): subnormal
+// numbers, 2^-22 c for the first and third pair and 2^-18 c for the others (the
+// mantissa's top; the matrix instructions do not normalise their operands, so
+// the higher the code sits the more bits its products keep).
+template <bool CENTRE> __device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t (&u)[4]) {
+  const uint32_t v = w << 2, x = w >> 6;
+  u[0] = v & 0x003c003cu;
+  u[1] = v & 0x03c003c0u;
+  u[2] = x & 0x003c003cu;
+  u[3] = x & 0x03c003c0u;
+  if (CENTRE) {
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const uint32_t x = w >> (8 * j);
-    uint32_t a = (x & 0x000f000fu) | 0x64006400u, b = (x & 0x00f000f0u) | 0x64006400u;
-    const __half2 p = __hadd2(*reinterpret_cast<__half2*>(&a), low);
-    const __half2 q = __hfma2(*reinterpret_cast<__half2*>(&b), sixteenth, high);
-    u[2 * j] = *reinterpret_cast<const uint32_t*>(&p);
-    u[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&q);
+    for (int j = 0; j < 4; ++j) {
+      uint32_t eight = j & 1 ? 0x82008200u : 0x80208020u;  // -8 times the unit
+      const __half2 r = __hadd2(*reinterpret_cast<__half2*>(&u[j]),
+                                *reinterpret_cast<__half2*>(&eight));
+      u[j] = *reinterpret_cast<const uint32_t*>(&r);
+    }
   }
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-template <bool BF16> __device__ __forceinline__ float to_float(uint16_t b) {
-  if (BF16) return __uint_as_float((uint32_t)b << 16);
-  return __half2float(__ushort_as_half(b));
+// The same with nothing to add to.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+
 template <bool BF16> __device__ __forceinline__ float2 pair_to_float(uint32_t w) {
   if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -79,30 +96,30 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// N consecutive 16-bit values of a row: one load where the row allows it, or
-// those below `left` one by one, zeros behind them.
+// N consecutive 16-bit values of a row: in one load, or those below `left` one
+// by one with zeros behind them.
 template <int N> struct Packed {
   uint32_t w[(N + 1) / 2];
 };
-template <int N>
-__device__ __forceinline__ Packed<N> load_packed(const uint16_t* p, bool whole, int left) {
+template <int N> __device__ __forceinline__ Packed<N> load_whole(const uint16_t* p) {
   Packed<N> v;
-  if (whole) {
-    if (N == 4) {
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-      v.w[0] = x.x;
-      v.w[(N + 1) / 2 - 1] = x.y;
-    } else if (N == 2) {
-      v.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-    } else {
-      v.w[0] = __ldg(p);
-    }
+  if (N == 4) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    v.w[0] = x.x;
+    v.w[(N + 1) / 2 - 1] = x.y;
+  } else if (N == 2) {
+    v.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
   } else {
+    v.w[0] = __ldg(p);
+  }
+  return v;
+}
+template <int N> __device__ __forceinline__ Packed<N> load_single(const uint16_t* p, int left) {
+  Packed<N> v;
 #pragma unroll
-    for (int i = 0; i < (N + 1) / 2; ++i) {
-      v.w[i] = 2 * i < left ? __ldg(p + 2 * i) : 0u;
-      if (2 * i + 1 < N && 2 * i + 1 < left) v.w[i] |= (uint32_t)__ldg(p + 2 * i + 1) << 16;
-    }
+  for (int i = 0; i < (N + 1) / 2; ++i) {
+    v.w[i] = 2 * i < left ? __ldg(p + 2 * i) : 0u;
+    if (2 * i + 1 < N && 2 * i + 1 < left) v.w[i] |= (uint32_t)__ldg(p + 2 * i + 1) << 16;
   }
   return v;
 }
@@ -123,21 +140,21 @@ struct Q4Launch {
   const uint16_t *scales, *mins, *h;
   const int32_t* ids;
   int64_t n;
-  int d, M, K;     // M hidden vectors from h; K candidates a vector (gather)
-  int k_lo, k_hi;  // codes [k_lo, k_hi) of each row are summed
-  int add;         // add to out instead of writing it
+  int d, M, K;         // M hidden vectors from h; K candidates a vector (gather)
+  int k_lo, k_hi;      // codes [k_lo, k_hi) of each row are summed
+  int add;             // add to out instead of writing it
   int64_t ldo;
   float* out;
-  int tiles;       // row tiles (of each vector in the gather)
-  int split;       // warps that share a tile's codes
+  int tiles;           // row tiles (of each vector in the gather)
+  int split;           // warps that share a tile's codes
   int scales_aligned;  // scales and mins at 16 bytes
 };
 
 // Shared memory: h of the call's vectors, [vector][block][i][t] 16-byte words
 // (8 codes' worth, codes 0,4,1,5,2,6,3,7), rows 64 bytes off a multiple of
 // 128 so that the 8 lanes of a 16-byte read phase (2 vectors x 4 chunks) hit
-// all banks once; then H per group and vector; each warp's ring of codes; and
-// the warps' partial sums where several share a tile.
+// all banks once; then H per group and vector; each warp's ring of codes; and,
+// twice, the warps' partial sums where several share a tile.
 __host__ __device__ inline int h_stride(int blocks) { return blocks * 256 + 64; }
 // Bytes of h and H together: the rings behind them start at a multiple of 128.
 __host__ __device__ inline int h_bytes(int blocks, int vecs, int sums) {
@@ -159,12 +176,15 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
                : "memory");
 }
 
-template <bool BF16, int G, int NT, int WARPS, int SB, int NS, bool MINS, bool GATHER>
-__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 2 : 1)
+template <bool BF16, int G, int NT, int WARPS, int SB, int NS, int MODE, bool GATHER>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1)
 q4_kernel(Q4Launch a, int* err) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t sh_top[WARPS];
-  __shared__ float sh_back[NT * 8];  // what each vector's sums are scaled back by
+  // what each vector's sums are scaled back by (the gather has two in turn: one
+  // is read for the last tile of a vector while the next is laid out)
+  __shared__ float sh_back[GATHER ? 2 : NT * 8];
+  constexpr bool MINS = MODE == kMins, SUMS = MODE != kCentred;
   constexpr int GB = kBlockK / G;          // groups a block
   constexpr int HC = GATHER ? 1 : NT * 8;  // vectors of H
   constexpr int CPY = SB * 4;              // copies a lane and stage
@@ -176,145 +196,157 @@ q4_kernel(Q4Launch a, int* err) {
   const int nv = GATHER ? 1 : min(a.M, NT * 8);
   unsigned char* hs = smem;
   float* Hs = reinterpret_cast<float*>(smem + (size_t)nv * stride);  // [group][HC]
-  unsigned char* rings = smem + h_bytes(blocks, nv, MINS ? blocks * GB * HC : 0);
+  unsigned char* rings = smem + h_bytes(blocks, nv, SUMS ? blocks * GB * HC : 0);
   unsigned char* ring = rings + (size_t)warp * (NS * SB * 2048);
   float* part = reinterpret_cast<float*>(rings + (size_t)WARPS * (NS * SB * 2048));
   pdl_wait();
   pdl_trigger();
-  const int vec0 = GATHER ? blockIdx.y : 0;
   const int64_t count = GATHER ? a.K : a.n;
   const int row_bytes = a.d / 2, row_groups = a.d / G;
 
-  const int tiles_cta = WARPS / a.split;
-  const int k_warp = warp % a.split, slot = warp / a.split;
+  // A unit is the next tile of each of the CTA's teams of `split` warps, of one
+  // hidden vector (the gather) or of all of them; a CTA takes a run of units.
+  const int teams = WARPS / a.split, k_warp = warp % a.split, slot = warp / a.split;
   const int all_stages = (blocks + SB - 1) / SB;
   const int s_lo = all_stages * k_warp / a.split, s_hi = all_stages * (k_warp + 1) / a.split;
-  const int step = gridDim.x * tiles_cta;
+  const int per_vec = (a.tiles + teams - 1) / teams;
+  const int64_t units = (int64_t)per_vec * (GATHER ? a.M : 1);
+  const int64_t u_lo = units * blockIdx.x / gridDim.x, u_hi = units * (blockIdx.x + 1) / gridDim.x;
+  auto row_id = [&](int vec, int64_t i) -> int32_t {  // the row behind entry i, 0 for none
+    if (!GATHER) return i < count ? (int32_t)i : 0;
+    if (i >= count) return 0;
+    const int32_t id = a.ids[(size_t)vec * a.K + i];
+    return id >= 0 && id < a.n ? id : 0;
+  };
 
   // ---- the copies of this warp's codes run NS - 1 stages ahead, over the ends
   // of its tiles
   const int c_row = lane / CPY, c_chunk = lane % CPY;  // of the warp's first copy
-  int c_tile = blockIdx.x * tiles_cta + slot, c_stage = s_lo, c_slot = 0;
+  int64_t c_unit = u_lo;
+  int c_vec = (int)(u_lo / per_vec), c_rem = (int)(u_lo - (int64_t)c_vec * per_vec);
+  int c_tile = c_rem * teams + slot, c_stage = s_lo, c_slot = 0;
   int32_t c_id[GATHER ? CPY : 1];
-  auto row_id = [&](int64_t i) -> int32_t {  // the row behind entry i, 0 for none
-    if (!GATHER) return i < count ? (int32_t)i : 0;
-    if (i >= count) return 0;
-    const int32_t id = a.ids[(size_t)vec0 * a.K + i];
-    return id >= 0 && id < a.n ? id : 0;
-  };
-  auto copy_ids = [&]() {
-    if (GATHER)
+  auto copy_ids = [&]() {  // of the next unit in which this team has a tile
+    while (c_tile >= a.tiles && c_unit < u_hi) {
+      ++c_unit;
+      c_rem = 0;  // only a vector's last unit lacks tiles
+      ++c_vec;
+      c_tile = slot;
+    }
+    if (GATHER && c_unit < u_hi)
 #pragma unroll
       for (int j = 0; j < CPY; ++j)
-        c_id[j] = row_id((int64_t)c_tile * kRowsWarp + j * CR + c_row);
+        c_id[j] = row_id(c_vec, (int64_t)c_tile * kRowsWarp + j * CR + c_row);
   };
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
   auto copy_stage = [&]() {
-    if (c_tile < a.tiles && s_lo < s_hi) {
+    if (c_unit < u_hi) {
       const int at = a.k_lo / 2 + (c_stage * SB * 4 + c_chunk) * 16;
-      const bool in_k = at < a.k_hi / 2;
+      // rows of the tile, none when past the end of the piece
+      const int rows =
+          at < a.k_hi / 2 ? (int)min((int64_t)kRowsWarp, count - (int64_t)c_tile * kRowsWarp) : 0;
+      const uint8_t* src = a.codes + at;
+      if (!GATHER) src += ((int64_t)c_tile * kRowsWarp + c_row) * row_bytes;
 #pragma unroll
       for (int j = 0; j < CPY; ++j) {
         const int r = j * CR + c_row;
-        const int64_t i = (int64_t)c_tile * kRowsWarp + r;
-        const int64_t row = GATHER ? (int64_t)c_id[j] : i;
-        const bool in = in_k && i < count;
+        const bool in = r < rows;
+        const uint8_t* p =
+            GATHER ? src + (int64_t)c_id[j] * row_bytes : src + (int64_t)(j * CR) * row_bytes;
         copy16(ring_s + c_slot * (SB * 2048) + ring_at(c_chunk >> 2, r, c_chunk & 3),
-               a.codes + (in ? row * row_bytes + at : 0), in);
+               in ? p : a.codes, in);
       }
       if (++c_stage == s_hi) {
         c_stage = s_lo;
-        c_tile += step;
-        if (c_tile < a.tiles) copy_ids();
+        ++c_unit;
+        if (++c_rem == per_vec) {
+          c_rem = 0;
+          ++c_vec;
+        }
+        c_tile = c_rem * teams + slot;
+        copy_ids();
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     c_slot = c_slot + 1 == NS ? 0 : c_slot + 1;
   };
-  if (c_tile < a.tiles) copy_ids();
+  copy_ids();
 #pragma unroll
   for (int i = 0; i < NS - 1; ++i) copy_stage();
 
-  // ---- h, laid out as the codes unpack, in fp16: bf16 values are first scaled
-  // by the power of two that takes the vector's largest below 2^15, which keeps
-  // all of their bits down to 2^-29 of the largest (and 2^-40 of it throughout);
-  // the sums are scaled back. A warp takes a vector, or all of them the one.
-  {
+  // ---- h, laid out as the codes unpack, in fp16: values are first scaled by
+  // the power of two that takes the vector's largest to 2^14..2^15, which keeps
+  // all bits of those down to 2^-25 of the largest, and 2^-36 of it throughout;
+  // the pairs that meet 2^-18 c are divided by 16. A warp takes a vector, or
+  // all of them the one.
+  auto lay_out = [&](int vec0) {
     const int words = blocks * 16;
     const int lanes = GATHER ? WARPS * 32 : 32, me = GATHER ? tid : lane;
     for (int v = GATHER ? 0 : warp; v < nv; v += GATHER ? 1 : WARPS) {
       const uint16_t* src = a.h + (size_t)(vec0 + v) * a.d + a.k_lo;
       unsigned char* dst = hs + (size_t)v * stride;
-      float scale = 1.f;
-      if (BF16) {
-        uint32_t top = 0;  // the order of magnitudes is that of their bits
-        for (int w = me; w * 8 < kd; w += lanes) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src + w * 8);
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+      uint32_t top = 0;  // the order of magnitudes is that of their bits
+      for (int w = me; w * 8 < kd; w += lanes) {
+        const uint4 x = *reinterpret_cast<const uint4*>(src + w * 8);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top = max(top, max((u[i] << 16) & 0x7FFF0000u, u[i] & 0x7FFF0000u));
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = pair_to_float<BF16>(u[i]);
+          top = max(top, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
         }
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        if (GATHER) {
-          if (lane == 0) sh_top[warp] = top;
-          cta_sync();
-#pragma unroll
-          for (int i = 0; i < WARPS; ++i) top = max(top, sh_top[i]);
-        }
-        const int e = (int)(top >> 23) - 127;                  // floor of its logarithm
-        const int k = top == 0 ? 0 : max(-126, min(127, 14 - e));
-        scale = __uint_as_float((uint32_t)(k + 127) << 23);
-        if (me == 0) sh_back[v] = __uint_as_float((uint32_t)(127 - max(k, -126)) << 23);
-        if (me == 0 && k == 127) sh_back[v] = 5.877471754111438e-39f;  // 2^-127
-      } else if (me == 0) {
-        sh_back[v] = 1.f;
       }
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if (GATHER) {
+        if (lane == 0) sh_top[warp] = top;
+        cta_sync();
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) top = max(top, sh_top[i]);
+      }
+      const int e = (int)(top >> 23) - 127;  // floor of its logarithm
+      const int k = top == 0 ? 0 : max(-126, min(126, 14 - e));
+      const float scale = __uint_as_float((uint32_t)(127 + k) << 23), sixteenth = scale * 0.0625f;
+      if (me == 0) sh_back[GATHER ? vec0 & 1 : v] = __uint_as_float((uint32_t)(127 - k) << 23);
       for (int w = me; w < words; w += lanes) {
         const int b = w >> 4, p = w & 15, at = b * 16 + word_of<G>(p & 3, p >> 2);
         uint4 x = make_uint4(0, 0, 0, 0);
         if (at * 8 < kd) x = *reinterpret_cast<const uint4*>(src + at * 8);
-        if (BF16) {
-          uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};  // 0 1, 2 3, 4 5, 6 7
+        uint32_t r[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = pair_to_float<true>(u[i]);
-            const __half2 r = __floats2half2_rn(f.x * scale, f.y * scale);
-            u[i] = *reinterpret_cast<const uint32_t*>(&r);
-          }
-          x = make_uint4(u[0], u[1], u[2], u[3]);
+        for (int i = 0; i < 2; ++i) {
+          const float2 lo = pair_to_float<BF16>(u[i]), hi = pair_to_float<BF16>(u[i + 2]);
+          const __half2 even = __floats2half2_rn(lo.x * scale, hi.x * scale);
+          const __half2 odd = __floats2half2_rn(lo.y * sixteenth, hi.y * sixteenth);
+          r[2 * i] = *reinterpret_cast<const uint32_t*>(&even);
+          r[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&odd);
         }
-        uint4 y;
-        y.x = __byte_perm(x.x, x.z, 0x5410);  // 0, 4
-        y.y = __byte_perm(x.x, x.z, 0x7632);  // 1, 5
-        y.z = __byte_perm(x.y, x.w, 0x5410);  // 2, 6
-        y.w = __byte_perm(x.y, x.w, 0x7632);  // 3, 7
-        *reinterpret_cast<uint4*>(dst + w * 16) = y;
+        *reinterpret_cast<uint4*>(dst + w * 16) = make_uint4(r[0], r[1], r[2], r[3]);
       }
-    }
-  }
-  cta_sync();
-  if (MINS) {
-    // a group's words lie at i in [q * 4 / GB, (q + 1) * 4 / GB), every t
-    for (int e = tid; e < blocks * GB * HC; e += WARPS * 32) {
-      const int v = e % HC, gi = e / HC, b = gi / GB, q = gi - b * GB;
-      float s = 0.f;
-      if (v < nv) {
-        const unsigned char* src = hs + (size_t)v * stride + b * 256 + q * (256 / GB);
-#pragma unroll
-        for (int w = 0; w < 16 / GB; ++w) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src + w * 16);
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = pair_to_float<false>(u[i]);
-            s += f.x + f.y;
-          }
-        }
-      }
-      Hs[e] = s;
     }
     cta_sync();
-  }
+    if (SUMS) {
+      // H, times 2^-22 like the products; a group's words lie at i in
+      // [q * 4 / GB, (q + 1) * 4 / GB), every t
+      for (int e = tid; e < blocks * GB * HC; e += WARPS * 32) {
+        const int v = e % HC, gi = e / HC, b = gi / GB, q = gi - b * GB;
+        float even = 0.f, odd = 0.f;
+        if (v < nv) {
+          const unsigned char* src = hs + (size_t)v * stride + b * 256 + q * (256 / GB);
+#pragma unroll
+          for (int w = 0; w < 16 / GB; ++w) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + w * 16);
+            const float2 f0 = pair_to_float<false>(x.x), f1 = pair_to_float<false>(x.y);
+            const float2 f2 = pair_to_float<false>(x.z), f3 = pair_to_float<false>(x.w);
+            even += (f0.x + f0.y) + (f2.x + f2.y);
+            odd += (f1.x + f1.y) + (f3.x + f3.y);
+          }
+        }
+        Hs[e] = fmaf(16.f, odd, even) * 2.384185791015625e-7f;
+      }
+      cta_sync();
+    }
+  };
+  if (!GATHER) lay_out(0);
 
   // This lane's vector columns (columns past the last repeat it and are not
   // stored) and its places in a stage: row g, with rows g + 8 r 512 bytes apart.
@@ -324,9 +356,14 @@ q4_kernel(Q4Launch a, int* err) {
   constexpr int SC = SB * GB;  // scales of a row and stage
   const bool whole = row_groups % SC == 0 && a.scales_aligned && (a.k_lo / G) % SC == 0;
   const int groups = kd / G;
-  int use = 0;  // ring slot
-  for (int tile0 = blockIdx.x * tiles_cta; tile0 < a.tiles; tile0 += step) {
-    const int tile = tile0 + slot;
+  int use = 0, turn = 0;  // ring slot; which of the partial sums
+  int vec = (int)(u_lo / per_vec), rem = (int)(u_lo - (int64_t)vec * per_vec);
+  for (int64_t unit = u_lo; unit < u_hi; ++unit) {
+    if (GATHER && (unit == u_lo || rem == 0)) {
+      if (a.split == 1) cta_sync();  // the last vector is read no more
+      lay_out(vec);
+    }
+    const int tile = rem * teams + slot;
     const bool on = tile < a.tiles;
     const int64_t first = (int64_t)tile * kRowsWarp;
     float2 acc[2][NT][2];  // columns 2 t and 2 t + 1 of rows g + 16 x + 8 z
@@ -341,19 +378,27 @@ q4_kernel(Q4Launch a, int* err) {
       const uint16_t *sp[4], *op[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int64_t row = row_id(first + g + 8 * r);
+        const int64_t row = row_id(vec, first + g + 8 * r);
         sp[r] = a.scales + row * row_groups + a.k_lo / G;
         op[r] = MINS ? a.mins + row * row_groups + a.k_lo / G : nullptr;
       }
       Packed<SC> sc_n[4], of_n[4];
       auto load_scales = [&](int st) {
+        if (whole) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          sc_n[r] = load_packed<SC>(sp[r] + st * SC, whole, groups - st * SC);
-          if (MINS) of_n[r] = load_packed<SC>(op[r] + st * SC, whole, groups - st * SC);
+          for (int r = 0; r < 4; ++r) {
+            sc_n[r] = load_whole<SC>(sp[r] + st * SC);
+            if (MINS) of_n[r] = load_whole<SC>(op[r] + st * SC);
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sc_n[r] = load_single<SC>(sp[r] + st * SC, groups - st * SC);
+            if (MINS) of_n[r] = load_single<SC>(op[r] + st * SC, groups - st * SC);
+          }
         }
       };
-      if (s_lo < s_hi) load_scales(s_lo);
+      load_scales(s_lo);
 #pragma unroll 1
       for (int st = s_lo; st < s_hi; ++st) {
         copy_stage();
@@ -396,12 +441,6 @@ q4_kernel(Q4Launch a, int* err) {
           for (int q = 0; q < GB; ++q) {
             float p[2][NT][4];
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int y = 0; y < NT; ++y)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) p[x][y][z] = 0.f;
-#pragma unroll
             for (int i = q * (4 / GB); i < (q + 1) * (4 / GB); ++i) {
               uint4 hb[NT];
 #pragma unroll
@@ -410,11 +449,14 @@ q4_kernel(Q4Launch a, int* err) {
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 uint32_t u0[4], u1[4];
-                unpack_codes(c[2 * x][i], u0);
-                unpack_codes(c[2 * x + 1][i], u1);
+                unpack_codes<MODE == kCentred>(c[2 * x][i], u0);
+                unpack_codes<MODE == kCentred>(c[2 * x + 1][i], u1);
 #pragma unroll
                 for (int y = 0; y < NT; ++y) {
-                  mma_f16(p[x][y], u0[0], u1[0], u0[1], u1[1], hb[y].x, hb[y].y);
+                  if (i == q * (4 / GB))
+                    mma_f16_first(p[x][y], u0[0], u1[0], u0[1], u1[1], hb[y].x, hb[y].y);
+                  else
+                    mma_f16(p[x][y], u0[0], u1[0], u0[1], u1[1], hb[y].x, hb[y].y);
                   mma_f16(p[x][y], u0[2], u1[2], u0[3], u1[3], hb[y].z, hb[y].w);
                 }
               }
@@ -423,12 +465,12 @@ q4_kernel(Q4Launch a, int* err) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               s4[r] = packed_at<BF16, SC>(sc[r], u * GB + q);
-              if (MINS) o4[r] = fmaf(8.f, s4[r], packed_at<BF16, SC>(of[r], u * GB + q));
+              o4[r] = MINS ? packed_at<BF16, SC>(of[r], u * GB + q) : -8.f * s4[r];
             }
 #pragma unroll
             for (int y = 0; y < NT; ++y) {
               float2 H = make_float2(0.f, 0.f);
-              if (MINS) {
+              if (SUMS) {
                 const float* hq = Hs + (b * GB + q) * HC + (GATHER ? 0 : y * 8 + 2 * t);
                 H = GATHER ? make_float2(hq[0], 0.f) : *reinterpret_cast<const float2*>(hq);
               }
@@ -440,7 +482,7 @@ q4_kernel(Q4Launch a, int* err) {
                   float2& d = acc[x][y][z];
                   d = fma2(make_float2(s4[r], s4[r]),
                            make_float2(p[x][y][2 * z], p[x][y][2 * z + 1]), d);
-                  if (MINS) d = fma2(make_float2(o4[r], o4[r]), H, d);
+                  if (SUMS) d = fma2(make_float2(o4[r], o4[r]), H, d);
                 }
             }
           }
@@ -448,11 +490,17 @@ q4_kernel(Q4Launch a, int* err) {
         __syncwarp();  // the next copy may overwrite what was read here
       }
     }
+    const int tile_vec = vec;
+    if (++rem == per_vec) {
+      rem = 0;
+      ++vec;
+    }
     if (a.split > 1) {
       // the tile's other warps hand their sums over in shared memory, and its
-      // first one adds them in their order
+      // first one adds them in their order, while the others go on
       constexpr int PER = 2 * NT * 2;
-      float2* mine = reinterpret_cast<float2*>(part) + (size_t)warp * PER * 32 + lane;
+      float2* mine = reinterpret_cast<float2*>(part) + (size_t)(turn * WARPS + warp) * PER * 32 + lane;
+      turn ^= 1;
       if (k_warp > 0) {
 #pragma unroll
         for (int e = 0; e < PER; ++e) mine[e * 32] = acc[e / (NT * 2)][e / 2 % NT][e % 2];
@@ -469,7 +517,6 @@ q4_kernel(Q4Launch a, int* err) {
           }
         }
       }
-      cta_sync();
     }
     if (!on || k_warp != 0) continue;
 #pragma unroll
@@ -481,11 +528,12 @@ q4_kernel(Q4Launch a, int* err) {
           const int64_t i = first + 16 * x + g + 8 * (z >> 1);
           const int col = y * 8 + 2 * t + (z & 1);
           if (i >= count || col >= nv) continue;
-          float* o = a.out + (size_t)(vec0 + col) * a.ldo + i;
-          float v = (z & 1 ? acc[x][y][z >> 1].y : acc[x][y][z >> 1].x) * sh_back[col];
+          float* o = a.out + (size_t)(GATHER ? tile_vec : col) * a.ldo + i;
+          float v = (z & 1 ? acc[x][y][z >> 1].y : acc[x][y][z >> 1].x) * 4194304.f *
+                    sh_back[GATHER ? tile_vec & 1 : col];
           if (a.add) v += *o;
           if (GATHER) {
-            const int32_t id = a.ids[(size_t)vec0 * a.K + i];
+            const int32_t id = a.ids[(size_t)tile_vec * a.K + i];
             if (id < 0 || id >= a.n) {
               record_error(err, kDevErrBadId);
               v = __int_as_float(0x7fc00000);
@@ -499,81 +547,79 @@ q4_kernel(Q4Launch a, int* err) {
 
 constexpr size_t kSmemMost = 226 * 1024;
 
-// The kernel's shapes. Up to 8 vectors: stages of 256 codes, 8 warps, two CTAs
-// an SM; up to 16: 128 codes (h alone takes 160 KB at d = 5120), one CTA.
+// The kernel's shapes: stages of 256 codes (128 for groups of 32, which carry
+// four scales a row and block), 16 warps an SM, in two CTAs for the gather. From
+// 9 vectors on stages of 128 codes and 12 warps (h alone takes 160 KB at d = 5120).
 struct Form {
   int nt, warps, sb, ns;
 };
-constexpr Form kFormOne = {1, 8, 2, 3}, kFormTwo = {2, 8, 1, 3};
-// Groups of 32 carry four scales a row and block ahead: stages of one block.
-constexpr Form kFormOne32 = {1, 8, 1, 5};
-constexpr Form form_of(int nt, int group) {
-  return nt == 2 ? kFormTwo : group == 32 ? kFormOne32 : kFormOne;
+constexpr Form form_of(int nt, int group, bool gather) {
+  return nt == 2 ? Form{2, 12, 1, 2}
+                 : Form{1, gather ? 8 : 16, group == 32 ? 1 : 2, group == 32 ? 4 : 2};
 }
 
-size_t smem_bytes(const Form& f, int kd, int group, int vecs, int cols, bool mins, bool split) {
+size_t smem_bytes(const Form& f, int kd, int group, int vecs, int cols, bool split) {
   const int blocks = (kd + kBlockK - 1) / kBlockK;
-  return (size_t)h_bytes(blocks, vecs, mins ? blocks * (kBlockK / group) * cols : 0) +
+  return (size_t)h_bytes(blocks, vecs, blocks * (kBlockK / group) * cols) +
          (size_t)f.warps * f.ns * f.sb * 2048 +
-         (split ? (size_t)f.warps * f.nt * 8 * 32 * sizeof(float) : 0);
+         (split ? (size_t)2 * f.warps * f.nt * 8 * 32 * sizeof(float) : 0);
 }
 
-template <bool BF16, int G, int NT, bool MINS, bool GATHER>
+template <bool BF16, int G, int NT, int MODE, bool GATHER>
 cudaError_t launch_one(const Q4Launch& in, int* err, cudaStream_t s) {
-  constexpr Form f = form_of(NT, G);
-  auto kernel = q4_kernel<BF16, G, NT, f.warps, f.sb, f.ns, MINS, GATHER>;
+  constexpr Form f = form_of(NT, G, GATHER);
+  auto kernel = q4_kernel<BF16, G, NT, f.warps, f.sb, f.ns, MODE, GATHER>;
   Q4Launch a = in;
   const int kd = a.k_hi - a.k_lo, vecs = GATHER ? 1 : (a.M < NT * 8 ? a.M : NT * 8);
   const int cols = GATHER ? 1 : NT * 8;
   const int64_t rows = GATHER ? a.K : a.n;
   a.tiles = (int)((rows + kRowsWarp - 1) / kRowsWarp);
   const int stages = ((kd + kBlockK - 1) / kBlockK + f.sb - 1) / f.sb;
-  const size_t alone = smem_bytes(f, kd, G, vecs, cols, MINS, false);
-  const int per_sm = alone <= 105 * 1024 && NT == 1 ? 2 : 1;
-  const int64_t warps = (int64_t)sm_count() * per_sm * f.warps;
-  // How many warps share a tile: the last round of tiles leaves warps idle, and
-  // shares of a tile fill it better; a round of s-shares takes 1/s of the time
-  // of a round of tiles (plus the join, so s must gain a twentieth at least).
-  const int64_t all = (int64_t)a.tiles * (GATHER ? a.M : 1);
+  const size_t most = smem_bytes(f, kd, G, vecs, cols, true);
+  const int resident = sm_count() * (f.warps == 8 && 2 * (most + 1024) <= 228 * 1024 ? 2 : 1);
+  // How many warps share a tile: whole tiles leave warps idle in the last round,
+  // and a CTA's longest run of units sets the time; a unit of s-shares takes
+  // 1/s of the time of a tile (plus the join, so it must gain a twentieth).
+  const int64_t vectors = GATHER ? a.M : 1;
   a.split = 1;
-  double best = (double)((all + warps - 1) / warps);
-  for (int x = 2; x <= f.warps && x <= stages; x *= 2) {
-    if (smem_bytes(f, kd, G, vecs, cols, MINS, true) > kSmemMost) break;
-    const int64_t teams = warps / x;
-    const double time = (double)((all + teams - 1) / teams) / x;
+  double best = 1e300;
+  for (int x = 1; x <= f.warps && x <= stages && f.warps % x == 0; x *= 2) {
+    if (x > 1 && most > kSmemMost) break;
+    const int64_t teams = f.warps / x, units = (a.tiles + teams - 1) / teams * vectors;
+    const double time = (double)((units + resident - 1) / resident) / x;
     if (time < 0.95 * best) {
       best = time;
       a.split = x;
     }
   }
-  const size_t smem = smem_bytes(f, kd, G, vecs, cols, MINS, a.split > 1);
+  const size_t smem = smem_bytes(f, kd, G, vecs, cols, a.split > 1);
   static int smem_set[64] = {0};
   cudaError_t e = ensure_dynamic_smem(kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
-  const int per = f.warps / a.split, ctas = (a.tiles + per - 1) / per;
-  const int resident = sm_count() * per_sm;
-  const unsigned gx = GATHER ? ctas : (ctas < resident ? ctas : resident);
-  return launch_kernel(true, kernel, dim3(gx, GATHER ? a.M : 1), dim3(f.warps * 32), smem, s, a,
-                       err);
+  const int64_t teams = f.warps / a.split, units = (a.tiles + teams - 1) / teams * vectors;
+  return launch_kernel(true, kernel, dim3((unsigned)(units < resident ? units : resident)),
+                       dim3(f.warps * 32), smem, s, a, err);
 }
 
-template <bool BF16, int G, bool MINS>
+template <bool BF16, int G, int MODE>
 cudaError_t launch_cols(const Q4Launch& a, int* err, cudaStream_t s) {
-  if (a.ids) return launch_one<BF16, G, 1, MINS, true>(a, err, s);
-  if (a.M <= 8) return launch_one<BF16, G, 1, MINS, false>(a, err, s);
-  return launch_one<BF16, G, 2, MINS, false>(a, err, s);
+  if (a.ids) return launch_one<BF16, G, 1, MODE, true>(a, err, s);
+  if (a.M <= 8 || MODE == kCentred) return launch_one<BF16, G, 1, MODE, false>(a, err, s);
+  return launch_one<BF16, G, MODE == kCentred ? 1 : 2, MODE, false>(a, err, s);
 }
 
 template <bool BF16, int G>
-cudaError_t launch_mins(const Q4Launch& a, int* err, cudaStream_t s) {
-  return a.mins ? launch_cols<BF16, G, true>(a, err, s) : launch_cols<BF16, G, false>(a, err, s);
+cudaError_t launch_mode(const Q4Launch& a, int* err, cudaStream_t s) {
+  if (a.mins) return launch_cols<BF16, G, kMins>(a, err, s);
+  return a.d < kCentreD ? launch_cols<BF16, G, kCentred>(a, err, s)
+                        : launch_cols<BF16, G, kPlain>(a, err, s);
 }
 
 template <bool BF16>
 cudaError_t launch_group(const Q4Launch& a, int group, int* err, cudaStream_t s) {
-  if (group == 128) return launch_mins<BF16, 128>(a, err, s);
-  if (group == 64) return launch_mins<BF16, 64>(a, err, s);
-  return launch_mins<BF16, 32>(a, err, s);
+  if (group == 128) return launch_mode<BF16, 128>(a, err, s);
+  if (group == 64) return launch_mode<BF16, 64>(a, err, s);
+  return launch_mode<BF16, 32>(a, err, s);
 }
 
 }  // namespace
@@ -592,15 +638,15 @@ cudaError_t launch_q4(const Q4Args& q, int* err, cudaStream_t s) {
       ((reinterpret_cast<uintptr_t>(q.scales) | reinterpret_cast<uintptr_t>(q.mins)) & 15u) == 0;
   // hidden vectors of one pass over the rows, then pieces of d, as far as h
   // fits in shared memory; a later piece adds to the former's sums
-  const int most = q.ids ? q.M : 16;
+  const int most = q.ids ? q.M : !q.mins && q.d < kCentreD ? 8 : 16;
   for (int m = 0; m < q.M; m += most) {
     a.M = q.M - m < most ? q.M - m : most;
     a.h = static_cast<const uint16_t*>(q.h) + (size_t)m * q.d;
     a.out = q.out + (size_t)m * a.ldo;
-    const Form f = form_of(!q.ids && a.M > 8 ? 2 : 1, q.group);
+    const Form f = form_of(!q.ids && a.M > 8 ? 2 : 1, q.group, q.ids != nullptr);
     const int vecs = q.ids ? 1 : a.M, cols = q.ids ? 1 : f.nt * 8;
     int piece = q.d;
-    while (smem_bytes(f, piece, q.group, vecs, cols, q.mins != nullptr, false) > kSmemMost)
+    while (smem_bytes(f, piece, q.group, vecs, cols, false) > kSmemMost)
       piece = ((piece + 1) / 2 + kBlockK - 1) / kBlockK * kBlockK;
     for (int k = 0; k < q.d; k += piece) {
       a.k_lo = k;
