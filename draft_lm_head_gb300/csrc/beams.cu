@@ -5,15 +5,16 @@
 // score(b, j) = parent_b + (x_bj - lse_b), lse_b = log sum_j exp x_bj. Within a
 // row the order of the scores is the order of x, so one pass over a row gives
 // both its log-sum-exp and its k largest x; only those few are ever scored.
-//   beam_rows:  a CTA streams one slice of one row through registers (32
-//     values a thread a tile), keeping the running maximum and sum of the
-//     softmax and the slice's k best so far.
+//   beam_rows:  a warp streams one slice of one row through registers (16
+//     values a lane a tile, the next tile's loads in flight), keeping a running
+//     reference and sum of the softmax and the slice's k best so far; no
+//     barrier, and past the first tile little but the exponentials.
 //   beam_merge: a CTA per sequence turns the slices' sums into lse and picks
 //     the k best of beams x slices x k scored entries.
 // Bound by reading the logits once. The sums of exp are 32-bit within a
-// thread (at most 32 x tiles terms) and 64-bit across threads, and the scores
-// of the few candidates are formed and compared in 64 bits: beams meet at the
-// border of the k with gaps below 32-bit rounding.
+// lane and 64-bit across lanes, and the scores of the few candidates are formed
+// and compared in 64 bits: beams meet at the border of the k with gaps below
+// 32-bit rounding.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -23,10 +24,11 @@ namespace lmhead {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kPerThread = 32;
-constexpr int kTile = kRowThreads * kPerThread;  // 8192 entries
-constexpr int kBuf = 1024;                       // candidates held between compactions
+constexpr int kPerLane = 16;
+constexpr int kTile = 32 * kPerLane;  // entries of a warp's tile
+constexpr int kBuf = 1024;            // the merge's candidates
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLog2e = 1.4426950408889634f;
 
 template <typename T> struct Elem;
 template <> struct Elem<float> {
@@ -59,10 +61,32 @@ template <> struct Elem<__half> {
 };
 
 struct Slice {  // what a slice of a row leaves
-  float top;    // its largest value
+  float top;    // a reference value
   float pad;
   double sum;   // of exp(x - top)
 };
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // The k-th largest (or -inf) of the block's per-thread values, by warp 0:
 // each round takes one copy of the current largest away.
@@ -102,148 +126,111 @@ __device__ __forceinline__ float kth_of_threads(float mine, int k, float* sh, fl
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads)
-beam_rows_kernel(const T* logits, int64_t stride, int n, int slice_len, int k,
+__global__ void __launch_bounds__(kRowThreads, 4)
+beam_rows_kernel(const T* logits, int64_t stride, int n, int rows, int nsl, int slice_len, int k,
                  const uint8_t* finished, Slice* slices, float* best_v, int32_t* best_i) {
-  __shared__ uint64_t buf[kBuf + kBeamMaxK];
-  __shared__ uint64_t best[kBeamMaxK];
-  __shared__ float sh_f[kRowThreads];
-  __shared__ double sh_d[kRowThreads / 32];
-  __shared__ float sh_out;
-  __shared__ int sh_count[3];  // in turn: one counts, the next one is cleared
-  __shared__ uint64_t sh_key[kRowThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x;
-  const int row = blockIdx.y, sl = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + warp;
+  if (unit >= (int64_t)rows * nsl) return;
+  const int row = (int)(unit / nsl), sl = (int)(unit - (int64_t)row * nsl);
   if (finished && finished[row]) return;  // its one entry is its own score
-  constexpr int V = Elem<T>::kVec;
+  constexpr int V = Elem<T>::kVec, U = kPerLane / V;
   const T* x = logits + (int64_t)row * stride;
   // 16-byte reads at 16-byte boundaries: the row starts `off` entries after
   // one, and slices are cut at them
   const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
   const int lo = max(0, sl * slice_len - off), hi = min(n, (sl + 1) * slice_len - off);
-  float m = kNegInf, s = 0.f;
-  int have = 0;              // entries in `best`, sorted, best first
-  float floor_v = kNegInf;   // the k-th best so far once have == k
-  if (tid < 3) sh_count[tid] = 0;
-  cta_sync();
-  int turn = 0;
-  for (int base = sl * (slice_len / V); base * V - off < hi; base += kTile / V) {
-    float f[kPerThread];
-    float tm = kNegInf;
+  auto inside = [&](int base) { return base * V - off >= lo && base * V - off + kTile <= hi; };
+  auto load = [&](int base, uint4 (&raw)[U]) {  // of a tile that lies within the slice
+    if (inside(base))
 #pragma unroll
-    for (int u = 0; u < kPerThread / V; ++u) {
-      const int e = (base + u * kRowThreads + tid) * V - off;
-      if (e >= lo && e + V <= hi) {
-        Elem<T>::unpack(ldg_nc_v4(x + e), f + u * V);
-      } else {
+      for (int u = 0; u < U; ++u) raw[u] = ldg_nc_v4(x + (base + u * 32 + lane) * V - off);
+  };
+  float m = kNegInf;
+  float2 s2 = make_float2(0.f, 0.f);
+  uint64_t best = 0;        // lane j: the (j + 1)-th best entry so far, 0 for none
+  float floor_v = kNegInf;  // the k-th of them
+  int base = sl * (slice_len / V);
+  uint4 raw[U];
+  load(base, raw);
+  for (; base * V - off < hi; base += kTile / V) {
+    float f[kPerLane];
+    if (inside(base)) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          f[u * V + i] = e + i >= lo && e + i < hi ? Elem<T>::get(x + e + i) : kNegInf;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) tm = fmaxf(tm, f[i]);
-    // the softmax's running maximum and sum
-    const float nm = fmaxf(m, tm), ref = nm == kNegInf ? 0.f : nm;
-    if (m != nm) s *= expf(m - ref);
-    m = nm;
-    float ts = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) ts += expf(f[i] - ref);
-    s += ts;
-    // candidates: everything that may be among the slice's k best. While fewer
-    // than k are held, the k-th largest of the threads' maxima bounds them from
-    // below; later entries must beat the k-th best (an equal one comes later).
-    const bool first = have < k;
-    const float bound = first ? kth_of_threads(tm, k, sh_f, &sh_out) : floor_v;
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-      mine += (first ? f[i] >= bound : f[i] > bound) && f[i] > kNegInf;
-    int at = 0;
-    if (mine) at = atomicAdd(&sh_count[turn], mine);
-    if (tid == 0) sh_count[turn == 2 ? 0 : turn + 1] = 0;
-    cta_sync();
-    const int total = sh_count[turn];
-    turn = turn == 2 ? 0 : turn + 1;
-    if (total == 0) continue;
-    int fill = total;
-    if (total <= kBuf) {
-      if (mine) {
-#pragma unroll
-        for (int u = 0; u < kPerThread / V; ++u)
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float v = f[u * V + i];
-            if ((first ? v >= bound : v > bound) && v > kNegInf)
-              buf[at++] = select_key(v, (base + u * kRowThreads + tid) * V - off + i);
-          }
-      }
+      for (int u = 0; u < U; ++u) Elem<T>::unpack(raw[u], f + u * V);
     } else {
-      // many equal values: take the tile's k best one by one
-      uint64_t last = ~0ull;
-      for (fill = 0; fill < k; ++fill) {
-        uint64_t top = 0;
 #pragma unroll
-        for (int u = 0; u < kPerThread / V; ++u)
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float v = f[u * V + i];
-            const uint64_t key = select_key(v, (base + u * kRowThreads + tid) * V - off + i);
-            if (v > kNegInf && key < last && key > top) top = key;
-          }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, top, o);
-          top = other > top ? other : top;
-        }
-        if ((tid & 31) == 0) sh_key[tid >> 5] = top;
-        cta_sync();
-        top = 0;
-        for (int w = 0; w < kRowThreads / 32; ++w) top = sh_key[w] > top ? sh_key[w] : top;
-        cta_sync();
-        if (top == 0) break;
-        if (tid == 0) buf[fill] = top;
-        last = top;
+      for (int i = 0; i < kPerLane; ++i) {
+        const int e = (base + i / V * 32 + lane) * V - off + i % V;
+        f[i] = e >= lo && e < hi ? Elem<T>::get(x + e) : kNegInf;
       }
     }
-    // join with the best so far; an entry's place is the count of larger keys
-    if (tid < have) buf[fill + tid] = best[tid];
-    cta_sync();
-    const int all = fill + have;
-    for (int c = tid; c < all; c += kRowThreads) {
-      const uint64_t key = buf[c];
-      int place = 0;
-      for (int o = 0; o < all && place < k; ++o) place += buf[o] > key;
-      if (place < k) best[place] = key;
+    load(base + kTile / V, raw);
+    float tm = f[0];
+#pragma unroll
+    for (int i = 1; i < kPerLane; ++i) tm = fmaxf(tm, f[i]);
+    if (!(tm >= kNegInf)) tm = kNegInf;  // all NaN
+    // the sum is kept relative to a reference that moves only when the values
+    // pass it by far (2^86 is well within fp32)
+    if (tm > m + 60.f || (m == kNegInf && tm > kNegInf)) {
+      const float f0 = m == kNegInf ? 0.f : exp2_fast((m - tm) * kLog2e);
+      s2.x *= f0;
+      s2.y *= f0;
+      m = tm;
     }
-    have = min(all, k);
-    cta_sync();
-    if (have == k) floor_v = key_score(best[k - 1]);
+    const float ref = m == kNegInf ? 0.f : -m;
+#pragma unroll
+    for (int i = 0; i < kPerLane; i += 2) {
+      const float2 d = mul2(add2(make_float2(f[i], f[i + 1]), make_float2(ref, ref)),
+                            make_float2(kLog2e, kLog2e));
+      s2 = add2(s2, make_float2(exp2_fast(d.x), exp2_fast(d.y)));
+    }
+    // Into the k best, one after the other: the largest value not yet taken (the
+    // lowest index among equals) while it beats the k-th best. An equal value
+    // further on has a higher index and stays out.
+    while (true) {
+      const bool want = tm > floor_v;
+      if (!__any_sync(0xFFFFFFFFu, want)) break;
+      const uint32_t key = want ? float_key(tm) : 0u;
+      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, key);
+      int own = 0;  // the first place of the lane's largest
+#pragma unroll
+      for (int i = kPerLane - 1; i >= 0; --i) own = f[i] == tm ? i : own;
+      const uint32_t index =
+          key == top ? (uint32_t)((base + own / V * 32 + lane) * V - off + own % V) : ~0u;
+      const uint32_t win = __reduce_min_sync(0xFFFFFFFFu, index);
+      const uint64_t entry = ((uint64_t)top << 32) | (uint32_t)~win;
+      const int place = __popc(__ballot_sync(0xFFFFFFFFu, best > entry));
+      const uint64_t above = __shfl_up_sync(0xFFFFFFFFu, best, 1);
+      if (lane > place) best = above;
+      if (lane == place) best = entry;
+      const uint64_t least = __shfl_sync(0xFFFFFFFFu, best, k - 1);
+      floor_v = least == 0 ? kNegInf : key_score(least);
+      if (index == win) {
+        tm = kNegInf;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+          if (i == own) f[i] = kNegInf;
+          tm = fmaxf(tm, f[i]);
+        }
+      }
+    }
   }
-  // the slice's maximum and sum
-  sh_f[tid] = m;
-  cta_sync();
-  float top = kNegInf;
-  for (int i = 0; i < kRowThreads; i += 32) top = fmaxf(top, sh_f[i + (tid & 31)]);
-  top = warp_max(top);
-  double part = s == 0.f && m == kNegInf ? 0.0 : (double)s * exp((double)m - (double)top);
+  // the slice's reference and sum
+  const float s = s2.x + s2.y, top = warp_max(m);
+  // (the GPU's fp64 units are few: the factor is fp32's, like each term's)
+  double part = m == kNegInf && s == 0.f ? 0.f : s * exp2_fast((m - top) * kLog2e);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
-  if ((tid & 31) == 0) sh_d[tid >> 5] = part;
-  cta_sync();
-  const size_t at = (size_t)row * gridDim.x + sl;
-  if (tid == 0) {
-    double sum = 0;
-    for (int w = 0; w < kRowThreads / 32; ++w) sum += sh_d[w];
-    slices[at].top = top;
-    slices[at].sum = sum;
+  if (lane == 0) {
+    slices[unit].top = top;
+    slices[unit].sum = part;
   }
-  if (tid < k) {
-    best_v[at * k + tid] = tid < have ? key_score(best[tid]) : kNegInf;
-    best_i[at * k + tid] = tid < have ? key_id(best[tid]) : -1;
+  if (lane < k) {
+    best_v[unit * k + lane] = best ? key_score(best) : kNegInf;
+    best_i[unit * k + lane] = best ? key_id(best) : -1;
   }
 }
 
@@ -268,18 +255,25 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
   pdl_trigger();
   const int tid = threadIdx.x, seq = blockIdx.x, B = a.beams, k = a.k;
   const int32_t n = (int32_t)a.n;
-  for (int b = tid; b < B; b += kRowThreads) {
-    const int row = seq * B + b;
+  for (int b = tid >> 5; b < B; b += kRowThreads / 32) {  // a warp per row
+    const int row = seq * B + b, lane = tid & 31;
     if (a.finished && a.finished[row]) continue;
+    const Slice* sl = slices + (size_t)row * nsl;
     float top = kNegInf;
-    for (int i = 0; i < nsl; ++i) top = fmaxf(top, slices[(size_t)row * nsl + i].top);
+    for (int i = lane; i < nsl; i += 32) top = fmaxf(top, sl[i].top);
+    top = warp_max(top);
     double sum = 0;
-    for (int i = 0; i < nsl; ++i) {
-      const Slice sl = slices[(size_t)row * nsl + i];
-      if (sl.top != kNegInf || sl.sum != 0.0) sum += sl.sum * exp((double)sl.top - (double)top);
+    for (int i = lane; i < nsl; i += 32) {
+      const Slice v = sl[i];
+      if (v.top != kNegInf || v.sum != 0.0)
+        sum += v.sum * (double)exp2_fast((v.top - top) * kLog2e);
     }
-    row_top[b] = top;
-    row_log[b] = log(sum);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) {
+      row_top[b] = top;
+      row_log[b] = log(sum);
+    }
   }
   if (tid == 0) sh_count = 0;
   cta_sync();
@@ -301,23 +295,39 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
     return sc == sc ? sc : (double)kNegInf;
   };
   // scores rounded to 32 bits keep their order, so the k-th largest of the
-  // threads' rounded maxima bounds the k best from below
+  // threads' rounded maxima bounds the k best from below; a thread keeps its
+  // first kKept scores (fp64 arithmetic is slow here)
+  constexpr int kKept = 4;
+  double kept[kKept];
   float mine = kNegInf;
-  for (int e = tid; e < all; e += kRowThreads) {
+#pragma unroll
+  for (int j = 0; j < kKept; ++j) {
+    int32_t flat;
+    const int e = tid + j * kRowThreads;
+    kept[j] = e < all ? entry(e, flat) : (double)kNegInf;
+    mine = fmaxf(mine, (float)kept[j]);
+  }
+  for (int e = tid + kKept * kRowThreads; e < all; e += kRowThreads) {
     int32_t flat;
     mine = fmaxf(mine, (float)entry(e, flat));
   }
   const float bound = kth_of_threads(mine, k, sh_f, &sh_out);
-  for (int e = tid; e < all; e += kRowThreads) {
+  auto offer = [&](int e, double sc) {
+    const int at = atomicAdd(&sh_count, 1);
+    if (at < kBuf) {
+      int32_t flat;
+      entry(e, flat);
+      b_score[at] = sc;
+      b_flat[at] = flat;
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < kKept; ++j)
+    if (kept[j] > (double)kNegInf && (float)kept[j] >= bound) offer(tid + j * kRowThreads, kept[j]);
+  for (int e = tid + kKept * kRowThreads; e < all; e += kRowThreads) {
     int32_t flat;
     const double sc = entry(e, flat);
-    if (sc > (double)kNegInf && (float)sc >= bound) {
-      const int at = atomicAdd(&sh_count, 1);
-      if (at < kBuf) {
-        b_score[at] = sc;
-        b_flat[at] = flat;
-      }
-    }
+    if (sc > (double)kNegInf && (float)sc >= bound) offer(e, sc);
   }
   cta_sync();
   int fill = sh_count;
@@ -421,12 +431,13 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(ReorderArgs a, int* e
   }
 }
 
-// Entries of a row per CTA: whole tiles, enough CTAs to fill the GPU, but
-// slices as long as that allows (each slice costs k merged entries).
+// Entries of a row per warp: whole tiles, as many slices as leave every warp
+// slot of the GPU (32 an SM at the kernel's registers) one of them.
 int slice_len(int rows, int64_t n) {
   const int64_t tiles = (n + kTile - 1) / kTile;
   const int sms = sm_count() > 0 ? sm_count() : 1;
-  const int64_t want = ((int64_t)sms * 8 + rows - 1) / rows;  // slices a row
+  int64_t want = (int64_t)sms * 32 / rows;
+  if (want < 1) want = 1;
   const int64_t per = tiles <= want ? 1 : (tiles + want - 1) / want;
   return (int)(per * kTile);
 }
@@ -448,18 +459,19 @@ cudaError_t launch_beam_select(const BeamArgs& a, void* scratch, cudaStream_t s)
   Slice* sl = static_cast<Slice*>(scratch);
   float* bv = reinterpret_cast<float*>(sl + cells);
   int32_t* bi = reinterpret_cast<int32_t*>(bv + cells * a.k);
-  const dim3 grid(nsl, rows), block(kRowThreads);
+  const int warps = kRowThreads / 32;
+  const dim3 grid((unsigned)((cells + warps - 1) / warps)), block(kRowThreads);
   cudaError_t e;
   if (a.dtype == LMHEAD_FP32)
     e = launch_kernel(true, beam_rows_kernel<float>, grid, block, 0, s, (const float*)a.logits,
-                      a.row_stride, (int)a.n, len, a.k, a.finished, sl, bv, bi);
+                      a.row_stride, (int)a.n, rows, nsl, len, a.k, a.finished, sl, bv, bi);
   else if (a.dtype == LMHEAD_BF16)
     e = launch_kernel(true, beam_rows_kernel<__nv_bfloat16>, grid, block, 0, s,
-                      (const __nv_bfloat16*)a.logits, a.row_stride, (int)a.n, len, a.k, a.finished,
-                      sl, bv, bi);
+                      (const __nv_bfloat16*)a.logits, a.row_stride, (int)a.n, rows, nsl, len, a.k,
+                      a.finished, sl, bv, bi);
   else
     e = launch_kernel(true, beam_rows_kernel<__half>, grid, block, 0, s, (const __half*)a.logits,
-                      a.row_stride, (int)a.n, len, a.k, a.finished, sl, bv, bi);
+                      a.row_stride, (int)a.n, rows, nsl, len, a.k, a.finished, sl, bv, bi);
   if (e != cudaSuccess) return e;
   return launch_kernel(true, beam_merge_kernel, dim3(a.S), block, 0, s, a, nsl, (const Slice*)sl,
                        (const float*)bv, (const int32_t*)bi);
