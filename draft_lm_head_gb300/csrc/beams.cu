@@ -244,6 +244,8 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
   // lse in its two parts: x - top is small where top is not
   __shared__ float row_top[kBeamMaxBeams];
   __shared__ double row_log[kBeamMaxBeams];
+  __shared__ float row_score[kBeamMaxBeams];
+  __shared__ bool row_done[kBeamMaxBeams];
   __shared__ double b_score[kBuf];
   __shared__ int32_t b_flat[kBuf];
   __shared__ float sh_f[kRowThreads];
@@ -253,58 +255,72 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
   __shared__ int32_t w_flat[kRowThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, seq = blockIdx.x, B = a.beams, k = a.k;
+  const int tid = threadIdx.x, lane = tid & 31, seq = blockIdx.x, B = a.beams, k = a.k;
   const int32_t n = (int32_t)a.n;
+  const int per = nsl * k, all = B * per;
+  const size_t row0 = (size_t)seq * B, e0 = row0 * per;
+  // a thread's first kKept entries are under way while the rows' sums are made
+  constexpr int kKept = 4;
+  float kept_v[kKept];
+  int32_t kept_i[kKept];
+#pragma unroll
+  for (int j = 0; j < kKept; ++j) {
+    const int e = tid + j * kRowThreads;
+    kept_v[j] = e < all ? best_v[e0 + e] : 0.f;
+    kept_i[j] = e < all ? best_i[e0 + e] : -1;
+  }
   for (int b = tid >> 5; b < B; b += kRowThreads / 32) {  // a warp per row
-    const int row = seq * B + b, lane = tid & 31;
-    if (a.finished && a.finished[row]) continue;
-    const Slice* sl = slices + (size_t)row * nsl;
+    const Slice* sl = slices + (row0 + b) * nsl;
+    const bool done = a.finished && a.finished[row0 + b];
+    const float score = a.scores[row0 + b];
     float top = kNegInf;
-    for (int i = lane; i < nsl; i += 32) top = fmaxf(top, sl[i].top);
-    top = warp_max(top);
     double sum = 0;
-    for (int i = lane; i < nsl; i += 32) {
-      const Slice v = sl[i];
+    for (int i0 = 0; i0 < nsl; i0 += 32) {
+      Slice v;
+      v.top = kNegInf;
+      v.sum = 0;
+      if (i0 + lane < nsl) v = sl[i0 + lane];
+      const float now = fmaxf(top, warp_max(v.top));
+      if (now != top) sum *= (double)exp2_fast((top - now) * kLog2e);
+      top = now;
       if (v.top != kNegInf || v.sum != 0.0)
         sum += v.sum * (double)exp2_fast((v.top - top) * kLog2e);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) {
+      row_done[b] = done;
+      row_score[b] = score;
       row_top[b] = top;
-      row_log[b] = log(sum);
+      row_log[b] = done ? 0.0 : log(sum);
     }
   }
   if (tid == 0) sh_count = 0;
   cta_sync();
-  const int per = nsl * k, all = B * per;
-  // entry e of the sequence: its score, -inf when it cannot be taken
-  auto entry = [&](int e, int32_t& flat) -> double {
-    const int b = e / per, r = e - b * per, row = seq * B + b;
+  // entry e of the sequence, value v at index i of its row: its score, -inf when
+  // it cannot be taken
+  auto score_of = [&](int e, float v, int32_t i, int32_t& flat) -> double {
+    const int b = e / per;
     double sc;
-    if (a.finished && a.finished[row]) {
+    if (row_done[b]) {
       flat = b * n;
-      sc = r == 0 ? (double)a.scores[row] : (double)kNegInf;
+      sc = e == b * per ? (double)row_score[b] : (double)kNegInf;
     } else {
-      const int32_t i = best_i[(size_t)row * per + r];
       flat = b * n + i;
       if (i < 0) return (double)kNegInf;
-      sc = (double)a.scores[row] +
-           (((double)best_v[(size_t)row * per + r] - (double)row_top[b]) - row_log[b]);
+      sc = (double)row_score[b] + (((double)v - (double)row_top[b]) - row_log[b]);
     }
     return sc == sc ? sc : (double)kNegInf;
   };
+  auto entry = [&](int e, int32_t& flat) { return score_of(e, best_v[e0 + e], best_i[e0 + e], flat); };
   // scores rounded to 32 bits keep their order, so the k-th largest of the
-  // threads' rounded maxima bounds the k best from below; a thread keeps its
-  // first kKept scores (fp64 arithmetic is slow here)
-  constexpr int kKept = 4;
+  // threads' rounded maxima bounds the k best from below
   double kept[kKept];
   float mine = kNegInf;
 #pragma unroll
   for (int j = 0; j < kKept; ++j) {
-    int32_t flat;
     const int e = tid + j * kRowThreads;
-    kept[j] = e < all ? entry(e, flat) : (double)kNegInf;
+    kept[j] = e < all ? score_of(e, kept_v[j], kept_i[j], kept_i[j]) : (double)kNegInf;
     mine = fmaxf(mine, (float)kept[j]);
   }
   for (int e = tid + kKept * kRowThreads; e < all; e += kRowThreads) {
@@ -312,22 +328,20 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
     mine = fmaxf(mine, (float)entry(e, flat));
   }
   const float bound = kth_of_threads(mine, k, sh_f, &sh_out);
-  auto offer = [&](int e, double sc) {
+  auto offer = [&](double sc, int32_t flat) {
+    if (!(sc > (double)kNegInf) || (float)sc < bound) return;
     const int at = atomicAdd(&sh_count, 1);
     if (at < kBuf) {
-      int32_t flat;
-      entry(e, flat);
       b_score[at] = sc;
       b_flat[at] = flat;
     }
   };
 #pragma unroll
-  for (int j = 0; j < kKept; ++j)
-    if (kept[j] > (double)kNegInf && (float)kept[j] >= bound) offer(tid + j * kRowThreads, kept[j]);
+  for (int j = 0; j < kKept; ++j) offer(kept[j], kept_i[j]);
   for (int e = tid + kKept * kRowThreads; e < all; e += kRowThreads) {
     int32_t flat;
     const double sc = entry(e, flat);
-    if (sc > (double)kNegInf && (float)sc >= bound) offer(e, sc);
+    offer(sc, flat);
   }
   cta_sync();
   int fill = sh_count;
@@ -389,7 +403,7 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
     if (place >= k) continue;
     const int b = flat / n, i = flat - b * n, row = seq * B + b;
     parent[place] = b;
-    token[place] = a.finished && a.finished[row] ? a.eos
+    token[place] = row_done[b] ? a.eos
                    : a.ids ? a.ids[(size_t)row * n + i] : i;
     score[place] = (float)sc;
   }
