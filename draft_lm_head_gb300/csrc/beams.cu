@@ -11,10 +11,11 @@
 //     barrier, and past the first tile little but the exponentials.
 //   beam_merge: a CTA per sequence turns the slices' sums into lse and picks
 //     the k best of beams x slices x k scored entries.
-// Bound by reading the logits once. The sums of exp are 32-bit within a
-// lane and 64-bit across lanes, and the scores of the few candidates are formed
-// and compared in 64 bits: beams meet at the border of the k with gaps below
-// 32-bit rounding.
+// Bound by reading the logits once. Beams meet at the border of the k with gaps
+// below 32-bit rounding, so a lane's sums of exp are 32-bit, but everything
+// across lanes, and the scores of the few candidates, are pairs of fp32 numbers
+// (the rounded value and what its rounding left: about 48 bits; fp64 units are
+// too few on this GPU, the merge took twice as long with them).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -60,10 +61,30 @@ template <> struct Elem<__half> {
   }
 };
 
-struct Slice {  // what a slice of a row leaves
-  float top;    // a reference value
+// h + l, |l| at most half a step of h.
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {  // exactly
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = two_sum(a.h, b.h);
+  const float l = s.l + (a.l + b.l), h = s.h + l;
+  return {h, l - (h - s.h)};
+}
+__device__ __forceinline__ Pair warp_sum(Pair v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = add(v, Pair{__shfl_xor_sync(0xFFFFFFFFu, v.h, o), __shfl_xor_sync(0xFFFFFFFFu, v.l, o)});
+  return v;
+}
+
+struct __align__(16) Slice {  // what a slice of a row leaves
+  float top;  // a reference value
+  Pair sum;   // of exp(x - top)
   float pad;
-  double sum;   // of exp(x - top)
 };
 
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -220,21 +241,18 @@ beam_rows_kernel(const T* logits, int64_t stride, int n, int rows, int nsl, int 
   }
   // the slice's reference and sum
   const float s = s2.x + s2.y, top = warp_max(m);
-  // (the GPU's fp64 units are few: the factor is fp32's, like each term's)
-  double part = m == kNegInf && s == 0.f ? 0.f : s * exp2_fast((m - top) * kLog2e);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
-  if (lane == 0) {
-    slices[unit].top = top;
-    slices[unit].sum = part;
-  }
+  const Pair sum =
+      warp_sum(Pair{m == kNegInf && s == 0.f ? 0.f : s * exp2_fast((m - top) * kLog2e), 0.f});
+  if (lane == 0) slices[unit] = {top, sum, 0.f};
   if (lane < k) {
     best_v[unit * k + lane] = best ? key_score(best) : kNegInf;
     best_i[unit * k + lane] = best ? key_id(best) : -1;
   }
 }
 
-__device__ __forceinline__ bool ahead(double sa, int32_t ia, double sb, int32_t ib) {
+// Order of the merge: the larger score (as a key that orders like the pair of
+// it; 0 is below every score that can be taken), then the lower index.
+__device__ __forceinline__ bool ahead(uint64_t sa, int32_t ia, uint64_t sb, int32_t ib) {
   return sa > sb || (sa == sb && ia < ib);
 }
 
@@ -243,15 +261,15 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
                   const int32_t* best_i) {
   // lse in its two parts: x - top is small where top is not
   __shared__ float row_top[kBeamMaxBeams];
-  __shared__ double row_log[kBeamMaxBeams];
+  __shared__ Pair row_log[kBeamMaxBeams];
   __shared__ float row_score[kBeamMaxBeams];
   __shared__ bool row_done[kBeamMaxBeams];
-  __shared__ double b_score[kBuf];
+  __shared__ uint64_t b_score[kBuf];
   __shared__ int32_t b_flat[kBuf];
   __shared__ float sh_f[kRowThreads];
   __shared__ float sh_out;
   __shared__ int sh_count;
-  __shared__ double w_score[kRowThreads / 32];
+  __shared__ uint64_t w_score[kRowThreads / 32];
   __shared__ int32_t w_flat[kRowThreads / 32];
   pdl_wait();
   pdl_trigger();
@@ -274,62 +292,72 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
     const bool done = a.finished && a.finished[row0 + b];
     const float score = a.scores[row0 + b];
     float top = kNegInf;
-    double sum = 0;
+    Pair sum = {0.f, 0.f};
     for (int i0 = 0; i0 < nsl; i0 += 32) {
-      Slice v;
-      v.top = kNegInf;
-      v.sum = 0;
+      Slice v = {kNegInf, {0.f, 0.f}, 0.f};
       if (i0 + lane < nsl) v = sl[i0 + lane];
       const float now = fmaxf(top, warp_max(v.top));
-      if (now != top) sum *= (double)exp2_fast((top - now) * kLog2e);
+      if (now != top) {
+        const float f = exp2_fast((top - now) * kLog2e);
+        sum.h *= f;
+        sum.l *= f;
+      }
       top = now;
-      if (v.top != kNegInf || v.sum != 0.0)
-        sum += v.sum * (double)exp2_fast((v.top - top) * kLog2e);
+      if (v.top != kNegInf || v.sum.h != 0.f) {
+        const float f = exp2_fast((v.top - top) * kLog2e);
+        sum = add(sum, Pair{v.sum.h * f, v.sum.l * f});
+      }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    sum = warp_sum(sum);
     if (lane == 0) {
       row_done[b] = done;
       row_score[b] = score;
       row_top[b] = top;
-      row_log[b] = done ? 0.0 : log(sum);
+      row_log[b] = sum;
     }
+  }
+  cta_sync();
+  for (int b = tid; b < B; b += kRowThreads) {  // a lane per row: a warp's logarithms at once
+    const double l = log((double)row_log[b].h + (double)row_log[b].l);
+    row_log[b] = {(float)l, (float)(l - (double)(float)l)};
   }
   if (tid == 0) sh_count = 0;
   cta_sync();
-  // entry e of the sequence, value v at index i of its row: its score, -inf when
-  // it cannot be taken
-  auto score_of = [&](int e, float v, int32_t i, int32_t& flat) -> double {
+  // entry e of the sequence, value v at index i of its row: the key of its
+  // score, 0 when it cannot be taken
+  auto score_of = [&](int e, float v, int32_t i, int32_t& flat) -> uint64_t {
     const int b = e / per;
-    double sc;
+    Pair sc;
     if (row_done[b]) {
       flat = b * n;
-      sc = e == b * per ? (double)row_score[b] : (double)kNegInf;
+      sc = {e == b * per ? row_score[b] : kNegInf, 0.f};
     } else {
       flat = b * n + i;
-      if (i < 0) return (double)kNegInf;
-      sc = (double)row_score[b] + (((double)v - (double)row_top[b]) - row_log[b]);
+      if (i < 0) return 0;
+      const Pair lg = row_log[b];
+      sc = add(add(Pair{row_score[b], 0.f}, two_sum(v, -row_top[b])), Pair{-lg.h, -lg.l});
     }
-    return sc == sc ? sc : (double)kNegInf;
+    if (!(fabsf(sc.h) < -kNegInf)) return 0;  // NaN too
+    return ((uint64_t)float_key(sc.h) << 32) | float_key(sc.l);
   };
   auto entry = [&](int e, int32_t& flat) { return score_of(e, best_v[e0 + e], best_i[e0 + e], flat); };
-  // scores rounded to 32 bits keep their order, so the k-th largest of the
-  // threads' rounded maxima bounds the k best from below
-  double kept[kKept];
+  auto rounded = [](uint64_t key) { return key ? key_float((uint32_t)(key >> 32)) : kNegInf; };
+  // the k-th largest of the threads' rounded maxima bounds the k best from below
+  uint64_t kept[kKept];
   float mine = kNegInf;
 #pragma unroll
   for (int j = 0; j < kKept; ++j) {
     const int e = tid + j * kRowThreads;
-    kept[j] = e < all ? score_of(e, kept_v[j], kept_i[j], kept_i[j]) : (double)kNegInf;
-    mine = fmaxf(mine, (float)kept[j]);
+    kept[j] = e < all ? score_of(e, kept_v[j], kept_i[j], kept_i[j]) : 0;
+    mine = fmaxf(mine, rounded(kept[j]));
   }
   for (int e = tid + kKept * kRowThreads; e < all; e += kRowThreads) {
     int32_t flat;
-    mine = fmaxf(mine, (float)entry(e, flat));
+    mine = fmaxf(mine, rounded(entry(e, flat)));
   }
   const float bound = kth_of_threads(mine, k, sh_f, &sh_out);
-  auto offer = [&](double sc, int32_t flat) {
-    if (!(sc > (double)kNegInf) || (float)sc < bound) return;
+  auto offer = [&](uint64_t sc, int32_t flat) {
+    if (sc == 0 || rounded(sc) < bound) return;
     const int at = atomicAdd(&sh_count, 1);
     if (at < kBuf) {
       b_score[at] = sc;
@@ -340,29 +368,29 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
   for (int j = 0; j < kKept; ++j) offer(kept[j], kept_i[j]);
   for (int e = tid + kKept * kRowThreads; e < all; e += kRowThreads) {
     int32_t flat;
-    const double sc = entry(e, flat);
+    const uint64_t sc = entry(e, flat);
     offer(sc, flat);
   }
   cta_sync();
   int fill = sh_count;
   if (fill > kBuf) {
     // more equal scores than places: one by one
-    double ls = __longlong_as_double(0x7ff0000000000000ll);
+    uint64_t ls = ~0ull;
     int32_t li = -1;
     for (fill = 0; fill < k; ++fill) {
-      double ts = (double)kNegInf;
+      uint64_t ts = 0;
       int32_t ti = INT32_MAX;
       for (int e = tid; e < all; e += kRowThreads) {
         int32_t flat;
-        const double sc = entry(e, flat);
-        if (sc > (double)kNegInf && ahead(ls, li, sc, flat) && ahead(sc, flat, ts, ti)) {
+        const uint64_t sc = entry(e, flat);
+        if (sc != 0 && ahead(ls, li, sc, flat) && ahead(sc, flat, ts, ti)) {
           ts = sc;
           ti = flat;
         }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
-        const double os = __shfl_xor_sync(0xFFFFFFFFu, ts, o);
+        const uint64_t os = __shfl_xor_sync(0xFFFFFFFFu, ts, o);
         const int32_t oi = __shfl_xor_sync(0xFFFFFFFFu, ti, o);
         if (ahead(os, oi, ts, ti)) {
           ts = os;
@@ -396,7 +424,7 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
   int32_t* token = a.token + (size_t)seq * k;
   float* score = a.out_score + (size_t)seq * k;
   for (int c = tid; c < fill; c += kRowThreads) {
-    const double sc = b_score[c];
+    const uint64_t sc = b_score[c];
     const int32_t flat = b_flat[c];
     int place = 0;
     for (int o = 0; o < fill && place < k; ++o) place += ahead(b_score[o], b_flat[o], sc, flat);
@@ -405,7 +433,7 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
     parent[place] = b;
     token[place] = row_done[b] ? a.eos
                    : a.ids ? a.ids[(size_t)row * n + i] : i;
-    score[place] = (float)sc;
+    score[place] = rounded(sc);
   }
   for (int c = fill + tid; c < k; c += kRowThreads) {
     parent[c] = -1;

@@ -486,7 +486,7 @@ int lmhead_q4_gather_logits(int dtype, const void* codes, const void* scales, co
  *   finished  S*beams bytes or NULL: a beam with a non-zero byte has ended and
  *             offers one entry, token eos with its score unchanged (as j = 0).
  *   out_parent, out_token, out_score  S x k: the beam (0..beams-1), the token
- *             and the score. Entries that score -inf or NaN (a masked logit, a
+ *             and the score. Entries whose score is not finite (a masked logit, a
  *             dead beam, a row with a NaN or +inf) are never taken; places left
  *             over hold -1, -1 and -inf.
  * 1 <= k <= 32, beams <= 256, S * beams <= 65535, n <= 2^30 and beams * n below 2^31.
