@@ -255,7 +255,7 @@ constexpr int kBadSlots = 16;  // more pieces than the TMA warp can be ahead
 
 template <int NS> struct Ctl {
   uint64_t full[NS], empty[NS];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
   uint64_t ex1, ex2, drain;
   uint32_t tmem;
   int abort;
@@ -313,7 +313,8 @@ struct Cursor {
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
                                          long long budget) {
-  return __all_sync(0xFFFFFFFFu, tc::mbar_wait(bar, parity, abort, budget));
+  const bool now = budget > 0 && tc::mbar_try_wait(bar, parity);
+  return __all_sync(0xFFFFFFFFu, now || tc::mbar_wait(bar, parity, abort, budget));
 }
 
 // Bits [lo, hi) of 32, either end anywhere.
@@ -373,6 +374,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     for (int w = 0; w < 2; ++w) {
       tc::mbar_init(&ctl.q_full[w], kRows);
       tc::mbar_init(&ctl.s_full[w], 1);
+      tc::mbar_init(&ctl.p_half[w], kRows);
       tc::mbar_init(&ctl.p_full[w], kRows);
       tc::mbar_init(&ctl.o_full[w], 1);
     }
@@ -430,7 +432,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             record_error(err, kDevErrBadId);
           }
           const int off = key & ((1 << a.page_shift) - 1);
-  #pragma unroll
+#pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const int slot = (int)(n % NS);
             if (n >= (uint32_t)NS) {
@@ -494,7 +496,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             // addresses count 16 bytes and stay below 2^14 of them
             const uint64_t qd = q_desc + (pair ? w : 0) * (kRows * D * 2 / 16);
             const uint64_t kd = k_desc + slot * (Sh::kBuf / 16);
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               constexpr int kHalf = kRows * 128 / 16;
               tc::mma_bf16(tmem + w * 128, qd + (c / 4) * kHalf + (c % 4) * 2,
@@ -521,29 +523,35 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             for (int e = lane; e < kKeys * 8; e += 32) {
               const int r = e >> 3;
               if (r < lo || r >= hi)
-  #pragma unroll
+#pragma unroll
                 for (int h = 0; h < Sh::kHalves; ++h)
                   *reinterpret_cast<uint4*>(v + h * (kKeys * 128) + e * 16) = make_uint4(0, 0, 0, 0);
             }
             tc::fence_async_smem();
             __syncwarp();
           }
+          // the weights come in two halves
           const uint32_t use = w ? np1++ : np0++;
-          if (!wait_all(&ctl.p_full[w], use & 1, abort_flag, budget)) return false;
-          tc::fence_after_sync();
+          const uint64_t vd = v_desc + slot * (Sh::kBuf / 16);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!wait_all(h ? &ctl.p_full[w] : &ctl.p_half[w], use & 1, abort_flag, budget))
+              return false;
+            tc::fence_after_sync();
+            if (lane == 0)
+#pragma unroll
+              for (int c = h * (kKeys / 32); c < (h + 1) * (kKeys / 32); ++c)
+                tc::mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + c * 8,
+                               vd + c * (16 * 128 / 16), idesc_o, k >= 2 || c > 0);
+          }
           if (lane == 0) {
-            const uint64_t vd = v_desc + slot * (Sh::kBuf / 16);
-  #pragma unroll
-            for (int c = 0; c < kKeys / 16; ++c)
-              tc::mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + c * 8, vd + c * (16 * 128 / 16),
-                             idesc_o, k >= 2 || c > 0);
             if (!pair || w == 1) tc::mma_commit(&ctl.empty[slot]);
             if (k + 2 >= steps) tc::mma_commit(&ctl.o_full[w]);
           }
           __syncwarp();
           return true;
         };
-  #pragma unroll 1
+#pragma unroll 1
         for (int k = -2; k < steps && ok; ++k)
           ok = (k < 0 || values(k)) && (k + 2 >= steps || scores(k + 2));
         blocks += nb;
@@ -602,8 +610,12 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const int m = it.kend - it.len;
         if (m < 64) bits &= (1ull << m) - 1;
       }
+      // keys [lo_most, hi_least) are seen by every row of the warp
+      const int hi_least = __reduce_min_sync(0xFFFFFFFFu, hi);
+      const int lo_most = __reduce_max_sync(0xFFFFFFFFu, lo);
       const bool idle = !__any_sync(0xFFFFFFFFu, valid);  // no row of this warp is one
-      float ref = kNegInf, sum = 0.f;
+      float ref = kNegInf;
+      float2 sum = make_float2(0.f, 0.f);
       const int steps = pair ? nb : (nb + 1 - w) / 2;
       for (int j = 0; j < steps; ++j) {
         const int b = cur.b0 + (pair ? j : 2 * j + w);
@@ -612,68 +624,80 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (!ok) break;
         tc::fence_after_sync();
         if (!idle) {
-          float s[kKeys];
+          uint32_t s[kKeys] = {};
+          auto val = [&](int c) { return __uint_as_float(s[c]); };
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             tc::tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
-          tc::tmem_ld_wait();
-          uint32_t see[4];
-          bool whole = true;
+          tc::tmem_ld_wait(s);
+          if (key0 < lo_most || key0 + kKeys > hi_least) {
+            // an edge of the mask in this warp's rows
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int k0 = key0 + 32 * c;
-            see[c] = span_bits(lo - k0, hi - k0);
-            if (a.tree) {
-              const int x = k0 - it.len;
-              if (x > -32 && x < 64) see[c] |= (uint32_t)(x < 0 ? bits << -x : bits >> x);
+            for (int c = 0; c < 4; ++c) {
+              const int k0 = key0 + 32 * c;
+              uint32_t see = span_bits(lo - k0, hi - k0);
+              if (a.tree) {
+                const int x = k0 - it.len;
+                if (x > -32 && x < 64) see |= (uint32_t)(x < 0 ? bits << -x : bits >> x);
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                s[c * 32 + i] = (see >> i) & 1 ? s[c * 32 + i] : __float_as_uint(kNegInf);
             }
-            whole &= see[c] == ~0u;
           }
-          if (!__all_sync(0xFFFFFFFFu, whole)) {
+          float mx[4] = {val(0), val(1), val(2), val(3)};
 #pragma unroll
-            for (int c = 0; c < kKeys; ++c)
-              s[c] = (see[c / 32] >> (c % 32)) & 1 ? s[c] : kNegInf;
-          }
-          float mx[4] = {s[0], s[1], s[2], s[3]};
+          for (int c = 4; c + 8 <= kKeys; c += 8)
 #pragma unroll
-          for (int c = 4; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+            for (int i = 0; i < 4; ++i) mx[i] = tc::max3(mx[i], val(c + i), val(c + 4 + i));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], val(kKeys - 4 + i));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
           const bool grow = top > ref + 8.f || (ref == kNegInf && top > kNegInf);
           if (__any_sync(0xFFFFFFFFu, grow)) {
             const float f = grow ? tc::exp2_approx(ref - top) : 1.f;
             if (grow) {
               ref = top;
-              sum *= f;
+              sum.x *= f;
+              sum.y *= f;
             }
             if (j > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t v[16];
+                tc::tmem_ld16(t_o + c * 16, v);
+                tc::tmem_ld_wait(v);
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t v[32];
-                tc::tmem_ld32(t_o + c * 32, v);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                tc::tmem_st32(t_o + c * 32, v);
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                tc::tmem_st16(t_o + c * 16, v);
               }
             }
           }
           const float neg = ref == kNegInf ? 0.f : -ref;
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          const float2 sl2 = make_float2(sl, sl), neg2 = make_float2(neg, neg);
+          float2 part[2] = {sum, make_float2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float x = tc::exp2_approx(fmaf(s[c * 32 + 2 * i], sl, neg));
-              const float y = tc::exp2_approx(fmaf(s[c * 32 + 2 * i + 1], sl, neg));
-              part[i & 1] += x;
-              part[2 + (i & 1)] += y;
-              pk[i] = pack2<BF16>(x, y);
+              float2 x = tc::fma_x2(make_float2(val(c * 32 + 2 * i), val(c * 32 + 2 * i + 1)), sl2, neg2);
+              x.x = tc::exp2_approx(x.x);
+              x.y = tc::exp2_approx(x.y);
+              part[i & 1] = tc::add_x2(part[i & 1], x);
+              pk[i] = pack2<BF16>(x.x, x.y);
             }
             tc::tmem_st16(t_s + c * 16, pk);
+            if (c == 1) {
+              tc::tmem_st_wait();
+              tc::fence_before_sync();
+              tc::mbar_arrive(&ctl.p_half[w]);
+            }
           }
-          sum += (part[0] + part[1]) + (part[2] + part[3]);
+          sum = tc::add_x2(part[0], part[1]);
           tc::tmem_st_wait();
+        } else {
+          tc::mbar_arrive(&ctl.p_half[w]);
         }
         tc::fence_before_sync();
         tc::mbar_arrive(&ctl.p_full[w]);
@@ -688,6 +712,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       no1 += both;
       if (!ok) break;
       tc::fence_after_sync();
+      const float l_row = sum.x + sum.y;
       const bool bad = *(volatile int*)&ctl.bad[piece % kBadSlots] != 0;
       const float nan = __int_as_float(0x7fc00000);
       // where the row goes: the output, or the piece's place in the scratch
@@ -705,16 +730,16 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       };
       if (!join) {
         if (pair || w == 0) {
-          const float f = finish(ref, sum);
+          const float f = finish(ref, l_row);
           if (!idle) {
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t v[32];
               tc::tmem_ld32(t_o + c * 32, v);
-              tc::tmem_ld_wait();
+              tc::tmem_ld_wait(v);
               float x[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = sum == 0.f && !bad ? 0.f : __uint_as_float(v[i]) * f;
+              for (int i = 0; i < 32; ++i) x[i] = l_row == 0.f && !bad ? 0.f : __uint_as_float(v[i]) * f;
               if (valid) store_cols<BF16>(x, out16, out32, c * 32);
             }
           }
@@ -723,7 +748,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // the warpgroups join: they exchange references and sums in the columns
         // of the scores, and each finishes one half of both outputs' columns
         if (!idle) {
-          tc::tmem_st2(t_s, ref, sum);
+          tc::tmem_st2(t_s, ref, l_row);
           tc::tmem_st_wait();
         }
         tc::fence_before_sync();
@@ -735,7 +760,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           const float2 other = tc::tmem_ld2(tmem + lanes + (1 - w) * 128);
           const float m = fmaxf(ref, other.x), ms = m == kNegInf ? 0.f : m;
           const float f0 = tc::exp2_approx(ref - ms), f1 = tc::exp2_approx(other.x - ms);
-          const float l = sum * f0 + other.y * f1;
+          const float l = l_row * f0 + other.y * f1;
           const float f = finish(m, l);
           const bool none = l == 0.f && !bad;
 #pragma unroll
@@ -744,7 +769,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             const uint32_t at = w * (D / 2) + c * 32;
             tc::tmem_ld32(t_o + at, v);
             tc::tmem_ld32(tmem + lanes + 256 + (1 - w) * 128 + at, u);
-            tc::tmem_ld_wait();
+            tc::tmem_ld_wait(v);
+            tc::tmem_ld_wait(u);
             float x[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i)
