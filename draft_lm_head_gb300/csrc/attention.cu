@@ -363,7 +363,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* q_s = base;
   uint8_t* ring = base + Sh::kQ;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* abort_flag = &ctl.abort;
 
   if (threadIdx.x == 0) {
@@ -395,7 +395,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   tc::fence_before_sync();
   cta_sync();
   tc::fence_after_sync();
-  const uint32_t tmem = ctl.tmem;  // scores and weights at 0 and 128, outputs at 256 and 384
+  // all 512 columns: scores and weights at 0 and 128, outputs at 256 and 384
+  constexpr uint32_t tmem = 0;
   pdl_wait();
   pdl_trigger();
   const int group = a.heads / a.kv_heads, tile_tok = kRows / group;
@@ -474,6 +475,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // the weights that they overwrite (MMAs of one thread run in order).
       const uint32_t idesc_s = tc::idesc_f16_f32(BF16, kRows, kKeys, false);
       const uint32_t idesc_o = tc::idesc_f16_f32(BF16, kRows, D, true);
+      const bool issuer = tc::elect_one();
       const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_addr(q_s));
       const uint64_t k_desc = tc::sw128_kmajor_desc(tc::smem_addr(ring));
       const uint64_t v_desc = tc::sw128_mnmajor_desc(tc::smem_addr(ring), kKeys * 128);
@@ -483,18 +485,20 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const bool pair = cur.it.ntile == 2;
         const int nb = cur.b1 - cur.b0, steps = pair ? 2 * nb : nb;
         auto scores = [&](int k) -> bool {
-          const int w = k & 1, j = pair ? k >> 1 : k;
+          const int j = pair ? k >> 1 : k;
           const uint32_t n = 2 * (blocks + j);
-          const int slot = (int)(n % NS);
+          const int what =
+              __shfl_sync(0xFFFFFFFFu, (int)(n % NS) | (k & 1) << 8 | (pair ? k & 1 : 0) << 9, 0);
+          const int slot = what & 255, w = (what >> 8) & 1, tile = what >> 9;
           if (k == 0 || (pair && k == 1)) {
             const uint32_t use = k ? nq1++ : nq0++;
             if (!wait_all(&ctl.q_full[k], use & 1, abort_flag, budget)) return false;
           }
           if (!wait_all(&ctl.full[slot], (n / NS) & 1, abort_flag, budget)) return false;
           tc::fence_after_sync();
-          if (lane == 0) {
+          if (issuer) {
             // addresses count 16 bytes and stay below 2^14 of them
-            const uint64_t qd = q_desc + (pair ? w : 0) * (kRows * D * 2 / 16);
+            const uint64_t qd = q_desc + tile * (kRows * D * 2 / 16);
             const uint64_t kd = k_desc + slot * (Sh::kBuf / 16);
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
@@ -509,9 +513,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           return true;
         };
         auto values = [&](int k) -> bool {
-          const int w = k & 1, j = pair ? k >> 1 : k;
+          const int j = pair ? k >> 1 : k;
           const uint32_t n = 2 * (blocks + j) + 1;
-          const int slot = (int)(n % NS);
+          const int what =
+              __shfl_sync(0xFFFFFFFFu, (int)(n % NS) | (k & 1) << 8 | (k >= 2) << 9, 0);
+          const int slot = what & 255, w = (what >> 8) & 1, more = what >> 9;
           if (!wait_all(&ctl.full[slot], (n / NS) & 1, abort_flag, budget)) return false;
           // keys that are no token's, or whose page was not loaded, hold anything
           // at all, and weight 0 times NaN is NaN: they are zeroed
@@ -538,13 +544,13 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             if (!wait_all(h ? &ctl.p_full[w] : &ctl.p_half[w], use & 1, abort_flag, budget))
               return false;
             tc::fence_after_sync();
-            if (lane == 0)
+            if (issuer)
 #pragma unroll
               for (int c = h * (kKeys / 32); c < (h + 1) * (kKeys / 32); ++c)
                 tc::mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + c * 8,
-                               vd + c * (16 * 128 / 16), idesc_o, k >= 2 || c > 0);
+                               vd + c * (16 * 128 / 16), idesc_o, c > 0 ? 1u : (uint32_t)more);
           }
-          if (lane == 0) {
+          if (issuer) {
             if (!pair || w == 1) tc::mma_commit(&ctl.empty[slot]);
             if (k + 2 >= steps) tc::mma_commit(&ctl.o_full[w]);
           }
@@ -556,7 +562,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           ok = (k < 0 || values(k)) && (k + 2 >= steps || scores(k + 2));
         blocks += nb;
       }
-      if (!ok && lane == 0) {
+      if (!ok && issuer) {
         *abort_flag = 1;
         record_error(err, kDevErrTimeout);
         tc::mma_drain(&ctl.drain);  // TMEM is freed below
