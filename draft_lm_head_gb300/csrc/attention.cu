@@ -481,85 +481,94 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       const uint64_t v_desc = tc::sw128_mnmajor_desc(tc::smem_addr(ring), kKeys * 128);
       uint32_t blocks = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;
       bool ok = true;
-      while (ok && cur.next()) {
-        const bool pair = cur.it.ntile == 2;
-        const int nb = cur.b1 - cur.b0, steps = pair ? 2 * nb : nb;
-        auto scores = [&](int k) -> bool {
-          const int j = pair ? k >> 1 : k;
-          const uint32_t n = 2 * (blocks + j);
-          const int what =
-              __shfl_sync(0xFFFFFFFFu, (int)(n % NS) | (k & 1) << 8 | (pair ? k & 1 : 0) << 9, 0);
-          const int slot = what & 255, w = (what >> 8) & 1, tile = what >> 9;
-          if (k == 0 || (pair && k == 1)) {
-            const uint32_t use = k ? nq1++ : nq0++;
-            if (!wait_all(&ctl.q_full[k], use & 1, abort_flag, budget)) return false;
+      while (ok) {
+        // what branches and operands depend on comes by shuffle from lane 0, so
+        // that the compiler knows it to be the warp's own
+        const int found = cur.next() ? (cur.b1 - cur.b0) << 2 | (cur.it.ntile == 2) << 1 | 1 : 0;
+        const int info = __shfl_sync(0xFFFFFFFFu, found, 0);
+        if (info == 0) break;
+        const bool pair = info & 2;
+        const int nb = info >> 2, steps = pair ? 2 * nb : nb;
+#pragma unroll 1
+        for (int k = -2; k < steps && ok; ++k) {
+          // values of step k, then scores of step k + 2; everything but the
+          // weights is waited for first
+          const bool has_v = k >= 0, has_s = k + 2 < steps;
+          const int jv = pair ? k >> 1 : k, js = pair ? (k + 2) >> 1 : k + 2;
+          const uint32_t nv = 2 * (blocks + jv) + 1, nk = 2 * (blocks + js);
+          const int v_slot = (int)(nv % NS), k_slot = (int)(nk % NS), w = k & 1;
+          const int tile = pair ? w : 0;
+          // a pair's second step uses the block of its first
+          const bool opens = !pair || w == 0, closes = !pair || w == 1;
+          if (has_v && opens) {
+            ok = wait_all(&ctl.full[v_slot], (nv / NS) & 1, abort_flag, budget);
+            if (!ok) break;
+            // keys that are no token's, or whose page was not loaded, hold anything
+            // at all, and weight 0 times NaN is NaN: they are zeroed
+            const int first = (cur.it.kb0 + cur.b0 + jv) * kKeys;
+            const int lo = max(0, min(kKeys, cur.it.kbeg - first));
+            const int hi = min(kKeys, cur.it.kend - first);
+            if (lo > 0 || hi < kKeys) {
+              uint8_t* v = ring + v_slot * Sh::kBuf;
+              for (int e = lane; e < kKeys * 8; e += 32) {
+                const int r = e >> 3;
+                if (r < lo || r >= hi)
+#pragma unroll
+                  for (int h = 0; h < Sh::kHalves; ++h)
+                    *reinterpret_cast<uint4*>(v + h * (kKeys * 128) + e * 16) =
+                        make_uint4(0, 0, 0, 0);
+              }
+              tc::fence_async_smem();
+              __syncwarp();
+            }
           }
-          if (!wait_all(&ctl.full[slot], (n / NS) & 1, abort_flag, budget)) return false;
-          tc::fence_after_sync();
-          if (issuer) {
+          if (has_s) {
+            if (k + 2 == 0 || (pair && k + 2 == 1)) {
+              const uint32_t use = w ? nq1++ : nq0++;
+              ok = wait_all(&ctl.q_full[w], use & 1, abort_flag, budget);
+            }
+            if (!ok) break;
+          }
+          if (has_v) {  // the weights come in two halves
+            const uint32_t use = w ? np1++ : np0++;
+            const uint64_t vd = v_desc + v_slot * (Sh::kBuf / 16);
+            ok = wait_all(&ctl.p_half[w], use & 1, abort_flag, budget);
+            if (!ok) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < kKeys / 32; ++c)
+              tc::mma_ts_one(issuer, tmem + 256 + w * 128, tmem + w * 128 + c * 8,
+                             vd + c * (16 * 128 / 16), idesc_o, c > 0 ? 1u : (uint32_t)(k >= 2));
+            ok = wait_all(&ctl.p_full[w], use & 1, abort_flag, budget);
+            if (!ok) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int c = kKeys / 32; c < kKeys / 16; ++c)
+              tc::mma_ts_one(issuer, tmem + 256 + w * 128, tmem + w * 128 + c * 8,
+                             vd + c * (16 * 128 / 16), idesc_o, 1u);
+            if (closes) tc::commit_one(issuer, &ctl.empty[v_slot]);
+            if (!has_s) tc::commit_one(issuer, &ctl.o_full[w]);
+          }
+          if (has_s) {
+            if (opens) {
+              ok = wait_all(&ctl.full[k_slot], (nk / NS) & 1, abort_flag, budget);
+              if (!ok) break;
+            }
+            tc::fence_after_sync();
             // addresses count 16 bytes and stay below 2^14 of them
             const uint64_t qd = q_desc + tile * (kRows * D * 2 / 16);
-            const uint64_t kd = k_desc + slot * (Sh::kBuf / 16);
+            const uint64_t kd = k_desc + k_slot * (Sh::kBuf / 16);
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               constexpr int kHalf = kRows * 128 / 16;
-              tc::mma_bf16(tmem + w * 128, qd + (c / 4) * kHalf + (c % 4) * 2,
-                           kd + (c / 4) * kHalf + (c % 4) * 2, idesc_s, c > 0);
+              tc::mma_ss_one(issuer, tmem + w * 128, qd + (c / 4) * kHalf + (c % 4) * 2,
+                             kd + (c / 4) * kHalf + (c % 4) * 2, idesc_s, c > 0);
             }
-            tc::mma_commit(&ctl.s_full[w]);
-            if (!pair || w == 1) tc::mma_commit(&ctl.empty[slot]);
+            tc::commit_one(issuer, &ctl.s_full[w]);
+            if (closes) tc::commit_one(issuer, &ctl.empty[k_slot]);
           }
           __syncwarp();
-          return true;
-        };
-        auto values = [&](int k) -> bool {
-          const int j = pair ? k >> 1 : k;
-          const uint32_t n = 2 * (blocks + j) + 1;
-          const int what =
-              __shfl_sync(0xFFFFFFFFu, (int)(n % NS) | (k & 1) << 8 | (k >= 2) << 9, 0);
-          const int slot = what & 255, w = (what >> 8) & 1, more = what >> 9;
-          if (!wait_all(&ctl.full[slot], (n / NS) & 1, abort_flag, budget)) return false;
-          // keys that are no token's, or whose page was not loaded, hold anything
-          // at all, and weight 0 times NaN is NaN: they are zeroed
-          const int first = (cur.it.kb0 + cur.b0 + j) * kKeys;
-          const int lo = max(0, min(kKeys, cur.it.kbeg - first));
-          const int hi = min(kKeys, cur.it.kend - first);
-          if ((lo > 0 || hi < kKeys) && (!pair || w == 0)) {
-            uint8_t* v = ring + slot * Sh::kBuf;
-            for (int e = lane; e < kKeys * 8; e += 32) {
-              const int r = e >> 3;
-              if (r < lo || r >= hi)
-#pragma unroll
-                for (int h = 0; h < Sh::kHalves; ++h)
-                  *reinterpret_cast<uint4*>(v + h * (kKeys * 128) + e * 16) = make_uint4(0, 0, 0, 0);
-            }
-            tc::fence_async_smem();
-            __syncwarp();
-          }
-          // the weights come in two halves
-          const uint32_t use = w ? np1++ : np0++;
-          const uint64_t vd = v_desc + slot * (Sh::kBuf / 16);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!wait_all(h ? &ctl.p_full[w] : &ctl.p_half[w], use & 1, abort_flag, budget))
-              return false;
-            tc::fence_after_sync();
-            if (issuer)
-#pragma unroll
-              for (int c = h * (kKeys / 32); c < (h + 1) * (kKeys / 32); ++c)
-                tc::mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + c * 8,
-                               vd + c * (16 * 128 / 16), idesc_o, c > 0 ? 1u : (uint32_t)more);
-          }
-          if (issuer) {
-            if (!pair || w == 1) tc::mma_commit(&ctl.empty[slot]);
-            if (k + 2 >= steps) tc::mma_commit(&ctl.o_full[w]);
-          }
-          __syncwarp();
-          return true;
-        };
-#pragma unroll 1
-        for (int k = -2; k < steps && ok; ++k)
-          ok = (k < 0 || values(k)) && (k + 2 >= steps || scores(k + 2));
+        }
         blocks += nb;
       }
       if (!ok && issuer) {

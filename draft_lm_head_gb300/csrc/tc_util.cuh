@@ -240,17 +240,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs, fp32 accumulate.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -322,16 +311,46 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(bool bf16, uint32_t m, uint
          ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// One lane of a converged warp, always the same. MMAs issued under this in code
-// whose warp index and operands the compiler can see to be the warp's own (a
-// shuffle from lane 0 shows it) go out one in 64 cycles at M = N = 128, K = 16;
-// issued by `lane == 0` with operands from a thread's registers, one in 130.
+// One lane of a converged warp, always the same.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
       "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(p));
   return p != 0;
+}
+
+// The MMAs and commits of a whole converged warp of which one lane (`one`, from
+// elect_one) acts. With a predicate in place of a branch around them, and
+// operands that the compiler can see to be the warp's own (from constants, or
+// shuffled from lane 0), their descriptors are formed in uniform registers and
+// they go out one in 64 cycles at M = N = 128, K = 16; under `lane == 0`, each
+// moving its operands there first, one in 130.
+__device__ __forceinline__ void mma_ss_one(bool one, uint32_t d_tmem, uint64_t a_desc,
+                                           uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"((int)one)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_one(bool one, uint32_t d_tmem, uint32_t a_tmem,
+                                           uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"((int)one)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(bool one, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar)),
+      "r"((int)one)
+      : "memory");
 }
 
 // Order this thread's shared-memory stores before later reads of the async
