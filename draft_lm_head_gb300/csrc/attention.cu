@@ -26,11 +26,11 @@
 // Bound: few rows, by reading K and V once; many rows, by the tensor cores.
 //
 // The softmax runs in the base-2 domain with a running reference instead of
-// the running maximum: while no row's maximum has passed its reference by more
-// than 2^8, accumulators keep it and need no rescaling (weights up to 256 are
-// as exact in fp16 and bf16 as weights up to 1). Scores, sums, references and
-// accumulators are fp32; the weights are rounded once, to 16 bits, as the
-// tensor cores take them.
+// the running maximum: a row's first block with a key sets it, and it moves only
+// when weights pass 2^9 or so, which their sum shows; a block's maximum is not
+// even looked for before (it cost a fifth of a block's time). Scores, sums,
+// references and accumulators are fp32; the weights are rounded once, to 16
+// bits, as the tensor cores take them.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -255,7 +255,7 @@ constexpr int kBadSlots = 16;  // more pieces than the TMA warp can be ahead
 
 template <int NS> struct Ctl {
   uint64_t full[NS], empty[NS];
-  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2], p_half[2], h_done[2], p_full[2], o_full[2];
   uint64_t ex1, ex2, drain;
   uint32_t tmem;
   int abort;
@@ -375,6 +375,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       tc::mbar_init(&ctl.q_full[w], kRows);
       tc::mbar_init(&ctl.s_full[w], 1);
       tc::mbar_init(&ctl.p_half[w], kRows);
+      tc::mbar_init(&ctl.h_done[w], 1);
       tc::mbar_init(&ctl.p_full[w], kRows);
       tc::mbar_init(&ctl.o_full[w], 1);
     }
@@ -539,6 +540,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             for (int c = 0; c < kKeys / 32; ++c)
               tc::mma_ts_one(issuer, tmem + 256 + w * 128, tmem + w * 128 + c * 8,
                              vd + c * (16 * 128 / 16), idesc_o, c > 0 ? 1u : (uint32_t)(k >= 2));
+            tc::commit_one(issuer, &ctl.h_done[w]);
             ok = wait_all(&ctl.p_full[w], use & 1, abort_flag, budget);
             if (!ok) break;
             tc::fence_after_sync();
@@ -660,23 +662,38 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 s[c * 32 + i] = (see >> i) & 1 ? s[c * 32 + i] : __float_as_uint(kNegInf);
             }
           }
-          float mx[4] = {val(0), val(1), val(2), val(3)};
+          const float2 sl2 = make_float2(sl, sl);
+          uint32_t pk[32];
+          // The weights of one half of the keys, into pk; returns their sum.
+          auto half = [&](int h) {
+            const float neg = ref == kNegInf ? 0.f : -ref;
+            const float2 neg2 = make_float2(neg, neg);
+            float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 4; c + 8 <= kKeys; c += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = tc::max3(mx[i], val(c + i), val(c + 4 + i));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], val(kKeys - 4 + i));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
-          const bool grow = top > ref + 8.f || (ref == kNegInf && top > kNegInf);
-          if (__any_sync(0xFFFFFFFFu, grow)) {
-            const float f = grow ? tc::exp2_approx(ref - top) : 1.f;
-            if (grow) {
-              ref = top;
-              sum.x *= f;
-              sum.y *= f;
+            for (int i = 0; i < 32; ++i) {
+              const int c = h * 64 + 2 * i;
+              float2 x = tc::fma_x2(make_float2(val(c), val(c + 1)), sl2, neg2);
+              x.x = tc::exp2_approx(x.x);
+              x.y = tc::exp2_approx(x.y);
+              part[i & 1] = tc::add_x2(part[i & 1], x);
+              pk[i] = pack2<BF16>(x.x, x.y);
             }
-            if (j > 0) {
+            return tc::add_x2(part[0], part[1]);
+          };
+          // The block's maximum becomes the reference of the rows that it passes
+          // by more than 2^8; what they have summed up is scaled to it.
+          auto set_reference = [&](bool live) {
+            float mx[4] = {val(0), val(1), val(2), val(3)};
+#pragma unroll
+            for (int c = 4; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], val(c));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+            const bool grow = top > ref + 8.f || (ref == kNegInf && top > kNegInf);
+            if (!__any_sync(0xFFFFFFFFu, grow)) return;
+            const float f = grow ? tc::exp2_approx(ref - top) : 1.f;
+            if (grow) ref = top;
+            sum.x *= f;
+            sum.y *= f;
+            if (live) {
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t v[16];
@@ -687,29 +704,38 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 tc::tmem_st16(t_o + c * 16, v);
               }
             }
+          };
+          // A row's sum over half a block tells when weights have become large,
+          // so that the maximum is looked for only then, and while a row has
+          // no reference. Weights up to 2^15 are as exact as weights up to 1.
+          auto large = [&](float2 p) {
+            return __any_sync(0xFFFFFFFFu, !(p.x + p.y <= 32768.f));
+          };
+          bool sure = __any_sync(0xFFFFFFFFu, ref == kNegInf);
+          if (sure) set_reference(j > 0);
+          float2 p = half(0);
+          if (!sure && large(p)) {
+            sure = true;
+            set_reference(j > 0);
+            p = half(0);
           }
-          const float neg = ref == kNegInf ? 0.f : -ref;
-          const float2 sl2 = make_float2(sl, sl), neg2 = make_float2(neg, neg);
-          float2 part[2] = {sum, make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float2 x = tc::fma_x2(make_float2(val(c * 32 + 2 * i), val(c * 32 + 2 * i + 1)), sl2, neg2);
-              x.x = tc::exp2_approx(x.x);
-              x.y = tc::exp2_approx(x.y);
-              part[i & 1] = tc::add_x2(part[i & 1], x);
-              pk[i] = pack2<BF16>(x.x, x.y);
-            }
-            tc::tmem_st16(t_s + c * 16, pk);
-            if (c == 1) {
-              tc::tmem_st_wait();
-              tc::fence_before_sync();
-              tc::mbar_arrive(&ctl.p_half[w]);
-            }
+          tc::tmem_st32(t_s, pk);
+          tc::tmem_st_wait();
+          tc::fence_before_sync();
+          tc::mbar_arrive(&ctl.p_half[w]);
+          sum = tc::add_x2(sum, p);
+          p = half(1);
+          if (!sure && large(p)) {
+            // the first half is with the MMAs: its values are summed up before
+            // the accumulators are scaled
+            ok = wait_all(&ctl.h_done[w], (ns - 1) & 1, abort_flag, budget);
+            if (!ok) break;
+            tc::fence_after_sync();
+            set_reference(true);
+            p = half(1);
           }
-          sum = tc::add_x2(part[0], part[1]);
+          tc::tmem_st32(t_s + 32, pk);
+          sum = tc::add_x2(sum, p);
           tc::tmem_st_wait();
         } else {
           tc::mbar_arrive(&ctl.p_half[w]);
