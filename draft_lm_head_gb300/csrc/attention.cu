@@ -10,7 +10,7 @@
 // the G = heads / kv_heads query heads that share it) are packed into tiles of
 // 128, so that a decoding step of G heads reads its K and V once, and a block
 // of 128 keys is one 128 x 128 product of scores and one 128 x dim product of
-// values. Three launches:
+// values. Two launches:
 //   prepare   writes the chunk's K and V to the cache, and (one CTA) cuts the
 //             work into items (a request's one or two row tiles x a K/V head)
 //             and shares their key blocks out evenly over the CTAs, wherever
@@ -22,7 +22,9 @@
 //             own and both use every block; with one tile they take blocks in
 //             turn and join at the end, so the tensor cores work on one while
 //             the other is exponentiated;
-//   combine   joins the pieces of items that were cut between CTAs.
+//             Of an item that was cut between CTAs each leaves its piece in the
+//             scratch, and the warp that brings the last one of its rows joins
+//             them, in the order of the pieces.
 // Bound: few rows, by reading K and V once; many rows, by the tensor cores.
 //
 // The softmax runs in the base-2 domain with a running reference instead of
@@ -75,18 +77,18 @@ __device__ __forceinline__ int block_at(int x, int nblk, int ntile) {
 struct Scratch {
   Header* head;
   int4* start;    // per CTA: item, K/V head, units of the item before its range
-  int4* flag;     // per CTA, [0] piece of an item begun earlier, [1] of one that
-                  // goes on later: state (0 none, 1, 2 the item's last), item, head
-  float2* ml;     // per CTA and piece, 256 rows: reference (base 2) and sum
+  float2* ml;     // per CTA and piece (place 2 c: of an item begun earlier, 2 c + 1: of
+                  // one that goes on later), 256 rows: reference (base 2) and sum
   float* o;       // per CTA and piece, 256 rows x dim, not normalised
   Item* items;
+  int* done;      // per item, K/V head and warp's rows (below): blocks done
 };
 
 struct ScratchSize {
-  size_t start, flag, ml, o, items, total;
+  size_t start, ml, o, items, done, total;
 };
 
-__host__ inline ScratchSize scratch_size(int parts, int64_t items, int dim) {
+__host__ inline ScratchSize scratch_size(int parts, int64_t items, int kv_heads, int dim) {
   ScratchSize z;
   size_t at = 256;
   auto take = [&](size_t bytes) {
@@ -95,10 +97,10 @@ __host__ inline ScratchSize scratch_size(int parts, int64_t items, int dim) {
     return was;
   };
   z.start = take((size_t)parts * sizeof(int4));
-  z.flag = take((size_t)parts * 2 * sizeof(int4));
   z.ml = take((size_t)parts * 2 * 256 * sizeof(float2));
   z.o = take((size_t)parts * 2 * 256 * dim * sizeof(float));
   z.items = take((size_t)items * sizeof(Item));
+  z.done = take((size_t)items * kv_heads * 8 * sizeof(int));
   z.total = at;
   return z;
 }
@@ -208,21 +210,25 @@ __device__ void make_plan(const AttnArgs& a, const Scratch& sc, int most_parts) 
   }
 }
 
-// CTA 0 plans; the others copy K and V of the new tokens to their slots, 16
-// bytes a thread.
+// CTA 0 plans; the others clear the counts of finished blocks and copy K and V of
+// the new tokens to their slots, 16 bytes a thread.
 __global__ void __launch_bounds__(kPrepThreads)
-prepare_kernel(AttnArgs a, Scratch sc, int most_parts, int pieces, int* err) {
+prepare_kernel(AttnArgs a, Scratch sc, int most_parts, int64_t counts, int pieces, int* err) {
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0) {
     make_plan(a, sc, most_parts);
     return;
   }
+  const int64_t first = (int64_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x;
+  const int64_t stride = (int64_t)(gridDim.x - 1) * blockDim.x;
+  for (int64_t e = first * 4; e < counts; e += stride * 4)  // a multiple of 8 of them
+    *reinterpret_cast<int4*>(sc.done + e) = make_int4(0, 0, 0, 0);
+  if (!a.k) return;
   const int per = a.kv_heads * pieces;
   const int64_t all = (int64_t)a.T * per;
   const int64_t num_slots = a.pages << a.page_shift;
-  for (int64_t e = (int64_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x; e < all;
-       e += (int64_t)(gridDim.x - 1) * blockDim.x) {
+  for (int64_t e = first; e < all; e += stride) {
     const int t = (int)(e / per), x = (int)(e - (int64_t)t * per);
     const int hd = x / pieces, c = (x - hd * pieces) * 16;
     const int32_t slot = a.slots[t];
@@ -292,7 +298,7 @@ struct Cursor {
       const int4 x = src[0], y = src[1], z = src[2];
       it.s = x.x; it.tok0 = x.y; it.ntok = x.z; it.len = x.w;
       it.i0 = y.x; it.kb0 = y.y; it.nblk = y.z; it.ntile = y.w;
-      it.kend = z.x; it.kbeg = z.y;
+      it.kend = z.x; it.kbeg = z.y; it.prefix = z.z;
       const int w = item_units(it.nblk, it.ntile);
       const int end = (int)min((long long)w, off + left);
       b0 = block_at(off, it.nblk, it.ntile);
@@ -347,6 +353,104 @@ __device__ __forceinline__ void store_cols(const float (&v)[32], char* out16, fl
     for (int i = 0; i < 8; ++i)
       *reinterpret_cast<float4*>(out32 + c + 4 * i) =
           make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+}
+
+// Joins the pieces of 32 rows (of row tile `tile`, quarter `quarter`) in COLS
+// columns from col on, by one warp:
+//   o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
+// Lane r holds row r's references and sums; the lanes share the elements.
+template <bool BF16, int D, int COLS>
+__device__ void join_rows(const AttnArgs& a, const Scratch& sc, const Item& it, int hk, int tile,
+                          int quarter, int col, int64_t out_row, bool valid) {
+  constexpr int N4 = COLS / 4, EL = COLS / 4;  // float4 of a row; of a lane at 32 rows
+  const int lane = threadIdx.x & 31;
+  const long long units = sc.head->units;
+  const int parts = sc.head->parts, w = item_units(it.nblk, it.ntile);
+  const long long ub = (long long)hk * sc.head->per_head + it.prefix;
+  const int c0 = (int)(((ub + 1) * parts + units - 1) / units) - 1;  // its first CTA
+  // the piece of CTA c: its place, -1 if it has none, -2 past the item's last
+  auto place_of = [&](int c) -> int {
+    const long long lo = units * c / parts, hi = units * (c + 1) / parts;
+    if (c >= parts || lo >= ub + w) return -2;
+    const int b0 = block_at((int)max(lo - ub, 0ll), it.nblk, it.ntile);
+    const int b1 = block_at((int)min(hi - ub, (long long)w), it.nblk, it.ntile);
+    return b1 > b0 ? 2 * c + (b0 == 0 ? 1 : 0) : -1;
+  };
+  const int row = tile * kRows + quarter * 32 + lane;
+  const int rows = __popc(__ballot_sync(0xFFFFFFFFu, valid)), elems = rows * N4;
+  // kAtOnce pieces at a time, all of their loads under way together; the sums
+  // move to a larger reference as it comes
+  constexpr int kAtOnce = 8;
+  float ref = kNegInf, l = 0.f;
+  float4 acc[EL];
+#pragma unroll
+  for (int i = 0; i < EL; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0;; c += 32) {
+    const int place = place_of(c + lane);
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, place == -2);
+    const int count = past ? __ffs(past) - 1 : 32;
+    for (int p0 = 0; p0 < count; p0 += kAtOnce) {
+      float2 ml[kAtOnce];
+      const float* from[kAtOnce];
+      float top = ref;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int p = __shfl_sync(0xFFFFFFFFu, place, (p0 + k) & 31);
+        const bool some = p0 + k < count && p >= 0;
+        ml[k] = some && valid ? __ldcg(sc.ml + (int64_t)p * 256 + row) : make_float2(kNegInf, 0.f);
+        from[k] = some ? sc.o + ((int64_t)p * 256 + tile * kRows + quarter * 32) * D + col : nullptr;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
+      const float zero = top == kNegInf ? 0.f : top;
+      const float old = tc::exp2_approx(ref - zero);
+      l *= old;
+      float f[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        f[k] = tc::exp2_approx(ml[k].x - zero);
+        l = fmaf(f[k], ml[k].y, l);
+      }
+      ref = top;
+#pragma unroll
+      for (int i = 0; i < EL; ++i) {
+        if (i * 32 >= elems) break;
+        const int e = i * 32 + lane, r = e / N4;
+        float4 v[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+          v[k] = from[k] && e < elems
+                     ? __ldcg(reinterpret_cast<const float4*>(from[k] + (int64_t)r * D) + e % N4)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float fo = __shfl_sync(0xFFFFFFFFu, old, r & 31);
+        acc[i].x *= fo;
+        acc[i].y *= fo;
+        acc[i].z *= fo;
+        acc[i].w *= fo;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const float fr = __shfl_sync(0xFFFFFFFFu, f[k], r & 31);
+          acc[i].x = fmaf(fr, v[k].x, acc[i].x);
+          acc[i].y = fmaf(fr, v[k].y, acc[i].y);
+          acc[i].z = fmaf(fr, v[k].z, acc[i].z);
+          acc[i].w = fmaf(fr, v[k].w, acc[i].w);
+        }
+      }
+    }
+    if (past) break;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (a.lse && valid && col == 0) a.lse[out_row] = l == 0.f ? kNegInf : ref * kLn2 + logf(l);
+#pragma unroll
+  for (int i = 0; i < EL; ++i) {
+    if (i * 32 >= elems) break;
+    const int e = i * 32 + lane, r = e / N4;
+    const float s = __shfl_sync(0xFFFFFFFFu, inv, r & 31);
+    const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, r & 31);
+    if (e < elems)
+      *reinterpret_cast<uint2*>(static_cast<char*>(a.out) + (to * D + col) * 2 + e % N4 * 8) =
+          make_uint2(pack2<BF16>(acc[i].x * s, acc[i].y * s), pack2<BF16>(acc[i].z * s, acc[i].w * s));
   }
 }
 
@@ -592,10 +696,43 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int row_head = r - r / group * group;
     uint32_t ns = 0, no0 = 0, no1 = 0, nx = 0;
     int piece = 0;
-    int4 flag0 = make_int4(0, 0, 0, 0), flag1 = make_int4(0, 0, 0, 0);
     bool ok = true;
-    for (; ok && cur.next(); ++piece) {
-      const Item& it = cur.it;
+    // Rows of the piece at the cursor into the tile of this warpgroup, if it has
+    // one there: 16 bytes a lane, row by row; rows that are none are zeroed.
+    auto load_q = [&]() {
+      if (cur.it.ntile == 1 && w == 1) return;
+      const int t = cur.it.ntile == 2 ? w : 0, quarter = warp & 3;
+      const uint32_t dst = tc::smem_addr(q_s) + t * (kRows * D * 2);
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const int e = i * 32 + lane, row = quarter * 32 + e / (D / 8), c = e % (D / 8);
+        const int rt = row / group, tk = t * tile_tok + rt;
+        const bool in = rt < tile_tok && tk < cur.it.ntok;
+        const char* src = static_cast<const char*>(a.q) + c * 16;
+        if (in)
+          src += (int64_t)(cur.it.tok0 + tk) * a.q_tok +
+                 (int64_t)(cur.p_hk * group + row - rt * group) * a.q_head;
+        const int size = in ? 16 : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         dst + (c / 8) * (kRows * 128) + row * 128 + (((c % 8) ^ (row & 7)) << 4)),
+                     "l"(src), "r"(size)
+                     : "memory");
+      }
+    };
+    auto q_loaded = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (cur.it.ntile == 1 && w == 1) return;
+      tc::fence_async_smem();
+      tc::mbar_arrive(&ctl.q_full[cur.it.ntile == 2 ? w : 0]);
+    };
+    bool have = cur.next();
+    if (have) {
+      load_q();
+      q_loaded();
+    }
+    for (; ok && have; ++piece) {
+      const Item it = cur.it;
+      const int p_hk = cur.p_hk, p_idx = cur.p_idx, b_first = cur.b0;
       const bool pair = it.ntile == 2;
       const int nb = cur.b1 - cur.b0;
       const int tile = pair ? w : 0;
@@ -603,21 +740,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       const int tok = tile * tile_tok + row_tok;
       const bool valid = r < tile_tok * group && tok < it.ntok;
       const int tokc = min(tok, it.ntok - 1);
-      const int head = cur.p_hk * group + row_head;
+      const int head = p_hk * group + row_head;
       const int64_t out_row = (int64_t)(it.tok0 + tok) * a.heads + head;
-      if (pair || w == 0) {
-        const char* q = static_cast<const char*>(a.q) + (int64_t)(it.tok0 + tok) * a.q_tok +
-                        head * a.q_head;
-        uint8_t* dst = q_s + tile * (kRows * D * 2) + r * 128;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (valid) v = *reinterpret_cast<const uint4*>(q + c * 16);
-          *reinterpret_cast<uint4*>(dst + (c / 8) * (kRows * 128) + (((c % 8) ^ (r & 7)) << 4)) = v;
-        }
-        tc::fence_async_smem();
-        tc::mbar_arrive(&ctl.q_full[tile]);
-      }
       // the row's keys: [lo, hi), and the new tokens of its tree word
       const int hi = a.tree ? it.len : it.len + it.i0 + tokc + 1;
       const int lo = a.window > 0 ? max(0, hi - a.window) : 0;
@@ -635,7 +759,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       float2 sum = make_float2(0.f, 0.f);
       const int steps = pair ? nb : (nb + 1 - w) / 2;
       for (int j = 0; j < steps; ++j) {
-        const int b = cur.b0 + (pair ? j : 2 * j + w);
+        const int b = b_first + (pair ? j : 2 * j + w);
         const int key0 = (it.kb0 + b) * kKeys;
         ok = wait_all(&ctl.s_full[w], ns++ & 1, abort_flag, budget);
         if (!ok) break;
@@ -753,6 +877,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       no1 += both;
       if (!ok) break;
       tc::fence_after_sync();
+      // every product of this piece with Q is done: the next piece's rows are on
+      // their way while this one's are written
+      have = cur.next();
+      if (have) load_q();
       const float l_row = sum.x + sum.y;
       const bool bad = *(volatile int*)&ctl.bad[piece % kBadSlots] != 0;
       const float nan = __int_as_float(0x7fc00000);
@@ -824,18 +952,32 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         ok = wait_all(&ctl.ex2, nx++ & 1, abort_flag, budget);
         if (!ok) break;
       }
+      if (!(first && last) && !idle && (pair || join || w == 0)) {
+        // a piece of an item: its blocks are counted for each warp's rows, of a
+        // tile, or of a half of the columns where a single tile's are divided
+        constexpr int kCols = D < 64 * 2 ? D / 2 : 64;
+        const int only = pair || join ? w : -1;
+        for (int h = only < 0 ? 0 : only; h < (only < 0 ? 2 : only + 1); ++h) {
+          __threadfence();
+          __syncwarp();
+          int before = 0;
+          if (lane == 0)
+            before = atomicAdd(sc.done + ((int64_t)p_idx * a.kv_heads + p_hk) * 8 + h * 4 + (warp & 3), nb);
+          before = __shfl_sync(0xFFFFFFFFu, before, 0);
+          if (before + nb != it.nblk) continue;
+          __threadfence();
+          const int from = pair ? 0 : h * (D / 2), to = pair ? D : from + D / 2;
+          for (int c = from; c < to; c += kCols)
+            join_rows<BF16, D, kCols>(a, sc, it, p_hk, tile, warp & 3, c, out_row, valid);
+        }
+      }
+      if (have) q_loaded();
       // the next piece's first values overwrite what was read here
       tc::fence_before_sync();
-      if (!first) flag0 = make_int4(last ? 2 : 1, cur.p_idx, cur.p_hk, 0);
-      else if (!last) flag1 = make_int4(1, cur.p_idx, cur.p_hk, 0);
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
       record_error(err, kDevErrTimeout);
-    }
-    if (threadIdx.x == 0) {
-      sc.flag[blockIdx.x * 2] = flag0;
-      sc.flag[blockIdx.x * 2 + 1] = flag1;
     }
   }
   tc::fence_before_sync();
@@ -843,95 +985,6 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   if (warp == 9) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
-  }
-}
-
-// ------------------------------------------------------------------ combine
-// CTA (c, y) joins 32 rows of the item that begins in CTA c's range and goes
-// on in those after it: o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
-template <bool BF16, int D>
-__global__ void __launch_bounds__(256) combine_kernel(AttnArgs a, Scratch sc) {
-  extern __shared__ int places[];  // the pieces' places, in order
-  __shared__ int sh_n;
-  pdl_wait();
-  pdl_trigger();
-  const int c = blockIdx.x, parts = sc.head->parts;
-  if (c >= parts) return;
-  const int4 f = sc.flag[c * 2 + 1];
-  if (f.x == 0) return;
-  const int group = a.heads / a.kv_heads, tile_tok = kRows / group;
-  const Item it = sc.items[f.y];
-  const int row0 = blockIdx.y * 32;
-  if (row0 >= it.ntile * kRows || (row0 >> 7) * tile_tok + (row0 & 127) / group >= it.ntok ||
-      (row0 & 127) >= tile_tok * group)
-    return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    int n = 1;
-    if (lane == 0) places[0] = c * 2 + 1;
-    for (int x = c + 1; x < parts; x += 32) {
-      const int state = x + lane < parts ? sc.flag[(x + lane) * 2].x : 0;
-      const uint32_t ends = __ballot_sync(0xFFFFFFFFu, state == 2);
-      const uint32_t some = __ballot_sync(0xFFFFFFFFu, state != 0) &
-                            (ends ? (2u << (__ffs(ends) - 1)) - 1u : ~0u);
-      if (some >> lane & 1) places[n + __popc(some & ((1u << lane) - 1u))] = (x + lane) * 2;
-      n += __popc(some);
-      if (ends) break;
-    }
-    if (lane == 0) sh_n = n;
-  }
-  cta_sync();
-  const int n = sh_n;
-  constexpr int E = D / 32;
-  for (int i = warp; i < 32; i += 8) {
-    const int r = row0 + i, tile = r >> 7, rr = r & 127;
-    const int tok = tile * tile_tok + rr / group;
-    if (rr >= tile_tok * group || tok >= it.ntok) continue;
-    float top = kNegInf;
-    for (int p = lane; p < n; p += 32) top = fmaxf(top, sc.ml[(int64_t)places[p] * 256 + r].x);
-    top = warp_max(top);
-    const float ref = top == kNegInf ? 0.f : top;
-    float l = 0.f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int p0 = 0; p0 < n; p0 += 32) {
-      float g = 0.f;
-      int place = 0;
-      if (p0 + lane < n) {
-        place = places[p0 + lane];
-        const float2 ml = sc.ml[(int64_t)place * 256 + r];
-        g = tc::exp2_approx(ml.x - ref);
-        l += g * ml.y;
-      }
-      const int cnt = min(32, n - p0);
-#pragma unroll 4
-      for (int p = 0; p < cnt; ++p) {
-        const float gp = __shfl_sync(0xFFFFFFFFu, g, p);
-        const int pl = __shfl_sync(0xFFFFFFFFu, place, p);
-        const float* o = sc.o + ((int64_t)pl * 256 + r) * D + lane * E;
-        if (E == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(o);
-          acc[0] = fmaf(gp, v.x, acc[0]);
-          acc[1] = fmaf(gp, v.y, acc[1]);
-          acc[2 % E] = fmaf(gp, v.z, acc[2 % E]);
-          acc[3 % E] = fmaf(gp, v.w, acc[3 % E]);
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(o);
-          acc[0] = fmaf(gp, v.x, acc[0]);
-          acc[1] = fmaf(gp, v.y, acc[1]);
-        }
-      }
-    }
-    l = warp_sum(l);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t out_row =
-        (int64_t)(it.tok0 + tok) * a.heads + f.z * group + (rr - rr / group * group);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + out_row * (D * 2)) +
-                    lane * (E / 2);
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      dst[e / 2] = l == 0.f ? 0u : (l != l ? 0x7fff7fffu : pack2<BF16>(acc[e] * inv, acc[e + 1] * inv));
-    if (a.lse && lane == 0) a.lse[out_row] = l == 0.f ? kNegInf : ref * kLn2 + logf(l);
   }
 }
 
@@ -943,38 +996,36 @@ cudaError_t launch_all(const AttnArgs& a, const Scratch& sc, int parts, int* err
   if (!make_cache_map(&kmap, a.k_cache, BF16, D, page, a.kv_heads, a.pages, a.ks, box, kf) ||
       !make_cache_map(&vmap, a.v_cache, BF16, D, page, a.kv_heads, a.pages, a.vs, box, vf))
     return cudaErrorInvalidValue;
-  int64_t ctas = 0;
-  if (a.k) {
-    const int64_t all = (int64_t)a.T * a.kv_heads * (D / 8);
-    ctas = (all + kPrepThreads - 1) / kPrepThreads;
-    if (ctas > (int64_t)parts * 8) ctas = (int64_t)parts * 8;
-  }
+  const int64_t counts = most_items(a.S, a.T, a.heads / a.kv_heads) * a.kv_heads * 8;
+  int64_t work = counts / 4;
+  if (a.k && (int64_t)a.T * a.kv_heads * (D / 8) > work) work = (int64_t)a.T * a.kv_heads * (D / 8);
+  int64_t ctas = (work + kPrepThreads - 1) / kPrepThreads;
+  if (ctas > (int64_t)parts * 8) ctas = (int64_t)parts * 8;
   cudaError_t e = launch_kernel(true, prepare_kernel, dim3((unsigned)ctas + 1), dim3(kPrepThreads),
-                                0, s, a, sc, parts, D / 8, err);
+                                0, s, a, sc, parts, counts, D / 8, err);
   if (e != cudaSuccess) return e;
   static int smem_set[64] = {0};
   e = ensure_dynamic_smem(attend_kernel<BF16, D>, Shape<D>::kSmem, smem_set);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(true, attend_kernel<BF16, D>, dim3(parts), dim3(kThreads), Shape<D>::kSmem, s,
-                    kmap, vmap, a, sc, (int)kf, (int)vf, role_wait_cycles(), err);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(true, combine_kernel<BF16, D>, dim3(parts, 2 * kRows / 32), dim3(256),
-                       (size_t)(parts + 1) * sizeof(int), s, a, sc);
+  return launch_kernel(true, attend_kernel<BF16, D>, dim3(parts), dim3(kThreads),
+                       Shape<D>::kSmem, s, kmap, vmap, a, sc, (int)kf, (int)vf, role_wait_cycles(),
+                       err);
 }
 
 }  // namespace
 
 size_t attention_scratch_bytes(int S, int T, int heads, int kv_heads, int dim) {
-  return scratch_size(part_count(), most_items(S, T, heads / kv_heads), dim).total;
+  return scratch_size(part_count(), most_items(S, T, heads / kv_heads), kv_heads, dim).total;
 }
 
 cudaError_t launch_attention(const AttnArgs& a, void* scratch, int* err, cudaStream_t s) {
   const int parts = part_count();
-  const ScratchSize z = scratch_size(parts, most_items(a.S, a.T, a.heads / a.kv_heads), a.dim);
+  const ScratchSize z = scratch_size(parts, most_items(a.S, a.T, a.heads / a.kv_heads), a.kv_heads,
+                                     a.dim);
   char* p = static_cast<char*>(scratch);
-  const Scratch sc = {reinterpret_cast<Header*>(p),          reinterpret_cast<int4*>(p + z.start),
-                      reinterpret_cast<int4*>(p + z.flag),   reinterpret_cast<float2*>(p + z.ml),
-                      reinterpret_cast<float*>(p + z.o),     reinterpret_cast<Item*>(p + z.items)};
+  const Scratch sc = {reinterpret_cast<Header*>(p),           reinterpret_cast<int4*>(p + z.start),
+                      reinterpret_cast<float2*>(p + z.ml),    reinterpret_cast<float*>(p + z.o),
+                      reinterpret_cast<Item*>(p + z.items),   reinterpret_cast<int*>(p + z.done)};
   if (a.dtype == LMHEAD_BF16)
     return a.dim == 64 ? launch_all<true, 64>(a, sc, parts, err, s)
                        : launch_all<true, 128>(a, sc, parts, err, s);

@@ -12,6 +12,7 @@ using namespace lmhead;
 namespace {
 
 constexpr int kMaxRows = 1 << 20;
+constexpr int kMaxRequests = 1 << 16;  // of one attention call
 constexpr int kMaxDim = 65536;
 
 inline bool aligned(const void* p, uintptr_t a) {
@@ -24,7 +25,7 @@ inline int status(cudaError_t e) { return e == cudaSuccess ? LMHEAD_OK : LMHEAD_
 inline bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < (1ll << 38); }
 
 int check_attention(int heads, int kv_heads, int dim, int S, int T) {
-  if (S < 1 || S > kMaxRows || T < 1 || kv_heads < 1 || heads < kv_heads || heads % kv_heads ||
+  if (S < 1 || S > kMaxRequests || T < 1 || kv_heads < 1 || heads < kv_heads || heads % kv_heads ||
       heads > 65535 || heads / kv_heads > 128)
     return LMHEAD_ERR_SHAPE;
   if ((int64_t)T * heads > INT32_MAX) return LMHEAD_ERR_SHAPE;
