@@ -106,7 +106,7 @@ __host__ inline ScratchSize scratch_size(int parts, int64_t items, int kv_heads,
 }
 
 inline int64_t most_items(int S, int T, int group) { return (int64_t)S + T / (2 * (kRows / group)) + 1; }
-inline int part_count() { return sm_count() > 0 ? sm_count() : 1; }
+inline int part_count() { return sm_count() > 255 ? 255 : sm_count() > 0 ? sm_count() : 1; }
 
 // ------------------------------------------------------------------ prepare
 
@@ -189,7 +189,8 @@ __device__ void make_plan(const AttnArgs& a, const Scratch& sc, int most_parts) 
     cta_sync();
   }
   const long long units = (long long)base_w * a.kv_heads;
-  const int parts = (int)min((long long)most_parts, units);
+  // a CTA has work for both warpgroups at least
+  const int parts = (int)min((long long)most_parts, (units + 1) / 2);
   if (tid == 0) {
     sc.head->units = units;
     sc.head->items = base_n;
@@ -270,22 +271,34 @@ template <int NS> struct Ctl {
 
 // The CTA's pieces, in order; every role walks over them by itself.
 struct Cursor {
-  const Header* head;
   const Item* items;
-  long long left;
+  long long units, left;
+  int parts, per_head;
   int idx, hk, off, n_items;
   // the piece
   Item it;
   int b0, b1, p_hk, p_idx;
 
+  // The units of CTA c begin at floor(units c / parts).
+  __device__ long long start_of(int c) const {
+    if (units < (1 << 24)) return (uint32_t)units * (uint32_t)c / (uint32_t)parts;  // parts < 256
+    return units * c / parts;
+  }
+  // The CTA that has unit u.
+  __device__ int cta_of(long long u) const {
+    if (units < (1 << 24))
+      return (int)(((uint32_t)(u + 1) * (uint32_t)parts + (uint32_t)units - 1) / (uint32_t)units) - 1;
+    return (int)(((u + 1) * parts + units - 1) / units) - 1;
+  }
   __device__ void init(const Scratch& sc, int cta) {
-    head = sc.head;
+    const Header* head = sc.head;
     items = sc.items;
-    const int parts = head->parts;
+    parts = head->parts;
     left = 0;
     if (cta >= parts) return;
-    const long long u = head->units;
-    left = u * (cta + 1) / parts - u * cta / parts;
+    units = head->units;
+    per_head = head->per_head;
+    left = start_of(cta + 1) - start_of(cta);
     n_items = head->items;
     const int4 st = sc.start[cta];
     idx = st.x;
@@ -356,88 +369,108 @@ __device__ __forceinline__ void store_cols(const float (&v)[32], char* out16, fl
   }
 }
 
+template <int N> struct Const {
+  static constexpr int value = N;
+};
+
 // Joins the pieces of 32 rows (of row tile `tile`, quarter `quarter`) in COLS
 // columns from col on, by one warp:
 //   o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
-// Lane r holds row r's references and sums; the lanes share the elements.
+// Lane r holds row r's references and sums; the lanes share the elements. What
+// it costs is latency, so many loads are under way together.
 template <bool BF16, int D, int COLS>
-__device__ void join_rows(const AttnArgs& a, const Scratch& sc, const Item& it, int hk, int tile,
-                          int quarter, int col, int64_t out_row, bool valid) {
+__device__ void join_rows(const AttnArgs& a, const Scratch& sc, const Cursor& cur, const Item& it,
+                          int hk, int tile, int quarter, int col, int64_t out_row, bool valid) {
   constexpr int N4 = COLS / 4, EL = COLS / 4;  // float4 of a row; of a lane at 32 rows
   const int lane = threadIdx.x & 31;
-  const long long units = sc.head->units;
-  const int parts = sc.head->parts, w = item_units(it.nblk, it.ntile);
-  const long long ub = (long long)hk * sc.head->per_head + it.prefix;
-  const int c0 = (int)(((ub + 1) * parts + units - 1) / units) - 1;  // its first CTA
-  // the piece of CTA c: its place, -1 if it has none, -2 past the item's last
+  const int w = item_units(it.nblk, it.ntile);
+  const long long ub = (long long)hk * cur.per_head + it.prefix;
+  // its first CTA, and the piece of CTA c: its place, -1 if it has none, -2 past
+  // the item's last
+  const int c0 = cur.cta_of(ub);
   auto place_of = [&](int c) -> int {
-    const long long lo = units * c / parts, hi = units * (c + 1) / parts;
-    if (c >= parts || lo >= ub + w) return -2;
+    if (c >= cur.parts) return -2;
+    const long long lo = cur.start_of(c), hi = cur.start_of(c + 1);
+    if (lo >= ub + w) return -2;
     const int b0 = block_at((int)max(lo - ub, 0ll), it.nblk, it.ntile);
     const int b1 = block_at((int)min(hi - ub, (long long)w), it.nblk, it.ntile);
     return b1 > b0 ? 2 * c + (b0 == 0 ? 1 : 0) : -1;
   };
-  const int row = tile * kRows + quarter * 32 + lane;
+  const int row0 = tile * kRows + quarter * 32;
   const int rows = __popc(__ballot_sync(0xFFFFFFFFu, valid)), elems = rows * N4;
-  // kAtOnce pieces at a time, all of their loads under way together; the sums
-  // move to a larger reference as it comes
-  constexpr int kAtOnce = 8;
-  float ref = kNegInf, l = 0.f;
-  float4 acc[EL];
-#pragma unroll
-  for (int i = 0; i < EL; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float top = kNegInf;
   for (int c = c0;; c += 32) {
     const int place = place_of(c + lane);
     const uint32_t past = __ballot_sync(0xFFFFFFFFu, place == -2);
     const int count = past ? __ffs(past) - 1 : 32;
-    for (int p0 = 0; p0 < count; p0 += kAtOnce) {
-      float2 ml[kAtOnce];
-      const float* from[kAtOnce];
-      float top = ref;
+    for (int p0 = 0; p0 < count; p0 += 8) {
+      float m[8];
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
+      for (int k = 0; k < 8; ++k) {
         const int p = __shfl_sync(0xFFFFFFFFu, place, (p0 + k) & 31);
-        const bool some = p0 + k < count && p >= 0;
-        ml[k] = some && valid ? __ldcg(sc.ml + (int64_t)p * 256 + row) : make_float2(kNegInf, 0.f);
-        from[k] = some ? sc.o + ((int64_t)p * 256 + tile * kRows + quarter * 32) * D + col : nullptr;
+        m[k] = p0 + k < count && p >= 0 && valid ? sc.ml[(int64_t)p * 256 + row0 + lane].x : kNegInf;
       }
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
-      const float zero = top == kNegInf ? 0.f : top;
-      const float old = tc::exp2_approx(ref - zero);
-      l *= old;
-      float f[kAtOnce];
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        f[k] = tc::exp2_approx(ml[k].x - zero);
-        l = fmaf(f[k], ml[k].y, l);
-      }
-      ref = top;
-#pragma unroll
-      for (int i = 0; i < EL; ++i) {
-        if (i * 32 >= elems) break;
-        const int e = i * 32 + lane, r = e / N4;
-        float4 v[kAtOnce];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k)
-          v[k] = from[k] && e < elems
-                     ? __ldcg(reinterpret_cast<const float4*>(from[k] + (int64_t)r * D) + e % N4)
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float fo = __shfl_sync(0xFFFFFFFFu, old, r & 31);
-        acc[i].x *= fo;
-        acc[i].y *= fo;
-        acc[i].z *= fo;
-        acc[i].w *= fo;
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          const float fr = __shfl_sync(0xFFFFFFFFu, f[k], r & 31);
-          acc[i].x = fmaf(fr, v[k].x, acc[i].x);
-          acc[i].y = fmaf(fr, v[k].y, acc[i].y);
-          acc[i].z = fmaf(fr, v[k].z, acc[i].z);
-          acc[i].w = fmaf(fr, v[k].w, acc[i].w);
-        }
-      }
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, m[k]);
     }
+    if (past) break;
+  }
+  const float ref = top == kNegInf ? 0.f : top;
+  float l = 0.f;
+  float4 acc[EL];
+#pragma unroll
+  for (int i = 0; i < EL; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // pieces p0.. (NP of them), NI elements of a lane at a time
+  auto add_pieces = [&](auto np, auto ni, int place, int p0, int count) {
+    constexpr int NP = decltype(np)::value, NI = decltype(ni)::value;
+    float f[NP];
+    const float* from[NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int p = __shfl_sync(0xFFFFFFFFu, place, (p0 + k) & 31);
+      const bool some = p0 + k < count && p >= 0;
+      const float2 ml = some && valid ? sc.ml[(int64_t)p * 256 + row0 + lane]
+                                      : make_float2(kNegInf, 0.f);
+      f[k] = tc::exp2_approx(ml.x - ref);
+      l = fmaf(f[k], ml.y, l);
+      from[k] = some ? sc.o + ((int64_t)p * 256 + row0) * D + col : nullptr;
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < EL; i0 += NI) {
+      if (i0 * 32 >= elems) break;
+      float4 v[NI][NP];
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const int e = (i0 + i) * 32 + lane;
+          v[i][k] = from[k] && e < elems
+                        ? __ldcg(reinterpret_cast<const float4*>(from[k] + (e / N4) * D) + e % N4)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const float fr = __shfl_sync(0xFFFFFFFFu, f[k], (((i0 + i) * 32 + lane) / N4) & 31);
+          float4& s = acc[i0 + i];
+          s.x = fmaf(fr, v[i][k].x, s.x);
+          s.y = fmaf(fr, v[i][k].y, s.y);
+          s.z = fmaf(fr, v[i][k].z, s.z);
+          s.w = fmaf(fr, v[i][k].w, s.w);
+        }
+    }
+  };
+  for (int c = c0;; c += 32) {
+    const int place = place_of(c + lane);
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, place == -2);
+    const int count = past ? __ffs(past) - 1 : 32;
+    if (elems <= 64)
+      for (int p0 = 0; p0 < count; p0 += 8)
+        add_pieces(Const<8>{}, Const<2>{}, place, p0, count);
+    else
+      for (int p0 = 0; p0 < count; p0 += 4)
+        add_pieces(Const<4>{}, Const<4>{}, place, p0, count);
     if (past) break;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -968,7 +1001,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           __threadfence();
           const int from = pair ? 0 : h * (D / 2), to = pair ? D : from + D / 2;
           for (int c = from; c < to; c += kCols)
-            join_rows<BF16, D, kCols>(a, sc, it, p_hk, tile, warp & 3, c, out_row, valid);
+            join_rows<BF16, D, kCols>(a, sc, cur, it, p_hk, tile, warp & 3, c, out_row, valid);
         }
       }
       if (have) q_loaded();
