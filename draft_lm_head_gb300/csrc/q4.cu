@@ -96,8 +96,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// N consecutive 16-bit values of a row: in one load, or those below `left` one
-// by one with zeros behind them.
+// N consecutive 16-bit values of a row.
 template <int N> struct Packed {
   uint32_t w[(N + 1) / 2];
 };
@@ -114,6 +113,7 @@ template <int N> __device__ __forceinline__ Packed<N> load_whole(const uint16_t*
   }
   return v;
 }
+// Those below `left` one by one, zeros behind them.
 template <int N> __device__ __forceinline__ Packed<N> load_single(const uint16_t* p, int left) {
   Packed<N> v;
 #pragma unroll
@@ -122,6 +122,19 @@ template <int N> __device__ __forceinline__ Packed<N> load_single(const uint16_t
     if (2 * i + 1 < N && 2 * i + 1 < left) v.w[i] |= (uint32_t)__ldg(p + 2 * i + 1) << 16;
   }
   return v;
+}
+// Values [N pos, N pos + N) of 8.
+template <int N> __device__ __forceinline__ Packed<N> packed_of(const uint4& v, int pos) {
+  Packed<N> r;
+  if (N == 4) {
+    r.w[0] = pos & 1 ? v.z : v.x;
+    r.w[(N + 1) / 2 - 1] = pos & 1 ? v.w : v.y;
+  } else {
+    const int word = N == 2 ? pos : pos >> 1;
+    const uint32_t x = word & 2 ? (word & 1 ? v.w : v.z) : (word & 1 ? v.y : v.x);
+    r.w[0] = N == 1 && (pos & 1) ? x >> 16 : x;
+  }
+  return r;
 }
 template <bool BF16, int N> __device__ __forceinline__ float packed_at(const Packed<N>& v, int i) {
   const float2 f = pair_to_float<BF16>(v.w[i >> 1]);
@@ -170,8 +183,11 @@ __device__ __forceinline__ uint32_t ring_at(int blk, int row, int chunk) {
   return (uint32_t)(blk * 2048 + (row ^ blk) * 64 + ((chunk ^ x) * 16));
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
-  const int n = in ? 16 : 0;  // the rest is zero-filled
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool in) {
+  const int n = in ? 16 : 0;
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
 }
@@ -238,24 +254,40 @@ q4_kernel(Q4Launch a, int* err) {
       for (int j = 0; j < CPY; ++j)
         c_id[j] = row_id(c_vec, (int64_t)c_tile * kRowsWarp + j * CR + c_row);
   };
+  // where this lane's chunks go in a stage, and where the next ones come from
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
+  uint32_t c_dst[CPY];
+#pragma unroll
+  for (int j = 0; j < CPY; ++j)
+    c_dst[j] = ring_s + ring_at(c_chunk >> 2, j * CR + c_row, c_chunk & 3);
+  const uint8_t* c_src[CPY];
+  int c_rows = 0;  // of the tile
+  auto copy_tile = [&]() {
+    copy_ids();
+    if (c_unit >= u_hi) return;
+    c_rows = (int)min((int64_t)kRowsWarp, count - (int64_t)c_tile * kRowsWarp);
+    const uint8_t* src = a.codes + a.k_lo / 2 + (s_lo * SB * 4 + c_chunk) * 16;
+#pragma unroll
+    for (int j = 0; j < CPY; ++j)
+      c_src[j] = src + (GATHER ? (int64_t)c_id[j] : (int64_t)c_tile * kRowsWarp + j * CR + c_row) *
+                           row_bytes;
+  };
   auto copy_stage = [&]() {
     if (c_unit < u_hi) {
-      const int at = a.k_lo / 2 + (c_stage * SB * 4 + c_chunk) * 16;
-      // rows of the tile, none when past the end of the piece
-      const int rows =
-          at < a.k_hi / 2 ? (int)min((int64_t)kRowsWarp, count - (int64_t)c_tile * kRowsWarp) : 0;
-      const uint8_t* src = a.codes + at;
-      if (!GATHER) src += ((int64_t)c_tile * kRowsWarp + c_row) * row_bytes;
+      const uint32_t slot_at = c_slot * (SB * 2048);
+      if (c_rows == kRowsWarp && (c_stage + 1) * SB * kBlockK <= kd) {
 #pragma unroll
-      for (int j = 0; j < CPY; ++j) {
-        const int r = j * CR + c_row;
-        const bool in = r < rows;
-        const uint8_t* p =
-            GATHER ? src + (int64_t)c_id[j] * row_bytes : src + (int64_t)(j * CR) * row_bytes;
-        copy16(ring_s + c_slot * (SB * 2048) + ring_at(c_chunk >> 2, r, c_chunk & 3),
-               in ? p : a.codes, in);
+        for (int j = 0; j < CPY; ++j) copy16(c_dst[j] + slot_at, c_src[j]);
+      } else {
+        const bool in = (c_stage * SB * 4 + c_chunk) * 32 < kd;  // of the piece
+#pragma unroll
+        for (int j = 0; j < CPY; ++j) {
+          const bool there = in && j * CR + c_row < c_rows;
+          copy16_or_zero(c_dst[j] + slot_at, there ? c_src[j] : a.codes, there);
+        }
       }
+#pragma unroll
+      for (int j = 0; j < CPY; ++j) c_src[j] += SB * (kBlockK / 2);
       if (++c_stage == s_hi) {
         c_stage = s_lo;
         ++c_unit;
@@ -264,13 +296,13 @@ q4_kernel(Q4Launch a, int* err) {
           ++c_vec;
         }
         c_tile = c_rem * teams + slot;
-        copy_ids();
+        copy_tile();
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     c_slot = c_slot + 1 == NS ? 0 : c_slot + 1;
   };
-  copy_ids();
+  copy_tile();
 #pragma unroll
   for (int i = 0; i < NS - 1; ++i) copy_stage();
 
@@ -354,7 +386,16 @@ q4_kernel(Q4Launch a, int* err) {
 #pragma unroll
   for (int y = 0; y < NT; ++y) hp[y] = hs + (size_t)min(y * 8 + g, nv - 1) * stride + t * 16;
   constexpr int SC = SB * GB;  // scales of a row and stage
-  const bool whole = row_groups % SC == 0 && a.scales_aligned && (a.k_lo / G) % SC == 0;
+  // Scales of 8 groups are 16 bytes where the rows allow it. With two vector
+  // tiles a lane loads those of one row (g + 8 t) for 8 / SC stages and hands
+  // them round: loaded stage by stage they took as much of the L2 as the codes, a
+  // sector a row (194 against 136 us for 16 vectors over the wide head). With
+  // one there is room for the sectors in the L1 and the shuffles cost more than
+  // they save (61 against 56 us for one vector).
+  constexpr int PER = 8 / SC;
+  constexpr bool CHUNKS = NT == 2;
+  constexpr int ALIGN = CHUNKS ? 8 : SC;
+  const bool whole = row_groups % ALIGN == 0 && a.scales_aligned && (a.k_lo / G) % ALIGN == 0;
   const int groups = kd / G;
   int use = 0, turn = 0;  // ring slot; which of the partial sums
   int vec = (int)(u_lo / per_vec), rem = (int)(u_lo - (int64_t)vec * per_vec);
@@ -374,17 +415,18 @@ q4_kernel(Q4Launch a, int* err) {
 #pragma unroll
         for (int z = 0; z < 2; ++z) acc[x][y][z] = make_float2(0.f, 0.f);
     if (on) {
-      // scales of this lane's rows g, g + 8, g + 16, g + 24, one stage ahead
-      const uint16_t *sp[4], *op[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t row = row_id(vec, first + g + 8 * r);
-        sp[r] = a.scales + row * row_groups + a.k_lo / G;
-        op[r] = MINS ? a.mins + row * row_groups + a.k_lo / G : nullptr;
-      }
+      // scales of this lane's rows g, g + 8, g + 16, g + 24: one stage ahead, or
+      // in chunks one chunk ahead
+      const uint16_t *sp[4] = {}, *op[4] = {};
+      uint4 s_now, s_next, o_now, o_next;
       Packed<SC> sc_n[4], of_n[4];
+      auto load_chunk = [&](int ch) {
+        if (ch * 8 >= groups) return;
+        s_next = __ldg(reinterpret_cast<const uint4*>(sp[0]) + ch);
+        if (MINS) o_next = __ldg(reinterpret_cast<const uint4*>(op[0]) + ch);
+      };
       auto load_scales = [&](int st) {
-        if (whole) {
+        if (!CHUNKS && whole) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             sc_n[r] = load_whole<SC>(sp[r] + st * SC);
@@ -398,19 +440,51 @@ q4_kernel(Q4Launch a, int* err) {
           }
         }
       };
-      load_scales(s_lo);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (CHUNKS && whole && r > 0) break;
+        const int64_t at =
+            (int64_t)row_id(vec, first + g + 8 * (CHUNKS && whole ? t : r)) * row_groups + a.k_lo / G;
+        sp[r] = a.scales + at;
+        op[r] = MINS ? a.mins + at : nullptr;
+      }
+      if (CHUNKS && whole) {
+        load_chunk(s_lo / PER);
+        s_now = s_next;
+        if (MINS) o_now = o_next;
+        load_chunk(s_lo / PER + 1);
+      } else {
+        load_scales(s_lo);
+      }
 #pragma unroll 1
       for (int st = s_lo; st < s_hi; ++st) {
         copy_stage();
         asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
         __syncwarp();
         Packed<SC> sc[4], of[4];
+        if (CHUNKS && whole) {
+          if (st % PER == 0 && st != s_lo) {
+            s_now = s_next;
+            if (MINS) o_now = o_next;
+            load_chunk(st / PER + 1);
+          }
+          const Packed<SC> ms = packed_of<SC>(s_now, st % PER);
+          const Packed<SC> mo = MINS ? packed_of<SC>(o_now, st % PER) : ms;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          sc[r] = sc_n[r];
-          if (MINS) of[r] = of_n[r];
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < (SC + 1) / 2; ++i) {
+              sc[r].w[i] = __shfl_sync(0xFFFFFFFFu, ms.w[i], (lane & ~3) | r);
+              if (MINS) of[r].w[i] = __shfl_sync(0xFFFFFFFFu, mo.w[i], (lane & ~3) | r);
+            }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sc[r] = sc_n[r];
+            if (MINS) of[r] = of_n[r];
+          }
+          if (st + 1 < s_hi) load_scales(st + 1);
         }
-        if (st + 1 < s_hi) load_scales(st + 1);
         const unsigned char* codes = ring + use * (SB * 2048);
         use = use + 1 == NS ? 0 : use + 1;
 #pragma unroll
