@@ -11,12 +11,15 @@
 //     barrier, and past the first tile little but the exponentials.
 //   beam_merge: a CTA per sequence turns the slices' sums into lse and picks
 //     the k best of beams x slices x k scored entries.
+//   beam_small: both in one launch where a sequence has few slices.
 // Bound by reading the logits once. Beams meet at the border of the k with gaps
 // below 32-bit rounding, so a lane's sums of exp are 32-bit, but everything
 // across lanes, and the scores of the few candidates, are pairs of fp32 numbers
 // (the rounded value and what its rounding left: about 48 bits; fp64 units are
 // too few on this GPU, the merge took twice as long with them).
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -146,19 +149,12 @@ __device__ __forceinline__ float kth_of_threads(float mine, int k, float* sh, fl
   return *out;
 }
 
+// Slice sl of the row at x, by one warp.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 4)
-beam_rows_kernel(const T* logits, int64_t stride, int n, int rows, int nsl, int slice_len, int k,
-                 const uint8_t* finished, Slice* slices, float* best_v, int32_t* best_i) {
-  pdl_wait();
-  pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + warp;
-  if (unit >= (int64_t)rows * nsl) return;
-  const int row = (int)(unit / nsl), sl = (int)(unit - (int64_t)row * nsl);
-  if (finished && finished[row]) return;  // its one entry is its own score
+__device__ __forceinline__ void scan_slice(const T* x, int n, int sl, int slice_len, int k,
+                                           Slice* slice, float* best_v, int32_t* best_i) {
+  const int lane = threadIdx.x & 31;
   constexpr int V = Elem<T>::kVec, U = kPerLane / V;
-  const T* x = logits + (int64_t)row * stride;
   // 16-byte reads at 16-byte boundaries: the row starts `off` entries after
   // one, and slices are cut at them
   const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
@@ -243,11 +239,25 @@ beam_rows_kernel(const T* logits, int64_t stride, int n, int rows, int nsl, int 
   const float s = s2.x + s2.y, top = warp_max(m);
   const Pair sum =
       warp_sum(Pair{m == kNegInf && s == 0.f ? 0.f : s * exp2_fast((m - top) * kLog2e), 0.f});
-  if (lane == 0) slices[unit] = {top, sum, 0.f};
+  if (lane == 0) *slice = {top, sum, 0.f};
   if (lane < k) {
-    best_v[unit * k + lane] = best ? key_score(best) : kNegInf;
-    best_i[unit * k + lane] = best ? key_id(best) : -1;
+    best_v[lane] = best ? key_score(best) : kNegInf;
+    best_i[lane] = best ? key_id(best) : -1;
   }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads, 4)
+beam_rows_kernel(const T* logits, int64_t stride, int n, int rows, int nsl, int slice_len, int k,
+                 const uint8_t* finished, Slice* slices, float* best_v, int32_t* best_i) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (unit >= (int64_t)rows * nsl) return;
+  const int row = (int)(unit / nsl), sl = (int)(unit - (int64_t)row * nsl);
+  if (finished && finished[row]) return;  // its one entry is its own score
+  scan_slice(logits + (int64_t)row * stride, n, sl, slice_len, k, slices + unit, best_v + unit * k,
+             best_i + unit * k);
 }
 
 // Order of the merge: the larger score (as a key that orders like the pair of
@@ -256,9 +266,10 @@ __device__ __forceinline__ bool ahead(uint64_t sa, int32_t ia, uint64_t sb, int3
   return sa > sb || (sa == sb && ia < ib);
 }
 
-__global__ void __launch_bounds__(kRowThreads)
-beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
-                  const int32_t* best_i) {
+// The k best of a sequence from its rows' slices, by one CTA.
+__device__ __forceinline__ void merge_sequence(const BeamArgs& a, int seq, int nsl,
+                                               const Slice* slices, const float* best_v,
+                                               const int32_t* best_i) {
   // lse in its two parts: x - top is small where top is not
   __shared__ float row_top[kBeamMaxBeams];
   __shared__ Pair row_log[kBeamMaxBeams];
@@ -271,12 +282,10 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
   __shared__ int sh_count;
   __shared__ uint64_t w_score[kRowThreads / 32];
   __shared__ int32_t w_flat[kRowThreads / 32];
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, seq = blockIdx.x, B = a.beams, k = a.k;
+  const int tid = threadIdx.x, lane = tid & 31, B = a.beams, k = a.k;
   const int32_t n = (int32_t)a.n;
   const int per = nsl * k, all = B * per;
-  const size_t row0 = (size_t)seq * B, e0 = row0 * per;
+  const size_t row0 = (size_t)seq * B;
   // a thread's first kKept entries are under way while the rows' sums are made
   constexpr int kKept = 4;
   float kept_v[kKept];
@@ -284,11 +293,11 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
 #pragma unroll
   for (int j = 0; j < kKept; ++j) {
     const int e = tid + j * kRowThreads;
-    kept_v[j] = e < all ? best_v[e0 + e] : 0.f;
-    kept_i[j] = e < all ? best_i[e0 + e] : -1;
+    kept_v[j] = e < all ? best_v[e] : 0.f;
+    kept_i[j] = e < all ? best_i[e] : -1;
   }
   for (int b = tid >> 5; b < B; b += kRowThreads / 32) {  // a warp per row
-    const Slice* sl = slices + (row0 + b) * nsl;
+    const Slice* sl = slices + (size_t)b * nsl;
     const bool done = a.finished && a.finished[row0 + b];
     const float score = a.scores[row0 + b];
     float top = kNegInf;
@@ -340,7 +349,7 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
     if (!(fabsf(sc.h) < -kNegInf)) return 0;  // NaN too
     return ((uint64_t)float_key(sc.h) << 32) | float_key(sc.l);
   };
-  auto entry = [&](int e, int32_t& flat) { return score_of(e, best_v[e0 + e], best_i[e0 + e], flat); };
+  auto entry = [&](int e, int32_t& flat) { return score_of(e, best_v[e], best_i[e], flat); };
   auto rounded = [](uint64_t key) { return key ? key_float((uint32_t)(key >> 32)) : kNegInf; };
   // the k-th largest of the threads' rounded maxima bounds the k best from below
   uint64_t kept[kKept];
@@ -442,6 +451,37 @@ beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
   }
 }
 
+__global__ void __launch_bounds__(kRowThreads)
+beam_merge_kernel(BeamArgs a, int nsl, const Slice* slices, const float* best_v,
+                  const int32_t* best_i) {
+  pdl_wait();
+  pdl_trigger();
+  const size_t unit = (size_t)blockIdx.x * a.beams * nsl;
+  merge_sequence(a, blockIdx.x, nsl, slices + unit, best_v + unit * a.k, best_i + unit * a.k);
+}
+
+// Both steps of a sequence whose rows have few slices, in one launch: the head's
+// candidates, short vocabularies.
+constexpr int kFewSlices = 16;
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads)
+beam_small_kernel(const T* logits, BeamArgs a, int nsl, int slice_len) {
+  __shared__ Slice slices[kFewSlices];
+  __shared__ float best_v[kFewSlices * kBeamMaxK];
+  __shared__ int32_t best_i[kFewSlices * kBeamMaxK];
+  pdl_wait();
+  pdl_trigger();
+  for (int u = threadIdx.x >> 5; u < a.beams * nsl; u += kRowThreads / 32) {
+    const int b = u / nsl;
+    const size_t row = (size_t)blockIdx.x * a.beams + b;
+    if (a.finished && a.finished[row]) continue;
+    scan_slice(logits + (int64_t)row * a.row_stride, (int)a.n, u - b * nsl, slice_len, a.k,
+               slices + u, best_v + u * a.k, best_i + u * a.k);
+  }
+  cta_sync();
+  merge_sequence(a, blockIdx.x, nsl, slices, best_v, best_i);
+}
+
 // ---- states of the chosen beams: out[s, j] = state[s, parent[s, j]], zeros
 // where there is no parent. A copy: 16 bytes a thread where the row allows.
 constexpr int kCopyBytes = 16384;  // of a row, per CTA
@@ -503,18 +543,18 @@ cudaError_t launch_beam_select(const BeamArgs& a, void* scratch, cudaStream_t s)
   int32_t* bi = reinterpret_cast<int32_t*>(bv + cells * a.k);
   const int warps = kRowThreads / 32;
   const dim3 grid((unsigned)((cells + warps - 1) / warps)), block(kRowThreads);
-  cudaError_t e;
-  if (a.dtype == LMHEAD_FP32)
-    e = launch_kernel(true, beam_rows_kernel<float>, grid, block, 0, s, (const float*)a.logits,
-                      a.row_stride, (int)a.n, rows, nsl, len, a.k, a.finished, sl, bv, bi);
-  else if (a.dtype == LMHEAD_BF16)
-    e = launch_kernel(true, beam_rows_kernel<__nv_bfloat16>, grid, block, 0, s,
-                      (const __nv_bfloat16*)a.logits, a.row_stride, (int)a.n, rows, nsl, len, a.k,
-                      a.finished, sl, bv, bi);
-  else
-    e = launch_kernel(true, beam_rows_kernel<__half>, grid, block, 0, s, (const __half*)a.logits,
-                      a.row_stride, (int)a.n, rows, nsl, len, a.k, a.finished, sl, bv, bi);
-  if (e != cudaSuccess) return e;
+  const bool few = a.beams * nsl <= kFewSlices;
+  auto scan = [&](auto* logits) -> cudaError_t {
+    using T = std::remove_cv_t<std::remove_pointer_t<decltype(logits)>>;
+    if (few)
+      return launch_kernel(true, beam_small_kernel<T>, dim3(a.S), block, 0, s, logits, a, nsl, len);
+    return launch_kernel(true, beam_rows_kernel<T>, grid, block, 0, s, logits, a.row_stride,
+                         (int)a.n, rows, nsl, len, a.k, a.finished, sl, bv, bi);
+  };
+  const cudaError_t e = a.dtype == LMHEAD_FP32   ? scan(static_cast<const float*>(a.logits))
+                        : a.dtype == LMHEAD_BF16 ? scan(static_cast<const __nv_bfloat16*>(a.logits))
+                                                 : scan(static_cast<const __half*>(a.logits));
+  if (e != cudaSuccess || few) return e;
   return launch_kernel(true, beam_merge_kernel, dim3(a.S), block, 0, s, a, nsl, (const Slice*)sl,
                        (const float*)bv, (const int32_t*)bi);
 }

@@ -98,19 +98,24 @@ def page_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor,
     if out is None:
         if max_tokens < 1 or S < 1:
             raise ValueError("max_tokens: must be positive, as must the number of requests")
-        out = PagePlan(_empty(max_tokens, i32, dev, stream), _empty(max_tokens, i32, dev, stream),
-                       _empty(S + 1, i32, dev, stream), _empty(S, i32, dev, stream),
-                       _empty(1, i32, dev, stream))
-    slots, positions, cu, granted, free_left = out
+        # one allocation, its parts one behind the other
+        buf = _empty(2 * max_tokens + 2 * S + 2, i32, dev, stream)
+        at = buf.data_ptr()
+        ptrs = (at, at + 4 * max_tokens, at + 8 * max_tokens, at + 8 * max_tokens + 4 * (S + 1),
+                at + 8 * max_tokens + 4 * (2 * S + 1))
+        out = PagePlan(*buf.split_with_sizes((max_tokens, max_tokens, S + 1, S, 1)))
+    else:
+        slots, positions, cu, granted, free_left = out
+        ptrs = (_dense(slots, i32, (max_tokens,), dev, "slots"),
+                _dense(positions, i32, (max_tokens,), dev, "positions"),
+                _dense(cu, i32, (S + 1,), dev, "cu"), _dense(granted, i32, (S,), dev, "granted"),
+                _dense(free_left, i32, (1,), dev, "free_left"))
     check(load().lmhead_page_plan(
         _dense(lens, i32, (S,), dev, "lens"), _dense(new_lens, i32, (S,), dev, "new_lens"), S,
         _dense(table, i32, (S, width), dev, "table"), width,
         _dense(free_pages, i32, (cap,), dev, "free_pages"), cap,
-        _dense(free_count, i32, (1,), dev, "free_count"), page_size, max_tokens,
-        _dense(slots, i32, (max_tokens,), dev, "slots"),
-        _dense(positions, i32, (max_tokens,), dev, "positions"),
-        _dense(cu, i32, (S + 1,), dev, "cu"), _dense(granted, i32, (S,), dev, "granted"),
-        _dense(free_left, i32, (1,), dev, "free_left"), _stream(stream, dev)), "page_plan")
+        _dense(free_count, i32, (1,), dev, "free_count"), page_size, max_tokens, *ptrs,
+        _stream(stream, dev)), "page_plan")
     return out
 
 
@@ -280,8 +285,11 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, k: int,
     if out is None:
         parent, token = _empty((S, k), i32, dev, stream), _empty((S, k), i32, dev, stream)
         score = _empty((S, k), torch.float32, dev, stream)
+        ptrs = (parent.data_ptr(), token.data_ptr(), score.data_ptr())
     else:
         parent, token, score = out
+        ptrs = (_dense(parent, i32, (S, k), dev, "parent"), _dense(token, i32, (S, k), dev, "token"),
+                _dense(score, torch.float32, (S, k), dev, "score"))
     ws = _workspace(workspace, _beam_bytes(dev, S, beams, n, k), dev, stream)
     # a bool is a byte
     kind = torch.uint8 if finished is None or finished.dtype is torch.uint8 else torch.bool
@@ -289,11 +297,12 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, k: int,
         _DTYPES[logits.dtype], logits.data_ptr(), stride,
         _dense(scores, torch.float32, (rows,), dev, "scores"),
         _dense(ids, i32, (rows, n), dev, "ids"),
-        _dense(finished, kind, (rows,), dev, "finished"), S, beams, n, k, eos,
-        _dense(parent, i32, (S, k), dev, "parent"), _dense(token, i32, (S, k), dev, "token"),
-        _dense(score, torch.float32, (S, k), dev, "score"), ws.data_ptr(), ws.numel(),
-        _stream(stream, dev)), "beam_select")
+        _dense(finished, kind, (rows,), dev, "finished"), S, beams, n, k, eos, *ptrs,
+        ws.data_ptr(), ws.numel(), _stream(stream, dev)), "beam_select")
     return parent, token, score
+
+
+_Table = ctypes.c_int64 * 24  # up to 8 sources, destinations and sizes
 
 
 def beam_reorder(parent: torch.Tensor, states: Sequence[torch.Tensor], beams: int, out=None,
@@ -309,7 +318,7 @@ def beam_reorder(parent: torch.Tensor, states: Sequence[torch.Tensor], beams: in
         raise ValueError("states, beams: expected 1 to 8 tensors and a positive number of beams")
     if out is not None and len(out) != n:
         raise ValueError("out: expected one tensor per state")
-    res, table = [], (ctypes.c_int64 * (3 * n))()
+    res, table = [], _Table()
     for i, t in enumerate(states):
         shape, dt = t.shape, t.dtype
         if t.dim() < 1 or shape[0] != rows or t.device != dev or not t.is_contiguous():
@@ -318,10 +327,10 @@ def beam_reorder(parent: torch.Tensor, states: Sequence[torch.Tensor], beams: in
         o = out[i] if out is not None else _empty(want, dt, dev, stream)
         res.append(o)
         table[i] = t.data_ptr()
-        table[n + i] = _dense(o, dt, want, dev, "out") if out is not None else o.data_ptr()
-        table[2 * n + i] = t.numel() // rows * t.element_size()
+        table[8 + i] = _dense(o, dt, want, dev, "out") if out is not None else o.data_ptr()
+        table[16 + i] = t.numel() // rows * t.element_size()
     at = ctypes.addressof(table)
     check(load().lmhead_beam_reorder(
-        _dense(parent, torch.int32, (S, k), dev, "parent"), S, beams, k, n, at, at + 8 * n,
-        at + 16 * n, _stream(stream, dev)), "beam_reorder")
+        _dense(parent, torch.int32, (S, k), dev, "parent"), S, beams, k, n, at, at + 64, at + 128,
+        _stream(stream, dev)), "beam_reorder")
     return res
