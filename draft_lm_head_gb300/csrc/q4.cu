@@ -159,15 +159,15 @@ struct Q4Launch {
   int64_t ldo;
   float* out;
   int tiles;           // row tiles (of each vector in the gather)
-  int split;           // warps that share a tile's codes
+  int share;           // a tile's codes may be divided between warps
   int scales_aligned;  // scales and mins at 16 bytes
 };
 
 // Shared memory: h of the call's vectors, [vector][block][i][t] 16-byte words
 // (8 codes' worth, codes 0,4,1,5,2,6,3,7), rows 64 bytes off a multiple of
 // 128 so that the 8 lanes of a 16-byte read phase (2 vectors x 4 chunks) hit
-// all banks once; then H per group and vector; each warp's ring of codes; and,
-// twice, the warps' partial sums where several share a tile.
+// all banks once; then H per group and vector; each warp's ring of codes; and
+// a tile's sums per warp where warps share tiles.
 __host__ __device__ inline int h_stride(int blocks) { return blocks * 256 + 64; }
 // Bytes of h and H together: the rings behind them start at a multiple of 128.
 __host__ __device__ inline int h_bytes(int blocks, int vecs, int sums) {
@@ -192,24 +192,25 @@ __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bo
                : "memory");
 }
 
+// Hidden vectors that a CTA of the gather holds at a time.
+constexpr int kGatherVecs = 2;
+
 template <bool BF16, int G, int NT, int WARPS, int SB, int NS, int MODE, bool GATHER>
 __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1)
 q4_kernel(Q4Launch a, int* err) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t sh_top[WARPS];
-  // what each vector's sums are scaled back by (the gather has two in turn: one
-  // is read for the last tile of a vector while the next is laid out)
-  __shared__ float sh_back[GATHER ? 2 : NT * 8];
+  __shared__ float sh_back[GATHER ? kGatherVecs : NT * 8];  // what a vector's sums are scaled back by
   constexpr bool MINS = MODE == kMins, SUMS = MODE != kCentred;
   constexpr int GB = kBlockK / G;          // groups a block
-  constexpr int HC = GATHER ? 1 : NT * 8;  // vectors of H
+  constexpr int HC = GATHER ? kGatherVecs : NT * 8;  // vectors of H
   constexpr int CPY = SB * 4;              // copies a lane and stage
   constexpr int CR = 32 / CPY;             // rows a copy of the warp covers
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int kd = a.k_hi - a.k_lo;
   const int blocks = (kd + kBlockK - 1) / kBlockK;
   const int stride = h_stride(blocks);
-  const int nv = GATHER ? 1 : min(a.M, NT * 8);
+  const int nv = GATHER ? kGatherVecs : min(a.M, NT * 8);
   unsigned char* hs = smem;
   float* Hs = reinterpret_cast<float*>(smem + (size_t)nv * stride);  // [group][HC]
   unsigned char* rings = smem + h_bytes(blocks, nv, SUMS ? blocks * GB * HC : 0);
@@ -220,14 +221,22 @@ q4_kernel(Q4Launch a, int* err) {
   const int64_t count = GATHER ? a.K : a.n;
   const int row_bytes = a.d / 2, row_groups = a.d / G;
 
-  // A unit is the next tile of each of the CTA's teams of `split` warps, of one
-  // hidden vector (the gather) or of all of them; a CTA takes a run of units.
-  const int teams = WARPS / a.split, k_warp = warp % a.split, slot = warp / a.split;
+  // The CTA takes a run of tiles (of vector after vector in the gather) and
+  // divides their stages evenly among its warps, wherever a tile's end falls, so
+  // that no warp waits for another before the end: a warp whose stages begin
+  // inside a tile and reach its end adds the sums that earlier warps left for it.
+  // It goes through its tiles from the last to the first, so that what it
+  // leaves itself is done first and what it waits for comes last. In the gather
+  // this is repeated for each kGatherVecs vectors of the run.
   const int all_stages = (blocks + SB - 1) / SB;
-  const int s_lo = all_stages * k_warp / a.split, s_hi = all_stages * (k_warp + 1) / a.split;
-  const int per_vec = (a.tiles + teams - 1) / teams;
-  const int64_t units = (int64_t)per_vec * (GATHER ? a.M : 1);
-  const int64_t u_lo = units * blockIdx.x / gridDim.x, u_hi = units * (blockIdx.x + 1) / gridDim.x;
+  const int64_t tiles = (int64_t)a.tiles * (GATHER ? a.M : 1);
+  const int64_t run_lo = tiles * blockIdx.x / gridDim.x, run_hi = tiles * (blockIdx.x + 1) / gridDim.x;
+  int64_t part_lo = run_lo;  // of the run
+  int mine_lo = 0, mine_hi = 0;  // this warp's stages of the part
+  auto share_of = [&](int w, int64_t count_tiles) -> int {  // where warp w's stages begin
+    return a.share ? (int)(count_tiles * all_stages * w / WARPS)
+                   : (int)(count_tiles * w / WARPS) * all_stages;
+  };
   auto row_id = [&](int vec, int64_t i) -> int32_t {  // the row behind entry i, 0 for none
     if (!GATHER) return i < count ? (int32_t)i : 0;
     if (i >= count) return 0;
@@ -238,22 +247,7 @@ q4_kernel(Q4Launch a, int* err) {
   // ---- the copies of this warp's codes run NS - 1 stages ahead, over the ends
   // of its tiles
   const int c_row = lane / CPY, c_chunk = lane % CPY;  // of the warp's first copy
-  int64_t c_unit = u_lo;
-  int c_vec = (int)(u_lo / per_vec), c_rem = (int)(u_lo - (int64_t)c_vec * per_vec);
-  int c_tile = c_rem * teams + slot, c_stage = s_lo, c_slot = 0;
-  int32_t c_id[GATHER ? CPY : 1];
-  auto copy_ids = [&]() {  // of the next unit in which this team has a tile
-    while (c_tile >= a.tiles && c_unit < u_hi) {
-      ++c_unit;
-      c_rem = 0;  // only a vector's last unit lacks tiles
-      ++c_vec;
-      c_tile = slot;
-    }
-    if (GATHER && c_unit < u_hi)
-#pragma unroll
-      for (int j = 0; j < CPY; ++j)
-        c_id[j] = row_id(c_vec, (int64_t)c_tile * kRowsWarp + j * CR + c_row);
-  };
+  int c_end = 0, c_stage = 0, c_last = 0, c_slot = 0;  // c_end: stages not yet begun end here
   // where this lane's chunks go in a stage, and where the next ones come from
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
   uint32_t c_dst[CPY];
@@ -262,18 +256,26 @@ q4_kernel(Q4Launch a, int* err) {
     c_dst[j] = ring_s + ring_at(c_chunk >> 2, j * CR + c_row, c_chunk & 3);
   const uint8_t* c_src[CPY];
   int c_rows = 0;  // of the tile
-  auto copy_tile = [&]() {
-    copy_ids();
-    if (c_unit >= u_hi) return;
-    c_rows = (int)min((int64_t)kRowsWarp, count - (int64_t)c_tile * kRowsWarp);
-    const uint8_t* src = a.codes + a.k_lo / 2 + (s_lo * SB * 4 + c_chunk) * 16;
+  auto copy_tile = [&]() {  // on to the tile before, if this warp has stages there
+    c_stage = c_last = 0;
+    if (c_end <= mine_lo) return;
+    const int tl = (c_end - 1) / all_stages;
+    c_stage = max(0, mine_lo - tl * all_stages);
+    c_last = c_end - tl * all_stages;
+    c_end = tl * all_stages;
+    const int64_t flat = part_lo + tl;
+    const int vec = GATHER ? (int)(flat / a.tiles) : 0;
+    const int64_t first = (flat - (int64_t)vec * a.tiles) * kRowsWarp;
+    c_rows = (int)min((int64_t)kRowsWarp, count - first);
+    const uint8_t* src = a.codes + a.k_lo / 2 + (c_stage * SB * 4 + c_chunk) * 16;
 #pragma unroll
-    for (int j = 0; j < CPY; ++j)
-      c_src[j] = src + (GATHER ? (int64_t)c_id[j] : (int64_t)c_tile * kRowsWarp + j * CR + c_row) *
-                           row_bytes;
+    for (int j = 0; j < CPY; ++j) {
+      const int64_t i = first + j * CR + c_row;
+      c_src[j] = src + (GATHER ? (int64_t)row_id(vec, i) : i) * row_bytes;
+    }
   };
   auto copy_stage = [&]() {
-    if (c_unit < u_hi) {
+    if (c_stage < c_last) {
       const uint32_t slot_at = c_slot * (SB * 2048);
       if (c_rows == kRowsWarp && (c_stage + 1) * SB * kBlockK <= kd) {
 #pragma unroll
@@ -288,33 +290,20 @@ q4_kernel(Q4Launch a, int* err) {
       }
 #pragma unroll
       for (int j = 0; j < CPY; ++j) c_src[j] += SB * (kBlockK / 2);
-      if (++c_stage == s_hi) {
-        c_stage = s_lo;
-        ++c_unit;
-        if (++c_rem == per_vec) {
-          c_rem = 0;
-          ++c_vec;
-        }
-        c_tile = c_rem * teams + slot;
-        copy_tile();
-      }
+      if (++c_stage == c_last) copy_tile();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     c_slot = c_slot + 1 == NS ? 0 : c_slot + 1;
   };
-  copy_tile();
-#pragma unroll
-  for (int i = 0; i < NS - 1; ++i) copy_stage();
-
   // ---- h, laid out as the codes unpack, in fp16: values are first scaled by
   // the power of two that takes the vector's largest to 2^14..2^15, which keeps
   // all bits of those down to 2^-25 of the largest, and 2^-36 of it throughout;
-  // the pairs that meet 2^-18 c are divided by 16. A warp takes a vector, or
-  // all of them the one.
-  auto lay_out = [&](int vec0) {
+  // the pairs that meet 2^-18 c are divided by 16. A warp takes a vector, in the
+  // gather all of them one after the other.
+  auto lay_out = [&](int vec0, int vecs) {
     const int words = blocks * 16;
     const int lanes = GATHER ? WARPS * 32 : 32, me = GATHER ? tid : lane;
-    for (int v = GATHER ? 0 : warp; v < nv; v += GATHER ? 1 : WARPS) {
+    for (int v = GATHER ? 0 : warp; v < vecs; v += GATHER ? 1 : WARPS) {
       const uint16_t* src = a.h + (size_t)(vec0 + v) * a.d + a.k_lo;
       unsigned char* dst = hs + (size_t)v * stride;
       uint32_t top = 0;  // the order of magnitudes is that of their bits
@@ -333,11 +322,12 @@ q4_kernel(Q4Launch a, int* err) {
         cta_sync();
 #pragma unroll
         for (int i = 0; i < WARPS; ++i) top = max(top, sh_top[i]);
+        cta_sync();
       }
       const int e = (int)(top >> 23) - 127;  // floor of its logarithm
       const int k = top == 0 ? 0 : max(-126, min(126, 14 - e));
       const float scale = __uint_as_float((uint32_t)(127 + k) << 23), sixteenth = scale * 0.0625f;
-      if (me == 0) sh_back[GATHER ? vec0 & 1 : v] = __uint_as_float((uint32_t)(127 - k) << 23);
+      if (me == 0) sh_back[v] = __uint_as_float((uint32_t)(127 - k) << 23);
       for (int w = me; w < words; w += lanes) {
         const int b = w >> 4, p = w & 15, at = b * 16 + word_of<G>(p & 3, p >> 2);
         uint4 x = make_uint4(0, 0, 0, 0);
@@ -362,7 +352,7 @@ q4_kernel(Q4Launch a, int* err) {
       for (int e = tid; e < blocks * GB * HC; e += WARPS * 32) {
         const int v = e % HC, gi = e / HC, b = gi / GB, q = gi - b * GB;
         float even = 0.f, odd = 0.f;
-        if (v < nv) {
+        if (v < vecs) {
           const unsigned char* src = hs + (size_t)v * stride + b * 256 + q * (256 / GB);
 #pragma unroll
           for (int w = 0; w < 16 / GB; ++w) {
@@ -378,13 +368,12 @@ q4_kernel(Q4Launch a, int* err) {
       cta_sync();
     }
   };
-  if (!GATHER) lay_out(0);
-
   // This lane's vector columns (columns past the last repeat it and are not
   // stored) and its places in a stage: row g, with rows g + 8 r 512 bytes apart.
   const unsigned char* hp[NT];
+  if (!GATHER)
 #pragma unroll
-  for (int y = 0; y < NT; ++y) hp[y] = hs + (size_t)min(y * 8 + g, nv - 1) * stride + t * 16;
+    for (int y = 0; y < NT; ++y) hp[y] = hs + (size_t)min(y * 8 + g, nv - 1) * stride + t * 16;
   constexpr int SC = SB * GB;  // scales of a row and stage
   // Scales of 8 groups are 16 bytes where the rows allow it. With two vector
   // tiles a lane loads those of one row (g + 8 t) for 8 / SC stages and hands
@@ -397,24 +386,66 @@ q4_kernel(Q4Launch a, int* err) {
   constexpr int ALIGN = CHUNKS ? 8 : SC;
   const bool whole = row_groups % ALIGN == 0 && a.scales_aligned && (a.k_lo / G) % ALIGN == 0;
   const int groups = kd / G;
-  int use = 0, turn = 0;  // ring slot; which of the partial sums
-  int vec = (int)(u_lo / per_vec), rem = (int)(u_lo - (int64_t)vec * per_vec);
-  for (int64_t unit = u_lo; unit < u_hi; ++unit) {
-    if (GATHER && (unit == u_lo || rem == 0)) {
-      if (a.split == 1) cta_sync();  // the last vector is read no more
-      lay_out(vec);
-    }
-    const int tile = rem * teams + slot;
-    const bool on = tile < a.tiles;
-    const int64_t first = (int64_t)tile * kRowsWarp;
-    float2 acc[2][NT][2];  // columns 2 t and 2 t + 1 of rows g + 16 x + 8 z
+  // the sums of tile `flat` to where they belong
+  auto put = [&](int64_t flat, const float2 (&acc)[2][NT][2]) {
+    const int vec = GATHER ? (int)(flat / a.tiles) : 0;
+    const int64_t first = (flat - (int64_t)vec * a.tiles) * kRowsWarp;
+    const int vec0 = GATHER ? (int)(part_lo / a.tiles) : 0;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int y = 0; y < NT; ++y)
 #pragma unroll
-        for (int z = 0; z < 2; ++z) acc[x][y][z] = make_float2(0.f, 0.f);
-    if (on) {
+        for (int z = 0; z < 4; ++z) {
+          const int64_t i = first + 16 * x + g + 8 * (z >> 1);
+          const int col = y * 8 + 2 * t + (z & 1);
+          if (i >= count || col >= (GATHER ? 1 : nv)) continue;
+          float* o = a.out + (size_t)(GATHER ? vec : col) * a.ldo + i;
+          float v = (z & 1 ? acc[x][y][z >> 1].y : acc[x][y][z >> 1].x) * 4194304.f *
+                    sh_back[GATHER ? vec - vec0 : col];
+          if (a.add) v += *o;
+          if (GATHER) {
+            const int32_t id = a.ids[(size_t)vec * a.K + i];
+            if (id < 0 || id >= a.n) {
+              record_error(err, kDevErrBadId);
+              v = __int_as_float(0x7fc00000);
+            }
+          }
+          *o = v;
+        }
+  };
+  constexpr int PER_LANE = 2 * NT * 2;  // pairs of sums
+  float2* left = reinterpret_cast<float2*>(part) + lane;  // [warp][pair][lane]
+  while (part_lo < run_hi) {
+    int64_t part_hi = run_hi;
+    const int vec0 = GATHER ? (int)(part_lo / a.tiles) : 0;
+    if (GATHER) part_hi = min(run_hi, (int64_t)(vec0 + kGatherVecs) * a.tiles);
+    mine_lo = share_of(warp, part_hi - part_lo);
+    mine_hi = share_of(warp + 1, part_hi - part_lo);
+    if (part_lo > run_lo) cta_sync();  // what the part before had laid out is read no more
+    c_end = mine_hi;
+    c_slot = 0;
+    copy_tile();
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i) copy_stage();
+    lay_out(vec0, GATHER ? (int)((part_hi - 1) / a.tiles) - vec0 + 1 : nv);
+    int use = 0;  // ring slot
+    int64_t waits = -1;  // the tile whose earlier stages other warps have
+    float2 acc[2][NT][2];  // columns 2 t and 2 t + 1 of rows g + 16 x + 8 z
+    for (int end = mine_hi; end > mine_lo;) {
+      const int tl = (end - 1) / all_stages;
+      const int s_lo = max(0, mine_lo - tl * all_stages), s_hi = end - tl * all_stages;
+      end = tl * all_stages;
+      const int64_t flat = part_lo + tl;
+      const int vec = GATHER ? (int)(flat / a.tiles) : 0;
+      const int64_t first = (flat - (int64_t)vec * a.tiles) * kRowsWarp;
+      if (GATHER) hp[0] = hs + (size_t)(vec - vec0) * stride + t * 16;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < NT; ++y)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) acc[x][y][z] = make_float2(0.f, 0.f);
       // scales of this lane's rows g, g + 8, g + 16, g + 24: one stage ahead, or
       // in chunks one chunk ahead
       const uint16_t *sp[4] = {}, *op[4] = {};
@@ -545,7 +576,7 @@ q4_kernel(Q4Launch a, int* err) {
             for (int y = 0; y < NT; ++y) {
               float2 H = make_float2(0.f, 0.f);
               if (SUMS) {
-                const float* hq = Hs + (b * GB + q) * HC + (GATHER ? 0 : y * 8 + 2 * t);
+                const float* hq = Hs + (b * GB + q) * HC + (GATHER ? vec - vec0 : y * 8 + 2 * t);
                 H = GATHER ? make_float2(hq[0], 0.f) : *reinterpret_cast<const float2*>(hq);
               }
 #pragma unroll
@@ -563,58 +594,44 @@ q4_kernel(Q4Launch a, int* err) {
         }
         __syncwarp();  // the next copy may overwrite what was read here
       }
-    }
-    const int tile_vec = vec;
-    if (++rem == per_vec) {
-      rem = 0;
-      ++vec;
-    }
-    if (a.split > 1) {
-      // the tile's other warps hand their sums over in shared memory, and its
-      // first one adds them in their order, while the others go on
-      constexpr int PER = 2 * NT * 2;
-      float2* mine = reinterpret_cast<float2*>(part) + (size_t)(turn * WARPS + warp) * PER * 32 + lane;
-      turn ^= 1;
-      if (k_warp > 0) {
+      if (s_hi < all_stages) {
 #pragma unroll
-        for (int e = 0; e < PER; ++e) mine[e * 32] = acc[e / (NT * 2)][e / 2 % NT][e % 2];
+        for (int e = 0; e < PER_LANE; ++e)
+          left[(warp * PER_LANE + e) * 32] = acc[e / (NT * 2)][e / 2 % NT][e % 2];
+      } else if (s_lo > 0) {
+        waits = flat;
+      } else {
+        put(flat, acc);
       }
+    }
+    if (a.share) {
       cta_sync();
-      if (k_warp == 0) {
-        for (int o = 1; o < a.split; ++o) {
+      if (waits >= 0) {
+        // the earlier warps' sums in their order, then this one's
+        const int begin = (int)(waits - part_lo) * all_stages;
+        float2 sum[2][NT][2] = {};
+        for (int o = 0; o < warp; ++o) {
+          const int lo = share_of(o, part_hi - part_lo), hi = share_of(o + 1, part_hi - part_lo);
+          if (lo == hi || hi <= begin) continue;
 #pragma unroll
-          for (int e = 0; e < PER; ++e) {
-            const float2 v = mine[(o * PER + e) * 32];
-            float2& d = acc[e / (NT * 2)][e / 2 % NT][e % 2];
+          for (int e = 0; e < PER_LANE; ++e) {
+            const float2 v = left[(o * PER_LANE + e) * 32];
+            float2& d = sum[e / (NT * 2)][e / 2 % NT][e % 2];
             d.x += v.x;
             d.y += v.y;
           }
         }
+#pragma unroll
+        for (int e = 0; e < PER_LANE; ++e) {
+          float2& d = acc[e / (NT * 2)][e / 2 % NT][e % 2];
+          const float2 v = sum[e / (NT * 2)][e / 2 % NT][e % 2];
+          d.x = v.x + d.x;
+          d.y = v.y + d.y;
+        }
+        put(waits, acc);
       }
     }
-    if (!on || k_warp != 0) continue;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int y = 0; y < NT; ++y)
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const int64_t i = first + 16 * x + g + 8 * (z >> 1);
-          const int col = y * 8 + 2 * t + (z & 1);
-          if (i >= count || col >= nv) continue;
-          float* o = a.out + (size_t)(GATHER ? tile_vec : col) * a.ldo + i;
-          float v = (z & 1 ? acc[x][y][z >> 1].y : acc[x][y][z >> 1].x) * 4194304.f *
-                    sh_back[GATHER ? tile_vec & 1 : col];
-          if (a.add) v += *o;
-          if (GATHER) {
-            const int32_t id = a.ids[(size_t)tile_vec * a.K + i];
-            if (id < 0 || id >= a.n) {
-              record_error(err, kDevErrBadId);
-              v = __int_as_float(0x7fc00000);
-            }
-          }
-          *o = v;
-        }
+    part_lo = part_hi;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -632,11 +649,11 @@ constexpr Form form_of(int nt, int group, bool gather) {
                  : Form{1, gather ? 8 : 16, group == 32 ? 1 : 2, group == 32 ? 4 : 2};
 }
 
-size_t smem_bytes(const Form& f, int kd, int group, int vecs, int cols, bool split) {
+size_t smem_bytes(const Form& f, int kd, int group, int vecs, int cols, bool share) {
   const int blocks = (kd + kBlockK - 1) / kBlockK;
   return (size_t)h_bytes(blocks, vecs, blocks * (kBlockK / group) * cols) +
          (size_t)f.warps * f.ns * f.sb * 2048 +
-         (split ? (size_t)2 * f.warps * f.nt * 8 * 32 * sizeof(float) : 0);
+         (share ? (size_t)f.warps * f.nt * 8 * 32 * sizeof(float) : 0);
 }
 
 template <bool BF16, int G, int NT, int MODE, bool GATHER>
@@ -644,34 +661,24 @@ cudaError_t launch_one(const Q4Launch& in, int* err, cudaStream_t s) {
   constexpr Form f = form_of(NT, G, GATHER);
   auto kernel = q4_kernel<BF16, G, NT, f.warps, f.sb, f.ns, MODE, GATHER>;
   Q4Launch a = in;
-  const int kd = a.k_hi - a.k_lo, vecs = GATHER ? 1 : (a.M < NT * 8 ? a.M : NT * 8);
-  const int cols = GATHER ? 1 : NT * 8;
+  const int kd = a.k_hi - a.k_lo;
+  const int vecs = GATHER ? kGatherVecs : a.M < NT * 8 ? a.M : NT * 8;
+  const int cols = GATHER ? kGatherVecs : NT * 8;
   const int64_t rows = GATHER ? a.K : a.n;
   a.tiles = (int)((rows + kRowsWarp - 1) / kRowsWarp);
-  const int stages = ((kd + kBlockK - 1) / kBlockK + f.sb - 1) / f.sb;
-  const size_t most = smem_bytes(f, kd, G, vecs, cols, true);
-  const int resident = sm_count() * (f.warps == 8 && 2 * (most + 1024) <= 228 * 1024 ? 2 : 1);
-  // How many warps share a tile: whole tiles leave warps idle in the last round,
-  // and a CTA's longest run of units sets the time; a unit of s-shares takes
-  // 1/s of the time of a tile (plus the join, so it must gain a twentieth).
-  const int64_t vectors = GATHER ? a.M : 1;
-  a.split = 1;
-  double best = 1e300;
-  for (int x = 1; x <= f.warps && x <= stages && f.warps % x == 0; x *= 2) {
-    if (x > 1 && most > kSmemMost) break;
-    const int64_t teams = f.warps / x, units = (a.tiles + teams - 1) / teams * vectors;
-    const double time = (double)((units + resident - 1) / resident) / x;
-    if (time < 0.95 * best) {
-      best = time;
-      a.split = x;
-    }
-  }
-  const size_t smem = smem_bytes(f, kd, G, vecs, cols, a.split > 1);
+  const int64_t tiles = (int64_t)a.tiles * (GATHER ? a.M : 1);
+  // tiles are shared where the sums that this hands round fit beside the rest
+  // (all but the widest rows with many vectors); a run of tiles counts its
+  // stages in 32 bits
+  size_t smem = smem_bytes(f, kd, G, vecs, cols, true);
+  a.share = smem <= kSmemMost;
+  if (!a.share) smem = smem_bytes(f, kd, G, vecs, cols, false);
   static int smem_set[64] = {0};
   cudaError_t e = ensure_dynamic_smem(kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
-  const int64_t teams = f.warps / a.split, units = (a.tiles + teams - 1) / teams * vectors;
-  return launch_kernel(true, kernel, dim3((unsigned)(units < resident ? units : resident)),
+  const int resident = sm_count() * (f.warps == 8 && 2 * (smem + 1024) <= 228 * 1024 ? 2 : 1);
+  const int64_t want = a.share ? tiles : (tiles + f.warps - 1) / f.warps;
+  return launch_kernel(true, kernel, dim3((unsigned)(want < resident ? want : resident)),
                        dim3(f.warps * 32), smem, s, a, err);
 }
 
@@ -718,7 +725,7 @@ cudaError_t launch_q4(const Q4Args& q, int* err, cudaStream_t s) {
     a.h = static_cast<const uint16_t*>(q.h) + (size_t)m * q.d;
     a.out = q.out + (size_t)m * a.ldo;
     const Form f = form_of(!q.ids && a.M > 8 ? 2 : 1, q.group, q.ids != nullptr);
-    const int vecs = q.ids ? 1 : a.M, cols = q.ids ? 1 : f.nt * 8;
+    const int vecs = q.ids ? kGatherVecs : a.M, cols = q.ids ? kGatherVecs : f.nt * 8;
     int piece = q.d;
     while (smem_bytes(f, piece, q.group, vecs, cols, false) > kSmemMost)
       piece = ((piece + 1) / 2 + kBlockK - 1) / kBlockK * kBlockK;
