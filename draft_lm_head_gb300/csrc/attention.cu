@@ -596,8 +596,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         record_error(err, kDevErrTimeout);
       }
       __syncwarp();
-      if (*abort_flag && lane == 0) {
-        // drain (bounded) the copies issued last on every stage
+      if (lane == 0) {
+        // no copy may be under way when the CTA ends, whichever role gave up
+        // (bounded; in a run that did not, all of them are long done)
         const uint32_t first = n > (uint32_t)NS ? n - NS : 0;
         for (uint32_t j = first; j < n; ++j) {
           const long long t0 = clock64();
@@ -710,11 +711,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         blocks += nb;
       }
-      if (!ok && issuer) {
+      if (!ok && lane == 0) {
         *abort_flag = 1;
         record_error(err, kDevErrTimeout);
-        tc::mma_drain(&ctl.drain);  // TMEM is freed below
       }
+      if (issuer) tc::mma_drain(&ctl.drain);  // TMEM is freed below
       __syncwarp();
     }
   } else {

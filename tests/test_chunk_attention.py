@@ -202,6 +202,55 @@ def test_scales(scale):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", ["rising", "falling", "late", "spikes"])
+def test_scores_that_outgrow_the_reference(shape, D, dtype):
+    """Scores along one direction that climb by far more than the softmax's
+    reference allows, between blocks and within them, for one tile and for two."""
+    import torch
+    from gpu_util import lib
+    c = _case([700, 0, 90], [1, 300, 40], 4, 1, D, 32, dtype, 3)
+    T, t = c["q"].shape[0], c["q"].dtype
+    u = torch.ones(D, device="cuda") / 4
+    qkv = torch.cat([(u * 2).expand(T, 4, D).to(t), c["k"], c["v"]], 1)
+    a = torch.arange(1024, device="cuda", dtype=torch.float32)
+    a = {"rising": a / 8, "falling": 80 - a / 8, "late": 60.0 * (a % 128 >= 100) + a / 16,
+         "spikes": 90.0 * (a % 150 == 77) * (1 + a / 400)}[shape]
+    # position j of every request has the key a_j u (and some of the direction's noise)
+    key = (a[:, None] * u + 0.05 * torch.randn(1024, D, device="cuda", generator=torch.Generator("cuda").manual_seed(1))).to(t)
+    lens, cu = c["lens"].tolist(), c["cu"].tolist()
+    for s, l in enumerate(lens):
+        m = cu[s + 1] - cu[s]
+        j = torch.arange(l, device="cuda")
+        slot = (c["table"][s].long()[j // 32] * 32 + j % 32)
+        c["kc"].view(-1, 1, D)[slot, 0] = key[:l]
+        qkv[cu[s]:cu[s + 1], 4] = key[l:l + m]
+    c.update(q=qkv[:, :4], k=qkv[:, 4:5], v=qkv[:, 5:])
+    _check(lib(), c, dtype)
+
+
+@pytest.mark.gpu
+def test_waits_that_run_out():
+    """With no time to wait the kernel gives up, says so and leaves the GPU as it
+    was: the next call is right."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    c = _case([300, 1000], [3, 200], 8, 2, 128, 32, "bfloat16", 5)
+    want, _ = _check(L, c, "bfloat16")
+    before = L.debug_set_wait_cycles(0)
+    try:
+        L.chunk_attention(c["q"], c["kc"], c["vc"], c["table"], c["lens"], c["cu"])
+        assert L.last_device_error() == -8
+    finally:
+        L.debug_set_wait_cycles(-1)
+    assert before > 0
+    assert torch.equal(L.chunk_attention(c["q"], c["kc"], c["vc"], c["table"], c["lens"], c["cu"]), want)
+    assert L.last_device_error() == 0
+
+
+@pytest.mark.gpu
 def test_other_cache_orders_and_streams():
     """Heads before tokens in a page, a cache that is part of a larger one, no
     new K and V (already cached), another stream."""

@@ -148,6 +148,45 @@ def test_wide_rows(M, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,scale", [("bfloat16", 1e-30), ("bfloat16", 1e30), ("float16", 1e-4), ("float16", 1e4),
+                                         ("bfloat16", 0.0)])
+@pytest.mark.parametrize("mins", [False, True])
+def test_hidden_vectors_of_any_size(dtype, scale, mins):
+    """Large, small and zero vectors, and elements far apart within one: they are
+    held relative to a vector's largest, to 2^-36 of it at least."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    codes, scales, off, h = _inputs(300, 512, 64, 5, dtype, mins, 4)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    e = torch.randint(-25, 1, h.shape, generator=g, device="cuda").float()
+    h = (h.float() * torch.exp2(e) * scale).to(h.dtype)
+    got = L.q4_head(codes, scales, h, 64, mins=off).double().cpu().numpy()
+    want, tol = _exact(codes, scales, off, h, 64)
+    rest = np.abs(SO.q4_rows(codes.cpu().numpy(), scales.double().cpu().numpy(),
+                             None if off is None else off.double().cpu().numpy(), 64)).sum(1)
+    tol = tol + 2.0 ** -36 * h.double().abs().amax(1).cpu().numpy()[:, None] * rest
+    assert np.all(np.abs(got - want) <= tol)
+    ids = torch.arange(300, device="cuda", dtype=torch.int32).repeat(5, 1)
+    got = L.q4_gather_logits(codes, scales, h, ids, 64, mins=off).double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K", [(7, 1), (3, 33), (40, 65), (1, 3000)])
+def test_gather_of_few_and_many(M, K):
+    """Runs of tiles over several hidden vectors, one tile, and many."""
+    import torch
+    from gpu_util import lib
+    codes, scales, off, h = _inputs(1000, 1024, 128, M, "bfloat16", False, M)
+    ids = torch.randint(0, 1000, (M, K), device="cuda", dtype=torch.int32, generator=torch.Generator("cuda").manual_seed(K))
+    got = lib().q4_gather_logits(codes, scales, h, ids, 128).double().cpu().numpy()
+    want, tol = _exact(codes, scales, off, h, 128)
+    at = ids.long().cpu().numpy()
+    assert np.all(np.abs(got - np.take_along_axis(want, at, 1)) <= np.take_along_axis(tol, at, 1))
+
+
+@pytest.mark.gpu
 def test_bad_ids_streams_and_refusals():
     import torch
     from gpu_util import lib
