@@ -21,12 +21,17 @@
 //             scores into weights. With two row tiles each warpgroup has its
 //             own and both use every block; with one tile they take blocks in
 //             turn and join at the end, so the tensor cores work on one while
-//             the other is exponentiated;
-//             Of an item that was cut between CTAs each leaves its piece in the
-//             scratch, and the warp that brings the last one of its rows joins
-//             them, in the order of the pieces.
+//             the other is exponentiated. Of an item that was cut between
+//             CTAs each leaves its piece in the scratch, and the warp that
+//             brings the last one of its rows joins them, in the order of the
+//             pieces.
 // Bound: few rows, by reading K and V once; many rows, by the tensor cores.
-//
+// Measured (whole call, both launches): 32 requests of 4000-8000 cached tokens
+// and one new each, 32 heads over 8, dim 128: 134 us for 824 MB (6.1 TB/s); two
+// chunks of 2048 tokens over 6144 cached: 350-365 us for 0.48 TFLOP (1.32-1.38
+// PFLOP/s; the tensor pipe is busy 58 % of the time). The rest is the softmax: a
+// warpgroup's exponentials and packing of a block take longer than the other
+// one's MMAs, and each block is handed over through barriers twice.
 // The softmax runs in the base-2 domain with a running reference instead of
 // the running maximum: a row's first block with a key sets it, and it moves only
 // when weights pass 2^9 or so, which their sum shows; a block's maximum is not
@@ -291,16 +296,15 @@ struct Cursor {
     return (int)(((u + 1) * parts + units - 1) / units) - 1;
   }
   __device__ void init(const Scratch& sc, int cta) {
-    const Header* head = sc.head;
-    items = sc.items;
-    parts = head->parts;
-    left = 0;
-    if (cta >= parts) return;
-    units = head->units;
-    per_head = head->per_head;
-    left = start_of(cta + 1) - start_of(cta);
-    n_items = head->items;
+    // all under way before any is looked at (every CTA has a place in `start`)
+    const Header head = *sc.head;
     const int4 st = sc.start[cta];
+    items = sc.items;
+    parts = head.parts;
+    units = head.units;
+    per_head = head.per_head;
+    n_items = head.items;
+    left = cta < parts ? start_of(cta + 1) - start_of(cta) : 0;
     idx = st.x;
     hk = st.y;
     off = st.z;

@@ -12,6 +12,9 @@
 //   beam_merge: a CTA per sequence turns the slices' sums into lse and picks
 //     the k best of beams x slices x k scored entries.
 //   beam_small: both in one launch where a sequence has few slices.
+// Measured: 512 rows of 151936 fp32 logits, k = 8: 67 us for the scan (4.6 TB/s;
+// torch's row maximum alone takes 62), 10 for the merge; with the reordering of
+// 512 states 76 us in all.
 // Bound by reading the logits once. Beams meet at the border of the k with gaps
 // below 32-bit rounding, so a lane's sums of exp are 32-bit, but everything
 // across lanes, and the scores of the few candidates, are pairs of fp32 numbers

@@ -22,6 +22,9 @@
 // (Operands of the tcgen05 instructions would have to be written to shared or
 // tensor memory first, at a store per two codes; here they never leave
 // registers.)
+// Measured: 128256 rows of 4096 codes, groups of 128: 54 us for one hidden vector
+// (5.1 TB/s of codes and scales, at 1.8 instructions a cycle and SM), 1002 candidate rows for each of 64 vectors 33 us;
+// 151936 rows of 5120, groups of 64 with mins, 16 vectors: 123 us.
 //   The matrix instructions cut the products of a sum at a place set by the
 // largest. With codes up to 15 in place of -8..7 a symmetric row's sums lose
 // about two bits more; over long rows that stays near 2^-21 of the result, in

@@ -378,7 +378,9 @@ int lmhead_shard_softmax(const float* all_stats, int G, const float* logits, int
  * have no counterpart to them beyond the steps they name ("EAGLE -> EAGLE-2
  * -> EAGLE-3 -> DFlash": the drafter's layer attends over the accepted prefix
  * and the draft tree; Expansion Phase: the best nodes of a layer are
- * expanded). Conventions as above; sizes and errors as said at each.
+ * expanded). Conventions as above; sizes and errors as said at each. int32 and
+ * fp32 arrays need no more than 4-byte alignment here; what is read 16 bytes at
+ * a time says so.
  *
  * Page plan: block tables and slot maps of a step's new tokens, from the
  * requests' lengths.
@@ -426,8 +428,8 @@ int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_
  *   k_cache, v_cache  pages x page_size x kv_heads x dim; *c_page, *c_token,
  *             *c_head: strides in elements, any order. page_size 16, 32, 64,
  *             128 or 256. Bases 16-byte aligned, strides multiples of 8.
- *   table, lens, cu  as of lmhead_page_plan: pages (S x width), tokens cached
- *             before the chunk, starts of the requests' tokens (S + 1).
+ *   table, lens, cu  as of lmhead_page_plan: pages (S x width, S <= 65536), tokens
+ *             cached before the chunk, starts of the requests' tokens (S + 1).
  *   slots     T int32 (only with k and v): where each token goes, negative:
  *             nowhere.
  *   tree      NULL: token i of a request sees the keys at positions <= len + i,
