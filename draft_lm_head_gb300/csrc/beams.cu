@@ -5,16 +5,16 @@
 // score(b, j) = parent_b + (x_bj - lse_b), lse_b = log sum_j exp x_bj. Within a
 // row the order of the scores is the order of x, so one pass over a row gives
 // both its log-sum-exp and its k largest x; only those few are ever scored.
-//   beam_rows:  a warp streams one slice of one row through registers (16
-//     values a lane a tile, the next tile's loads in flight), keeping a running
-//     reference and sum of the softmax and the slice's k best so far; no
-//     barrier, and past the first tile little but the exponentials.
+//   beam_rows:  a warp streams one slice of one row through a ring of shared
+//     memory (16 values a lane a tile, several tiles' copies in flight), keeping
+//     a running reference and sum of the softmax and the slice's k best so far;
+//     no barrier, and past the first tile little but the exponentials.
 //   beam_merge: a CTA per sequence turns the slices' sums into lse and picks
 //     the k best of beams x slices x k scored entries.
 //   beam_small: both in one launch where a sequence has few slices.
-// Measured: 512 rows of 151936 fp32 logits, k = 8: 67 us for the scan (4.6 TB/s;
-// torch's row maximum alone takes 62), 10 for the merge; with the reordering of
-// 512 states 76 us in all.
+// Measured: 64 sequences x 8 rows of 151936 fp32 logits, k = 8, with the
+// reordering of the 512 states: 64 us, 4.9 TB/s (torch's maximum of those rows
+// alone takes 62).
 // Bound by reading the logits once. Beams meet at the border of the k with gaps
 // below 32-bit rounding, so a lane's sums of exp are 32-bit, but everything
 // across lanes, and the scores of the few candidates, are pairs of fp32 numbers
@@ -33,6 +33,11 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kPerLane = 16;
 constexpr int kTile = 32 * kPerLane;  // entries of a warp's tile
+// A warp's ring of tiles, and the warps an SM has room for by it: 144 KB of an
+// SM's copies in flight. (4, 6 and 12 KB with 32, 32 and 16 warps: 64 x 8 rows of
+// 151936 69, 68 and 65 us in all against 64; loads to registers, a tile ahead: 77.)
+constexpr int kRing = 8192, kWarpsSm = 24;
+constexpr int kRowsSmem = kRowThreads / 32 * kRing;
 constexpr int kBuf = 1024;            // the merge's candidates
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
@@ -152,34 +157,49 @@ __device__ __forceinline__ float kth_of_threads(float mine, int k, float* sh, fl
   return *out;
 }
 
-// Slice sl of the row at x, by one warp.
+// Slice sl of the row at x, by one warp. Tiles are copied to the warp's ring
+// several ahead; a lane reads back what it copied itself, so its own waits are
+// all there is, and a stage is filled again an iteration after it was read.
 template <typename T>
 __device__ __forceinline__ void scan_slice(const T* x, int n, int sl, int slice_len, int k,
-                                           Slice* slice, float* best_v, int32_t* best_i) {
+                                           char* ring, Slice* slice, float* best_v,
+                                           int32_t* best_i) {
   const int lane = threadIdx.x & 31;
+  constexpr int kStage = kTile * (int)sizeof(T), kStages = kRing / kStage;
   constexpr int V = Elem<T>::kVec, U = kPerLane / V;
   // 16-byte reads at 16-byte boundaries: the row starts `off` entries after
   // one, and slices are cut at them
   const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
   const int lo = max(0, sl * slice_len - off), hi = min(n, (sl + 1) * slice_len - off);
   auto inside = [&](int base) { return base * V - off >= lo && base * V - off + kTile <= hi; };
-  auto load = [&](int base, uint4 (&raw)[U]) {  // of a tile that lies within the slice
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16;
+  auto fetch = [&](int base, int stage) {
     if (inside(base))
 #pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = ldg_nc_v4(x + (base + u * 32 + lane) * V - off);
+      for (int u = 0; u < U; ++u)
+        asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(
+                         mine + stage * kStage + u * 512),
+                     "l"(x + (base + u * 32 + lane) * V - off)
+                     : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   float m = kNegInf;
   float2 s2 = make_float2(0.f, 0.f);
   uint64_t best = 0;        // lane j: the (j + 1)-th best entry so far, 0 for none
   float floor_v = kNegInf;  // the k-th of them
   int base = sl * (slice_len / V);
-  uint4 raw[U];
-  load(base, raw);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(base + i * (kTile / V), i);
+  int stage = 0, last = kStages - 1;
   for (; base * V - off < hi; base += kTile / V) {
     float f[kPerLane];
+    fetch(base + (kStages - 1) * (kTile / V), last);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     if (inside(base)) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) Elem<T>::unpack(raw[u], f + u * V);
+      for (int u = 0; u < U; ++u)
+        Elem<T>::unpack(*reinterpret_cast<const uint4*>(ring + stage * kStage + u * 512 + lane * 16),
+                        f + u * V);
     } else {
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) {
@@ -187,7 +207,8 @@ __device__ __forceinline__ void scan_slice(const T* x, int n, int sl, int slice_
         f[i] = e >= lo && e < hi ? Elem<T>::get(x + e) : kNegInf;
       }
     }
-    load(base + kTile / V, raw);
+    last = stage;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
     float tm = f[0];
 #pragma unroll
     for (int i = 1; i < kPerLane; ++i) tm = fmaxf(tm, f[i]);
@@ -250,16 +271,18 @@ __device__ __forceinline__ void scan_slice(const T* x, int n, int sl, int slice_
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 4)
+__global__ void __launch_bounds__(kRowThreads, kWarpsSm * 32 / kRowThreads)
 beam_rows_kernel(const T* logits, int64_t stride, int n, int rows, int nsl, int slice_len, int k,
                  const uint8_t* finished, Slice* slices, float* best_v, int32_t* best_i) {
+  extern __shared__ __align__(16) char rings[];
   pdl_wait();
   pdl_trigger();
   const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
   if (unit >= (int64_t)rows * nsl) return;
   const int row = (int)(unit / nsl), sl = (int)(unit - (int64_t)row * nsl);
   if (finished && finished[row]) return;  // its one entry is its own score
-  scan_slice(logits + (int64_t)row * stride, n, sl, slice_len, k, slices + unit, best_v + unit * k,
+  scan_slice(logits + (int64_t)row * stride, n, sl, slice_len, k,
+             rings + (threadIdx.x >> 5) * kRing, slices + unit, best_v + unit * k,
              best_i + unit * k);
 }
 
@@ -472,6 +495,7 @@ beam_small_kernel(const T* logits, BeamArgs a, int nsl, int slice_len) {
   __shared__ Slice slices[kFewSlices];
   __shared__ float best_v[kFewSlices * kBeamMaxK];
   __shared__ int32_t best_i[kFewSlices * kBeamMaxK];
+  extern __shared__ __align__(16) char rings[];
   pdl_wait();
   pdl_trigger();
   for (int u = threadIdx.x >> 5; u < a.beams * nsl; u += kRowThreads / 32) {
@@ -479,7 +503,7 @@ beam_small_kernel(const T* logits, BeamArgs a, int nsl, int slice_len) {
     const size_t row = (size_t)blockIdx.x * a.beams + b;
     if (a.finished && a.finished[row]) continue;
     scan_slice(logits + (int64_t)row * a.row_stride, (int)a.n, u - b * nsl, slice_len, a.k,
-               slices + u, best_v + u * a.k, best_i + u * a.k);
+               rings + (threadIdx.x >> 5) * kRing, slices + u, best_v + u * a.k, best_i + u * a.k);
   }
   cta_sync();
   merge_sequence(a, blockIdx.x, nsl, slices, best_v, best_i);
@@ -517,11 +541,11 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(ReorderArgs a, int* e
 }
 
 // Entries of a row per warp: whole tiles, as many slices as leave every warp
-// slot of the GPU (32 an SM at the kernel's registers) one of them.
+// slot of the GPU one of them.
 int slice_len(int rows, int64_t n) {
   const int64_t tiles = (n + kTile - 1) / kTile;
   const int sms = sm_count() > 0 ? sm_count() : 1;
-  int64_t want = (int64_t)sms * 32 / rows;
+  int64_t want = (int64_t)sms * kWarpsSm / rows;
   if (want < 1) want = 1;
   const int64_t per = tiles <= want ? 1 : (tiles + want - 1) / want;
   return (int)(per * kTile);
@@ -549,9 +573,16 @@ cudaError_t launch_beam_select(const BeamArgs& a, void* scratch, cudaStream_t s)
   const bool few = a.beams * nsl <= kFewSlices;
   auto scan = [&](auto* logits) -> cudaError_t {
     using T = std::remove_cv_t<std::remove_pointer_t<decltype(logits)>>;
-    if (few)
-      return launch_kernel(true, beam_small_kernel<T>, dim3(a.S), block, 0, s, logits, a, nsl, len);
-    return launch_kernel(true, beam_rows_kernel<T>, grid, block, 0, s, logits, a.row_stride,
+    static int smem_small[64], smem_rows[64];
+    if (few) {
+      const cudaError_t e = ensure_dynamic_smem(beam_small_kernel<T>, kRowsSmem, smem_small);
+      if (e != cudaSuccess) return e;
+      return launch_kernel(true, beam_small_kernel<T>, dim3(a.S), block, kRowsSmem, s, logits, a, nsl,
+                           len);
+    }
+    const cudaError_t e = ensure_dynamic_smem(beam_rows_kernel<T>, kRowsSmem, smem_rows);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(true, beam_rows_kernel<T>, grid, block, kRowsSmem, s, logits, a.row_stride,
                          (int)a.n, rows, nsl, len, a.k, a.finished, sl, bv, bi);
   };
   const cudaError_t e = a.dtype == LMHEAD_FP32   ? scan(static_cast<const float*>(a.logits))
