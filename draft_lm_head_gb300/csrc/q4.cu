@@ -23,7 +23,7 @@
 // tensor memory first, at a store per two codes; here they never leave
 // registers.)
 // Measured: 128256 rows of 4096 codes, groups of 128: 54 us for one hidden vector
-// (5.1 TB/s of codes and scales, at 1.8 instructions a cycle and SM), 1002 candidate rows for each of 64 vectors 33 us;
+// (5.1 TB/s of codes and scales, at 1.8 instructions a cycle and SM), 1002 candidate rows for each of 64 vectors 31 us;
 // 151936 rows of 5120, groups of 64 with mins, 16 vectors: 123 us.
 //   The matrix instructions cut the products of a sum at a place set by the
 // largest. With codes up to 15 in place of -8..7 a symmetric row's sums lose
@@ -99,20 +99,20 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// N consecutive 16-bit values of a row.
+// N consecutive 16-bit values of a row, in shared memory or not.
 template <int N> struct Packed {
   uint32_t w[(N + 1) / 2];
 };
 template <int N> __device__ __forceinline__ Packed<N> load_whole(const uint16_t* p) {
   Packed<N> v;
   if (N == 4) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
     v.w[0] = x.x;
     v.w[(N + 1) / 2 - 1] = x.y;
   } else if (N == 2) {
-    v.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    v.w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else {
-    v.w[0] = __ldg(p);
+    v.w[0] = *p;
   }
   return v;
 }
@@ -162,8 +162,8 @@ struct Q4Launch {
   int64_t ldo;
   float* out;
   int tiles;           // row tiles (of each vector in the gather)
-  int share;           // a tile's codes may be divided between warps
   int scales_aligned;  // scales and mins at 16 bytes
+  int share;           // a tile's codes may be divided between warps
 };
 
 // Shared memory: h of the call's vectors, [vector][block][i][t] 16-byte words
@@ -195,10 +195,13 @@ __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bo
                : "memory");
 }
 
+// A warp's slot for the scales of 8 groups of 32 rows, and for the mins.
+__host__ __device__ constexpr int slot_bytes(bool mins) { return mins ? 1024 : 512; }
+
 // Hidden vectors that a CTA of the gather holds at a time.
 constexpr int kGatherVecs = 2;
 
-template <bool BF16, int G, int NT, int WARPS, int SB, int NS, int MODE, bool GATHER>
+template <bool BF16, int G, int NT, int WARPS, int SB, int NS, int MODE, bool GATHER, bool COPIED>
 __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1)
 q4_kernel(Q4Launch a, int* err) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -218,7 +221,9 @@ q4_kernel(Q4Launch a, int* err) {
   float* Hs = reinterpret_cast<float*>(smem + (size_t)nv * stride);  // [group][HC]
   unsigned char* rings = smem + h_bytes(blocks, nv, SUMS ? blocks * GB * HC : 0);
   unsigned char* ring = rings + (size_t)warp * (NS * SB * 2048);
-  float* part = reinterpret_cast<float*>(rings + (size_t)WARPS * (NS * SB * 2048));
+  constexpr int SLOT = COPIED ? slot_bytes(MINS) : 0;
+  unsigned char* slots = rings + WARPS * NS * SB * 2048 + warp * (NS * SLOT);
+  float* part = reinterpret_cast<float*>(rings + (size_t)WARPS * NS * (SB * 2048 + SLOT));
   pdl_wait();
   pdl_trigger();
   const int64_t count = GATHER ? a.K : a.n;
@@ -259,6 +264,22 @@ q4_kernel(Q4Launch a, int* err) {
     c_dst[j] = ring_s + ring_at(c_chunk >> 2, j * CR + c_row, c_chunk & 3);
   const uint8_t* c_src[CPY];
   int c_rows = 0;  // of the tile
+  // Where rows of scales allow 16-byte copies a lane copies those of 8 groups of
+  // one row along with the first stage that needs them. (Loaded to registers
+  // stage by stage, as other rows' are, they want the L1, which the rings leave
+  // little of: one vector, groups of 64 with mins 68 us, so 60.)
+  constexpr int SC = SB * GB;  // scales of a row and stage
+  constexpr int PER = 8 / SC;  // stages they last
+  int64_t c_scale = 0;  // the lane's row's first scale
+  int c_scale_slot = 0, c_first = 0;
+  auto copy_scales = [&]() {
+    const uint32_t to =
+        (uint32_t)__cvta_generic_to_shared(slots) + c_scale_slot * SLOT + lane * 16;
+    c_scale_slot = c_scale_slot + 1 == NS ? 0 : c_scale_slot + 1;
+    const int64_t at = c_scale + c_stage / PER * 8;
+    copy16(to, a.scales + at);
+    if (MINS) copy16(to + 512, a.mins + at);
+  };
   auto copy_tile = [&]() {  // on to the tile before, if this warp has stages there
     c_stage = c_last = 0;
     if (c_end <= mine_lo) return;
@@ -270,6 +291,8 @@ q4_kernel(Q4Launch a, int* err) {
     const int vec = GATHER ? (int)(flat / a.tiles) : 0;
     const int64_t first = (flat - (int64_t)vec * a.tiles) * kRowsWarp;
     c_rows = (int)min((int64_t)kRowsWarp, count - first);
+    if (COPIED) c_scale = (int64_t)row_id(vec, first + lane) * row_groups + a.k_lo / G;
+    c_first = c_stage;
     const uint8_t* src = a.codes + a.k_lo / 2 + (c_stage * SB * 4 + c_chunk) * 16;
 #pragma unroll
     for (int j = 0; j < CPY; ++j) {
@@ -291,6 +314,7 @@ q4_kernel(Q4Launch a, int* err) {
           copy16_or_zero(c_dst[j] + slot_at, there ? c_src[j] : a.codes, there);
         }
       }
+      if (COPIED && (c_stage == c_first || c_stage % PER == 0)) copy_scales();
 #pragma unroll
       for (int j = 0; j < CPY; ++j) c_src[j] += SB * (kBlockK / 2);
       if (++c_stage == c_last) copy_tile();
@@ -377,14 +401,11 @@ q4_kernel(Q4Launch a, int* err) {
   if (!GATHER)
 #pragma unroll
     for (int y = 0; y < NT; ++y) hp[y] = hs + (size_t)min(y * 8 + g, nv - 1) * stride + t * 16;
-  constexpr int SC = SB * GB;  // scales of a row and stage
-  // Scales of 8 groups are 16 bytes where the rows allow it. With two vector
-  // tiles a lane loads those of one row (g + 8 t) for 8 / SC stages and hands
-  // them round: loaded stage by stage they took as much of the L2 as the codes, a
-  // sector a row (194 against 136 us for 16 vectors over the wide head). With
-  // one there is room for the sectors in the L1 and the shuffles cost more than
-  // they save (61 against 56 us for one vector).
-  constexpr int PER = 8 / SC;
+  // From nine vectors on, where h leaves no room for slots, a lane loads the
+  // scales of 8 groups of one row (g + 8 t) for PER stages and hands them round:
+  // loaded stage by stage they took as much of the L2 as the codes, a sector a
+  // row (194 against 136 us for 16 vectors over the wide head). Rows that allow
+  // neither load theirs a stage ahead.
   constexpr bool CHUNKS = NT == 2;
   constexpr int ALIGN = CHUNKS ? 8 : SC;
   const bool whole = row_groups % ALIGN == 0 && a.scales_aligned && (a.k_lo / G) % ALIGN == 0;
@@ -427,12 +448,12 @@ q4_kernel(Q4Launch a, int* err) {
     mine_hi = share_of(warp + 1, part_hi - part_lo);
     if (part_lo > run_lo) cta_sync();  // what the part before had laid out is read no more
     c_end = mine_hi;
-    c_slot = 0;
+    c_slot = c_scale_slot = 0;
     copy_tile();
 #pragma unroll
     for (int i = 0; i < NS - 1; ++i) copy_stage();
     lay_out(vec0, GATHER ? (int)((part_hi - 1) / a.tiles) - vec0 + 1 : nv);
-    int use = 0;  // ring slot
+    int use = 0, scale_use = -1;  // ring slots
     int64_t waits = -1;  // the tile whose earlier stages other warps have
     float2 acc[2][NT][2];  // columns 2 t and 2 t + 1 of rows g + 16 x + 8 z
     for (int end = mine_hi; end > mine_lo;) {
@@ -449,8 +470,8 @@ q4_kernel(Q4Launch a, int* err) {
         for (int y = 0; y < NT; ++y)
 #pragma unroll
           for (int z = 0; z < 2; ++z) acc[x][y][z] = make_float2(0.f, 0.f);
-      // scales of this lane's rows g, g + 8, g + 16, g + 24: one stage ahead, or
-      // in chunks one chunk ahead
+      // scales of this lane's rows g, g + 8, g + 16, g + 24 where they are not
+      // copied: one stage ahead, or in chunks one chunk ahead
       const uint16_t *sp[4] = {}, *op[4] = {};
       uint4 s_now, s_next, o_now, o_next;
       Packed<SC> sc_n[4], of_n[4];
@@ -474,21 +495,23 @@ q4_kernel(Q4Launch a, int* err) {
           }
         }
       };
+      if (!COPIED) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (CHUNKS && whole && r > 0) break;
-        const int64_t at =
-            (int64_t)row_id(vec, first + g + 8 * (CHUNKS && whole ? t : r)) * row_groups + a.k_lo / G;
-        sp[r] = a.scales + at;
-        op[r] = MINS ? a.mins + at : nullptr;
-      }
-      if (CHUNKS && whole) {
-        load_chunk(s_lo / PER);
-        s_now = s_next;
-        if (MINS) o_now = o_next;
-        load_chunk(s_lo / PER + 1);
-      } else {
-        load_scales(s_lo);
+        for (int r = 0; r < 4; ++r) {
+          if (CHUNKS && whole && r > 0) break;
+          const int64_t at =
+              (int64_t)row_id(vec, first + g + 8 * (CHUNKS && whole ? t : r)) * row_groups + a.k_lo / G;
+          sp[r] = a.scales + at;
+          op[r] = MINS ? a.mins + at : nullptr;
+        }
+        if (CHUNKS && whole) {
+          load_chunk(s_lo / PER);
+          s_now = s_next;
+          if (MINS) o_now = o_next;
+          load_chunk(s_lo / PER + 1);
+        } else {
+          load_scales(s_lo);
+        }
       }
 #pragma unroll 1
       for (int st = s_lo; st < s_hi; ++st) {
@@ -496,7 +519,16 @@ q4_kernel(Q4Launch a, int* err) {
         asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
         __syncwarp();
         Packed<SC> sc[4], of[4];
-        if (CHUNKS && whole) {
+        if (COPIED) {
+          if (st == s_lo || st % PER == 0) scale_use = scale_use + 1 == NS ? 0 : scale_use + 1;
+          const uint16_t* from = reinterpret_cast<const uint16_t*>(slots + scale_use * SLOT) + g * 8 +
+                                 st % PER * SC;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sc[r] = load_whole<SC>(from + r * 64);
+            if (MINS) of[r] = load_whole<SC>(from + r * 64 + 256);
+          }
+        } else if (CHUNKS && whole) {
           if (st % PER == 0 && st != s_lo) {
             s_now = s_next;
             if (MINS) o_now = o_next;
@@ -652,30 +684,31 @@ constexpr Form form_of(int nt, int group, bool gather) {
                  : Form{1, gather ? 8 : 16, group == 32 ? 1 : 2, group == 32 ? 4 : 2};
 }
 
-size_t smem_bytes(const Form& f, int kd, int group, int vecs, int cols, bool share) {
+size_t smem_bytes(const Form& f, int kd, int group, int vecs, int cols, int slot, bool share) {
   const int blocks = (kd + kBlockK - 1) / kBlockK;
   return (size_t)h_bytes(blocks, vecs, blocks * (kBlockK / group) * cols) +
-         (size_t)f.warps * f.ns * f.sb * 2048 +
+         (size_t)f.warps * f.ns * (f.sb * 2048 + slot) +
          (share ? (size_t)f.warps * f.nt * 8 * 32 * sizeof(float) : 0);
 }
 
-template <bool BF16, int G, int NT, int MODE, bool GATHER>
+template <bool BF16, int G, int NT, int MODE, bool GATHER, bool COPIED>
 cudaError_t launch_one(const Q4Launch& in, int* err, cudaStream_t s) {
   constexpr Form f = form_of(NT, G, GATHER);
-  auto kernel = q4_kernel<BF16, G, NT, f.warps, f.sb, f.ns, MODE, GATHER>;
+  auto kernel = q4_kernel<BF16, G, NT, f.warps, f.sb, f.ns, MODE, GATHER, COPIED>;
   Q4Launch a = in;
   const int kd = a.k_hi - a.k_lo;
   const int vecs = GATHER ? kGatherVecs : a.M < NT * 8 ? a.M : NT * 8;
   const int cols = GATHER ? kGatherVecs : NT * 8;
   const int64_t rows = GATHER ? a.K : a.n;
+  const int slot = COPIED ? slot_bytes(MODE == kMins) : 0;
   a.tiles = (int)((rows + kRowsWarp - 1) / kRowsWarp);
   const int64_t tiles = (int64_t)a.tiles * (GATHER ? a.M : 1);
   // tiles are shared where the sums that this hands round fit beside the rest
   // (all but the widest rows with many vectors); a run of tiles counts its
   // stages in 32 bits
-  size_t smem = smem_bytes(f, kd, G, vecs, cols, true);
+  size_t smem = smem_bytes(f, kd, G, vecs, cols, slot, true);
   a.share = smem <= kSmemMost;
-  if (!a.share) smem = smem_bytes(f, kd, G, vecs, cols, false);
+  if (!a.share) smem = smem_bytes(f, kd, G, vecs, cols, slot, false);
   static int smem_set[64] = {0};
   cudaError_t e = ensure_dynamic_smem(kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
@@ -685,25 +718,28 @@ cudaError_t launch_one(const Q4Launch& in, int* err, cudaStream_t s) {
                        dim3(f.warps * 32), smem, s, a, err);
 }
 
-template <bool BF16, int G, int MODE>
+template <bool BF16, int G, int MODE, bool COPIED>
 cudaError_t launch_cols(const Q4Launch& a, int* err, cudaStream_t s) {
-  if (a.ids) return launch_one<BF16, G, 1, MODE, true>(a, err, s);
-  if (a.M <= 8 || MODE == kCentred) return launch_one<BF16, G, 1, MODE, false>(a, err, s);
-  return launch_one<BF16, G, MODE == kCentred ? 1 : 2, MODE, false>(a, err, s);
+  if (a.ids) return launch_one<BF16, G, 1, MODE, true, COPIED>(a, err, s);
+  if (a.M <= 8 || MODE == kCentred) return launch_one<BF16, G, 1, MODE, false, COPIED>(a, err, s);
+  return launch_one<BF16, G, MODE == kCentred ? 1 : 2, MODE, false, false>(a, err, s);
 }
 
 template <bool BF16, int G>
-cudaError_t launch_mode(const Q4Launch& a, int* err, cudaStream_t s) {
-  if (a.mins) return launch_cols<BF16, G, kMins>(a, err, s);
-  return a.d < kCentreD ? launch_cols<BF16, G, kCentred>(a, err, s)
-                        : launch_cols<BF16, G, kPlain>(a, err, s);
+cudaError_t launch_mode(const Q4Launch& a, bool copied, int* err, cudaStream_t s) {
+  if (a.mins)
+    return copied ? launch_cols<BF16, G, kMins, true>(a, err, s)
+                  : launch_cols<BF16, G, kMins, false>(a, err, s);
+  if (a.d < kCentreD) return launch_cols<BF16, G, kCentred, false>(a, err, s);
+  return copied ? launch_cols<BF16, G, kPlain, true>(a, err, s)
+                : launch_cols<BF16, G, kPlain, false>(a, err, s);
 }
 
 template <bool BF16>
-cudaError_t launch_group(const Q4Launch& a, int group, int* err, cudaStream_t s) {
-  if (group == 128) return launch_mode<BF16, 128>(a, err, s);
-  if (group == 64) return launch_mode<BF16, 64>(a, err, s);
-  return launch_mode<BF16, 32>(a, err, s);
+cudaError_t launch_group(const Q4Launch& a, int group, bool copied, int* err, cudaStream_t s) {
+  if (group == 128) return launch_mode<BF16, 128>(a, copied, err, s);
+  if (group == 64) return launch_mode<BF16, 64>(a, copied, err, s);
+  return launch_mode<BF16, 32>(a, copied, err, s);
 }
 
 }  // namespace
@@ -718,11 +754,13 @@ cudaError_t launch_q4(const Q4Args& q, int* err, cudaStream_t s) {
   a.d = q.d;
   a.K = q.K;
   a.ldo = q.ids ? q.K : q.n;
-  a.scales_aligned =
-      ((reinterpret_cast<uintptr_t>(q.scales) | reinterpret_cast<uintptr_t>(q.mins)) & 15u) == 0;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(q.scales) | reinterpret_cast<uintptr_t>(q.mins);
+  a.scales_aligned = at % 16 == 0;
+  const bool centred = !q.mins && q.d < kCentreD;
+  const bool copied = !centred && a.scales_aligned && q.d / q.group % 8 == 0;
   // hidden vectors of one pass over the rows, then pieces of d, as far as h
   // fits in shared memory; a later piece adds to the former's sums
-  const int most = q.ids ? q.M : !q.mins && q.d < kCentreD ? 8 : 16;
+  const int most = q.ids ? q.M : centred ? 8 : 16;
   for (int m = 0; m < q.M; m += most) {
     a.M = q.M - m < most ? q.M - m : most;
     a.h = static_cast<const uint16_t*>(q.h) + (size_t)m * q.d;
@@ -730,14 +768,17 @@ cudaError_t launch_q4(const Q4Args& q, int* err, cudaStream_t s) {
     const Form f = form_of(!q.ids && a.M > 8 ? 2 : 1, q.group, q.ids != nullptr);
     const int vecs = q.ids ? kGatherVecs : a.M, cols = q.ids ? kGatherVecs : f.nt * 8;
     int piece = q.d;
-    while (smem_bytes(f, piece, q.group, vecs, cols, false) > kSmemMost)
-      piece = ((piece + 1) / 2 + kBlockK - 1) / kBlockK * kBlockK;
+    // pieces begin at whole 16 bytes of scales
+    const int unit = 8 * q.group > kBlockK ? 8 * q.group : kBlockK;
+    const int slot = copied && f.nt == 1 ? slot_bytes(q.mins) : 0;
+    while (piece > unit && smem_bytes(f, piece, q.group, vecs, cols, slot, false) > kSmemMost)
+      piece = ((piece + 1) / 2 + unit - 1) / unit * unit;
     for (int k = 0; k < q.d; k += piece) {
       a.k_lo = k;
       a.k_hi = k + piece < q.d ? k + piece : q.d;
       a.add = k > 0;
-      const cudaError_t e = q.dtype == LMHEAD_BF16 ? launch_group<true>(a, q.group, err, s)
-                                                   : launch_group<false>(a, q.group, err, s);
+      const cudaError_t e = q.dtype == LMHEAD_BF16 ? launch_group<true>(a, q.group, copied, err, s)
+                                                   : launch_group<false>(a, q.group, copied, err, s);
       if (e != cudaSuccess) return e;
     }
   }
