@@ -23,8 +23,9 @@
 // tensor memory first, at a store per two codes; here they never leave
 // registers.)
 // Measured: 128256 rows of 4096 codes, groups of 128: 54 us for one hidden vector
-// (5.1 TB/s of codes and scales, at 1.8 instructions a cycle and SM), 1002 candidate rows for each of 64 vectors 31 us;
-// 151936 rows of 5120, groups of 64 with mins, 16 vectors: 123 us.
+// (5.1 TB/s of codes and scales, at 1.8 instructions a cycle and SM), 56 for
+// eight, 31 for 1002 candidate rows of each of 64; 151936 rows of 5120, groups of
+// 64 with mins: 124 us for 16 vectors.
 //   The matrix instructions cut the products of a sum at a place set by the
 // largest. With codes up to 15 in place of -8..7 a symmetric row's sums lose
 // about two bits more; over long rows that stays near 2^-21 of the result, in
