@@ -28,10 +28,10 @@
 // Bound: few rows, by reading K and V once; many rows, by the tensor cores.
 // Measured (whole call, both launches): 32 requests of 4000-8000 cached tokens
 // and one new each, 32 heads over 8, dim 128: 134 us for 824 MB (6.1 TB/s); two
-// chunks of 2048 tokens over 6144 cached: 350-365 us for 0.48 TFLOP (1.32-1.38
-// PFLOP/s; the tensor pipe is busy 58 % of the time). The rest is the softmax: a
-// warpgroup's exponentials and packing of a block take longer than the other
-// one's MMAs, and each block is handed over through barriers twice.
+// chunks of 2048 tokens over 6144 cached: 325-340 us for 0.48 TFLOP (1.41-1.48
+// PFLOP/s). The latter is bound by the hand-overs between the roles: without the
+// exponentials it takes as long, with an eighth of the softmax 4 % less, without
+// loads 1 % less, with an eighth of the MMAs still three quarters of the time.
 // The softmax runs in the base-2 domain with a running reference instead of
 // the running maximum: a row's first block with a key sets it, and it moves only
 // when weights pass 2^9 or so, which their sum shows; a block's maximum is not
@@ -334,8 +334,18 @@ struct Cursor {
   }
 };
 
+// A warp's wait. The one that issues the MMAs is on the way of every block: it
+// polls for a while before it lets itself be suspended, from which a warp takes a
+// few hundred cycles to return (two prompts of 2048 tokens 351 to 325 us; with the
+// softmax's warps polling too, which takes issue slots from their neighbours, 332).
+template <bool POLL>
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
                                          long long budget) {
+  if (POLL && budget > 0) {
+#pragma unroll 1
+    for (int i = 0; i < 200; ++i)
+      if (__all_sync(0xFFFFFFFFu, tc::mbar_test(bar, parity))) return true;
+  }
   const bool now = budget > 0 && tc::mbar_try_wait(bar, parity);
   return __all_sync(0xFFFFFFFFu, now || tc::mbar_wait(bar, parity, abort, budget));
 }
@@ -579,7 +589,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const int slot = (int)(n % NS);
             if (n >= (uint32_t)NS) {
-              ok = wait_all(&ctl.empty[slot], ((n / NS) & 1) ^ 1, abort_flag, budget);
+              ok = wait_all<false>(&ctl.empty[slot], ((n / NS) & 1) ^ 1, abort_flag, budget);
               if (!ok) break;
             }
             if (lane == 0)
@@ -644,7 +654,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           // a pair's second step uses the block of its first
           const bool opens = !pair || w == 0, closes = !pair || w == 1;
           if (has_v && opens) {
-            ok = wait_all(&ctl.full[v_slot], (nv / NS) & 1, abort_flag, budget);
+            ok = wait_all<true>(&ctl.full[v_slot], (nv / NS) & 1, abort_flag, budget);
             if (!ok) break;
             // keys that are no token's, or whose page was not loaded, hold anything
             // at all, and weight 0 times NaN is NaN: they are zeroed
@@ -668,14 +678,14 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           if (has_s) {
             if (k + 2 == 0 || (pair && k + 2 == 1)) {
               const uint32_t use = w ? nq1++ : nq0++;
-              ok = wait_all(&ctl.q_full[w], use & 1, abort_flag, budget);
+              ok = wait_all<true>(&ctl.q_full[w], use & 1, abort_flag, budget);
             }
             if (!ok) break;
           }
           if (has_v) {  // the weights come in two halves
             const uint32_t use = w ? np1++ : np0++;
             const uint64_t vd = v_desc + v_slot * (Sh::kBuf / 16);
-            ok = wait_all(&ctl.p_half[w], use & 1, abort_flag, budget);
+            ok = wait_all<true>(&ctl.p_half[w], use & 1, abort_flag, budget);
             if (!ok) break;
             tc::fence_after_sync();
 #pragma unroll
@@ -683,7 +693,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               tc::mma_ts_one(issuer, tmem + 256 + w * 128, tmem + w * 128 + c * 8,
                              vd + c * (16 * 128 / 16), idesc_o, c > 0 ? 1u : (uint32_t)(k >= 2));
             tc::commit_one(issuer, &ctl.h_done[w]);
-            ok = wait_all(&ctl.p_full[w], use & 1, abort_flag, budget);
+            ok = wait_all<true>(&ctl.p_full[w], use & 1, abort_flag, budget);
             if (!ok) break;
             tc::fence_after_sync();
 #pragma unroll
@@ -695,7 +705,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           }
           if (has_s) {
             if (opens) {
-              ok = wait_all(&ctl.full[k_slot], (nk / NS) & 1, abort_flag, budget);
+              ok = wait_all<true>(&ctl.full[k_slot], (nk / NS) & 1, abort_flag, budget);
               if (!ok) break;
             }
             tc::fence_after_sync();
@@ -799,7 +809,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int j = 0; j < steps; ++j) {
         const int b = b_first + (pair ? j : 2 * j + w);
         const int key0 = (it.kb0 + b) * kKeys;
-        ok = wait_all(&ctl.s_full[w], ns++ & 1, abort_flag, budget);
+        ok = wait_all<false>(&ctl.s_full[w], ns++ & 1, abort_flag, budget);
         if (!ok) break;
         tc::fence_after_sync();
         if (!idle) {
@@ -890,7 +900,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           if (!sure && large(p)) {
             // the first half is with the MMAs: its values are summed up before
             // the accumulators are scaled
-            ok = wait_all(&ctl.h_done[w], (ns - 1) & 1, abort_flag, budget);
+            ok = wait_all<false>(&ctl.h_done[w], (ns - 1) & 1, abort_flag, budget);
             if (!ok) break;
             tc::fence_after_sync();
             set_reference(true);
@@ -909,8 +919,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // with one tile and two blocks or more both warpgroups have values
       const bool join = !pair && nb > 1;
       const bool both = pair || nb > 1;  // warpgroup 1 has values
-      if (w == 0 || join) ok = wait_all(&ctl.o_full[0], no0 & 1, abort_flag, budget);
-      if (ok && both && (w == 1 || join)) ok = wait_all(&ctl.o_full[1], no1 & 1, abort_flag, budget);
+      if (w == 0 || join) ok = wait_all<false>(&ctl.o_full[0], no0 & 1, abort_flag, budget);
+      if (ok && both && (w == 1 || join)) ok = wait_all<false>(&ctl.o_full[1], no1 & 1, abort_flag, budget);
       ++no0;
       no1 += both;
       if (!ok) break;
@@ -960,7 +970,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         tc::fence_before_sync();
         tc::mbar_arrive(&ctl.ex1);
-        ok = wait_all(&ctl.ex1, nx & 1, abort_flag, budget);
+        ok = wait_all<false>(&ctl.ex1, nx & 1, abort_flag, budget);
         if (!ok) break;
         tc::fence_after_sync();
         if (!idle) {
@@ -987,7 +997,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         tc::fence_before_sync();
         tc::mbar_arrive(&ctl.ex2);
-        ok = wait_all(&ctl.ex2, nx++ & 1, abort_flag, budget);
+        ok = wait_all<false>(&ctl.ex2, nx++ & 1, abort_flag, budget);
         if (!ok) break;
       }
       if (!(first && last) && !idle && (pair || join || w == 0)) {
