@@ -104,16 +104,17 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 template <int N> struct Packed {
   uint32_t w[(N + 1) / 2];
 };
-template <int N> __device__ __forceinline__ Packed<N> load_whole(const uint16_t* p) {
+template <int N, bool SHARED> __device__ __forceinline__ Packed<N> load_whole(const uint16_t* p) {
+  auto get = [](auto* q) { return SHARED ? *q : __ldg(q); };
   Packed<N> v;
   if (N == 4) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    const uint2 x = get(reinterpret_cast<const uint2*>(p));
     v.w[0] = x.x;
     v.w[(N + 1) / 2 - 1] = x.y;
   } else if (N == 2) {
-    v.w[0] = *reinterpret_cast<const uint32_t*>(p);
+    v.w[0] = get(reinterpret_cast<const uint32_t*>(p));
   } else {
-    v.w[0] = *p;
+    v.w[0] = get(p);
   }
   return v;
 }
@@ -485,8 +486,8 @@ q4_kernel(Q4Launch a, int* err) {
         if (!CHUNKS && whole) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            sc_n[r] = load_whole<SC>(sp[r] + st * SC);
-            if (MINS) of_n[r] = load_whole<SC>(op[r] + st * SC);
+            sc_n[r] = load_whole<SC, false>(sp[r] + st * SC);
+            if (MINS) of_n[r] = load_whole<SC, false>(op[r] + st * SC);
           }
         } else {
 #pragma unroll
@@ -526,8 +527,8 @@ q4_kernel(Q4Launch a, int* err) {
                                  st % PER * SC;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            sc[r] = load_whole<SC>(from + r * 64);
-            if (MINS) of[r] = load_whole<SC>(from + r * 64 + 256);
+            sc[r] = load_whole<SC, true>(from + r * 64);
+            if (MINS) of[r] = load_whole<SC, true>(from + r * 64 + 256);
           }
         } else if (CHUNKS && whole) {
           if (st % PER == 0 && st != s_lo) {
@@ -758,7 +759,11 @@ cudaError_t launch_q4(const Q4Args& q, int* err, cudaStream_t s) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(q.scales) | reinterpret_cast<uintptr_t>(q.mins);
   a.scales_aligned = at % 16 == 0;
   const bool centred = !q.mins && q.d < kCentreD;
-  const bool copied = !centred && a.scales_aligned && q.d / q.group % 8 == 0;
+  // Scales are copied (kernel, COPIED) where rows of them allow it and the slots
+  // leave room for h of whole rows and for shared tiles; groups of 32 over the
+  // whole head gain nothing by it (one vector 62 us, with loads 60).
+  const bool copies = !centred && a.scales_aligned && q.d / q.group % 8 == 0 &&
+                      (q.group > 32 || q.ids);
   // hidden vectors of one pass over the rows, then pieces of d, as far as h
   // fits in shared memory; a later piece adds to the former's sums
   const int most = q.ids ? q.M : centred ? 8 : 16;
@@ -768,11 +773,13 @@ cudaError_t launch_q4(const Q4Args& q, int* err, cudaStream_t s) {
     a.out = q.out + (size_t)m * a.ldo;
     const Form f = form_of(!q.ids && a.M > 8 ? 2 : 1, q.group, q.ids != nullptr);
     const int vecs = q.ids ? kGatherVecs : a.M, cols = q.ids ? kGatherVecs : f.nt * 8;
+    const bool copied = copies && f.nt == 1 &&
+                        smem_bytes(f, q.d, q.group, vecs, cols, slot_bytes(q.mins), true) <= kSmemMost;
     int piece = q.d;
     // pieces begin at whole 16 bytes of scales
     const int unit = 8 * q.group > kBlockK ? 8 * q.group : kBlockK;
-    const int slot = copied && f.nt == 1 ? slot_bytes(q.mins) : 0;
-    while (piece > unit && smem_bytes(f, piece, q.group, vecs, cols, slot, false) > kSmemMost)
+    while (!copied && piece > unit &&
+           smem_bytes(f, piece, q.group, vecs, cols, 0, false) > kSmemMost)
       piece = ((piece + 1) / 2 + unit - 1) / unit * unit;
     for (int k = 0; k < q.d; k += piece) {
       a.k_lo = k;
