@@ -187,6 +187,34 @@ def test_gather_of_few_and_many(M, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("mins", [False, True])
+@pytest.mark.parametrize("group,d", [(32, 256), (64, 512), (128, 1024), (64, 4096), (128, 3968)])
+@pytest.mark.parametrize("n,M", [(20011, 1), (9973, 7)])
+def test_shared_tiles_and_scales_anywhere(n, M, group, d, mins):
+    """Tiles divided between warps at every stage; scales at an address that allows
+    wide copies and at one that allows none."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    codes, scales, off, h = _inputs(n, d, group, M, "bfloat16", mins, n + d)
+
+    def moved(x):
+        if x is None:
+            return None
+        y = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(x.shape)
+        return y.copy_(x)
+
+    want, tol = _exact(codes, scales, off, h, group)
+    ids = torch.randint(0, n, (M, 333), device="cuda", dtype=torch.int32, generator=torch.Generator("cuda").manual_seed(d))
+    at = ids.long().cpu().numpy()
+    for sc, mi in ((scales, off), (moved(scales), moved(off))):
+        got = L.q4_head(codes, sc, h, group, mins=mi).double().cpu().numpy()
+        assert np.all(np.abs(got - want) <= tol)
+        got = L.q4_gather_logits(codes, sc, h, ids, group, mins=mi).double().cpu().numpy()
+        assert np.all(np.abs(got - np.take_along_axis(want, at, 1)) <= np.take_along_axis(tol, at, 1))
+
+
+@pytest.mark.gpu
 def test_bad_ids_streams_and_refusals():
     import torch
     from gpu_util import lib
