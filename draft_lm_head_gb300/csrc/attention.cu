@@ -58,18 +58,26 @@ constexpr int kPrepThreads = 256;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// An item: up to two row tiles of one request, for every K/V head alike.
+// What becomes of a request's rows: kFillNan those of one whose lengths the
+// table has no room for.
+enum Fate { kAttend, kFillNan };
+
+// An item: up to two row tiles of one request, for every K/V head alike. One of
+// rows that are only filled has no key blocks.
 struct Item {
   int s, tok0, ntok, len;        // request, its first token (of all), tokens, cached before
   int i0, kb0, nblk, ntile;      // first token in the request, key blocks, row tiles
-  int kend, kbeg, prefix, pad;   // keys [kbeg, kend) are loaded; units before it
+  int kend, kbeg, prefix, fate;  // keys [kbeg, kend) are loaded; units before it
 };
 static_assert(sizeof(Item) == 48, "three 16-byte loads");
 
 struct Header {
   long long units;  // of all heads
   int items, per_head, parts;
+  int fill;  // kFillSome: items among them that are only filled; kFillAll: no
+             // plan could be made, every row is
 };
+enum Fill { kFillNone, kFillSome, kFillAll };
 
 // Work units of an item: one per row tile and block, and kItemCost for what an
 // item costs besides. Unit x of an item is at block ceil((x - kItemCost) / ntile).
@@ -115,55 +123,92 @@ inline int part_count() { return sm_count() > 255 ? 255 : sm_count() > 0 ? sm_co
 
 // ------------------------------------------------------------------ prepare
 
-__device__ __forceinline__ Item make_item(const AttnArgs& a, int s, int tok0, int m, int len,
-                                          int x, int tile_tok) {
+// The tokens of request s: cu is the caller's, so whatever it holds the range
+// returned lies within [0, T); `sane` is cleared where it begins below 0 or
+// decreases. Ranges of a cu that does neither are disjoint, which is what the
+// number of items (most_items) rests on.
+struct Request {
+  int tok0, m, len;
+  int seen;  // new tokens that are keys
+  Fate fate;
+};
+__device__ __forceinline__ Request request_of(const AttnArgs& a, int s, bool& sane) {
+  Request r;
+  const int end = a.cu[s + 1];
+  r.tok0 = a.cu[s];
+  r.len = a.lens[s];
+  sane = r.tok0 >= 0 && end >= r.tok0;
+  r.tok0 = max(0, min(r.tok0, a.T));
+  r.m = max(r.tok0, min(end, a.T)) - r.tok0;
+  // the keys that the request's rows may see, within its pages? (lengths that
+  // are keep all arithmetic on them in 32 bits)
+  r.seen = a.tree ? min(r.m, 64) : r.m;
+  r.fate = r.len >= 0 && r.len <= (a.width << a.page_shift) - r.seen ? kAttend : kFillNan;
+  if (r.fate != kAttend) r.len = 0;
+  return r;
+}
+
+__device__ __forceinline__ Item make_item(const AttnArgs& a, int s, const Request& r, int x,
+                                          int tile_tok) {
   Item it;
   it.s = s;
   it.i0 = x * 2 * tile_tok;
-  it.tok0 = tok0 + it.i0;
-  it.ntok = min(m - it.i0, 2 * tile_tok);
-  it.len = len;
+  it.tok0 = r.tok0 + it.i0;
+  it.ntok = min(r.m - it.i0, 2 * tile_tok);
+  it.len = r.len;
   it.ntile = it.ntok > tile_tok ? 2 : 1;
-  it.kend = len + m;
-  const int end = a.tree ? len + min(m, 64) : len + it.i0 + it.ntok;
-  const int beg = a.window > 0 ? max(0, len + it.i0 + 1 - a.window) : 0;
+  it.kend = r.len + r.seen;
+  const int end = a.tree ? it.kend : r.len + it.i0 + it.ntok;
+  const int beg = a.window > 0 ? max(0, r.len + it.i0 + 1 - a.window) : 0;
   it.kb0 = beg / kKeys;
-  it.nblk = (end + kKeys - 1) / kKeys - it.kb0;
+  it.nblk = r.fate == kAttend ? (end + kKeys - 1) / kKeys - it.kb0 : 0;
   it.kbeg = beg >> a.page_shift << a.page_shift;
   it.prefix = 0;
-  it.pad = 0;
+  it.fate = r.fate;
   return it;
 }
 
 // The items of all requests with the units before each, and where each CTA
 // starts: CTA c of `parts` has the units [c U / parts, (c + 1) U / parts) of the
 // sequence (K/V head, item).
-__device__ void make_plan(const AttnArgs& a, const Scratch& sc, int most_parts) {
+__device__ void make_plan(const AttnArgs& a, const Scratch& sc, int most_parts, int* err) {
   constexpr int kKept = 1024;
-  __shared__ int sh_n[kPrepThreads / 32], sh_w[kPrepThreads / 32];
+  __shared__ int sh_n[kPrepThreads / 32];
+  __shared__ long long sh_w[kPrepThreads / 32];
   __shared__ int sh_prefix[kKept];
+  __shared__ int sh_bad, sh_fill;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile_tok = kRows / (a.heads / a.kv_heads);
-  int base_n = 0, base_w = 0;
+  if (tid == 0) sh_bad = sh_fill = 0;
+  cta_sync();
+  int base_n = 0;
+  long long base_w = 0;
+  bool bad = false;
   for (int s0 = 0; s0 < a.S; s0 += kPrepThreads) {
     const int s = s0 + tid;
-    int tok0 = 0, m = 0, len = 0, n = 0, w = 0;
+    Request req = {};
+    int n = 0;
+    long long w = 0;
     if (s < a.S) {
-      tok0 = a.cu[s];
-      m = a.cu[s + 1] - tok0;
-      len = max(a.lens[s], 0);
-      if (tok0 < 0 || tok0 > a.T) m = 0;
-      m = max(0, min(m, a.T - tok0));
-      n = (m + 2 * tile_tok - 1) / (2 * tile_tok);
+      bool sane;
+      req = request_of(a, s, sane);
+      if (!sane) sh_bad = 1;
+      n = req.m > 0 ? (req.m - 1) / (2 * tile_tok) + 1 : 0;
       for (int x = 0; x < n; ++x) {
-        const Item it = make_item(a, s, tok0, m, len, x, tile_tok);
+        const Item it = make_item(a, s, req, x, tile_tok);
         w += item_units(it.nblk, it.ntile);
       }
+      if (n > 0 && req.fate != kAttend) {
+        sh_fill = 1;
+        record_error(err, kDevErrBadId);
+      }
     }
-    int sn = n, sw = w;
+    int sn = n;
+    long long sw = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int pn = __shfl_up_sync(0xFFFFFFFFu, sn, o), pw = __shfl_up_sync(0xFFFFFFFFu, sw, o);
+      const int pn = __shfl_up_sync(0xFFFFFFFFu, sn, o);
+      const long long pw = __shfl_up_sync(0xFFFFFFFFu, sw, o);
       if (lane >= o) {
         sn += pn;
         sw += pw;
@@ -174,7 +219,8 @@ __device__ void make_plan(const AttnArgs& a, const Scratch& sc, int most_parts) 
       sh_w[warp] = sw;
     }
     cta_sync();
-    int bn = base_n, bw = base_w;
+    int bn = base_n;
+    long long bw = base_w;
     for (int i = 0; i < kPrepThreads / 32; ++i) {
       if (i < warp) {
         bn += sh_n[i];
@@ -183,9 +229,13 @@ __device__ void make_plan(const AttnArgs& a, const Scratch& sc, int most_parts) 
       base_n += sh_n[i];
       base_w += sh_w[i];
     }
-    int at = bn + sn - n, pre = bw + sw - w;
+    // nothing of a cu that decreases is planned (its items might be more than the
+    // scratch has places for), nor more units than their 32 bits can count
+    bad = sh_bad || base_w > INT32_MAX;
+    if (bad) break;
+    int at = bn + sn - n, pre = (int)(bw + sw - w);
     for (int x = 0; x < n; ++x, ++at) {
-      Item it = make_item(a, s, tok0, m, len, x, tile_tok);
+      Item it = make_item(a, s, req, x, tile_tok);
       it.prefix = pre;
       pre += item_units(it.nblk, it.ntile);
       sc.items[at] = it;
@@ -193,14 +243,17 @@ __device__ void make_plan(const AttnArgs& a, const Scratch& sc, int most_parts) 
     }
     cta_sync();
   }
-  const long long units = (long long)base_w * a.kv_heads;
+  if (bad) base_n = 0, base_w = 0;
+  const long long units = base_w * a.kv_heads;
   // a CTA has work for both warpgroups at least
   const int parts = (int)min((long long)most_parts, (units + 1) / 2);
   if (tid == 0) {
     sc.head->units = units;
     sc.head->items = base_n;
-    sc.head->per_head = base_w;
+    sc.head->per_head = (int)base_w;
     sc.head->parts = parts;
+    sc.head->fill = bad ? kFillAll : sh_fill ? kFillSome : kFillNone;
+    if (bad) record_error(err, kDevErrBadId);
   }
   for (int c = tid; c < parts; c += kPrepThreads) {
     const long long u = units * c / parts;
@@ -223,7 +276,7 @@ prepare_kernel(AttnArgs a, Scratch sc, int most_parts, int64_t counts, int piece
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0) {
-    make_plan(a, sc, most_parts);
+    make_plan(a, sc, most_parts, err);
     return;
   }
   const int64_t first = (int64_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x;
@@ -309,13 +362,15 @@ struct Cursor {
     hk = st.y;
     off = st.z;
   }
-  __device__ bool next() {
+  // On to the next piece; with FILLED also to an item that is only filled, which
+  // is the CTA's that has its one unit.
+  template <bool FILLED = false> __device__ bool next() {
     while (left > 0) {
       const int4* src = reinterpret_cast<const int4*>(items + idx);
       const int4 x = src[0], y = src[1], z = src[2];
       it.s = x.x; it.tok0 = x.y; it.ntok = x.z; it.len = x.w;
       it.i0 = y.x; it.kb0 = y.y; it.nblk = y.z; it.ntile = y.w;
-      it.kend = z.x; it.kbeg = z.y; it.prefix = z.z;
+      it.kend = z.x; it.kbeg = z.y; it.prefix = z.z; it.fate = z.w;
       const int w = item_units(it.nblk, it.ntile);
       const int end = (int)min((long long)w, off + left);
       b0 = block_at(off, it.nblk, it.ntile);
@@ -328,7 +383,7 @@ struct Cursor {
         idx = 0;
         ++hk;
       }
-      if (b1 > b0) return true;
+      if (b1 > b0 || (FILLED && it.nblk == 0)) return true;
     }
     return false;
   }
@@ -498,6 +553,39 @@ __device__ void join_rows(const AttnArgs& a, const Scratch& sc, const Cursor& cu
     if (e < elems)
       *reinterpret_cast<uint2*>(static_cast<char*>(a.out) + (to * D + col) * 2 + e % N4 * 8) =
           make_uint2(pack2<BF16>(acc[i].x * s, acc[i].y * s), pack2<BF16>(acc[i].z * s, acc[i].w * s));
+  }
+}
+
+// One row of the output and its log-sum-exp that were not computed, by a warp.
+template <bool BF16, int D>
+__device__ __forceinline__ void fill_row(const AttnArgs& a, int64_t row, float v) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t two = pack2<BF16>(v, v);
+  if (lane < D / 8)
+    *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + (row * D + lane * 8) * 2) =
+        make_uint4(two, two, two, two);
+  if (lane == 0 && a.lse) a.lse[row] = v;
+}
+
+// The CTA's share of the rows that are only filled, by eight warps.
+template <bool BF16, int D>
+__device__ __forceinline__ void fill_rows(const AttnArgs& a, const Scratch& sc, int warp) {
+  const float nan = __int_as_float(0x7fc00000);
+  if (sc.head->fill == kFillAll) {
+    const int64_t rows = (int64_t)a.T * a.heads;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + warp; r < rows; r += (int64_t)gridDim.x * 8)
+      fill_row<BF16, D>(a, r, nan);
+  }
+  const int group = a.heads / a.kv_heads;
+  Cursor cur;
+  cur.init(sc, blockIdx.x);
+  while (cur.next<true>()) {
+    if (cur.it.nblk > 0) continue;
+    for (int i = warp; i < cur.it.ntok * group; i += 8) {
+      const int tk = i / group;
+      fill_row<BF16, D>(a, (int64_t)(cur.it.tok0 + tk) * a.heads + cur.p_hk * group + i - tk * group,
+                        nan);
+    }
   }
 }
 
@@ -1034,6 +1122,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
+  // at the end, so that a call without such rows pays one look at the header
+  if (warp < 8 && sc.head->fill != kFillNone) fill_rows<BF16, D>(a, sc, warp);
 }
 
 template <bool BF16, int D>

@@ -443,7 +443,11 @@ int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_
  * past a request's tokens are never used, whatever they hold; a non-finite V
  * of a token of the request itself may reach every row of its chunk.
  * A page id outside [0, pages) makes its request's rows NaN and records
- * LMHEAD_ERR_DEVICE_CHECK. scale > 0. No two calls in flight may share the
+ * LMHEAD_ERR_DEVICE_CHECK; so does a negative length, or one whose keys (len and
+ * the new tokens, with a tree the first 64 of them) pass width * page_size. cu
+ * must not decrease nor begin below 0: where it does, or where the key blocks of
+ * all row tiles pass 2^31, nothing is computed, every row is NaN and the
+ * error is recorded. scale > 0. No two calls in flight may share the
  * workspace (lmhead_chunk_attention_workspace_size bytes, 256-byte aligned).
  */
 size_t lmhead_chunk_attention_workspace_size(int S, int T, int heads, int kv_heads, int dim);

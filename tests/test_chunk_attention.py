@@ -330,3 +330,67 @@ def test_graph_capture():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, w)
+
+
+def _call_guarded(L, c, cu, lens):
+    """A call on other ranges and lengths with bytes behind its workspace that it
+    must leave alone: (out, lse, error)."""
+    import torch
+    S, (T, H, D) = c["lens"].shape[0], c["q"].shape
+    need = L.load().lmhead_chunk_attention_workspace_size(S, T, H, c["kc"].shape[2], D)
+    ws = torch.full((need + (1 << 20),), 0x5a, dtype=torch.uint8, device="cuda")
+    out = (torch.zeros(T, H, D, dtype=c["q"].dtype, device="cuda"), torch.zeros(T, H, device="cuda"))
+    L.chunk_attention(c["q"], c["kc"], c["vc"], c["table"], lens, cu, workspace=ws[:need], out=out)
+    err = L.last_device_error()
+    assert torch.all(ws[need:] == 0x5a)
+    return out[0], out[1], err
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("S", [2, 40, 700])
+def test_token_ranges_that_decrease(S):
+    """Ranges that overlap would be more work than the workspace has places for:
+    nothing is computed, every row is NaN and the error is recorded."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    c = _case([40] * S, [2] * S, 4, 2, 64, 16, "bfloat16", 1)
+    good, _ = _check(L, c, "bfloat16")
+    T = 2 * S
+    back = c["cu"].clone()
+    back[1::2], back[0::2] = T, 0
+    one = c["cu"].clone()
+    one[S // 2] = T + 1
+    low = c["cu"].clone()
+    low[0] = -3
+    for cu in (back, one, low):
+        out, lse, err = _call_guarded(L, c, cu, c["lens"])
+        assert err == -7 and torch.isnan(out).all() and torch.isnan(lse).all()
+    # a plan's ranges may pass its tokens: the rest has no rows
+    past = c["cu"].clone()
+    past[-1] = T + 1000
+    out, _, err = _call_guarded(L, c, past, c["lens"])
+    assert err == 0 and torch.equal(out, good)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("len_of", [-1, -2 ** 31, 2 ** 31 - 1, "past"])
+@pytest.mark.parametrize("mask", ["causal", "tree"])
+def test_lengths_that_no_table_holds(mask, len_of):
+    """Such a request's rows are NaN and the error is recorded, whatever the
+    length; the others' are right."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    c = _case([100, 50, 300], [2, 70, 4], 4, 2, 64, 16, "float16", 2, mask=mask)
+    call = lambda lens: L.chunk_attention(c["q"], c["kc"], c["vc"], c["table"], lens, c["cu"], tree=c["tree"], with_lse=True)
+    _check(L, c, "float16")
+    good, gl = call(c["lens"])
+    lens = c["lens"].clone()
+    lens[1] = c["table"].shape[1] * 16 - (64 if mask == "tree" else 70) + 1 if len_of == "past" else len_of
+    out, lse = call(lens)
+    assert L.last_device_error() == -7
+    assert torch.isnan(out[2:72]).all() and torch.isnan(lse[2:72]).all()
+    for got, want in ((out, good), (lse, gl)):
+        assert torch.equal(got[:2], want[:2]) and torch.equal(got[72:], want[72:])
+    assert L.last_device_error() == 0
