@@ -22,6 +22,7 @@ from typing import Optional
 import torch
 
 from ._lib import LIB_PATH, LmheadError, check, load, status_string  # noqa: F401
+from ._memory import Workspace, scratch
 
 GLOBAL = 0
 LOCAL = 1
@@ -90,27 +91,6 @@ def workspace_size(mode: int, n: int, d: int, r: int, M: int, C_or_tile: int,
     return int(load().lmhead_workspace_size(mode, n, d, r, M, C_or_tile, k_tile))
 
 
-class Workspace:
-    """A reusable device workspace (grows on demand; 256-byte aligned)."""
-
-    def __init__(self, device=None):
-        self.device = device
-        self.buf = None
-
-    def get(self, nbytes: int, device) -> torch.Tensor:
-        if self.buf is None or self.buf.numel() < nbytes or self.buf.device != device:
-            self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-        return self.buf
-
-
-def _ws(workspace, nbytes, device):
-    if workspace is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    if isinstance(workspace, Workspace):
-        return workspace.get(nbytes, device)
-    return workspace
-
-
 def project_u(B: torch.Tensor, h: torch.Tensor, out: Optional[torch.Tensor] = None,
               stream=None) -> torch.Tensor:
     r, d = B.shape
@@ -133,7 +113,7 @@ def lowrank_score_topk(mode: int, A: torch.Tensor, B: torch.Tensor, h: torch.Ten
     ids = torch.empty((M, K), dtype=torch.int32, device=h.device)
     scores = torch.empty((M, K), dtype=torch.float32, device=h.device) if with_scores else None
     nbytes = workspace_size(mode, n, d, r, M, C_or_tile, k_tile)
-    ws = _ws(workspace, nbytes, h.device)
+    ws = scratch(workspace, nbytes, h.device, stream)
     check(load().lmhead_lowrank_score_topk(
         mode, _bf16(A, "A"), _bf16(B, "B"), _bf16(h, "h"), _typed(token_ids, torch.int32, "token_ids"),
         n, d, r, M, C_or_tile, k_tile, ids.data_ptr(), _typed(scores, torch.float32, "scores"),
@@ -182,7 +162,7 @@ def two_stage(mode: int, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, h: t
                   token_ids=(token_ids, (n,)), ids=(ids, (M, K)), logits=(L, (M, K)),
                   q=(q, (M, K)))
     nbytes = workspace_size(mode, n, d, r, M, C_or_tile, k_tile)
-    ws = _ws(workspace, nbytes, h.device)
+    ws = scratch(workspace, nbytes, h.device, stream)
     check(load().lmhead_two_stage(
         mode, _bf16(W, "W"), _bf16(A, "A"), _bf16(B, "B"), _bf16(h, "h"),
         _typed(token_ids, torch.int32, "token_ids"), n, d, r, M, C_or_tile, k_tile,
@@ -251,7 +231,7 @@ def shard_two_stage(W_shard: torch.Tensor, A_shard: torch.Tensor, B: torch.Tenso
                   token_ids_shard=(token_ids_shard, (n_shard,)), ids=(ids, (M, K)),
                   logits=(L, (M, K)), stats=(stats, (M, 2)))
     nbytes = shard_workspace_size(n_shard, d, r, M, T, k_tile)
-    ws = _ws(workspace, nbytes, dev)
+    ws = scratch(workspace, nbytes, dev, stream)
     check(load().lmhead_shard_two_stage(
         _bf16(W_shard, "W_shard"), _bf16(A_shard, "A_shard"), _bf16(B, "B"), _bf16(h, "h"),
         _typed(token_ids_shard, torch.int32, "token_ids_shard"),
@@ -321,7 +301,7 @@ def cluster_two_stage(W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, h: torc
                   ids=(ids, (M, K)), logits=(L, (M, K)), q=(q, (M, K)))
     gs = torch.empty((M, G), dtype=torch.float32, device=dev) if with_group_scores else None
     nbytes = cluster_workspace_size(n, d, r, M, group, G)
-    ws = _ws(workspace, nbytes, dev)
+    ws = scratch(workspace, nbytes, dev, stream)
     check(load().lmhead_cluster_two_stage(
         _bf16(W, "W"), _bf16(A, "A"), _bf16(B, "B"), _bf16(h, "h"), n, d, r, M, group, G,
         float(temperature), _typed(groups, torch.int32, "groups"),

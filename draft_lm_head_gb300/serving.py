@@ -18,6 +18,7 @@ from typing import NamedTuple, Optional, Sequence
 import torch
 
 from ._lib import check, load
+from ._memory import scratch, stream_handle
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -57,18 +58,6 @@ def _cuda(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
-# the current stream's handle without building a Stream object
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream(stream, device) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
-
-
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
     """A new tensor that the call's stream may use: one that is not the current
     stream has to be named to the allocator."""
@@ -76,12 +65,6 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
     if stream is not None:
         t.record_stream(stream)
     return t
-
-
-def _workspace(workspace, nbytes: int, device, stream) -> torch.Tensor:
-    if workspace is None:
-        return _empty(max(nbytes, 256), torch.uint8, device, stream)
-    return workspace if isinstance(workspace, torch.Tensor) else workspace.get(nbytes, device)
 
 
 def page_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor,
@@ -115,7 +98,7 @@ def page_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor,
         _dense(table, i32, (S, width), dev, "table"), width,
         _dense(free_pages, i32, (cap,), dev, "free_pages"), cap,
         _dense(free_count, i32, (1,), dev, "free_count"), page_size, max_tokens, *ptrs,
-        _stream(stream, dev)), "page_plan")
+        stream_handle(stream, dev)), "page_plan")
     return out
 
 
@@ -192,7 +175,7 @@ def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
             raise ValueError("slots: expected a slot per token")
         slots = slots[:T]
     i32 = torch.int32
-    ws = _workspace(workspace, _attention_bytes(dev, S, T, heads, kv_heads, dim), dev, stream)
+    ws = scratch(workspace, _attention_bytes(dev, S, T, heads, kv_heads, dim), dev, stream)
     check(load().lmhead_chunk_attention(
         _DTYPES[dt], qa, q_tok, q_head, ka, k_tok, k_head, va, v_tok, v_head, kca, kc_page, kc_tok,
         kc_head, vca, vc_page, vc_tok, vc_head, pages, P,
@@ -201,7 +184,7 @@ def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _dense(tree, torch.int64, (T,), dev, "tree"), S, T, heads, kv_heads, dim, window,
         dim ** -0.5 if scale is None else scale, _dense(o, dt, (T, heads, dim), dev, "out"),
         _dense(lse, torch.float32, (T, heads), dev, "lse"), ws.data_ptr(), ws.numel(),
-        _stream(stream, dev)), "chunk_attention")
+        stream_handle(stream, dev)), "chunk_attention")
     return o if lse is None else (o, lse)
 
 
@@ -224,11 +207,11 @@ def _q4(name, codes, scales, h, ids, group, mins, out, stream):
             _dense(mins, dt, (n, d // group), dev, "mins"), _dense(h, dt, (M, d), dev, "h")]
     o = _dense(out, torch.float32, (M, K), dev, "out")
     if ids is None:
-        check(load().lmhead_q4_head(*args, n, d, group, M, o, _stream(stream, dev)), name)
+        check(load().lmhead_q4_head(*args, n, d, group, M, o, stream_handle(stream, dev)), name)
     else:
         check(load().lmhead_q4_gather_logits(
             *args, _dense(ids, torch.int32, (M, K), dev, "ids"), n, d, group, M, K, o,
-            _stream(stream, dev)), name)
+            stream_handle(stream, dev)), name)
     return out
 
 
@@ -290,7 +273,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, k: int,
         parent, token, score = out
         ptrs = (_dense(parent, i32, (S, k), dev, "parent"), _dense(token, i32, (S, k), dev, "token"),
                 _dense(score, torch.float32, (S, k), dev, "score"))
-    ws = _workspace(workspace, _beam_bytes(dev, S, beams, n, k), dev, stream)
+    ws = scratch(workspace, _beam_bytes(dev, S, beams, n, k), dev, stream)
     # a bool is a byte
     kind = torch.uint8 if finished is None or finished.dtype is torch.uint8 else torch.bool
     check(load().lmhead_beam_select(
@@ -298,7 +281,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, k: int,
         _dense(scores, torch.float32, (rows,), dev, "scores"),
         _dense(ids, i32, (rows, n), dev, "ids"),
         _dense(finished, kind, (rows,), dev, "finished"), S, beams, n, k, eos, *ptrs,
-        ws.data_ptr(), ws.numel(), _stream(stream, dev)), "beam_select")
+        ws.data_ptr(), ws.numel(), stream_handle(stream, dev)), "beam_select")
     return parent, token, score
 
 
@@ -332,5 +315,5 @@ def beam_reorder(parent: torch.Tensor, states: Sequence[torch.Tensor], beams: in
     at = ctypes.addressof(table)
     check(load().lmhead_beam_reorder(
         _dense(parent, torch.int32, (S, k), dev, "parent"), S, beams, k, n, at, at + 64, at + 128,
-        _stream(stream, dev)), "beam_reorder")
+        stream_handle(stream, dev)), "beam_reorder")
     return res

@@ -1,0 +1,102 @@
+"""Memory of calls that run on a stream other than the current one: the
+allocator may not hand it out again before that stream is done with it. Shown by
+addresses alone, while a stream is kept busy for a while."""
+import pytest
+import torch
+
+import draft_lm_head_gb300 as L
+from draft_lm_head_gb300 import _memory
+
+
+class Named(torch.Tensor):
+    """A tensor that lists the streams it is told about."""
+
+    def record_stream(self, s):
+        self.seen = getattr(self, "seen", []) + [s]
+
+
+class FakeStream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+def test_scratch_is_named_to_the_allocator():
+    cpu = torch.device("cpu")
+    a, b = FakeStream(1), FakeStream(2)
+    t = torch.empty(512, dtype=torch.uint8).as_subclass(Named)
+    assert _memory.scratch(t, 256, cpu, a) is t and t.seen == [a]
+    ws = L.Workspace()
+    ws.buf = torch.empty(512, dtype=torch.uint8).as_subclass(Named)
+    for s in (a, b, a, b):  # once a stream
+        assert _memory.scratch(ws, 512, cpu, s) is ws.buf
+    assert ws.buf.seen == [a, b]
+
+
+def _overlap(a: torch.Tensor, ptr: int, nbytes: int) -> bool:
+    return a.data_ptr() < ptr + nbytes and ptr < a.data_ptr() + a.numel() * a.element_size()
+
+
+def _busy(stream):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(200_000_000)  # about a tenth of a second
+
+
+def _beams(n):
+    g = torch.Generator("cuda").manual_seed(n)
+    return torch.randn(64, n, device="cuda", generator=g), torch.zeros(64, device="cuda")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("explicit", [True, False])
+def test_workspace_that_grows_while_its_stream_is_busy(explicit):
+    from gpu_util import lib
+    lib()
+    small, large = _beams(4000), _beams(200000)
+    want = [L.beam_select(x, sc, 4, 8) for x, sc in (small, large)]
+    s = torch.cuda.Stream()
+    ws = L.Workspace()
+    L.beam_select(*small, 4, 8, workspace=ws)  # allocated on the current stream
+    torch.cuda.synchronize()
+    _busy(s)
+    if explicit:
+        got = [L.beam_select(*small, 4, 8, workspace=ws, stream=s)]
+    else:
+        with torch.cuda.stream(s):
+            got = [L.beam_select(*small, 4, 8, workspace=ws)]
+    old = ws.buf.data_ptr(), ws.buf.numel()
+    got.append(L.beam_select(*large, 4, 8, workspace=ws))
+    assert ws.buf.numel() > old[1]
+    blocks = [torch.empty(old[1], dtype=torch.uint8, device="cuda") for _ in range(4)]
+    idle = s.query()
+    assert idle or not any(_overlap(b, *old) for b in blocks)
+    assert not idle  # the wait was long enough for the test to mean something
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for x, y in zip(g, w):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_scratch_of_a_call_on_a_busy_stream():
+    """No workspace given: the one of the call is gone when it returns."""
+    from gpu_util import lib
+    lib()
+    x, sc = _beams(4000)
+    need = L.load().lmhead_beam_workspace_size(16, 4, 4000, 8)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    taken = []
+    real = _memory._allocate
+    try:
+        _memory._allocate = lambda *a: taken.append(real(*a)) or taken[-1]
+        _busy(s)
+        L.beam_select(x, sc, 4, 8, stream=s)
+    finally:
+        _memory._allocate = real
+    old = taken[0].data_ptr(), taken[0].numel()
+    assert old[1] >= need
+    taken.clear()
+    blocks = [torch.empty(old[1], dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert not s.query()
+    assert not any(_overlap(b, *old) for b in blocks)
+    torch.cuda.synchronize()
