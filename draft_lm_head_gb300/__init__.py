@@ -22,7 +22,7 @@ from typing import Optional
 import torch
 
 from ._lib import LIB_PATH, LmheadError, check, load, status_string  # noqa: F401
-from ._memory import Workspace, scratch
+from ._memory import Workspace, result, scratch
 
 GLOBAL = 0
 LOCAL = 1
@@ -96,7 +96,7 @@ def project_u(B: torch.Tensor, h: torch.Tensor, out: Optional[torch.Tensor] = No
     r, d = B.shape
     M = h.shape[0]
     _check_shapes(B.device, h=(h, (M, d)), out=(out, (M, r)))
-    u = out if out is not None else torch.empty((M, r), dtype=torch.bfloat16, device=h.device)
+    u = out if out is not None else result((M, r), torch.bfloat16, h.device, stream)
     check(load().lmhead_project_u(_bf16(B, "B"), _bf16(h, "h"), d, r, M, _bf16(u, "u"),
                                   _stream_ptr(stream)), "project_u")
     return u
@@ -110,8 +110,8 @@ def lowrank_score_topk(mode: int, A: torch.Tensor, B: torch.Tensor, h: torch.Ten
     M = h.shape[0]
     _check_shapes(A.device, B=(B, (r, d)), h=(h, (M, d)), token_ids=(token_ids, (n,)))
     K = candidate_count(mode, n, C_or_tile, k_tile)
-    ids = torch.empty((M, K), dtype=torch.int32, device=h.device)
-    scores = torch.empty((M, K), dtype=torch.float32, device=h.device) if with_scores else None
+    ids = result((M, K), torch.int32, h.device, stream)
+    scores = result((M, K), torch.float32, h.device, stream) if with_scores else None
     nbytes = workspace_size(mode, n, d, r, M, C_or_tile, k_tile)
     ws = scratch(workspace, nbytes, h.device, stream)
     check(load().lmhead_lowrank_score_topk(
@@ -126,7 +126,7 @@ def gather_logits(W: torch.Tensor, h: torch.Tensor, ids: torch.Tensor,
     n, d = W.shape
     M, K = ids.shape
     _check_shapes(W.device, h=(h, (M, d)), ids=(ids, (M, K)), out=(out, (M, K)))
-    L = out if out is not None else torch.empty((M, K), dtype=torch.float32, device=h.device)
+    L = out if out is not None else result((M, K), torch.float32, h.device, stream)
     check(load().lmhead_gather_logits(_bf16(W, "W"), _bf16(h, "h"), _typed(ids, torch.int32, "ids"),
                                       n, d, M, K, _typed(L, torch.float32, "out"),
                                       _stream_ptr(stream)), "gather_logits")
@@ -137,7 +137,7 @@ def candidate_softmax(logits: torch.Tensor, temperature: float = 1.0,
                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     M, K = logits.shape
     _check_shapes(logits.device, out=(out, (M, K)))
-    q = out if out is not None else torch.empty_like(logits)
+    q = out if out is not None else result(logits.shape, logits.dtype, logits.device, stream)
     check(load().lmhead_candidate_softmax(_typed(logits, torch.float32, "logits"), M, K,
                                           float(temperature), _typed(q, torch.float32, "out"),
                                           _stream_ptr(stream)), "candidate_softmax")
@@ -153,9 +153,9 @@ def two_stage(mode: int, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, h: t
     M = h.shape[0]
     K = candidate_count(mode, n, C_or_tile, k_tile)
     if out is None:
-        ids = torch.empty((M, K), dtype=torch.int32, device=h.device)
-        L = torch.empty((M, K), dtype=torch.float32, device=h.device)
-        q = torch.empty((M, K), dtype=torch.float32, device=h.device)
+        ids = result((M, K), torch.int32, h.device, stream)
+        L = result((M, K), torch.float32, h.device, stream)
+        q = result((M, K), torch.float32, h.device, stream)
     else:
         ids, L, q = out
     _check_shapes(W.device, A=(A, (n, r)), B=(B, (r, d)), h=(h, (M, d)),
@@ -177,8 +177,8 @@ def dense_head(W: torch.Tensor, h: torch.Tensor, temperature: float = 1.0, with_
     n, d = W.shape
     M = h.shape[0]
     if out is None:
-        L = torch.empty((M, n), dtype=torch.float32, device=h.device)
-        q = torch.empty((M, n), dtype=torch.float32, device=h.device) if with_q else None
+        L = result((M, n), torch.float32, h.device, stream)
+        q = result((M, n), torch.float32, h.device, stream) if with_q else None
     else:
         L, q = out
     _check_shapes(W.device, h=(h, (M, d)), logits=(L, (M, n)), q=(q, (M, n)))
@@ -193,8 +193,8 @@ def pruned_head(W_pruned: torch.Tensor, h: torch.Tensor, temperature: float = 1.
     n_keep, d = W_pruned.shape
     M = h.shape[0]
     if out is None:
-        L = torch.empty((M, n_keep), dtype=torch.float32, device=h.device)
-        q = torch.empty((M, n_keep), dtype=torch.float32, device=h.device) if with_q else None
+        L = result((M, n_keep), torch.float32, h.device, stream)
+        q = result((M, n_keep), torch.float32, h.device, stream) if with_q else None
     else:
         L, q = out
     _check_shapes(W_pruned.device, h=(h, (M, d)), logits=(L, (M, n_keep)), q=(q, (M, n_keep)))
@@ -222,9 +222,9 @@ def shard_two_stage(W_shard: torch.Tensor, A_shard: torch.Tensor, B: torch.Tenso
     K = candidate_count(LOCAL, n_shard, T, k_tile)
     dev = h.device
     if out is None:
-        ids = torch.empty((M, K), dtype=torch.int32, device=dev)
-        L = torch.empty((M, K), dtype=torch.float32, device=dev)
-        stats = torch.empty((M, 2), dtype=torch.float32, device=dev)
+        ids = result((M, K), torch.int32, dev, stream)
+        L = result((M, K), torch.float32, dev, stream)
+        stats = result((M, 2), torch.float32, dev, stream)
     else:
         ids, L, stats = out
     _check_shapes(A_shard.device, W_shard=(W_shard, (n_shard, d)), B=(B, (r, d)), h=(h, (M, d)),
@@ -248,7 +248,7 @@ def shard_softmax(all_stats: torch.Tensor, logits: torch.Tensor, temperature: fl
     M, K = logits.shape
     G = all_stats.shape[0]
     _check_shapes(logits.device, all_stats=(all_stats, (G, M, 2)), out=(out, (M, K)))
-    q = out if out is not None else torch.empty_like(logits)
+    q = out if out is not None else result(logits.shape, logits.dtype, logits.device, stream)
     check(load().lmhead_shard_softmax(
         _typed(all_stats, torch.float32, "all_stats"), G, _typed(logits, torch.float32, "logits"),
         M, K, float(temperature), _typed(q, torch.float32, "out"), _stream_ptr(stream)),
@@ -291,15 +291,15 @@ def cluster_two_stage(W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, h: torc
     K = cluster_candidate_count(n, group, G)
     dev = h.device
     if out is None:
-        groups = torch.empty((M, G), dtype=torch.int32, device=dev)
-        ids = torch.empty((M, K), dtype=torch.int32, device=dev)
-        L = torch.empty((M, K), dtype=torch.float32, device=dev)
-        q = torch.empty((M, K), dtype=torch.float32, device=dev)
+        groups = result((M, G), torch.int32, dev, stream)
+        ids = result((M, K), torch.int32, dev, stream)
+        L = result((M, K), torch.float32, dev, stream)
+        q = result((M, K), torch.float32, dev, stream)
     else:
         groups, ids, L, q = out
     _check_shapes(W.device, A=(A, (n, r)), B=(B, (r, d)), h=(h, (M, d)), groups=(groups, (M, G)),
                   ids=(ids, (M, K)), logits=(L, (M, K)), q=(q, (M, K)))
-    gs = torch.empty((M, G), dtype=torch.float32, device=dev) if with_group_scores else None
+    gs = result((M, G), torch.float32, dev, stream) if with_group_scores else None
     nbytes = cluster_workspace_size(n, d, r, M, group, G)
     ws = scratch(workspace, nbytes, dev, stream)
     check(load().lmhead_cluster_two_stage(
@@ -322,11 +322,11 @@ def draft_select(q: torch.Tensor, ids: torch.Tensor, k_sel: int,
     dev = q.device
     _check_shapes(dev, ids=(ids, (M, K)), parent_value=(parent_value, (M,)),
                   uniforms=(uniforms, (M, K)))
-    top_ids = torch.empty((M, k_sel), dtype=torch.int32, device=dev)
-    top_q = torch.empty((M, k_sel), dtype=torch.float32, device=dev)
-    top_value = torch.empty((M, k_sel), dtype=torch.float32, device=dev)
-    sid = torch.empty(M, dtype=torch.int32, device=dev) if uniforms is not None else None
-    sq = torch.empty(M, dtype=torch.float32, device=dev) if uniforms is not None else None
+    top_ids = result((M, k_sel), torch.int32, dev, stream)
+    top_q = result((M, k_sel), torch.float32, dev, stream)
+    top_value = result((M, k_sel), torch.float32, dev, stream)
+    sid = result(M, torch.int32, dev, stream) if uniforms is not None else None
+    sq = result(M, torch.float32, dev, stream) if uniforms is not None else None
     check(load().lmhead_draft_select(
         _typed(q, torch.float32, "q"), _typed(ids, torch.int32, "ids"), M, K, k_sel,
         _typed(parent_value, torch.float32, "parent_value"),
@@ -347,8 +347,8 @@ def verify_chain(p: torch.Tensor, x: torch.Tensor, cand_ids: torch.Tensor, cand_
     dev = p.device
     _check_shapes(dev, x=(x, (B, Kd)), cand_ids=(cand_ids, (B, Kd, K)),
                   cand_q=(cand_q, (B, Kd, K)), r=(r, (B, Kd)), u=(u, (B, Kd + 1)))
-    tokens = torch.empty((B, Kd + 1), dtype=torch.int32, device=dev)
-    count = torch.empty(B, dtype=torch.int32, device=dev)
+    tokens = result((B, Kd + 1), torch.int32, dev, stream)
+    count = result(B, torch.int32, dev, stream)
     check(load().lmhead_verify_chain(
         _typed(p, torch.float32, "p"), n, B, Kd, _typed(x, torch.int32, "x"),
         _typed(cand_ids, torch.int32, "cand_ids"), _typed(cand_q, torch.float32, "cand_q"), K,

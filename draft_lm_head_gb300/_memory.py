@@ -1,4 +1,4 @@
-"""Device memory of the calls: workspaces."""
+"""Device memory of the calls: results and workspaces."""
 from __future__ import annotations
 
 import torch
@@ -23,6 +23,19 @@ def _allocate(nbytes: int, device, stream) -> torch.Tensor:
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def result(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor for a call's result. One of a call on an explicit stream is
+    of that stream's pool too (one of the current stream's may be memory that the
+    current stream is not done with), and the current stream, where the
+    caller goes on with it, is named to the allocator."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 class Workspace:

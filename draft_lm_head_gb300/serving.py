@@ -18,7 +18,7 @@ from typing import NamedTuple, Optional, Sequence
 import torch
 
 from ._lib import check, load
-from ._memory import scratch, stream_handle
+from ._memory import result, scratch, stream_handle
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -58,15 +58,6 @@ def _cuda(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """A new tensor that the call's stream may use: one that is not the current
-    stream has to be named to the allocator."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def page_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor,
               free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int, max_tokens: int,
               out: Optional[PagePlan] = None, stream=None) -> PagePlan:
@@ -82,7 +73,7 @@ def page_plan(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor,
         if max_tokens < 1 or S < 1:
             raise ValueError("max_tokens: must be positive, as must the number of requests")
         # one allocation, its parts one behind the other
-        buf = _empty(2 * max_tokens + 2 * S + 2, i32, dev, stream)
+        buf = result(2 * max_tokens + 2 * S + 2, i32, dev, stream)
         at = buf.data_ptr()
         ptrs = (at, at + 4 * max_tokens, at + 8 * max_tokens, at + 8 * max_tokens + 4 * (S + 1),
                 at + 8 * max_tokens + 4 * (2 * S + 1))
@@ -166,9 +157,9 @@ def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         q_head = 0
     o, lse = out if isinstance(out, (tuple, list)) else (out, None)
     if o is None:
-        o = _empty((T, heads, dim), dt, dev, stream)
+        o = result((T, heads, dim), dt, dev, stream)
     if lse is None and with_lse:
-        lse = _empty((T, heads), torch.float32, dev, stream)
+        lse = result((T, heads), torch.float32, dev, stream)
     if slots is not None and slots.shape[0] != T:
         # a plan's buffers may be longer than the step's tokens
         if slots.dim() != 1 or slots.shape[0] < T:
@@ -201,7 +192,7 @@ def _q4(name, codes, scales, h, ids, group, mins, out, stream):
         raise ValueError(f"group: must be 32, 64 or 128 and divide d = {d}, got {group}")
     K = n if ids is None else ids.shape[1]
     if out is None:
-        out = _empty((M, K), torch.float32, dev, stream)
+        out = result((M, K), torch.float32, dev, stream)
     args = [_DTYPES[dt], _dense(codes, torch.uint8, (n, d // 2), dev, "codes"),
             _dense(scales, dt, (n, d // group), dev, "scales"),
             _dense(mins, dt, (n, d // group), dev, "mins"), _dense(h, dt, (M, d), dev, "h")]
@@ -266,8 +257,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, k: int,
     S = rows // beams
     i32 = torch.int32
     if out is None:
-        parent, token = _empty((S, k), i32, dev, stream), _empty((S, k), i32, dev, stream)
-        score = _empty((S, k), torch.float32, dev, stream)
+        parent, token = result((S, k), i32, dev, stream), result((S, k), i32, dev, stream)
+        score = result((S, k), torch.float32, dev, stream)
         ptrs = (parent.data_ptr(), token.data_ptr(), score.data_ptr())
     else:
         parent, token, score = out
@@ -307,7 +298,7 @@ def beam_reorder(parent: torch.Tensor, states: Sequence[torch.Tensor], beams: in
         if t.dim() < 1 or shape[0] != rows or t.device != dev or not t.is_contiguous():
             raise ValueError(f"states[{i}]: expected {rows} contiguous rows on {dev}")
         want = (S * k, *shape[1:])
-        o = out[i] if out is not None else _empty(want, dt, dev, stream)
+        o = out[i] if out is not None else result(want, dt, dev, stream)
         res.append(o)
         table[i] = t.data_ptr()
         table[8 + i] = _dense(o, dt, want, dev, "out") if out is not None else o.data_ptr()

@@ -100,3 +100,45 @@ def test_scratch_of_a_call_on_a_busy_stream():
     assert not s.query()
     assert not any(_overlap(b, *old) for b in blocks)
     torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_results_of_a_call_on_another_stream():
+    """Memory that the current stream is not done with is not taken for the
+    result of a call on another stream; nor is such a result's own memory while
+    the current stream still reads it."""
+    from gpu_util import lib
+    lib()
+    g = torch.Generator("cuda").manual_seed(0)
+    codes = torch.randint(0, 256, (60000, 128), device="cuda", dtype=torch.uint8, generator=g)
+    scales = torch.rand(60000, 4, device="cuda", generator=g).to(torch.bfloat16)
+    h = torch.randn(8, 256, device="cuda", generator=g).to(torch.bfloat16)
+    want = L.q4_head(codes, scales, h, 64)
+    cur, s = torch.cuda.current_stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # blocks in both pools, so that no call below has to ask the driver (which waits)
+    for at in (cur, s):
+        with torch.cuda.stream(at):
+            blocks = [torch.empty_like(want) for _ in range(4)]
+            del blocks
+    # a tensor that the current stream writes late, freed before the call
+    kept, y = torch.empty_like(want), torch.empty_like(want)
+    _busy(cur)
+    y.zero_()
+    old = y.data_ptr(), y.numel() * 4
+    del y
+    out = L.q4_head(codes, scales, h, 64, stream=s)
+    assert not cur.query() and not _overlap(out, *old)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    # the result, read late by the current stream and freed before the next call
+    h2 = h * 2
+    torch.cuda.synchronize()
+    _busy(cur)
+    kept.copy_(out)
+    old = out.data_ptr(), out.numel() * 4
+    del out
+    again = L.q4_head(codes, scales, h2, 64, stream=s)
+    assert not cur.query() and not _overlap(again, *old)
+    torch.cuda.synchronize()
+    assert torch.equal(kept, want)
