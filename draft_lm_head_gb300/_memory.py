@@ -67,6 +67,11 @@ def scratch(workspace, nbytes: int, device, stream) -> torch.Tensor:
     if workspace is None:
         return _allocate(nbytes, device, stream)
     if isinstance(workspace, torch.Tensor):
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on {device}, got one on "
+                             f"{workspace.device} (contiguous={workspace.is_contiguous()})")
+        if workspace.dtype is not torch.uint8:
+            workspace = workspace.view(torch.uint8)  # callers count bytes
         if stream is not None:
             workspace.record_stream(stream)
         return workspace

@@ -32,6 +32,16 @@ def test_scratch_is_named_to_the_allocator():
     assert ws.buf.seen == [a, b]
 
 
+def test_workspace_tensors_are_checked():
+    cpu, meta = torch.device("cpu"), torch.device("meta")
+    t = torch.zeros(1024, dtype=torch.uint8)
+    assert _memory.scratch(t, 512, cpu, None) is t
+    assert _memory.scratch(torch.zeros(256), 512, cpu, None).numel() == 1024
+    for bad, dev in ((t, meta), (t[::2], cpu), (torch.zeros(32, 32).t(), cpu)):
+        with pytest.raises(ValueError, match="workspace"):
+            _memory.scratch(bad, 512, dev, None)
+
+
 def _overlap(a: torch.Tensor, ptr: int, nbytes: int) -> bool:
     return a.data_ptr() < ptr + nbytes and ptr < a.data_ptr() + a.numel() * a.element_size()
 
