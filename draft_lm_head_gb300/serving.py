@@ -23,6 +23,10 @@ from ._memory import result, scratch, stream_handle
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+# the current device's index without torch.cuda's checks around it
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 class PagePlan(NamedTuple):
     slots: torch.Tensor
     positions: torch.Tensor
@@ -55,6 +59,10 @@ def _dense(t: Optional[torch.Tensor], dtype, shape, device, name: str) -> int:
 def _cuda(t: torch.Tensor, name: str) -> torch.device:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
+    # launches, the error word and the library's per-device state are the current
+    # device's: another device's stream and addresses must not meet them
+    if t.device.index != _current_device():
+        raise ValueError(f"{name}: on {t.device}, which is not the current device")
     return t.device
 
 

@@ -42,6 +42,24 @@ def test_workspace_tensors_are_checked():
             _memory.scratch(bad, 512, dev, None)
 
 
+class Elsewhere(torch.Tensor):
+    """A host tensor that says to be on the second GPU."""
+    is_cuda = property(lambda self: True)
+    device = property(lambda self: torch.device("cuda", 1))
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    from draft_lm_head_gb300 import serving
+    monkeypatch.setattr(serving, "_current_device", lambda: 0)
+    x = torch.zeros(4, 4).as_subclass(Elsewhere)
+    i = torch.zeros(4, dtype=torch.int32)
+    for call in (lambda: L.page_plan(x, i, i, i, i, 16, 4), lambda: L.chunk_attention(x, x, x, i, i, i),
+                 lambda: L.q4_head(i, x, x, 32), lambda: L.q4_gather_logits(i, x, x, i, 32),
+                 lambda: L.beam_select(x, x, 2, 2), lambda: L.beam_reorder(x, [x], 2)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
 def _overlap(a: torch.Tensor, ptr: int, nbytes: int) -> bool:
     return a.data_ptr() < ptr + nbytes and ptr < a.data_ptr() + a.numel() * a.element_size()
 
