@@ -49,6 +49,10 @@ SIGNATURES = {
                                     _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I, _P, _I,
                                     _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ,
                                     _P]),
+    "lmhead_chunk_attention_granted": (
+        _I, [_I, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64,
+             _I64, _I64, _I64, _I, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P,
+             _P, _SZ, _P]),
     "lmhead_q4_head": (_I, [_I, _P, _P, _P, _P, _I64, _I, _I, _I, _P, _P]),
     "lmhead_q4_gather_logits": (_I, [_I, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P]),
     "lmhead_beam_workspace_size": (_SZ, [_I, _I, _I64, _I]),

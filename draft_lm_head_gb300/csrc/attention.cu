@@ -58,9 +58,10 @@ constexpr int kPrepThreads = 256;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// What becomes of a request's rows: kFillNan those of one whose lengths the
-// table has no room for.
-enum Fate { kAttend, kFillNan };
+// What becomes of a request's rows: kFillZero those of one that was refused (its
+// pages were never taken, so there is nothing to read), kFillNan those of one
+// whose lengths the table has no room for.
+enum Fate { kAttend, kFillZero, kFillNan };
 
 // An item: up to two row tiles of one request, for every K/V head alike. One of
 // rows that are only filled has no key blocks.
@@ -144,6 +145,7 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int s, bool& sa
   // are keep all arithmetic on them in 32 bits)
   r.seen = a.tree ? min(r.m, 64) : r.m;
   r.fate = r.len >= 0 && r.len <= (a.width << a.page_shift) - r.seen ? kAttend : kFillNan;
+  if (a.granted && a.granted[s] == 0) r.fate = kFillZero;
   if (r.fate != kAttend) r.len = 0;
   return r;
 }
@@ -200,7 +202,7 @@ __device__ void make_plan(const AttnArgs& a, const Scratch& sc, int most_parts, 
       }
       if (n > 0 && req.fate != kAttend) {
         sh_fill = 1;
-        record_error(err, kDevErrBadId);
+        if (req.fate == kFillNan) record_error(err, kDevErrBadId);
       }
     }
     int sn = n;
@@ -558,13 +560,13 @@ __device__ void join_rows(const AttnArgs& a, const Scratch& sc, const Cursor& cu
 
 // One row of the output and its log-sum-exp that were not computed, by a warp.
 template <bool BF16, int D>
-__device__ __forceinline__ void fill_row(const AttnArgs& a, int64_t row, float v) {
+__device__ __forceinline__ void fill_row(const AttnArgs& a, int64_t row, float v, float lse) {
   const int lane = threadIdx.x & 31;
   const uint32_t two = pack2<BF16>(v, v);
   if (lane < D / 8)
     *reinterpret_cast<uint4*>(static_cast<char*>(a.out) + (row * D + lane * 8) * 2) =
         make_uint4(two, two, two, two);
-  if (lane == 0 && a.lse) a.lse[row] = v;
+  if (lane == 0 && a.lse) a.lse[row] = lse;
 }
 
 // The CTA's share of the rows that are only filled, by eight warps.
@@ -574,17 +576,18 @@ __device__ __forceinline__ void fill_rows(const AttnArgs& a, const Scratch& sc, 
   if (sc.head->fill == kFillAll) {
     const int64_t rows = (int64_t)a.T * a.heads;
     for (int64_t r = (int64_t)blockIdx.x * 8 + warp; r < rows; r += (int64_t)gridDim.x * 8)
-      fill_row<BF16, D>(a, r, nan);
+      fill_row<BF16, D>(a, r, nan, nan);
   }
   const int group = a.heads / a.kv_heads;
   Cursor cur;
   cur.init(sc, blockIdx.x);
   while (cur.next<true>()) {
     if (cur.it.nblk > 0) continue;
+    const bool zero = cur.it.fate == kFillZero;
     for (int i = warp; i < cur.it.ntok * group; i += 8) {
       const int tk = i / group;
       fill_row<BF16, D>(a, (int64_t)(cur.it.tok0 + tk) * a.heads + cur.p_hk * group + i - tk * group,
-                        nan);
+                        zero ? 0.f : nan, zero ? kNegInf : nan);
     }
   }
 }

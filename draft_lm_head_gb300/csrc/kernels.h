@@ -169,7 +169,7 @@ struct AttnArgs {
   CacheStrides ks, vs;
   int64_t pages;
   int page_shift;  // log2 of the page size
-  const int32_t *table, *lens, *cu, *slots;
+  const int32_t *table, *lens, *cu, *granted, *slots;  // granted: or nullptr
   int width, S, T, heads, kv_heads, dim, window;
   const uint64_t* tree;
   float scale;

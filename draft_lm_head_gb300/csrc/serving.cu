@@ -107,6 +107,21 @@ int lmhead_chunk_attention(int dtype, const void* q, int64_t q_tok, int64_t q_he
                            int kv_heads, int dim, int window, float scale, void* out,
                            float* out_lse, void* workspace, size_t workspace_bytes,
                            lmhead_stream stream) {
+  return lmhead_chunk_attention_granted(
+      dtype, q, q_tok, q_head, k, k_tok, k_head, v, v_tok, v_head, k_cache, kc_page, kc_token,
+      kc_head, v_cache, vc_page, vc_token, vc_head, pages, page_size, table, width, lens, cu,
+      nullptr, slots, tree, S, T, heads, kv_heads, dim, window, scale, out, out_lse, workspace,
+      workspace_bytes, stream);
+}
+
+int lmhead_chunk_attention_granted(
+    int dtype, const void* q, int64_t q_tok, int64_t q_head, const void* k, int64_t k_tok,
+    int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, void* k_cache, int64_t kc_page,
+    int64_t kc_token, int64_t kc_head, void* v_cache, int64_t vc_page, int64_t vc_token,
+    int64_t vc_head, int64_t pages, int page_size, const int32_t* table, int width,
+    const int32_t* lens, const int32_t* cu, const int32_t* granted, const int32_t* slots,
+    const uint64_t* tree, int S, int T, int heads, int kv_heads, int dim, int window, float scale,
+    void* out, float* out_lse, void* workspace, size_t workspace_bytes, lmhead_stream stream) {
   if (!q || !k_cache || !v_cache || !table || !lens || !cu || !out) return LMHEAD_ERR_NULL;
   if ((k == nullptr) != (v == nullptr) || (k && !slots)) return LMHEAD_ERR_NULL;
   if (dtype != LMHEAD_BF16 && dtype != LMHEAD_FP16) return LMHEAD_ERR_UNSUPPORTED;
@@ -154,6 +169,7 @@ int lmhead_chunk_attention(int dtype, const void* q, int64_t q_tok, int64_t q_he
   a.table = table;
   a.lens = lens;
   a.cu = cu;
+  a.granted = granted;
   a.slots = slots;
   a.width = width;
   a.S = S;

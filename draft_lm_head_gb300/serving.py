@@ -2,7 +2,8 @@
 operators around the head").
 
     plan = page_plan(lens, new_lens, table, free_pages, free_count, P, max_tokens)
-    o = chunk_attention(q, k_cache, v_cache, table, lens, plan.cu, k=k, v=v, slots=plan.slots)
+    o = chunk_attention(q, k_cache, v_cache, table, lens, plan.cu, k=k, v=v, slots=plan.slots,
+                        granted=plan.granted)
     logits = q4_gather_logits(codes, scales, h, ids, group)
     parent, token, score = beam_select(logits, scores, beams, k, ids=ids)
     h, table = beam_reorder(parent, [h, table], beams)
@@ -125,13 +126,15 @@ def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
                     slots: Optional[torch.Tensor] = None, tree: Optional[torch.Tensor] = None,
                     window: int = 0, scale: Optional[float] = None, with_lse: bool = False,
-                    workspace=None, out=None, stream=None):
+                    workspace=None, out=None, stream=None,
+                    granted: Optional[torch.Tensor] = None):
     """Attention of T new tokens (q: T x heads x dim) over the paged caches
     (pages x page_size x kv_heads x dim, any strides with dim contiguous), after
     writing k and v (T x kv_heads x dim) to `slots`, if given. lens: tokens
     cached before; cu: starts of the requests' tokens. Causal within a request,
     over the last `window` keys if window > 0, or by `tree` (int64 bits of the
-    new tokens each new token sees, besides all cached ones). Returns out, or
+    new tokens each new token sees, besides all cached ones). granted: a plan's (0:
+    the request was refused; its rows are zero, its lse -inf). Returns out, or
     (out, lse) with with_lse or when `out` is such a pair (see
     lmhead_chunk_attention)."""
     dev = _cuda(q, "q")
@@ -175,11 +178,12 @@ def chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         slots = slots[:T]
     i32 = torch.int32
     ws = scratch(workspace, _attention_bytes(dev, S, T, heads, kv_heads, dim), dev, stream)
-    check(load().lmhead_chunk_attention(
+    check(load().lmhead_chunk_attention_granted(
         _DTYPES[dt], qa, q_tok, q_head, ka, k_tok, k_head, va, v_tok, v_head, kca, kc_page, kc_tok,
         kc_head, vca, vc_page, vc_tok, vc_head, pages, P,
         _dense(table, i32, (S, width), dev, "table"), width, _dense(lens, i32, (S,), dev, "lens"),
-        _dense(cu, i32, (S + 1,), dev, "cu"), _dense(slots, i32, (T,), dev, "slots"),
+        _dense(cu, i32, (S + 1,), dev, "cu"), _dense(granted, i32, (S,), dev, "granted"),
+        _dense(slots, i32, (T,), dev, "slots"),
         _dense(tree, torch.int64, (T,), dev, "tree"), S, T, heads, kv_heads, dim, window,
         dim ** -0.5 if scale is None else scale, _dense(o, dt, (T, heads, dim), dev, "out"),
         _dense(lse, torch.float32, (T, heads), dev, "lse"), ws.data_ptr(), ws.numel(),

@@ -55,12 +55,12 @@ class Drafter:
         self.out = rand(heads * dim, d)
         self.ws = L.Workspace()
 
-    def attend(self, x, cache, table, lens, cu, slots):
+    def attend(self, x, cache, table, lens, cu, slots, granted=None):
         """x (tokens x d) through the layer, its K and V into the cache."""
         H, Hk, D = self.heads, self.kv_heads, self.dim
         qkv = (x @ self.qkv).view(-1, H + 2 * Hk, D)
         o = L.chunk_attention(qkv[:, :H], cache[0], cache[1], table, lens, cu, k=qkv[:, H:H + Hk],
-                              v=qkv[:, H + Hk:], slots=slots, workspace=self.ws)
+                              v=qkv[:, H + Hk:], slots=slots, workspace=self.ws, granted=granted)
         return x + o.view(-1, H * D) @ self.out
 
     def candidates(self, h):
@@ -90,7 +90,7 @@ def draft(model, prompts, beams, steps, page=16):
     free = torch.arange(pool, dtype=I32, device=dev)
     plan = L.page_plan(i32([0] * S), i32(lens), table, free, i32([pool]), page, sum(lens))
     x = model.embed[torch.tensor(sum(prompts, []), device=dev)]
-    h = model.attend(x, cache, table, i32([0] * S), plan.cu, plan.slots)
+    h = model.attend(x, cache, table, i32([0] * S), plan.cu, plan.slots, plan.granted)
     h = h[(plan.cu[1:] - 1).long()]                        # of each prompt's last token
 
     # ---- tables of the beams, for either set of tail pages

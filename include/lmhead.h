@@ -461,6 +461,19 @@ int lmhead_chunk_attention(int dtype, const void* q, int64_t q_tok, int64_t q_he
                            int kv_heads, int dim, int window, float scale, void* out,
                            float* out_lse, void* workspace, size_t workspace_bytes,
                            lmhead_stream stream);
+/* The same with lmhead_page_plan's out_granted (S int32, or NULL: all are): the
+ * rows of a request whose entry is 0 are 0 and -inf, and neither its table nor
+ * any page is read for it. A plan counts a refused request's tokens in out_cu and
+ * leaves its table entries as they were, so a call without `granted` attends
+ * for it over whatever pages those name. */
+int lmhead_chunk_attention_granted(
+    int dtype, const void* q, int64_t q_tok, int64_t q_head, const void* k, int64_t k_tok,
+    int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, void* k_cache, int64_t kc_page,
+    int64_t kc_token, int64_t kc_head, void* v_cache, int64_t vc_page, int64_t vc_token,
+    int64_t vc_head, int64_t pages, int page_size, const int32_t* table, int width,
+    const int32_t* lens, const int32_t* cu, const int32_t* granted, const int32_t* slots,
+    const uint64_t* tree, int S, int T, int heads, int kv_heads, int dim, int window, float scale,
+    void* out, float* out_lse, void* workspace, size_t workspace_bytes, lmhead_stream stream);
 
 /*
  * The head with 4-bit weights: row i is s * (c - 8) (mins NULL) or s * c + min

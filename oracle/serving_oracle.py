@@ -70,10 +70,11 @@ def q4_rows(codes, scales, mins, group):
     return w.reshape(codes.shape[0], -1)
 
 
-def chunk_attention(q, k_cache, v_cache, table, lens, cu, scale, window=0, tree=None):
+def chunk_attention(q, k_cache, v_cache, table, lens, cu, scale, window=0, tree=None, granted=None):
     """q T x H x D, caches pages x P x Hk x D (the chunk's own K and V already in
     them), all fp64. Returns (out, lse, magnitude, reach): magnitude is sum_j
-    p_j |v_j| and reach max_j scale sum_d |q_d k_jd| over the visible keys."""
+    p_j |v_j| and reach max_j scale sum_d |q_d k_jd| over the visible keys. Requests
+    with granted 0 see none."""
     T, H, D = q.shape
     P, Hk = k_cache.shape[1], k_cache.shape[2]
     G = H // Hk
@@ -81,6 +82,8 @@ def chunk_attention(q, k_cache, v_cache, table, lens, cu, scale, window=0, tree=
     lse, reach = np.full((T, H), -np.inf), np.zeros((T, H))
     for s in range(len(lens)):
         l, m = int(lens[s]), int(cu[s + 1] - cu[s])
+        if granted is not None and not granted[s]:
+            continue
         j = np.arange(l + m)
         slot = np.asarray(table[s])[j // P].astype(np.int64) * P + j % P
         K = k_cache.reshape(-1, Hk, D)[slot]

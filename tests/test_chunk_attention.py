@@ -394,3 +394,67 @@ def test_lengths_that_no_table_holds(mask, len_of):
     for got, want in ((out, good), (lse, gl)):
         assert torch.equal(got[:2], want[:2]) and torch.equal(got[72:], want[72:])
     assert L.last_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("stale", [True, False])
+@pytest.mark.parametrize("mask", ["causal", "tree"])
+def test_refused_requests_of_a_plan(mask, stale):
+    """A plan whose pool runs out, into attention: the granted requests' rows are
+    right, the refused ones' are zero and -inf, nothing is recorded, whether the
+    table names other requests' pages in their places or none."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    P, H, Hk, D = 16, 8, 2, 64
+    rng = np.random.default_rng(3)
+    lens, new = [30, 5, 0, 64, 17, 200], [2, 300, 40, 1, 60, 8]
+    held = [-(-l // P) for l in lens]
+    ids = rng.permutation(120)
+    table = np.full((6, 24), -1)
+    if stale:
+        table[:] = ids[:24]
+    at = 0
+    for s, n in enumerate(held):
+        table[s, :n] = ids[at:at + n]
+        at += n
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    tab, T = i32(table), sum(new)
+    # 19 pages are wanted by the second request and 18 are there
+    plan = L.page_plan(i32(lens), i32(new), tab, i32(ids[at:]), i32([18]), P, T)
+    ok = plan.granted.cpu().numpy()
+    assert 0 < ok.sum() < 6
+    g = torch.Generator("cuda").manual_seed(0)
+    kc, vc = (torch.randn(120, P, Hk, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    qkv = torch.randn(T, H + 2 * Hk, D, generator=g, device="cuda").to(torch.bfloat16)
+    tree = None
+    if mask == "tree":
+        tree = torch.tensor(rng.integers(0, 1 << 62, T), dtype=torch.int64, device="cuda")
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:]
+    out = (torch.full((T, H, D), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((T, H), 7.0, device="cuda"))
+    L.chunk_attention(q, kc, vc, tab, i32(lens), plan.cu, k=k, v=v, slots=plan.slots, tree=tree, out=out,
+                      granted=plan.granted)
+    assert L.last_device_error() == 0
+    n64 = lambda x: x.double().cpu().numpy()
+    tr = None if tree is None else tree.cpu().numpy()
+    cu = plan.cu.cpu().numpy()
+    want, wl, A, R = SO.chunk_attention(n64(q), n64(kc), n64(vc), tab.cpu().numpy(), lens, cu, D ** -0.5, 0, tr, ok)
+    got, gl = n64(out[0]), n64(out[1])
+    u = 2.0 ** -8
+    delta = (D + 4) * 2.0 ** -23 * R
+    rel = 2 * delta + 2.0 ** -20 + 2.0 ** -22 * R + 2 * 520 * 2.0 ** -23
+    tol = (u + rel[..., None] * (1 + u)) * A
+    assert np.all(np.abs(got - want) <= tol + u * (np.abs(want) + tol))
+    live = np.isfinite(wl)
+    assert np.array_equal(live, np.isfinite(gl))
+    assert np.all(np.abs(gl - np.where(live, wl, 0))[live] <= (
+        delta + 2.0 ** -20 + 2.0 ** -22 * R + 520 * 2.0 ** -23 + 2.0 ** -23 * np.abs(np.where(live, wl, 0)))[live])
+    for s in range(6):
+        if not ok[s]:
+            rows = slice(cu[s], cu[s + 1])
+            assert not out[0][rows].any() and torch.all(out[1][rows] == -float("inf"))
+    # none granted
+    L.chunk_attention(q, kc, vc, tab, i32(lens), plan.cu, out=out, granted=torch.zeros_like(plan.granted))
+    assert not out[0].any() and torch.all(out[1] == -float("inf")) and L.last_device_error() == 0
+    with pytest.raises(ValueError, match="granted"):
+        L.chunk_attention(q, kc, vc, tab, i32(lens), plan.cu, granted=plan.granted[1:])
