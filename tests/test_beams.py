@@ -231,3 +231,45 @@ def test_reorder():
         L.beam_reorder(parent, [], B)
     with pytest.raises(ValueError, match="states"):
         L.beam_reorder(parent, [states[0][1:]], B)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("climb", [1.5, 3, 10, 20, 30, 45, 59.5, 200])
+def test_rows_that_climb(climb, dtype):
+    """Few values at 0 to 1 in a row's first tile, and two far above them in a late
+    one that decide the sum, in a row of one slice.
+
+    A value may lie 1 above the reference that its exponential is taken from (and no
+    value matters that lies far below the top: z e^-z < 1). An exponential is within
+    2^-22, its argument is rounded three times (difference, product, the factor
+    itself: 2^-24 of its size each), and the same goes for the scaling of a lane's
+    sum to its warp's and of a slice's to its row's, and for two moves of the
+    reference. With at most four values a lane every sum is rounded four times in it."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    g = torch.Generator("cuda").manual_seed(int(climb * 10))
+    R, n = 4000, 6000
+    x = torch.full((R, n), -np.inf, device="cuda")
+    first = torch.arange(0, 512, 4, device="cuda")
+    x[:, first] = torch.rand(R, 128, generator=g, device="cuda")
+    x[:, 3200] = climb + torch.rand(R, generator=g, device="cuda")
+    x[:, 3205] = climb + torch.rand(R, generator=g, device="cuda")
+    x = x.to(getattr(torch, dtype))
+    scores = -torch.rand(R, generator=g, device="cuda")
+    parent, token, score = L.beam_select(x, scores, 2, 3)
+    x64 = x.double()
+    want = scores.double()[:, None] + (x64 - torch.logsumexp(x64, 1, keepdim=True))
+    want, flat = want.view(R // 2, 2 * n).topk(4, dim=1)
+    tol = 5 * (2.0 ** -22 + 3 * 2.0 ** -24) + 4 * 2.0 ** -24
+    off = (score.double() - want[:, :3]).abs() - 2.0 ** -24 * want[:, :3].abs()
+    assert off.max().item() <= tol, (off.max().item(), tol)
+    # where the scores are that far apart, so is their order
+    got = parent.long() * n + token.long()
+    alone = torch.ones_like(got, dtype=torch.bool)
+    gap = want[:, :3] - want[:, 1:]
+    wide = 2 * (tol + 2.0 ** -24 * want[:, 1:].abs())
+    alone &= gap > wide
+    alone[:, 1:] &= (gap > wide)[:, :2]
+    assert torch.equal(got[alone], flat[:, :3][alone])
