@@ -79,7 +79,8 @@ int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_
                      const int32_t* free_count, int page_size, int max_tokens,
                      int32_t* out_slots, int32_t* out_positions, int32_t* out_cu,
                      int32_t* out_granted, int32_t* out_free_left, lmhead_stream stream) {
-  if (!lens || !new_lens || !table || !free_pages || !free_count || !out_slots ||
+  // (an empty list of free pages may have no address)
+  if (!lens || !new_lens || !table || (!free_pages && free_cap != 0) || !free_count || !out_slots ||
       !out_positions || !out_cu || !out_granted || !out_free_left)
     return LMHEAD_ERR_NULL;
   if (S < 1 || S > kMaxRows || width < 1 || free_cap < 0 || page_size < 1 || page_size > 65536 ||

@@ -391,7 +391,8 @@ int lmhead_shard_softmax(const float* all_stats, int G, const float* logits, int
  *   free_pages  int32 page ids, a stack whose first *free_count entries
  *               (at most free_cap) are free. Pages are taken from its top in
  *               request order: page j of a request whose predecessors need e
- *               pages is free_pages[*free_count - 1 - e - j].
+ *               pages is free_pages[*free_count - 1 - e - j]. May be NULL with
+ *               free_cap 0.
  *   max_tokens  capacity of out_slots and out_positions.
  *   out_slots   max_tokens int32: page * page_size + offset of each new
  *               token, request after request; -1 for tokens of a request that

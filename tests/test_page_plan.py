@@ -119,3 +119,13 @@ def test_other_stream_and_reused_buffers():
         L.page_plan(lens, new[:1], a, free, count, 16, 30)
     with pytest.raises(TypeError, match="table"):
         L.page_plan(lens, new, a.t().contiguous().t(), free, count, 16, 30)
+
+
+@pytest.mark.gpu
+def test_empty_list_of_free_pages():
+    """Requests that stay within the pages they hold are granted, the others are
+    not; an empty tensor has no address."""
+    table = np.arange(12).reshape(4, 3)
+    for count in (0, 5):
+        L = _run([4, 16, 30, 0], [3, 1, 2, 0], table, np.zeros(0, dtype=np.int32), count, 16, 8)
+        assert L.last_device_error() == 0
