@@ -18,6 +18,11 @@ constexpr int kMaxDim = 65536;
 inline bool aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
+// Do two ranges of bytes have one in common?
+inline bool meet(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
 inline int status(cudaError_t e) { return e == cudaSuccess ? LMHEAD_OK : LMHEAD_ERR_CUDA; }
 
 // Strides of a tensor read 16 bytes at a time: non-negative multiples of 8
@@ -258,6 +263,16 @@ int lmhead_beam_reorder(const int32_t* parent, int S, int beams, int k, int coun
     a.src[i] = src[i];
     a.dst[i] = dst[i];
     a.bytes[i] = row_bytes[i];
+  }
+  // what one CTA writes is read by no other: moving rows within one buffer, as any
+  // destination that meets a source, the parents or another destination, is refused
+  const int64_t from = (int64_t)S * beams, to = (int64_t)S * k;
+  for (int i = 0; i < count; ++i) {
+    if (meet(dst[i], to * row_bytes[i], parent, to * 4)) return LMHEAD_ERR_SHAPE;
+    for (int j = 0; j < count; ++j)
+      if (meet(dst[i], to * row_bytes[i], src[j], from * row_bytes[j]) ||
+          (i != j && meet(dst[i], to * row_bytes[i], dst[j], to * row_bytes[j])))
+        return LMHEAD_ERR_SHAPE;
   }
   a.count = count;
   a.S = S;

@@ -521,7 +521,8 @@ int lmhead_beam_select(int dtype, const void* logits, int64_t row_stride, const 
 /*
  * The states of the chosen beams: for each of `count` (1..8) state tensors,
  * dst[s, j] = src[s, parent[s, j]], rows of row_bytes[i] bytes, src S*beams
- * rows, dst S*k rows (not overlapping src). parent -1 gives zeros; any other
+ * rows, dst S*k rows (LMHEAD_ERR_SHAPE where one meets a src, another dst or
+ * parent). parent -1 gives zeros; any other
  * value outside 0..beams-1 does too and records LMHEAD_ERR_DEVICE_CHECK.
  *   src, dst, row_bytes  HOST arrays of `count` device pointers and sizes.
  */

@@ -273,3 +273,33 @@ def test_rows_that_climb(climb, dtype):
     alone &= gap > wide
     alone[:, 1:] &= (gap > wide)[:, :2]
     assert torch.equal(got[alone], flat[:, :3][alone])
+
+
+def test_reorder_within_a_buffer_is_refused():
+    """S = 2, 4 beams, k = 3: 8 source rows and 6 destination rows of 64 bytes."""
+    from draft_lm_head_gb300 import build, _lib
+    build.build()
+    re = _lib.load().lmhead_beam_reorder
+    at = lambda *x: (ctypes.c_void_p * len(x))(*x)
+    size = (ctypes.c_int64 * 2)(64, 64)
+    A, B, PARENT = 1 << 20, 1 << 21, 1 << 22
+    for dst in (A, A + 511, A - 383, PARENT + 23, PARENT - 383):
+        assert re(PARENT, 2, 4, 3, 1, at(A), at(dst), size, None) == -2
+    assert re(PARENT, 2, 4, 3, 2, at(A, B), at(3 * A, B - 383), size, None) == -2    # the other's source
+    assert re(PARENT, 2, 4, 3, 2, at(A, B), at(3 * A, 3 * A + 383), size, None) == -2  # the other's destination
+
+
+@pytest.mark.gpu
+def test_reorder_next_to_its_source():
+    """Destinations that begin where a source ends."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    buf = torch.arange(8 * 16 + 6 * 16, device="cuda", dtype=torch.int32)
+    parent = torch.tensor([[3, 0, -1], [1, 1, 2]], device="cuda", dtype=torch.int32)
+    src, dst = buf[:128].view(8, 16), buf[128:].view(6, 16)
+    want = torch.cat([src[3:4], src[:1], torch.zeros_like(src[:1]), src[5:6], src[5:6], src[6:7]])
+    got, = L.beam_reorder(parent, [src], 4, out=[dst])
+    assert torch.equal(got, want)
+    with pytest.raises(L.LmheadError):
+        L.beam_reorder(parent, [src], 4, out=[src[2:]])
