@@ -485,7 +485,11 @@ int lmhead_chunk_attention_granted(
  *   lmhead_q4_head: out_logits M x n fp32, every row.
  *   lmhead_q4_gather_logits: out_logits M x K fp32, row ids[m, j] (an id
  *           outside [0, n) gives NaN and LMHEAD_ERR_DEVICE_CHECK).
- * Codes are exact, products are summed in fp32, scales applied in fp32.
+ * Codes are exact, products are summed in fp32, scales applied in fp32. h is held
+ * in fp16 relative to each vector's largest element: all bits of elements down to
+ * 2^-25 of it, 2^-36 of it throughout. A vector with an element that is infinite
+ * or NaN gives no finite logit: NaN also where the products would sum to an
+ * infinity (a code's zero point is subtracted behind the sum).
  */
 int lmhead_q4_head(int dtype, const void* codes, const void* scales, const void* mins,
                    const void* h, int64_t n, int d, int group, int M, float* out_logits,

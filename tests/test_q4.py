@@ -237,3 +237,29 @@ def test_bad_ids_streams_and_refusals():
         L.q4_head(codes, scales.half(), h, 64)
     with pytest.raises(ValueError, match="ids"):
         L.q4_gather_logits(codes, scales, h, ids[:1], 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("mins", [False, True])
+@pytest.mark.parametrize("group,d", [(32, 128), (64, 512), (128, 1024)])
+@pytest.mark.parametrize("M", [5, 12])
+def test_infinite_and_nan_elements(M, group, d, mins, dtype):
+    """A vector with one gives no finite logit; the others' are what they were."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    codes, scales, off, h = _inputs(300, d, group, M, dtype, mins, M)
+    ids = torch.randint(0, 300, (M, 77), device="cuda", dtype=torch.int32, generator=torch.Generator("cuda").manual_seed(1))
+    ids[:, -1] = ids[:, 0]
+    calls = (lambda x: L.q4_head(codes, scales, x, group, mins=off),
+             lambda x: L.q4_gather_logits(codes, scales, x, ids, group, mins=off))
+    want = [f(h) for f in calls]
+    bad = h.clone()
+    bad[1, 3], bad[2, d - 1], bad[3, d // 2] = float("inf"), float("nan"), -float("inf")
+    rest = [0] + list(range(4, M))
+    for f, w in zip(calls, want):
+        got = f(bad)
+        assert not torch.isfinite(got[1:4]).any()
+        assert torch.equal(got[rest], w[rest])
+    assert L.last_device_error() == 0
