@@ -458,3 +458,21 @@ def test_refused_requests_of_a_plan(mask, stale):
     assert not out[0].any() and torch.all(out[1] == -float("inf")) and L.last_device_error() == 0
     with pytest.raises(ValueError, match="granted"):
         L.chunk_attention(q, kc, vc, tab, i32(lens), plan.cu, granted=plan.granted[1:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("H,Hk,D,P", [(5, 1, 64, 16), (8, 2, 128, 16), (12, 4, 64, 64), (2, 2, 128, 128), (6, 2, 64, 256)])
+@pytest.mark.parametrize("window", [1, 63, 128, 300])
+def test_windows_of_either_type_over_any_pages(window, H, Hk, D, P, dtype):
+    """The pages that lie wholly before every window have been given away: their
+    table entries are no page's."""
+    import torch
+    from gpu_util import lib
+    c = _case([0, 511, 1300, 77], [5, 1, 140, 64], H, Hk, D, P, dtype, window)
+    want, wl = _check(lib(), c, dtype, window=window)
+    for s, l in enumerate([0, 511, 1300, 77]):
+        c["table"][s, :max(0, l + 1 - window) // P] = -1
+    L = lib()
+    got, gl = L.chunk_attention(c["q"], c["kc"], c["vc"], c["table"], c["lens"], c["cu"], window=window, with_lse=True)
+    assert torch.equal(got, want) and torch.equal(gl, wl) and L.last_device_error() == 0
