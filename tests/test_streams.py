@@ -66,7 +66,7 @@ def _overlap(a: torch.Tensor, ptr: int, nbytes: int) -> bool:
 
 def _busy(stream):
     with torch.cuda.stream(stream):
-        torch.cuda._sleep(200_000_000)  # about a tenth of a second
+        torch.cuda._sleep(1_000_000_000)  # about half a second
 
 
 def _beams(n):
