@@ -11,7 +11,8 @@ input (> 2x the 129 MB L2) keep each step's reads cold.
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--M 64] [--impl ours|reference]
 
-Prints one JSON line. Under torchrun (N > 1) every rank runs an independent
+Prints one JSON line on stdout (and the tables beside it - the sweep over M, every
+configuration, the steps after q, the other routes - as one on stderr). Under torchrun (N > 1) every rank runs an independent
 replica on its own hidden vectors (no collective on the data path) and rank
 0 prints the aggregate over ranks with the max time over ranks.
 """
@@ -911,7 +912,7 @@ def run_ours(args):
         configs = time_configs(torch, L, hbm)
     clocks = sampler.stop()
 
-    cpu = None
+    cpu = cpu_rates = None
     parity = None
     if rank == 0 and not args.no_cpu:
         rate, cores, sample = oracle_sample_rate(head, hb)
@@ -919,7 +920,7 @@ def run_ours(args):
                "sample": sample}
         parity = parity_sample(head, hb, outs[0])
         if not args.no_configs:
-            cpu["per_config"] = cpu_configs()
+            cpu_rates = cpu_configs()
 
     if rank == 0:
         line = {
@@ -932,10 +933,16 @@ def run_ours(args):
             "clocks": clocks, "kernel_us": {k: round(v, 3) for k, v in kern_us.items()},
             "step_bytes": step_bytes,
             "step_hbm_frac": round(step_bytes / (ms / args.steps * 1e-3) / 1e9 / hbm, 4),
-            "unique_rows": U, "latency_us": lat, "parity_counts": parity, "sweep": sweep,
-            "configs": configs, "vs_dense": dense_speedups(configs), "after_q": after_q,
-            "cluster_route": cluster, "noalloc": noalloc, "sharded": shards,
+            "unique_rows": U, "latency_us": lat, "parity_counts": parity,
         }
+        # the tables beside the headline would make its line too long to be read
+        # back whole: they are a line of their own on stderr
+        tables = {
+            "sweep": sweep, "configs": configs, "vs_dense": dense_speedups(configs),
+            "after_q": after_q, "cluster_route": cluster, "noalloc": noalloc, "sharded": shards,
+            "cpu_per_config": cpu_rates,
+        }
+        print(json.dumps(tables), file=sys.stderr, flush=True)
         print(json.dumps(line), flush=True)
     if world > 1:
         dist.barrier()
