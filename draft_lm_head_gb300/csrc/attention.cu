@@ -26,18 +26,21 @@
 //             brings the last one of its rows joins them, in the order of the
 //             pieces.
 // Bound: few rows, by reading K and V once; many rows, by the tensor cores.
-// Measured (whole call, both launches): 32 requests of 4000-8000 cached tokens
-// and one new each, 32 heads over 8, dim 128: 134 us for 824 MB (6.1 TB/s); two
-// chunks of 2048 tokens over 6144 cached: 325-340 us for 0.48 TFLOP (1.41-1.48
-// PFLOP/s). The latter is bound by the hand-overs between the roles: without the
-// exponentials it takes as long, with an eighth of the softmax 4 % less, without
-// loads 1 % less, with an eighth of the MMAs still three quarters of the time.
+// Measured (whole call, both launches, other inputs each time): 32 requests of
+// 4000-8000 cached tokens and one new each, 32 heads over 8, dim 128: 132-135 us for
+// 801 MB (5.9-6.1 TB/s); two chunks of 2048 tokens over 6144 cached: 345-348 us for
+// 0.48 TFLOP (1.39 PFLOP/s; 325-331 us where one set of inputs is replayed). The
+// latter is bound by the hand-overs between the roles: without the exponentials it
+// takes as long, with an eighth of the softmax 4 % less, without loads 1 % less,
+// with an eighth of the MMAs still three quarters of the time.
 // The softmax runs in the base-2 domain with a running reference instead of
 // the running maximum: a row's first block with a key sets it, and it moves only
 // when weights pass 2^9 or so, which their sum shows; a block's maximum is not
 // even looked for before (it cost a fifth of a block's time). Scores, sums,
-// references and accumulators are fp32; the weights are rounded once, to 16
-// bits, as the tensor cores take them.
+// references and accumulators are fp32; the weights are rounded once, to the
+// tensors' 16 bits, as the tensor cores take them beside V (the row's sum keeps them
+// in fp32): against 64 bits 2.3e-3 of the outputs' size for bf16 and 2.9e-4 for
+// fp16, where rounding the output alone leaves 1.7e-3 and 2.1e-4.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -393,8 +396,9 @@ struct Cursor {
 
 // A warp's wait. The one that issues the MMAs is on the way of every block: it
 // polls for a while before it lets itself be suspended, from which a warp takes a
-// few hundred cycles to return (two prompts of 2048 tokens 351 to 325 us; with the
-// softmax's warps polling too, which takes issue slots from their neighbours, 332).
+// few hundred cycles to return (two prompts of 2048 tokens, one set of inputs
+// replayed, 351 to 325 us; with the softmax's warps polling too, which takes issue
+// slots from their neighbours, 332).
 template <bool POLL>
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
                                          long long budget) {
@@ -1125,7 +1129,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
-  // at the end, so that a call without such rows pays one look at the header
+  // at the end, so that a call without such rows pays one look at the header (on the
+  // softmax's way to its next piece it took 8 us of the 346 of two prompts)
   if (warp < 8 && sc.head->fill != kFillNone) fill_rows<BF16, D>(a, sc, warp);
 }
 

@@ -22,8 +22,8 @@
 // (Operands of the tcgen05 instructions would have to be written to shared or
 // tensor memory first, at a store per two codes; here they never leave
 // registers.)
-// Measured: 128256 rows of 4096 codes, groups of 128: 54 us for one hidden vector
-// (5.1 TB/s of codes and scales, at 1.8 instructions a cycle and SM), 56 for
+// Measured: 128256 rows of 4096 codes, groups of 128: 49-53 us for one hidden vector
+// (5.1-5.5 TB/s of codes and scales, at 1.8 instructions a cycle and SM), 56 for
 // eight, 31 for 1002 candidate rows of each of 64; 151936 rows of 5120, groups of
 // 64 with mins: 124 us for 16 vectors.
 //   The matrix instructions cut the products of a sum at a place set by the

@@ -407,7 +407,8 @@ int lmhead_shard_softmax(const float* all_stats, int G, const float* logits, int
  *   out_free_left  1 int32: free pages after the plan (the caller's next
  *               free_count; must not alias free_count).
  * More new tokens than max_tokens: the excess gets no slots and
- * LMHEAD_ERR_DEVICE_CHECK is recorded. page_size 1..65536, S up to 2^20;
+ * LMHEAD_ERR_DEVICE_CHECK is recorded. page_size 1..65536, S up to 2^20 (made for
+ * thousands of requests: the time grows with S squared, 2 ms at 2^17);
  * page ids * page_size must stay below 2^31.
  */
 int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_t* table,
@@ -439,7 +440,9 @@ int lmhead_page_plan(const int32_t* lens, const int32_t* new_lens, int S, int32_
  *             new tokens j < 64 of its request whose bit j is set (its own
  *             counts too).
  *   out       T x heads x dim; out_lse T x heads fp32 (natural log) or NULL.
- *             A row that sees no key gives 0 and -inf.
+ *             A row that sees no key gives 0 and -inf. Scores, softmax sums and
+ *             accumulators are fp32; the softmax weights are rounded to dtype
+ *             before they meet V, and the result to dtype once more.
  * Tokens outside every [cu[s], cu[s+1]) are left unwritten. Slots of the cache
  * past a request's tokens are never used, whatever they hold; a non-finite V
  * of a token of the request itself may reach every row of its chunk.
@@ -513,6 +516,8 @@ int lmhead_q4_gather_logits(int dtype, const void* codes, const void* scales, co
  *             and the score. Entries whose score is not finite (a masked logit, a
  *             dead beam, a row with a NaN or +inf) are never taken; places left
  *             over hold -1, -1 and -inf.
+ * The exponentials of a row are fp32, as are their sums within a lane; sums across
+ * lanes and the scores are pairs of fp32 numbers, rounded at the end.
  * 1 <= k <= 32, beams <= 256, S * beams <= 65535, n <= 2^30 and beams * n below 2^31.
  * Workspace: lmhead_beam_workspace_size bytes, 256-byte aligned.
  */
