@@ -11,8 +11,9 @@ def stream_handle(stream, device) -> int:
     """The cudaStream_t of a call: that of `stream`, or the device's current one."""
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(device.index)
+    index = getattr(device, "index", None)
+    if _raw_stream is not None and index is not None:
+        return _raw_stream(index)
     return torch.cuda.current_stream(device).cuda_stream
 
 

@@ -170,3 +170,29 @@ def test_results_of_a_call_on_another_stream():
     assert not cur.query() and not _overlap(again, *old)
     torch.cuda.synchronize()
     assert torch.equal(kept, want)
+
+
+@pytest.mark.gpu
+def test_calls_on_a_stream_of_a_capture():
+    """A stream that joins the capture and takes a call with its results and
+    workspace; a device without an index is the current one."""
+    from gpu_util import lib
+    lib()
+    x, sc = _beams(4000)
+    want = L.beam_select(x, sc, 4, 8)
+    ws, s = L.Workspace(), torch.cuda.Stream()
+    assert ws.get(1000, torch.device("cuda")).numel() >= 1000
+    L.beam_select(x, sc, 4, 8, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.wait_stream(torch.cuda.current_stream())
+        a = L.beam_select(x, sc, 4, 8, workspace=ws, stream=s)
+        b = L.beam_select(x, sc, 4, 8, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+    for y in (*a, *b):
+        y.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for y, z, w in zip(a, b, want):
+        assert torch.equal(y, w) and torch.equal(z, w)
