@@ -8,8 +8,8 @@ views of bf16 bits. Names follow the C ABI (include/lmhead.h) without the
 
     ids, logits, q = two_stage(LOCAL, W, A, B, h, token_ids, T, k_tile)
 
-The serving operators around the head are in draft_lm_head_gb300.serving and
-re-exported here.
+The serving operators around the head are in draft_lm_head_gb300.serving, those of
+a step over the paged cache in draft_lm_head_gb300.step; both are re-exported here.
 
 Offline preparation of A and B (the Freq-aware SVD) is in
 draft_lm_head_gb300.prep.
@@ -34,6 +34,7 @@ __all__ = [
     "draft_select", "verify_chain", "last_device_error", "debug_set_wait_cycles", "version",
     "Workspace", "shard_workspace_size", "shard_two_stage", "shard_softmax", "PagePlan",
     "page_plan", "chunk_attention", "q4_head", "q4_gather_logits", "beam_select", "beam_reorder",
+    "rotary", "verify_tree", "cache_keep", "page_release", "cache_weights", "cache_select",
 ]
 
 _BF16_OK = (torch.bfloat16, torch.int16, torch.uint16) if hasattr(torch, "uint16") else (
@@ -359,3 +360,5 @@ def verify_chain(p: torch.Tensor, x: torch.Tensor, cand_ids: torch.Tensor, cand_
 
 from .serving import (PagePlan, beam_reorder, beam_select, chunk_attention,  # noqa: E402,F401
                       page_plan, q4_gather_logits, q4_head)
+from .step import (cache_keep, cache_select, cache_weights, page_release, rotary,  # noqa: E402,F401
+                   verify_tree)

@@ -59,6 +59,19 @@ SIGNATURES = {
     "lmhead_beam_select": (_I, [_I, _P, _I64, _P, _P, _P, _I, _I, _I64, _I, _I, _P, _P, _P, _P,
                                 _SZ, _P]),
     "lmhead_beam_reorder": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "lmhead_rotary": (_I, [_I, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F,
+                           _P, _I64, _I64, _P, _I64, _I64, _P]),
+    "lmhead_verify_tree": (_I, [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P,
+                                _P]),
+    "lmhead_cache_keep": (_I, [_I, _P, _P, _P, _P, _P, _I64, _I, _I, _P, _I, _P, _I, _I, _P, _I, _P,
+                               _P]),
+    "lmhead_page_release": (_I, [_P, _P, _P, _P, _I, _P, _I, _P, _I, _P, _I, _P, _P]),
+    "lmhead_cache_weights_workspace_size": (_SZ, [_I]),
+    "lmhead_cache_weights": (_I, [_I, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I, _P, _I, _P, _P,
+                                  _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _F, _P, _I64, _I64, _I64,
+                                  _P, _SZ, _P]),
+    "lmhead_cache_select": (_I, [_P, _I64, _I64, _I64, _I64, _I, _I, _P, _I, _P, _I, _I, _I, _I, _P,
+                                 _P]),
     "lmhead_two_stage_local_noalloc": (_I, [_P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _I, _F,
                                             _P, _P, _P, _P]),
 }

@@ -221,6 +221,91 @@ struct ReorderArgs {
 };
 cudaError_t launch_beam_reorder(const ReorderArgs& a, int* err, cudaStream_t s);
 
+// ---- operators of a step over the paged cache
+// Rotary positions (rotary.cu); strides in elements, k may be nullptr.
+struct RotaryArgs {
+  int dtype;  // lmhead_dtype
+  const void *q, *k;
+  void *qo, *ko;
+  int64_t q_tok, q_head, k_tok, k_head, qo_tok, qo_head, ko_tok, ko_head;
+  const int32_t* pos;
+  const int64_t* turns;
+  int T, heads, kv_heads, dim, rot;  // kv_heads 0 without k
+  bool interleaved, backward;
+  float magnitude;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s);
+
+// Draft trees against the target's probabilities (tree.cu).
+constexpr int kTreeMaxNodes = 64;
+struct TreeArgs {
+  const float* p;  // T x n
+  int64_t n;
+  const int32_t *tokens, *parent, *cu, *granted;
+  const float *r, *u;
+  const int32_t* cand_ids;  // T x K, or nullptr
+  const float* cand_q;
+  int S, T, K, depth;
+  int32_t *out_tokens, *out_path, *out_accepted;
+};
+cudaError_t launch_verify_tree(const TreeArgs& a, int* err, cudaStream_t s);
+
+// Sums of attention weights a cached token (weights.cu); strides in bytes.
+struct WeightArgs {
+  int dtype;
+  const void* q;
+  int64_t q_tok, q_head;
+  const void* k_cache;
+  CacheStrides ks;
+  int64_t pages;
+  int page_shift;
+  const int32_t *table, *lens, *cu, *granted;
+  int width, S, T, heads, kv_heads, dim, window;
+  const uint64_t* tree;
+  const float* lse;
+  float scale, decay;
+  void* weights;
+  CacheStrides ws;
+};
+size_t weights_scratch_bytes(int S);
+cudaError_t launch_cache_weights(const WeightArgs& a, void* scratch, int* err, cudaStream_t s);
+
+// Tokens that stay, rows moved together and pages given back (keep.cu).
+struct SelectArgs {
+  const void* weights;
+  CacheStrides ws;
+  int64_t pages;
+  int page, width, S, kv_heads, budget, sinks, recent;
+  const int32_t *table, *lens;
+  int32_t* kept;
+};
+cudaError_t launch_cache_select(const SelectArgs& a, int* err, cudaStream_t s);
+constexpr int kKeepMax = 8;
+struct KeepTensor {
+  void* base;
+  CacheStrides st;
+  int row;                 // bytes of a token and head
+  int vec, slice, slices;  // set by the launch
+};
+struct KeepArgs {
+  KeepTensor t[kKeepMax];
+  int count;
+  int64_t pages;
+  int page, width, S, kv_heads, n;
+  bool per_head;
+  const int32_t *table, *kept, *first;
+  int32_t* new_lens;
+};
+cudaError_t launch_cache_keep(KeepArgs a, int* err, cudaStream_t s);
+struct ReleaseArgs {
+  const int32_t *lens, *new_lens, *cu, *granted, *table;
+  int S, width, page, free_cap;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* free_left;
+};
+cudaError_t launch_page_release(const ReleaseArgs& a, int* err, cudaStream_t s);
+
 int* device_error_word();  // this device's error word (nullptr on failure)
 // Budget (SM cycles) of the tensor-core kernels' role waits; tc::kWaitCycles
 // unless lmhead_debug_set_wait_cycles changed it.

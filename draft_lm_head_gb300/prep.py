@@ -22,12 +22,13 @@ counts (the frequency scale cancels in A B).
 """
 from __future__ import annotations
 
+import math
 from typing import Optional
 
 import numpy as np
 
 __all__ = ["smoothed_frequency", "freq_aware_factors", "bf16_bits", "pruned_rows",
-           "quantise_rows"]
+           "quantise_rows", "rotary_turns"]
 
 
 def smoothed_frequency(counts: np.ndarray) -> np.ndarray:
@@ -126,3 +127,46 @@ def quantise_rows(W: np.ndarray, group: int, offsets: bool = False, fp16: bool =
         c = np.clip(np.rint(c), 0, 15).astype(np.uint8).reshape(-1, d)
         codes[r0:r0 + block] = c[:, 0::2] | (c[:, 1::2] << 4)
     return {"codes": codes, "scales": scales, "mins": mins}
+
+
+def rotary_turns(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                 original: float = 8192.0, low: float = 1.0, high: float = 4.0) -> np.ndarray:
+    """Frequencies of rotary positions for rotary(): rot / 2 int64, turns a position
+    in units of 2^-64 (modulo 1), of base^(-2 i / rot) radians.
+
+    scaling stretches them for contexts `factor` times as long:
+      "linear"      all of them divided by factor;
+      "base"        base times factor^(rot / (rot - 2)), which divides the slowest
+                    by factor and leaves the fastest;
+      "wavelength"  those that turn less than `low` times in `original` positions
+                    divided by factor, those that turn more than `high` times left,
+                    blended linearly in their number of turns between;
+      "ramp"        the same, blended linearly in the pair's index (a magnitude of
+                    1 + 0.1 ln(factor) goes with it)."""
+    if rot < 2 or rot % 2 or not base > 0 or not factor > 0:
+        raise ValueError(f"rot={rot} must be even, base={base} and factor={factor} positive")
+    i = np.arange(rot // 2, dtype=np.float64)
+    if scaling == "base":
+        if rot == 2:
+            raise ValueError("scaling by the base needs more than one pair")
+        base = base * factor ** (rot / (rot - 2))
+    w = base ** (-2 * i / rot)
+    if scaling == "linear":
+        w = w / factor
+    elif scaling in ("wavelength", "ramp"):
+        if not 0 < low < high:
+            raise ValueError(f"low={low} must be below high={high}")
+        if scaling == "wavelength":
+            keep = (original * w / (2 * math.pi) - low) / (high - low)
+        else:
+            # the (real) index of the pair that turns so many times
+            def at(turns):
+                return rot * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+            first, last = max(0.0, math.floor(at(high))), min(rot / 2 - 1.0, math.ceil(at(low)))
+            keep = 1 - (i - first) / max(last - first, 1e-3)
+        keep = np.clip(keep, 0.0, 1.0)
+        w = w * keep + w / factor * (1 - keep)
+    elif scaling not in (None, "base"):
+        raise ValueError(f"scaling={scaling!r} must be None, linear, base, wavelength or ramp")
+    turns = [round(float(x) / (2 * math.pi) * 2.0 ** 64) & (2 ** 64 - 1) for x in w]
+    return np.array(turns, dtype=np.uint64).view(np.int64)

@@ -540,6 +540,183 @@ int lmhead_beam_reorder(const int32_t* parent, int S, int beams, int k, int coun
                         lmhead_stream stream);
 
 /*
+ * ---- Operators of a step over the paged cache. Between the page plan and the
+ * attention stand the rotary positions of the new queries and keys; behind the
+ * target's head stands the verification of the draft tree, the accepted rows kept
+ * in the cache and the pages behind them given back; and a cache that has outgrown
+ * its room is cut down to the tokens that draw most of the attention. ("EAGLE ->
+ * EAGLE-2 -> EAGLE-3 -> DFlash": a tree of drafts is verified in one pass of the
+ * target; "Speculative decoding and EAGLE": the exactness rule. The pages have no
+ * counterpart to the rest.) Conventions as above.
+ *
+ * Rotary positions: each pair (a, b) of the first `rot` elements of a head turns by
+ * the angle t = 2 pi frac(position * turns / 2^64):
+ *   (a cos t - b sin t, b cos t + a sin t) * magnitude,
+ * or by -t with `backward`, which is the gradient's way back through it. What lies
+ * behind `rot` is copied (in place: left).
+ *   dtype     LMHEAD_BF16, LMHEAD_FP16 or LMHEAD_FP32, of q, k and the results.
+ *   q, k      T x heads x dim, T x kv_heads x dim (k and out_k NULL: q alone);
+ *             *_tok, *_head: strides in elements (dim is contiguous).
+ *   positions T int32 (a page plan's out_positions); the rows of a token whose
+ *             position is negative are not written.
+ *   turns     rot / 2 int64: turns a position of each pair, in units of 2^-64 and
+ *             modulo 1, so that angles of far positions lose nothing.
+ *   interleaved  0: pair i is (i, i + rot / 2); else (2 i, 2 i + 1).
+ *   out_q, out_k  the tensors themselves (same strides), or others that do not meet
+ *             them. No two places of a result may coincide.
+ * Arithmetic is fp32, the result is rounded once. Whole loads of 16 bytes where
+ * addresses, strides and the parts of a head allow them, else element by element.
+ */
+int lmhead_rotary(int dtype, const void* q, int64_t q_tok, int64_t q_head, const void* k,
+                  int64_t k_tok, int64_t k_head, const int32_t* positions, const int64_t* turns,
+                  int T, int heads, int kv_heads, int dim, int rot, int interleaved, int backward,
+                  float magnitude, void* out_q, int64_t oq_tok, int64_t oq_head, void* out_k,
+                  int64_t ok_tok, int64_t ok_head, lmhead_stream stream);
+
+/*
+ * Verification of draft trees. The new tokens of request s, cu[s] .. cu[s+1]-1 of a
+ * chunk, are the nodes of its tree: node 0 is the root (the last token that is
+ * certain), the others are drafts. Nodes are walked in index order from the root; a
+ * node is tried when its parent is the node that the walk stands on, and when it is
+ * accepted the walk goes on from it.
+ *   Without cand_ids (children that are given, as the most likely ones): with Z = 1
+ *     at each node at first, x is accepted if r Z < p(x), where p(x) counts 0 for a
+ *     token tried there before; otherwise p(x) becomes 0 and Z falls by it.
+ *   With cand_ids (children drawn from q in index order without replacement; one
+ *     child: a chain): with Z = Q = 1, w = p and g = q over the candidates, x is
+ *     accepted if r Z g(x) < w(x) Q; otherwise, with t = fl(fl(Z / Q) g) in fp32,
+ *     w becomes w - min(w, t), Z falls by the sum of min(w, t), Q by g(x), and g(x)
+ *     becomes 0. q is zero outside the candidates.
+ * Either way, the last token is drawn from what is left of p at the last node: the
+ * smallest vocabulary id whose running sum of weights exceeds u times their sum (p
+ * itself if nothing is left). Tokens come out distributed as the target's.
+ *   p         T x n fp32: the target's distribution behind each node (rows sum to
+ *             1; negative entries and NaN count 0).
+ *   tokens, parent  T int32: each node's token and the index of its parent in its
+ *             request. What the root has there is not read; a node whose parent is not
+ *             an earlier node of its request is never tried.
+ *   granted   S int32 or NULL: 0 for a request that was refused (page plan).
+ *   r         T fp32 uniforms of the nodes; u  S fp32 uniforms of the last tokens.
+ *   cand_ids, cand_q  T x K (1 <= K <= 4096): the distribution that each node's
+ *             children were drawn from (ids outside [0, n) count as none; of an id
+ *             listed twice the first counts), or NULL.
+ *   depth     most drafts of a path, 0..63.
+ *   out_tokens  S x (depth + 1) int32: the accepted drafts, the last token, then -1.
+ *   out_path  S x (depth + 1) int32: the accepted path's nodes from the root on,
+ *             then -1 (lmhead_cache_keep's `kept`).
+ *   out_accepted  S int32: drafts accepted; -1 for a request that was refused or
+ *             has no tokens (its entries are all -1).
+ * At most 64 nodes a request. More of them, a cu that decreases or leaves [0, T], a
+ * tried token outside [0, n) or, with cand_ids, not among its parent's candidates,
+ * and a path deeper than depth give -1 too and record LMHEAD_ERR_DEVICE_CHECK.
+ * Accept tests, masses and running sums carry 48 bits or more.
+ */
+int lmhead_verify_tree(const float* p, int64_t n, const int32_t* tokens, const int32_t* parent,
+                       const int32_t* cu, const int32_t* granted, const float* r, const float* u,
+                       const int32_t* cand_ids, const float* cand_q, int K, int S, int T, int depth,
+                       int32_t* out_tokens, int32_t* out_path, int32_t* out_accepted,
+                       lmhead_stream stream);
+
+/*
+ * Rows of a paged cache moved together: row first[s] + i of request s becomes what
+ * row first[s] + kept[s, i] was, for every entry that is not negative (kept[i] >= i;
+ * those that are leave their row alone).
+ *   base, *_stride, row_bytes  HOST arrays of `count` (1..8) tensors, pages x
+ *             page_size x kv_heads rows of row_bytes contiguous bytes each; strides in
+ *             bytes, any order, rows not meeting. A K and a V cache, and the weights
+ *             below with rows of 4 bytes.
+ *   table     S x width int32, as of lmhead_page_plan.
+ *   kept      S x n int32, or S x kv_heads x n with per_head: every head's own rows.
+ *   first     S int32, or NULL: 0. lens and a verified tree's out_path keep the
+ *             accepted nodes of the chunk behind the lens cached tokens.
+ *   out_new_lens  S int32: first[s] plus the number of entries up to the last one
+ *             that is not negative (with per_head, of head 0); must not meet first.
+ * Rows behind the new length are left as they were. Requests share no page that is
+ * moved in (prefixes that they share come before first and the first entry that
+ * differs from its index). An entry below its index, a row past width * page_size or
+ * a page id outside [0, pages) is not moved and records LMHEAD_ERR_DEVICE_CHECK, as
+ * does a negative first, whose request is left alone.
+ * page_size 1..65536, S <= 65536.
+ */
+int lmhead_cache_keep(int count, void* const* base, const int64_t* page_stride,
+                      const int64_t* token_stride, const int64_t* head_stride,
+                      const int64_t* row_bytes, int64_t pages, int page_size, int kv_heads,
+                      const int32_t* table, int width, const int32_t* kept, int n, int per_head,
+                      const int32_t* first, int S, int32_t* out_new_lens, lmhead_stream stream);
+
+/*
+ * The counterpart of lmhead_page_plan: the pages of requests that have become
+ * shorter go back behind the free ones, request after request in the order of their
+ * tables (which stay as they are).
+ *   lens      S int32: tokens before the step; with cu (S + 1 int32, or NULL) a
+ *             request holds cu[s+1] - cu[s] more, unless granted (S int32, or NULL) is
+ *             0 for it.
+ *   new_lens  S int32: tokens it holds from now on. Pages from ceil(new / page_size)
+ *             up to ceil(held / page_size) are released.
+ *   free_pages  free_cap int32, in place: the stack whose first *free_count entries
+ *             are free; must not meet table.
+ *   out_free_left  1 int32: free pages afterwards (the next free_count; must not
+ *             alias free_count).
+ * A negative length, one that has grown, or more than width * page_size tokens: the
+ * request releases nothing; pages past free_cap are dropped. Both record
+ * LMHEAD_ERR_DEVICE_CHECK. S up to 2^20 (the time grows with S squared).
+ */
+int lmhead_page_release(const int32_t* lens, const int32_t* new_lens, const int32_t* cu,
+                        const int32_t* granted, int S, const int32_t* table, int width,
+                        int32_t* free_pages, int free_cap, const int32_t* free_count,
+                        int page_size, int32_t* out_free_left, lmhead_stream stream);
+
+/*
+ * How much attention each cached token has drawn, summed up: for key j of request s
+ * and K/V head a, over the request's new tokens i and the query heads h of a that see
+ * it,
+ *   w[j] = (j < lens[s] ? decay * w[j] : 0) + sum exp(scale * q_ih . k_j - lse_ih).
+ * The chunk's own keys are in the cache already (lmhead_chunk_attention wrote them).
+ *   dtype, q, k_cache, table, lens, cu, granted, tree, window, scale, dim, page_size
+ *             as of lmhead_chunk_attention (the rows of q do not meet).
+ *   lse       T x heads fp32: that call's out_lse. A row of -inf draws nothing.
+ *   weights   pages x page_size x kv_heads fp32, in place; w_page, w_token, w_head:
+ *             strides in elements. What a page holds for tokens that are new
+ *             (j >= lens) is not read, nor anything with decay 0.
+ *   decay     >= 0.
+ * Products are those of the 16-bit values, sums and exponentials fp32. No result
+ * depends on the order in which CTAs run.
+ * Requests that were refused (granted 0) are left alone; so are, with
+ * LMHEAD_ERR_DEVICE_CHECK recorded, those whose lengths are negative or pass width *
+ * page_size, and the tokens of a page id outside [0, pages). Where cu decreases or
+ * leaves [0, T], nothing is computed and the error recorded. Requests share no
+ * page. A token with a non-finite key, or seen by a row whose q or lse is NaN, gets
+ * NaN or an infinity.
+ * Workspace: lmhead_cache_weights_workspace_size bytes, 256-byte aligned.
+ */
+size_t lmhead_cache_weights_workspace_size(int S);
+int lmhead_cache_weights(int dtype, const void* q, int64_t q_tok, int64_t q_head,
+                         const void* k_cache, int64_t kc_page, int64_t kc_token, int64_t kc_head,
+                         int64_t pages, int page_size, const int32_t* table, int width,
+                         const int32_t* lens, const int32_t* cu, const int32_t* granted,
+                         const uint64_t* tree, const float* lse, int S, int T, int heads,
+                         int kv_heads, int dim, int window, float scale, float decay,
+                         float* weights, int64_t w_page, int64_t w_token, int64_t w_head,
+                         void* workspace, size_t workspace_bytes, lmhead_stream stream);
+
+/*
+ * Which tokens of each request and K/V head stay when its cache is cut down to
+ * `budget`: the first `sinks`, the last `recent` and, between them, those with the
+ * largest weights (ties: the lower position; a NaN counts below all others).
+ *   weights   as of lmhead_cache_weights; lens  S int32, the tokens cached.
+ *   out_kept  S x kv_heads x budget int32: positions, ascending, then -1
+ *             (lmhead_cache_keep's `kept` with per_head, first NULL). A request of
+ *             budget tokens or fewer keeps them all.
+ * sinks + recent <= budget. A negative length or one past width * page_size gives -1
+ * throughout, a page id outside [0, pages) counts its tokens as NaN; both record
+ * LMHEAD_ERR_DEVICE_CHECK.
+ */
+int lmhead_cache_select(const float* weights, int64_t w_page, int64_t w_token, int64_t w_head,
+                        int64_t pages, int page_size, int kv_heads, const int32_t* table, int width,
+                        const int32_t* lens, int S, int budget, int sinks, int recent,
+                        int32_t* out_kept, lmhead_stream stream);
+
+/*
  * Test hook for the timeout path (the pages have no counterpart). Every wait
  * between the warp roles of the tensor-core kernels (the fused score + tile
  * top-k, the global path's score writeback, the dense and pruned heads) is
