@@ -394,29 +394,8 @@ struct Cursor {
   }
 };
 
-// A warp's wait. The one that issues the MMAs is on the way of every block: it
-// polls for a while before it lets itself be suspended, from which a warp takes a
-// few hundred cycles to return (two prompts of 2048 tokens, one set of inputs
-// replayed, 351 to 325 us; with the softmax's warps polling too, which takes issue
-// slots from their neighbours, 332).
-template <bool POLL>
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                         long long budget) {
-  if (POLL && budget > 0) {
-#pragma unroll 1
-    for (int i = 0; i < 200; ++i)
-      if (__all_sync(0xFFFFFFFFu, tc::mbar_test(bar, parity))) return true;
-  }
-  const bool now = budget > 0 && tc::mbar_try_wait(bar, parity);
-  return __all_sync(0xFFFFFFFFu, now || tc::mbar_wait(bar, parity, abort, budget));
-}
-
-// Bits [lo, hi) of 32, either end anywhere.
-__device__ __forceinline__ uint32_t span_bits(int lo, int hi) {
-  const uint32_t below_hi = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u;
-  const uint32_t below_lo = lo >= 32 ? ~0u : lo <= 0 ? 0u : (1u << lo) - 1u;
-  return below_hi & ~below_lo;
-}
+using tc::span_bits;
+using tc::wait_all;
 
 template <bool BF16> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;

@@ -267,7 +267,7 @@ struct WeightArgs {
   void* weights;
   CacheStrides ws;
 };
-size_t weights_scratch_bytes(int S);
+size_t weights_scratch_bytes();
 cudaError_t launch_cache_weights(const WeightArgs& a, void* scratch, int* err, cudaStream_t s);
 
 // Tokens that stay, rows moved together and pages given back (keep.cu).
@@ -321,6 +321,10 @@ bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t c
 bool make_cache_map(CUtensorMap* map, const void* base, bool bf16, int dim, int page_tokens,
                     int heads, int64_t pages, const CacheStrides& st, int box_tokens,
                     bool head_first);
+// TMA map of tokens x heads x dim (16-bit elements, strides in bytes): boxes of 64
+// elements of box_heads heads of box_tokens tokens.
+bool make_rows_map(CUtensorMap* map, const void* base, bool bf16, int dim, int heads, int64_t tokens,
+                   int64_t head_stride, int64_t token_stride, int box_heads, int box_tokens);
 int sm_count();  // SMs of the current device (cached)
 
 }  // namespace lmhead

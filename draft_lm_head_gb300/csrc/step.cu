@@ -218,7 +218,7 @@ int lmhead_page_release(const int32_t* lens, const int32_t* new_lens, const int3
 }
 
 size_t lmhead_cache_weights_workspace_size(int S) {
-  return S < 1 || S > kMaxRequests ? 0 : weights_scratch_bytes(S);
+  return S < 1 || S > kMaxRequests ? 0 : weights_scratch_bytes();
 }
 
 int lmhead_cache_weights(int dtype, const void* q, int64_t q_tok, int64_t q_head,
@@ -255,7 +255,7 @@ int lmhead_cache_weights(int dtype, const void* q, int64_t q_tok, int64_t q_head
     return LMHEAD_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(tree, 8) || !aligned(weights, 4))
     return LMHEAD_ERR_ALIGN;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < weights_scratch_bytes(S))
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < weights_scratch_bytes())
     return LMHEAD_ERR_WORKSPACE;
   WeightArgs a = {};
   a.dtype = dtype;

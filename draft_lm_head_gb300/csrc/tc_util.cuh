@@ -240,6 +240,16 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// 3-D tiled TMA load into shared memory, completion counted on `bar`.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -390,6 +400,30 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// A warp's wait. The one that issues the MMAs is on the way of every block: it
+// polls for a while before it lets itself be suspended, from which a warp takes a
+// few hundred cycles to return (two prompts of 2048 tokens, one set of inputs
+// replayed, 351 to 325 us; with the softmax's warps polling too, which takes issue
+// slots from their neighbours, 332).
+template <bool POLL>
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         long long budget) {
+  if (POLL && budget > 0) {
+#pragma unroll 1
+    for (int i = 0; i < 200; ++i)
+      if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
+  }
+  const bool now = budget > 0 && mbar_try_wait(bar, parity);
+  return __all_sync(0xFFFFFFFFu, now || mbar_wait(bar, parity, abort, budget));
+}
+
+// Bits [lo, hi) of 32, either end anywhere.
+__device__ __forceinline__ uint32_t span_bits(int lo, int hi) {
+  const uint32_t below_hi = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u;
+  const uint32_t below_lo = lo >= 32 ? ~0u : lo <= 0 ? 0u : (1u << lo) - 1u;
+  return below_hi & ~below_lo;
 }
 
 }  // namespace tc

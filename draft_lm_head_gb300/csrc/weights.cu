@@ -3,127 +3,734 @@
 // For key j of request s and K/V head a, over the new tokens i and the heads h of
 // a that see it:
 //   w_j = decay w_j [j < len_s] + sum_i,h exp(scale q_ih . k_j - lse_ih),
-// with lse as attention left it, so that a token's weights over all keys sum to 1.
+// with lse as attention left it, so that a row's weights over all keys sum to 1.
 //
-// A CTA takes 64 keys of one request and head: they are read once, to shared
-// memory, and the queries in turn; a thread has a key and every fourth row.
+// The products run on the tensor cores with the keys as their rows: 128 keys times
+// a tile of up to 128 rows of queries (tokens x the G heads that share the K/V
+// head), so a thread has a key and its sum runs along the tensor memory's columns,
+// with no exchange between threads and no maximum to find. The keys of a pair of
+// such tiles are loaded once and stay in shared memory while the request's query
+// tiles pass by; a decoding step has one query tile, and its keys stream.
+// One CTA an SM, warp-specialised: a warp loads keys (TMA, page by page), one loads
+// queries and their lse, one issues the MMAs, and two warpgroups (a key tile each)
+// exponentiate and sum. The CTAs share out pairs x query tiles evenly, in the order
+// (K/V head, request, pair). Where requests bring many tiles a pair may be cut
+// between CTAs; each leaves its sums in the scratch and a second launch adds them up
+// in order, so no result depends on which CTA came first.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "lmhead.h"
+#include "tc_util.cuh"
 
 namespace lmhead {
 namespace {
 
-constexpr int kKeys = 64, kGroups = 4, kThreads = kKeys * kGroups, kRows = 16;
+constexpr int kKeys = 128;         // keys of a tile
+constexpr int kPair = 2 * kKeys;   // of a unit
+constexpr int kRows = 128;         // query rows of a tile
+constexpr int kThreads = 384;      // two warpgroups that sum, four warps of which three work
+constexpr int kRegsMore = 184, kRegsLess = 136;  // of 168 a thread at launch
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kInf = __builtin_huge_valf();
 
-template <bool BF16> __device__ __forceinline__ float load16(const char* p) {
-  const uint16_t x = *reinterpret_cast<const uint16_t*>(p);
-  return BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
+template <int D> struct Shape {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = kKeys * D * 2;           // a key tile
+  static constexpr int kPairBytes = 2 * kTile;
+  static constexpr int kPairs = D == 128 ? 2 : 4;       // pairs in shared memory
+  static constexpr int kQ = kRows * D * 2;              // a query tile
+  static constexpr int kTiles = D == 128 ? 3 : 5;       // of them
+  static constexpr int kSmem = kPairs * kPairBytes + kTiles * kQ + 1024;
+};
+
+template <int NP, int NQ> struct Ctl {
+  uint64_t k_full[NP], k_empty[NP], q_full[NQ], q_empty[NQ];
+  uint64_t s_full[2][2], s_empty[2][2];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+  float lse[NQ][kRows];  // in base 2; +inf where there is no row
+  // the plan
+  long long per_head;    // cost of one K/V head's units
+  long long lo, hi;      // the CTA's share of all
+  int bad, s0, p0, off0, hk0;
+};
+
+// What a request has to do for one K/V head.
+struct Req {
+  int tok0, m, len;
+  int np, qt;  // pairs of key tiles, query tiles
+};
+
+// The query tiles [t0, t0 + n) that see any key of pair p.
+struct Span {
+  int t0, n;
+};
+
+__device__ __forceinline__ Req request_of(const WeightArgs& a, int s, int tile_tok, bool& sane) {
+  Req r;
+  r.tok0 = a.cu[s];
+  r.m = a.cu[s + 1] - r.tok0;
+  r.len = a.lens[s];
+  sane = true;
+  r.np = r.qt = 0;
+  if (a.granted && a.granted[s] == 0) return r;
+  if (r.len < 0 || r.len > (a.width << a.page_shift) - r.m) {
+    sane = false;
+    return r;
+  }
+  if (r.m == 0 && a.decay == 1.f) return r;  // nothing changes
+  r.np = (r.len + r.m + kPair - 1) / kPair;
+  r.qt = (r.m + tile_tok - 1) / tile_tok;
+  return r;
 }
+
+__device__ __forceinline__ Span span_of(const WeightArgs& a, const Req& r, int p, int tile_tok) {
+  Span x = {0, r.qt};
+  if (!a.tree) {
+    const int first = p * kPair - r.len;  // the first token that sees the pair's first key
+    if (first > 0) x.t0 = min(r.qt, first / tile_tok);
+    if (a.window > 0) {
+      // the last key is out of sight from here on (64 bits: the window may be any)
+      const long long past = (long long)first + kPair - 1 + a.window;
+      x.n = past <= 0 ? 0 : (int)min((long long)r.qt, (past + tile_tok - 1) / tile_tok);
+    }
+    x.n = max(0, x.n - x.t0);
+  }
+  return x;
+}
+
+// Cost of a unit: its query tiles, and 1 for the keys.
+__device__ __forceinline__ int cost_of(const WeightArgs& a, const Req& r, int p, int tile_tok) {
+  return 1 + span_of(a, r, p, tile_tok).n;
+}
+// Pairs that every query tile sees.
+__device__ __forceinline__ int full_pairs(const WeightArgs& a, const Req& r) {
+  return a.window > 0 ? 0 : a.tree ? r.np : min(r.np, r.len / kPair + 1);
+}
+__device__ __forceinline__ long long cost_of(const WeightArgs& a, const Req& r, int tile_tok) {
+  const int full = full_pairs(a, r);
+  long long c = (long long)full * (1 + r.qt);
+  for (int p = full; p < r.np; ++p) c += cost_of(a, r, p, tile_tok);
+  return c;
+}
+
+// The CTA's share of all units, found by the CTA for itself.
+template <typename C>
+__device__ void make_plan(const WeightArgs& a, C& ctl, int tile_tok, int* err) {
+  __shared__ long long warp_sum[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) ctl.bad = 0;
+  cta_sync();
+  long long target = 0;
+  // pass 0 sums up, pass 1 finds the request in which the share begins
+  for (int pass = 0; pass < 2; ++pass) {
+    long long base = 0;
+    for (int s0 = 0; s0 < a.S; s0 += kThreads) {
+      const int s = s0 + tid;
+      Req r = {};
+      long long c = 0;
+      if (s < a.S) {
+        const int b = a.cu[s], e = a.cu[s + 1];
+        if (b < 0 || e < b || e > a.T) {
+          ctl.bad = 1;
+        } else {
+          bool sane;
+          r = request_of(a, s, tile_tok, sane);
+          c = cost_of(a, r, tile_tok);
+          if (!sane && pass == 0 && blockIdx.x == 0) record_error(err, kDevErrBadId);
+        }
+      }
+      long long incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (lane == 31) warp_sum[warp] = incl;
+      cta_sync();
+      long long before = base + incl - c;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        base += warp_sum[w];
+      }
+      if (pass == 1 && before <= target && target < before + c) {
+        long long rem = target - before;
+        const int full = full_pairs(a, r);
+        int p = (int)min((long long)full, rem / (1 + r.qt));
+        rem -= (long long)p * (1 + r.qt);
+        for (; p < r.np; ++p) {
+          const int w = cost_of(a, r, p, tile_tok);
+          if (rem < w) break;
+          rem -= w;
+        }
+        ctl.s0 = s;
+        ctl.p0 = p;
+        ctl.off0 = (int)rem;
+      }
+      cta_sync();
+    }
+    if (pass == 0) {
+      const long long all = ctl.bad ? 0 : base * a.kv_heads;
+      // no CTA's share is empty before another's that is not
+      const long long parts = min((long long)gridDim.x, all), c = blockIdx.x;
+      long long lo = all, hi = all;
+      if (c < parts) {
+        lo = all / parts * c + all % parts * c / parts;
+        hi = all / parts * (c + 1) + all % parts * (c + 1) / parts;
+      }
+      if (tid == 0) {
+        ctl.per_head = base;
+        ctl.lo = lo;
+        ctl.hi = hi;
+        ctl.hk0 = base > 0 ? (int)(lo / base) : 0;
+        if (ctl.bad && blockIdx.x == 0) record_error(err, kDevErrBadId);
+      }
+      if (lo >= hi) break;  // the same in every thread
+      target = lo - lo / base * base;
+    }
+  }
+  cta_sync();
+}
+
+// A CTA's units, in order; every role walks over them by itself.
+struct Cursor {
+  int s, p, hk, off, tile_tok;
+  bool whole_only;
+  long long left;
+  Req r;
+  // the unit: its place, its query tiles [a, b) of n from t0 on
+  int u_s, u_p, u_hk, t0, n, a, b, kend;
+
+  template <typename C> __device__ void init(const WeightArgs& w, const C& ctl, int tok, bool whole) {
+    tile_tok = tok;
+    whole_only = whole;
+    left = ctl.hi - ctl.lo;
+    if (left <= 0) return;
+    s = ctl.s0;
+    p = ctl.p0;
+    hk = ctl.hk0;
+    off = ctl.off0;
+    bool sane;
+    r = request_of(w, s, tile_tok, sane);
+  }
+  __device__ bool next(const WeightArgs& w) {
+    while (left > 0) {
+      while (p >= r.np) {  // on to the next request with a unit: there is one while any cost is left
+        if (++s == w.S) s = 0, ++hk;
+        p = 0;
+        bool sane;
+        r = request_of(w, s, tile_tok, sane);
+      }
+      const Span x = span_of(w, r, p, tile_tok);
+      const int cost = 1 + x.n;
+      u_s = s;
+      u_p = p++;
+      u_hk = hk;
+      t0 = x.t0;
+      n = x.n;
+      kend = r.len + r.m;
+      if (whole_only) {
+        // a unit is the CTA's in whose share it begins
+        left -= cost - off;
+        const bool mine = off == 0;
+        off = 0;
+        a = 0;
+        b = n;
+        if (mine) return true;
+        continue;
+      }
+      const int end = (int)min((long long)cost, off + left);
+      a = max(off - 1, 0);
+      b = max(end - 1, 0);
+      left -= end - off;
+      off = 0;
+      if (b > a || n == 0) return true;
+    }
+    return false;
+  }
+};
+
+// Pieces of cut pairs: of CTA c one that began earlier (place 2 c) and one that
+// begins there and goes on (2 c + 1), with the latter's unit.
+struct Piece {
+  int s, p, hk, flags;
+};
+constexpr int kBegins = 1, kGoesOn = 2;  // place 2 c + 1 is one; that in place 2 c does not end here
+struct Scratch {
+  Piece* piece;
+  float* sums;  // 256 a place
+};
+
+__device__ __forceinline__ float* weight_at(const WeightArgs& a, int32_t id, int j, int hk) {
+  return reinterpret_cast<float*>(static_cast<char*>(a.weights) + id * a.ws.page +
+                                  (j & ((1 << a.page_shift) - 1)) * a.ws.token + hk * a.ws.head);
+}
+
+static_assert(Shape<128>::kSmem + sizeof(Ctl<2, 3>) + 128 <= 227 * 1024, "shared memory");
+static_assert(Shape<64>::kSmem + sizeof(Ctl<4, 5>) + 128 <= 227 * 1024, "shared memory");
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kThreads)
-weights_kernel(const WeightArgs a, int* err) {
-  __shared__ float ks[kKeys][D + 1];
-  __shared__ float qs[kRows][D];
-  __shared__ float lse[kRows];
-  __shared__ float part[kGroups][kKeys];
+__global__ void __launch_bounds__(kThreads, 1)
+weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
+               const WeightArgs a, const Scratch sc, int k_head_first, int q_by_tma, int whole_only,
+               long long budget, int* err) {
+  using Sh = Shape<D>;
+  constexpr int NP = Sh::kPairs, NQ = Sh::kTiles;
+  extern __shared__ uint8_t dsmem_raw[];
+  __shared__ Ctl<NP, NQ> ctl;
+  uint8_t* k_s = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* q_s = k_s + NP * Sh::kPairBytes;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  volatile int* abort_flag = &ctl.abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NP; ++i) {
+      tc::mbar_init(&ctl.k_full[i], 1);
+      tc::mbar_init(&ctl.k_empty[i], 1);
+    }
+    for (int i = 0; i < NQ; ++i) {
+      tc::mbar_init(&ctl.q_full[i], 33);      // the warp's lanes, and one for a copy's bytes
+      tc::mbar_init(&ctl.q_empty[i], 1 + 2 * kKeys);  // the MMAs, and the readers of lse
+    }
+    for (int w = 0; w < 2; ++w)
+      for (int i = 0; i < 2; ++i) {
+        tc::mbar_init(&ctl.s_full[w][i], 1);
+        tc::mbar_init(&ctl.s_empty[w][i], kKeys);
+      }
+    tc::mbar_init(&ctl.drain, 1);
+    ctl.abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(&ctl.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tc::prefetch_tmap(&kmap);
+    tc::prefetch_tmap(&qmap);
+  }
+  const int group = a.heads / a.kv_heads, tile_tok = kRows / group;
+  if (tile_tok * group < kRows) {
+    // rows that no tile has: zeros throughout
+    for (int e = threadIdx.x; e < NQ * Sh::kQ / 16; e += kThreads)
+      reinterpret_cast<uint4*>(q_s)[e] = make_uint4(0, 0, 0, 0);
+    tc::fence_async_smem();
+  }
+  tc::fence_before_sync();
+  cta_sync();
+  tc::fence_after_sync();
+  constexpr uint32_t tmem = 0;  // all 512 columns: 128 a key tile and buffer
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, x = tid % kKeys, grp = tid / kKeys;
-  const int hk = blockIdx.y, group = a.heads / a.kv_heads;
-  const int j = blockIdx.x * kKeys + x;
-  __shared__ int bad;
-  if (tid == 0) bad = 0;
-  cta_sync();
-  for (int s = tid; s < a.S; s += kThreads)
-    if (a.cu[s] < 0 || a.cu[s + 1] < a.cu[s] || a.cu[s + 1] > a.T) bad = 1;
-  cta_sync();
-  if (bad) {
-    if (tid == 0) record_error(err, kDevErrBadId);
-    return;
-  }
-  for (int s = blockIdx.z; s < a.S; s += gridDim.z) {
-    if (a.granted && a.granted[s] == 0) continue;
-    const int tok0 = a.cu[s], end = a.cu[s + 1], len = a.lens[s];
-    const int m = end - tok0;
-    if (len < 0 || len > (a.width << a.page_shift) - m) {
-      if (tid == 0) record_error(err, kDevErrBadId);
-      continue;
-    }
-    const int kend = len + m;
-    if ((int)blockIdx.x * kKeys >= kend) continue;
-    // the key's place
-    const int off = j & ((1 << a.page_shift) - 1);
-    int32_t id = -1;
-    if (j < kend) {
-      id = a.table[(int64_t)s * a.width + (j >> a.page_shift)];
-      if (id < 0 || id >= a.pages) {
-        record_error(err, kDevErrBadId);
-        id = -1;
-      }
-    }
-    cta_sync();
-    if (id >= 0) {
-      const char* k = static_cast<const char*>(a.k_cache) + id * a.ks.page + off * a.ks.token + hk * a.ks.head;
-      for (int d = grp; d < D; d += kGroups) ks[x][d] = load16<BF16>(k + d * 2);
-    }
-    float sum = 0.f;
-    const int rows = m * group;
-    for (int r0 = 0; r0 < rows; r0 += kRows) {
-      cta_sync();
-      for (int e = tid; e < kRows * D; e += kThreads) {
-        const int r = r0 + e / D, d = e % D;
-        if (r >= rows) break;
-        const char* q = static_cast<const char*>(a.q) + (int64_t)(tok0 + r / group) * a.q_tok +
-                        (int64_t)(hk * group + r % group) * a.q_head;
-        qs[e / D][d] = load16<BF16>(q + d * 2);
-      }
-      if (tid < kRows && r0 + tid < rows) {
-        const int r = r0 + tid;
-        lse[tid] = a.lse[(int64_t)(tok0 + r / group) * a.heads + hk * group + r % group];
-      }
-      cta_sync();
-      for (int y = grp; y < kRows && r0 + y < rows; y += kGroups) {
-        const int i = (r0 + y) / group;
-        bool see;
-        if (a.tree) {
-          see = j < len || (j - len < 64 && (a.tree[tok0 + i] >> (j - len) & 1));
-        } else {
-          see = j <= len + i && (a.window == 0 || j > len + i - a.window);
+  make_plan(a, ctl, tile_tok, err);
+  Cursor cur;
+  cur.init(a, ctl, tile_tok, whole_only != 0);
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLess));
+    if (warp == 8) {
+      // ------------------------------------------------------------ keys by TMA
+      // the cache was written by the launch before through the other proxy
+      asm volatile("fence.proxy.async;" ::: "memory");
+      const int unit_tok = min(kKeys, 1 << a.page_shift), units = kPair / unit_tok;
+      uint32_t n = 0;
+      bool ok = true;
+      while (ok && cur.next(a)) {
+        const int slot = (int)(n % NP);
+        if (cur.b == cur.a) continue;  // no row sees the pair
+        if (n >= (uint32_t)NP) {
+          ok = tc::wait_all<false>(&ctl.k_empty[slot], ((n / NP) & 1) ^ 1, abort_flag, budget);
+          if (!ok) break;
         }
-        if (!see || lse[y] == -INFINITY) continue;
-        float dot = 0.f;
-        for (int d = 0; d < D; ++d) dot = fmaf(qs[y][d], ks[x][d], dot);
-        sum += expf(fmaf(dot, a.scale, -lse[y]));
+        const int32_t* row = a.table + (int64_t)cur.u_s * a.width;
+        // a lane loads one run of keys, or half its dimensions (32 of them at most)
+        const int u = lane / Sh::kHalves, half = lane % Sh::kHalves;
+        const int key = cur.u_p * kPair + u * unit_tok;
+        bool want = u < units && key < cur.kend;
+        int32_t id = 0;
+        if (want) {
+          id = row[key >> a.page_shift];
+          if (id < 0 || id >= a.pages) {
+            want = false;
+            record_error(err, kDevErrBadId);
+          }
+        }
+        const uint32_t load = __ballot_sync(0xFFFFFFFFu, want);
+        if (lane == 0)
+          tc::mbar_arrive_expect_tx(&ctl.k_full[slot], (uint32_t)(__popc(load) * unit_tok * 128));
+        __syncwarp();
+        if (want) {
+          const int at = u * unit_tok;  // key of the pair
+          uint8_t* dst = k_s + slot * Sh::kPairBytes + at / kKeys * Sh::kTile + half * (kKeys * 128) +
+                         at % kKeys * 128;
+          const int off = key & ((1 << a.page_shift) - 1);
+          tc::tma_load_4d(dst, &kmap, &ctl.k_full[slot], half * 64, k_head_first ? cur.u_hk : off,
+                          k_head_first ? off : cur.u_hk, id);
+        }
+        ++n;
+      }
+      if (!ok && lane == 0) {
+        *abort_flag = 1;
+        record_error(err, kDevErrTimeout);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        // no copy may be under way when the CTA ends, whichever role gave up
+        const uint32_t first = n > (uint32_t)NP ? n - NP : 0;
+        for (uint32_t j = first; j < n; ++j) {
+          const long long t = clock64();
+          while (!tc::mbar_try_wait(&ctl.k_full[j % NP], (j / NP) & 1) &&
+                 clock64() - t < tc::kWaitCycles) {
+          }
+        }
+      }
+    } else if (warp == 10) {
+      // ------------------------------------------------------------ queries and lse
+      asm volatile("fence.proxy.async;" ::: "memory");
+      uint32_t n = 0;
+      bool ok = true;
+      while (ok && cur.next(a)) {
+        for (int t = cur.t0 + cur.a; t < cur.t0 + cur.b; ++t, ++n) {
+          const int slot = (int)(n % NQ);
+          if (n >= (uint32_t)NQ) {
+            ok = tc::wait_all<false>(&ctl.q_empty[slot], ((n / NQ) & 1) ^ 1, abort_flag, budget);
+            if (!ok) break;
+          }
+          uint8_t* dst = q_s + slot * Sh::kQ;
+          const int tok = cur.r.tok0 + t * tile_tok, toks = min(tile_tok, cur.r.m - t * tile_tok);
+          const bool tma = q_by_tma && toks == tile_tok;
+          if (lane == 0)
+            tc::mbar_arrive_expect_tx(&ctl.q_full[slot],
+                                      tma ? (uint32_t)(tile_tok * group * 128 * Sh::kHalves) : 0u);
+          __syncwarp();
+          if (tma) {
+            if (lane < Sh::kHalves)
+              tc::tma_load_3d(dst + lane * (kRows * 128), &qmap, &ctl.q_full[slot], lane * 64,
+                              cur.u_hk * group, tok);
+          } else {
+            // a tile that is not full: row by row, zeros up to the product's columns
+            const int rows = toks * group, cols = (rows + 15) & ~15;
+            const uint32_t to = tc::smem_addr(dst);
+            for (int e = lane; e < cols * (D / 8); e += 32) {
+              const int row = e / (D / 8), c = e % (D / 8), tk = row / group;
+              const bool in = row < rows;
+              const char* src = static_cast<const char*>(a.q) + c * 16;
+              if (in)
+                src += (int64_t)(tok + tk) * a.q_tok + (int64_t)(cur.u_hk * group + row - tk * group) * a.q_head;
+              const int size = in ? 16 : 0;
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                               to + (c / 8) * (kRows * 128) + row * 128 + (((c % 8) ^ (row & 7)) << 4)),
+                           "l"(src), "r"(size)
+                           : "memory");
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kRows / 32; ++i) {
+            const int row = i * 32 + lane, tk = row / group;
+            float l = kInf;
+            if (tk < toks) {
+              l = a.lse[(int64_t)(tok + tk) * a.heads + cur.u_hk * group + row - tk * group];
+              l = l == -kInf ? kInf : l * kLog2e;  // a row that sees nothing draws nothing
+            }
+            ctl.lse[slot][row] = l;
+          }
+          if (!tma) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            tc::fence_async_smem();
+          }
+          tc::mbar_arrive(&ctl.q_full[slot]);
+        }
+      }
+      if (!ok && lane == 0) {
+        *abort_flag = 1;
+        record_error(err, kDevErrTimeout);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t first = n > (uint32_t)NQ ? n - NQ : 0;
+        for (uint32_t j = first; j < n; ++j) {
+          const long long t = clock64();
+          while (!tc::mbar_try_wait(&ctl.q_full[j % NQ], (j / NQ) & 1) &&
+                 clock64() - t < tc::kWaitCycles) {
+          }
+        }
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMAs
+      const bool issuer = tc::elect_one();
+      const uint64_t k_desc = tc::sw128_kmajor_desc(tc::smem_addr(k_s));
+      const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_addr(q_s));
+      uint32_t pairs = 0, step = 0, step1 = 0;  // step1: of the second tile
+      bool ok = true;
+      while (ok) {
+        // what branches and operands depend on comes by shuffle from lane 0, so that
+        // the compiler knows it to be the warp's own
+        const bool found = cur.next(a);
+        const int steps = __shfl_sync(0xFFFFFFFFu, found ? cur.b - cur.a : -1, 0);
+        if (steps < 0) break;
+        if (steps == 0) continue;
+        const bool both = __shfl_sync(0xFFFFFFFFu, (int)(cur.u_p * kPair + kKeys < cur.kend), 0) != 0;
+        const int first = __shfl_sync(0xFFFFFFFFu, (cur.r.m - (cur.t0 + cur.a) * tile_tok), 0);
+        const int k_slot = (int)(pairs % NP);
+        ok = tc::wait_all<true>(&ctl.k_full[k_slot], (pairs / NP) & 1, abort_flag, budget);
+        if (!ok) break;
+#pragma unroll 1
+        for (int t = 0; t < steps; ++t, ++step) {
+          const int q_slot = (int)(step % NQ);
+          const int rows = min(tile_tok, first - t * tile_tok) * group;
+          const uint32_t idesc = tc::idesc_f16_f32(BF16, kKeys, (uint32_t)((rows + 15) & ~15), false);
+          ok = tc::wait_all<true>(&ctl.q_full[q_slot], (step / NQ) & 1, abort_flag, budget);
+          if (!ok) break;
+          const uint64_t qd = q_desc + q_slot * (Sh::kQ / 16);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (w == 1 && !both) break;
+            const uint32_t use = w ? step1 : step;
+            const int buf = (int)(use & 1);
+            if (use >= 2) {
+              ok = tc::wait_all<true>(&ctl.s_empty[w][buf], ((use >> 1) & 1) ^ 1, abort_flag, budget);
+              if (!ok) break;
+            }
+            tc::fence_after_sync();
+            const uint64_t kd = k_desc + k_slot * (Sh::kPairBytes / 16) + w * (Sh::kTile / 16);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              constexpr int kHalf = kKeys * 128 / 16;
+              tc::mma_ss_one(issuer, tmem + (w * 2 + buf) * 128, kd + (c / 4) * kHalf + (c % 4) * 2,
+                             qd + (c / 4) * kHalf + (c % 4) * 2, idesc, c > 0);
+            }
+            tc::commit_one(issuer, &ctl.s_full[w][buf]);
+          }
+          if (!ok) break;
+          if (both) ++step1;
+          tc::commit_one(issuer, &ctl.q_empty[q_slot]);
+          __syncwarp();
+        }
+        if (!ok) break;
+        tc::commit_one(issuer, &ctl.k_empty[k_slot]);
+        ++pairs;
+      }
+      if (!ok && lane == 0) {
+        *abort_flag = 1;
+        record_error(err, kDevErrTimeout);
+      }
+      if (issuer) tc::mma_drain(&ctl.drain);  // TMEM is freed below
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ exponentials and sums
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMore));
+    const int w = warp >> 2, r = threadIdx.x & 127;  // key tile, key of it = TMEM lane
+    const uint32_t t_s = tmem + ((uint32_t)((warp & 3) * 32) << 16) + w * 256;
+    const float sl = a.scale * kLog2e;
+    const float2 sl2 = make_float2(sl, sl);
+    uint32_t step = 0, used = 0;  // query tiles, and those that this warpgroup had scores of
+    bool ok = true;
+    Piece piece = {0, 0, 0, 0};
+    auto page_of = [&]() -> int32_t {  // of this thread's key of the cursor's unit, or -1
+      const int j = cur.u_p * kPair + w * kKeys + r;
+      if (j >= cur.kend) return -1;
+      const int32_t id = a.table[(int64_t)cur.u_s * a.width + (j >> a.page_shift)];
+      return id;
+    };
+    bool have = cur.next(a);
+    int32_t next_id = have ? page_of() : -1;
+    while (ok && have) {
+      const int j = cur.u_p * kPair + w * kKeys + r, hk = cur.u_hk, len = cur.r.len;
+      const int tok0 = cur.r.tok0, m = cur.r.m, n = cur.n;
+      const int ta = cur.a, tb = cur.b, t0 = cur.t0, us = cur.u_s, up = cur.u_p;
+      int32_t id = next_id;
+      if (id >= a.pages) id = -1;
+      const bool idle = up * kPair + w * kKeys >= cur.kend;  // no key of this tile is one
+      // under way while the products are waited for: what the weight was, and the
+      // next unit's page
+      float old = 0.f;
+      const bool add = id >= 0 && j < len && a.decay != 0.f;
+      const bool cut = ta > 0 || tb < n;
+      if (add && !cut) old = *weight_at(a, id, j, hk);
+      have = cur.next(a);
+      next_id = have ? page_of() : -1;
+      float sum = 0.f;
+      for (int t = t0 + ta; t < t0 + tb; ++t, ++step) {
+        const int slot = (int)(step % NQ);
+        ok = tc::wait_all<false>(&ctl.q_full[slot], (step / NQ) & 1, abort_flag, budget);
+        if (!ok) break;
+        if (!idle) {
+          const int buf = (int)(used & 1);
+          ok = tc::wait_all<false>(&ctl.s_full[w][buf], (used >> 1) & 1, abort_flag, budget);
+          if (!ok) break;
+          ++used;
+          tc::fence_after_sync();
+          const int i0 = t * tile_tok, toks = min(tile_tok, m - i0), cols = toks * group;
+          // columns [lo, hi) see the key
+          int lo = 0, hi = cols;
+          if (!a.tree) {
+            const int late = j - len - i0;  // tokens of the tile that come before the key
+            lo = late <= 0 ? 0 : late >= toks ? cols : late * group;
+            if (a.window > 0) {
+              const long long past = (long long)late + a.window;
+              hi = past <= 0 ? 0 : past >= toks ? cols : (int)past * group;
+            }
+          } else if (j >= len) {
+            lo = cols;  // by their words, below
+          }
+          const float4* l4 = reinterpret_cast<const float4*>(ctl.lse[slot]);
+          const uint32_t from = t_s + buf * 128;
+          if (__all_sync(0xFFFFFFFFu, lo == 0 && hi == cols && cols > kRows - 16)) {
+            // every row of a whole product (what is behind the last has lse +inf and
+            // zeros for q): 32 columns are summed while the next are loaded
+            uint32_t s[2][32];
+            tc::tmem_ld32(from, s[0]);
+            float2 part[4] = {};
+#pragma unroll
+            for (int q = 0; q < kRows / 32; ++q) {
+              uint32_t(&v)[32] = s[q & 1];
+              tc::tmem_ld_wait(v);
+              if (q + 1 < kRows / 32) {
+                tc::tmem_ld32(from + (q + 1) * 32, s[(q + 1) & 1]);
+              } else {
+                tc::fence_before_sync();
+                tc::mbar_arrive(&ctl.s_empty[w][buf]);
+              }
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float4 l = l4[q * 8 + c];
+                float2 x = tc::fma_x2(make_float2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), sl2,
+                                      make_float2(-l.x, -l.y));
+                float2 y = tc::fma_x2(make_float2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), sl2,
+                                      make_float2(-l.z, -l.w));
+                x.x = tc::exp2_approx(x.x);
+                x.y = tc::exp2_approx(x.y);
+                y.x = tc::exp2_approx(y.x);
+                y.y = tc::exp2_approx(y.y);
+                part[c % 2 * 2] = tc::add_x2(part[c % 2 * 2], x);
+                part[c % 2 * 2 + 1] = tc::add_x2(part[c % 2 * 2 + 1], y);
+              }
+            }
+            const float2 x = tc::add_x2(tc::add_x2(part[0], part[1]), tc::add_x2(part[2], part[3]));
+            sum += x.x + x.y;
+          } else {
+            float some = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 32) {
+              uint32_t v[32];
+              tc::tmem_ld32(from + c, v);
+              tc::tmem_ld_wait(v);
+              uint32_t see = tc::span_bits(lo - c, hi - c);
+              if (a.tree && j >= len && j - len < 64) {
+                for (int i = c / group; i <= (c + 31) / group && i < toks; ++i)
+                  if (a.tree[tok0 + i0 + i] >> (j - len) & 1)
+                    see |= tc::span_bits(i * group - c, (i + 1) * group - c);
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float x = tc::exp2_approx(fmaf(__uint_as_float(v[i]), sl, -ctl.lse[slot][c + i]));
+                some += (see >> i) & 1 ? x : 0.f;
+              }
+            }
+            sum += some;
+            tc::fence_before_sync();
+            tc::mbar_arrive(&ctl.s_empty[w][buf]);
+          }
+        }
+        tc::mbar_arrive(&ctl.q_empty[slot]);
+      }
+      if (!ok) break;
+      if (cut) {
+        const bool begins = ta == 0, ends = tb == n;
+        if (begins) piece = {us, up, hk, piece.flags | kBegins};
+        else if (!ends) piece.flags |= kGoesOn;
+        sc.sums[((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kPair + w * kKeys + r] = sum;
+      } else if (id >= 0) {
+        *weight_at(a, id, j, hk) = add ? fmaf(a.decay, old, sum) : sum;
       }
     }
-    part[grp][x] = sum;
-    cta_sync();
-    if (grp == 0 && id >= 0) {
-      float* w = reinterpret_cast<float*>(static_cast<char*>(a.weights) + id * a.ws.page +
-                                          off * a.ws.token + hk * a.ws.head);
-      const float fresh = (part[0][x] + part[1][x]) + (part[2][x] + part[3][x]);
-      *w = j < len && a.decay != 0.f ? fmaf(a.decay, *w, fresh) : fresh;
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      record_error(err, kDevErrTimeout);
     }
-    cta_sync();
+    if (threadIdx.x == 0 && !whole_only) sc.piece[blockIdx.x] = piece;
+  }
+  tc::fence_before_sync();
+  cta_sync();
+  if (warp == 9) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
   }
 }
+
+// The sums of the pair that begins in CTA c and goes on behind it, in order.
+__global__ void __launch_bounds__(kPair) join_kernel(const WeightArgs a, const Scratch sc, int parts) {
+  pdl_wait();
+  pdl_trigger();
+  const int k = threadIdx.x;
+  int c = blockIdx.x;
+  const Piece u = sc.piece[c];
+  if (!(u.flags & kBegins)) return;
+  float sum = sc.sums[((int64_t)c * 2 + 1) * kPair + k];
+  for (++c; c < parts; ++c) {
+    sum += sc.sums[(int64_t)c * 2 * kPair + k];
+    if (!(sc.piece[c].flags & kGoesOn)) break;
+  }
+  const int j = u.p * kPair + k, len = a.lens[u.s];
+  if (j >= len + a.cu[u.s + 1] - a.cu[u.s]) return;
+  const int32_t id = a.table[(int64_t)u.s * a.width + (j >> a.page_shift)];
+  if (id < 0 || id >= a.pages) return;
+  float* w = weight_at(a, id, j, u.hk);
+  *w = j < len && a.decay != 0.f ? fmaf(a.decay, *w, sum) : sum;
+}
+
+inline int part_count() { return sm_count() > 0 ? sm_count() : 1; }
+
+template <bool BF16, int D>
+cudaError_t launch_all(const WeightArgs& a, const Scratch& sc, int parts, int* err, cudaStream_t s) {
+  const int page = 1 << a.page_shift, group = a.heads / a.kv_heads, tile_tok = kRows / group;
+  const bool head_first = a.ks.head <= a.ks.token;
+  CUtensorMap kmap, qmap;
+  if (!make_cache_map(&kmap, a.k_cache, BF16, D, page, a.kv_heads, a.pages, a.ks,
+                      page < kKeys ? page : kKeys, head_first))
+    return cudaErrorInvalidValue;
+  // a full tile of queries comes by one copy where a token's heads lie within its stride
+  const int64_t row = (int64_t)D * 2;
+  const int64_t q_head = a.heads > 1 ? a.q_head : row;
+  const int64_t q_tok = a.T > 1 ? a.q_tok : q_head * a.heads;
+  const bool by_tma = q_tok >= (a.heads - 1) * q_head + row && a.T >= tile_tok;
+  qmap = kmap;
+  if (by_tma && !make_rows_map(&qmap, a.q, BF16, D, a.heads, a.T, q_head, q_tok, group, tile_tok))
+    return cudaErrorInvalidValue;
+  // Cutting pairs between CTAs costs the second launch; it pays where a request has
+  // several query tiles a pair.
+  const bool whole = a.T <= (int64_t)2 * tile_tok * a.S;
+  static int smem_set[64] = {0};
+  cudaError_t e = ensure_dynamic_smem(weights_kernel<BF16, D>, Shape<D>::kSmem, smem_set);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(true, weights_kernel<BF16, D>, dim3(parts), dim3(kThreads), Shape<D>::kSmem, s, kmap,
+                    qmap, a, sc, (int)head_first, (int)by_tma, (int)whole, role_wait_cycles(), err);
+  if (e != cudaSuccess || whole) return e;
+  return launch_kernel(true, join_kernel, dim3(parts), dim3(kPair), 0, s, a, sc, parts);
+}
+
+inline size_t sums_at(int parts) { return ((size_t)parts * sizeof(Piece) + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t weights_scratch_bytes(int) { return 256; }
+size_t weights_scratch_bytes() {
+  const int parts = part_count();
+  return sums_at(parts) + (size_t)parts * 2 * kPair * sizeof(float);
+}
 
-cudaError_t launch_cache_weights(const WeightArgs& a, void*, int* err, cudaStream_t s) {
-  const dim3 grid((((unsigned)a.width << a.page_shift) + kKeys - 1) / kKeys, a.kv_heads,
-                  a.S < 65535 ? a.S : 65535);
+cudaError_t launch_cache_weights(const WeightArgs& a, void* scratch, int* err, cudaStream_t s) {
+  const int parts = part_count();
+  char* p = static_cast<char*>(scratch);
+  const Scratch sc = {reinterpret_cast<Piece*>(p), reinterpret_cast<float*>(p + sums_at(parts))};
   if (a.dtype == LMHEAD_BF16)
-    return a.dim == 64 ? launch_kernel(true, weights_kernel<true, 64>, grid, dim3(kThreads), 0, s, a, err)
-                       : launch_kernel(true, weights_kernel<true, 128>, grid, dim3(kThreads), 0, s, a, err);
-  return a.dim == 64 ? launch_kernel(true, weights_kernel<false, 64>, grid, dim3(kThreads), 0, s, a, err)
-                     : launch_kernel(true, weights_kernel<false, 128>, grid, dim3(kThreads), 0, s, a, err);
+    return a.dim == 64 ? launch_all<true, 64>(a, sc, parts, err, s)
+                       : launch_all<true, 128>(a, sc, parts, err, s);
+  return a.dim == 64 ? launch_all<false, 64>(a, sc, parts, err, s)
+                     : launch_all<false, 128>(a, sc, parts, err, s);
 }
 
 }  // namespace lmhead

@@ -527,3 +527,24 @@ def test_release_bad_lengths():
     assert L.last_device_error() == -7 and left.tolist() == [6]
     left = L.page_release(_i32([16]), _i32([16]), table[:1], torch.zeros(0, dtype=torch.int32, device="cuda"), _i32([0]), 16)
     assert L.last_device_error() == 0 and left.tolist() == [0]
+
+
+@pytest.mark.gpu
+def test_weights_waits_that_run_out():
+    """With no time to wait a call gives up, says so, and the next one is right."""
+    from gpu_util import lib
+    L = lib()
+    c = _weights_case([600, 70], [300, 3], 8, 2, 128, 64, "bfloat16", 13)
+    lse, _ = _lse(c, 0)
+    args = (c["q"], c["kc"], c["table"], c["lens"], c["cu"], lse)
+    want = L.cache_weights(*args, c["w"].clone())
+    assert L.last_device_error() == 0
+    L.debug_set_wait_cycles(0)
+    try:
+        L.cache_weights(*args, c["w"].clone())
+        status = L.last_device_error()
+    finally:
+        L.debug_set_wait_cycles(-1)
+    assert status == -8
+    assert np.array_equal(_n64(L.cache_weights(*args, c["w"].clone())), _n64(want), equal_nan=True)
+    assert L.last_device_error() == 0
