@@ -9,36 +9,50 @@
 namespace lmhead {
 namespace {
 
+// Page and place in it of a position: pages of a power of two by shift, others by
+// division.
+__device__ __forceinline__ void split_pos(uint32_t pos, int page, int shift, int& pg, int& off) {
+  if (shift >= 0) {
+    pg = (int)(pos >> shift);
+    off = (int)(pos & ((1u << shift) - 1u));
+  } else {
+    pg = (int)(pos / (uint32_t)page);
+    off = (int)(pos - (uint32_t)pg * (uint32_t)page);
+  }
+}
+
 // ------------------------------------------------------------------ select
 // Of a request's L tokens and one K/V head the first `sinks`, the last `recent`
 // and, of those between, the ones with the largest weights (ties: the lower
 // position) up to `budget` in all, in ascending order.
 // One CTA a request and head: the weights' order-preserving keys go to shared
-// memory, four passes of eight bits find the key of the last one to stay and how
-// many equal to it stay with it, and a last pass writes the positions that pass,
-// each warp those of a run of its own behind the counts of the runs before.
+// memory and are counted by digits from the top (11, 11 and 10 bits, while the digit
+// of the last one to stay holds others that do not) in four copies, as weights crowd
+// in few exponents; a last pass writes the positions that pass, each warp those of
+// a run of its own behind the counts of the runs before.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048, kCopies = 4;
+constexpr int kMostStaged = 48 * 1024 - kBins * kCopies;  // keys; those behind are read again
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   return w != w ? 0u : float_key(w);  // a NaN comes last
 }
 
 __global__ void __launch_bounds__(kSelThreads)
-select_kernel(const SelectArgs a, int staged, int* err) {
-  extern __shared__ uint32_t keys[];
-  __shared__ int hist[256];
+select_kernel(const SelectArgs a, int shift, int staged, int* err) {
+  extern __shared__ __align__(16) int hist[];  // kBins x kCopies, then the keys
+  uint32_t* keys = reinterpret_cast<uint32_t*>(hist + kBins * kCopies);
   __shared__ int more_w[kSelWarps], same_w[kSelWarps];
-  __shared__ int sh_need, sh_digit;
+  __shared__ int sh_need, sh_digit, sh_count;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int head = blockIdx.x;
   for (int s = blockIdx.y; s < a.S; s += gridDim.y) {
     int32_t* out = a.kept + ((int64_t)s * a.kv_heads + head) * a.budget;
-    const int64_t room = (int64_t)a.width * a.page;
     int L = a.lens[s];
-    if (L < 0 || L > room) {
+    if (L < 0 || L > (int64_t)a.width * a.page) {
       if (tid == 0) record_error(err, kDevErrBadId);
       L = 0;
     }
@@ -48,92 +62,118 @@ select_kernel(const SelectArgs a, int staged, int* err) {
     }
     const int lo = min(a.sinks, L), hi = max(lo, L - a.recent);  // positions that are chosen from
     int need = a.budget - lo - (L - hi);
+    for (int i = tid; i < lo; i += kSelThreads) out[i] = i;
+    for (int i = tid; i < L - hi; i += kSelThreads) out[a.budget - (L - hi) + i] = hi + i;
+    if (need == 0) continue;
     const int32_t* row = a.table + (int64_t)s * a.width;
+    const char* weights = static_cast<const char*>(a.weights) + head * a.ws.head;
     auto key_of = [&](int j) -> uint32_t {
-      const int pg = j / a.page;
+      int pg, off;
+      split_pos((uint32_t)j, a.page, shift, pg, off);
       const int32_t id = row[pg];
       if (id < 0 || id >= a.pages) {
         record_error(err, kDevErrBadId);
         return 0u;
       }
-      return weight_key(*reinterpret_cast<const float*>(static_cast<const char*>(a.weights) +
-                                                        id * a.ws.page + (j - pg * a.page) * a.ws.token +
-                                                        head * a.ws.head));
+      return weight_key(*reinterpret_cast<const float*>(weights + id * a.ws.page + off * a.ws.token));
     };
-    for (int j = lo + tid; j < hi && j - lo < staged; j += kSelThreads) keys[j - lo] = key_of(j);
-    auto key = [&](int j) { return j - lo < staged ? keys[j - lo] : key_of(j); };
+    const int kept_keys = min(staged, hi - lo);
+    auto key = [&](int i) { return i < kept_keys ? keys[i] : key_of(lo + i); };  // of position lo + i
+    const int total = hi - lo;
     uint32_t prefix = 0, mask = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+    int top = 21, bits = 11;
+    for (;;) {
+      for (int i = tid; i < kBins * kCopies / 4; i += kSelThreads)
+        reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
       cta_sync();
-      for (int j = lo + tid; j < hi; j += kSelThreads) {
-        const uint32_t k = key(j);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+      if (mask == 0) {  // the first time the keys are read
+#pragma unroll 4
+        for (int i = tid; i < total; i += kSelThreads) {
+          const uint32_t k = key_of(lo + i);
+          if (i < kept_keys) keys[i] = k;
+          atomicAdd(&hist[(k >> top) * kCopies + (lane & (kCopies - 1))], 1);
+        }
+      } else {
+        for (int i = tid; i < total; i += kSelThreads) {
+          const uint32_t k = key(i);
+          if ((k & mask) == prefix)
+            atomicAdd(&hist[((k >> top) & ((1u << bits) - 1u)) * kCopies + (lane & (kCopies - 1))], 1);
+        }
       }
       cta_sync();
-      if (warp == 0) {
-        // the digit in which the need-th largest lies: counts from the top
-        int c[8], sum = 0;
+      // the digit in which the need-th largest lies: counts from the top, two bins a thread
+      constexpr int kPer = kBins / kSelThreads;
+      int c[kPer], sum = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          c[i] = hist[255 - (lane * 8 + i)];
-          sum += c[i];
-        }
-        int incl = sum;
+      for (int i = 0; i < kPer; ++i) {
+        const int4 v = reinterpret_cast<const int4*>(hist)[kBins - 1 - (tid * kPer + i)];
+        c[i] = v.x + v.y + v.z + v.w;
+        sum += c[i];
+      }
+      int incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int p = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += p;
+      }
+      if (lane == 31) more_w[warp] = incl;
+      cta_sync();
+      int at = incl - sum;
+      {
+        const int w = more_w[lane];
+        int before = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int p = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-          if (lane >= o) incl += p;
+          const int p = __shfl_up_sync(0xFFFFFFFFu, before, o);
+          if (lane >= o) before += p;
         }
-        int at = incl - sum;
-        if (at < need && need <= incl) {
+        at += __shfl_sync(0xFFFFFFFFu, before - w, warp);
+      }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (at < need && need <= at + c[i]) {
-              sh_digit = 255 - (lane * 8 + i);
-              sh_need = need - at;
-            }
-            at += c[i];
-          }
+      for (int i = 0; i < kPer; ++i) {
+        if (at < need && need <= at + c[i]) {
+          sh_digit = kBins - 1 - (tid * kPer + i);
+          sh_need = need - at;
+          sh_count = c[i];
         }
-        if (need == 0 && lane == 0) sh_digit = 255, sh_need = 0;
+        at += c[i];
       }
       cta_sync();
-      prefix |= (uint32_t)sh_digit << shift;
-      mask |= 255u << shift;
+      prefix |= (uint32_t)sh_digit << top;
+      mask |= ((1u << bits) - 1u) << top;
       need = sh_need;
-      cta_sync();
+      if (sh_count == need || top == 0) break;  // all of the digit's stay, or they are equal
+      bits = top >= 11 ? min(11, top) : top;
+      top -= bits;
     }
-    // `need` of the keys equal to prefix stay, the first ones; with nothing to
-    // choose prefix is the largest key of all, and none of its equals stays
-    const int run = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-    const int r0 = min(hi, lo + warp * run), r1 = min(hi, r0 + run);
+    // keys above prefix (in the digits looked at) stay, and the first `need` equal to it
+    const int run = ((total + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+    const int r0 = min(total, warp * run), r1 = min(total, r0 + run);
     int more = 0, same = 0;
-    for (int j = r0 + lane; j < r1; j += 32) {
-      const uint32_t k = key(j);
+    for (int i = r0 + lane; i < r1; i += 32) {
+      const uint32_t k = key(i) & mask;
       more += k > prefix;
       same += k == prefix;
     }
     more = __reduce_add_sync(0xFFFFFFFFu, more);
     same = __reduce_add_sync(0xFFFFFFFFu, same);
+    cta_sync();
     if (lane == 0) more_w[warp] = more, same_w[warp] = same;
     cta_sync();
-    int before = 0, equal = 0;
-    for (int w = 0; w < warp; ++w) before += more_w[w], equal += same_w[w];
-    for (int j0 = r0; j0 < r1; j0 += 32) {
-      const int j = j0 + lane;
-      const uint32_t k = j < r1 ? key(j) : 0u;
-      const bool is_more = j < r1 && k > prefix, is_same = j < r1 && k == prefix;
+    int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? more_w[lane] : 0);
+    int equal = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? same_w[lane] : 0);
+    for (int i0 = r0; i0 < r1; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t k = i < r1 ? key(i) & mask : 0u;
+      const bool is_more = i < r1 && k > prefix, is_same = i < r1 && k == prefix;
       const uint32_t m = __ballot_sync(0xFFFFFFFFu, is_more), e = __ballot_sync(0xFFFFFFFFu, is_same);
       const uint32_t below = (1u << lane) - 1u;
       const int eq = equal + __popc(e & below);
       if (is_more || (is_same && eq < need))
-        out[lo + before + __popc(m & below) + min(eq, need)] = j;
+        out[lo + before + __popc(m & below) + min(eq, need)] = lo + i;
       before += __popc(m);
       equal += __popc(e);
     }
-    for (int i = tid; i < lo; i += kSelThreads) out[i] = i;
-    for (int i = tid; i < L - hi; i += kSelThreads) out[a.budget - (L - hi) + i] = hi + i;
     cta_sync();
   }
 }
@@ -142,92 +182,115 @@ select_kernel(const SelectArgs a, int staged, int* err) {
 // Row first + i of a request becomes what row first + kept[i] was, kept[i] >= i.
 // A row is read from its own place or from one behind it, so rows moved in
 // ascending order are read before they are overwritten. A CTA moves one slice of
-// the rows' bytes of one tensor and head, for all of the request's list, tile
-// after tile: it reads a tile's rows, waits for all its threads, and writes them;
-// what it reads later lies behind all that it has written. CTAs share no bytes.
+// the rows' bytes of one tensor and head, for all of the request's list, chunk after
+// chunk: where the rows lie is worked out once for each (a thread a row), then their
+// vectors are read into registers, all threads waited for, and written; what is read
+// later lies behind all that has been written. CTAs share no bytes.
 constexpr int kKeepThreads = 256;
 constexpr int kKeepUnroll = 8;
+constexpr int kKeepChunk = 1024;  // rows
+
+struct KeepRows {
+  int64_t from[kKeepChunk], to[kKeepChunk];  // byte offsets; from < 0: not moved
+};
 
 template <typename V>
-__device__ __forceinline__ void move_slice(const KeepArgs& a, const KeepTensor& t, int s, int head,
-                                           int byte0, int bytes, int* err) {
-  const int lanes = bytes / (int)sizeof(V);  // of a row; 256 at most
+__device__ __forceinline__ void move_rows(const KeepRows& rows, int count, char* base, int bytes) {
+  const int lanes = bytes / (int)sizeof(V);  // of a row; no more than the CTA has threads
   const int per = kKeepThreads / lanes;      // rows a pass
   const int c = threadIdx.x % lanes, r = threadIdx.x / lanes;
-  const bool in = r < per;
-  const int32_t* row = a.table + (int64_t)s * a.width;
-  const int32_t* kept = a.kept + ((int64_t)s * (a.per_head ? a.kv_heads : 1) + (a.per_head ? head : 0)) * a.n;
-  const int64_t first = a.first ? a.first[s] : 0, room = (int64_t)a.width * a.page;
-  char* base = static_cast<char*>(t.base) + head * t.st.head + byte0 + c * sizeof(V);
-  auto place = [&](int64_t pos) -> char* {
-    const int pg = (int)(pos / a.page);
-    const int32_t id = row[pg];
-    if (id < 0 || id >= a.pages) return nullptr;
-    return base + id * t.st.page + (pos - (int64_t)pg * a.page) * t.st.token;
-  };
-  for (int i0 = 0; i0 < a.n; i0 += per * kKeepUnroll) {
+  base += c * sizeof(V);
+  for (int i0 = 0; i0 < count; i0 += per * kKeepUnroll) {
     V v[kKeepUnroll];
-    char* to[kKeepUnroll];
+    uint32_t some = 0;
 #pragma unroll
     for (int k = 0; k < kKeepUnroll; ++k) {
       const int i = i0 + k * per + r;
-      to[k] = nullptr;
-      const int32_t from = in && i < a.n ? kept[i] : -1;
-      if (from < 0 || from == i) continue;
-      char* src = nullptr;
-      if (from > i && first + from < room) {
-        src = place(first + from);
-        to[k] = place(first + i);
+      if (r < per && i < count && rows.from[i] >= 0) {
+        v[k] = *reinterpret_cast<const V*>(base + rows.from[i]);
+        some |= 1u << k;
       }
-      if (!src || !to[k]) {
-        to[k] = nullptr;
-        record_error(err, kDevErrBadId);
-        continue;
-      }
-      v[k] = *reinterpret_cast<const V*>(src);
     }
     cta_sync();
 #pragma unroll
     for (int k = 0; k < kKeepUnroll; ++k)
-      if (to[k]) *reinterpret_cast<V*>(to[k]) = v[k];
+      if (some >> k & 1) *reinterpret_cast<V*>(base + rows.to[i0 + k * per + r]) = v[k];
   }
 }
 
 __global__ void __launch_bounds__(kKeepThreads)
-keep_kernel(const KeepArgs a, int* err) {
+keep_kernel(const KeepArgs a, int shift, int* err) {
+  __shared__ KeepRows rows;
+  __shared__ int sh_last, sh_moves;
   pdl_wait();
   pdl_trigger();
   // the slice: of which tensor, head and bytes
+  const int tid = threadIdx.x;
   int x = blockIdx.x, ti = 0;
   while (x >= a.t[ti].slices * a.kv_heads) x -= a.t[ti++].slices * a.kv_heads;
   const KeepTensor& t = a.t[ti];
   const int head = x / t.slices, sl = x - head * t.slices;
   const int byte0 = sl * t.slice, bytes = min(t.slice, t.row - byte0);
+  char* base = static_cast<char*>(t.base) + head * t.st.head + byte0;
+  const int64_t room = (int64_t)a.width * a.page;
   for (int s = blockIdx.y; s < a.S; s += gridDim.y) {
     const int32_t first = a.first ? a.first[s] : 0;
+    const int32_t* table = a.table + (int64_t)s * a.width;
+    const int32_t* kept = a.kept + ((int64_t)s * (a.per_head ? a.kv_heads : 1) + (a.per_head ? head : 0)) * a.n;
+    auto place = [&](int64_t pos) -> int64_t {
+      int pg, off;
+      split_pos((uint32_t)pos, a.page, shift, pg, off);
+      const int32_t id = table[pg];
+      return id < 0 || id >= a.pages ? -1 : id * t.st.page + off * t.st.token;
+    };
+    int last = 0;
+    if (tid == 0) sh_last = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kKeepChunk) {
+      const int count = min(kKeepChunk, a.n - i0);
+      cta_sync();  // the chunk before has been moved
+      if (tid == 0) sh_moves = 0;
+      cta_sync();
+      bool moves = false;
+#pragma unroll
+      for (int k = 0; k < kKeepChunk / kKeepThreads; ++k) {
+        const int i = i0 + k * kKeepThreads + tid;
+        const int32_t from = i < a.n ? kept[i] : -1;
+        int64_t src = -1, dst = -1;
+        if (from >= 0) last = i + 1;
+        if (from >= 0 && from != i && first >= 0) {
+          if (from > i && (int64_t)first + from < room) {
+            src = place((int64_t)first + from);
+            dst = place((int64_t)first + i);
+          }
+          if (src < 0 || dst < 0) {
+            src = -1;
+            record_error(err, kDevErrBadId);
+          } else {
+            moves = true;
+          }
+        }
+        rows.from[i - i0] = src;
+        rows.to[i - i0] = dst;
+      }
+      if (__any_sync(0xFFFFFFFFu, moves) && (tid & 31) == 0) sh_moves = 1;
+      cta_sync();
+      if (!sh_moves) continue;
+      switch (t.vec) {
+        case 16: move_rows<uint4>(rows, count, base, bytes); break;
+        case 4: move_rows<uint32_t>(rows, count, base, bytes); break;
+        case 2: move_rows<uint16_t>(rows, count, base, bytes); break;
+        default: move_rows<uint8_t>(rows, count, base, bytes); break;
+      }
+    }
     if (blockIdx.x == 0) {
       // the rows that the list leaves: up to its last entry that is one
-      const int32_t* kept = a.kept + (int64_t)s * (a.per_head ? a.kv_heads : 1) * a.n;
-      __shared__ int sh_last;
-      if (threadIdx.x == 0) sh_last = 0;
-      cta_sync();
-      int last = 0;
-      for (int i = threadIdx.x; i < a.n; i += kKeepThreads)
-        if (kept[i] >= 0) last = i + 1;
       last = __reduce_max_sync(0xFFFFFFFFu, last);
-      if ((threadIdx.x & 31) == 0) atomicMax(&sh_last, last);
+      if ((tid & 31) == 0) atomicMax(&sh_last, last);
       cta_sync();
-      if (threadIdx.x == 0) {
+      if (tid == 0) {
         a.new_lens[s] = first + (first >= 0 ? sh_last : 0);
         if (first < 0) record_error(err, kDevErrBadId);
       }
-    }
-    if (first < 0) continue;
-    switch (t.vec) {
-      case 16: move_slice<uint4>(a, t, s, head, byte0, bytes, err); break;
-      case 4: move_slice<uint32_t>(a, t, s, head, byte0, bytes, err); break;
-      case 2: move_slice<uint16_t>(a, t, s, head, byte0, bytes, err); break;
-      default: move_slice<uint8_t>(a, t, s, head, byte0, bytes, err); break;
     }
     cta_sync();
   }
@@ -239,6 +302,7 @@ keep_kernel(const KeepArgs a, int* err) {
 // kReleaseReqs requests and counts the pages of all earlier ones by itself.
 constexpr int kReleaseThreads = 256;
 constexpr int kReleaseReqs = 8;
+constexpr int kReleaseUnroll = 4;  // pages of a thread under way together
 
 struct Gone {
   int first, count;  // pages of the request's table that go
@@ -266,73 +330,120 @@ __device__ __forceinline__ Gone gone_of(const ReleaseArgs& a, int s) {
 __global__ void __launch_bounds__(kReleaseThreads)
 release_kernel(const ReleaseArgs a, int* err) {
   __shared__ int sh_sum[kReleaseThreads / 32];
-  __shared__ int r_at[kReleaseReqs], r_first[kReleaseReqs], r_count[kReleaseReqs];
+  __shared__ int r_end[kReleaseReqs + 1], r_first[kReleaseReqs];
+  __shared__ int64_t sh_at;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, first = blockIdx.x * kReleaseReqs;
+  const int tid = threadIdx.x, lane = tid & 31, first = blockIdx.x * kReleaseReqs;
   const int count = min(kReleaseReqs, a.S - first);
   int sum = 0;  // S * width fits 32 bits
   for (int s = tid; s < first; s += kReleaseThreads) sum += gone_of(a, s).count;
   sum = __reduce_add_sync(0xFFFFFFFFu, sum);
-  if ((tid & 31) == 0) sh_sum[tid >> 5] = sum;
-  cta_sync();
-  if (tid == 0) {
-    const int F = max(0, min(*a.free_count, a.free_cap));
-    int64_t at = F;
-    for (int w = 0; w < kReleaseThreads / 32; ++w) at += sh_sum[w];
-    for (int i = 0; i < count; ++i) {
-      const Gone g = gone_of(a, first + i);
-      if (!g.sane) record_error(err, kDevErrBadId);
-      // what has no room in the list is not put there
-      const int fit = (int)max((int64_t)0, min((int64_t)g.count, a.free_cap - at));
-      if (fit < g.count) record_error(err, kDevErrBadId);
-      r_at[i] = (int)min(at, (int64_t)a.free_cap);
-      r_first[i] = g.first;
-      r_count[i] = fit;
-      at += g.count;
+  if (lane == 0) sh_sum[tid >> 5] = sum;
+  if (tid < 32) {
+    // the CTA's requests, a lane each: where their pages lie among the CTA's
+    Gone g = {0, 0, true};
+    if (lane < count) g = gone_of(a, first + lane);
+    if (!g.sane && blockIdx.y == 0) record_error(err, kDevErrBadId);
+    int incl = g.count;
+#pragma unroll
+    for (int o = 1; o < kReleaseReqs; o <<= 1) {
+      const int p = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += p;
     }
-    if (first + count == a.S) *a.free_left = (int32_t)min(at, (int64_t)a.free_cap);
+    if (lane < kReleaseReqs) {
+      r_end[lane + 1] = incl;
+      r_first[lane] = g.first;
+    }
+    if (lane == 0) r_end[0] = 0;
   }
   cta_sync();
-  for (int i = tid >> 5; i < count; i += kReleaseThreads / 32)
-    for (int j = tid & 31; j < r_count[i]; j += 32)
-      a.free_pages[r_at[i] + j] = a.table[(int64_t)(first + i) * a.width + r_first[i] + j];
+  if (tid == 0) {
+    int64_t at = max(0, min(*a.free_count, a.free_cap));
+    for (int w = 0; w < kReleaseThreads / 32; ++w) at += sh_sum[w];
+    sh_at = at;
+    const int64_t end = at + r_end[count];
+    // what has no room in the list is not put there
+    if (blockIdx.y == 0 && end > a.free_cap) record_error(err, kDevErrBadId);
+    if (blockIdx.y == 0 && first + count == a.S) *a.free_left = (int32_t)min(end, (int64_t)a.free_cap);
+  }
+  cta_sync();
+  const int64_t at = sh_at;
+  const int total = (int)max((int64_t)0, min((int64_t)r_end[count], a.free_cap - at));
+  const int stride = gridDim.y * kReleaseThreads;
+  for (int64_t e0 = blockIdx.y * kReleaseThreads + tid; e0 < total; e0 += kReleaseUnroll * stride) {
+    int32_t id[kReleaseUnroll];
+#pragma unroll
+    for (int k = 0; k < kReleaseUnroll; ++k) {
+      const int64_t e = e0 + k * stride;
+      if (e >= total) break;
+      int i = 0;
+      while (e >= r_end[i + 1]) ++i;
+      id[k] = a.table[(int64_t)(first + i) * a.width + r_first[i] + (e - r_end[i])];
+    }
+#pragma unroll
+    for (int k = 0; k < kReleaseUnroll; ++k) {
+      const int64_t e = e0 + k * stride;
+      if (e < total) a.free_pages[at + e] = id[k];
+    }
+  }
+}
+
+}  // namespace
+
+namespace {
+
+inline int shift_of(int page) {  // log2 of a power of two, else -1
+  int s = 0;
+  while ((1 << s) < page) ++s;
+  return (1 << s) == page ? s : -1;
 }
 
 }  // namespace
 
 cudaError_t launch_cache_select(const SelectArgs& a, int* err, cudaStream_t s) {
-  // keys that do not fit in shared memory are read again in each pass
-  constexpr int kMost = 48 * 1024;
   const int64_t room = (int64_t)a.width * a.page;
-  const int staged = (int)(room < kMost ? room : kMost);
+  const int staged = (int)(room < kMostStaged ? room : kMostStaged);
   static int smem_set[64] = {0};
-  const size_t smem = (size_t)staged * 4;
+  const size_t smem = (size_t)(kBins * kCopies + staged) * 4;
   cudaError_t e = ensure_dynamic_smem(select_kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
   return launch_kernel(true, select_kernel, dim3(a.kv_heads, a.S < 65535 ? a.S : 65535),
-                       dim3(kSelThreads), smem, s, a, staged, err);
+                       dim3(kSelThreads), smem, s, a, shift_of(a.page), staged, err);
 }
 
 cudaError_t launch_cache_keep(KeepArgs a, int* err, cudaStream_t s) {
+  // Short lists are moved in whole rows, long ones in slices of 256 bytes, or fewer
+  // down to 64 where there are too few of them to fill the GPU.
+  int slice = a.n > 64 ? 256 : kKeepThreads * 16;
+  const int64_t want = 4ll * (sm_count() > 0 ? sm_count() : 1);
+  auto slices_of = [&](int width) {
+    int64_t n = 0;
+    for (int i = 0; i < a.count; ++i) n += (a.t[i].row + width - 1) / width;
+    return n * a.kv_heads;
+  };
+  while (a.n > 64 && slice > 64 && slices_of(slice) * a.S < want) slice /= 2;
   int64_t slices = 0;
   for (int i = 0; i < a.count; ++i) {
     KeepTensor& t = a.t[i];
     const uintptr_t bits = reinterpret_cast<uintptr_t>(t.base) | (uintptr_t)t.st.page |
                            (uintptr_t)t.st.token | (uintptr_t)t.st.head | (uintptr_t)t.row;
     t.vec = (bits & 15) == 0 ? 16 : (bits & 3) == 0 ? 4 : (bits & 1) == 0 ? 2 : 1;
-    // long lists are moved in narrow slices, so that a request's rows are many CTAs'
-    // work; short ones in whole rows, of no more vectors than a CTA has threads
-    t.slice = a.n > 64 ? 64 : t.vec * kKeepThreads;
+    // no more vectors than a CTA has threads
+    t.slice = slice < t.vec * kKeepThreads ? slice : t.vec * kKeepThreads;
     t.slices = (t.row + t.slice - 1) / t.slice;
     slices += (int64_t)t.slices * a.kv_heads;
   }
+  if (slices > INT32_MAX) return cudaErrorInvalidValue;
   return launch_kernel(true, keep_kernel, dim3((unsigned)slices, a.S < 65535 ? a.S : 65535),
-                       dim3(kKeepThreads), 0, s, a, err);
+                       dim3(kKeepThreads), 0, s, a, shift_of(a.page), err);
 }
 
 cudaError_t launch_page_release(const ReleaseArgs& a, int* err, cudaStream_t s) {
-  return launch_kernel(true, release_kernel, dim3((a.S + kReleaseReqs - 1) / kReleaseReqs),
+  // several CTAs for the pages of the same requests where tables are wide
+  int64_t y = (int64_t)a.width * kReleaseReqs / (kReleaseThreads * kReleaseUnroll * 2);
+  y = y < 1 ? 1 : y > 64 ? 64 : y;
+  return launch_kernel(true, release_kernel, dim3((a.S + kReleaseReqs - 1) / kReleaseReqs, (unsigned)y),
                        dim3(kReleaseThreads), 0, s, a, err);
 }
 

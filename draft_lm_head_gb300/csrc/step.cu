@@ -154,7 +154,9 @@ int lmhead_cache_keep(int count, void* const* base, const int64_t* page_stride,
   if (count < 1 || count > kKeepMax) return LMHEAD_ERR_UNSUPPORTED;
   const int st = check_table(S, width, pages, page_size);
   if (st != LMHEAD_OK) return st;
-  if (kv_heads < 1 || kv_heads > 65535 || n < 1 || (int64_t)S * n > INT32_MAX) return LMHEAD_ERR_SHAPE;
+  if (kv_heads < 1 || kv_heads > 65535 || n < 1 || n > (1 << 30) ||
+      (int64_t)S * n > INT32_MAX)
+    return LMHEAD_ERR_SHAPE;
   if (first && meet(first, 4ll * S, out_new_lens, 4ll * S)) return LMHEAD_ERR_SHAPE;
   KeepArgs a = {};
   for (int i = 0; i < count; ++i) {

@@ -16,11 +16,14 @@
 // Weights are fp32 (w - fl(fl(Z / Q) g) is rounded once each), masses and
 // running sums 64 bits or pairs of fp32 numbers.
 //
-// One cluster of 8 CTAs a request: each takes the same walk, then an eighth of the
-// last node's row of p, from memory to shared memory, where the changed weights
-// replace what was read; the sums meet in distributed shared memory and the CTA that
-// has the draw finds its place. Bound by latency: of dependent reads, one row of
-// candidates a node, then the row of p.
+// One cluster of CTAs a request. Its first CTA takes the walk: the candidates of the
+// node it stands on lie in shared memory, a rejection changes them all and sums up
+// what was taken. Then each CTA takes its share of the last node's row of p, from
+// memory to shared memory, where the changed weights replace what was read; the sums
+// meet in distributed shared memory and the CTA that has the draw finds its place.
+// Bound by latency: of dependent reads, one row of candidates a node, then the row of
+// p. This GPU adds two fp64 numbers a cycle and SM, so they are left to single warps
+// (summed up by every thread they took two thirds of the time).
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_util.cuh"
@@ -30,26 +33,25 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;
+constexpr int kMaxCluster = 8;
 constexpr int kNodes = 64;      // of a request
-constexpr int kMaxRun = 2048;   // entries of p that a warp has in shared memory at a time
+constexpr int kMaxRun = 1024;   // entries of p that a warp has in shared memory at a time
 
-// What is in shared memory: `chunk` entries of p (in their place, while the walk
-// lasts, a table of 2^slot_bits keys and places), then the candidates.
+// What is in shared memory: the candidates, then `chunk` entries of p (in their
+// place, while the walk lasts, a table of 2^slot_bits keys and places).
 struct Layout {
+  int cluster;
   int run, chunk;  // a warp's entries (a multiple of 32), a CTA's
   int slot_bits, cands;
   size_t bytes;
 };
-struct Shared {
-  float* row;
-  int32_t* ids;
-  float *w, *g;
-};
 
-inline Layout layout_of(int64_t n, int K) {
+inline Layout layout_of(int64_t n, int K, int S) {
   Layout l;
-  const int64_t per = (n + kCluster - 1) / kCluster;
+  // no more CTAs than the GPU holds at once, two an SM
+  l.cluster = kMaxCluster;
+  while (l.cluster > 2 && (int64_t)l.cluster * S > 2 * (sm_count() > 0 ? sm_count() : 1)) l.cluster /= 2;
+  const int64_t per = ((n + l.cluster - 1) / l.cluster + 3) / 4 * 4;
   const int64_t run = ((per + kWarps - 1) / kWarps + 31) / 32 * 32;
   l.run = (int)(run < kMaxRun ? run : kMaxRun);
   l.chunk = l.run * kWarps;
@@ -73,11 +75,9 @@ __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-
-__device__ __forceinline__ double warp_sum_f64(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
+// What p points to in CTA 0 of the cluster.
+__device__ __forceinline__ int of_first(const int* p) {
+  return ld_cluster_s32(tc::map_to_rank(tc::smem_addr(p), 0));
 }
 
 // (hi, lo) += x without a rounding of hi + lo but in lo.
@@ -86,26 +86,49 @@ __device__ __forceinline__ void add_exact(float& hi, float& lo, float x) {
   lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
   hi = s;
 }
-
-// The sum over the CTA of v, the same in every thread.
-__device__ __forceinline__ double cta_sum(double v, double* part) {
-  v = warp_sum_f64(v);
-  cta_sync();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  cta_sync();
-  double t = 0;
+// The sum of a warp's pairs, in every lane.
+__device__ __forceinline__ void warp_sum_exact(float& hi, float& lo) {
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) t += part[i];
-  return t;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float h = __shfl_xor_sync(0xFFFFFFFFu, hi, o), l = __shfl_xor_sync(0xFFFFFFFFu, lo, o);
+    add_exact(hi, lo, h);
+    lo = __fadd_rn(lo, l);
+  }
+}
+__device__ __forceinline__ double warp_scan_f64(double v, int lane) {  // up to and with the lane
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double t = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
 }
 
-// Of candidates listed twice the first counts: the others lose their id.
-__device__ void drop_repeats(const Shared& sh, int K, int slot_bits) {
+struct Cands {
+  int32_t* ids;
+  float *w, *g;
+};
+
+struct Walk {
+  int parent[kNodes];
+  int32_t token[kNodes];
+  float r[kNodes], px[kNodes];
+  int hit[kNodes];
+  float2 part[kWarps];
+  float share;
+  int verdict;
+  // where it ended, for all CTAs
+  int cur, count, changed, state;
+  unsigned long long path;
+};
+enum State { kWalked, kIdle, kBad };
+enum Verdict { kNo, kYes, kNoCandidate };
+
+// Of candidates listed twice the first counts: the others lose their id. The table's
+// keys are -1 before and afterwards.
+__device__ void drop_repeats(const Cands& c, int K, int* key, int slot_bits) {
   const int slots = 1 << slot_bits;
-  int* key = reinterpret_cast<int*>(sh.row);
-  int* at = key + slots;
-  for (int i = threadIdx.x; i < slots; i += kThreads) key[i] = -1, at[i] = INT32_MAX;
-  cta_sync();
+  int* at = key + slots;  // INT32_MAX, likewise
   auto slot_of = [&](int32_t id) {  // where id is, or its place
     uint32_t h = ((uint32_t)id * 2654435761u) >> (32 - slot_bits);
     for (int probe = 0; probe < slots; ++probe) {
@@ -115,164 +138,255 @@ __device__ void drop_repeats(const Shared& sh, int K, int slot_bits) {
     }
     return (int)h;
   };
-  for (int j = threadIdx.x; j < K; j += kThreads)
-    if (sh.ids[j] >= 0) atomicMin(&at[slot_of(sh.ids[j])], j);
-  cta_sync();
-  for (int j = threadIdx.x; j < K; j += kThreads)
-    if (sh.ids[j] >= 0 && at[slot_of(sh.ids[j])] != j) {
-      sh.ids[j] = -1;
-      sh.w[j] = sh.g[j] = 0.f;
+  int slot[kSelectMaxK / kThreads];
+#pragma unroll
+  for (int i = 0; i < kSelectMaxK / kThreads; ++i) {
+    const int j = i * kThreads + threadIdx.x;
+    slot[i] = -1;
+    if (j < K && c.ids[j] >= 0) {
+      slot[i] = slot_of(c.ids[j]);
+      atomicMin(&at[slot[i]], j);
     }
+  }
   cta_sync();
+#pragma unroll
+  for (int i = 0; i < kSelectMaxK / kThreads; ++i) {
+    const int j = i * kThreads + threadIdx.x;
+    if (slot[i] >= 0 && at[slot[i]] != j) {
+      c.ids[j] = -1;
+      c.w[j] = c.g[j] = 0.f;
+    }
+  }
+  cta_sync();
+#pragma unroll
+  for (int i = 0; i < kSelectMaxK / kThreads; ++i)
+    if (slot[i] >= 0) key[slot[i]] = -1, at[slot[i]] = INT32_MAX;
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+// The nodes whose parent is c, c < kNodes.
+__device__ __forceinline__ uint64_t children(const Walk& wk, int c, int lane) {
+  const uint32_t lo = __ballot_sync(0xFFFFFFFFu, wk.parent[lane] == c);
+  const uint32_t hi = __ballot_sync(0xFFFFFFFFu, wk.parent[lane + 32] == c);
+  const uint64_t kids = (uint64_t)hi << 32 | lo;
+  return c >= 63 ? 0 : kids >> (c + 1) << (c + 1);  // a parent comes before its children
+}
+
+// The walk over children that are given, by one warp.
+__device__ void walk_given(const TreeArgs& a, Walk& wk, int lane) {
+  int cur = 0, count = 0, state = kWalked;
+  unsigned long long path = 1;
+  bool changed = false;
+  for (bool on = true; on;) {
+    on = false;
+    changed = false;
+    double Z = 1;
+    for (uint64_t kids = children(wk, cur, lane); kids; kids &= kids - 1) {
+      const int x = __ffsll((long long)kids) - 1;
+      const int32_t tok = wk.token[x];
+      if (tok < 0 || tok >= a.n) {
+        state = kBad;
+        break;
+      }
+      // nothing is left of a token that was tried before
+      const bool twin = (lane < x && wk.parent[lane] == cur && wk.token[lane] == tok) ||
+                        (lane + 32 < x && wk.parent[lane + 32] == cur && wk.token[lane + 32] == tok);
+      const double w = __any_sync(0xFFFFFFFFu, twin) ? 0.0 : (double)wk.px[x];
+      if ((double)wk.r[x] * Z < w) {
+        if (count == a.depth) {  // deeper than there is room for
+          state = kBad;
+          break;
+        }
+        ++count;
+        path |= 1ull << x;
+        cur = x;
+        on = true;
+        break;
+      }
+      Z = Z > w ? Z - w : 0;
+      changed = true;
+    }
+    if (state == kBad) break;
+  }
+  if (lane == 0) {
+    wk.cur = cur;
+    wk.count = count;
+    wk.changed = changed;
+    wk.state = state;
+    wk.path = path;
+  }
+}
+
+// The walk over children drawn from their parent's candidates, by a CTA.
+__device__ void walk_drawn(const TreeArgs& a, Walk& wk, const Cands& c, int* table, int slot_bits,
+                           int base) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t n = a.n;
+  for (int i = tid; i < 2 << slot_bits; i += kThreads) table[i] = i < 1 << slot_bits ? -1 : INT32_MAX;
+  int cur = 0, count = 0, state = kWalked;
+  unsigned long long path = 1;
+  bool changed = false;
+  for (;;) {
+    changed = false;
+    const uint64_t all = children(wk, cur, lane);
+    if (!all) break;
+    const int64_t row = (int64_t)(base + cur);
+    for (int j = tid; j < a.K; j += kThreads) {
+      int32_t id = a.cand_ids[row * a.K + j];
+      const float g = weight_of(a.cand_q[row * a.K + j]);
+      if (id < 0 || id >= n) id = -1;
+      c.ids[j] = id;
+      c.g[j] = id < 0 ? 0.f : g;
+      c.w[j] = id < 0 ? 0.f : weight_of(a.p[row * n + id]);
+      for (uint64_t kids = all; kids; kids &= kids - 1) {
+        const int x = __ffsll((long long)kids) - 1;
+        if (wk.token[x] == id && id >= 0) atomicMin(&wk.hit[x], j);
+      }
+    }
+    cta_sync();
+    double Z = 1, Q = 1;  // (of warp 0)
+    int next = -1;
+    for (uint64_t kids = all; kids; kids &= kids - 1) {
+      const int x = __ffsll((long long)kids) - 1;
+      const int hit = wk.hit[x];
+      if (warp == 0) {
+        int v = kNoCandidate;
+        float f = 0.f;
+        if (hit < a.K) {
+          v = (double)wk.r[x] * Z * (double)c.g[hit] < (double)c.w[hit] * Q ? kYes : kNo;
+          if (v == kNo && Q > 0) f = (float)(Z / Q);
+        }
+        if (lane == 0) {
+          wk.verdict = v;
+          wk.share = f;
+        }
+      }
+      cta_sync();
+      const int v = wk.verdict;
+      if (v == kNoCandidate || (v == kYes && count == a.depth)) {
+        state = kBad;
+        break;
+      }
+      if (v == kYes) {
+        next = x;
+        break;
+      }
+      const float f = wk.share;
+      if (!changed) drop_repeats(c, a.K, table, slot_bits);
+      changed = true;
+      float hi = 0.f, lo = 0.f;
+      for (int j = tid; j < a.K; j += kThreads) {
+        const float w = c.w[j], took = fminf(w, __fmul_rn(f, c.g[j]));
+        c.w[j] = __fsub_rn(w, took);
+        add_exact(hi, lo, took);
+      }
+      warp_sum_exact(hi, lo);
+      if (lane == 0) wk.part[warp] = make_float2(hi, lo);
+      cta_sync();
+      if (warp == 0) {
+        const float2 s = lane < kWarps ? wk.part[lane] : make_float2(0.f, 0.f);
+        hi = s.x;
+        lo = s.y;
+        warp_sum_exact(hi, lo);
+        const double took = (double)hi + (double)lo;
+        Z = Z > took ? Z - took : 0;
+        Q -= (double)c.g[hit];
+        __syncwarp();
+        if (lane == 0) c.g[hit] = 0.f;
+        __syncwarp();
+      }
+    }
+    if (next < 0) break;
+    ++count;
+    path |= 1ull << next;
+    cur = next;
+    cta_sync();  // the candidates have been read before the next node's come
+  }
+  if (tid == 0) {
+    wk.cur = cur;
+    wk.count = count;
+    wk.changed = changed;
+    wk.state = state;
+    wk.path = path;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 2)
 verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
   extern __shared__ __align__(16) uint8_t dsmem[];
-  Shared sh;
-  sh.g = reinterpret_cast<float*>(dsmem);
-  sh.w = sh.g + lay.cands;
-  sh.ids = reinterpret_cast<int32_t*>(sh.w + lay.cands);
-  sh.row = reinterpret_cast<float*>(sh.ids + lay.cands);
-  __shared__ int parent[kNodes];
-  __shared__ int32_t token[kNodes];
-  __shared__ float r[kNodes], px[kNodes];
-  __shared__ double part[kWarps], seg[kWarps];
-  __shared__ double cta_total;
-  __shared__ int cta_last, sh_hit, sh_pick;
+  float* row_s = reinterpret_cast<float*>(dsmem);
+  Cands cand;
+  cand.g = reinterpret_cast<float*>(dsmem + lay.bytes) - lay.cands;
+  cand.w = cand.g - lay.cands;
+  cand.ids = reinterpret_cast<int32_t*>(cand.w - lay.cands);
+  __shared__ Walk wk;
+  __shared__ double seg[kWarps], seg_at[kWarps];
+  __shared__ double cta_total, sh_all, sh_off, sh_base;
+  __shared__ int cta_last, sh_pick, sh_last_rank;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = (int)tc::cluster_ctarank();
+  const int rank = (int)tc::cluster_ctarank(), ranks = lay.cluster;
   const int64_t n = a.n;
   pdl_wait();
   pdl_trigger();
   for (int s = blockIdx.y; s < a.S; s += gridDim.y) {
-    cta_sync();  // what follows overwrites the last request's
     int32_t* out_tokens = a.out_tokens + (int64_t)s * (a.depth + 1);
     int32_t* out_path = a.out_path + (int64_t)s * (a.depth + 1);
     const int base = a.cu[s], m = a.cu[s + 1] - base;
-    const bool idle = (a.granted && a.granted[s] == 0) || a.cu[s + 1] == base;
-    const bool sane = base >= 0 && m >= 0 && m <= kNodes && base <= a.T - m;
-    bool bad = !idle && !sane;
-    int count = -1, cur = 0;
-    uint64_t path = 1;  // nodes of the accepted path
-    bool changed = false;
-    if (!idle && !bad) {
-      if (tid < kNodes) {
-        parent[tid] = tid > 0 && tid < m ? a.parent[base + tid] : -1;
-        token[tid] = tid < m ? a.tokens[base + tid] : -1;
-        r[tid] = tid < m ? a.r[base + tid] : 0.f;
-        const bool in = token[tid] >= 0 && token[tid] < n && parent[tid] >= 0 && parent[tid] < tid;
-        px[tid] = in ? weight_of(a.p[(int64_t)(base + parent[tid]) * n + token[tid]]) : 0.f;
-      }
+    if (rank == 0) {
+      const bool idle = (a.granted && a.granted[s] == 0) || a.cu[s + 1] == base;
+      const bool sane = base >= 0 && m >= 0 && m <= kNodes && base <= a.T - m;
       cta_sync();
-      count = 0;
-      double Z = 1, Q = 1;
-      // the children of node c behind node `behind`
-      auto next_child = [&](int c, int behind) -> int {
-        const uint32_t lo = __ballot_sync(0xFFFFFFFFu, parent[lane] == c);
-        const uint32_t hi = __ballot_sync(0xFFFFFFFFu, parent[lane + 32] == c);
-        uint64_t kids = (uint64_t)hi << 32 | lo;
-        kids = behind >= 63 ? 0 : kids >> (behind + 1) << (behind + 1);
-        return kids ? __ffsll((long long)kids) - 1 : -1;
-      };
-      int x = next_child(0, 0);
-      bool fresh = true;  // the candidates of `cur` are not loaded yet
-      while (x >= 0) {
-        const int32_t tok = token[x];
-        if (tok < 0 || tok >= n) {
-          bad = true;
-          break;
-        }
-        bool yes;
-        if (a.cand_ids) {
-          const int64_t row = (int64_t)(base + cur);
-          if (fresh) {
-            for (int j = tid; j < a.K; j += kThreads) {
-              int32_t id = a.cand_ids[row * a.K + j];
-              if (id < 0 || id >= n) id = -1;
-              sh.ids[j] = id;
-              sh.g[j] = id < 0 ? 0.f : weight_of(a.cand_q[row * a.K + j]);
-              sh.w[j] = id < 0 ? 0.f : weight_of(a.p[row * n + id]);
-            }
-            Z = Q = 1;
-            changed = false;
-          }
-          if (tid == 0) sh_hit = a.K;
-          cta_sync();
-          for (int j = tid; j < a.K; j += kThreads)
-            if (sh.ids[j] == tok) atomicMin(&sh_hit, j);
-          cta_sync();
-          const int hit = sh_hit;
-          if (hit == a.K) {  // no candidate of its parent's
-            bad = true;
-            break;
-          }
-          const double gx = sh.g[hit];
-          yes = (double)r[x] * Z * gx < (double)sh.w[hit] * Q;
-          cta_sync();  // seen by all before it changes
-          if (!yes) {
-            if (!changed) drop_repeats(sh, a.K, lay.slot_bits);
-            changed = true;
-            const float f = Q > 0 ? (float)(Z / Q) : 0.f;
-            float hi = 0.f, lo = 0.f;
-            for (int j = tid; j < a.K; j += kThreads) {
-              const float took = fminf(sh.w[j], __fmul_rn(f, sh.g[j]));
-              sh.w[j] = __fsub_rn(sh.w[j], took);
-              add_exact(hi, lo, took);
-            }
-            const double took = cta_sum((double)hi + (double)lo, part);  // (its barriers order the reads of g)
-            Z = Z > took ? Z - took : 0;
-            Q -= gx;
-            if (tid == 0) sh.g[hit] = 0.f;
-          }
-        } else {
-          if (fresh) Z = 1;
-          // nothing is left of a token that was tried before
-          const bool twin0 = lane < x && parent[lane] == cur && token[lane] == tok;
-          const bool twin1 = lane + 32 < x && parent[lane + 32] == cur && token[lane + 32] == tok;
-          const double w = __any_sync(0xFFFFFFFFu, twin0 || twin1) ? 0.0 : (double)px[x];
-          yes = (double)r[x] * Z < w;
-          if (!yes) Z = Z > w ? Z - w : 0;
-          changed = true;
-        }
-        fresh = yes;
-        if (yes) {
-          if (count == a.depth) {  // deeper than there is room for
-            bad = true;
-            break;
-          }
-          ++count;
-          path |= 1ull << x;
-          cur = x;
-          changed = false;
+      if (idle || !sane) {
+        if (tid == 0) wk.state = idle ? kIdle : kBad;
+      } else {
+        if (tid < kNodes) {
+          const bool in = tid < m;
+          const int parent = in && tid > 0 ? a.parent[base + tid] : -1;
+          const int32_t token = in ? a.tokens[base + tid] : -1;
+          wk.parent[tid] = parent;
+          wk.token[tid] = token;
+          wk.r[tid] = in ? a.r[base + tid] : 0.f;
+          wk.hit[tid] = a.K;
+          if (!a.cand_ids)
+            wk.px[tid] = token >= 0 && token < n && parent >= 0 && parent < tid
+                             ? weight_of(a.p[(int64_t)(base + parent) * n + token])
+                             : 0.f;
         }
         cta_sync();
-        x = next_child(cur, x);
+        if (a.cand_ids)
+          walk_drawn(a, wk, cand, reinterpret_cast<int*>(row_s), lay.slot_bits, base);
+        else if (warp == 0)
+          walk_given(a, wk, lane);
       }
-    }
-    if (bad || idle) {
-      if (rank == 0) {
-        if (bad && tid == 0) record_error(err, kDevErrBadId);
+      cta_sync();
+      if (wk.state != kWalked) {
+        if (wk.state == kBad && tid == 0) record_error(err, kDevErrBadId);
         for (int i = tid; i <= a.depth; i += kThreads) out_tokens[i] = out_path[i] = -1;
         if (tid == 0) a.out_accepted[s] = -1;
+      } else {
+        // entry i: the i-th node of the path, the (i + 1)-th node's token
+        for (int i = tid; i <= a.depth; i += kThreads) {
+          unsigned long long rest = wk.path;
+          for (int k = 0; k < i; ++k) rest &= rest - 1;
+          const unsigned long long after = rest & (rest - 1);
+          out_path[i] = i <= wk.count ? __ffsll((long long)rest) - 1 : -1;
+          if (i != wk.count) out_tokens[i] = i < wk.count ? wk.token[__ffsll((long long)after) - 1] : -1;
+        }
+        if (tid == 0) a.out_accepted[s] = wk.count;
       }
-      continue;  // every CTA of the cluster alike
     }
-    if (rank == 0) {
-      // entry i: the i-th node of the path, the (i + 1)-th node's token
-      for (int i = tid; i <= a.depth; i += kThreads) {
-        uint64_t rest = path;
-        for (int k = 0; k < i; ++k) rest &= rest - 1;
-        const uint64_t after = rest & (rest - 1);
-        out_path[i] = i <= count ? __ffsll((long long)rest) - 1 : -1;
-        if (i != count) out_tokens[i] = i < count ? token[__ffsll((long long)after) - 1] : -1;
-      }
-      if (tid == 0) a.out_accepted[s] = count;
+    tc::cluster_sync();
+    const int state = of_first(&wk.state);
+    if (state != kWalked) {
+      tc::cluster_sync();  // read before the first CTA goes on or ends
+      continue;
     }
+    const int cur = of_first(&wk.cur), count = of_first(&wk.count);
+    const bool changed = of_first(&wk.changed) != 0;
     // ---- the token behind the path
     const float* row = a.p + (int64_t)(base + cur) * n;
-    const int64_t per = (n + kCluster - 1) / kCluster;
+    const int64_t per = ((n + ranks - 1) / ranks + 3) / 4 * 4;
     const int64_t v0 = min(n, rank * per), v1 = min(n, v0 + per);
+    const bool quads = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
     const float u = a.u[s];
     for (int pass = 0; pass < 2; ++pass) {
       const bool patch = changed && pass == 0;  // what is left may be nothing: then p itself
@@ -280,119 +394,137 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
       // its run of it; returns the last place with a weight in this thread's part
       auto load = [&](int64_t at, int len) -> int {
         cta_sync();
+        if (quads) {  // (what a chunk begins at is a multiple of four)
+          const float4* src = reinterpret_cast<const float4*>(row + at);
+#pragma unroll 4
+          for (int i = tid; i < len / 4; i += kThreads) {
+            const float4 v = src[i];
+            reinterpret_cast<float4*>(row_s)[i] =
+                make_float4(weight_of(v.x), weight_of(v.y), weight_of(v.z), weight_of(v.w));
+          }
+          for (int i = (len & ~3) + tid; i < len; i += kThreads) row_s[i] = weight_of(row[at + i]);
+        } else {
 #pragma unroll 8
-        for (int i = tid; i < len; i += kThreads) sh.row[i] = weight_of(row[at + i]);
+          for (int i = tid; i < len; i += kThreads) row_s[i] = weight_of(row[at + i]);
+        }
         cta_sync();
         if (patch && a.cand_ids) {
           for (int j = tid; j < a.K; j += kThreads) {
-            const int64_t i = sh.ids[j] - at;
-            if (sh.ids[j] >= 0 && i >= 0 && i < len) sh.row[i] = sh.w[j];
+            const int id = of_first(cand.ids + j);
+            const int64_t i = id - at;
+            if (id >= 0 && i >= 0 && i < len)
+              row_s[i] = __int_as_float(of_first(reinterpret_cast<const int*>(cand.w) + j));
           }
-        } else if (patch && tid < kNodes && parent[tid] == cur) {
-          const int64_t i = token[tid] - at;
-          if (i >= 0 && i < len) sh.row[i] = 0.f;
+        } else if (patch && tid < kNodes && tid > cur && of_first(&wk.parent[tid]) == cur) {
+          const int64_t i = of_first(&wk.token[tid]) - at;
+          if (i >= 0 && i < len) row_s[i] = 0.f;
         }
         cta_sync();
         float hi = 0.f, lo = 0.f;
         int last = -1;
+#pragma unroll 4
         for (int i = warp * lay.run + lane; i < min(len, (warp + 1) * lay.run); i += 32) {
-          const float w = sh.row[i];
+          const float w = row_s[i];
           add_exact(hi, lo, w);
           if (w > 0.f) last = i;
         }
-        const double sum = warp_sum_f64((double)hi + (double)lo);
-        if (lane == 0) seg[warp] = sum;
+        warp_sum_exact(hi, lo);
+        if (lane == 0) seg[warp] = (double)hi + (double)lo;
+        cta_sync();
+        if (warp == 0) {
+          // where each warp's run begins in the running sum
+          const double mine = lane < kWarps ? seg[lane] : 0.0;
+          const double to = warp_scan_f64(mine, lane), from = sh_base;
+          if (lane < kWarps) seg_at[lane] = from + (to - mine);
+          __syncwarp();
+          if (lane == kWarps - 1) sh_base = from + to;
+        }
         cta_sync();
         return last;
       };
-      double total = 0;
-      int64_t last = -1;
+      if (tid == 0) cta_last = -1, sh_pick = -1, sh_base = 0;
+      int last = -1;
       for (int64_t at = v0; at < v1; at += lay.chunk) {
         const int l = load(at, (int)min((int64_t)lay.chunk, v1 - at));
-        if (l >= 0) last = at + l;
-        for (int w = 0; w < kWarps; ++w) total += seg[w];
+        if (l >= 0) last = (int)(at + l);
       }
-      last = __reduce_max_sync(0xFFFFFFFFu, (int)last);
-      if (tid == 0) cta_last = -1, cta_total = total, sh_pick = -1;
       cta_sync();
-      if (lane == 0) atomicMax(&cta_last, (int)last);
+      last = __reduce_max_sync(0xFFFFFFFFu, last);
+      if (lane == 0) atomicMax(&cta_last, last);
+      if (tid == 0) cta_total = sh_base;
       cta_sync();
       tc::cluster_sync();
-      double all = 0, off = 0;
-      int last_rank = -1;
-      for (int q = 0; q < kCluster; ++q) {
-        const double t = ld_cluster_f64(tc::map_to_rank(tc::smem_addr(&cta_total), (uint32_t)q));
-        if (ld_cluster_s32(tc::map_to_rank(tc::smem_addr(&cta_last), (uint32_t)q)) >= 0) last_rank = q;
-        if (q == rank) off = all;
-        all += t;
-      }
-      tc::cluster_sync();  // read before any CTA goes on or ends
-      if (!(all > 0)) {
-        if (pass == 1 && rank == kCluster - 1 && tid == 0) out_tokens[count] = (int32_t)(n - 1);
-        continue;
-      }
-      const double target = (double)u * all;
-      const bool past = !(target < all);  // u * total rounded up to the total
-      const double end = rank + 1 < kCluster ? off + total : all;
-      if (past ? rank == last_rank : off <= target && target < end) {
-        if (!past) {
-          double before = off;
-          for (int64_t at = v0; at < v1; at += lay.chunk) {
-            const int len = (int)min((int64_t)lay.chunk, v1 - at);
-            if (v1 - v0 > lay.chunk) load(at, len);  // a single chunk is still there
-            double mine = before;
-            for (int w = 0; w < kWarps; ++w) {
-              if (w == warp) mine = before;
-              before += seg[w];
-            }
-            if (mine <= target && target < mine + seg[warp]) {
-              // a lane sums neighbours (each lane beginning elsewhere, for the banks), and
-              // those of the lane that passes the target are looked at 32 at a time
-              const int many = lay.run / 32, first = warp * lay.run + lane * many;
-              float hi = 0.f, lo = 0.f;
-              for (int i = 0, e = lane % many; i < many; ++i, e = e + 1 == many ? 0 : e + 1)
-                if (first + e < len) add_exact(hi, lo, sh.row[first + e]);
-              const double own = (double)hi + (double)lo;
-              double run = own;
-#pragma unroll
-              for (int o = 1; o < 32; o <<= 1) {
-                const double t = __shfl_up_sync(0xFFFFFFFFu, run, o);
-                if (lane >= o) run += t;
-              }
-              const uint32_t over = __ballot_sync(0xFFFFFFFFu, own > 0 && mine + run > target);
-              if (over) {
-                const int k = __ffs(over) - 1, from = warp * lay.run + k * many;
-                double under = mine + __shfl_sync(0xFFFFFFFFu, run - own, k);
-                int pick = -1;
-                for (int i = 0; i < many; i += 32) {
-                  const int e = from + i + lane;
-                  const float w = i + lane < many && e < len ? sh.row[e] : 0.f;
-                  double sum = w;
-#pragma unroll
-                  for (int o = 1; o < 32; o <<= 1) {
-                    const double t = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-                    if (lane >= o) sum += t;
-                  }
-                  const uint32_t some = __ballot_sync(0xFFFFFFFFu, w > 0.f);
-                  const uint32_t hit = __ballot_sync(0xFFFFFFFFu, w > 0.f && under + sum > target);
-                  if (some) pick = from + i + 31 - __clz(some);  // where none passes: the last
-                  if (hit) {
-                    pick = from + i + __ffs(hit) - 1;
-                    break;
-                  }
-                  under += __shfl_sync(0xFFFFFFFFu, sum, 31);
-                }
-                if (lane == 0) atomicMax(&sh_pick, (int)(at + pick));
-              }
-            }
-            cta_sync();
-            if (sh_pick >= 0) break;
-          }
+      if (warp == 0) {
+        double t = 0;
+        int l = -1;
+        if (lane < ranks) {
+          t = ld_cluster_f64(tc::map_to_rank(tc::smem_addr(&cta_total), (uint32_t)lane));
+          l = ld_cluster_s32(tc::map_to_rank(tc::smem_addr(&cta_last), (uint32_t)lane));
         }
-        // rounding kept the target from being passed: the last that has a weight
-        if (tid == 0) out_tokens[count] = sh_pick >= 0 ? sh_pick : cta_last;
+        const double to = warp_scan_f64(t, lane);
+        const uint32_t some = __ballot_sync(0xFFFFFFFFu, l >= 0);
+        if (lane == rank) sh_off = to - t;
+        if (lane == 31) {
+          sh_all = to;
+          sh_last_rank = 31 - __clz(some);
+        }
       }
-      break;
+      cta_sync();
+      const double all = sh_all, off = sh_off;
+      const bool none = !(all > 0);
+      if (!none) {
+        const double target = (double)u * all;
+        const bool past = !(target < all);  // u * total rounded up to the total
+        const double end = rank + 1 < ranks ? off + cta_total : all;
+        if (past ? rank == sh_last_rank : off <= target && target < end) {
+          if (!past) {
+            cta_sync();
+            if (tid == 0) sh_base = 0;
+            for (int64_t at = v0; at < v1; at += lay.chunk) {
+              const int len = (int)min((int64_t)lay.chunk, v1 - at);
+              if (v1 - v0 > lay.chunk) load(at, len);  // a single chunk is still there
+              const double mine = off + seg_at[warp];
+              if (mine <= target && target < mine + seg[warp]) {
+                // a lane sums neighbours (each lane beginning elsewhere, for the banks), and
+                // those of the lane that passes the target are looked at 32 at a time
+                const int many = lay.run / 32, first = warp * lay.run + lane * many;
+                float hi = 0.f, lo = 0.f;
+                for (int i = 0, e = lane % many; i < many; ++i, e = e + 1 == many ? 0 : e + 1)
+                  if (first + e < len) add_exact(hi, lo, row_s[first + e]);
+                const double own = (double)hi + (double)lo, run = warp_scan_f64(own, lane);
+                const uint32_t over = __ballot_sync(0xFFFFFFFFu, own > 0 && mine + run > target);
+                if (over) {
+                  const int k = __ffs(over) - 1, from = warp * lay.run + k * many;
+                  double under = mine + __shfl_sync(0xFFFFFFFFu, run - own, k);
+                  int pick = -1;
+                  for (int i = 0; i < many; i += 32) {
+                    const int e = from + i + lane;
+                    const float w = i + lane < many && e < len ? row_s[e] : 0.f;
+                    const double sum = warp_scan_f64(w, lane);
+                    const uint32_t some = __ballot_sync(0xFFFFFFFFu, w > 0.f);
+                    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, w > 0.f && under + sum > target);
+                    if (some) pick = from + i + 31 - __clz(some);  // where none passes: the last
+                    if (hit) {
+                      pick = from + i + __ffs(hit) - 1;
+                      break;
+                    }
+                    under += __shfl_sync(0xFFFFFFFFu, sum, 31);
+                  }
+                  if (lane == 0) atomicMax(&sh_pick, (int)(at + pick));
+                }
+              }
+              cta_sync();
+              if (sh_pick >= 0) break;
+            }
+          }
+          // rounding kept the target from being passed: the last that has a weight
+          if (tid == 0) out_tokens[count] = sh_pick >= 0 ? sh_pick : cta_last;
+        }
+      } else if (pass == 1 && rank == ranks - 1 && tid == 0) {
+        out_tokens[count] = (int32_t)(n - 1);
+      }
+      tc::cluster_sync();  // what the others read is kept until all are done
+      if (!none) break;
     }
   }
 }
@@ -400,12 +532,24 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
 }  // namespace
 
 cudaError_t launch_verify_tree(const TreeArgs& a, int* err, cudaStream_t s) {
-  const Layout lay = layout_of(a.n, a.cand_ids ? a.K : 0);
+  const Layout lay = layout_of(a.n, a.cand_ids ? a.K : 0, a.S);
   static int smem_set[64] = {0};
   const cudaError_t e = ensure_dynamic_smem(verify_tree_kernel, lay.bytes, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_kernel(true, verify_tree_kernel, dim3(kCluster, a.S < 65535 ? a.S : 65535),
-                       dim3(kThreads), lay.bytes, s, a, lay, err);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(lay.cluster, a.S < 65535 ? a.S : 65535);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = lay.bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = lay.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, verify_tree_kernel, a, lay, err);
 }
 
 }  // namespace lmhead
