@@ -8,15 +8,17 @@
 // The products run on the tensor cores with the keys as their rows: 128 keys times
 // a tile of up to 128 rows of queries (tokens x the G heads that share the K/V
 // head), so a thread has a key and its sum runs along the tensor memory's columns,
-// with no exchange between threads and no maximum to find. The keys of a pair of
-// such tiles are loaded once and stay in shared memory while the request's query
-// tiles pass by; a decoding step has one query tile, and its keys stream.
+// with no exchange between threads and no maximum to find. Four such tiles of keys
+// make a unit: they are loaded once and stay in shared memory while the request's
+// query tiles pass by; a decoding step has one query tile, and its keys stream.
 // One CTA an SM, warp-specialised: a warp loads keys (TMA, page by page), one loads
-// queries and their lse, one issues the MMAs, and two warpgroups (a key tile each)
-// exponentiate and sum. The CTAs share out pairs x query tiles evenly, in the order
-// (K/V head, request, pair). Where requests bring many tiles a pair may be cut
-// between CTAs; each leaves its sums in the scratch and a second launch adds them up
-// in order, so no result depends on which CTA came first.
+// queries and their lse, one issues the MMAs, and four warpgroups (a key tile each,
+// with a quarter of the tensor memory) exponentiate and sum; while one waits for its
+// next product the others use the exponential units. The CTAs share out key tiles x
+// query tiles evenly, in the order (K/V head, request, unit). Where requests bring
+// many query tiles a unit may be cut between CTAs; each leaves its sums in the
+// scratch and a second launch adds them up in order, so no result depends on which
+// CTA came first.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -28,43 +30,45 @@ namespace lmhead {
 namespace {
 
 constexpr int kKeys = 128;         // keys of a tile
-constexpr int kPair = 2 * kKeys;   // of a unit
+constexpr int kGroups = 4;         // tiles of a unit, a warpgroup each
+constexpr int kUnit = kGroups * kKeys;
 constexpr int kRows = 128;         // query rows of a tile
-constexpr int kThreads = 384;      // two warpgroups that sum, four warps of which three work
-constexpr int kRegsMore = 184, kRegsLess = 136;  // of 168 a thread at launch
+// Four warpgroups that sum, four warps of which three work; of the 96 registers a
+// thread at launch the former get 104 and the latter 64.
+constexpr int kThreads = 640;
+constexpr int kRegsMore = 104, kRegsLess = 64;
+constexpr int kWarpK = 16, kWarpMma = 17, kWarpQ = 18;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_huge_valf();
 
 template <int D> struct Shape {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kKeys * D * 2;           // a key tile
-  static constexpr int kPairBytes = 2 * kTile;
-  static constexpr int kPairs = D == 128 ? 2 : 4;       // pairs in shared memory
+  static constexpr int kTiles = D == 128 ? 4 : 8;       // of them in shared memory
   static constexpr int kQ = kRows * D * 2;              // a query tile
-  static constexpr int kTiles = D == 128 ? 3 : 5;       // of them
-  static constexpr int kSmem = kPairs * kPairBytes + kTiles * kQ + 1024;
+  static constexpr int kQTiles = D == 128 ? 3 : 5;
+  static constexpr int kSmem = kTiles * kTile + kQTiles * kQ + 1024;
 };
 
-template <int NP, int NQ> struct Ctl {
-  uint64_t k_full[NP], k_empty[NP], q_full[NQ], q_empty[NQ];
-  uint64_t s_full[2][2], s_empty[2][2];
+template <int NK, int NQ> struct Ctl {
+  uint64_t k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ];
+  uint64_t s_full[kGroups], s_empty[kGroups];
   uint64_t drain;
   uint32_t tmem;
   int abort;
   float lse[NQ][kRows];  // in base 2; +inf where there is no row
-  // the plan
-  long long per_head;    // cost of one K/V head's units
-  long long lo, hi;      // the CTA's share of all
+  // the plan: the CTA's share of all cost, and the unit in which it begins
+  long long lo, hi;
   int bad, s0, p0, off0, hk0;
 };
 
 // What a request has to do for one K/V head.
 struct Req {
   int tok0, m, len;
-  int np, qt;  // pairs of key tiles, query tiles
+  int np, qt;  // units, query tiles
 };
 
-// The query tiles [t0, t0 + n) that see any key of pair p.
+// The query tiles [t0, t0 + n) that see any key of unit p.
 struct Span {
   int t0, n;
 };
@@ -76,13 +80,14 @@ __device__ __forceinline__ Req request_of(const WeightArgs& a, int s, int tile_t
   r.len = a.lens[s];
   sane = true;
   r.np = r.qt = 0;
-  if (a.granted && a.granted[s] == 0) return r;
-  if (r.len < 0 || r.len > (a.width << a.page_shift) - r.m) {
-    sane = false;
+  const bool refused = a.granted && a.granted[s] == 0;
+  if (refused || r.len < 0 || r.len > (a.width << a.page_shift) - r.m) {
+    sane = refused;
+    r.len = 0;  // (whatever it was, no arithmetic is done on it)
     return r;
   }
   if (r.m == 0 && a.decay == 1.f) return r;  // nothing changes
-  r.np = (r.len + r.m + kPair - 1) / kPair;
+  r.np = (r.len + r.m + kUnit - 1) / kUnit;
   r.qt = (r.m + tile_tok - 1) / tile_tok;
   return r;
 }
@@ -90,11 +95,11 @@ __device__ __forceinline__ Req request_of(const WeightArgs& a, int s, int tile_t
 __device__ __forceinline__ Span span_of(const WeightArgs& a, const Req& r, int p, int tile_tok) {
   Span x = {0, r.qt};
   if (!a.tree) {
-    const int first = p * kPair - r.len;  // the first token that sees the pair's first key
+    const int first = p * kUnit - r.len;  // the first token that sees the unit's first key
     if (first > 0) x.t0 = min(r.qt, first / tile_tok);
     if (a.window > 0) {
       // the last key is out of sight from here on (64 bits: the window may be any)
-      const long long past = (long long)first + kPair - 1 + a.window;
+      const long long past = (long long)first + kUnit - 1 + a.window;
       x.n = past <= 0 ? 0 : (int)min((long long)r.qt, (past + tile_tok - 1) / tile_tok);
     }
     x.n = max(0, x.n - x.t0);
@@ -102,17 +107,27 @@ __device__ __forceinline__ Span span_of(const WeightArgs& a, const Req& r, int p
   return x;
 }
 
-// Cost of a unit: its query tiles, and 1 for the keys.
-__device__ __forceinline__ int cost_of(const WeightArgs& a, const Req& r, int p, int tile_tok) {
-  return 1 + span_of(a, r, p, tile_tok).n;
+// A unit's key tiles. They cost 1 each, and 1 for each query tile: the unit's step x
+// (query tile) ends at cost tiles (x + 2), and what is cut at cost c falls to step
+// step_at(c).
+__device__ __forceinline__ int tiles_of(const Req& r, int p) {
+  return min(kGroups, (r.len + r.m - p * kUnit + kKeys - 1) / kKeys);
 }
-// Pairs that every query tile sees.
-__device__ __forceinline__ int full_pairs(const WeightArgs& a, const Req& r) {
-  return a.window > 0 ? 0 : a.tree ? r.np : min(r.np, r.len / kPair + 1);
+__device__ __forceinline__ int step_at(int cost, int tiles) {
+  return max(0, (cost + tiles - 1) / tiles - 1);
+}
+__device__ __forceinline__ int cost_of(const WeightArgs& a, const Req& r, int p, int tile_tok) {
+  return tiles_of(r, p) * (1 + span_of(a, r, p, tile_tok).n);
+}
+// Units of four tiles that every query tile sees.
+__device__ __forceinline__ int full_units(const WeightArgs& a, const Req& r) {
+  if (a.window > 0) return 0;
+  const int all = (r.len + r.m) / kUnit;  // of four tiles
+  return min(r.np, a.tree ? all : min(all, r.len / kUnit + 1));
 }
 __device__ __forceinline__ long long cost_of(const WeightArgs& a, const Req& r, int tile_tok) {
-  const int full = full_pairs(a, r);
-  long long c = (long long)full * (1 + r.qt);
+  const int full = full_units(a, r);
+  long long c = (long long)full * (kGroups * (1 + r.qt));
   for (int p = full; p < r.np; ++p) c += cost_of(a, r, p, tile_tok);
   return c;
 }
@@ -158,9 +173,9 @@ __device__ void make_plan(const WeightArgs& a, C& ctl, int tile_tok, int* err) {
       }
       if (pass == 1 && before <= target && target < before + c) {
         long long rem = target - before;
-        const int full = full_pairs(a, r);
-        int p = (int)min((long long)full, rem / (1 + r.qt));
-        rem -= (long long)p * (1 + r.qt);
+        const int each = kGroups * (1 + r.qt);
+        int p = (int)min((long long)full_units(a, r), rem / each);
+        rem -= (long long)p * each;
         for (; p < r.np; ++p) {
           const int w = cost_of(a, r, p, tile_tok);
           if (rem < w) break;
@@ -182,7 +197,6 @@ __device__ void make_plan(const WeightArgs& a, C& ctl, int tile_tok, int* err) {
         hi = all / parts * (c + 1) + all % parts * (c + 1) / parts;
       }
       if (tid == 0) {
-        ctl.per_head = base;
         ctl.lo = lo;
         ctl.hi = hi;
         ctl.hk0 = base > 0 ? (int)(lo / base) : 0;
@@ -201,8 +215,8 @@ struct Cursor {
   bool whole_only;
   long long left;
   Req r;
-  // the unit: its place, its query tiles [a, b) of n from t0 on
-  int u_s, u_p, u_hk, t0, n, a, b, kend;
+  // the unit: its place, its key tiles, its query tiles [a, b) of n from t0 on
+  int u_s, u_p, u_hk, tiles, t0, n, a, b, kend;
 
   template <typename C> __device__ void init(const WeightArgs& w, const C& ctl, int tok, bool whole) {
     tile_tok = tok;
@@ -225,43 +239,43 @@ struct Cursor {
         r = request_of(w, s, tile_tok, sane);
       }
       const Span x = span_of(w, r, p, tile_tok);
-      const int cost = 1 + x.n;
+      tiles = tiles_of(r, p);
+      const int cost = tiles * (1 + x.n);
       u_s = s;
       u_p = p++;
       u_hk = hk;
       t0 = x.t0;
       n = x.n;
       kend = r.len + r.m;
+      const int from = off, to = (int)min((long long)cost, off + left);
+      off = 0;
       if (whole_only) {
         // a unit is the CTA's in whose share it begins
-        left -= cost - off;
-        const bool mine = off == 0;
-        off = 0;
+        left -= cost - from;
         a = 0;
         b = n;
-        if (mine) return true;
+        if (from == 0) return true;
         continue;
       }
-      const int end = (int)min((long long)cost, off + left);
-      a = max(off - 1, 0);
-      b = max(end - 1, 0);
-      left -= end - off;
-      off = 0;
-      if (b > a || n == 0) return true;
+      left -= to - from;
+      a = step_at(from, tiles);
+      b = step_at(to, tiles);
+      if (b > a || (n == 0 && from == 0)) return true;
     }
     return false;
   }
 };
 
-// Pieces of cut pairs: of CTA c one that began earlier (place 2 c) and one that
+// Pieces of cut units: of CTA c one that began earlier (place 2 c) and one that
 // begins there and goes on (2 c + 1), with the latter's unit.
 struct Piece {
   int s, p, hk, flags;
 };
-constexpr int kBegins = 1, kGoesOn = 2;  // place 2 c + 1 is one; that in place 2 c does not end here
+constexpr int kBegins = 1;  // there is a piece in place 2 c + 1
+constexpr int kHas = 2, kEnds = 4;  // there is one in place 2 c; the unit ends with it
 struct Scratch {
   Piece* piece;
-  float* sums;  // 256 a place
+  float* sums;  // kUnit a place
 };
 
 __device__ __forceinline__ float* weight_at(const WeightArgs& a, int32_t id, int j, int hk) {
@@ -269,8 +283,9 @@ __device__ __forceinline__ float* weight_at(const WeightArgs& a, int32_t id, int
                                   (j & ((1 << a.page_shift) - 1)) * a.ws.token + hk * a.ws.head);
 }
 
-static_assert(Shape<128>::kSmem + sizeof(Ctl<2, 3>) + 128 <= 227 * 1024, "shared memory");
-static_assert(Shape<64>::kSmem + sizeof(Ctl<4, 5>) + 128 <= 227 * 1024, "shared memory");
+constexpr int kPlanBytes = kThreads / 32 * 8;  // make_plan's own
+static_assert(Shape<128>::kSmem + sizeof(Ctl<4, 3>) + kPlanBytes <= 227 * 1024, "shared memory");
+static_assert(Shape<64>::kSmem + sizeof(Ctl<8, 5>) + kPlanBytes <= 227 * 1024, "shared memory");
 
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -278,38 +293,37 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                const WeightArgs a, const Scratch sc, int k_head_first, int q_by_tma, int whole_only,
                long long budget, int* err) {
   using Sh = Shape<D>;
-  constexpr int NP = Sh::kPairs, NQ = Sh::kTiles;
+  constexpr int NK = Sh::kTiles, NQ = Sh::kQTiles;
   extern __shared__ uint8_t dsmem_raw[];
-  __shared__ Ctl<NP, NQ> ctl;
+  __shared__ Ctl<NK, NQ> ctl;
   uint8_t* k_s = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* q_s = k_s + NP * Sh::kPairBytes;
+  uint8_t* q_s = k_s + NK * Sh::kTile;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* abort_flag = &ctl.abort;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NP; ++i) {
+    for (int i = 0; i < NK; ++i) {
       tc::mbar_init(&ctl.k_full[i], 1);
       tc::mbar_init(&ctl.k_empty[i], 1);
     }
     for (int i = 0; i < NQ; ++i) {
-      tc::mbar_init(&ctl.q_full[i], 33);      // the warp's lanes, and one for a copy's bytes
-      tc::mbar_init(&ctl.q_empty[i], 1 + 2 * kKeys);  // the MMAs, and the readers of lse
+      tc::mbar_init(&ctl.q_full[i], 33);               // the warp's lanes, and one for a copy's bytes
+      tc::mbar_init(&ctl.q_empty[i], 1 + 4 * kGroups);  // the MMAs, and a warp each of the readers of lse
     }
-    for (int w = 0; w < 2; ++w)
-      for (int i = 0; i < 2; ++i) {
-        tc::mbar_init(&ctl.s_full[w][i], 1);
-        tc::mbar_init(&ctl.s_empty[w][i], kKeys);
-      }
+    for (int w = 0; w < kGroups; ++w) {
+      tc::mbar_init(&ctl.s_full[w], 1);
+      tc::mbar_init(&ctl.s_empty[w], 4);
+    }
     tc::mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kWarpMma) {
     tc::tmem_alloc(&ctl.tmem, 512);
     tc::tmem_relinquish();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kWarpK && lane == 0) {
     tc::prefetch_tmap(&kmap);
     tc::prefetch_tmap(&qmap);
   }
@@ -323,54 +337,56 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   tc::fence_before_sync();
   cta_sync();
   tc::fence_after_sync();
-  constexpr uint32_t tmem = 0;  // all 512 columns: 128 a key tile and buffer
+  constexpr uint32_t tmem = 0;  // all 512 columns: 128 a key tile
   pdl_wait();
   pdl_trigger();
   make_plan(a, ctl, tile_tok, err);
   Cursor cur;
   cur.init(a, ctl, tile_tok, whole_only != 0);
-  if (warp >= 8) {
+  if (warp >= kWarpK) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLess));
-    if (warp == 8) {
+    if (warp == kWarpK) {
       // ------------------------------------------------------------ keys by TMA
       // the cache was written by the launch before through the other proxy
       asm volatile("fence.proxy.async;" ::: "memory");
-      const int unit_tok = min(kKeys, 1 << a.page_shift), units = kPair / unit_tok;
+      const int run_tok = min(kKeys, 1 << a.page_shift), runs = kKeys / run_tok;  // of a tile
+      const int run = lane / Sh::kHalves, half = lane % Sh::kHalves;
       uint32_t n = 0;
       bool ok = true;
       while (ok && cur.next(a)) {
-        const int slot = (int)(n % NP);
-        if (cur.b == cur.a) continue;  // no row sees the pair
-        if (n >= (uint32_t)NP) {
-          ok = tc::wait_all<false>(&ctl.k_empty[slot], ((n / NP) & 1) ^ 1, abort_flag, budget);
-          if (!ok) break;
-        }
-        const int32_t* row = a.table + (int64_t)cur.u_s * a.width;
-        // a lane loads one run of keys, or half its dimensions (32 of them at most)
-        const int u = lane / Sh::kHalves, half = lane % Sh::kHalves;
-        const int key = cur.u_p * kPair + u * unit_tok;
-        bool want = u < units && key < cur.kend;
-        int32_t id = 0;
-        if (want) {
-          id = row[key >> a.page_shift];
-          if (id < 0 || id >= a.pages) {
-            want = false;
-            record_error(err, kDevErrBadId);
+        if (cur.b == cur.a) continue;  // no row sees the unit
+        // a lane looks up the page of one run of the unit's keys (32 of them at most)
+        int32_t id = -1;
+        {
+          const int key = cur.u_p * kUnit + lane * run_tok;
+          if (lane < kGroups * runs && key < cur.kend) {
+            id = a.table[(int64_t)cur.u_s * a.width + (key >> a.page_shift)];
+            if (id < 0 || id >= a.pages) {
+              id = -1;
+              record_error(err, kDevErrBadId);
+            }
           }
         }
-        const uint32_t load = __ballot_sync(0xFFFFFFFFu, want);
-        if (lane == 0)
-          tc::mbar_arrive_expect_tx(&ctl.k_full[slot], (uint32_t)(__popc(load) * unit_tok * 128));
-        __syncwarp();
-        if (want) {
-          const int at = u * unit_tok;  // key of the pair
-          uint8_t* dst = k_s + slot * Sh::kPairBytes + at / kKeys * Sh::kTile + half * (kKeys * 128) +
-                         at % kKeys * 128;
-          const int off = key & ((1 << a.page_shift) - 1);
-          tc::tma_load_4d(dst, &kmap, &ctl.k_full[slot], half * 64, k_head_first ? cur.u_hk : off,
-                          k_head_first ? off : cur.u_hk, id);
+        for (int t = 0; t < cur.tiles; ++t, ++n) {
+          const int slot = (int)(n % NK);
+          if (n >= (uint32_t)NK) {
+            ok = tc::wait_all<false>(&ctl.k_empty[slot], ((n / NK) & 1) ^ 1, abort_flag, budget);
+            if (!ok) break;
+          }
+          // and loads one of the tile, or half its dimensions
+          const int32_t page = __shfl_sync(0xFFFFFFFFu, id, (t * runs + run) & 31);
+          const bool want = run < runs && page >= 0;
+          const uint32_t load = __ballot_sync(0xFFFFFFFFu, want);
+          if (lane == 0)
+            tc::mbar_arrive_expect_tx(&ctl.k_full[slot], (uint32_t)(__popc(load) * run_tok * 128));
+          __syncwarp();
+          if (want) {
+            const int off = (cur.u_p * kUnit + t * kKeys + run * run_tok) & ((1 << a.page_shift) - 1);
+            tc::tma_load_4d(k_s + slot * Sh::kTile + half * (kKeys * 128) + run * run_tok * 128, &kmap,
+                            &ctl.k_full[slot], half * 64, k_head_first ? cur.u_hk : off,
+                            k_head_first ? off : cur.u_hk, page);
+          }
         }
-        ++n;
       }
       if (!ok && lane == 0) {
         *abort_flag = 1;
@@ -379,15 +395,15 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       __syncwarp();
       if (lane == 0) {
         // no copy may be under way when the CTA ends, whichever role gave up
-        const uint32_t first = n > (uint32_t)NP ? n - NP : 0;
+        const uint32_t first = n > (uint32_t)NK ? n - NK : 0;
         for (uint32_t j = first; j < n; ++j) {
           const long long t = clock64();
-          while (!tc::mbar_try_wait(&ctl.k_full[j % NP], (j / NP) & 1) &&
+          while (!tc::mbar_try_wait(&ctl.k_full[j % NK], (j / NK) & 1) &&
                  clock64() - t < tc::kWaitCycles) {
           }
         }
       }
-    } else if (warp == 10) {
+    } else if (warp == kWarpQ) {
       // ------------------------------------------------------------ queries and lse
       asm volatile("fence.proxy.async;" ::: "memory");
       uint32_t n = 0;
@@ -427,16 +443,16 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                            : "memory");
             }
           }
+          float l[kRows / 32];
 #pragma unroll
           for (int i = 0; i < kRows / 32; ++i) {
             const int row = i * 32 + lane, tk = row / group;
-            float l = kInf;
-            if (tk < toks) {
-              l = a.lse[(int64_t)(tok + tk) * a.heads + cur.u_hk * group + row - tk * group];
-              l = l == -kInf ? kInf : l * kLog2e;  // a row that sees nothing draws nothing
-            }
-            ctl.lse[slot][row] = l;
+            l[i] = -kInf;
+            if (tk < toks) l[i] = a.lse[(int64_t)(tok + tk) * a.heads + cur.u_hk * group + row - tk * group];
           }
+#pragma unroll
+          for (int i = 0; i < kRows / 32; ++i)  // a row that sees nothing draws nothing
+            ctl.lse[slot][i * 32 + lane] = l[i] == -kInf ? kInf : l[i] * kLog2e;
           if (!tma) {
             asm volatile("cp.async.wait_all;" ::: "memory");
             tc::fence_async_smem();
@@ -458,12 +474,14 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
           }
         }
       }
-    } else if (warp == 9) {
+    } else if (warp == kWarpMma) {
       // ------------------------------------------------------------ MMAs
       const bool issuer = tc::elect_one();
       const uint64_t k_desc = tc::sw128_kmajor_desc(tc::smem_addr(k_s));
       const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_addr(q_s));
-      uint32_t pairs = 0, step = 0, step1 = 0;  // step1: of the second tile
+      uint32_t keys = 0, step = 0;
+      uint32_t uses = 0;  // a bit a tile: whether it was used an odd number of times
+      uint32_t met = 0;   // and whether it was used at all
       bool ok = true;
       while (ok) {
         // what branches and operands depend on comes by shuffle from lane 0, so that
@@ -472,46 +490,46 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         const int steps = __shfl_sync(0xFFFFFFFFu, found ? cur.b - cur.a : -1, 0);
         if (steps < 0) break;
         if (steps == 0) continue;
-        const bool both = __shfl_sync(0xFFFFFFFFu, (int)(cur.u_p * kPair + kKeys < cur.kend), 0) != 0;
+        const int tiles = __shfl_sync(0xFFFFFFFFu, cur.tiles, 0);
         const int first = __shfl_sync(0xFFFFFFFFu, (cur.r.m - (cur.t0 + cur.a) * tile_tok), 0);
-        const int k_slot = (int)(pairs % NP);
-        ok = tc::wait_all<true>(&ctl.k_full[k_slot], (pairs / NP) & 1, abort_flag, budget);
-        if (!ok) break;
 #pragma unroll 1
-        for (int t = 0; t < steps; ++t, ++step) {
+        for (int t = 0; t < steps && ok; ++t, ++step) {
           const int q_slot = (int)(step % NQ);
           const int rows = min(tile_tok, first - t * tile_tok) * group;
           const uint32_t idesc = tc::idesc_f16_f32(BF16, kKeys, (uint32_t)((rows + 15) & ~15), false);
           ok = tc::wait_all<true>(&ctl.q_full[q_slot], (step / NQ) & 1, abort_flag, budget);
           if (!ok) break;
           const uint64_t qd = q_desc + q_slot * (Sh::kQ / 16);
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (w == 1 && !both) break;
-            const uint32_t use = w ? step1 : step;
-            const int buf = (int)(use & 1);
-            if (use >= 2) {
-              ok = tc::wait_all<true>(&ctl.s_empty[w][buf], ((use >> 1) & 1) ^ 1, abort_flag, budget);
+#pragma unroll 1
+          for (int w = 0; w < tiles; ++w) {
+            const uint32_t nk = keys + w;
+            const int k_slot = (int)(nk % NK);
+            if (t == 0) {
+              ok = tc::wait_all<true>(&ctl.k_full[k_slot], (nk / NK) & 1, abort_flag, budget);
               if (!ok) break;
             }
+            if (met >> w & 1) {
+              ok = tc::wait_all<true>(&ctl.s_empty[w], (uses >> w & 1) ^ 1, abort_flag, budget);
+              if (!ok) break;
+            }
+            met |= 1u << w;
+            uses ^= 1u << w;
             tc::fence_after_sync();
-            const uint64_t kd = k_desc + k_slot * (Sh::kPairBytes / 16) + w * (Sh::kTile / 16);
+            const uint64_t kd = k_desc + k_slot * (Sh::kTile / 16);
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               constexpr int kHalf = kKeys * 128 / 16;
-              tc::mma_ss_one(issuer, tmem + (w * 2 + buf) * 128, kd + (c / 4) * kHalf + (c % 4) * 2,
+              tc::mma_ss_one(issuer, tmem + w * 128, kd + (c / 4) * kHalf + (c % 4) * 2,
                              qd + (c / 4) * kHalf + (c % 4) * 2, idesc, c > 0);
             }
-            tc::commit_one(issuer, &ctl.s_full[w][buf]);
+            tc::commit_one(issuer, &ctl.s_full[w]);
+            if (t + 1 == steps) tc::commit_one(issuer, &ctl.k_empty[k_slot]);
           }
           if (!ok) break;
-          if (both) ++step1;
           tc::commit_one(issuer, &ctl.q_empty[q_slot]);
           __syncwarp();
         }
-        if (!ok) break;
-        tc::commit_one(issuer, &ctl.k_empty[k_slot]);
-        ++pairs;
+        keys += tiles;
       }
       if (!ok && lane == 0) {
         *abort_flag = 1;
@@ -524,32 +542,34 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     // ------------------------------------------------------------ exponentials and sums
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMore));
     const int w = warp >> 2, r = threadIdx.x & 127;  // key tile, key of it = TMEM lane
-    const uint32_t t_s = tmem + ((uint32_t)((warp & 3) * 32) << 16) + w * 256;
+    const uint32_t t_s = tmem + ((uint32_t)((warp & 3) * 32) << 16) + w * 128;
     const float sl = a.scale * kLog2e;
     const float2 sl2 = make_float2(sl, sl);
     uint32_t step = 0, used = 0;  // query tiles, and those that this warpgroup had scores of
     bool ok = true;
     Piece piece = {0, 0, 0, 0};
     auto page_of = [&]() -> int32_t {  // of this thread's key of the cursor's unit, or -1
-      const int j = cur.u_p * kPair + w * kKeys + r;
-      if (j >= cur.kend) return -1;
-      const int32_t id = a.table[(int64_t)cur.u_s * a.width + (j >> a.page_shift)];
-      return id;
+      const int j = cur.u_p * kUnit + w * kKeys + r;
+      return j < cur.kend ? a.table[(int64_t)cur.u_s * a.width + (j >> a.page_shift)] : -1;
     };
     bool have = cur.next(a);
     int32_t next_id = have ? page_of() : -1;
     while (ok && have) {
-      const int j = cur.u_p * kPair + w * kKeys + r, hk = cur.u_hk, len = cur.r.len;
+      const int j = cur.u_p * kUnit + w * kKeys + r, hk = cur.u_hk, len = cur.r.len;
       const int tok0 = cur.r.tok0, m = cur.r.m, n = cur.n;
-      const int ta = cur.a, tb = cur.b, t0 = cur.t0, us = cur.u_s, up = cur.u_p;
+      const int ta = cur.a, tb = cur.b, t0 = cur.t0;
       int32_t id = next_id;
       if (id >= a.pages) id = -1;
-      const bool idle = up * kPair + w * kKeys >= cur.kend;  // no key of this tile is one
+      const bool idle = w >= cur.tiles;  // no key of this tile is one
+      const bool add = id >= 0 && j < len && a.decay != 0.f;
+      const bool cut = ta > 0 || tb < n;
+      if (cut) {
+        if (ta == 0) piece = {cur.u_s, cur.u_p, hk, piece.flags | kBegins};
+        else piece.flags |= kHas | (tb == n ? kEnds : 0);
+      }
       // under way while the products are waited for: what the weight was, and the
       // next unit's page
       float old = 0.f;
-      const bool add = id >= 0 && j < len && a.decay != 0.f;
-      const bool cut = ta > 0 || tb < n;
       if (add && !cut) old = *weight_at(a, id, j, hk);
       have = cur.next(a);
       next_id = have ? page_of() : -1;
@@ -559,8 +579,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         ok = tc::wait_all<false>(&ctl.q_full[slot], (step / NQ) & 1, abort_flag, budget);
         if (!ok) break;
         if (!idle) {
-          const int buf = (int)(used & 1);
-          ok = tc::wait_all<false>(&ctl.s_full[w][buf], (used >> 1) & 1, abort_flag, budget);
+          ok = tc::wait_all<false>(&ctl.s_full[w], used & 1, abort_flag, budget);
           if (!ok) break;
           ++used;
           tc::fence_after_sync();
@@ -578,22 +597,22 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             lo = cols;  // by their words, below
           }
           const float4* l4 = reinterpret_cast<const float4*>(ctl.lse[slot]);
-          const uint32_t from = t_s + buf * 128;
           if (__all_sync(0xFFFFFFFFu, lo == 0 && hi == cols && cols > kRows - 16)) {
             // every row of a whole product (what is behind the last has lse +inf and
             // zeros for q): 32 columns are summed while the next are loaded
             uint32_t s[2][32];
-            tc::tmem_ld32(from, s[0]);
+            tc::tmem_ld32(t_s, s[0]);
             float2 part[4] = {};
 #pragma unroll
             for (int q = 0; q < kRows / 32; ++q) {
               uint32_t(&v)[32] = s[q & 1];
               tc::tmem_ld_wait(v);
               if (q + 1 < kRows / 32) {
-                tc::tmem_ld32(from + (q + 1) * 32, s[(q + 1) & 1]);
+                tc::tmem_ld32(t_s + (q + 1) * 32, s[(q + 1) & 1]);
               } else {
                 tc::fence_before_sync();
-                tc::mbar_arrive(&ctl.s_empty[w][buf]);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ctl.s_empty[w]);
               }
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
@@ -617,7 +636,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll 1
             for (int c = 0; c < cols; c += 32) {
               uint32_t v[32];
-              tc::tmem_ld32(from + c, v);
+              tc::tmem_ld32(t_s + c, v);
               tc::tmem_ld_wait(v);
               uint32_t see = tc::span_bits(lo - c, hi - c);
               if (a.tree && j >= len && j - len < 64) {
@@ -633,20 +652,18 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             }
             sum += some;
             tc::fence_before_sync();
-            tc::mbar_arrive(&ctl.s_empty[w][buf]);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl.s_empty[w]);
           }
         }
-        tc::mbar_arrive(&ctl.q_empty[slot]);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl.q_empty[slot]);
       }
       if (!ok) break;
-      if (cut) {
-        const bool begins = ta == 0, ends = tb == n;
-        if (begins) piece = {us, up, hk, piece.flags | kBegins};
-        else if (!ends) piece.flags |= kGoesOn;
-        sc.sums[((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kPair + w * kKeys + r] = sum;
-      } else if (id >= 0) {
+      if (cut)
+        sc.sums[((int64_t)blockIdx.x * 2 + (ta == 0 ? 1 : 0)) * kUnit + w * kKeys + r] = sum;
+      else if (id >= 0)
         *weight_at(a, id, j, hk) = add ? fmaf(a.decay, old, sum) : sum;
-      }
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -656,26 +673,27 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   }
   tc::fence_before_sync();
   cta_sync();
-  if (warp == 9) {
+  if (warp == kWarpMma) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
 }
 
-// The sums of the pair that begins in CTA c and goes on behind it, in order.
-__global__ void __launch_bounds__(kPair) join_kernel(const WeightArgs a, const Scratch sc, int parts) {
+// The sums of the unit that begins in CTA c and goes on behind it, in order.
+__global__ void __launch_bounds__(kUnit) join_kernel(const WeightArgs a, const Scratch sc, int parts) {
   pdl_wait();
   pdl_trigger();
   const int k = threadIdx.x;
   int c = blockIdx.x;
   const Piece u = sc.piece[c];
   if (!(u.flags & kBegins)) return;
-  float sum = sc.sums[((int64_t)c * 2 + 1) * kPair + k];
+  float sum = sc.sums[((int64_t)c * 2 + 1) * kUnit + k];
   for (++c; c < parts; ++c) {
-    sum += sc.sums[(int64_t)c * 2 * kPair + k];
-    if (!(sc.piece[c].flags & kGoesOn)) break;
+    const int flags = sc.piece[c].flags;
+    if (flags & kHas) sum += sc.sums[(int64_t)c * 2 * kUnit + k];
+    if (flags & kEnds) break;
   }
-  const int j = u.p * kPair + k, len = a.lens[u.s];
+  const int j = u.p * kUnit + k, len = a.lens[u.s];
   if (j >= len + a.cu[u.s + 1] - a.cu[u.s]) return;
   const int32_t id = a.table[(int64_t)u.s * a.width + (j >> a.page_shift)];
   if (id < 0 || id >= a.pages) return;
@@ -701,8 +719,8 @@ cudaError_t launch_all(const WeightArgs& a, const Scratch& sc, int parts, int* e
   qmap = kmap;
   if (by_tma && !make_rows_map(&qmap, a.q, BF16, D, a.heads, a.T, q_head, q_tok, group, tile_tok))
     return cudaErrorInvalidValue;
-  // Cutting pairs between CTAs costs the second launch; it pays where a request has
-  // several query tiles a pair.
+  // Cutting units between CTAs costs the second launch; it pays where a request has
+  // several query tiles a unit.
   const bool whole = a.T <= (int64_t)2 * tile_tok * a.S;
   static int smem_set[64] = {0};
   cudaError_t e = ensure_dynamic_smem(weights_kernel<BF16, D>, Shape<D>::kSmem, smem_set);
@@ -710,7 +728,7 @@ cudaError_t launch_all(const WeightArgs& a, const Scratch& sc, int parts, int* e
   e = launch_kernel(true, weights_kernel<BF16, D>, dim3(parts), dim3(kThreads), Shape<D>::kSmem, s, kmap,
                     qmap, a, sc, (int)head_first, (int)by_tma, (int)whole, role_wait_cycles(), err);
   if (e != cudaSuccess || whole) return e;
-  return launch_kernel(true, join_kernel, dim3(parts), dim3(kPair), 0, s, a, sc, parts);
+  return launch_kernel(true, join_kernel, dim3(parts), dim3(kUnit), 0, s, a, sc, parts);
 }
 
 inline size_t sums_at(int parts) { return ((size_t)parts * sizeof(Piece) + 255) / 256 * 256; }
@@ -719,7 +737,7 @@ inline size_t sums_at(int parts) { return ((size_t)parts * sizeof(Piece) + 255) 
 
 size_t weights_scratch_bytes() {
   const int parts = part_count();
-  return sums_at(parts) + (size_t)parts * 2 * kPair * sizeof(float);
+  return sums_at(parts) + (size_t)parts * 2 * kUnit * sizeof(float);
 }
 
 cudaError_t launch_cache_weights(const WeightArgs& a, void* scratch, int* err, cudaStream_t s) {
