@@ -47,16 +47,17 @@ template <int D> struct Shape {
   static constexpr int kTiles = D == 128 ? 4 : 8;       // of them in shared memory
   static constexpr int kQ = kRows * D * 2;              // a query tile
   static constexpr int kQTiles = D == 128 ? 3 : 5;
-  static constexpr int kSmem = kTiles * kTile + kQTiles * kQ + 1024;
+  static constexpr int kLse = 5;                        // query tiles' lse
+  static constexpr int kSmem = kTiles * kTile + kQTiles * kQ;
 };
 
-template <int NK, int NQ> struct Ctl {
-  uint64_t k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ];
+template <int NK, int NQ, int NL> struct Ctl {
+  uint64_t k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ], l_full[NL], l_empty[NL];
   uint64_t s_full[kGroups], s_empty[kGroups];
   uint64_t drain;
   uint32_t tmem;
   int abort;
-  float lse[NQ][kRows];  // in base 2; +inf where there is no row
+  float neg_lse[NL][kRows];  // -lse in base 2; -inf where there is no row
   // the plan: the CTA's share of all cost, and the unit in which it begins
   long long lo, hi;
   int bad, s0, p0, off0, hk0;
@@ -284,8 +285,9 @@ __device__ __forceinline__ float* weight_at(const WeightArgs& a, int32_t id, int
 }
 
 constexpr int kPlanBytes = kThreads / 32 * 8;  // make_plan's own
-static_assert(Shape<128>::kSmem + sizeof(Ctl<4, 3>) + kPlanBytes <= 227 * 1024, "shared memory");
-static_assert(Shape<64>::kSmem + sizeof(Ctl<8, 5>) + kPlanBytes <= 227 * 1024, "shared memory");
+// (the tiles begin on a multiple of 1024 bytes)
+static_assert(Shape<128>::kSmem + 3072 <= 227 * 1024 && sizeof(Ctl<4, 3, 5>) + kPlanBytes <= 3072, "shared memory");
+static_assert(Shape<64>::kSmem + 4096 <= 227 * 1024 && sizeof(Ctl<8, 5, 5>) + kPlanBytes <= 4096, "shared memory");
 
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -293,11 +295,13 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                const WeightArgs a, const Scratch sc, int k_head_first, int q_by_tma, int whole_only,
                long long budget, int* err) {
   using Sh = Shape<D>;
-  constexpr int NK = Sh::kTiles, NQ = Sh::kQTiles;
-  extern __shared__ uint8_t dsmem_raw[];
-  __shared__ Ctl<NK, NQ> ctl;
-  uint8_t* k_s = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  constexpr int NK = Sh::kTiles, NQ = Sh::kQTiles, NL = Sh::kLse;
+  extern __shared__ __align__(1024) uint8_t k_s[];
+  __shared__ Ctl<NK, NQ, NL> ctl;
+  if (tc::smem_addr(k_s) & 1023) {  // (the same in every thread; swizzles count from there)
+    if (threadIdx.x == 0) record_error(err, kDevErrTimeout);
+    return;
+  }
   uint8_t* q_s = k_s + NK * Sh::kTile;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* abort_flag = &ctl.abort;
@@ -308,8 +312,12 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       tc::mbar_init(&ctl.k_empty[i], 1);
     }
     for (int i = 0; i < NQ; ++i) {
-      tc::mbar_init(&ctl.q_full[i], 33);               // the warp's lanes, and one for a copy's bytes
-      tc::mbar_init(&ctl.q_empty[i], 1 + 4 * kGroups);  // the MMAs, and a warp each of the readers of lse
+      tc::mbar_init(&ctl.q_full[i], 33);  // the warp's lanes, and one for a copy's bytes
+      tc::mbar_init(&ctl.q_empty[i], 1);
+    }
+    for (int i = 0; i < NL; ++i) {
+      tc::mbar_init(&ctl.l_full[i], 32);
+      tc::mbar_init(&ctl.l_empty[i], 4 * kGroups);  // a warp each of the readers
     }
     for (int w = 0; w < kGroups; ++w) {
       tc::mbar_init(&ctl.s_full[w], 1);
@@ -410,9 +418,13 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       bool ok = true;
       while (ok && cur.next(a)) {
         for (int t = cur.t0 + cur.a; t < cur.t0 + cur.b; ++t, ++n) {
-          const int slot = (int)(n % NQ);
+          const int slot = (int)(n % NQ), l_slot = (int)(n % NL);
           if (n >= (uint32_t)NQ) {
             ok = tc::wait_all<false>(&ctl.q_empty[slot], ((n / NQ) & 1) ^ 1, abort_flag, budget);
+            if (!ok) break;
+          }
+          if (n >= (uint32_t)NL) {
+            ok = tc::wait_all<false>(&ctl.l_empty[l_slot], ((n / NL) & 1) ^ 1, abort_flag, budget);
             if (!ok) break;
           }
           uint8_t* dst = q_s + slot * Sh::kQ;
@@ -452,7 +464,8 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
           }
 #pragma unroll
           for (int i = 0; i < kRows / 32; ++i)  // a row that sees nothing draws nothing
-            ctl.lse[slot][i * 32 + lane] = l[i] == -kInf ? kInf : l[i] * kLog2e;
+            ctl.neg_lse[l_slot][i * 32 + lane] = l[i] == -kInf ? -kInf : l[i] * -kLog2e;
+          tc::mbar_arrive(&ctl.l_full[l_slot]);
           if (!tma) {
             asm volatile("cp.async.wait_all;" ::: "memory");
             tc::fence_async_smem();
@@ -575,8 +588,8 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       next_id = have ? page_of() : -1;
       float sum = 0.f;
       for (int t = t0 + ta; t < t0 + tb; ++t, ++step) {
-        const int slot = (int)(step % NQ);
-        ok = tc::wait_all<false>(&ctl.q_full[slot], (step / NQ) & 1, abort_flag, budget);
+        const int slot = (int)(step % NL);
+        ok = tc::wait_all<false>(&ctl.l_full[slot], (step / NL) & 1, abort_flag, budget);
         if (!ok) break;
         if (!idle) {
           ok = tc::wait_all<false>(&ctl.s_full[w], used & 1, abort_flag, budget);
@@ -596,9 +609,9 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
           } else if (j >= len) {
             lo = cols;  // by their words, below
           }
-          const float4* l4 = reinterpret_cast<const float4*>(ctl.lse[slot]);
+          const float4* l4 = reinterpret_cast<const float4*>(ctl.neg_lse[slot]);
           if (__all_sync(0xFFFFFFFFu, lo == 0 && hi == cols && cols > kRows - 16)) {
-            // every row of a whole product (what is behind the last has lse +inf and
+            // every row of a whole product (what is behind the last has -lse -inf and
             // zeros for q): 32 columns are summed while the next are loaded
             uint32_t s[2][32];
             tc::tmem_ld32(t_s, s[0]);
@@ -618,9 +631,9 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
               for (int c = 0; c < 8; ++c) {
                 const float4 l = l4[q * 8 + c];
                 float2 x = tc::fma_x2(make_float2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), sl2,
-                                      make_float2(-l.x, -l.y));
+                                      make_float2(l.x, l.y));
                 float2 y = tc::fma_x2(make_float2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), sl2,
-                                      make_float2(-l.z, -l.w));
+                                      make_float2(l.z, l.w));
                 x.x = tc::exp2_approx(x.x);
                 x.y = tc::exp2_approx(x.y);
                 y.x = tc::exp2_approx(y.x);
@@ -646,7 +659,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
               }
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const float x = tc::exp2_approx(fmaf(__uint_as_float(v[i]), sl, -ctl.lse[slot][c + i]));
+                const float x = tc::exp2_approx(fmaf(__uint_as_float(v[i]), sl, ctl.neg_lse[slot][c + i]));
                 some += (see >> i) & 1 ? x : 0.f;
               }
             }
@@ -657,7 +670,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
           }
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ctl.q_empty[slot]);
+        if (lane == 0) tc::mbar_arrive(&ctl.l_empty[slot]);
       }
       if (!ok) break;
       if (cut)
