@@ -33,18 +33,20 @@ constexpr int kKeys = 128;         // keys of a tile
 constexpr int kGroups = 4;         // tiles of a unit, a warpgroup each
 constexpr int kUnit = kGroups * kKeys;
 constexpr int kRows = 128;         // query rows of a tile
-// Four warpgroups that sum, four warps of which three work; of the 96 registers a
-// thread at launch the former get 104 and the latter 64.
+// Four warpgroups that sum, and four warps that load (keys, queries) and issue the
+// MMAs (of two tiles each); of the 96 registers a thread at launch the former get 104
+// and the latter 64.
 constexpr int kThreads = 640;
 constexpr int kRegsMore = 104, kRegsLess = 64;
-constexpr int kWarpK = 16, kWarpMma = 17, kWarpQ = 18;
+constexpr int kWarpK = 16, kWarpQ = 17, kWarpMma = 18;  // and kWarpMma + 1
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_huge_valf();
 
 template <int D> struct Shape {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kKeys * D * 2;           // a key tile
-  static constexpr int kTiles = D == 128 ? 4 : 8;       // of them in shared memory
+  static constexpr int kSets = D == 128 ? 1 : 2;        // units whose keys are in shared memory
+  static constexpr int kTiles = kSets * kGroups;
   static constexpr int kQ = kRows * D * 2;              // a query tile
   static constexpr int kQTiles = D == 128 ? 3 : 5;
   static constexpr int kLse = 5;                        // query tiles' lse
@@ -54,10 +56,10 @@ template <int D> struct Shape {
 template <int NK, int NQ, int NL> struct Ctl {
   uint64_t k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ], l_full[NL], l_empty[NL];
   uint64_t s_full[kGroups], s_empty[kGroups];
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem;
   int abort;
-  float neg_lse[NL][kRows];  // -lse in base 2; -inf where there is no row
+  alignas(16) float neg_lse[NL][kRows];  // -lse in base 2; -inf where there is no row
   // the plan: the CTA's share of all cost, and the unit in which it begins
   long long lo, hi;
   int bad, s0, p0, off0, hk0;
@@ -313,7 +315,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     }
     for (int i = 0; i < NQ; ++i) {
       tc::mbar_init(&ctl.q_full[i], 33);  // the warp's lanes, and one for a copy's bytes
-      tc::mbar_init(&ctl.q_empty[i], 1);
+      tc::mbar_init(&ctl.q_empty[i], 2);  // from both issuing warps
     }
     for (int i = 0; i < NL; ++i) {
       tc::mbar_init(&ctl.l_full[i], 32);
@@ -323,7 +325,8 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       tc::mbar_init(&ctl.s_full[w], 1);
       tc::mbar_init(&ctl.s_empty[w], 4);
     }
-    tc::mbar_init(&ctl.drain, 1);
+    tc::mbar_init(&ctl.drain[0], 1);
+    tc::mbar_init(&ctl.drain[1], 1);
     ctl.abort = 0;
     tc::fence_mbar_init();
   }
@@ -359,7 +362,8 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       asm volatile("fence.proxy.async;" ::: "memory");
       const int run_tok = min(kKeys, 1 << a.page_shift), runs = kKeys / run_tok;  // of a tile
       const int run = lane / Sh::kHalves, half = lane % Sh::kHalves;
-      uint32_t n = 0;
+      uint32_t n = 0;     // units
+      uint32_t used = 0;  // a bit a slot: whether it was used, and above them, an odd number of times
       bool ok = true;
       while (ok && cur.next(a)) {
         if (cur.b == cur.a) continue;  // no row sees the unit
@@ -375,12 +379,13 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             }
           }
         }
-        for (int t = 0; t < cur.tiles; ++t, ++n) {
-          const int slot = (int)(n % NK);
-          if (n >= (uint32_t)NK) {
-            ok = tc::wait_all<false>(&ctl.k_empty[slot], ((n / NK) & 1) ^ 1, abort_flag, budget);
+        for (int t = 0; t < cur.tiles; ++t) {
+          const int slot = (int)(n % Sh::kSets) * kGroups + t;
+          if (used >> slot & 1) {
+            ok = tc::wait_all<false>(&ctl.k_empty[slot], (used >> (slot + 16) & 1) ^ 1, abort_flag, budget);
             if (!ok) break;
           }
+          used = (used | 1u << slot) ^ 1u << (slot + 16);
           // and loads one of the tile, or half its dimensions
           const int32_t page = __shfl_sync(0xFFFFFFFFu, id, (t * runs + run) & 31);
           const bool want = run < runs && page >= 0;
@@ -395,6 +400,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             k_head_first ? off : cur.u_hk, page);
           }
         }
+        ++n;
       }
       if (!ok && lane == 0) {
         *abort_flag = 1;
@@ -403,10 +409,10 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       __syncwarp();
       if (lane == 0) {
         // no copy may be under way when the CTA ends, whichever role gave up
-        const uint32_t first = n > (uint32_t)NK ? n - NK : 0;
-        for (uint32_t j = first; j < n; ++j) {
+        for (int i = 0; i < NK; ++i) {
+          if (!(used >> i & 1)) continue;
           const long long t = clock64();
-          while (!tc::mbar_try_wait(&ctl.k_full[j % NK], (j / NK) & 1) &&
+          while (!tc::mbar_try_wait(&ctl.k_full[i], (used >> (i + 16) & 1) ^ 1) &&
                  clock64() - t < tc::kWaitCycles) {
           }
         }
@@ -487,14 +493,21 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
           }
         }
       }
-    } else if (warp == kWarpMma) {
+    } else {
       // ------------------------------------------------------------ MMAs
+      // of tiles w0 and w0 + 1. Two warps, because one spends as long between tiles,
+      // waiting and forming descriptors, as half of the tensor cores' time (a warp for
+      // all four, 8 products of 64 cycles a tile, took 850 a tile).
+      const int w0 = (warp - kWarpMma) * 2;
       const bool issuer = tc::elect_one();
-      const uint64_t k_desc = tc::sw128_kmajor_desc(tc::smem_addr(k_s));
+      // (addresses count 16 bytes in the low 14 bits: sums stay in the low word)
+      const uint64_t k_desc = tc::sw128_kmajor_desc(tc::smem_addr(k_s) + w0 * Sh::kTile);
       const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_addr(q_s));
-      uint32_t keys = 0, step = 0;
-      uint32_t uses = 0;  // a bit a tile: whether it was used an odd number of times
-      uint32_t met = 0;   // and whether it was used at all
+      const uint32_t hi = (uint32_t)(k_desc >> 32);
+      auto desc = [&](uint32_t lo) { return (uint64_t)hi << 32 | lo; };
+      uint32_t n = 0, step = 0;
+      uint32_t uses = 0;  // a bit a tile: whether it was used, and above them, an odd number of times
+      uint32_t seen = 0;  // a bit a slot of keys: whether it was used an odd number of times
       bool ok = true;
       while (ok) {
         // what branches and operands depend on comes by shuffle from lane 0, so that
@@ -503,52 +516,55 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         const int steps = __shfl_sync(0xFFFFFFFFu, found ? cur.b - cur.a : -1, 0);
         if (steps < 0) break;
         if (steps == 0) continue;
-        const int tiles = __shfl_sync(0xFFFFFFFFu, cur.tiles, 0);
+        const int tiles = __shfl_sync(0xFFFFFFFFu, cur.tiles, 0) - w0;
         const int first = __shfl_sync(0xFFFFFFFFu, (cur.r.m - (cur.t0 + cur.a) * tile_tok), 0);
+        const int set = (int)(n % Sh::kSets);
+        const uint32_t kd = (uint32_t)k_desc + set * (kGroups * Sh::kTile / 16);
+        ++n;
 #pragma unroll 1
         for (int t = 0; t < steps && ok; ++t, ++step) {
           const int q_slot = (int)(step % NQ);
           const int rows = min(tile_tok, first - t * tile_tok) * group;
           const uint32_t idesc = tc::idesc_f16_f32(BF16, kKeys, (uint32_t)((rows + 15) & ~15), false);
+          const uint32_t qd = (uint32_t)q_desc + q_slot * (Sh::kQ / 16);
           ok = tc::wait_all<true>(&ctl.q_full[q_slot], (step / NQ) & 1, abort_flag, budget);
           if (!ok) break;
-          const uint64_t qd = q_desc + q_slot * (Sh::kQ / 16);
-#pragma unroll 1
-          for (int w = 0; w < tiles; ++w) {
-            const uint32_t nk = keys + w;
-            const int k_slot = (int)(nk % NK);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (w >= tiles) break;
+            uint64_t* k_empty = &ctl.k_empty[set * kGroups + w0 + w];
             if (t == 0) {
-              ok = tc::wait_all<true>(&ctl.k_full[k_slot], (nk / NK) & 1, abort_flag, budget);
+              ok = tc::wait_all<true>(&ctl.k_full[set * kGroups + w0 + w], seen >> (set * 2 + w) & 1, abort_flag,
+                                      budget);
+              if (!ok) break;
+              seen ^= 1u << (set * 2 + w);
+            }
+            if (uses >> w & 1) {
+              ok = tc::wait_all<true>(&ctl.s_empty[w0 + w], (uses >> (w + 2) & 1) ^ 1, abort_flag, budget);
               if (!ok) break;
             }
-            if (met >> w & 1) {
-              ok = tc::wait_all<true>(&ctl.s_empty[w], (uses >> w & 1) ^ 1, abort_flag, budget);
-              if (!ok) break;
-            }
-            met |= 1u << w;
-            uses ^= 1u << w;
+            uses = (uses | 1u << w) ^ 1u << (w + 2);
             tc::fence_after_sync();
-            const uint64_t kd = k_desc + k_slot * (Sh::kTile / 16);
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               constexpr int kHalf = kKeys * 128 / 16;
-              tc::mma_ss_one(issuer, tmem + w * 128, kd + (c / 4) * kHalf + (c % 4) * 2,
-                             qd + (c / 4) * kHalf + (c % 4) * 2, idesc, c > 0);
+              tc::mma_ss_one(issuer, tmem + (w0 + w) * 128,
+                             desc(kd + w * (Sh::kTile / 16) + (c / 4) * kHalf + (c % 4) * 2),
+                             desc(qd + (c / 4) * kHalf + (c % 4) * 2), idesc, c > 0);
             }
-            tc::commit_one(issuer, &ctl.s_full[w]);
-            if (t + 1 == steps) tc::commit_one(issuer, &ctl.k_empty[k_slot]);
+            tc::commit_one(issuer, &ctl.s_full[w0 + w]);
+            if (t + 1 == steps) tc::commit_one(issuer, k_empty);
           }
           if (!ok) break;
           tc::commit_one(issuer, &ctl.q_empty[q_slot]);
           __syncwarp();
         }
-        keys += tiles;
       }
       if (!ok && lane == 0) {
         *abort_flag = 1;
         record_error(err, kDevErrTimeout);
       }
-      if (issuer) tc::mma_drain(&ctl.drain);  // TMEM is freed below
+      if (issuer) tc::mma_drain(&ctl.drain[warp - kWarpMma]);  // TMEM is freed below
       __syncwarp();
     }
   } else {
@@ -564,6 +580,13 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     auto page_of = [&]() -> int32_t {  // of this thread's key of the cursor's unit, or -1
       const int j = cur.u_p * kUnit + w * kKeys + r;
       return j < cur.kend ? a.table[(int64_t)cur.u_s * a.width + (j >> a.page_shift)] : -1;
+    };
+    // sum += 2^(s sl - lse), two columns at once
+    auto add_weights = [&](float2& to, uint32_t s0, uint32_t s1, float l0, float l1) {
+      float2 x = tc::fma_x2(make_float2(__uint_as_float(s0), __uint_as_float(s1)), sl2, make_float2(l0, l1));
+      x.x = tc::exp2_approx(x.x);
+      x.y = tc::exp2_approx(x.y);
+      to = tc::add_x2(to, x);
     };
     bool have = cur.next(a);
     int32_t next_id = have ? page_of() : -1;
@@ -587,6 +610,21 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       have = cur.next(a);
       next_id = have ? page_of() : -1;
       float sum = 0.f;
+      // the query tiles of which every row is one and sees every key of this warp
+      int fast0 = 0, fast1 = 0;
+      if (tile_tok * group > kRows - 16) {
+        const int j1 = (j | 31) - len;  // the warp's last key, counted from the first new token
+        fast1 = m / tile_tok;
+        if (a.tree)
+          fast1 = j1 < 0 ? fast1 : 0;
+        else if (j1 > 0)
+          fast0 = (j1 + tile_tok - 1) / tile_tok;
+        if (a.window > 0) {
+          // its first key is in sight of a tile's last token
+          const long long past = (long long)(j & ~31) - len + a.window;
+          fast1 = past <= 0 ? 0 : (int)min((long long)fast1, past / tile_tok);
+        }
+      }
       for (int t = t0 + ta; t < t0 + tb; ++t, ++step) {
         const int slot = (int)(step % NL);
         ok = tc::wait_all<false>(&ctl.l_full[slot], (step / NL) & 1, abort_flag, budget);
@@ -596,21 +634,8 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
           if (!ok) break;
           ++used;
           tc::fence_after_sync();
-          const int i0 = t * tile_tok, toks = min(tile_tok, m - i0), cols = toks * group;
-          // columns [lo, hi) see the key
-          int lo = 0, hi = cols;
-          if (!a.tree) {
-            const int late = j - len - i0;  // tokens of the tile that come before the key
-            lo = late <= 0 ? 0 : late >= toks ? cols : late * group;
-            if (a.window > 0) {
-              const long long past = (long long)late + a.window;
-              hi = past <= 0 ? 0 : past >= toks ? cols : (int)past * group;
-            }
-          } else if (j >= len) {
-            lo = cols;  // by their words, below
-          }
           const float4* l4 = reinterpret_cast<const float4*>(ctl.neg_lse[slot]);
-          if (__all_sync(0xFFFFFFFFu, lo == 0 && hi == cols && cols > kRows - 16)) {
+          if (t >= fast0 && t < fast1) {
             // every row of a whole product (what is behind the last has -lse -inf and
             // zeros for q): 32 columns are summed while the next are loaded
             uint32_t s[2][32];
@@ -630,37 +655,55 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
                 const float4 l = l4[q * 8 + c];
-                float2 x = tc::fma_x2(make_float2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1])), sl2,
-                                      make_float2(l.x, l.y));
-                float2 y = tc::fma_x2(make_float2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3])), sl2,
-                                      make_float2(l.z, l.w));
-                x.x = tc::exp2_approx(x.x);
-                x.y = tc::exp2_approx(x.y);
-                y.x = tc::exp2_approx(y.x);
-                y.y = tc::exp2_approx(y.y);
-                part[c % 2 * 2] = tc::add_x2(part[c % 2 * 2], x);
-                part[c % 2 * 2 + 1] = tc::add_x2(part[c % 2 * 2 + 1], y);
+                add_weights(part[c % 2 * 2], v[4 * c], v[4 * c + 1], l.x, l.y);
+                add_weights(part[c % 2 * 2 + 1], v[4 * c + 2], v[4 * c + 3], l.z, l.w);
               }
             }
             const float2 x = tc::add_x2(tc::add_x2(part[0], part[1]), tc::add_x2(part[2], part[3]));
             sum += x.x + x.y;
           } else {
+            const int i0 = t * tile_tok, toks = min(tile_tok, m - i0), cols = toks * group;
+            // columns [lo, hi) see the key
+            int lo = 0, hi = cols;
+            if (!a.tree) {
+              const int late = j - len - i0;  // tokens of the tile that come before the key
+              lo = late <= 0 ? 0 : late >= toks ? cols : late * group;
+              if (a.window > 0) {
+                const long long past = (long long)late + a.window;
+                hi = past <= 0 ? 0 : past >= toks ? cols : (int)past * group;
+              }
+            } else if (j >= len) {
+              lo = cols;  // by their words, below
+            }
             float some = 0.f;
 #pragma unroll 1
             for (int c = 0; c < cols; c += 32) {
-              uint32_t v[32];
-              tc::tmem_ld32(t_s + c, v);
-              tc::tmem_ld_wait(v);
               uint32_t see = tc::span_bits(lo - c, hi - c);
               if (a.tree && j >= len && j - len < 64) {
                 for (int i = c / group; i <= (c + 31) / group && i < toks; ++i)
                   if (a.tree[tok0 + i0 + i] >> (j - len) & 1)
                     see |= tc::span_bits(i * group - c, (i + 1) * group - c);
               }
+              if (!__any_sync(0xFFFFFFFFu, see != 0)) continue;
+              uint32_t v[32];
+              tc::tmem_ld32(t_s + c, v);
+              tc::tmem_ld_wait(v);
+              if (__all_sync(0xFFFFFFFFu, see == ~0u)) {
+                float2 part[2] = {};
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float x = tc::exp2_approx(fmaf(__uint_as_float(v[i]), sl, ctl.neg_lse[slot][c + i]));
-                some += (see >> i) & 1 ? x : 0.f;
+                for (int i = 0; i < 8; ++i) {
+                  const float4 l = l4[c / 4 + i];
+                  add_weights(part[0], v[4 * i], v[4 * i + 1], l.x, l.y);
+                  add_weights(part[1], v[4 * i + 2], v[4 * i + 3], l.z, l.w);
+                }
+                const float2 x = tc::add_x2(part[0], part[1]);
+                some += x.x + x.y;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float x = tc::exp2_approx(fmaf(__uint_as_float(v[i]), sl, ctl.neg_lse[slot][c + i]));
+                  some += (see >> i) & 1 ? x : 0.f;
+                }
               }
             }
             sum += some;
