@@ -13,7 +13,7 @@
 // query tiles pass by; a decoding step has one query tile, and its keys stream.
 // One CTA an SM, warp-specialised: a warp loads keys (TMA, page by page), one loads
 // queries and their lse, one issues the MMAs, and four warpgroups (a key tile each,
-// with a quarter of the tensor memory) exponentiate and sum; while one waits for its
+// with 128 columns of tensor memory) exponentiate and sum; while one waits for its
 // next product the others use the exponential units. The CTAs share out key tiles x
 // query tiles evenly, in the order (K/V head, request, unit). Where requests bring
 // many query tiles a unit may be cut between CTAs; each leaves its sums in the
@@ -33,12 +33,12 @@ constexpr int kKeys = 128;         // keys of a tile
 constexpr int kGroups = 4;         // tiles of a unit, a warpgroup each
 constexpr int kUnit = kGroups * kKeys;
 constexpr int kRows = 128;         // query rows of a tile
-// Four warpgroups that sum, and four warps that load (keys, queries) and issue the
-// MMAs (of two tiles each); of the 96 registers a thread at launch the former get 104
-// and the latter 64.
-constexpr int kThreads = 640;
+// Four warpgroups that sum, and four warps that load keys, load queries and issue the
+// MMAs (two, of two tiles each); of the 96 registers a thread at launch the former get
+// 104 and the latter 64.
+constexpr int kThreads = kGroups * 128 + 128;
 constexpr int kRegsMore = 104, kRegsLess = 64;
-constexpr int kWarpK = 16, kWarpQ = 17, kWarpMma = 18;  // and kWarpMma + 1
+constexpr int kWarpK = kGroups * 4, kWarpQ = kWarpK + 1, kWarpMma = kWarpK + 2;  // and kWarpMma + 1
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_huge_valf();
 
@@ -49,11 +49,26 @@ template <int D> struct Shape {
   static constexpr int kTiles = kSets * kGroups;
   static constexpr int kQ = kRows * D * 2;              // a query tile
   static constexpr int kQTiles = D == 128 ? 3 : 5;
-  static constexpr int kLse = 5;                        // query tiles' lse
+  static constexpr int kLse = 4;                        // query tiles' lse
+  static constexpr int kUnits = 2 * kSets;              // units ahead
   static constexpr int kSmem = kTiles * kTile + kQTiles * kQ;
 };
 
-template <int NK, int NQ, int NL> struct Ctl {
+// A unit as the other roles need it: they learn of it from the warp that loads the keys.
+struct Unit {
+  int s, p, hk, flags;
+  int tok0, m, len, tiles;  // of the request; key tiles
+  int first, steps;         // query tiles [first, first + steps); steps < 0: no unit, the end
+  int unused[2];
+  int32_t page[32];  // of its runs of keys, -1 where there is none
+};
+constexpr int kAgain = 1;  // its one query tile is the one of the unit before
+constexpr int kKeep = 2;   // it has one query tile, which the next unit may use too
+constexpr int kCutHead = 4, kCutTail = 8;  // of its steps the first, the last are not here
+
+template <int NK, int NQ, int NL, int NU> struct Ctl {
+  Unit unit[NU];
+  uint64_t u_full[NU], u_empty[NU];
   uint64_t k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ], l_full[NL], l_empty[NL];
   uint64_t s_full[kGroups], s_empty[kGroups];
   uint64_t drain[2];
@@ -212,7 +227,7 @@ __device__ void make_plan(const WeightArgs& a, C& ctl, int tile_tok, int* err) {
   cta_sync();
 }
 
-// A CTA's units, in order; every role walks over them by itself.
+// A CTA's units, in order.
 struct Cursor {
   int s, p, hk, off, tile_tok;
   bool whole_only;
@@ -220,11 +235,17 @@ struct Cursor {
   Req r;
   // the unit: its place, its key tiles, its query tiles [a, b) of n from t0 on
   int u_s, u_p, u_hk, tiles, t0, n, a, b, kend;
+  bool again;  // its one query tile is that of the unit's before it, whose step this CTA took too
+  bool ran;    // it has a step here
 
   template <typename C> __device__ void init(const WeightArgs& w, const C& ctl, int tok, bool whole) {
     tile_tok = tok;
     whole_only = whole;
     left = ctl.hi - ctl.lo;
+    u_s = -1;
+    u_p = u_hk = tiles = t0 = n = a = b = kend = 0;
+    r = {};
+    again = ran = false;
     if (left <= 0) return;
     s = ctl.s0;
     p = ctl.p0;
@@ -244,6 +265,7 @@ struct Cursor {
       const Span x = span_of(w, r, p, tile_tok);
       tiles = tiles_of(r, p);
       const int cost = tiles * (1 + x.n);
+      again = ran && n == 1 && x.n == 1 && x.t0 == t0 && u_s == s && u_hk == hk;
       u_s = s;
       u_p = p++;
       u_hk = hk;
@@ -257,12 +279,14 @@ struct Cursor {
         left -= cost - from;
         a = 0;
         b = n;
+        ran = from == 0 && n > 0;
         if (from == 0) return true;
         continue;
       }
       left -= to - from;
       a = step_at(from, tiles);
       b = step_at(to, tiles);
+      ran = b > a;
       if (b > a || (n == 0 && from == 0)) return true;
     }
     return false;
@@ -288,8 +312,8 @@ __device__ __forceinline__ float* weight_at(const WeightArgs& a, int32_t id, int
 
 constexpr int kPlanBytes = kThreads / 32 * 8;  // make_plan's own
 // (the tiles begin on a multiple of 1024 bytes)
-static_assert(Shape<128>::kSmem + 3072 <= 227 * 1024 && sizeof(Ctl<4, 3, 5>) + kPlanBytes <= 3072, "shared memory");
-static_assert(Shape<64>::kSmem + 4096 <= 227 * 1024 && sizeof(Ctl<8, 5, 5>) + kPlanBytes <= 4096, "shared memory");
+static_assert(Shape<128>::kSmem + 3072 <= 227 * 1024 && sizeof(Ctl<4, 3, 4, 2>) + kPlanBytes <= 3072, "shared memory");
+static_assert(Shape<64>::kSmem + 4096 <= 227 * 1024 && sizeof(Ctl<8, 5, 4, 4>) + kPlanBytes <= 4096, "shared memory");
 
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -297,9 +321,9 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                const WeightArgs a, const Scratch sc, int k_head_first, int q_by_tma, int whole_only,
                long long budget, int* err) {
   using Sh = Shape<D>;
-  constexpr int NK = Sh::kTiles, NQ = Sh::kQTiles, NL = Sh::kLse;
+  constexpr int NK = Sh::kTiles, NQ = Sh::kQTiles, NL = Sh::kLse, NU = Sh::kUnits;
   extern __shared__ __align__(1024) uint8_t k_s[];
-  __shared__ Ctl<NK, NQ, NL> ctl;
+  __shared__ Ctl<NK, NQ, NL, NU> ctl;
   if (tc::smem_addr(k_s) & 1023) {  // (the same in every thread; swizzles count from there)
     if (threadIdx.x == 0) record_error(err, kDevErrTimeout);
     return;
@@ -320,6 +344,10 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     for (int i = 0; i < NL; ++i) {
       tc::mbar_init(&ctl.l_full[i], 32);
       tc::mbar_init(&ctl.l_empty[i], 4 * kGroups);  // a warp each of the readers
+    }
+    for (int i = 0; i < NU; ++i) {
+      tc::mbar_init(&ctl.u_full[i], 32);
+      tc::mbar_init(&ctl.u_empty[i], 3 + 4 * kGroups);  // a warp each of its readers
     }
     for (int w = 0; w < kGroups; ++w) {
       tc::mbar_init(&ctl.s_full[w], 1);
@@ -352,24 +380,32 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
   pdl_wait();
   pdl_trigger();
   make_plan(a, ctl, tile_tok, err);
-  Cursor cur;
-  cur.init(a, ctl, tile_tok, whole_only != 0);
+  const int run_tok = min(kKeys, 1 << a.page_shift), runs = kKeys / run_tok;  // keys of a page, of a tile
+  // Unit number n of the CTA, for a reader: waited for, and given back.
+  auto unit_wait = [&](uint32_t n) {
+    return tc::wait_all<false>(&ctl.u_full[n % NU], (n / NU) & 1, abort_flag, budget);
+  };
+  auto unit_done = [&](uint32_t n) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&ctl.u_empty[n % NU]);
+  };
   if (warp >= kWarpK) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLess));
     if (warp == kWarpK) {
       // ------------------------------------------------------------ keys by TMA
       // the cache was written by the launch before through the other proxy
       asm volatile("fence.proxy.async;" ::: "memory");
-      const int run_tok = min(kKeys, 1 << a.page_shift), runs = kKeys / run_tok;  // of a tile
       const int run = lane / Sh::kHalves, half = lane % Sh::kHalves;
-      uint32_t n = 0;     // units
+      uint32_t n = 0, units = 0;  // units, and those with a step
       uint32_t used = 0;  // a bit a slot: whether it was used, and above them, an odd number of times
-      bool ok = true;
-      while (ok && cur.next(a)) {
-        if (cur.b == cur.a) continue;  // no row sees the unit
+      Cursor cur;
+      cur.init(a, ctl, tile_tok, whole_only != 0);
+      bool ok = true, more = true;
+      while (ok && more) {
+        more = cur.next(a);
         // a lane looks up the page of one run of the unit's keys (32 of them at most)
         int32_t id = -1;
-        {
+        if (more) {
           const int key = cur.u_p * kUnit + lane * run_tok;
           if (lane < kGroups * runs && key < cur.kend) {
             id = a.table[(int64_t)cur.u_s * a.width + (key >> a.page_shift)];
@@ -379,8 +415,33 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             }
           }
         }
+        // the other roles are told
+        if (n >= (uint32_t)NU) {
+          ok = tc::wait_all<false>(&ctl.u_empty[n % NU], ((n / NU) & 1) ^ 1, abort_flag, budget);
+          if (!ok) break;
+        }
+        Unit& u = ctl.unit[n % NU];
+        u.page[lane] = id;
+        if (lane == 0) {
+          u.s = cur.u_s;
+          u.p = cur.u_p;
+          u.hk = cur.u_hk;
+          u.flags = (cur.again ? kAgain : 0) | (cur.n == 1 ? kKeep : 0) | (cur.a > 0 ? kCutHead : 0) |
+                    (cur.b < cur.n ? kCutTail : 0);
+          u.tok0 = cur.r.tok0;
+          u.m = cur.r.m;
+          u.len = cur.r.len;
+          u.tiles = cur.tiles;
+          u.first = cur.t0 + cur.a;
+          u.steps = more ? cur.b - cur.a : -1;
+        }
+        tc::mbar_arrive(&ctl.u_full[n % NU]);
+        ++n;
+        if (!more || cur.b == cur.a) continue;  // (no row sees the unit)
+        const int set = (int)(units++ % Sh::kSets) * kGroups;
+#pragma unroll 1
         for (int t = 0; t < cur.tiles; ++t) {
-          const int slot = (int)(n % Sh::kSets) * kGroups + t;
+          const int slot = set + t;
           if (used >> slot & 1) {
             ok = tc::wait_all<false>(&ctl.k_empty[slot], (used >> (slot + 16) & 1) ^ 1, abort_flag, budget);
             if (!ok) break;
@@ -400,7 +461,6 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             k_head_first ? off : cur.u_hk, page);
           }
         }
-        ++n;
       }
       if (!ok && lane == 0) {
         *abort_flag = 1;
@@ -409,6 +469,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       __syncwarp();
       if (lane == 0) {
         // no copy may be under way when the CTA ends, whichever role gave up
+#pragma unroll 1
         for (int i = 0; i < NK; ++i) {
           if (!(used >> i & 1)) continue;
           const long long t = clock64();
@@ -420,10 +481,19 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     } else if (warp == kWarpQ) {
       // ------------------------------------------------------------ queries and lse
       asm volatile("fence.proxy.async;" ::: "memory");
-      uint32_t n = 0;
+      uint32_t n = 0;  // query tiles
       bool ok = true;
-      while (ok && cur.next(a)) {
-        for (int t = cur.t0 + cur.a; t < cur.t0 + cur.b; ++t, ++n) {
+      for (uint32_t un = 0;; ++un) {
+        ok = unit_wait(un);
+        if (!ok) break;
+        const Unit& u = ctl.unit[un % NU];
+        const int steps = u.steps, first = u.first, tok0 = u.tok0, m = u.m, head0 = u.hk * group;
+        const bool again = u.flags & kAgain;
+        unit_done(un);
+        if (steps < 0) break;
+        if (again) continue;
+#pragma unroll 1
+        for (int t = first; t < first + steps; ++t, ++n) {
           const int slot = (int)(n % NQ), l_slot = (int)(n % NL);
           if (n >= (uint32_t)NQ) {
             ok = tc::wait_all<false>(&ctl.q_empty[slot], ((n / NQ) & 1) ^ 1, abort_flag, budget);
@@ -434,7 +504,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if (!ok) break;
           }
           uint8_t* dst = q_s + slot * Sh::kQ;
-          const int tok = cur.r.tok0 + t * tile_tok, toks = min(tile_tok, cur.r.m - t * tile_tok);
+          const int tok = tok0 + t * tile_tok, toks = min(tile_tok, m - t * tile_tok);
           const bool tma = q_by_tma && toks == tile_tok;
           if (lane == 0)
             tc::mbar_arrive_expect_tx(&ctl.q_full[slot],
@@ -443,17 +513,18 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
           if (tma) {
             if (lane < Sh::kHalves)
               tc::tma_load_3d(dst + lane * (kRows * 128), &qmap, &ctl.q_full[slot], lane * 64,
-                              cur.u_hk * group, tok);
+                              head0, tok);
           } else {
             // a tile that is not full: row by row, zeros up to the product's columns
             const int rows = toks * group, cols = (rows + 15) & ~15;
             const uint32_t to = tc::smem_addr(dst);
+#pragma unroll 1
             for (int e = lane; e < cols * (D / 8); e += 32) {
               const int row = e / (D / 8), c = e % (D / 8), tk = row / group;
               const bool in = row < rows;
               const char* src = static_cast<const char*>(a.q) + c * 16;
               if (in)
-                src += (int64_t)(tok + tk) * a.q_tok + (int64_t)(cur.u_hk * group + row - tk * group) * a.q_head;
+                src += (int64_t)(tok + tk) * a.q_tok + (int64_t)(head0 + row - tk * group) * a.q_head;
               const int size = in ? 16 : 0;
               asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                                to + (c / 8) * (kRows * 128) + row * 128 + (((c % 8) ^ (row & 7)) << 4)),
@@ -466,7 +537,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
           for (int i = 0; i < kRows / 32; ++i) {
             const int row = i * 32 + lane, tk = row / group;
             l[i] = -kInf;
-            if (tk < toks) l[i] = a.lse[(int64_t)(tok + tk) * a.heads + cur.u_hk * group + row - tk * group];
+            if (tk < toks) l[i] = a.lse[(int64_t)(tok + tk) * a.heads + head0 + row - tk * group];
           }
 #pragma unroll
           for (int i = 0; i < kRows / 32; ++i)  // a row that sees nothing draws nothing
@@ -478,6 +549,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
           }
           tc::mbar_arrive(&ctl.q_full[slot]);
         }
+        if (!ok) break;
       }
       if (!ok && lane == 0) {
         *abort_flag = 1;
@@ -495,9 +567,9 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       }
     } else {
       // ------------------------------------------------------------ MMAs
-      // of tiles w0 and w0 + 1. Two warps, because one spends as long between tiles,
-      // waiting and forming descriptors, as half of the tensor cores' time (a warp for
-      // all four, 8 products of 64 cycles a tile, took 850 a tile).
+      // of tiles w0 and w0 + 1. One warp for all spends as long between tiles, waiting
+      // and forming descriptors, as half of the tensor cores' time (two prompts of 2048
+      // tokens with four tiles a unit: 207 us, 184 with two warps).
       const int w0 = (warp - kWarpMma) * 2;
       const bool issuer = tc::elect_one();
       // (addresses count 16 bytes in the low 14 bits: sums stay in the low word)
@@ -505,45 +577,54 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       const uint64_t q_desc = tc::sw128_kmajor_desc(tc::smem_addr(q_s));
       const uint32_t hi = (uint32_t)(k_desc >> 32);
       auto desc = [&](uint32_t lo) { return (uint64_t)hi << 32 | lo; };
-      uint32_t n = 0, step = 0;
+      uint32_t units = 0, count = 0;  // units with a step, query tiles
       uint32_t uses = 0;  // a bit a tile: whether it was used, and above them, an odd number of times
+      bool held = false;  // the last query tile is not given back yet
       uint32_t seen = 0;  // a bit a slot of keys: whether it was used an odd number of times
       bool ok = true;
-      while (ok) {
+      for (uint32_t un = 0; ok; ++un) {
+        ok = unit_wait(un);
+        if (!ok) break;
         // what branches and operands depend on comes by shuffle from lane 0, so that
         // the compiler knows it to be the warp's own
-        const bool found = cur.next(a);
-        const int steps = __shfl_sync(0xFFFFFFFFu, found ? cur.b - cur.a : -1, 0);
+        const Unit& u = ctl.unit[un % NU];
+        const int steps = __shfl_sync(0xFFFFFFFFu, u.steps, 0), flags = __shfl_sync(0xFFFFFFFFu, u.flags, 0);
+        const int tiles = __shfl_sync(0xFFFFFFFFu, u.tiles, 0) - w0;
+        const int first = __shfl_sync(0xFFFFFFFFu, u.m - u.first * tile_tok, 0);
+        unit_done(un);
         if (steps < 0) break;
         if (steps == 0) continue;
-        const int tiles = __shfl_sync(0xFFFFFFFFu, cur.tiles, 0) - w0;
-        const int first = __shfl_sync(0xFFFFFFFFu, (cur.r.m - (cur.t0 + cur.a) * tile_tok), 0);
-        const int set = (int)(n % Sh::kSets);
+        const uint32_t set = __shfl_sync(0xFFFFFFFFu, units, 0) % Sh::kSets;
         const uint32_t kd = (uint32_t)k_desc + set * (kGroups * Sh::kTile / 16);
-        ++n;
+        ++units;
+        const bool again = flags & kAgain, keep = flags & kKeep;
+        const uint32_t base = __shfl_sync(0xFFFFFFFFu, count, 0) - (again ? 1u : 0u);
 #pragma unroll 1
-        for (int t = 0; t < steps && ok; ++t, ++step) {
-          const int q_slot = (int)(step % NQ);
+        for (int t = 0; t < steps && ok; ++t) {
           const int rows = min(tile_tok, first - t * tile_tok) * group;
           const uint32_t idesc = tc::idesc_f16_f32(BF16, kKeys, (uint32_t)((rows + 15) & ~15), false);
+          const uint32_t q_slot = (base + t) % NQ;
+          if (!again) {
+            if (held && t == 0) tc::commit_one(issuer, &ctl.q_empty[(base - 1) % NQ]);
+            ok = tc::wait_all<true>(&ctl.q_full[q_slot], ((base + t) / NQ) & 1, abort_flag, budget);
+            if (!ok) break;
+          }
           const uint32_t qd = (uint32_t)q_desc + q_slot * (Sh::kQ / 16);
-          ok = tc::wait_all<true>(&ctl.q_full[q_slot], (step / NQ) & 1, abort_flag, budget);
-          if (!ok) break;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (w >= tiles) break;
             uint64_t* k_empty = &ctl.k_empty[set * kGroups + w0 + w];
             if (t == 0) {
-              ok = tc::wait_all<true>(&ctl.k_full[set * kGroups + w0 + w], seen >> (set * 2 + w) & 1, abort_flag,
+              ok = tc::wait_all<true>(&ctl.k_full[set * kGroups + w0 + w], seen >> (set * kGroups + w) & 1, abort_flag,
                                       budget);
               if (!ok) break;
-              seen ^= 1u << (set * 2 + w);
+              seen ^= 1u << (set * kGroups + w);
             }
             if (uses >> w & 1) {
-              ok = tc::wait_all<true>(&ctl.s_empty[w0 + w], (uses >> (w + 2) & 1) ^ 1, abort_flag, budget);
+              ok = tc::wait_all<true>(&ctl.s_empty[w0 + w], (uses >> (w + 4) & 1) ^ 1, abort_flag, budget);
               if (!ok) break;
             }
-            uses = (uses | 1u << w) ^ 1u << (w + 2);
+            uses = (uses | 1u << w) ^ 1u << (w + 4);
             tc::fence_after_sync();
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
@@ -556,9 +637,11 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if (t + 1 == steps) tc::commit_one(issuer, k_empty);
           }
           if (!ok) break;
-          tc::commit_one(issuer, &ctl.q_empty[q_slot]);
+          if (!keep) tc::commit_one(issuer, &ctl.q_empty[q_slot]);
           __syncwarp();
         }
+        count = base + steps;
+        held = keep;
       }
       if (!ok && lane == 0) {
         *abort_flag = 1;
@@ -574,13 +657,10 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     const uint32_t t_s = tmem + ((uint32_t)((warp & 3) * 32) << 16) + w * 128;
     const float sl = a.scale * kLog2e;
     const float2 sl2 = make_float2(sl, sl);
-    uint32_t step = 0, used = 0;  // query tiles, and those that this warpgroup had scores of
+    uint32_t slot = NL - 1, phase = 1, used = 0;  // the query tile's lse; products that this warpgroup had
+    bool held = false;            // the last tile's lse is not given back yet
     bool ok = true;
     Piece piece = {0, 0, 0, 0};
-    auto page_of = [&]() -> int32_t {  // of this thread's key of the cursor's unit, or -1
-      const int j = cur.u_p * kUnit + w * kKeys + r;
-      return j < cur.kend ? a.table[(int64_t)cur.u_s * a.width + (j >> a.page_shift)] : -1;
-    };
     // sum += 2^(s sl - lse), two columns at once
     auto add_weights = [&](float2& to, uint32_t s0, uint32_t s1, float l0, float l1) {
       float2 x = tc::fma_x2(make_float2(__uint_as_float(s0), __uint_as_float(s1)), sl2, make_float2(l0, l1));
@@ -588,33 +668,31 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
       x.y = tc::exp2_approx(x.y);
       to = tc::add_x2(to, x);
     };
-    bool have = cur.next(a);
-    int32_t next_id = have ? page_of() : -1;
-    while (ok && have) {
-      const int j = cur.u_p * kUnit + w * kKeys + r, hk = cur.u_hk, len = cur.r.len;
-      const int tok0 = cur.r.tok0, m = cur.r.m, n = cur.n;
-      const int ta = cur.a, tb = cur.b, t0 = cur.t0;
-      int32_t id = next_id;
-      if (id >= a.pages) id = -1;
-      const bool idle = w >= cur.tiles;  // no key of this tile is one
-      const bool add = id >= 0 && j < len && a.decay != 0.f;
-      const bool cut = ta > 0 || tb < n;
+    for (uint32_t un = 0;; ++un) {
+      ok = unit_wait(un);
+      if (!ok) break;
+      const Unit& u = ctl.unit[un % NU];  // (kept until its sums are written)
+      const int steps = u.steps;
+      if (steps < 0) break;
+      const int flags = u.flags, len = u.len;
+      const int j = u.p * kUnit + w * kKeys + r;
+      const bool idle = w >= u.tiles;  // no key of this tile is one
+      const int32_t id = j < len + u.m ? u.page[(w * kKeys + r) >> min(7, a.page_shift)] : -1;
+      const bool add = id >= 0 && j < len && a.decay != 0.f, cut = flags & (kCutHead | kCutTail);
       if (cut) {
-        if (ta == 0) piece = {cur.u_s, cur.u_p, hk, piece.flags | kBegins};
-        else piece.flags |= kHas | (tb == n ? kEnds : 0);
+        if (!(flags & kCutHead)) piece = {u.s, u.p, u.hk, piece.flags | kBegins};
+        else piece.flags |= kHas | (flags & kCutTail ? 0 : kEnds);
       }
-      // under way while the products are waited for: what the weight was, and the
-      // next unit's page
+      // what the weight was, under way while the products are waited for
+      float* at = id >= 0 ? weight_at(a, id, j, u.hk) : nullptr;
       float old = 0.f;
-      if (add && !cut) old = *weight_at(a, id, j, hk);
-      have = cur.next(a);
-      next_id = have ? page_of() : -1;
+      if (add && !cut) old = *at;
       float sum = 0.f;
       // the query tiles of which every row is one and sees every key of this warp
       int fast0 = 0, fast1 = 0;
-      if (tile_tok * group > kRows - 16) {
+      if (tile_tok * group > kRows - 16 && steps > 1) {
         const int j1 = (j | 31) - len;  // the warp's last key, counted from the first new token
-        fast1 = m / tile_tok;
+        fast1 = u.m / tile_tok;
         if (a.tree)
           fast1 = j1 < 0 ? fast1 : 0;
         else if (j1 > 0)
@@ -625,10 +703,18 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
           fast1 = past <= 0 ? 0 : (int)min((long long)fast1, past / tile_tok);
         }
       }
-      for (int t = t0 + ta; t < t0 + tb; ++t, ++step) {
-        const int slot = (int)(step % NL);
-        ok = tc::wait_all<false>(&ctl.l_full[slot], (step / NL) & 1, abort_flag, budget);
-        if (!ok) break;
+      const int t0 = u.first;
+      for (int t = t0; t < t0 + steps; ++t) {
+        if (!(flags & kAgain)) {
+          if (held) {
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl.l_empty[slot]);
+          }
+          if (++slot == NL) slot = 0, phase ^= 1;
+          ok = tc::wait_all<false>(&ctl.l_full[slot], phase, abort_flag, budget);
+          if (!ok) break;
+        }
+        held = flags & kKeep;
         if (!idle) {
           ok = tc::wait_all<false>(&ctl.s_full[w], used & 1, abort_flag, budget);
           if (!ok) break;
@@ -662,7 +748,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             const float2 x = tc::add_x2(tc::add_x2(part[0], part[1]), tc::add_x2(part[2], part[3]));
             sum += x.x + x.y;
           } else {
-            const int i0 = t * tile_tok, toks = min(tile_tok, m - i0), cols = toks * group;
+            const int i0 = t * tile_tok, toks = min(tile_tok, u.m - i0), cols = toks * group;
             // columns [lo, hi) see the key
             int lo = 0, hi = cols;
             if (!a.tree) {
@@ -681,7 +767,7 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
               uint32_t see = tc::span_bits(lo - c, hi - c);
               if (a.tree && j >= len && j - len < 64) {
                 for (int i = c / group; i <= (c + 31) / group && i < toks; ++i)
-                  if (a.tree[tok0 + i0 + i] >> (j - len) & 1)
+                  if (a.tree[u.tok0 + i0 + i] >> (j - len) & 1)
                     see |= tc::span_bits(i * group - c, (i + 1) * group - c);
               }
               if (!__any_sync(0xFFFFFFFFu, see != 0)) continue;
@@ -712,14 +798,17 @@ weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if (lane == 0) tc::mbar_arrive(&ctl.s_empty[w]);
           }
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ctl.l_empty[slot]);
+        if (!held) {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&ctl.l_empty[slot]);
+        }
       }
       if (!ok) break;
       if (cut)
-        sc.sums[((int64_t)blockIdx.x * 2 + (ta == 0 ? 1 : 0)) * kUnit + w * kKeys + r] = sum;
+        sc.sums[((int64_t)blockIdx.x * 2 + (flags & kCutHead ? 0 : 1)) * kUnit + w * kKeys + r] = sum;
       else if (id >= 0)
-        *weight_at(a, id, j, hk) = add ? fmaf(a.decay, old, sum) : sum;
+        *at = add ? fmaf(a.decay, old, sum) : sum;
+      unit_done(un);
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
