@@ -32,8 +32,9 @@ __device__ __forceinline__ void split_pos(uint32_t pos, int page, int shift, int
 // a run of its own behind the counts of the runs before.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048, kCopies = 4;
-constexpr int kMostStaged = 48 * 1024 - kBins * kCopies;  // keys; those behind are read again
+constexpr int kSelLoads = 8;
+constexpr int kBins = 2048, kCopies = 4, kCopy = kBins + 8;  // (copies begin in other banks)
+constexpr int kMostStaged = 48 * 1024 - kCopy * kCopies;  // keys; those behind are read again
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   return w != w ? 0u : float_key(w);  // a NaN comes last
@@ -41,8 +42,9 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 __global__ void __launch_bounds__(kSelThreads)
 select_kernel(const SelectArgs a, int shift, int staged, int* err) {
-  extern __shared__ __align__(16) int hist[];  // kBins x kCopies, then the keys
-  uint32_t* keys = reinterpret_cast<uint32_t*>(hist + kBins * kCopies);
+  extern __shared__ __align__(16) int hist[];  // kCopies counts of each bin, then the keys
+  uint32_t* keys = reinterpret_cast<uint32_t*>(hist + kCopy * kCopies);
+  int* mine = hist + (threadIdx.x & (kCopies - 1)) * kCopy;
   __shared__ int more_w[kSelWarps], same_w[kSelWarps];
   __shared__ int sh_need, sh_digit, sh_count;
   pdl_wait();
@@ -67,15 +69,21 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
     if (need == 0) continue;
     const int32_t* row = a.table + (int64_t)s * a.width;
     const char* weights = static_cast<const char*>(a.weights) + head * a.ws.head;
-    auto key_of = [&](int j) -> uint32_t {
-      int pg, off;
+    bool bad = false;
+    auto page_at = [&](int j, int& off) -> int32_t {  // or -1
+      int pg;
       split_pos((uint32_t)j, a.page, shift, pg, off);
       const int32_t id = row[pg];
-      if (id < 0 || id >= a.pages) {
-        record_error(err, kDevErrBadId);
-        return 0u;
-      }
+      return id < 0 || id >= a.pages ? -1 : id;
+    };
+    auto key_at = [&](int32_t id, int off) -> uint32_t {
+      if (id < 0) return 0u;
       return weight_key(*reinterpret_cast<const float*>(weights + id * a.ws.page + off * a.ws.token));
+    };
+    auto key_of = [&](int j) -> uint32_t {
+      int off;
+      const int32_t id = page_at(j, off);
+      return key_at(id, off);
     };
     const int kept_keys = min(staged, hi - lo);
     auto key = [&](int i) { return i < kept_keys ? keys[i] : key_of(lo + i); };  // of position lo + i
@@ -83,21 +91,38 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
     uint32_t prefix = 0, mask = 0;
     int top = 21, bits = 11;
     for (;;) {
-      for (int i = tid; i < kBins * kCopies / 4; i += kSelThreads)
+      for (int i = tid; i < kCopy * kCopies / 4; i += kSelThreads)
         reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
       cta_sync();
-      if (mask == 0) {  // the first time the keys are read
+      if (mask == 0) {  // the first time the keys are read, several of a thread under way together
+        for (int i0 = tid; i0 < total; i0 += kSelLoads * kSelThreads) {
+          int32_t id[kSelLoads];
+          int off[kSelLoads];
+          uint32_t k[kSelLoads];
+#pragma unroll
+          for (int n = 0; n < kSelLoads; ++n) {
+            id[n] = -1;
+            if (i0 + n * kSelThreads < total) {
+              id[n] = page_at(lo + i0 + n * kSelThreads, off[n]);
+              bad |= id[n] < 0;
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < kSelLoads; ++n) k[n] = key_at(id[n], off[n]);
+#pragma unroll
+          for (int n = 0; n < kSelLoads; ++n) {
+            const int i = i0 + n * kSelThreads;
+            if (i >= total) break;
+            if (i < kept_keys) keys[i] = k[n];
+            atomicAdd(&mine[k[n] >> top], 1);
+          }
+        }
+        if (bad) record_error(err, kDevErrBadId);
+      } else {
 #pragma unroll 4
         for (int i = tid; i < total; i += kSelThreads) {
-          const uint32_t k = key_of(lo + i);
-          if (i < kept_keys) keys[i] = k;
-          atomicAdd(&hist[(k >> top) * kCopies + (lane & (kCopies - 1))], 1);
-        }
-      } else {
-        for (int i = tid; i < total; i += kSelThreads) {
           const uint32_t k = key(i);
-          if ((k & mask) == prefix)
-            atomicAdd(&hist[((k >> top) & ((1u << bits) - 1u)) * kCopies + (lane & (kCopies - 1))], 1);
+          if ((k & mask) == prefix) atomicAdd(&mine[(k >> top) & ((1u << bits) - 1u)], 1);
         }
       }
       cta_sync();
@@ -106,8 +131,8 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
       int c[kPer], sum = 0;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int4 v = reinterpret_cast<const int4*>(hist)[kBins - 1 - (tid * kPer + i)];
-        c[i] = v.x + v.y + v.z + v.w;
+        const int* h = hist + kBins - 1 - (tid * kPer + i);
+        c[i] = (h[0] + h[kCopy]) + (h[2 * kCopy] + h[3 * kCopy]);
         sum += c[i];
       }
       int incl = sum;
@@ -150,6 +175,7 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
     const int run = ((total + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
     const int r0 = min(total, warp * run), r1 = min(total, r0 + run);
     int more = 0, same = 0;
+#pragma unroll 4
     for (int i = r0 + lane; i < r1; i += 32) {
       const uint32_t k = key(i) & mask;
       more += k > prefix;
@@ -162,17 +188,28 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
     cta_sync();
     int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? more_w[lane] : 0);
     int equal = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? same_w[lane] : 0);
-    for (int i0 = r0; i0 < r1; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t k = i < r1 ? key(i) & mask : 0u;
-      const bool is_more = i < r1 && k > prefix, is_same = i < r1 && k == prefix;
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, is_more), e = __ballot_sync(0xFFFFFFFFu, is_same);
+    constexpr int kAhead = 4;  // chunks of 32 looked at together
+    for (int i0 = r0; i0 < r1; i0 += 32 * kAhead) {
+      uint32_t m[kAhead], e[kAhead];
+      bool is_more[kAhead], is_same[kAhead];
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) {
+        const int i = i0 + 32 * n + lane;
+        const uint32_t k = i < r1 ? key(i) & mask : 0u;
+        is_more[n] = i < r1 && k > prefix;
+        is_same[n] = i < r1 && k == prefix;
+        m[n] = __ballot_sync(0xFFFFFFFFu, is_more[n]);
+        e[n] = __ballot_sync(0xFFFFFFFFu, is_same[n]);
+      }
       const uint32_t below = (1u << lane) - 1u;
-      const int eq = equal + __popc(e & below);
-      if (is_more || (is_same && eq < need))
-        out[lo + before + __popc(m & below) + min(eq, need)] = lo + i;
-      before += __popc(m);
-      equal += __popc(e);
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) {
+        const int eq = equal + __popc(e[n] & below);
+        if (is_more[n] || (is_same[n] && eq < need))
+          out[lo + before + __popc(m[n] & below) + min(eq, need)] = lo + i0 + 32 * n + lane;
+        before += __popc(m[n]);
+        equal += __popc(e[n]);
+      }
     }
     cta_sync();
   }
@@ -187,7 +224,7 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
 // vectors are read into registers, all threads waited for, and written; what is read
 // later lies behind all that has been written. CTAs share no bytes.
 constexpr int kKeepThreads = 256;
-constexpr int kKeepUnroll = 8;
+constexpr int kKeepUnroll = 4;
 constexpr int kKeepChunk = 1024;  // rows
 
 struct KeepRows {
@@ -218,10 +255,10 @@ __device__ __forceinline__ void move_rows(const KeepRows& rows, int count, char*
   }
 }
 
-__global__ void __launch_bounds__(kKeepThreads)
+__global__ void __launch_bounds__(kKeepThreads, 5)
 keep_kernel(const KeepArgs a, int shift, int* err) {
   __shared__ KeepRows rows;
-  __shared__ int sh_last, sh_moves;
+  __shared__ int sh_last, sh_first;
   pdl_wait();
   pdl_trigger();
   // the slice: of which tensor, head and bytes
@@ -243,20 +280,39 @@ keep_kernel(const KeepArgs a, int shift, int* err) {
       const int32_t id = table[pg];
       return id < 0 || id >= a.pages ? -1 : id * t.st.page + off * t.st.token;
     };
-    int last = 0;
-    if (tid == 0) sh_last = 0;
-    for (int i0 = 0; i0 < a.n; i0 += kKeepChunk) {
-      const int count = min(kKeepChunk, a.n - i0);
+    // the first row that moves and the last one of the list
+    if (tid == 0) sh_last = 0, sh_first = a.n;
+    cta_sync();
+    int last = 0, from0 = a.n;
+#pragma unroll 8
+    for (int i = tid; i < a.n; i += kKeepThreads) {
+      const int32_t x = kept[i];
+      if (x >= 0) {
+        last = i + 1;
+        if (x != i) from0 = min(from0, i);
+      }
+    }
+    last = __reduce_max_sync(0xFFFFFFFFu, last);
+    from0 = __reduce_min_sync(0xFFFFFFFFu, from0);
+    if ((tid & 31) == 0) {
+      atomicMax(&sh_last, last);
+      atomicMin(&sh_first, from0);
+    }
+    cta_sync();
+    last = sh_last;
+    from0 = sh_first;
+    if (blockIdx.x == 0 && tid == 0) {
+      a.new_lens[s] = first + (first >= 0 ? last : 0);
+      if (first < 0) record_error(err, kDevErrBadId);
+    }
+    for (int i0 = from0; i0 < last; i0 += kKeepChunk) {
+      const int count = min(kKeepChunk, last - i0);
       cta_sync();  // the chunk before has been moved
-      if (tid == 0) sh_moves = 0;
-      cta_sync();
-      bool moves = false;
 #pragma unroll
       for (int k = 0; k < kKeepChunk / kKeepThreads; ++k) {
         const int i = i0 + k * kKeepThreads + tid;
-        const int32_t from = i < a.n ? kept[i] : -1;
+        const int32_t from = i < last ? kept[i] : -1;
         int64_t src = -1, dst = -1;
-        if (from >= 0) last = i + 1;
         if (from >= 0 && from != i && first >= 0) {
           if (from > i && (int64_t)first + from < room) {
             src = place((int64_t)first + from);
@@ -265,31 +321,17 @@ keep_kernel(const KeepArgs a, int shift, int* err) {
           if (src < 0 || dst < 0) {
             src = -1;
             record_error(err, kDevErrBadId);
-          } else {
-            moves = true;
           }
         }
         rows.from[i - i0] = src;
         rows.to[i - i0] = dst;
       }
-      if (__any_sync(0xFFFFFFFFu, moves) && (tid & 31) == 0) sh_moves = 1;
       cta_sync();
-      if (!sh_moves) continue;
       switch (t.vec) {
         case 16: move_rows<uint4>(rows, count, base, bytes); break;
         case 4: move_rows<uint32_t>(rows, count, base, bytes); break;
         case 2: move_rows<uint16_t>(rows, count, base, bytes); break;
         default: move_rows<uint8_t>(rows, count, base, bytes); break;
-      }
-    }
-    if (blockIdx.x == 0) {
-      // the rows that the list leaves: up to its last entry that is one
-      last = __reduce_max_sync(0xFFFFFFFFu, last);
-      if ((tid & 31) == 0) atomicMax(&sh_last, last);
-      cta_sync();
-      if (tid == 0) {
-        a.new_lens[s] = first + (first >= 0 ? sh_last : 0);
-        if (first < 0) record_error(err, kDevErrBadId);
       }
     }
     cta_sync();
@@ -405,7 +447,7 @@ cudaError_t launch_cache_select(const SelectArgs& a, int* err, cudaStream_t s) {
   const int64_t room = (int64_t)a.width * a.page;
   const int staged = (int)(room < kMostStaged ? room : kMostStaged);
   static int smem_set[64] = {0};
-  const size_t smem = (size_t)(kBins * kCopies + staged) * 4;
+  const size_t smem = (size_t)(kCopy * kCopies + staged) * 4;
   cudaError_t e = ensure_dynamic_smem(select_kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
   return launch_kernel(true, select_kernel, dim3(a.kv_heads, a.S < 65535 ? a.S : 65535),

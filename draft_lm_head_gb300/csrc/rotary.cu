@@ -21,37 +21,66 @@ namespace lmhead {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kResident = 3;  // CTAs an SM, of 80 registers a thread
 
-template <int DT> struct Elem;
-template <> struct Elem<LMHEAD_BF16> {
-  using type = uint16_t;
-  static __device__ float load(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
-  static __device__ uint16_t store(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
+// V elements as one load or store: 16 bytes, or (V = 1) the element itself.
+template <int DT, int V> struct Pack;
+template <int DT> struct Pack<DT, 8> {  // of 16 bits each
+  uint4 v;
+  __device__ __forceinline__ void get(float* f) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (DT == LMHEAD_BF16) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[2 * i] = x.x;
+        f[2 * i + 1] = x.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (DT == LMHEAD_BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+      else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 };
-template <> struct Elem<LMHEAD_FP16> {
-  using type = uint16_t;
-  static __device__ float load(uint16_t x) { return __half2float(__ushort_as_half(x)); }
-  static __device__ uint16_t store(float f) { return __half_as_ushort(__float2half_rn(f)); }
+template <> struct Pack<LMHEAD_FP32, 4> {
+  float4 v;
+  __device__ __forceinline__ void get(float* f) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+  __device__ __forceinline__ void set(const float* f) { v = make_float4(f[0], f[1], f[2], f[3]); }
 };
-template <> struct Elem<LMHEAD_FP32> {
-  using type = float;
-  static __device__ float load(float x) { return x; }
-  static __device__ float store(float f) { return f; }
+template <> struct Pack<LMHEAD_FP32, 1> {
+  float v;
+  __device__ __forceinline__ void get(float* f) const { f[0] = v; }
+  __device__ __forceinline__ void set(const float* f) { v = f[0]; }
 };
-
-// V elements as one load or store (V = 1: the element itself).
-template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
-  T x[V];
+template <int DT> struct Pack<DT, 1> {
+  uint16_t v;
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = DT == LMHEAD_BF16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+  }
+  __device__ __forceinline__ void set(const float* f) {
+    v = DT == LMHEAD_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f[0]))
+                          : __half_as_ushort(__float2half_rn(f[0]));
+  }
 };
 
 // Thread x of a token: place u of a row (of `units`, the last of them copies
 // what does not turn) and the heads h0, h0 + groups, ...
 template <int DT, int V, bool PAIRS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, V == 1 ? 4 : kResident)
 rotary_kernel(const RotaryArgs a, int units, int groups) {
-  using E = Elem<DT>;
-  using T = typename E::type;
-  using P = Pack<T, V>;
+  using P = Pack<DT, V>;
+  constexpr int E = DT == LMHEAD_FP32 ? 4 : 2;  // bytes of an element
   pdl_wait();
   pdl_trigger();
   const int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -89,42 +118,42 @@ rotary_kernel(const RotaryArgs a, int units, int groups) {
       si[i] *= a.backward ? -a.magnitude : a.magnitude;
     }
   }
-  auto in_row = [&](int h) {
-    return h < a.heads ? static_cast<const T*>(a.q) + t * a.q_tok + h * a.q_head
-                       : static_cast<const T*>(a.k) + t * a.k_tok + (h - a.heads) * a.k_head;
-  };
-  auto out_row = [&](int h) {
-    return h < a.heads ? static_cast<T*>(a.qo) + t * a.qo_tok + h * a.qo_head
-                       : static_cast<T*>(a.ko) + t * a.ko_tok + (h - a.heads) * a.ko_head;
-  };
+  // (byte offsets of a token's first heads)
+  const char *q = static_cast<const char*>(a.q) + t * a.q_tok * E, *k = static_cast<const char*>(a.k) + t * a.k_tok * E;
+  char *qo = static_cast<char*>(a.qo) + t * a.qo_tok * E, *ko = static_cast<char*>(a.ko) + t * a.ko_tok * E;
   constexpr int N = 4;  // heads under way together
+#pragma unroll 1
   for (int h = h0; h < heads; h += N * groups) {
     P v0[N], v1[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int hn = h + n * groups;
       if (hn >= heads) break;
-      const T* src = in_row(hn);
-      v0[n] = *reinterpret_cast<const P*>(src + c0);
-      if (c1 >= 0) v1[n] = *reinterpret_cast<const P*>(src + c1);
+      const char* src = hn < a.heads ? q + hn * a.q_head * E : k + (hn - a.heads) * a.k_head * E;
+      v0[n] = *reinterpret_cast<const P*>(src + c0 * E);
+      if (c1 >= 0) v1[n] = *reinterpret_cast<const P*>(src + c1 * E);
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int hn = h + n * groups;
       if (hn >= heads) break;
       if (!copy) {
+        float f[2 * V];  // v0's, then v1's
+        v0[n].get(f);
+        v1[n].get(f + V);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          T& ra = PAIRS ? (2 * i < V ? v0[n].x[(2 * i) % V] : v1[n].x[(2 * i) % V]) : v0[n].x[i];
-          T& rb = PAIRS ? (2 * i + 1 < V ? v0[n].x[(2 * i + 1) % V] : v1[n].x[(2 * i + 1) % V]) : v1[n].x[i];
-          const float fa = E::load(ra), fb = E::load(rb);
-          ra = E::store(fmaf(fa, co[i], -(fb * si[i])));
-          rb = E::store(fmaf(fb, co[i], fa * si[i]));
+          float &fa = PAIRS ? f[2 * i] : f[i], &fb = PAIRS ? f[2 * i + 1] : f[V + i];
+          const float x = fa, y = fb;
+          fa = fmaf(x, co[i], -(y * si[i]));
+          fb = fmaf(y, co[i], x * si[i]);
         }
+        v0[n].set(f);
+        v1[n].set(f + V);
       }
-      T* dst = out_row(hn);
-      *reinterpret_cast<P*>(dst + c0) = v0[n];
-      if (c1 >= 0) *reinterpret_cast<P*>(dst + c1) = v1[n];
+      char* dst = hn < a.heads ? qo + hn * a.qo_head * E : ko + (hn - a.heads) * a.ko_head * E;
+      *reinterpret_cast<P*>(dst + c0 * E) = v0[n];
+      if (c1 >= 0) *reinterpret_cast<P*>(dst + c1 * E) = v1[n];
     }
   }
 }
@@ -148,7 +177,7 @@ cudaError_t launch_packs(const RotaryArgs& a, cudaStream_t s) {
 
 template <int DT>
 cudaError_t launch_typed(const RotaryArgs& a, cudaStream_t s) {
-  constexpr int V = 16 / (int)sizeof(typename Elem<DT>::type);
+  constexpr int V = DT == LMHEAD_FP32 ? 4 : 8;  // 16 bytes
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.qo) |
                        reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.ko);
   const int64_t st = a.q_tok | a.q_head | a.k_tok | a.k_head | a.qo_tok | a.qo_head | a.ko_tok | a.ko_head;

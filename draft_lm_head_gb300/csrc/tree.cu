@@ -13,8 +13,11 @@
 //     they change: the vocabulary is not read before the last token.
 // Then one token is drawn from w by inverse CDF. Either way the tokens that come
 // out are distributed as the target's.
-// Weights are fp32 (w - fl(fl(Z / Q) g) is rounded once each), masses and
-// running sums 64 bits or pairs of fp32 numbers.
+// Weights are fp32 (w - fl(fl(Z / Q) g) is rounded once each); masses, running sums and
+// what is compared are pairs of fp32 numbers, some 48 bits. (This GPU adds two fp64
+// numbers a cycle and SM, one after the other in some hundred cycles: with fp64 in their
+// place a draw took 12700 cycles in place of 3400, and sums made by every thread two
+// thirds of the time.)
 //
 // One cluster of CTAs a request. Its first CTA takes the walk: the candidates of the
 // node it stands on lie in shared memory, a rejection changes them all and sums up
@@ -22,8 +25,7 @@
 // memory to shared memory, where the changed weights replace what was read; the sums
 // meet in distributed shared memory and the CTA that has the draw finds its place.
 // Bound by latency: of dependent reads, one row of candidates a node, then the row of
-// p. This GPU adds two fp64 numbers a cycle and SM, so they are left to single warps
-// (summed up by every thread they took two thirds of the time).
+// p.
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_util.cuh"
@@ -35,6 +37,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kNodes = 64;      // of a request
+constexpr int kLoads = 4;       // of a thread under way together
 constexpr int kMaxRun = 1024;   // entries of p that a warp has in shared memory at a time
 
 // What is in shared memory: the candidates, then `chunk` entries of p (in their
@@ -65,9 +68,9 @@ inline Layout layout_of(int64_t n, int K, int S) {
 
 __device__ __forceinline__ float weight_of(float p) { return p > 0.f ? p : 0.f; }  // NaN: nothing
 
-__device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
-  double v;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
@@ -80,28 +83,55 @@ __device__ __forceinline__ int of_first(const int* p) {
   return ld_cluster_s32(tc::map_to_rank(tc::smem_addr(p), 0));
 }
 
-// (hi, lo) += x without a rounding of hi + lo but in lo.
-__device__ __forceinline__ void add_exact(float& hi, float& lo, float x) {
-  const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
-  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
-  hi = s;
+// ---- a sum of two fp32 numbers, the second below half a step of the first
+struct alignas(8) Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair joined(float hi, float lo) {  // |hi| >= |lo|
+  const float s = __fadd_rn(hi, lo);
+  return {s, __fsub_rn(lo, __fsub_rn(s, hi))};
 }
-// The sum of a warp's pairs, in every lane.
-__device__ __forceinline__ void warp_sum_exact(float& hi, float& lo) {
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
+  return joined(s, __fadd_rn(e, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Pair minus(Pair a) { return {-a.hi, -a.lo}; }
+__device__ __forceinline__ Pair times(Pair a, float b) {
+  const float p = __fmul_rn(a.hi, b);
+  return joined(p, __fmaf_rn(a.lo, b, __fmaf_rn(a.hi, b, -p)));
+}
+__device__ __forceinline__ bool less(Pair a, Pair b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
+// a / b rounded to fp32, b > 0.
+__device__ __forceinline__ float ratio(Pair a, Pair b) {
+  const float q = __fdiv_rn(a.hi, b.hi);
+  const Pair rest = add(a, minus(times(b, q)));
+  return __fadd_rn(q, __fdiv_rn(rest.hi, b.hi));
+}
+// (hi, lo) += x, not joined: lo gathers what hi rounds off.
+__device__ __forceinline__ void add_exact(Pair& a, float x) {
+  const float s = __fadd_rn(a.hi, x), b = __fsub_rn(s, a.hi);
+  a.lo = __fadd_rn(a.lo, __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
+  a.hi = s;
+}
+__device__ __forceinline__ Pair shuffled(Pair a, int lane) {
+  return {__shfl_sync(0xFFFFFFFFu, a.hi, lane), __shfl_sync(0xFFFFFFFFu, a.lo, lane)};
+}
+// The sum of a warp's pairs, in every lane (of the first `lanes` of them, a power of two).
+template <int LANES = 32> __device__ __forceinline__ Pair warp_sum_exact(Pair a) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float h = __shfl_xor_sync(0xFFFFFFFFu, hi, o), l = __shfl_xor_sync(0xFFFFFFFFu, lo, o);
-    add_exact(hi, lo, h);
-    lo = __fadd_rn(lo, l);
-  }
+  for (int o = LANES / 2; o > 0; o >>= 1)
+    a = add(a, {__shfl_xor_sync(0xFFFFFFFFu, a.hi, o), __shfl_xor_sync(0xFFFFFFFFu, a.lo, o)});
+  return a;
 }
-__device__ __forceinline__ double warp_scan_f64(double v, int lane) {  // up to and with the lane
+// The sum up to and with each lane.
+__device__ __forceinline__ Pair warp_scan_exact(Pair a, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double t = __shfl_up_sync(0xFFFFFFFFu, v, o);
-    if (lane >= o) v += t;
+    const Pair t = {__shfl_up_sync(0xFFFFFFFFu, a.hi, o), __shfl_up_sync(0xFFFFFFFFu, a.lo, o)};
+    if (lane >= o) a = add(t, a);
   }
-  return v;
+  return a;
 }
 
 struct Cands {
@@ -114,15 +144,12 @@ struct Walk {
   int32_t token[kNodes];
   float r[kNodes], px[kNodes];
   int hit[kNodes];
-  float2 part[kWarps];
-  float share;
-  int verdict;
+  Pair part[kWarps];
   // where it ended, for all CTAs
   int cur, count, changed, state;
   unsigned long long path;
 };
 enum State { kWalked, kIdle, kBad };
-enum Verdict { kNo, kYes, kNoCandidate };
 
 // Of candidates listed twice the first counts: the others lose their id. The table's
 // keys are -1 before and afterwards.
@@ -179,7 +206,7 @@ __device__ void walk_given(const TreeArgs& a, Walk& wk, int lane) {
   for (bool on = true; on;) {
     on = false;
     changed = false;
-    double Z = 1;
+    Pair Z = {1.f, 0.f};
     for (uint64_t kids = children(wk, cur, lane); kids; kids &= kids - 1) {
       const int x = __ffsll((long long)kids) - 1;
       const int32_t tok = wk.token[x];
@@ -190,8 +217,8 @@ __device__ void walk_given(const TreeArgs& a, Walk& wk, int lane) {
       // nothing is left of a token that was tried before
       const bool twin = (lane < x && wk.parent[lane] == cur && wk.token[lane] == tok) ||
                         (lane + 32 < x && wk.parent[lane + 32] == cur && wk.token[lane + 32] == tok);
-      const double w = __any_sync(0xFFFFFFFFu, twin) ? 0.0 : (double)wk.px[x];
-      if ((double)wk.r[x] * Z < w) {
+      const float w = __any_sync(0xFFFFFFFFu, twin) ? 0.f : wk.px[x];
+      if (less(times(Z, wk.r[x]), {w, 0.f})) {
         if (count == a.depth) {  // deeper than there is room for
           state = kBad;
           break;
@@ -202,7 +229,7 @@ __device__ void walk_given(const TreeArgs& a, Walk& wk, int lane) {
         on = true;
         break;
       }
-      Z = Z > w ? Z - w : 0;
+      Z = less({w, 0.f}, Z) ? add(Z, {-w, 0.f}) : Pair{0.f, 0.f};
       changed = true;
     }
     if (state == kBad) break;
@@ -230,70 +257,68 @@ __device__ void walk_drawn(const TreeArgs& a, Walk& wk, const Cands& c, int* tab
     const uint64_t all = children(wk, cur, lane);
     if (!all) break;
     const int64_t row = (int64_t)(base + cur);
-    for (int j = tid; j < a.K; j += kThreads) {
-      int32_t id = a.cand_ids[row * a.K + j];
-      const float g = weight_of(a.cand_q[row * a.K + j]);
-      if (id < 0 || id >= n) id = -1;
-      c.ids[j] = id;
-      c.g[j] = id < 0 ? 0.f : g;
-      c.w[j] = id < 0 ? 0.f : weight_of(a.p[row * n + id]);
-      for (uint64_t kids = all; kids; kids &= kids - 1) {
-        const int x = __ffsll((long long)kids) - 1;
-        if (wk.token[x] == id && id >= 0) atomicMin(&wk.hit[x], j);
+    for (int j0 = tid; j0 < a.K; j0 += kLoads * kThreads) {  // a few of a thread under way together
+      int32_t id[kLoads];
+      float g[kLoads], w[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int j = j0 + i * kThreads;
+        id[i] = j < a.K ? a.cand_ids[row * a.K + j] : -1;
+        g[i] = j < a.K ? a.cand_q[row * a.K + j] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        if (id[i] < 0 || id[i] >= n) id[i] = -1;
+        w[i] = id[i] < 0 ? 0.f : a.p[row * n + id[i]];
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int j = j0 + i * kThreads;
+        if (j >= a.K) break;
+        c.ids[j] = id[i];
+        c.g[j] = id[i] < 0 ? 0.f : weight_of(g[i]);
+        c.w[j] = weight_of(w[i]);
+        for (uint64_t kids = all; kids; kids &= kids - 1) {
+          const int x = __ffsll((long long)kids) - 1;
+          if (wk.token[x] == id[i] && id[i] >= 0) atomicMin(&wk.hit[x], j);
+        }
       }
     }
     cta_sync();
-    double Z = 1, Q = 1;  // (of warp 0)
+    Pair Z = {1.f, 0.f}, Q = {1.f, 0.f};  // the same in every thread
     int next = -1;
     for (uint64_t kids = all; kids; kids &= kids - 1) {
       const int x = __ffsll((long long)kids) - 1;
       const int hit = wk.hit[x];
-      if (warp == 0) {
-        int v = kNoCandidate;
-        float f = 0.f;
-        if (hit < a.K) {
-          v = (double)wk.r[x] * Z * (double)c.g[hit] < (double)c.w[hit] * Q ? kYes : kNo;
-          if (v == kNo && Q > 0) f = (float)(Z / Q);
-        }
-        if (lane == 0) {
-          wk.verdict = v;
-          wk.share = f;
-        }
-      }
-      cta_sync();
-      const int v = wk.verdict;
-      if (v == kNoCandidate || (v == kYes && count == a.depth)) {
+      if (hit == a.K) {  // no candidate of its parent's
         state = kBad;
         break;
       }
-      if (v == kYes) {
-        next = x;
+      const float gx = c.g[hit];
+      if (less(times(times(Z, wk.r[x]), gx), times(Q, c.w[hit]))) {
+        if (count == a.depth)  // deeper than there is room for
+          state = kBad;
+        else
+          next = x;
         break;
       }
-      const float f = wk.share;
+      const float f = Q.hi > 0.f ? ratio(Z, Q) : 0.f;
+      cta_sync();  // seen by all before it changes
       if (!changed) drop_repeats(c, a.K, table, slot_bits);
       changed = true;
-      float hi = 0.f, lo = 0.f;
+      Pair took = {0.f, 0.f};
       for (int j = tid; j < a.K; j += kThreads) {
-        const float w = c.w[j], took = fminf(w, __fmul_rn(f, c.g[j]));
-        c.w[j] = __fsub_rn(w, took);
-        add_exact(hi, lo, took);
+        const float w = c.w[j], t = fminf(w, __fmul_rn(f, c.g[j]));
+        c.w[j] = __fsub_rn(w, t);
+        add_exact(took, t);
+        if (j == hit) c.g[j] = 0.f;
       }
-      warp_sum_exact(hi, lo);
-      if (lane == 0) wk.part[warp] = make_float2(hi, lo);
+      took = warp_sum_exact(joined(took.hi, took.lo));
+      if (lane == 0) wk.part[warp] = took;
       cta_sync();
-      if (warp == 0) {
-        const float2 s = lane < kWarps ? wk.part[lane] : make_float2(0.f, 0.f);
-        hi = s.x;
-        lo = s.y;
-        warp_sum_exact(hi, lo);
-        const double took = (double)hi + (double)lo;
-        Z = Z > took ? Z - took : 0;
-        Q -= (double)c.g[hit];
-        __syncwarp();
-        if (lane == 0) c.g[hit] = 0.f;
-        __syncwarp();
-      }
+      took = warp_sum_exact<kWarps>(wk.part[lane % kWarps]);
+      Z = less(took, Z) ? add(Z, minus(took)) : Pair{0.f, 0.f};
+      Q = add(Q, {-gx, 0.f});
     }
     if (next < 0) break;
     ++count;
@@ -319,8 +344,8 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
   cand.w = cand.g - lay.cands;
   cand.ids = reinterpret_cast<int32_t*>(cand.w - lay.cands);
   __shared__ Walk wk;
-  __shared__ double seg[kWarps], seg_at[kWarps];
-  __shared__ double cta_total, sh_all, sh_off, sh_base;
+  __shared__ Pair seg[kWarps], seg_at[kWarps];  // each warp's sum, and the sum before it
+  __shared__ Pair cta_total, sh_all, sh_off, sh_base;
   __shared__ int cta_last, sh_pick, sh_last_rank;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)tc::cluster_ctarank(), ranks = lay.cluster;
@@ -396,11 +421,17 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
         cta_sync();
         if (quads) {  // (what a chunk begins at is a multiple of four)
           const float4* src = reinterpret_cast<const float4*>(row + at);
-#pragma unroll 4
-          for (int i = tid; i < len / 4; i += kThreads) {
-            const float4 v = src[i];
-            reinterpret_cast<float4*>(row_s)[i] =
-                make_float4(weight_of(v.x), weight_of(v.y), weight_of(v.z), weight_of(v.w));
+          constexpr int kQuads = 8;
+          for (int i0 = tid; i0 < len / 4; i0 += kQuads * kThreads) {
+            float4 v[kQuads];
+#pragma unroll
+            for (int k = 0; k < kQuads; ++k)
+              v[k] = i0 + k * kThreads < len / 4 ? src[i0 + k * kThreads] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kQuads; ++k)
+              if (i0 + k * kThreads < len / 4)
+                reinterpret_cast<float4*>(row_s)[i0 + k * kThreads] =
+                    make_float4(weight_of(v[k].x), weight_of(v[k].y), weight_of(v[k].z), weight_of(v[k].w));
           }
           for (int i = (len & ~3) + tid; i < len; i += kThreads) row_s[i] = weight_of(row[at + i]);
         } else {
@@ -420,29 +451,32 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
           if (i >= 0 && i < len) row_s[i] = 0.f;
         }
         cta_sync();
-        float hi = 0.f, lo = 0.f;
+        Pair sum[2] = {};
         int last = -1;
+        const int end = min(len, (warp + 1) * lay.run);
 #pragma unroll 4
-        for (int i = warp * lay.run + lane; i < min(len, (warp + 1) * lay.run); i += 32) {
+        for (int i = warp * lay.run + lane, odd = 0; i < end; i += 32, odd ^= 1) {
           const float w = row_s[i];
-          add_exact(hi, lo, w);
+          add_exact(sum[odd], w);
           if (w > 0.f) last = i;
         }
-        warp_sum_exact(hi, lo);
-        if (lane == 0) seg[warp] = (double)hi + (double)lo;
+        const Pair whole = warp_sum_exact(add(joined(sum[0].hi, sum[0].lo), joined(sum[1].hi, sum[1].lo)));
+        if (lane == 0) seg[warp] = whole;
         cta_sync();
         if (warp == 0) {
           // where each warp's run begins in the running sum
-          const double mine = lane < kWarps ? seg[lane] : 0.0;
-          const double to = warp_scan_f64(mine, lane), from = sh_base;
-          if (lane < kWarps) seg_at[lane] = from + (to - mine);
+          const Pair from = sh_base;
+          Pair mine = lane < kWarps ? seg[lane] : Pair{0.f, 0.f};
+          mine = warp_scan_exact(mine, lane);
+          const Pair before = shuffled(mine, lane > 0 ? lane - 1 : 0);
+          if (lane < kWarps) seg_at[lane] = lane > 0 ? add(from, before) : from;
           __syncwarp();
-          if (lane == kWarps - 1) sh_base = from + to;
+          if (lane == kWarps - 1) sh_base = add(from, mine);
         }
         cta_sync();
         return last;
       };
-      if (tid == 0) cta_last = -1, sh_pick = -1, sh_base = 0;
+      if (tid == 0) cta_last = -1, sh_pick = -1, sh_base = {0.f, 0.f};
       int last = -1;
       for (int64_t at = v0; at < v1; at += lay.chunk) {
         const int l = load(at, (int)min((int64_t)lay.chunk, v1 - at));
@@ -454,61 +488,65 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
       if (tid == 0) cta_total = sh_base;
       cta_sync();
       tc::cluster_sync();
-      if (warp == 0) {
-        double t = 0;
+      if (warp == 0) {  // the sums of the CTAs before this one and of all
+        Pair t = {0.f, 0.f};
         int l = -1;
         if (lane < ranks) {
-          t = ld_cluster_f64(tc::map_to_rank(tc::smem_addr(&cta_total), (uint32_t)lane));
+          const float2 v = ld_cluster_f32x2(tc::map_to_rank(tc::smem_addr(&cta_total), (uint32_t)lane));
+          t = {v.x, v.y};
           l = ld_cluster_s32(tc::map_to_rank(tc::smem_addr(&cta_last), (uint32_t)lane));
         }
-        const double to = warp_scan_f64(t, lane);
+        const Pair to = warp_scan_exact(t, lane);
+        const Pair before = shuffled(to, rank > 0 ? rank - 1 : 0);
         const uint32_t some = __ballot_sync(0xFFFFFFFFu, l >= 0);
-        if (lane == rank) sh_off = to - t;
         if (lane == 31) {
+          sh_off = rank > 0 ? before : Pair{0.f, 0.f};
           sh_all = to;
           sh_last_rank = 31 - __clz(some);
         }
       }
       cta_sync();
-      const double all = sh_all, off = sh_off;
-      const bool none = !(all > 0);
+      const Pair all = sh_all, off = sh_off;
+      const bool none = !(all.hi > 0.f);
       if (!none) {
-        const double target = (double)u * all;
-        const bool past = !(target < all);  // u * total rounded up to the total
-        const double end = rank + 1 < ranks ? off + cta_total : all;
-        if (past ? rank == sh_last_rank : off <= target && target < end) {
+        const Pair target = times(all, u);
+        const bool past = !less(target, all);  // u * total rounded up to the total
+        const Pair end = rank + 1 < ranks ? add(off, cta_total) : all;
+        if (past ? rank == sh_last_rank : !less(target, off) && less(target, end)) {
           if (!past) {
             cta_sync();
-            if (tid == 0) sh_base = 0;
+            if (tid == 0) sh_base = {0.f, 0.f};
             for (int64_t at = v0; at < v1; at += lay.chunk) {
               const int len = (int)min((int64_t)lay.chunk, v1 - at);
               if (v1 - v0 > lay.chunk) load(at, len);  // a single chunk is still there
-              const double mine = off + seg_at[warp];
-              if (mine <= target && target < mine + seg[warp]) {
+              const Pair mine = add(off, seg_at[warp]);
+              if (!less(target, mine) && less(target, add(mine, seg[warp]))) {
                 // a lane sums neighbours (each lane beginning elsewhere, for the banks), and
                 // those of the lane that passes the target are looked at 32 at a time
                 const int many = lay.run / 32, first = warp * lay.run + lane * many;
-                float hi = 0.f, lo = 0.f;
+                Pair own = {0.f, 0.f};
                 for (int i = 0, e = lane % many; i < many; ++i, e = e + 1 == many ? 0 : e + 1)
-                  if (first + e < len) add_exact(hi, lo, row_s[first + e]);
-                const double own = (double)hi + (double)lo, run = warp_scan_f64(own, lane);
-                const uint32_t over = __ballot_sync(0xFFFFFFFFu, own > 0 && mine + run > target);
+                  if (first + e < len) add_exact(own, row_s[first + e]);
+                own = joined(own.hi, own.lo);
+                const Pair run = add(mine, warp_scan_exact(own, lane));
+                const uint32_t over = __ballot_sync(0xFFFFFFFFu, own.hi > 0.f && less(target, run));
                 if (over) {
                   const int k = __ffs(over) - 1, from = warp * lay.run + k * many;
-                  double under = mine + __shfl_sync(0xFFFFFFFFu, run - own, k);
+                  const Pair prior = shuffled(run, k > 0 ? k - 1 : 0);
+                  Pair under = k > 0 ? prior : mine;
                   int pick = -1;
                   for (int i = 0; i < many; i += 32) {
                     const int e = from + i + lane;
                     const float w = i + lane < many && e < len ? row_s[e] : 0.f;
-                    const double sum = warp_scan_f64(w, lane);
+                    const Pair sum = add(under, warp_scan_exact({w, 0.f}, lane));
                     const uint32_t some = __ballot_sync(0xFFFFFFFFu, w > 0.f);
-                    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, w > 0.f && under + sum > target);
+                    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, w > 0.f && less(target, sum));
                     if (some) pick = from + i + 31 - __clz(some);  // where none passes: the last
                     if (hit) {
                       pick = from + i + __ffs(hit) - 1;
                       break;
                     }
-                    under += __shfl_sync(0xFFFFFFFFu, sum, 31);
+                    under = shuffled(sum, 31);
                   }
                   if (lane == 0) atomicMax(&sh_pick, (int)(at + pick));
                 }
