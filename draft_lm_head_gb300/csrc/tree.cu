@@ -38,7 +38,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kNodes = 64;      // of a request
 constexpr int kLoads = 4;       // of a thread under way together
-constexpr int kMaxRun = 1024;   // entries of p that a warp has in shared memory at a time
+// Entries of p that a warp has in shared memory at a time: fewer where two CTAs are to
+// share an SM.
+constexpr int kMaxRun = 2048, kMaxRunShared = 1024;
 
 // What is in shared memory: the candidates, then `chunk` entries of p (in their
 // place, while the walk lasts, a table of 2^slot_bits keys and places).
@@ -56,7 +58,8 @@ inline Layout layout_of(int64_t n, int K, int S) {
   while (l.cluster > 2 && (int64_t)l.cluster * S > 2 * (sm_count() > 0 ? sm_count() : 1)) l.cluster /= 2;
   const int64_t per = ((n + l.cluster - 1) / l.cluster + 3) / 4 * 4;
   const int64_t run = ((per + kWarps - 1) / kWarps + 31) / 32 * 32;
-  l.run = (int)(run < kMaxRun ? run : kMaxRun);
+  const int most = (int64_t)l.cluster * S > (sm_count() > 0 ? sm_count() : 1) ? kMaxRunShared : kMaxRun;
+  l.run = (int)(run < most ? run : most);
   l.chunk = l.run * kWarps;
   l.cands = (K + 3) / 4 * 4;
   l.slot_bits = 6;
@@ -151,11 +154,18 @@ struct Walk {
 };
 enum State { kWalked, kIdle, kBad };
 
-// Of candidates listed twice the first counts: the others lose their id. The table's
-// keys are -1 before and afterwards.
+// (What runs once or twice a launch takes its time mostly for its instructions, which
+// come from memory the first time: such loops are not unrolled.)
+__device__ void clear_table(int* key, int slot_bits) {  // keys -1, places INT32_MAX
+#pragma unroll 1
+  for (int i = threadIdx.x; i < 2 << slot_bits; i += kThreads) key[i] = i < 1 << slot_bits ? -1 : INT32_MAX;
+}
+
+// Of candidates listed twice the first counts: the others lose their id. The table is
+// clear before and afterwards.
 __device__ void drop_repeats(const Cands& c, int K, int* key, int slot_bits) {
   const int slots = 1 << slot_bits;
-  int* at = key + slots;  // INT32_MAX, likewise
+  int* at = key + slots;
   auto slot_of = [&](int32_t id) {  // where id is, or its place
     uint32_t h = ((uint32_t)id * 2654435761u) >> (32 - slot_bits);
     for (int probe = 0; probe < slots; ++probe) {
@@ -165,29 +175,18 @@ __device__ void drop_repeats(const Cands& c, int K, int* key, int slot_bits) {
     }
     return (int)h;
   };
-  int slot[kSelectMaxK / kThreads];
-#pragma unroll
-  for (int i = 0; i < kSelectMaxK / kThreads; ++i) {
-    const int j = i * kThreads + threadIdx.x;
-    slot[i] = -1;
-    if (j < K && c.ids[j] >= 0) {
-      slot[i] = slot_of(c.ids[j]);
-      atomicMin(&at[slot[i]], j);
-    }
-  }
+#pragma unroll 1
+  for (int j = threadIdx.x; j < K; j += kThreads)
+    if (c.ids[j] >= 0) atomicMin(&at[slot_of(c.ids[j])], j);
   cta_sync();
-#pragma unroll
-  for (int i = 0; i < kSelectMaxK / kThreads; ++i) {
-    const int j = i * kThreads + threadIdx.x;
-    if (slot[i] >= 0 && at[slot[i]] != j) {
+#pragma unroll 1
+  for (int j = threadIdx.x; j < K; j += kThreads)
+    if (c.ids[j] >= 0 && at[slot_of(c.ids[j])] != j) {
       c.ids[j] = -1;
       c.w[j] = c.g[j] = 0.f;
     }
-  }
   cta_sync();
-#pragma unroll
-  for (int i = 0; i < kSelectMaxK / kThreads; ++i)
-    if (slot[i] >= 0) key[slot[i]] = -1, at[slot[i]] = INT32_MAX;
+  clear_table(key, slot_bits);
 }
 
 // The nodes whose parent is c, c < kNodes.
@@ -248,7 +247,7 @@ __device__ void walk_drawn(const TreeArgs& a, Walk& wk, const Cands& c, int* tab
                            int base) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t n = a.n;
-  for (int i = tid; i < 2 << slot_bits; i += kThreads) table[i] = i < 1 << slot_bits ? -1 : INT32_MAX;
+  clear_table(table, slot_bits);
   int cur = 0, count = 0, state = kWalked;
   unsigned long long path = 1;
   bool changed = false;
@@ -523,10 +522,13 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
               if (!less(target, mine) && less(target, add(mine, seg[warp]))) {
                 // a lane sums neighbours (each lane beginning elsewhere, for the banks), and
                 // those of the lane that passes the target are looked at 32 at a time
-                const int many = lay.run / 32, first = warp * lay.run + lane * many;
+                const int many = lay.run / 32, first = warp * lay.run + lane * many, from0 = lane % many;
                 Pair own = {0.f, 0.f};
-                for (int i = 0, e = lane % many; i < many; ++i, e = e + 1 == many ? 0 : e + 1)
-                  if (first + e < len) add_exact(own, row_s[first + e]);
+#pragma unroll 4
+                for (int i = 0; i < many; ++i) {
+                  const int e = first + (from0 + i < many ? from0 + i : from0 + i - many);
+                  if (e < len) add_exact(own, row_s[e]);
+                }
                 own = joined(own.hi, own.lo);
                 const Pair run = add(mine, warp_scan_exact(own, lane));
                 const uint32_t over = __ballot_sync(0xFFFFFFFFu, own.hi > 0.f && less(target, run));
