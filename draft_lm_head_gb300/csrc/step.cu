@@ -69,6 +69,7 @@ int lmhead_rotary(int dtype, const void* q, int64_t q_tok, int64_t q_head, const
   };
   if (!apart(oq_tok, oq_head, heads) || (k && !apart(ok_tok, ok_head, kv_heads)))
     return LMHEAD_ERR_SHAPE;
+  if (out_q == out_k) return LMHEAD_ERR_SHAPE;  // one tensor, turned twice
   const int size = dtype == LMHEAD_FP32 ? 4 : 2;
   if (!aligned(q, size) || !aligned(k, size) || !aligned(out_q, size) || !aligned(out_k, size) ||
       !aligned(turns, 8))

@@ -19,7 +19,6 @@
 // many query tiles a unit may be cut between CTAs; each leaves its sums in the
 // scratch and a second launch adds them up in order, so no result depends on which
 // CTA came first.
-#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -158,13 +157,30 @@ __device__ void make_plan(const WeightArgs& a, C& ctl, int tile_tok, int* err) {
   if (tid == 0) ctl.bad = 0;
   cta_sync();
   long long target = 0;
-  // pass 0 sums up, pass 1 finds the request in which the share begins
+  // The request in which the target lies, `before` it and of cost c, says where.
+  auto locate = [&](int s, const Req& r, long long before, long long c) {
+    if (target < before || target >= before + c) return;
+    long long rem = target - before;
+    const int each = kGroups * (1 + r.qt);
+    int p = (int)min((long long)full_units(a, r), rem / each);
+    rem -= (long long)p * each;
+    for (; p < r.np; ++p) {
+      const int w = cost_of(a, r, p, tile_tok);
+      if (rem < w) break;
+      rem -= w;
+    }
+    ctl.s0 = s;
+    ctl.p0 = p;
+    ctl.off0 = (int)rem;
+  };
+  // pass 0 sums up, and pass 1 finds the request in which the share begins (at once where
+  // every thread has one request)
   for (int pass = 0; pass < 2; ++pass) {
-    long long base = 0;
+    long long base = 0, c = 0, before = 0;
+    Req r = {};
     for (int s0 = 0; s0 < a.S; s0 += kThreads) {
       const int s = s0 + tid;
-      Req r = {};
-      long long c = 0;
+      c = 0;
       if (s < a.S) {
         const int b = a.cu[s], e = a.cu[s + 1];
         if (b < 0 || e < b || e > a.T) {
@@ -184,44 +200,34 @@ __device__ void make_plan(const WeightArgs& a, C& ctl, int tile_tok, int* err) {
       }
       if (lane == 31) warp_sum[warp] = incl;
       cta_sync();
-      long long before = base + incl - c;
+      before = base + incl - c;
       for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += warp_sum[w];
         base += warp_sum[w];
       }
-      if (pass == 1 && before <= target && target < before + c) {
-        long long rem = target - before;
-        const int each = kGroups * (1 + r.qt);
-        int p = (int)min((long long)full_units(a, r), rem / each);
-        rem -= (long long)p * each;
-        for (; p < r.np; ++p) {
-          const int w = cost_of(a, r, p, tile_tok);
-          if (rem < w) break;
-          rem -= w;
-        }
-        ctl.s0 = s;
-        ctl.p0 = p;
-        ctl.off0 = (int)rem;
-      }
+      if (pass == 1) locate(s, r, before, c);
       cta_sync();
     }
-    if (pass == 0) {
-      const long long all = ctl.bad ? 0 : base * a.kv_heads;
-      // no CTA's share is empty before another's that is not
-      const long long parts = min((long long)gridDim.x, all), c = blockIdx.x;
-      long long lo = all, hi = all;
-      if (c < parts) {
-        lo = all / parts * c + all % parts * c / parts;
-        hi = all / parts * (c + 1) + all % parts * (c + 1) / parts;
-      }
-      if (tid == 0) {
-        ctl.lo = lo;
-        ctl.hi = hi;
-        ctl.hk0 = base > 0 ? (int)(lo / base) : 0;
-        if (ctl.bad && blockIdx.x == 0) record_error(err, kDevErrBadId);
-      }
-      if (lo >= hi) break;  // the same in every thread
-      target = lo - lo / base * base;
+    if (pass == 1) break;
+    const long long all = ctl.bad ? 0 : base * a.kv_heads;
+    // no CTA's share is empty before another's that is not
+    const long long parts = min((long long)gridDim.x, all), x = blockIdx.x;
+    long long lo = all, hi = all;
+    if (x < parts) {
+      lo = all / parts * x + all % parts * x / parts;
+      hi = all / parts * (x + 1) + all % parts * (x + 1) / parts;
+    }
+    if (tid == 0) {
+      ctl.lo = lo;
+      ctl.hi = hi;
+      ctl.hk0 = base > 0 ? (int)(lo / base) : 0;
+      if (ctl.bad && blockIdx.x == 0) record_error(err, kDevErrBadId);
+    }
+    if (lo >= hi) break;  // the same in every thread
+    target = lo - lo / base * base;
+    if (a.S <= kThreads) {
+      locate(tid, r, before, c);
+      break;
     }
   }
   cta_sync();

@@ -72,6 +72,7 @@ def clib():
     (-2, dict(oq_tok=64, oq_head=64)),
     (-2, dict(oq=OK, oq_tok=1024)),                # in place with other strides
     (-2, dict(oq=OK + 64)),                        # over part of the input
+    (-2, dict(oq=OK + (1 << 32))),                 # q and k to one place
     (-3, dict(q=OK + 1)), (-3, dict(turns=OK + 4)),
 ])
 def test_refusals(clib, want, kw):
