@@ -34,12 +34,14 @@ from .serving import _DTYPES, _cuda, _dense, _heads_tensor
 def _strides(t: torch.Tensor):
     """Strides, with those of dimensions of one (which mean nothing) as in a
     contiguous tensor."""
-    st = list(t.stride())
-    at = 1
-    for i in range(t.dim() - 1, -1, -1):
-        if t.shape[i] == 1:
+    st, shape = t.stride(), t.shape
+    if 1 not in shape:
+        return st
+    st, at = list(st), 1
+    for i in range(len(shape) - 1, -1, -1):
+        if shape[i] == 1:
             st[i] = at
-        at = max(at, st[i] * t.shape[i])
+        at = max(at, st[i] * shape[i])
     return st
 
 
@@ -130,6 +132,9 @@ def verify_tree(p: torch.Tensor, tokens: torch.Tensor, parent: torch.Tensor, cu:
     return said, path, accepted
 
 
+_Caches = ctypes.c_int64 * 40  # up to 8 addresses, strides of pages, tokens and heads, and row sizes
+
+
 def cache_keep(caches: Sequence[torch.Tensor], table: torch.Tensor, kept: torch.Tensor,
                first: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
@@ -149,25 +154,27 @@ def cache_keep(caches: Sequence[torch.Tensor], table: torch.Tensor, kept: torch.
     if len(lead) != 3:
         raise ValueError("caches: expected pages x page_size x kv_heads (x dim)")
     pages, P, kv_heads = lead
-    arr = ctypes.c_int64 * count
-    base, page, tok, head, row = arr(), arr(), arr(), arr(), arr()
+    arr = _Caches()
     for i, t in enumerate(caches):
-        if t.dim() not in (3, 4) or t.shape[:3] != lead or t.device != dev:
+        shape = t.shape
+        if len(shape) not in (3, 4) or shape[:3] != lead or t.device != dev:
             raise ValueError(f"caches[{i}]: expected {tuple(lead)} (x dim) on {dev}")
-        size = t.element_size()
-        st = _strides(t)
-        if t.dim() == 4 and st[3] != 1:
-            raise TypeError(f"caches[{i}]: expected a contiguous last dimension")
-        base[i] = t.data_ptr()
-        page[i], tok[i], head[i] = st[0] * size, st[1] * size, st[2] * size
-        row[i] = size * (t.shape[3] if t.dim() == 4 else 1)
+        size, st = t.element_size(), _strides(t)
+        if len(shape) == 4:
+            if st[3] != 1:
+                raise TypeError(f"caches[{i}]: expected a contiguous last dimension")
+            arr[32 + i] = size * shape[3]
+        else:
+            arr[32 + i] = size
+        arr[i] = t.data_ptr()
+        arr[8 + i], arr[16 + i], arr[24 + i] = st[0] * size, st[1] * size, st[2] * size
     i32 = torch.int32
     want = (S, n) if kept.dim() == 2 else (S, kv_heads, n)
     if out is None:
         out = result((S,), i32, dev, stream)
-    at = ctypes.addressof
+    at = ctypes.addressof(arr)
     check(load().lmhead_cache_keep(
-        count, at(base), at(page), at(tok), at(head), at(row), pages, P, kv_heads,
+        count, at, at + 64, at + 128, at + 192, at + 256, pages, P, kv_heads,
         _dense(table, i32, (S, table.shape[1]), dev, "table"), table.shape[1],
         _dense(kept, i32, want, dev, "kept"), n, kept.dim() == 3,
         _dense(first, i32, (S,), dev, "first"), S, _dense(out, i32, (S,), dev, "out"),
