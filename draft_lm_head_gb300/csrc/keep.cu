@@ -29,7 +29,10 @@ __device__ __forceinline__ void split_pos(uint32_t pos, int page, int shift, int
 // memory and are counted by digits from the top (11, 11 and 10 bits, while the digit
 // of the last one to stay holds others that do not) in four copies, as weights crowd
 // in few exponents; a last pass writes the positions that pass, each warp those of
-// a run of its own behind the counts of the runs before.
+// a run of its own behind the counts of the runs before. Bound by latency for one
+// list (4096 tokens x 8 heads: 13 us alone, four passes over shared memory and the waits
+// between them) and by shared memory's atomic adds for long ones (16 lists of up to 32768
+// x 8 heads 38 us; a search bit by bit over keys held in registers took 44).
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelLoads = 8;
@@ -223,6 +226,12 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
 // chunk: where the rows lie is worked out once for each (a thread a row), then their
 // vectors are read into registers, all threads waited for, and written; what is read
 // later lies behind all that has been written. CTAs share no bytes.
+// Bound by memory: 16 prompts' rows, 4097 of up to 32768 a head (504 MB read and written),
+// 96 us, 5.3 TB/s, a chunk's reads and writes following one another; by latency for short
+// lists: 19 us for 2048 of 4096 rows of one request, reads behind those of list and table.
+// A slice of many rows is up to 256 bytes of each; with slices of 64 and 128 bytes, 2 or 8
+// vectors a thread, 3, 4 or 6 CTAs an SM, or batches read while the one before is written,
+// the 16 prompts' eviction took 149 to 199 us in place of 145.
 constexpr int kKeepThreads = 256;
 constexpr int kKeepUnroll = 4;
 constexpr int kKeepChunk = 1024;  // rows

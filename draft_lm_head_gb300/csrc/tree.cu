@@ -25,7 +25,10 @@
 // memory to shared memory, where the changed weights replace what was read; the sums
 // meet in distributed shared memory and the CTA that has the draw finds its place.
 // Bound by latency: of dependent reads, one row of candidates a node, then the row of
-// p.
+// p. Measured (device time, graphs replayed; with the launches that keep the path's rows
+// and give pages back): one tree of 10 given nodes over 128256 entries 19 us; 8 of 10
+// drawn nodes, 1572 candidates a place, over 201088 38 us; 64 of 60 over 128256 86 us, where
+// the longest walk of the batch bounds it (0.4 instructions a cycle, 8 % of the bandwidth).
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_util.cuh"

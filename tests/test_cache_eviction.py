@@ -216,7 +216,15 @@ def test_weights_against_oracle(dtype, lens, new, H, Hk, D, P, mask, window, dec
 @pytest.mark.parametrize("lens,new,H,Hk,D,P,dtype,mask,window", [
     ([700, 30], [300, 513], 8, 2, 128, 64, "bfloat16", "causal", 0), ([2049], [1], 4, 1, 64, 32, "float16", "causal", 0),
     ([0], [600], 12, 1, 128, 16, "float16", "causal", 0), ([1500], [200], 4, 4, 64, 128, "bfloat16", "causal", 700),
-    ([900] * 3, [64] * 3, 16, 2, 128, 64, "bfloat16", "tree", 0), ([3000, 1], [2, 400], 5, 1, 64, 16, "bfloat16", "causal", 1)])
+    ([900] * 3, [64] * 3, 16, 2, 128, 64, "bfloat16", "tree", 0), ([3000, 1], [2, 400], 5, 1, 64, 16, "bfloat16", "causal", 1),
+    # a CTA goes through many tiles of queries
+    ([2100, 900], [2048, 1500], 32, 8, 128, 64, "bfloat16", "causal", 0), ([500], [2500], 16, 2, 64, 128, "float16", "causal", 900),
+    ([37], [1900], 24, 1, 128, 32, "float16", "causal", 0),
+    # more requests than a CTA has threads
+    ([i * 37 % 300 for i in range(700)], [1] * 700, 8, 2, 128, 16, "bfloat16", "causal", 0),
+    ([i * 53 % 600 for i in range(1300)], [1 + i % 3 for i in range(1300)], 4, 1, 64, 32, "float16", "tree", 0),
+    ([i * 41 % 200 for i in range(700)], [33] * 700, 8, 1, 64, 16, "bfloat16", "causal", 90)],
+    ids=lambda x: f"x{len(x)}" if isinstance(x, list) and len(x) > 9 else None)
 def test_longer_weights(lens, new, H, Hk, D, P, dtype, mask, window):
     """Many tiles of keys and of queries, against fp64 on the GPU's own lse."""
     import torch
@@ -350,6 +358,18 @@ def test_weights_streams_graphs_and_determinism():
         g.replay()
     torch.cuda.synchronize()
     assert eq(a, want) and eq(b, want)
+    # two calls at once, of different sizes
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    d = _weights_case([5000], [1], 8, 2, 128, 64, "bfloat16", 12)
+    other = (d["q"], d["kc"], d["table"], d["lens"], d["cu"], torch.full((1, 8), 9.0, device="cuda"))
+    wanted = L.cache_weights(*other, d["w"].clone())
+    x, y = [c["w"].clone() for _ in range(4)], [d["w"].clone() for _ in range(4)]
+    torch.cuda.synchronize()
+    for i in range(4):
+        L.cache_weights(*args, x[i], stream=one)
+        L.cache_weights(*other, y[i], stream=two)
+    torch.cuda.synchronize()
+    assert all(eq(i, want) for i in x) and all(eq(i, wanted) for i in y)
     for bad in (dict(lse=lse[:5]), dict(lse=lse.double()), dict(w=c["w"][:-1]), dict(w=c["w"].half()), dict(q=c["q"].float())):
         k = dict(q=c["q"], lse=lse, w=c["w"])
         k.update(bad)
