@@ -69,11 +69,7 @@ int lmhead_rotary(int dtype, const void* q, int64_t q_tok, int64_t q_head, const
   };
   if (!apart(oq_tok, oq_head, heads) || (k && !apart(ok_tok, ok_head, kv_heads)))
     return LMHEAD_ERR_SHAPE;
-  if (out_q == out_k) return LMHEAD_ERR_SHAPE;  // one tensor, turned twice
   const int size = dtype == LMHEAD_FP32 ? 4 : 2;
-  if (!aligned(q, size) || !aligned(k, size) || !aligned(out_q, size) || !aligned(out_k, size) ||
-      !aligned(turns, 8))
-    return LMHEAD_ERR_ALIGN;
   // in place, or to somewhere else: no thread may write what another is to read
   auto same_or_apart = [&](const void* in, int64_t tok, int64_t head, const void* out, int64_t otok,
                            int64_t ohead, int h) {
@@ -82,6 +78,30 @@ int lmhead_rotary(int dtype, const void* q, int64_t q_tok, int64_t q_head, const
   };
   if (!same_or_apart(q, q_tok, q_head, out_q, oq_tok, oq_head, heads)) return LMHEAD_ERR_SHAPE;
   if (k && !same_or_apart(k, k_tok, k_head, out_k, ok_tok, ok_head, kv_heads)) return LMHEAD_ERR_SHAPE;
+  // q and k may lie in one tensor, their places among one another's, but share none
+  auto clear = [&](const void* x, int64_t x_tok, int64_t x_head, int x_h, const void* y, int64_t y_tok,
+                   int64_t y_head, int y_h) {
+    if (!meet(x, span(x_tok, x_head, x_h) * size, y, span(y_tok, y_head, y_h) * size)) return true;
+    const int64_t bytes = (int64_t)(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x));
+    if (bytes % size != 0) return false;
+    // blocks of x_n and y_n elements, repeated every `step`, y's begin `bytes` behind x's
+    auto between = [&](int64_t x_n, int64_t y_n, int64_t step) {
+      int64_t d = bytes / size % step;
+      if (d < 0) d += step;
+      return x_n <= d && d + y_n <= step;
+    };
+    return (T > 1 && x_tok == y_tok &&
+            between((x_h - 1) * x_head + dim, (y_h - 1) * y_head + dim, x_tok)) ||
+           (x_h > 1 && y_h > 1 && x_head == y_head &&
+            between((T - 1) * x_tok + dim, (T - 1) * y_tok + dim, x_head));
+  };
+  if (k && (!clear(out_q, oq_tok, oq_head, heads, out_k, ok_tok, ok_head, kv_heads) ||
+            !clear(out_q, oq_tok, oq_head, heads, k, k_tok, k_head, kv_heads) ||
+            !clear(out_k, ok_tok, ok_head, kv_heads, q, q_tok, q_head, heads)))
+    return LMHEAD_ERR_SHAPE;
+  if (!aligned(q, size) || !aligned(k, size) || !aligned(out_q, size) || !aligned(out_k, size) ||
+      !aligned(turns, 8))
+    return LMHEAD_ERR_ALIGN;
   RotaryArgs a = {};
   a.dtype = dtype;
   a.q = q;
@@ -122,7 +142,11 @@ int lmhead_verify_tree(const float* p, int64_t n, const int32_t* tokens, const i
   if (n < 1 || n > INT32_MAX || S < 1 || S > kMaxRequests || T < 1 || depth < 0 ||
       depth >= kTreeMaxNodes || (cand_ids && K < 1))
     return LMHEAD_ERR_SHAPE;
+  const int64_t out_bytes = 4ll * S * (depth + 1);
   if (cand_ids && K > kSelectMaxK) return LMHEAD_ERR_UNSUPPORTED;
+  if (meet(out_tokens, out_bytes, out_path, out_bytes) || meet(out_tokens, out_bytes, out_accepted, 4ll * S) ||
+      meet(out_path, out_bytes, out_accepted, 4ll * S))
+    return LMHEAD_ERR_SHAPE;
   TreeArgs a = {};
   a.p = p;
   a.n = n;

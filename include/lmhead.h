@@ -563,7 +563,8 @@ int lmhead_beam_reorder(const int32_t* parent, int S, int beams, int k, int coun
  *             modulo 1, so that angles of far positions lose nothing.
  *   interleaved  0: pair i is (i, i + rot / 2); else (2 i, 2 i + 1).
  *   out_q, out_k  the tensors themselves (same strides), or others that do not meet
- *             them. No two places of a result may coincide.
+ *             them. No two places of a result may coincide, nor one with a place of
+ *             the other result or its input (q and k may be parts of one tensor).
  * Arithmetic is fp32, the result is rounded once. Whole loads of 16 bytes where
  * addresses, strides and the parts of a head allow them, else element by element.
  */
@@ -605,7 +606,7 @@ int lmhead_rotary(int dtype, const void* q, int64_t q_tok, int64_t q_head, const
  *   out_path  S x (depth + 1) int32: the accepted path's nodes from the root on,
  *             then -1 (lmhead_cache_keep's `kept`).
  *   out_accepted  S int32: drafts accepted; -1 for a request that was refused or
- *             has no tokens (its entries are all -1).
+ *             has no tokens (its entries are all -1). The results do not meet.
  * At most 64 nodes a request. More of them, a cu that decreases or leaves [0, T], a
  * tried token outside [0, n) or, with cand_ids, not among its parent's candidates,
  * and a path deeper than depth give -1 too and record LMHEAD_ERR_DEVICE_CHECK.

@@ -474,6 +474,30 @@ def test_keep_against_oracle(dtype, D, lens, P, Hk, n, per_head):
 
 
 @pytest.mark.gpu
+def test_pages_far_apart():
+    """Caches of pages with offsets past 2^31 elements and 2^32 bytes: the same bits as of pages
+    side by side, from the weights to the rows moved."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    c = _weights_case([700, 90], [3, 1], 8, 2, 128, 64, "bfloat16", 21)
+    lse = torch.full((4, 8), 20.0, device="cuda")
+    pages, P, Hk, D = c["kc"].shape
+    far = lambda t, step: torch.empty(pages * step, dtype=t.dtype, device="cuda").as_strided(t.shape, (step, *t.stride()[1:])).copy_(t)
+    step = (1 << 32) // pages + 4096 & -4096
+    assert (pages - 1) * step > 2 ** 31
+    out = []
+    for kc, w in ((c["kc"].clone(), c["w"].clone()), (far(c["kc"], step), far(c["w"], step // 2))):
+        L.cache_weights(c["q"], kc, c["table"], c["lens"], c["cu"], lse, w, decay=0.5)
+        lens = c["lens"] + c["cu"].diff()
+        kept = L.cache_select(w, c["table"], lens, 64, 2, 16)
+        out.append([L.cache_keep([kc, w], c["table"], kept), kept, kc, w])
+    assert L.last_device_error() == 0
+    for a, b in zip(*out):
+        assert np.array_equal(_n64(a), _n64(b), equal_nan=True)
+
+
+@pytest.mark.gpu
 def test_keep_bad_lists():
     import torch
     from gpu_util import lib

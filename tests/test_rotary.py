@@ -73,6 +73,8 @@ def clib():
     (-2, dict(oq=OK, oq_tok=1024)),                # in place with other strides
     (-2, dict(oq=OK + 64)),                        # over part of the input
     (-2, dict(oq=OK + (1 << 32))),                 # q and k to one place
+    (-2, dict(oq=OK + (1 << 32) - 1024 * 3)),      # a result that begins in the other one
+    (-2, dict(oq=OK + (1 << 30) - 1024)),          # a result over the other's input
     (-3, dict(q=OK + 1)), (-3, dict(turns=OK + 4)),
 ])
 def test_refusals(clib, want, kw):
@@ -82,6 +84,16 @@ def test_refusals(clib, want, kw):
     assert clib.lmhead_rotary(a["dtype"], a["q"], a["q_tok"], a["q_head"], a["k"], 128, 64, a["pos"], a["turns"], a["T"], a["H"],
                               a["Hk"], a["dim"], a["rot"], 0, 0, a["m"], a["oq"], a["oq_tok"], a["oq_head"], a["ok"], 128, 64,
                               None) == want
+
+
+@pytest.mark.parametrize("k,heads,clear", [
+    (512 * 2, 2, True), (512 * 2, 4, True), (512 * 2, 5, False), (511 * 2, 2, False), (512 * 2 + 1, 2, False), (-256 * 2, 4, True),
+    (-256 * 2, 5, False), (768 * 3 * 2 + 512 * 2, 4, True), (768 * 3 * 2 + 448 * 2, 4, False), (0, 1, False)])
+def test_parts_of_one_tensor(clib, k, heads, clear):
+    """8 query heads and k's, of one row of 768 elements a token, both in place: a call whose
+    tensors are clear of one another gets as far as the check of alignment, which it fails."""
+    assert clib.lmhead_rotary(0, OK, 768, 64, OK + k, 768, 64, OK, OK + 4, 4, 8, heads, 64, 64, 0, 0, 1.0, OK, 768, 64, OK + k, 768, 64,
+                              None) == (-3 if clear else -2)
 
 
 def test_binding_takes_cuda_tensors_only():
@@ -168,6 +180,25 @@ def test_backward_is_the_gradient():
         g = L.rotary(dy, None, pos, turns, interleaved=inter, magnitude=1.5, backward=True)[0]
         # a step along all elements at once changes sum(y) by the sum of its gradient
         assert abs((y[0] - y[1]).sum().item() - g.double().sum().item()) <= 1e-4
+
+
+@pytest.mark.gpu
+def test_tokens_far_apart():
+    """Offsets past 2^31 elements and 2^32 bytes."""
+    import torch
+    from draft_lm_head_gb300 import prep
+    from gpu_util import lib
+    L = lib()
+    turns = torch.from_numpy(prep.rotary_turns(64)).cuda()
+    pos = torch.tensor([5, 70, 9], dtype=torch.int32, device="cuda")
+    step = (1 << 30) + 8
+    base = torch.empty(2 * step + 512, dtype=torch.bfloat16, device="cuda")
+    q, k = base.as_strided((3, 4, 64), (step, 64, 1)), base[256:].as_strided((3, 2, 64), (step, 128, 1))
+    q.copy_(torch.randn(3, 4, 64, device="cuda"))
+    k.copy_(torch.randn(3, 2, 64, device="cuda"))
+    want = L.rotary(q.contiguous(), k.contiguous(), pos, turns)
+    L.rotary(q, k, pos, turns)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
 
 
 @pytest.mark.gpu

@@ -77,14 +77,14 @@ def clib():
 
 @pytest.mark.parametrize("want,kw", [
     (-1, dict(p=None)), (-1, dict(tokens=None)), (-1, dict(ids=OK)), (-1, dict(path=None)), (-1, dict(u=None)),
-    (-2, dict(n=0)), (-2, dict(n=1 << 31)), (-2, dict(S=0)), (-2, dict(T=0)), (-2, dict(depth=-1)), (-2, dict(depth=64)),
+    (-2, dict(n=0)), (-2, dict(n=1 << 31)), (-2, dict(S=0)), (-2, dict(T=0)), (-2, dict(depth=-1)), (-2, dict(depth=64)), (-2, dict(path=2 * OK + 28)), (-2, dict(path=3 * OK - 4)),
     (-2, dict(ids=OK, q=OK, K=0)), (-5, dict(ids=OK, q=OK, K=4097)), (-2, dict(S=70000)),
 ])
 def test_refusals(clib, want, kw):
-    a = dict(p=OK, n=100, tokens=OK, u=OK, ids=None, q=None, K=8, S=2, T=4, depth=3, path=OK)
+    a = dict(p=OK, n=100, tokens=OK, u=OK, ids=None, q=None, K=8, S=2, T=4, depth=3, path=4 * OK)
     a.update(kw)
     assert clib.lmhead_verify_tree(a["p"], a["n"], a["tokens"], OK, OK, None, OK, a["u"], a["ids"], a["q"], a["K"], a["S"], a["T"],
-                                   a["depth"], OK, a["path"], OK, None) == want
+                                   a["depth"], 2 * OK, a["path"], 3 * OK, None) == want
 
 
 def test_binding_takes_cuda_tensors_only():
@@ -269,6 +269,27 @@ def test_chain_agrees_with_verify_chain():
                                 dev(c["ids"][at[:, :-1]], torch.int32), dev(c["q"][at[:, :-1]], torch.float32),
                                 dev(c["r"][at[:, 1:]], torch.float32), dev(np.repeat(c["u"][:, None], Kd + 1, 1), torch.float32))
     assert torch.equal(acc, count) and torch.equal(said, tok)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("drawn", [False, True])
+def test_rows_behind_the_first_billions(drawn):
+    """The last rows of a p with more than 2^31 entries."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    rng = np.random.default_rng(10)
+    n, T, m = 200001, 10800, 12
+    assert T * n > 2 ** 31
+    c = _case(rng, [m], n, 40, drawn, 3)
+    p = torch.full((T, n), 0.5, device="cuda")
+    p[T - m:] = torch.tensor(c["p"], device="cuda")
+    i32 = lambda x: torch.tensor(np.concatenate([np.zeros((T - m,) + x.shape[1:], dtype=x.dtype), x]), dtype=torch.int32, device="cuda")
+    f32 = lambda x: torch.tensor(np.concatenate([np.zeros((T - m,) + x.shape[1:], dtype=x.dtype), x]), dtype=torch.float32, device="cuda")
+    cu = torch.tensor([T - m, T], dtype=torch.int32, device="cuda")
+    got = L.verify_tree(p, i32(c["tokens"]), i32(c["parent"]), cu, f32(c["r"]), torch.tensor(c["u"], device="cuda"), m,
+                        cand_ids=i32(c["ids"]) if drawn else None, cand_q=f32(c["q"]) if drawn else None)
+    _compare(c, got, drawn, m)
 
 
 @pytest.mark.gpu
