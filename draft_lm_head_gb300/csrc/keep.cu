@@ -226,8 +226,8 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
 // chunk: where the rows lie is worked out once for each (a thread a row), then their
 // vectors are read into registers, all threads waited for, and written; what is read
 // later lies behind all that has been written. CTAs share no bytes.
-// Bound by memory: 16 prompts' rows, 4097 of up to 32768 a head (504 MB read and written),
-// 96 us, 5.3 TB/s, a chunk's reads and writes following one another; by latency for short
+// Bound by memory: 16 prompts' rows, 4097 of up to 32768 a head (540 MB read and written),
+// 96 us, 5.6 TB/s, a chunk's reads and writes following one another; by latency for short
 // lists: 19 us for 2048 of 4096 rows of one request, reads behind those of list and table.
 // A slice of many rows is up to 256 bytes of each; with slices of 64 and 128 bytes, 2 or 8
 // vectors a thread, 3, 4 or 6 CTAs an SM, or batches read while the one before is written,
