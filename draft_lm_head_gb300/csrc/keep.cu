@@ -29,13 +29,14 @@ __device__ __forceinline__ void split_pos(uint32_t pos, int page, int shift, int
 // memory and are counted by digits from the top (11, 11 and 10 bits, while the digit
 // of the last one to stay holds others that do not) in four copies, as weights crowd
 // in few exponents; a last pass writes the positions that pass, each warp those of
-// a run of its own behind the counts of the runs before. Bound by latency for one
+// a run of its own behind the counts of the runs before. Where a page's weights of a head
+// lie side by side they are read four at a time, page and place looked up once for them. Bound by latency for one
 // list (4096 tokens x 8 heads: 13 us alone, four passes over shared memory and the waits
 // between them) and by shared memory's atomic adds for long ones (16 lists of up to 32768
 // x 8 heads 38 us; a search bit by bit over keys held in registers took 44).
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelLoads = 8;
+constexpr int kSelLoads = 8, kSelQuads = 4;
 constexpr int kBins = 2048, kCopies = 4, kCopy = kBins + 8;  // (copies begin in other banks)
 constexpr int kMostStaged = 48 * 1024 - kCopy * kCopies;  // keys; those behind are read again
 
@@ -44,7 +45,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 __global__ void __launch_bounds__(kSelThreads)
-select_kernel(const SelectArgs a, int shift, int staged, int* err) {
+select_kernel(const SelectArgs a, int shift, int staged, int quads, int* err) {
   extern __shared__ __align__(16) int hist[];  // kCopies counts of each bin, then the keys
   uint32_t* keys = reinterpret_cast<uint32_t*>(hist + kCopy * kCopies);
   int* mine = hist + (threadIdx.x & (kCopies - 1)) * kCopy;
@@ -88,9 +89,24 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
       const int32_t id = page_at(j, off);
       return key_at(id, off);
     };
-    const int kept_keys = min(staged, hi - lo);
-    auto key = [&](int i) { return i < kept_keys ? keys[i] : key_of(lo + i); };  // of position lo + i
-    const int total = hi - lo;
+    // keys by their place behind `base`; those from `begin` to `end` are chosen from
+    const int base = quads ? lo & ~3 : lo, begin = lo - base, end = hi - base;
+    const int kept_keys = min(staged, end);
+    auto key = [&](int i) { return i < kept_keys ? keys[i] : key_of(base + i); };
+    auto each = [&](auto f) {
+      if (end <= kept_keys) {
+#pragma unroll 4
+        for (int i = 4 * tid; i < end; i += 4 * kSelThreads) {
+          const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+          if (i >= begin) f(k.x);
+          if (i + 1 >= begin && i + 1 < end) f(k.y);
+          if (i + 2 >= begin && i + 2 < end) f(k.z);
+          if (i + 3 >= begin && i + 3 < end) f(k.w);
+        }
+      } else {
+        for (int i = begin + tid; i < end; i += kSelThreads) f(key(i));
+      }
+    };
     uint32_t prefix = 0, mask = 0;
     int top = 21, bits = 11;
     for (;;) {
@@ -98,35 +114,62 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
         reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
       cta_sync();
       if (mask == 0) {  // the first time the keys are read, several of a thread under way together
-        for (int i0 = tid; i0 < total; i0 += kSelLoads * kSelThreads) {
-          int32_t id[kSelLoads];
-          int off[kSelLoads];
-          uint32_t k[kSelLoads];
+        if (quads) {
+          for (int i0 = 4 * tid; i0 < end; i0 += 4 * kSelQuads * kSelThreads) {
+            int32_t id[kSelQuads];
+            int off[kSelQuads];
+            float4 w[kSelQuads];
 #pragma unroll
-          for (int n = 0; n < kSelLoads; ++n) {
-            id[n] = -1;
-            if (i0 + n * kSelThreads < total) {
-              id[n] = page_at(lo + i0 + n * kSelThreads, off[n]);
-              bad |= id[n] < 0;
+            for (int n = 0; n < kSelQuads; ++n) {
+              const int i = i0 + 4 * n * kSelThreads;
+              id[n] = i < end ? page_at(base + i, off[n]) : -1;
+              bad |= i < end && id[n] < 0;
+            }
+#pragma unroll
+            for (int n = 0; n < kSelQuads; ++n)
+              if (id[n] >= 0) w[n] = *reinterpret_cast<const float4*>(weights + id[n] * a.ws.page + off[n] * 4ll);
+#pragma unroll
+            for (int n = 0; n < kSelQuads; ++n) {
+              const int i = i0 + 4 * n * kSelThreads;
+              if (i >= end) break;
+              uint4 k = {0u, 0u, 0u, 0u};
+              if (id[n] >= 0) k = {weight_key(w[n].x), weight_key(w[n].y), weight_key(w[n].z), weight_key(w[n].w)};
+              if (i < kept_keys) *reinterpret_cast<uint4*>(keys + i) = k;
+              if (i >= begin) atomicAdd(&mine[k.x >> top], 1);
+              if (i + 1 >= begin && i + 1 < end) atomicAdd(&mine[k.y >> top], 1);
+              if (i + 2 >= begin && i + 2 < end) atomicAdd(&mine[k.z >> top], 1);
+              if (i + 3 >= begin && i + 3 < end) atomicAdd(&mine[k.w >> top], 1);
             }
           }
+        } else {
+          for (int i0 = tid; i0 < end; i0 += kSelLoads * kSelThreads) {
+            int32_t id[kSelLoads];
+            int off[kSelLoads];
+            uint32_t k[kSelLoads];
 #pragma unroll
-          for (int n = 0; n < kSelLoads; ++n) k[n] = key_at(id[n], off[n]);
+            for (int n = 0; n < kSelLoads; ++n) {
+              id[n] = -1;
+              if (i0 + n * kSelThreads < end) {
+                id[n] = page_at(lo + i0 + n * kSelThreads, off[n]);
+                bad |= id[n] < 0;
+              }
+            }
 #pragma unroll
-          for (int n = 0; n < kSelLoads; ++n) {
-            const int i = i0 + n * kSelThreads;
-            if (i >= total) break;
-            if (i < kept_keys) keys[i] = k[n];
-            atomicAdd(&mine[k[n] >> top], 1);
+            for (int n = 0; n < kSelLoads; ++n) k[n] = key_at(id[n], off[n]);
+#pragma unroll
+            for (int n = 0; n < kSelLoads; ++n) {
+              const int i = i0 + n * kSelThreads;
+              if (i >= end) break;
+              if (i < kept_keys) keys[i] = k[n];
+              atomicAdd(&mine[k[n] >> top], 1);
+            }
           }
         }
         if (bad) record_error(err, kDevErrBadId);
       } else {
-#pragma unroll 4
-        for (int i = tid; i < total; i += kSelThreads) {
-          const uint32_t k = key(i);
+        each([&](uint32_t k) {
           if ((k & mask) == prefix) atomicAdd(&mine[(k >> top) & ((1u << bits) - 1u)], 1);
-        }
+        });
       }
       cta_sync();
       // the digit in which the need-th largest lies: counts from the top, two bins a thread
@@ -175,15 +218,21 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
       top -= bits;
     }
     // keys above prefix (in the digits looked at) stay, and the first `need` equal to it
-    const int run = ((total + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-    const int r0 = min(total, warp * run), r1 = min(total, r0 + run);
+    const int run = ((end + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+    const int r1 = min(end, (warp + 1) * run), r0 = max(begin, min(r1, warp * run));
     int more = 0, same = 0;
-#pragma unroll 4
-    for (int i = r0 + lane; i < r1; i += 32) {
-      const uint32_t k = key(i) & mask;
-      more += k > prefix;
-      same += k == prefix;
-    }
+    auto count = [&](auto key) {
+#pragma unroll 8
+      for (int i = r0 + lane; i < r1; i += 32) {
+        const uint32_t k = key(i) & mask;
+        more += k > prefix;
+        same += k == prefix;
+      }
+    };
+    if (r1 <= kept_keys)
+      count([&](int i) { return keys[i]; });
+    else
+      count(key);
     more = __reduce_add_sync(0xFFFFFFFFu, more);
     same = __reduce_add_sync(0xFFFFFFFFu, same);
     cta_sync();
@@ -191,27 +240,44 @@ select_kernel(const SelectArgs a, int shift, int staged, int* err) {
     cta_sync();
     int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? more_w[lane] : 0);
     int equal = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? same_w[lane] : 0);
+    const uint32_t below = (1u << lane) - 1u;
     constexpr int kAhead = 4;  // chunks of 32 looked at together
-    for (int i0 = r0; i0 < r1; i0 += 32 * kAhead) {
-      uint32_t m[kAhead], e[kAhead];
-      bool is_more[kAhead], is_same[kAhead];
+    int32_t* to = out + lo + before + min(equal, need);
+    // of a run whose equal keys all stay, or none, what passes is one comparison
+    auto place = [&](auto key, uint32_t least) {
+      for (int i0 = r0; i0 < r1; i0 += 32 * kAhead) {
+        uint32_t m[kAhead];
+        bool in[kAhead];
 #pragma unroll
-      for (int n = 0; n < kAhead; ++n) {
-        const int i = i0 + 32 * n + lane;
-        const uint32_t k = i < r1 ? key(i) & mask : 0u;
-        is_more[n] = i < r1 && k > prefix;
-        is_same[n] = i < r1 && k == prefix;
-        m[n] = __ballot_sync(0xFFFFFFFFu, is_more[n]);
-        e[n] = __ballot_sync(0xFFFFFFFFu, is_same[n]);
+        for (int n = 0; n < kAhead; ++n) {
+          const int i = i0 + 32 * n + lane;
+          in[n] = i < r1 && (key(i) & mask) >= least;
+          m[n] = __ballot_sync(0xFFFFFFFFu, in[n]);
+        }
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) {
+          if (in[n]) to[__popc(m[n] & below)] = base + i0 + 32 * n + lane;
+          to += __popc(m[n]);
+        }
       }
-      const uint32_t below = (1u << lane) - 1u;
-#pragma unroll
-      for (int n = 0; n < kAhead; ++n) {
-        const int eq = equal + __popc(e[n] & below);
-        if (is_more[n] || (is_same[n] && eq < need))
-          out[lo + before + __popc(m[n] & below) + min(eq, need)] = lo + i0 + 32 * n + lane;
-        before += __popc(m[n]);
-        equal += __popc(e[n]);
+    };
+    const bool all = equal + same <= need, none = equal >= need;
+    if (all || (none && prefix + ~mask != 0xFFFFFFFFu)) {
+      const uint32_t least = all ? prefix : (prefix | ~mask) + 1;
+      if (r1 <= kept_keys)
+        place([&](int i) { return keys[i]; }, least);
+      else
+        place(key, least);
+    } else {
+      for (int i0 = r0; i0 < r1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < r1 ? key(i) & mask : 0u;
+        const bool is_more = i < r1 && k > prefix, is_same = i < r1 && k == prefix;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, is_more), e = __ballot_sync(0xFFFFFFFFu, is_same);
+        const int eq = equal + __popc(e & below);
+        if (is_more || (is_same && eq < need)) out[lo + before + __popc(m & below) + min(eq, need)] = base + i;
+        before += __popc(m);
+        equal += __popc(e);
       }
     }
     cta_sync();
@@ -454,13 +520,15 @@ inline int shift_of(int page) {  // log2 of a power of two, else -1
 
 cudaError_t launch_cache_select(const SelectArgs& a, int* err, cudaStream_t s) {
   const int64_t room = (int64_t)a.width * a.page;
-  const int staged = (int)(room < kMostStaged ? room : kMostStaged);
+  const int staged = (int)(room < kMostStaged ? (room + 3) / 4 * 4 : kMostStaged);
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(a.weights) | (uintptr_t)a.ws.page | (uintptr_t)a.ws.head;
+  const int quads = a.ws.token == 4 && a.page % 4 == 0 && (bits & 15) == 0;
   static int smem_set[64] = {0};
   const size_t smem = (size_t)(kCopy * kCopies + staged) * 4;
   cudaError_t e = ensure_dynamic_smem(select_kernel, smem, smem_set);
   if (e != cudaSuccess) return e;
   return launch_kernel(true, select_kernel, dim3(a.kv_heads, a.S < 65535 ? a.S : 65535),
-                       dim3(kSelThreads), smem, s, a, shift_of(a.page), staged, err);
+                       dim3(kSelThreads), smem, s, a, shift_of(a.page), staged, quads, err);
 }
 
 cudaError_t launch_cache_keep(KeepArgs a, int* err, cudaStream_t s) {
