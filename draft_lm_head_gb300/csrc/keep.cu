@@ -30,10 +30,11 @@ __device__ __forceinline__ void split_pos(uint32_t pos, int page, int shift, int
 // of the last one to stay holds others that do not) in four copies, as weights crowd
 // in few exponents; a last pass writes the positions that pass, each warp those of
 // a run of its own behind the counts of the runs before. Where a page's weights of a head
-// lie side by side they are read four at a time, page and place looked up once for them. Bound by latency for one
-// list (4096 tokens x 8 heads: 13 us alone, four passes over shared memory and the waits
-// between them) and by shared memory's atomic adds for long ones (16 lists of up to 32768
-// x 8 heads 38 us; a search bit by bit over keys held in registers took 44).
+// lie side by side they are read four at a time, page and place looked up once for them. Bound by
+// latency for one list (4096 tokens x 8 heads: 13 us alone, passes over shared memory and
+// the waits between them), by instructions for long ones (16 lists of up to 32768 x 8 heads:
+// 38 us one by one, 21 by fours; eight copies of the counts 4 us more; keys in registers
+// and a search bit by bit 44).
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelLoads = 8, kSelQuads = 4;
@@ -293,11 +294,11 @@ select_kernel(const SelectArgs a, int shift, int staged, int quads, int* err) {
 // vectors are read into registers, all threads waited for, and written; what is read
 // later lies behind all that has been written. CTAs share no bytes.
 // Bound by memory: 16 prompts' rows, 4097 of up to 32768 a head (540 MB read and written),
-// 96 us, 5.6 TB/s, a chunk's reads and writes following one another; by latency for short
-// lists: 19 us for 2048 of 4096 rows of one request, reads behind those of list and table.
-// A slice of many rows is up to 256 bytes of each; with slices of 64 and 128 bytes, 2 or 8
-// vectors a thread, 3, 4 or 6 CTAs an SM, or batches read while the one before is written,
-// the 16 prompts' eviction took 149 to 199 us in place of 145.
+// 96 us, 5.6 TB/s, rows of 256 bytes in no order; by latency for short lists. More in flight
+// does not help: an eviction of the 16 prompts took 128 us as it is, 136 to 156 with rings of
+// 12 to 48 KB in shared memory written while the next rows come, 131 and 140 with three
+// and two rows a thread, 131 with loads that do not stay in caches; and, of 145 then, 149
+// to 199 with slices of 64 and 128 bytes, 8 rows a thread, 3 or 6 CTAs an SM.
 constexpr int kKeepThreads = 256;
 constexpr int kKeepUnroll = 4;
 constexpr int kKeepChunk = 1024;  // rows
@@ -533,7 +534,9 @@ cudaError_t launch_cache_select(const SelectArgs& a, int* err, cudaStream_t s) {
 
 cudaError_t launch_cache_keep(KeepArgs a, int* err, cudaStream_t s) {
   // Short lists are moved in whole rows, long ones in slices of 256 bytes, or fewer
-  // down to 64 where there are too few of them to fill the GPU.
+  // down to 64 where there are too few of them to fill the GPU, to 32 where they do not
+  // reach every SM (2048 of 4096 rows of one request, 8 heads of 256 bytes: with them the
+  // eviction takes 23 us in place of 25, with 16 bytes 26).
   int slice = a.n > 64 ? 256 : kKeepThreads * 16;
   const int64_t want = 4ll * (sm_count() > 0 ? sm_count() : 1);
   auto slices_of = [&](int width) {
@@ -542,6 +545,7 @@ cudaError_t launch_cache_keep(KeepArgs a, int* err, cudaStream_t s) {
     return n * a.kv_heads;
   };
   while (a.n > 64 && slice > 64 && slices_of(slice) * a.S < want) slice /= 2;
+  while (a.n > 64 && slice > 32 && slices_of(slice) * a.S < want / 4) slice /= 2;
   int64_t slices = 0;
   for (int i = 0; i < a.count; ++i) {
     KeepTensor& t = a.t[i];
