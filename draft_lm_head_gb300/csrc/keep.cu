@@ -31,9 +31,9 @@ __device__ __forceinline__ void split_pos(uint32_t pos, int page, int shift, int
 // in few exponents; a last pass writes the positions that pass, each warp those of
 // a run of its own behind the counts of the runs before. Where a page's weights of a head
 // lie side by side they are read four at a time, page and place looked up once for them. Bound by
-// latency for one list (4096 tokens x 8 heads: 13 us alone, passes over shared memory and
+// latency for one list (4096 tokens x 8 heads: 11 us alone, passes over shared memory and
 // the waits between them), by instructions for long ones (16 lists of up to 32768 x 8 heads:
-// 38 us one by one, 21 by fours; eight copies of the counts 4 us more; keys in registers
+// 38 us one by one, 22 by fours; eight copies of the counts 4 us more; keys in registers
 // and a search bit by bit 44).
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
