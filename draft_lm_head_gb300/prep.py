@@ -162,8 +162,10 @@ def rotary_turns(rot: int, base: float = 10000.0, scaling: Optional[str] = None,
             # the (real) index of the pair that turns so many times
             def at(turns):
                 return rot * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
-            first, last = max(0.0, math.floor(at(high))), min(rot / 2 - 1.0, math.ceil(at(low)))
-            keep = 1 - (i - first) / max(last - first, 1e-3)
+            # from the last (whole) index of at least `high` turns to the first of at most
+            # `low`, whether there are pairs there or not
+            first, last = math.floor(at(high)), math.ceil(at(low))
+            keep = 1 - (i - first) / (last - first)
         keep = np.clip(keep, 0.0, 1.0)
         w = w * keep + w / factor * (1 - keep)
     elif scaling not in (None, "base"):

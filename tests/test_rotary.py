@@ -41,6 +41,26 @@ def test_frequencies():
             prep.rotary_turns(**bad)
 
 
+@pytest.mark.parametrize("rot,base,factor,original,low,high", [
+    (128, 10000.0, 4.0, 131072, 1.0, 32.0),  # the slowest pair turns 2.4 times
+    (128, 10000.0, 8.0, 65536, 1.0, 4.0), (64, 10000.0, 16.0, 10 ** 6, 1.0, 32.0),
+    (128, 10000.0, 8.0, 100, 1.0, 32.0),     # and the fastest 15.9 times
+    (128, 500000.0, 8.0, 8192, 1.0, 4.0), (2, 10000.0, 2.0, 100, 1.0, 32.0)])
+def test_ramps_past_the_pairs(rot, base, factor, original, low, high):
+    """Pair by pair against the definition: the ramp runs between the whole indices that turn
+    `high` times or more and `low` times or fewer, found by counting, wherever they lie."""
+    from draft_lm_head_gb300 import prep
+    w = lambda i: base ** (-2 * i / rot)
+    turns = lambda i: original * w(i) / (2 * np.pi)
+    first = max(i for i in range(-3 * rot, 3 * rot) if turns(i) >= high)
+    last = min(i for i in range(-3 * rot, 3 * rot) if turns(i) <= low)
+    assert first >= 0 or last >= 0
+    got = prep.rotary_turns(rot, base, "ramp", factor, original, low, high).view(np.uint64).astype(np.float64) / 2.0 ** 64 * 2 * np.pi
+    for i in range(rot // 2):
+        k = min(max((last - i) / (last - first), 0.0), 1.0)
+        assert np.isclose(got[i], w(i) * k + w(i) / factor * (1 - k), rtol=1e-12), i
+
+
 def test_oracle_by_hand():
     """A quarter turn a position: (1, 2) -> (-2, 1) -> (-1, -2); its transpose the
     other way; in the far, whole turns drop out."""
