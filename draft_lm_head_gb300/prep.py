@@ -159,6 +159,8 @@ def rotary_turns(rot: int, base: float = 10000.0, scaling: Optional[str] = None,
         if scaling == "wavelength":
             keep = (original * w / (2 * math.pi) - low) / (high - low)
         else:
+            if not base > 1:
+                raise ValueError(f"base={base} must be above 1 for a ramp: frequencies fall along it")
             # the (real) index of the pair that turns so many times
             def at(turns):
                 return rot * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))

@@ -61,6 +61,14 @@ def test_ramps_past_the_pairs(rot, base, factor, original, low, high):
         assert np.isclose(got[i], w(i) * k + w(i) / factor * (1 - k), rtol=1e-12), i
 
 
+@pytest.mark.parametrize("base", [1.0, 0.5])
+def test_ramp_needs_falling_frequencies(base):
+    from draft_lm_head_gb300 import prep
+    with pytest.raises(ValueError, match="base"):
+        prep.rotary_turns(8, base, "ramp", 4.0)
+    prep.rotary_turns(8, base, "linear", 4.0)
+
+
 def test_oracle_by_hand():
     """A quarter turn a position: (1, 2) -> (-2, 1) -> (-1, -2); its transpose the
     other way; in the far, whole turns drop out."""
