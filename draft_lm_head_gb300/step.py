@@ -117,6 +117,8 @@ def verify_tree(p: torch.Tensor, tokens: torch.Tensor, parent: torch.Tensor, cu:
         if cand_ids is None or cand_q is None or cand_ids.dim() != 2:
             raise ValueError("cand_ids, cand_q: are given together, nodes x candidates")
         K = cand_ids.shape[1]
+        if K < 1:  # (no address would tell them from none given)
+            raise ValueError("cand_ids, cand_q: expected one candidate or more")
     W = depth + 1
     if out is None:
         out = (result((S, W), i32, dev, stream), result((S, W), i32, dev, stream), result((S,), i32, dev, stream))

@@ -99,3 +99,10 @@ def test_other_shapes_and_types(name):
     for a, x in wrong:
         with pytest.raises((ValueError, TypeError)):
             call(dict(ok, **{a: x.as_subclass(On)}))
+
+
+def test_candidates_of_no_column():
+    """An empty tensor has no address: it must not pass for children that are given."""
+    ok, calls = _calls()
+    with pytest.raises(ValueError, match="candidate"):
+        calls["verify_tree"][0](dict(ok, ids=_i(3, 0), cq=_t(3, 0)))
