@@ -346,9 +346,10 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
   cand.w = cand.g - lay.cands;
   cand.ids = reinterpret_cast<int32_t*>(cand.w - lay.cands);
   __shared__ Walk wk;
-  __shared__ Pair seg[kWarps], seg_at[kWarps];  // each warp's sum, and the sum before it
-  __shared__ Pair cta_total, sh_all, sh_off, sh_base;
-  __shared__ int cta_last, sh_pick, sh_last_rank;
+  __shared__ Pair seg[kWarps], seg_at[kWarps + 1];  // each warp's sum, and the sum before it
+  __shared__ Pair cta_total, sh_target, sh_off, sh_base;
+  __shared__ int cta_last, sh_pick, sh_owner;
+  __shared__ bool sh_past;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)tc::cluster_ctarank(), ranks = lay.cluster;
   const int64_t n = a.n;
@@ -414,7 +415,7 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
     const int64_t per = ((n + ranks - 1) / ranks + 3) / 4 * 4;
     const int64_t v0 = min(n, rank * per), v1 = min(n, v0 + per);
     const bool quads = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
-    const float u = a.u[s];
+    const float u = a.u[s] < 0.f ? 0.f : a.u[s];  // (a NaN stays one, and passes nothing)
     for (int pass = 0; pass < 2; ++pass) {
       const bool patch = changed && pass == 0;  // what is left may be nothing: then p itself
       // a chunk of the row into shared memory, as it is left, and each warp's sum of
@@ -471,7 +472,7 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
           Pair mine = lane < kWarps ? seg[lane] : Pair{0.f, 0.f};
           mine = warp_scan_exact(mine, lane);
           const Pair before = shuffled(mine, lane > 0 ? lane - 1 : 0);
-          if (lane < kWarps) seg_at[lane] = lane > 0 ? add(from, before) : from;
+          if (lane <= kWarps) seg_at[lane] = lane > 0 ? add(from, before) : from;
           __syncwarp();
           if (lane == kWarps - 1) sh_base = add(from, mine);
         }
@@ -500,32 +501,42 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
         }
         const Pair to = warp_scan_exact(t, lane);
         const Pair before = shuffled(to, rank > 0 ? rank - 1 : 0);
+        const Pair target = times(shuffled(to, 31), u);
         const uint32_t some = __ballot_sync(0xFFFFFFFFu, l >= 0);
+        const uint32_t over = __ballot_sync(0xFFFFFFFFu, l >= 0 && less(target, to));
         if (lane == 31) {
           sh_off = rank > 0 ? before : Pair{0.f, 0.f};
-          sh_all = to;
-          sh_last_rank = 31 - __clz(some);
+          sh_target = target;
+          sh_past = over == 0;
+          sh_owner = over ? __ffs(over) - 1 : 31 - __clz(some);
         }
       }
       cta_sync();
-      const Pair all = sh_all, off = sh_off;
-      const bool none = !(all.hi > 0.f);
+      // The draw's place: the first with a weight whose running sum passes the target, or,
+      // where none does (u is 1, or rounding), the last with a weight. It is looked for
+      // by the same rule among the CTAs, a CTA's warps, their lanes and a lane's
+      // entries. Running sums of one level are rounded in other places than those of
+      // the next; an interval with ends of both could hold a target that no other holds
+      // either, or two hold, where this names one place whatever the target.
+      const int owner = sh_owner;
+      const bool none = owner < 0;
       if (!none) {
-        const Pair target = times(all, u);
-        const bool past = !less(target, all);  // u * total rounded up to the total
-        const Pair end = rank + 1 < ranks ? add(off, cta_total) : all;
-        if (past ? rank == sh_last_rank : !less(target, off) && less(target, end)) {
-          if (!past) {
+        if (rank == owner) {
+          if (!sh_past) {
+            const Pair target = sh_target, off = sh_off;
             cta_sync();
             if (tid == 0) sh_base = {0.f, 0.f};
             for (int64_t at = v0; at < v1; at += lay.chunk) {
               const int len = (int)min((int64_t)lay.chunk, v1 - at);
               if (v1 - v0 > lay.chunk) load(at, len);  // a single chunk is still there
-              const Pair mine = add(off, seg_at[warp]);
-              if (!less(target, mine) && less(target, add(mine, seg[warp]))) {
+              const bool passes = lane < kWarps && seg[lane % kWarps].hi > 0.f &&
+                                  less(target, add(off, seg_at[lane % kWarps + 1]));
+              const uint32_t runs = __ballot_sync(0xFFFFFFFFu, passes);
+              if (runs && warp == __ffs(runs) - 1) {
                 // a lane sums neighbours (each lane beginning elsewhere, for the banks), and
                 // those of the lane that passes the target are looked at 32 at a time
                 const int many = lay.run / 32, first = warp * lay.run + lane * many, from0 = lane % many;
+                const Pair mine = add(off, seg_at[warp]);
                 Pair own = {0.f, 0.f};
 #pragma unroll 4
                 for (int i = 0; i < many; ++i) {
@@ -534,33 +545,31 @@ verify_tree_kernel(const TreeArgs a, const Layout lay, int* err) {
                 }
                 own = joined(own.hi, own.lo);
                 const Pair run = add(mine, warp_scan_exact(own, lane));
-                const uint32_t over = __ballot_sync(0xFFFFFFFFu, own.hi > 0.f && less(target, run));
-                if (over) {
-                  const int k = __ffs(over) - 1, from = warp * lay.run + k * many;
-                  const Pair prior = shuffled(run, k > 0 ? k - 1 : 0);
-                  Pair under = k > 0 ? prior : mine;
-                  int pick = -1;
-                  for (int i = 0; i < many; i += 32) {
-                    const int e = from + i + lane;
-                    const float w = i + lane < many && e < len ? row_s[e] : 0.f;
-                    const Pair sum = add(under, warp_scan_exact({w, 0.f}, lane));
-                    const uint32_t some = __ballot_sync(0xFFFFFFFFu, w > 0.f);
-                    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, w > 0.f && less(target, sum));
-                    if (some) pick = from + i + 31 - __clz(some);  // where none passes: the last
-                    if (hit) {
-                      pick = from + i + __ffs(hit) - 1;
-                      break;
-                    }
-                    under = shuffled(sum, 31);
+                const uint32_t has = __ballot_sync(0xFFFFFFFFu, own.hi > 0.f);
+                const uint32_t more = __ballot_sync(0xFFFFFFFFu, own.hi > 0.f && less(target, run));
+                const int k = more ? __ffs(more) - 1 : max(0, 31 - __clz(has)), from = warp * lay.run + k * many;
+                const Pair prior = shuffled(run, k > 0 ? k - 1 : 0);
+                Pair under = k > 0 ? prior : mine;
+                int pick = -1;
+                for (int i = 0; i < many; i += 32) {
+                  const int e = from + i + lane;
+                  const float w = i + lane < many && e < len ? row_s[e] : 0.f;
+                  const Pair sum = add(under, warp_scan_exact({w, 0.f}, lane));
+                  const uint32_t some = __ballot_sync(0xFFFFFFFFu, w > 0.f);
+                  const uint32_t hit = __ballot_sync(0xFFFFFFFFu, w > 0.f && less(target, sum));
+                  if (some) pick = from + i + 31 - __clz(some);  // where none passes: the last
+                  if (hit) {
+                    pick = from + i + __ffs(hit) - 1;
+                    break;
                   }
-                  if (lane == 0) atomicMax(&sh_pick, (int)(at + pick));
+                  under = shuffled(sum, 31);
                 }
+                if (lane == 0 && pick >= 0) sh_pick = (int)(at + pick);
               }
               cta_sync();
               if (sh_pick >= 0) break;
             }
           }
-          // rounding kept the target from being passed: the last that has a weight
           if (tid == 0) out_tokens[count] = sh_pick >= 0 ? sh_pick : cta_last;
         }
       } else if (pass == 1 && rank == ranks - 1 && tid == 0) {

@@ -597,7 +597,8 @@ int lmhead_rotary(int dtype, const void* q, int64_t q_tok, int64_t q_head, const
  *             request. What the root has there is not read; a node whose parent is not
  *             an earlier node of its request is never tried.
  *   granted   S int32 or NULL: 0 for a request that was refused (page plan).
- *   r         T fp32 uniforms of the nodes; u  S fp32 uniforms of the last tokens.
+ *   r         T fp32 uniforms of the nodes; u  S fp32 uniforms of the last tokens (below
+ *             0 they count 0; 1, above it or NaN gives the last id with a weight).
  *   cand_ids, cand_q  T x K (1 <= K <= 4096): the distribution that each node's
  *             children were drawn from (ids outside [0, n) count as none; of an id
  *             listed twice the first counts), or NULL.

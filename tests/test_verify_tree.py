@@ -327,3 +327,124 @@ def test_streams_graphs_and_binding():
         L.verify_tree(*args[:6], 64, **cands)
     with pytest.raises((TypeError, ValueError)):
         L.verify_tree(args[0].t().contiguous().t(), *args[1:], **cands)
+
+
+# ---- targets between two sums. The kernel adds up a row of p in levels (8 CTAs, 16 warps, 32
+# lanes) in pairs of fp32 numbers; sums of the same entries taken in two orders differ in their
+# last bit. A target that lies between the two belongs to the entry before or behind.
+
+f32 = np.float32
+
+
+def _add(a, b):
+    s, (h, l) = f32(a[0] + b[0]), (a[0], b[0])
+    t = f32(s - h)
+    e = f32(f32(f32(h - f32(s - t)) + f32(l - t)) + f32(a[1] + b[1]))
+    r = f32(s + e)
+    return r, f32(e - f32(r - s))
+
+
+def _scan(x):
+    x = list(x) + [(f32(0), f32(0))] * (32 - len(x))
+    o = 1
+    while o < 32:
+        x = [_add(x[i - o], x[i]) if i >= o else x[i] for i in range(32)]
+        o *= 2
+    return x
+
+
+def _butterfly(x):
+    o = len(x) // 2
+    while o:
+        x = [_add(x[i], x[i ^ o]) for i in range(len(x))]
+        o //= 2
+    return x[0]
+
+
+def _exactly(pair):
+    from fractions import Fraction
+    return Fraction(float(pair[0])) + Fraction(float(pair[1]))
+
+
+def _filled(row, at, total):
+    """row with the entries at `at` (two places) such that it sums to `total`, exactly or less."""
+    from fractions import Fraction
+    need = total - sum(Fraction(float(x)) for x in row)
+    if need <= 0:
+        return False
+    for i in at:
+        x = f32(float(need))
+        x = np.nextafter(x, f32(0)) if Fraction(float(x)) > need else x
+        row[i] = x
+        need -= Fraction(float(x))
+    return True
+
+
+def _between(rng, step):
+    """A row of 4096 of which half the sum lies between the sum of its first four parts of
+    `step` entries, one by one, and the same four in a tree; or, with step 1, between the
+    first 32 in a tree and in another. Returns it and the two entries at that border."""
+    while True:
+        row = np.zeros(4096, dtype=f32)
+        if step > 1:
+            at = lambda c: [c * step + 3, c * step + 20]
+            for c in range(7):
+                big = (rng.random() * 0.1 + 0.02) * (0.6 if c > 3 else 1.0)
+                row[at(c)] = big, big * 2.0 ** -25 * (1 + rng.random())
+            part = [_add((row[at(c)[0]], f32(0)), (row[at(c)[1]], f32(0))) for c in range(7)]
+            to = _scan(part)
+            low, high = _add(to[2], part[3]), to[3]
+            fill, border = at(7), (at(3)[1], at(4)[0])
+        else:
+            row[:32] = (rng.random(32) + 0.5) * 2.0 ** -rng.integers(4, 40, 32)
+            each = [(x, f32(0)) for x in row[:32]]
+            low, high = _scan(each)[31], _butterfly(each)
+            fill, border = [40, 300], (31, 40)
+        if low < high and _filled(row, fill, 2 * _exactly(low)):
+            return row, border
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("step", [512, 32, 1])
+def test_targets_between_two_sums(step):
+    """(512 entries a CTA, 32 a warp, one a lane.) Every request gets an entry at the border,
+    whatever the results held before."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    rng = np.random.default_rng(step)
+    S = 32
+    rows, borders = zip(*(_between(rng, step) for _ in range(S)))
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    for spread in (0, 1):  # with nothing behind, and with entries that do not reach the sum's last bit
+        p = np.stack(rows)
+        if spread:
+            p[:, 2000::500] = np.where(p[:, 2000::500] > 0, p[:, 2000::500], 1e-30)
+        out = tuple(torch.full(s, -5, dtype=torch.int32, device="cuda") for s in ((S, 1), (S, 1), (S,)))
+        L.verify_tree(torch.tensor(p, device="cuda"), i32([0] * S), i32([-1] * S), i32(range(S + 1)), torch.zeros(S, device="cuda"),
+                      torch.full((S,), 0.5, device="cuda"), 0, out=out)
+        assert L.last_device_error() == 0 and out[2].tolist() == [0] * S
+        got = out[0][:, 0].tolist()
+        # (an entry of 1e-30 between the two lies at the border itself: any sum of pairs, 2^-48 of
+        # some 0.4 at its finest, is the same with it and without)
+        right = [b[0] <= g <= b[1] and row[g] > 0 for g, b, row in zip(got, borders, p)]
+        assert all(right), [(g, b) for g, b, r in zip(got, borders, right) if not r][:5]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [5, 4096, 300007])
+def test_uniforms_outside_their_range(n):
+    """Below 0: the first entry with a weight; 1, above it and NaN: the last."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    u = [-0.25, -1e-30, -np.inf, -3e38, 1.0, 1.5, np.inf, np.nan]
+    S = len(u)
+    p = torch.zeros(S, n, device="cuda")
+    p[:, 1:n - 1] = torch.rand(S, n - 2, device="cuda") + 0.1
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    out = tuple(torch.full(s, -5, dtype=torch.int32, device="cuda") for s in ((S, 1), (S, 1), (S,)))
+    L.verify_tree(p, i32([0] * S), i32([-1] * S), i32(range(S + 1)), torch.zeros(S, device="cuda"),
+                  torch.tensor(u, dtype=torch.float32, device="cuda"), 0, out=out)
+    assert L.last_device_error() == 0
+    assert out[0][:, 0].tolist() == [1] * 4 + [n - 2] * 4
