@@ -416,11 +416,15 @@ keep_kernel(const KeepArgs a, int shift, int* err) {
 
 // ----------------------------------------------------------------- release
 // Pages ceil(new / P) .. ceil(held / P) - 1 of each request go back behind the
-// free ones, request after request. As in the page plan, each CTA takes
-// kReleaseReqs requests and counts the pages of all earlier ones by itself.
-constexpr int kReleaseThreads = 256;
-constexpr int kReleaseReqs = 8;
+// free ones, request after request. As in the page plan, each CTA takes a few
+// requests and counts the pages of all earlier ones by itself, which means to read
+// them: a request counts only if all of its entries are pages. Bound by latency (device
+// time, graphs replayed): one request 2.1 us (1.7 without the look), 64 of a page each 2.6,
+// 1024 3.8, 16 of 1000 to 1800 pages 4.6 (3.6 without); 16384 of a page each 40.
+constexpr int kReleaseThreads = 512;
+constexpr int kReleaseReqs = 8, kReleaseMost = 32;  // of a CTA: few requests in all, many
 constexpr int kReleaseUnroll = 4;  // pages of a thread under way together
+constexpr int kReleaseFew = 16;    // pages of a request that a lane looks over by itself
 
 struct Gone {
   int first, count;  // pages of the request's table that go
@@ -445,40 +449,89 @@ __device__ __forceinline__ Gone gone_of(const ReleaseArgs& a, int s) {
   return g;
 }
 
+// The same with the pages looked over: a request with an entry that is no page gives none
+// back, so that what is in the free list can be handed out. Whole warps come here, a
+// request each lane (s < 0: none); long lists are read by the warp, 16 bytes a lane.
+__device__ __forceinline__ Gone gone_checked(const ReleaseArgs& a, int s, int lane) {
+  Gone g = {0, 0, true};
+  const int32_t* pages = a.table;
+  if (s >= 0) {
+    g = gone_of(a, s);
+    pages += (int64_t)s * a.width + g.first;
+  }
+  int bits = 0;
+  if (g.count <= kReleaseFew) {
+#pragma unroll 4
+    for (int j = 0; j < g.count; ++j) bits |= pages[j];
+  }
+  for (uint32_t many = __ballot_sync(0xFFFFFFFFu, g.count > kReleaseFew); many; many &= many - 1) {
+    const int l = __ffs((int)many) - 1, n = __shfl_sync(0xFFFFFFFFu, g.count, l);
+    const int32_t* p = reinterpret_cast<const int32_t*>(
+        __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(pages), l));
+    const int lead = min(n, (int)(-(reinterpret_cast<uintptr_t>(p) >> 2) & 3));
+    const int quads = (n - lead) / 4, tail = lead + 4 * quads;
+    const int4* q = reinterpret_cast<const int4*>(p + lead);
+    int some = 0;
+    if (lane < lead) some |= p[lane];
+    if (tail + lane < n) some |= p[tail + lane];
+#pragma unroll 4
+    for (int i = lane; i < quads; i += 32) {
+      const int4 v = q[i];
+      some |= v.x | v.y | v.z | v.w;
+    }
+    some = __reduce_or_sync(0xFFFFFFFFu, (uint32_t)some);
+    if (lane == l) bits = some;
+  }
+  if (bits < 0) {
+    g.count = 0;
+    g.sane = false;
+  }
+  return g;
+}
+
 __global__ void __launch_bounds__(kReleaseThreads)
-release_kernel(const ReleaseArgs a, int* err) {
-  __shared__ int sh_sum[kReleaseThreads / 32];
-  __shared__ int r_end[kReleaseReqs + 1], r_first[kReleaseReqs];
+release_kernel(const ReleaseArgs a, int reqs, int* err) {
+  constexpr int kWarps = kReleaseThreads / 32;
+  __shared__ int sh_sum[kWarps], r_count[kReleaseMost];
+  __shared__ int r_end[kReleaseMost + 1], r_first[kReleaseMost];
   __shared__ int64_t sh_at;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, first = blockIdx.x * kReleaseReqs;
-  const int count = min(kReleaseReqs, a.S - first);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, first = blockIdx.x * reqs;
+  const int count = min(reqs, a.S - first);
+  // all requests up to the CTA's last; where each thread has one, neighbours are in
+  // different warps, which share out long lists
+  const bool spread = first + count <= kReleaseThreads;
   int sum = 0;  // S * width fits 32 bits
-  for (int s = tid; s < first; s += kReleaseThreads) sum += gone_of(a, s).count;
+  for (int s0 = 0; s0 < first + count; s0 += kReleaseThreads) {
+    const int s = spread ? lane * kWarps + warp : s0 + tid, i = s - first;
+    const Gone g = gone_checked(a, i < count ? s : -1, lane);
+    if (i < 0) {
+      sum += g.count;
+    } else if (i < count) {
+      r_count[i] = g.count;
+      r_first[i] = g.first;
+      if (!g.sane && blockIdx.y == 0) record_error(err, kDevErrBadId);
+    }
+  }
   sum = __reduce_add_sync(0xFFFFFFFFu, sum);
-  if (lane == 0) sh_sum[tid >> 5] = sum;
-  if (tid < 32) {
-    // the CTA's requests, a lane each: where their pages lie among the CTA's
-    Gone g = {0, 0, true};
-    if (lane < count) g = gone_of(a, first + lane);
-    if (!g.sane && blockIdx.y == 0) record_error(err, kDevErrBadId);
-    int incl = g.count;
+  if (lane == 0) sh_sum[warp] = sum;
+  cta_sync();
+  if (warp == 0) {
+    // where the pages of the CTA's requests, a lane each, lie among the CTA's
+    int incl = lane < count ? r_count[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < kReleaseReqs; o <<= 1) {
+    for (int o = 1; o < kReleaseMost; o <<= 1) {
       const int p = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += p;
     }
-    if (lane < kReleaseReqs) {
-      r_end[lane + 1] = incl;
-      r_first[lane] = g.first;
-    }
+    r_end[lane + 1] = incl;
     if (lane == 0) r_end[0] = 0;
   }
   cta_sync();
   if (tid == 0) {
     int64_t at = max(0, min(*a.free_count, a.free_cap));
-    for (int w = 0; w < kReleaseThreads / 32; ++w) at += sh_sum[w];
+    for (int w = 0; w < kWarps; ++w) at += sh_sum[w];
     sh_at = at;
     const int64_t end = at + r_end[count];
     // what has no room in the list is not put there
@@ -563,11 +616,12 @@ cudaError_t launch_cache_keep(KeepArgs a, int* err, cudaStream_t s) {
 }
 
 cudaError_t launch_page_release(const ReleaseArgs& a, int* err, cudaStream_t s) {
+  const int reqs = a.S <= 1024 ? kReleaseReqs : kReleaseMost;
   // several CTAs for the pages of the same requests where tables are wide
-  int64_t y = (int64_t)a.width * kReleaseReqs / (kReleaseThreads * kReleaseUnroll * 2);
+  int64_t y = (int64_t)a.width * reqs / (kReleaseThreads * kReleaseUnroll);
   y = y < 1 ? 1 : y > 64 ? 64 : y;
-  return launch_kernel(true, release_kernel, dim3((a.S + kReleaseReqs - 1) / kReleaseReqs, (unsigned)y),
-                       dim3(kReleaseThreads), 0, s, a, err);
+  return launch_kernel(true, release_kernel, dim3((a.S + reqs - 1) / reqs, (unsigned)y),
+                       dim3(kReleaseThreads), 0, s, a, reqs, err);
 }
 
 }  // namespace lmhead

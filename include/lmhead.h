@@ -659,9 +659,11 @@ int lmhead_cache_keep(int count, void* const* base, const int64_t* page_stride,
  *             are free; must not meet table.
  *   out_free_left  1 int32: free pages afterwards (the next free_count; must not
  *             alias free_count).
- * A negative length, one that has grown, or more than width * page_size tokens: the
- * request releases nothing; pages past free_cap are dropped. Both record
- * LMHEAD_ERR_DEVICE_CHECK. S up to 2^20 (the time grows with S squared).
+ * A negative length, one that has grown, more than width * page_size tokens, or a page
+ * id below 0 among those that would be released: the request releases nothing; pages
+ * past free_cap are dropped. Both record LMHEAD_ERR_DEVICE_CHECK. (The number of pages
+ * is not known here: an id past it is found by the operators that go by it.) S up to
+ * 2^20 (the time grows with S squared).
  */
 int lmhead_page_release(const int32_t* lens, const int32_t* new_lens, const int32_t* cu,
                         const int32_t* granted, int S, const int32_t* table, int width,

@@ -574,6 +574,42 @@ def test_release_bad_lengths():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("S,width", [(1, 3), (8, 9), (9, 40), (300, 9), (17, 1500), (2, 9001), (1030, 30)])
+def test_release_entries_that_are_no_pages(S, width):
+    """A request with an entry below 0 among the pages that it would give back gives none
+    back, and the error is recorded; entries before and behind those are not looked at."""
+    from gpu_util import lib
+    L = lib()
+    rng = np.random.default_rng(S + width)
+    held = rng.integers(0, width * 16 + 1, S)
+    now = np.where(rng.random(S) < 0.5, (held * rng.random(S)).astype(int), np.maximum(held - 40, 0))
+    held[-1], now[-1] = width * 16, 0
+    lo, hi = -(-now // 16), -(-held // 16)
+    table = rng.integers(0, 10 ** 6, (S, width))
+    for s in range(S):  # around them anything
+        table[s, :lo[s]] = -1
+        table[s, hi[s]:] = -(1 << 31)
+    F = 3
+    room = int((hi - lo).sum())
+    args = _i32(held), _i32(now)
+
+    def run(table, then, status):
+        free = _i32([5, 6, 7] + [-9] * room)
+        left = L.page_release(*args, _i32(table), free, _i32([F]), 16)
+        assert L.last_device_error() == status
+        want = O.page_release(held, then, table, [5, 6, 7], F, 16)
+        assert left.tolist() == [len(want)] and free.cpu().tolist() == want + [-9] * (F + room - len(want))
+
+    run(table, now, 0)
+    for turn in range(6):
+        bad = table.copy()
+        some = [s for s in range(S) if hi[s] > lo[s] and (rng.random() < 0.4 or s == S - 1)]
+        for s in some:  # one entry each: the first, the last or one between
+            bad[s, [lo[s], hi[s] - 1, rng.integers(lo[s], hi[s])][turn % 3]] = -1 if turn < 3 else -(1 << 31)
+        run(bad, np.where(np.isin(np.arange(S), some), held, now), -7)
+
+
+@pytest.mark.gpu
 def test_weights_waits_that_run_out():
     """With no time to wait a call gives up, says so, and the next one is right."""
     from gpu_util import lib
