@@ -222,6 +222,10 @@ struct ReorderArgs {
 cudaError_t launch_beam_reorder(const ReorderArgs& a, int* err, cudaStream_t s);
 
 // ---- operators of a step over the paged cache
+// Most tokens of a request where kernels walk over them in blocks: places behind the
+// last block stay within 32 bits.
+constexpr int kMaxTokens = INT32_MAX - 65535;
+
 // Rotary positions (rotary.cu); strides in elements, k may be nullptr.
 struct RotaryArgs {
   int dtype;  // lmhead_dtype

@@ -110,7 +110,7 @@ __device__ __forceinline__ Req request_of(const WeightArgs& a, int s, int tile_t
   sane = true;
   r.np = r.qt = 0;
   const bool refused = a.granted && a.granted[s] == 0;
-  if (refused || r.len < 0 || r.len > (a.width << a.page_shift) - r.m) {
+  if (refused || r.len < 0 || r.len > min(a.width << a.page_shift, kMaxTokens) - r.m) {
     sane = refused;
     r.len = 0;  // (whatever it was, no arithmetic is done on it)
     return r;

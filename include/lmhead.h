@@ -687,7 +687,7 @@ int lmhead_page_release(const int32_t* lens, const int32_t* new_lens, const int3
  * depends on the order in which CTAs run.
  * Requests that were refused (granted 0) are left alone; so are, with
  * LMHEAD_ERR_DEVICE_CHECK recorded, those whose lengths are negative or pass width *
- * page_size, and the tokens of a page id outside [0, pages). Where cu decreases or
+ * page_size or 2^31 - 2^16, and the tokens of a page id outside [0, pages). Where cu decreases or
  * leaves [0, T], nothing is computed and the error recorded. Requests share no
  * page. A token with a non-finite key, or seen by a row whose q or lse is NaN, gets
  * NaN or an infinity.

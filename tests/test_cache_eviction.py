@@ -377,6 +377,29 @@ def test_weights_streams_graphs_and_determinism():
             L.cache_weights(k["q"], c["kc"], c["table"], c["lens"], c["cu"], k["lse"], k["w"])
 
 
+@pytest.mark.gpu
+def test_weights_of_lengths_near_2_31():
+    """Within the table, but with places of blocks behind them that 32 bits do not hold: left
+    alone with the error recorded, the other requests served."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    c = _weights_case([300, 40], [2, 1], 4, 2, 64, 256, "bfloat16", 31)
+    lse, _ = _lse(c, 0)
+    width = (2 ** 31 - 1) // 256
+    table = torch.zeros(2, width, dtype=torch.int32, device="cuda")
+    table[:, :c["table"].shape[1]] = c["table"]
+    call = lambda lens: L.cache_weights(c["q"], c["kc"], table, _i32(lens), c["cu"], lse, c["w"].clone(), decay=0.5)
+    want = call([300, 40])
+    assert L.last_device_error() == 0
+    mine, other = c["table"][0, :2].long(), c["table"][1, :1].long()
+    for n in (width * 256 - 2, width * 256 - 3, 2 ** 31 - 513, 2 ** 31 - 65537, 2 ** 31 - 1):
+        got = call([n, 40])
+        assert L.last_device_error() == -7
+        assert np.array_equal(_n64(got[other]), _n64(want[other]), equal_nan=True)
+        assert np.array_equal(_n64(got[mine]), _n64(c["w"][mine]), equal_nan=True)
+
+
 # ------------------------------------------------------------------ select
 
 def _select_case(rng, lens, P, Hk, ties):
