@@ -59,7 +59,7 @@ select_kernel(const SelectArgs a, int shift, int staged, int quads, int* err) {
   for (int s = blockIdx.y; s < a.S; s += gridDim.y) {
     int32_t* out = a.kept + ((int64_t)s * a.kv_heads + head) * a.budget;
     int L = a.lens[s];
-    if (L < 0 || L > (int64_t)a.width * a.page) {
+    if (L < 0 || L > min((int64_t)a.width * a.page, (int64_t)kMaxTokens)) {
       if (tid == 0) record_error(err, kDevErrBadId);
       L = 0;
     }

@@ -711,8 +711,8 @@ int lmhead_cache_weights(int dtype, const void* q, int64_t q_tok, int64_t q_head
  *   out_kept  S x kv_heads x budget int32: positions, ascending, then -1
  *             (lmhead_cache_keep's `kept` with per_head, first NULL). A request of
  *             budget tokens or fewer keeps them all.
- * sinks + recent <= budget. A negative length or one past width * page_size gives -1
- * throughout, a page id outside [0, pages) counts its tokens as NaN; both record
+ * sinks + recent <= budget. A negative length or one past width * page_size or
+ * 2^31 - 2^16 gives -1 throughout, a page id outside [0, pages) counts its tokens as NaN; both record
  * LMHEAD_ERR_DEVICE_CHECK.
  */
 int lmhead_cache_select(const float* weights, int64_t w_page, int64_t w_token, int64_t w_head,

@@ -456,6 +456,21 @@ def test_select_bad_requests_and_equal_weights():
     assert np.array_equal(L.cache_select(z, td, _i32([100] * 3), 10, 2, 3).cpu().numpy()[2, 1], [0, 1, 2, 3, 4, 5, 6, 97, 98, 99])
 
 
+@pytest.mark.gpu
+def test_select_of_lengths_near_2_31():
+    """Within the table, but so that a loop's next place would pass 2^31: -1 throughout."""
+    from gpu_util import lib
+    L = lib()
+    rng = np.random.default_rng(3)
+    w, table, wd, _ = _select_case(rng, [100], 256, 2, 0)
+    width = (2 ** 31 - 1) // 256
+    td = _i32(np.zeros((2, width)))
+    for n in (2 ** 31 - 65535, 2 ** 31 - 8192, width * 256):
+        got = L.cache_select(wd, td, _i32([n, 100]), 10, 2, 3).cpu().numpy()
+        assert L.last_device_error() == -7 and (got[0] == -1).all()
+        assert np.array_equal(got[1], O.cache_select(w, [[0]], [100], 256, 10, 2, 3)[0])
+
+
 # -------------------------------------------------------------------- keep
 
 @pytest.mark.gpu
