@@ -377,9 +377,11 @@ keep_kernel(const KeepArgs a, int shift, int* err) {
     cta_sync();
     last = sh_last;
     from0 = sh_first;
-    if (blockIdx.x == 0 && tid == 0) {
-      a.new_lens[s] = first + (first >= 0 ? last : 0);
-      if (first < 0) record_error(err, kDevErrBadId);
+    if (tid == 0) {
+      const int64_t now = first >= 0 ? (int64_t)first + last : first;
+      if (blockIdx.x == 0) a.new_lens[s] = (int32_t)min(now, (int64_t)INT32_MAX);
+      // (entries at their own place are not looked at below: the last is past the table here)
+      if (first < 0 || (last > 0 && now > room)) record_error(err, kDevErrBadId);
     }
     for (int i0 = from0; i0 < last; i0 += kKeepChunk) {
       const int count = min(kKeepChunk, last - i0);

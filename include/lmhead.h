@@ -632,7 +632,8 @@ int lmhead_verify_tree(const float* p, int64_t n, const int32_t* tokens, const i
  *   first     S int32, or NULL: 0. lens and a verified tree's out_path keep the
  *             accepted nodes of the chunk behind the lens cached tokens.
  *   out_new_lens  S int32: first[s] plus the number of entries up to the last one
- *             that is not negative (with per_head, of head 0); must not meet first.
+ *             that is not negative (with per_head, of head 0), 2^31 - 1 at most; must
+ *             not meet first.
  * Rows behind the new length are left as they were. Requests share no page that is
  * moved in (prefixes that they share come before first and the first entry that
  * differs from its index). An entry below its index, a row past width * page_size or

@@ -562,6 +562,33 @@ def test_keep_bad_lists():
             L.cache_keep(x, _i32(table), _i32(kept))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("per_head", [False, True])
+def test_keep_entries_at_their_place_past_the_table(per_head):
+    """They move nothing, but there is no such row: the error is recorded. New lengths stay
+    within 32 bits."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    table, pages = _i32([[0, 1], [2, 3]]), 4
+    c = torch.randint(0, 1000, (pages, 16, 2, 8), device="cuda", dtype=torch.int32)
+    was = c.clone()
+
+    def run(kept, first):
+        k = np.asarray(kept)
+        k = np.stack([np.full_like(k, -1), k], 1) if per_head else k  # the second head's own list
+        new = L.cache_keep([c], table, _i32(k), first=_i32(first))
+        assert torch.equal(c, was)
+        return new.tolist(), L.last_device_error()
+    at = [0, 1, 2, 3]
+    own = lambda first, n: first if per_head else min(first + n, 2 ** 31 - 1)
+    assert run([at, at], [28, 0]) == ([own(28, 4), own(0, 4)], 0)
+    assert run([at, at], [29, 0]) == ([own(29, 4), own(0, 4)], -7)
+    assert run([at, [0, 1, 2, -1]], [0, 30]) == ([own(0, 4), own(30, 3)], -7)
+    assert run([at, [-1] * 4], [2 ** 31 - 2, 50]) == ([own(2 ** 31 - 2, 4), 50], -7)
+    assert run([[-1] * 4] * 2, [33, 2 ** 31 - 1]) == ([33, 2 ** 31 - 1], 0)  # (no row at all)
+
+
 # ----------------------------------------------------------------- release
 
 @pytest.mark.gpu
