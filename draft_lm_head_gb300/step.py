@@ -16,7 +16,9 @@ and, for a cache that outgrows its room,
     new = cache_keep([kc, vc, weights], table, kept)
     left = page_release(lens, new, table, free_pages, free_count, P)
 
-The frequencies of rotary come from prep.rotary_turns.
+(the weights of a tree's step go between verify_tree and cache_keep, with -inf in the lse
+of nodes that are not on `path`, where rejected drafts are not to count, and `weights` among
+the caches that cache_keep moves). The frequencies of rotary come from prep.rotary_turns.
 """
 from __future__ import annotations
 
@@ -232,7 +234,8 @@ def cache_weights(q: torch.Tensor, k_cache: torch.Tensor, table: torch.Tensor, l
     (pages x page_size x kv_heads fp32, any strides) times decay, plus the softmax
     weights that the chunk's tokens give it; new tokens' entries start from nothing.
     q, k_cache (the chunk's K in it), table, lens, cu, tree, window, scale, granted as
-    of chunk_attention, lse what it returned (see lmhead_cache_weights)."""
+    of chunk_attention, lse what it returned, -inf for rows that are not to count, as
+    those of rejected drafts (see lmhead_cache_weights)."""
     dev = _cuda(q, "q")
     if q.dim() != 3 or k_cache.dim() != 4 or table.dim() != 2:
         raise ValueError("q, k_cache, table: expected tokens x heads x dim, pages x page_size x "

@@ -8,9 +8,10 @@ lengths (page_plan, rotary, chunk_attention). Then each step drafts a tree behin
 sequence's last token (dense_head and draft_select over the drafts' embeddings), runs
 all trees through the target in one pass, takes the path that the target accepts and one
 token more (verify_tree), keeps that path's rows in the cache (cache_keep) and gives
-the other pages back (page_release). How much attention each cached token draws is summed
-up on the way (cache_weights); a sequence with more than `budget` tokens is cut down to
-those that draw most (cache_select, cache_keep, page_release).
+the other pages back (page_release). How much attention each cached token draws from the
+tokens that stay is summed up on the way (cache_weights, behind the verdict); a sequence
+with more than `budget` tokens is cut down to those that draw most (cache_select,
+cache_keep, page_release).
 """
 from __future__ import annotations
 
@@ -51,8 +52,9 @@ class Target:
         self.turns = torch.from_numpy(prep.rotary_turns(dim, 10000.0, "wavelength", 4.0, 1024)).to(device)
         self.ws = L.Workspace()
 
-    def forward(self, tokens, positions, cache, weights, table, lens, plan, tree=None):
-        """States behind the tokens; their keys and values go to the cache."""
+    def attend(self, tokens, positions, cache, table, lens, plan, tree=None):
+        """States behind the tokens, whose keys and values go to the cache, and what
+        cache_weights takes of them: queries and lse."""
         H, Hk, D = self.heads, self.kv_heads, self.dim
         x = self.embed[tokens.long()]
         qkv = (x @ self.qkv.T).view(-1, H + 2 * Hk, D)
@@ -60,9 +62,18 @@ class Target:
         L.rotary(q, k, positions, self.turns)
         o, lse = L.chunk_attention(q, cache[0], cache[1], table, lens, plan.cu, k=k, v=v, slots=plan.slots, tree=tree,
                                    with_lse=True, workspace=self.ws, granted=plan.granted)
+        return x + o.view(-1, H * D) @ self.out.T, q, lse
+
+    def weigh(self, q, lse, cache, weights, table, lens, plan, tree=None):
+        """What the tokens' queries drew on goes to the weights."""
         L.cache_weights(q, cache[0], table, lens, plan.cu, lse, weights, tree=tree, decay=0.9, granted=plan.granted,
                         workspace=self.ws)
-        return x + o.view(-1, H * D) @ self.out.T
+
+    def forward(self, tokens, positions, cache, weights, table, lens, plan, tree=None):
+        """Both, for tokens that all count."""
+        h, q, lse = self.attend(tokens, positions, cache, table, lens, plan, tree)
+        self.weigh(q, lse, cache, weights, table, lens, plan, tree)
+        return h
 
     def probabilities(self, h, temperature):
         logits, p = L.dense_head(self.W, h.contiguous(), temperature)
@@ -117,10 +128,13 @@ def generate(model, prompts, steps, page=16, budget=None, seed=1, temperature=1.
         tokens = tokens.view(-1)
         # the target's pass over them: a node's position is its depth's
         plan = L.page_plan(lens, count, table, free, free_count, page, S * N)
-        h = model.forward(tokens, (at[:, None] + level[None, :]).view(-1), cache, weights, table, lens, plan, tree)
+        h, q, lse = model.attend(tokens, (at[:, None] + level[None, :]).view(-1), cache, table, lens, plan, tree)
         p = model.probabilities(h, temperature)
         r, u = torch.rand(S * N, generator=g, device=dev), torch.rand(S, generator=g, device=dev)
         out, path, accepted = L.verify_tree(p, tokens, parent, plan.cu, r, u, depth, granted=plan.granted)
+        # rejected drafts draw nothing: a row of -inf; the others while their keys are in the chunk's places
+        on = torch.zeros(S, N + 1, dtype=torch.bool, device=dev).scatter_(1, path.long() % (N + 1), True)[:, :N]
+        model.weigh(q, lse.masked_fill_(~on.reshape(-1, 1), float("-inf")), cache, weights, table, lens, plan, tree)
         new_lens = L.cache_keep([*cache, weights], table, path, first=lens)
         free_count = L.page_release(lens, new_lens, table, free, plan.free_left, page, cu=plan.cu, granted=plan.granted)
         at = at + (new_lens - lens)

@@ -679,7 +679,10 @@ int lmhead_page_release(const int32_t* lens, const int32_t* new_lens, const int3
  * The chunk's own keys are in the cache already (lmhead_chunk_attention wrote them).
  *   dtype, q, k_cache, table, lens, cu, granted, tree, window, scale, dim, page_size
  *             as of lmhead_chunk_attention (the rows of q do not meet).
- *   lse       T x heads fp32: that call's out_lse. A row of -inf draws nothing.
+ *   lse       T x heads fp32: that call's out_lse. A row of -inf draws nothing. Of a
+ *             draft tree every node counts as it is, rejected ones too: where only the
+ *             accepted path is to, call behind the verdict, with -inf in the others'
+ *             rows, and before the path's rows are moved together.
  *   weights   pages x page_size x kv_heads fp32, in place; w_page, w_token, w_head:
  *             strides in elements. What a page holds for tokens that are new
  *             (j >= lens) is not read, nor anything with decay 0.

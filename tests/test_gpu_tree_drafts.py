@@ -83,6 +83,38 @@ def test_eviction_in_the_loop():
             assert _close(got[:2], want[:2][:n]) and _close(got[-min(12, n):], want[-min(12, n):])
 
 
+def test_rejected_drafts_draw_nothing(monkeypatch):
+    """What the weights are summed up from: of a tree's rows those of the accepted path."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    import tree_drafts as E
+    model = E.Target()
+    rng = np.random.default_rng(4)
+    prompts = [rng.integers(0, model.n, n).tolist() for n in (3, 20, 33)]
+    calls, paths = [], []
+    weigh, verify = L.cache_weights, L.verify_tree
+
+    def weights(q, kc, table, lens, cu, lse, w, **kw):
+        if kw.get("tree") is not None:
+            calls.append(lse.clone())
+        return weigh(q, kc, table, lens, cu, lse, w, **kw)
+
+    def verdict(*args, **kw):
+        paths.append(verify(*args, **kw))
+        return paths[-1]
+    monkeypatch.setattr(E.L, "cache_weights", weights)
+    monkeypatch.setattr(E.L, "verify_tree", verdict)
+    E.generate(model, prompts, 4)
+    assert L.last_device_error() == 0 and len(calls) == len(paths) == 4
+    for lse, (_, path, _) in zip(calls, paths):
+        lse = lse.view(3, len(E.PARENT), -1)
+        for s in range(3):
+            on = {x for x in path[s].tolist() if x >= 0}
+            for c in range(len(E.PARENT)):
+                assert bool(torch.isfinite(lse[s, c]).all() if c in on else (lse[s, c] == -float("inf")).all()), (s, c)
+
+
 def test_a_step_captured_and_replayed():
     """Plan, rotary, attention, weights, verification, kept rows and pages given back in one
     graph, replayed on two states, against the same calls made one by one."""
