@@ -883,7 +883,8 @@ cudaError_t launch_all(const WeightArgs& a, const Scratch& sc, int parts, int* e
   if (by_tma && !make_rows_map(&qmap, a.q, BF16, D, a.heads, a.T, q_head, q_tok, group, tile_tok))
     return cudaErrorInvalidValue;
   // Cutting units between CTAs costs the second launch; it pays where a request has
-  // several query tiles a unit.
+  // several query tiles a unit. (Told by the average: the host does not know the requests. A
+  // prompt among many single tokens stays whole, and its units are the longest shares.)
   const bool whole = a.T <= (int64_t)2 * tile_tok * a.S;
   static int smem_set[64] = {0};
   cudaError_t e = ensure_dynamic_smem(weights_kernel<BF16, D>, Shape<D>::kSmem, smem_set);

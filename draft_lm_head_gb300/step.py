@@ -1,17 +1,21 @@
 """The operators of a step over the paged cache (include/lmhead.h, "Operators of
 a step over the paged cache").
 
-    rotary(q, k, plan.positions, turns)                  # in place
+    rotary(q, k, positions, turns)                       # in place
     o, lse = chunk_attention(q, kc, vc, table, lens, plan.cu, k=k, v=v, slots=plan.slots,
-                             tree=bits, with_lse=True)
+                             tree=bits, with_lse=True, granted=plan.granted)
     ...                                                  # the target's p behind each node
-    tokens, path, accepted = verify_tree(p, drafts, parent, plan.cu, r, u, depth)
+    tokens, path, accepted = verify_tree(p, drafts, parent, plan.cu, r, u, depth,
+                                         granted=plan.granted)
     new = cache_keep([kc, vc], table, path, first=lens)  # the accepted rows
-    left = page_release(lens, new, table, free_pages, plan.free_left, P, cu=plan.cu)
+    left = page_release(lens, new, table, free_pages, plan.free_left, P, cu=plan.cu,
+                        granted=plan.granted)
 
-and, for a cache that outgrows its room,
+where a node's position is the root's and its depth on top: `read` + depth, with the tokens
+read so far (plan.positions are places in the cache, lens + i: right for chains, and as
+long as nothing was evicted). And, for a cache that outgrows its room,
 
-    cache_weights(q, kc, table, lens, plan.cu, lse, weights)
+    cache_weights(q, kc, table, lens, plan.cu, lse, weights, granted=plan.granted)
     kept = cache_select(weights, table, lens, budget, sinks=4, recent=256)
     new = cache_keep([kc, vc, weights], table, kept)
     left = page_release(lens, new, table, free_pages, free_count, P)
@@ -67,8 +71,8 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
            magnitude: float = 1.0, out=None, stream=None):
     """Rotary positions of q (T x heads x dim) and k (T x kv_heads x dim, or None)
     of bf16, fp16 or fp32, any strides with dim contiguous: in place, or into the
-    pair `out`, which is returned. positions: T int32 (a plan's), negative ones
-    leave their rows unwritten. turns: int64 from prep.rotary_turns, for the first
+    pair `out`, which is returned. positions: T int32 (a plan's for a chain of tokens, a
+    tree's by depth), negative ones leave their rows unwritten. turns: int64 from prep.rotary_turns, for the first
     2 * len(turns) elements of a head. backward: the rotation's transpose, the
     gradient's way back (see lmhead_rotary)."""
     dev = _cuda(q, "q")
@@ -192,7 +196,8 @@ def page_release(lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor
                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gives the pages of requests that have become shorter back: free_pages (a
     page plan's, with room for them) is extended in place behind its first
-    free_count entries, the new count (1 int32) is returned. A request held lens
+    free_count entries, the new count (1 int32) is returned. No other request may hold
+    the pages that go. A request held lens
     tokens, and its cu[s+1] - cu[s] new ones if cu is given and granted is not 0; it
     holds new_lens from now on (see lmhead_page_release)."""
     dev = _cuda(lens, "lens")
@@ -269,8 +274,9 @@ def cache_select(weights: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
                  stream=None) -> torch.Tensor:
     """The tokens of each request and K/V head that stay in a cache cut down to
     `budget`: the first `sinks`, the last `recent` and those with the largest weights
-    between, S x kv_heads x budget positions (int32, ascending, then -1), which
-    cache_keep takes (see lmhead_cache_select)."""
+    between, S x kv_heads x budget places (int32, ascending, then -1), which
+    cache_keep takes. Rotary positions of later tokens go on as if nothing had gone, a
+    plan's do not (see lmhead_cache_select)."""
     dev = _cuda(weights, "weights")
     w = _weights_tensor(weights, dev)
     if table.dim() != 2 or budget < 1:

@@ -557,8 +557,12 @@ int lmhead_beam_reorder(const int32_t* parent, int S, int beams, int k, int coun
  *   dtype     LMHEAD_BF16, LMHEAD_FP16 or LMHEAD_FP32, of q, k and the results.
  *   q, k      T x heads x dim, T x kv_heads x dim (k and out_k NULL: q alone);
  *             *_tok, *_head: strides in elements (dim is contiguous).
- *   positions T int32 (a page plan's out_positions); the rows of a token whose
- *             position is negative are not written.
+ *   positions T int32; the rows of a token whose position is negative are not
+ *             written. A page plan's out_positions are places in the cache, len + i: those
+ *             of a chain of tokens behind a cache that holds all before them. A draft
+ *             tree's node stands as many positions behind the root as it is deep (siblings
+ *             on the same one), whatever its place; and where tokens were evicted,
+ *             positions go on from the number of tokens read, not from len.
  *   turns     rot / 2 int64: turns a position of each pair, in units of 2^-64 and
  *             modulo 1, so that angles of far positions lose nothing.
  *   interleaved  0: pair i is (i, i + rot / 2); else (2 i, 2 i + 1).
@@ -611,7 +615,8 @@ int lmhead_rotary(int dtype, const void* q, int64_t q_tok, int64_t q_head, const
  * At most 64 nodes a request. More of them, a cu that decreases or leaves [0, T], a
  * tried token outside [0, n) or, with cand_ids, not among its parent's candidates,
  * and a path deeper than depth give -1 too and record LMHEAD_ERR_DEVICE_CHECK.
- * Accept tests, masses and running sums carry 48 bits or more.
+ * Accept tests, masses and running sums are pairs of fp32 numbers: some 48 bits, and for
+ * products below 2^-102, whose second number is subnormal, down to fp32's 24.
  */
 int lmhead_verify_tree(const float* p, int64_t n, const int32_t* tokens, const int32_t* parent,
                        const int32_t* cu, const int32_t* granted, const float* r, const float* u,
@@ -655,7 +660,7 @@ int lmhead_cache_keep(int count, void* const* base, const int64_t* page_stride,
  *             request holds cu[s+1] - cu[s] more, unless granted (S int32, or NULL) is
  *             0 for it.
  *   new_lens  S int32: tokens it holds from now on. Pages from ceil(new / page_size)
- *             up to ceil(held / page_size) are released.
+ *             up to ceil(held / page_size) are released; no other request holds them.
  *   free_pages  free_cap int32, in place: the stack whose first *free_count entries
  *             are free; must not meet table.
  *   out_free_left  1 int32: free pages afterwards (the next free_count; must not
@@ -695,7 +700,8 @@ int lmhead_page_release(const int32_t* lens, const int32_t* new_lens, const int3
  * leaves [0, T], nothing is computed and the error recorded. Requests share no
  * page. A token with a non-finite key, or seen by a row whose q or lse is NaN, gets
  * NaN or an infinity.
- * Workspace: lmhead_cache_weights_workspace_size bytes, 256-byte aligned.
+ * Workspace: lmhead_cache_weights_workspace_size bytes, 256-byte aligned; no two calls
+ * in flight may share it.
  */
 size_t lmhead_cache_weights_workspace_size(int S);
 int lmhead_cache_weights(int dtype, const void* q, int64_t q_tok, int64_t q_head,
@@ -712,9 +718,12 @@ int lmhead_cache_weights(int dtype, const void* q, int64_t q_tok, int64_t q_head
  * `budget`: the first `sinks`, the last `recent` and, between them, those with the
  * largest weights (ties: the lower position; a NaN counts below all others).
  *   weights   as of lmhead_cache_weights; lens  S int32, the tokens cached.
- *   out_kept  S x kv_heads x budget int32: positions, ascending, then -1
+ *   out_kept  S x kv_heads x budget int32: places, ascending, then -1
  *             (lmhead_cache_keep's `kept` with per_head, first NULL). A request of
  *             budget tokens or fewer keeps them all.
+ * Keys keep the rotary positions that they were written with, while the places
+ * behind them move up: a page plan's positions and the window of
+ * lmhead_chunk_attention and lmhead_cache_weights count places from then on.
  * sinks + recent <= budget. A negative length or one past width * page_size or
  * 2^31 - 2^16 gives -1 throughout, a page id outside [0, pages) counts its tokens as NaN; both record
  * LMHEAD_ERR_DEVICE_CHECK.
