@@ -437,6 +437,26 @@ def test_select_against_oracle(lens, P, Hk, budget, sinks, recent, ties):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,P,Hk,budget,sinks,recent", [
+    ([60001, 45003, 7], 256, 2, 5001, 5, 101), ([41500, 50002], 64, 3, 41000, 3, 2), ([52001], 16, 2, 600, 0, 0),
+    ([70002, 41111], 20, 2, 30001, 4093, 7)])
+@pytest.mark.parametrize("ties", [0, 1, 2])
+def test_select_of_long_lists_by_fours(lens, P, Hk, budget, sinks, recent, ties):
+    """More tokens than have room in shared memory, a head's side by side (read four at a time from
+    a multiple of four on, the sinks' end or not), the heads' side by side too."""
+    from gpu_util import lib
+    L = lib()
+    rng = np.random.default_rng(sum(lens) + budget + ties)
+    w, table, wd, td = _select_case(rng, lens, P, Hk, ties)
+    want = O.cache_select(w, table, lens, P, budget, sinks, recent)
+    first = wd.transpose(1, 2).contiguous().transpose(1, 2)
+    assert first.stride(1) == 1
+    for x in (first, wd):
+        assert np.array_equal(L.cache_select(x, td, _i32(lens), budget, sinks, recent).cpu().numpy(), want)
+    assert L.last_device_error() == 0
+
+
+@pytest.mark.gpu
 def test_select_bad_requests_and_equal_weights():
     import torch
     from gpu_util import lib

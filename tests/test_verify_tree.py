@@ -54,6 +54,35 @@ def test_tokens_come_out_as_the_targets(drawn):
     assert np.abs(first / N - p[0]).max() < 0.0125  # five standard deviations
 
 
+@pytest.mark.parametrize("drawn", [False, True])
+def test_second_tokens_come_out_as_the_targets(drawn):
+    """Behind each accepted first token the second is distributed as the target behind that
+    token, whose row depends on it: over m such draws every share p within five standard
+    deviations, 5 sqrt(p (1 - p) / m), and eight draws more for rare ones."""
+    rng = np.random.default_rng(15)
+    n, N = 6, 40000
+    root = np.array([0.25, 0.3, 0.05, 0.2, 0.1, 0.1], dtype=np.float32)  # (each child is met often)
+    behind = rng.dirichlet(np.ones(n) * 0.7, n).astype(np.float32)  # by the token before
+    q = rng.dirichlet(np.ones(4), 2).astype(np.float32)
+    ids = np.array([0, 1, 3, 5])
+    pick = lambda row, k: ids[rng.choice(4, k, replace=False, p=row / row.astype(float).sum())]
+    second = np.zeros((n, n))
+    for _ in range(N):
+        kids = pick(q[0], 2) if drawn else [1, 3]
+        grand = [pick(q[1], 2) if drawn else np.argsort(-behind[k])[:2] for k in kids]  # (given: the likely ones)
+        tokens = [0, kids[0], kids[1], grand[0][0], grand[1][0], grand[0][1], grand[1][1]]
+        p = np.stack([root, behind[kids[0]], behind[kids[1]]] + [behind[0]] * 4)
+        said, path = O.verify_tree(p, tokens, [-1, 0, 0, 1, 2, 1, 2], rng.random(7), rng.random(), [ids] * 7 if drawn else None,
+                                   [q[0], q[1], q[1]] + [q[0]] * 4 if drawn else None)
+        if len(path) > 1:
+            second[said[0], said[1]] += 1
+    met = second.sum(1)
+    assert (met > 4000).sum() >= 2
+    for t in np.nonzero(met > 1000)[0]:
+        b = behind[t].astype(float)
+        assert np.all(np.abs(second[t] / met[t] - b) < 5 * np.sqrt(b * (1 - b) / met[t]) + 8 / met[t]), t
+
+
 def test_a_chain_is_the_chain_rule():
     rng = np.random.default_rng(6)
     n, K, Kd = 50, 12, 4
