@@ -194,8 +194,14 @@ int lmhead_cache_keep(int count, void* const* base, const int64_t* page_stride,
     if ((page_size > 1 && token_stride[i] < row) || (pages > 1 && page_stride[i] < row) ||
         (kv_heads > 1 && head_stride[i] < row))
       return LMHEAD_ERR_SHAPE;
-    for (int j = 0; j < i; ++j)
-      if (base[j] == base[i]) return LMHEAD_ERR_SHAPE;  // its rows would be moved twice
+    for (int j = 0; j < i; ++j) {  // bytes that would be moved twice
+      if (base[j] == base[i]) return LMHEAD_ERR_SHAPE;
+      if ((pages == 1 || page_stride[j] == page_stride[i]) &&
+          (page_size == 1 || token_stride[j] == token_stride[i]) &&
+          (kv_heads == 1 || head_stride[j] == head_stride[i]) &&
+          meet(base[j], row_bytes[j], base[i], row))
+        return LMHEAD_ERR_SHAPE;  // parts of one row
+    }
     a.t[i].base = base[i];
     a.t[i].st = {page_stride[i], token_stride[i], head_stride[i]};
     a.t[i].row = (int)row;

@@ -630,8 +630,9 @@ int lmhead_verify_tree(const float* p, int64_t n, const int32_t* tokens, const i
  * those that are leave their row alone).
  *   base, *_stride, row_bytes  HOST arrays of `count` (1..8) tensors, pages x
  *             page_size x kv_heads rows of row_bytes contiguous bytes each; strides in
- *             bytes, any order, rows not meeting. A K and a V cache, and the weights
- *             below with rows of 4 bytes.
+ *             bytes, any order, rows not meeting (of one tensor or of two; parts of one
+ *             row may be two tensors, but not with bytes in common). A K and a V
+ *             cache, and the weights below with rows of 4 bytes.
  *   table     S x width int32, as of lmhead_page_plan.
  *   kept      S x n int32, or S x kv_heads x n with per_head: every head's own rows.
  *   first     S int32, or NULL: 0. lens and a verified tree's out_path keep the

@@ -96,6 +96,38 @@ def test_keep_refusals(clib, want, kw):
                                   a["S"], a["out"], None) == want
 
 
+@pytest.mark.parametrize("heads", [2, 1])
+@pytest.mark.parametrize("by", [4, 128, 255, -16])
+def test_keep_refuses_parts_of_a_row_that_meet(clib, by, heads):
+    import ctypes
+    arr = lambda *x: (ctypes.c_int64 * len(x))(*x)
+    a = [arr(OK, OK + (1 << 30), OK + by), arr(*[8192] * 3), arr(*[512] * 3), arr(*[256] * 3), arr(256, 256, 64)]
+    a[3][2] = 256 if heads > 1 else 64  # (the stride of a dimension of one means nothing)
+    a[4][2] = 256 if by < 0 else 64  # (one in front of it reaches into it)
+    assert clib.lmhead_cache_keep(3, *(ctypes.addressof(x) for x in a), 10, 16, heads, OK, 8, OK, 5, 0, None, 2, 2 * OK, None) == -2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [2, 1])
+def test_keep_parts_of_one_row(heads):
+    """K and V side by side in one tensor's rows are two caches; the row and a part of it are not."""
+    import torch
+    from gpu_util import lib
+    L = lib()
+    rng = np.random.default_rng(4)
+    table, pages = _paged(rng, [40, 70], 16)
+    kv = torch.randint(0, 1000, (pages, 16, heads, 24), device="cuda", dtype=torch.int32)
+    kept = np.stack([np.sort(rng.choice(40, 20, replace=False)) for _ in range(2)])
+    want = kv.cpu().numpy().copy()
+    O.cache_keep(want, table, kept, None, 16)
+    L.cache_keep([kv[..., :16], kv[..., 16:]], _i32(table), _i32(kept))
+    assert L.last_device_error() == 0 and np.array_equal(kv.cpu().numpy(), want)
+    for two in ([kv, kv[..., 16:]], [kv[..., 8:], kv[..., :9]]):
+        with pytest.raises(L.LmheadError):
+            L.cache_keep(two, _i32(table), _i32(kept))
+    assert np.array_equal(kv.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("want,kw", [
     (-1, dict(lens=None)), (-1, dict(free=None)), (-2, dict(S=0)), (-2, dict(cap=-1)), (-2, dict(P=0)), (-2, dict(left=OK)),
     (-2, dict(S=1 << 20, width=1 << 20)), (-2, dict(free=OK + 8)),
