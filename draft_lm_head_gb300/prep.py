@@ -154,8 +154,8 @@ def rotary_turns(rot: int, base: float = 10000.0, scaling: Optional[str] = None,
     if scaling == "linear":
         w = w / factor
     elif scaling in ("wavelength", "ramp"):
-        if not 0 < low < high:
-            raise ValueError(f"low={low} must be below high={high}")
+        if not 0 < low < high or not original > 0:
+            raise ValueError(f"low={low} must be below high={high}, original={original} positive")
         if scaling == "wavelength":
             keep = (original * w / (2 * math.pi) - low) / (high - low)
         else:

@@ -69,6 +69,14 @@ def test_ramp_needs_falling_frequencies(base):
     prep.rotary_turns(8, base, "linear", 4.0)
 
 
+@pytest.mark.parametrize("scaling", ["wavelength", "ramp"])
+@pytest.mark.parametrize("original", [0, -8192.0, float("nan")])
+def test_original_length_is_positive(scaling, original):
+    from draft_lm_head_gb300 import prep
+    with pytest.raises(ValueError, match="original"):
+        prep.rotary_turns(8, 10000.0, scaling, 4.0, original)
+
+
 def test_oracle_by_hand():
     """A quarter turn a position: (1, 2) -> (-2, 1) -> (-1, -2); its transpose the
     other way; in the far, whole turns drop out."""
