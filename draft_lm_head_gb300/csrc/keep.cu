@@ -295,7 +295,8 @@ select_kernel(const SelectArgs a, int shift, int staged, int quads, int* err) {
 // later lies behind all that has been written. CTAs share no bytes.
 // Bound by memory: 16 prompts' rows, 4097 of up to 32768 a head (540 MB read and written),
 // 96 us, 5.6 TB/s, rows of 256 bytes in no order; by latency for short lists. More in flight
-// does not help: an eviction of the 16 prompts took 128 us as it is, 136 to 156 with rings of
+// does not help: an eviction of the 16 prompts took 128 us as it is (131 since the pages
+// given back are looked over), 136 to 156 with rings of
 // 12 to 48 KB in shared memory written while the next rows come, 131 and 140 with three
 // and two rows a thread, 131 with loads that do not stay in caches; and, of 145 then, 149
 // to 199 with slices of 64 and 128 bytes, 8 rows a thread, 3 or 6 CTAs an SM.
